@@ -19,7 +19,15 @@ from .api import (  # noqa: F401
     cp_check_device_status,
     cp_debug_bounded_wait_probe,
     cp_lse_merge,
+    cp_paged_attn_decode,
+    cp_paged_attn_workspace_size,
+    cp_paged_kv_append,
     cp_ring_shard_table,
+    cp_scored_attn_bwd,
+    cp_scored_attn_bwd_workspace_size,
+    cp_scored_attn_fwd,
+    cp_scored_attn_validate,
+    cp_scored_attn_workspace_size,
     cp_status_string,
     cp_ulysses_anything_head2seq,
     cp_ulysses_anything_seq2head,

@@ -27,9 +27,17 @@ CP_F32 = 1
 CP_LAP_FUSED = 0
 CP_LAP_STEPWISE = 1
 
+class ScoreRule(ctypes.Structure):
+    """cp_score_rule."""
+    _fields_ = [("softcap", ctypes.c_float), ("slopes", ctypes.c_void_p), ("causal", ctypes.c_int),
+                ("prefix_lens", ctypes.c_void_p), ("q_docs", ctypes.c_void_p), ("kv_docs", ctypes.c_void_p),
+                ("q_pos0", ctypes.c_int64), ("kv_pos0", ctypes.c_int64)]
+
+
 # every symbol include/cp_attn.h declares, with (restype, argtypes)
 _vp, _i, _i64, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
 _ip = ctypes.POINTER(ctypes.c_int)
+_rule = ctypes.POINTER(ScoreRule)
 SIGNATURES = {
     "cp_status_string": (ctypes.c_char_p, [_i]),
     "cp_version": (_i, []),
@@ -56,6 +64,16 @@ SIGNATURES = {
     "cp_attention_bwd_launch_count": (_i, [_i, _i, _i, _i, _i, _i, _i]),
     "cp_attention_bwd": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _f, _i, _i, _i, _vp, _sz,
                               _i, _vp]),
+    "cp_scored_attn_validate": (_i, [_i, _i, _i, _i, _i, _i, _f, _rule, _i]),
+    "cp_scored_attn_workspace_size": (_sz, [_i, _i, _i, _i, _i]),
+    "cp_scored_attn_bwd_workspace_size": (_sz, [_i, _i, _i, _i, _i]),
+    "cp_scored_attn_fwd": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _f, _rule, _vp, _sz, _i, _i, _vp]),
+    "cp_scored_attn_bwd": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _f, _rule, _vp,
+                                _sz, _i, _i, _i, _vp]),
+    "cp_paged_kv_append": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _vp]),
+    "cp_paged_attn_workspace_size": (_sz, [_i, _i, _i, _i, _i]),
+    "cp_paged_attn_decode": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _f, _f, _vp, _vp, _sz,
+                                  _i, _i, _vp]),
 }
 CP_NO_ALLOC_WORKSPACE_BYTES = 64 * 1024 * 1024
 

@@ -7,6 +7,7 @@ memory and the stream.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 
 import torch
@@ -287,8 +288,242 @@ def cp_attention_bwd(q, k, v, out, dout, lse, dq, dk, dv, scale: float, ring_deg
     check(st, "cp_attention_bwd")
 
 
+# ---------------------------------------------------------------------------
+# attention with a score rule, and the paged cache
+# ---------------------------------------------------------------------------
+def _place(dev, stream):
+    """The context (device, stream) that a call on tensors of `dev` runs in: its launches and the memory
+    allocated for it belong to `stream` (None: the device's current stream)."""
+    if stream is None:
+        return contextlib.nullcontext() if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=dev)
+    if stream.device != dev:
+        raise ValueError(f"the stream is of {stream.device}, the tensors are on {dev}")
+    return torch.cuda.stream(stream)
+
+
+def _dense_on(dev, **ts):
+    for name, t in ts.items():
+        if t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, q (or k_new) on {dev}: tensors must live on one CUDA device")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be dense")
+
+
+def _i32(name, t, shape):
+    if t.dtype != torch.int32:
+        raise TypeError(f"{name} must be int32")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have the shape {tuple(shape)}")
+
+
+def _out_dt(name, t, like) -> int:
+    if t.dtype != torch.float32 and t.dtype != like.dtype:
+        raise TypeError(f"{name} must be float32 or {like.dtype}")
+    return _DT[t.dtype]
+
+
+def _scratch(workspace, need, dev):
+    """Pointer, size and owner of the caller's workspace, or of one allocated here."""
+    if workspace is None:
+        if need == 0:
+            return None, 0, None
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    else:
+        _dense_on(dev, workspace=workspace)
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+def _score_rule(q, k, softcap, slopes, causal, prefix_lens, q_docs, kv_docs, q_pos0, kv_pos0):
+    B, Sq, H, _ = q.shape
+    Skv = k.shape[1]
+    dev = q.device
+    r = _lib.ScoreRule(softcap=float(softcap), causal=int(bool(causal)), q_pos0=int(q_pos0), kv_pos0=int(kv_pos0))
+    if slopes is not None:
+        if slopes.dtype != torch.float32 or slopes.shape != (H,):
+            raise ValueError("slopes must be float32 [H]")
+        _dense_on(dev, slopes=slopes)
+        r.slopes = slopes.data_ptr()
+    if prefix_lens is not None:
+        _i32("prefix_lens", prefix_lens, (B,))
+        _dense_on(dev, prefix_lens=prefix_lens)
+        r.prefix_lens = prefix_lens.data_ptr() or 256  # an empty tensor has no address; no row reads it
+    if (q_docs is None) != (kv_docs is None):
+        raise ValueError("q_docs and kv_docs come together")
+    if q_docs is not None:
+        _i32("q_docs", q_docs, (B, Sq))
+        _i32("kv_docs", kv_docs, (B, Skv))
+        _dense_on(dev, q_docs=q_docs, kv_docs=kv_docs)
+        r.q_docs, r.kv_docs = q_docs.data_ptr() or 256, kv_docs.data_ptr() or 256
+    return r
+
+
+def _scored_shapes(q, k, v, lse):
+    _cuda(q, k, v, lse)
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q must be [B, Sq, H, D], k and v [B, Skv, Hkv, D]")
+    B, Sq, H, D = q.shape
+    Skv, Hkv = k.shape[1], k.shape[2]
+    if k.shape != (B, Skv, Hkv, D) or v.shape != k.shape or lse.shape != (B, H, Sq):
+        raise ValueError("shape mismatch")
+    if k.dtype != q.dtype or v.dtype != q.dtype or lse.dtype != torch.float32:
+        raise TypeError("q, k, v must share a dtype; lse must be float32")
+    return B, Sq, H, D, Skv, Hkv
+
+
+def cp_scored_attn_validate(B, H, Hkv, Sq, Skv, D, scale=1.0, softcap=0.0, causal=False, prefix=False,
+                            dtype=torch.bfloat16, q_pos0=0, kv_pos0=0) -> int:
+    """Status code of cp_scored_attn_fwd's checks of sizes and rule (0 = ok). Host only."""
+    r = _lib.ScoreRule(softcap=float(softcap), causal=int(bool(causal)), prefix_lens=256 if prefix else None,
+                       q_pos0=int(q_pos0), kv_pos0=int(kv_pos0))
+    return lib().cp_scored_attn_validate(B, H, Hkv, Sq, Skv, D, float(scale), ctypes.byref(r), _DT[dtype])
+
+
+def cp_scored_attn_workspace_size(B, H, Sq, Skv, docs=False) -> int:
+    return int(lib().cp_scored_attn_workspace_size(B, H, Sq, Skv, int(bool(docs))))
+
+
+def cp_scored_attn_bwd_workspace_size(B, H, Sq, Skv, docs=False) -> int:
+    return int(lib().cp_scored_attn_bwd_workspace_size(B, H, Sq, Skv, int(bool(docs))))
+
+
+def cp_scored_attn_fwd(q, k, v, out, lse, scale: float, softcap: float = 0.0, slopes=None, causal: bool = False,
+                       prefix_lens=None, q_docs=None, kv_docs=None, q_pos0: int = 0, kv_pos0: int = 0, workspace=None,
+                       stream=None):
+    """Attention of q [B,Sq,H,D] over k, v [B,Skv,Hkv,D] (H a multiple of Hkv) with a score rule ->
+    out [B,Sq,H,D] (float32 or q's dtype), lse [B,H,Sq] f32.
+
+    Scores scale * q.k are capped to softcap * tanh(x / softcap) (softcap > 0), lose slopes[h] * distance
+    (slopes: float32 [H]), and take part iff causal is off, the key's position is not after the query's, or it is
+    below prefix_lens[b] (int32 [B]), and iff q_docs and kv_docs (int32 [B,Sq], [B,Skv]; negative: padding) agree.
+    Row 0 of q and of k has the position q_pos0 and kv_pos0. workspace: a CUDA tensor of at least
+    cp_scored_attn_workspace_size(...) bytes; allocated here through torch when None.
+    """
+    B, Sq, H, D, Skv, Hkv = _scored_shapes(q, k, v, lse)
+    if out.shape != q.shape:
+        raise ValueError("shape mismatch")
+    dt, odt, dev = _dt(q), _out_dt("out", out, q), q.device
+    _dense_on(dev, q=q, k=k, v=v, out=out, lse=lse)
+    r = _score_rule(q, k, softcap, slopes, causal, prefix_lens, q_docs, kv_docs, q_pos0, kv_pos0)
+    with _place(dev, stream):
+        need = lib().cp_scored_attn_workspace_size(B, H, Sq, Skv, 1) if q_docs is not None else 0
+        ptr, size, _own = _scratch(workspace, need, dev)
+        st = lib().cp_scored_attn_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), B, H,
+                                      Hkv, Sq, Skv, D, float(scale), ctypes.byref(r), ptr, size, dt, odt, _stream(None))
+    check(st, "cp_scored_attn_fwd")
+
+
+def cp_scored_attn_bwd(q, k, v, out, dout, lse, dq, dk, dv, scale: float, softcap: float = 0.0, slopes=None,
+                       causal: bool = False, prefix_lens=None, q_docs=None, kv_docs=None, q_pos0: int = 0,
+                       kv_pos0: int = 0, workspace=None, stream=None):
+    """Backward of cp_scored_attn_fwd: dout [B,Sq,H,D] (q's dtype), out (float32 or q's dtype) and lse from the
+    forward -> dq [B,Sq,H,D], dk, dv [B,Skv,Hkv,D] (all float32 or all q's dtype; written).
+
+    For a block of a ring, out and lse are the row's results over all blocks, and the blocks' gradients add up.
+    workspace: a CUDA tensor of at least cp_scored_attn_bwd_workspace_size(...) bytes; allocated here when None.
+    """
+    B, Sq, H, D, Skv, Hkv = _scored_shapes(q, k, v, lse)
+    if out.shape != q.shape or dout.shape != q.shape or dq.shape != q.shape or dk.shape != k.shape or dv.shape != k.shape:
+        raise ValueError("shape mismatch")
+    if dout.dtype != q.dtype or dk.dtype != dq.dtype or dv.dtype != dq.dtype:
+        raise TypeError("dout must have q's dtype; dq, dk and dv must share one")
+    dt, odt, gdt, dev = _dt(q), _out_dt("out", out, q), _out_dt("dq", dq, q), q.device
+    _dense_on(dev, q=q, k=k, v=v, out=out, dout=dout, lse=lse, dq=dq, dk=dk, dv=dv)
+    r = _score_rule(q, k, softcap, slopes, causal, prefix_lens, q_docs, kv_docs, q_pos0, kv_pos0)
+    with _place(dev, stream):
+        need = lib().cp_scored_attn_bwd_workspace_size(B, H, Sq, Skv, int(q_docs is not None))
+        ptr, size, _own = _scratch(workspace, need, dev)
+        st = lib().cp_scored_attn_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), dout.data_ptr(),
+                                      lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, H, Hkv, Sq, Skv,
+                                      D, float(scale), ctypes.byref(r), ptr, size, dt, odt, gdt, _stream(None))
+    check(st, "cp_scored_attn_bwd")
+
+
+def _paged_shapes(k_cache, v_cache, block_table, seq_lens, B, Hkv, D, like):
+    _cuda(k_cache, v_cache, block_table, seq_lens)
+    if k_cache.dim() != 4 or k_cache.shape[2:] != (Hkv, D) or v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache must be [num_pages, page_size, Hkv, D]")
+    if k_cache.dtype != like.dtype or v_cache.dtype != like.dtype:
+        raise TypeError("the caches must have the dtype of the other tensors")
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B, max_pages]")
+    _i32("block_table", block_table, (B, block_table.shape[1]))
+    _i32("seq_lens", seq_lens, (B,))
+    return k_cache.shape[0], k_cache.shape[1], block_table.shape[1]
+
+
+def cp_paged_kv_append(k_new, v_new, k_cache, v_cache, block_table, seq_lens, new_lens=None, stream=None):
+    """Writes new tokens k_new, v_new [B,T,Hkv,D] into the pages of k_cache, v_cache [num_pages,page,Hkv,D].
+
+    Token t of sequence b (t < new_lens[b]; all T when new_lens is None) goes to position seq_lens[b] + t: row
+    position % page of page block_table[b, position // page]. seq_lens (int32 [B], the lengths before the call) is not
+    changed. A position or page out of range is skipped and reported by cp_check_device_status.
+    """
+    _cuda(k_new, v_new)
+    if k_new.dim() != 4 or v_new.shape != k_new.shape:
+        raise ValueError("k_new and v_new must be [B, T, Hkv, D]")
+    if v_new.dtype != k_new.dtype:
+        raise TypeError("k_new and v_new must share a dtype")
+    B, T, Hkv, D = k_new.shape
+    dt, dev = _dt(k_new), k_new.device
+    pages, page, max_pages = _paged_shapes(k_cache, v_cache, block_table, seq_lens, B, Hkv, D, k_new)
+    _dense_on(dev, k_new=k_new, v_new=v_new, k_cache=k_cache, v_cache=v_cache, block_table=block_table,
+              seq_lens=seq_lens)
+    if new_lens is not None:
+        _i32("new_lens", new_lens, (B,))
+        _dense_on(dev, new_lens=new_lens)
+    with _place(dev, stream):
+        st = lib().cp_paged_kv_append(k_new.data_ptr(), v_new.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                                      block_table.data_ptr() or 256, seq_lens.data_ptr(),
+                                      new_lens.data_ptr() if new_lens is not None else None, B, T, Hkv, D, pages, page,
+                                      max_pages, dt, _stream(None))
+    check(st, "cp_paged_kv_append")
+
+
+def cp_paged_attn_workspace_size(B, H, Hkv, D, dtype=torch.bfloat16) -> int:
+    return int(lib().cp_paged_attn_workspace_size(B, H, Hkv, D, _DT[dtype]))
+
+
+def cp_paged_attn_decode(q, k_cache, v_cache, block_table, seq_lens, out, lse, scale: float, softcap: float = 0.0,
+                         slopes=None, workspace=None, stream=None):
+    """Attention of one new token per sequence, q [B,H,D], over its seq_lens[b] tokens in the paged cache (the new
+    one among them, the last) -> out [B,H,D] (float32 or q's dtype), lse [B,H] f32.
+
+    softcap and slopes as in cp_scored_attn_fwd, the query's position being seq_lens[b] - 1. A sequence of length 0
+    gets out 0, lse -inf. workspace: a CUDA tensor of at least cp_paged_attn_workspace_size(...) bytes, one for each
+    call that may run at the same time; allocated here through torch when None.
+    """
+    _cuda(q, lse)
+    if q.dim() != 3 or k_cache.dim() != 4:
+        raise ValueError("q must be [B, H, D], the caches [num_pages, page_size, Hkv, D]")
+    B, H, D = q.shape
+    Hkv = k_cache.shape[2]
+    if out.shape != q.shape or lse.shape != (B, H):
+        raise ValueError("shape mismatch")
+    if lse.dtype != torch.float32:
+        raise TypeError("lse must be float32")
+    dt, odt, dev = _dt(q), _out_dt("out", out, q), q.device
+    pages, page, max_pages = _paged_shapes(k_cache, v_cache, block_table, seq_lens, B, Hkv, D, q)
+    _dense_on(dev, q=q, k_cache=k_cache, v_cache=v_cache, block_table=block_table, seq_lens=seq_lens, out=out, lse=lse)
+    if slopes is not None:
+        if slopes.dtype != torch.float32 or slopes.shape != (H,):
+            raise ValueError("slopes must be float32 [H]")
+        _dense_on(dev, slopes=slopes)
+    with _place(dev, stream):
+        need = lib().cp_paged_attn_workspace_size(B, H, Hkv, D, dt)
+        ptr, size, _own = _scratch(workspace, need, dev)
+        st = lib().cp_paged_attn_decode(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
+                                        seq_lens.data_ptr(), out.data_ptr(), lse.data_ptr(), B, H, Hkv, D, pages, page,
+                                        max_pages, float(scale), float(softcap),
+                                        slopes.data_ptr() if slopes is not None else None, ptr, size, dt, odt,
+                                        _stream(None))
+    check(st, "cp_paged_attn_decode")
+
+
 def cp_check_device_status(stream=None) -> int:
-    """Synchronizes the stream; returns 0, or CP_ERR_TIMEOUT if a kernel's bounded wait expired."""
+    """Synchronizes the stream; returns 0, CP_ERR_TIMEOUT if a kernel's bounded wait expired, or CP_ERR_INVALID_ARG
+    if a paged-cache kernel met a page index or a sequence length out of range."""
     return int(lib().cp_check_device_status(_stream(stream)))
 
 
@@ -309,5 +544,8 @@ __all__ = [
     "cp_ulysses_anything_seq2head", "cp_ulysses_anything_head2seq",
     "cp_attention_validate", "cp_ring_shard_table", "cp_attention_workspace_size", "cp_attention_launch_count",
     "cp_attention_bwd", "cp_attention_bwd_workspace_size", "cp_attention_bwd_launch_count",
-    "cp_attention_fwd", "cp_attention_fwd_no_alloc", "cp_attention_fwd_host", "cp_attention_host_buffer_size", "cp_check_device_status", "cp_debug_bounded_wait_probe", "cp_status_string", "cp_version",
+    "cp_attention_fwd", "cp_attention_fwd_no_alloc", "cp_attention_fwd_host", "cp_attention_host_buffer_size", "cp_check_device_status", "cp_debug_bounded_wait_probe",
+    "cp_scored_attn_validate", "cp_scored_attn_workspace_size", "cp_scored_attn_bwd_workspace_size",
+    "cp_scored_attn_fwd", "cp_scored_attn_bwd", "cp_paged_kv_append", "cp_paged_attn_workspace_size",
+    "cp_paged_attn_decode", "cp_status_string", "cp_version",
 ]

@@ -16,6 +16,7 @@
 
 #include "cp_attn.h"
 #include "cp_internal.h"
+#include "cp_score.h"
 
 namespace {
 
@@ -252,6 +253,24 @@ WsLayout ws_layout(int B, int H, int S, int D, int R, int U, cp_dtype dt, cp_lap
 }
 
 }  // namespace
+
+namespace cp {
+
+int host_device(uint32_t** err, int* sms) {
+  DeviceInfo* d = nullptr;
+  const cp_status st = current_device(&d);
+  if (st != CP_OK) return st;
+  *err = d->err;
+  *sms = d->sms;
+  return CP_OK;
+}
+
+bool host_tmap_bf16(CUtensorMap* m, const void* base, int D, int H, int S, int Bn, int box_rows) {
+  const int64_t row = static_cast<int64_t>(H) * D;
+  return make_tmap_bf16(m, base, D, H, S, Bn, row, row * S, box_rows);
+}
+
+}  // namespace cp
 
 extern "C" {
 
@@ -821,8 +840,9 @@ cp_status cp_check_device_status(void* stream) {
   if (cudaMemcpy(&word, dev->err, sizeof(word), cudaMemcpyDeviceToHost) != cudaSuccess) return CP_ERR_CUDA;
   if (word == 0) return CP_OK;
   if (cudaMemset(dev->err, 0, sizeof(word)) != cudaSuccess) return CP_ERR_CUDA;
-  // bit 0: a bounded wait expired; bit 1: a kernel found its shared memory misaligned
-  return (word & 1u) ? CP_ERR_TIMEOUT : CP_ERR_CUDA;
+  // bit 0: a bounded wait expired; bit 1: a kernel found its shared memory misaligned;
+  // bit 2: a page table entry or a sequence length was out of range
+  return (word & 1u) ? CP_ERR_TIMEOUT : (word & 2u) ? CP_ERR_CUDA : CP_ERR_INVALID_ARG;
 }
 
 cp_status cp_debug_bounded_wait_probe(int timeout_us, void* stream) {

@@ -62,7 +62,7 @@ __device__ __forceinline__ bool elect_one() {
 }
 
 // Error codes recorded in the device error word.
-enum : uint32_t { kDevErrTimeout = 1u, kDevErrLayout = 2u };
+enum : uint32_t { kDevErrTimeout = 1u, kDevErrLayout = 2u, kDevErrPage = 4u };
 
 // Bounded wait for the phase of `bar` with the given parity to complete.
 // Returns true on completion. Returns false when another role of the CTA has

@@ -1,0 +1,108 @@
+// cp_score.h — launch parameters of the score-rule attention (forward,
+// backward) and of the paged cache, shared by their kernels and host drivers.
+// Not part of the public ABI.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <climits>
+#include <cstdint>
+
+namespace cp {
+
+// One 64-row block of a document-id row: the smallest and largest id >= 0 in
+// it (INT_MAX, -1 if none) and whether it holds a negative id.
+struct DocRange {
+  int lo, hi, neg, pad;
+};
+constexpr int kDocBlock = 64;
+
+// A scored attention launch. Tensors are dense: q, out, dout, dq [B, Sq, H, D];
+// k, v, dk, dv [B, Skv, Hkv, D]; lse, delta [B, H, Sq].
+struct ScoreArgs {
+  int B, H, Hkv, G, Sq, Skv;  // G = H / Hkv query heads share a key/value head
+  float scale;
+  float cap;              // 0: none
+  const float* slopes;    // [H], or nullptr
+  int causal;
+  int rel;                // position of query row 0 minus position of key row 0
+  const int* prefix;      // [B] positions, or nullptr
+  int kv_pos0;            // position of key row 0 (prefix is in positions)
+  const int* qdoc;        // [B, Sq], or nullptr
+  const int* kdoc;        // [B, Skv]
+  const DocRange* qrange;  // [B, ceil(Sq / 64)], set with qdoc
+  const DocRange* krange;  // [B, ceil(Skv / 64)]
+  const void *q, *k, *v;
+  const void *o, *dout;  // backward: the forward's out, and its gradient
+  void* out;             // forward
+  float* lse;            // forward: written; backward: read
+  float* delta;          // backward
+  void *dq, *dk, *dv;
+  int out_bf16;   // type of out
+  int grad_bf16;  // type of dq, dk, dv
+  uint32_t* err;  // tensor-core kernels: device error word and the bound on each wait
+  uint64_t timeout_ns;
+};
+
+// Keys j < key_limit(i) satisfy the causal rule for query row i of batch entry
+// b: position(j) <= position(i), or position(j) < prefix.
+__device__ __forceinline__ int prefix_limit(const ScoreArgs& a, int b) {
+  return a.prefix ? max(a.prefix[b], 0) - a.kv_pos0 : INT_MIN;
+}
+__device__ __forceinline__ int key_limit(const ScoreArgs& a, int plim, int i) {
+  return a.causal ? max(a.rel + i + 1, plim) : INT_MAX;
+}
+
+// Whether any pair of two blocks can share a document.
+__device__ __forceinline__ bool docs_meet(const DocRange& q, const DocRange& k) {
+  return q.lo <= k.hi && k.lo <= q.hi;  // an empty block has lo = INT_MAX, hi = -1
+}
+__device__ __forceinline__ DocRange docs_join(const DocRange& x, const DocRange& y) {
+  return DocRange{min(x.lo, y.lo), max(x.hi, y.hi), x.neg | y.neg, 0};
+}
+// Whether every pair of the two blocks is of one document.
+__device__ __forceinline__ bool docs_same(const DocRange& q, const DocRange& k) {
+  return q.lo == q.hi && k.lo == k.hi && q.lo == k.lo && !q.neg && !k.neg;
+}
+
+// Fills qrange and krange from qdoc and kdoc.
+cudaError_t launch_doc_ranges(const ScoreArgs& a, cudaStream_t s);
+// fp32 on the CUDA cores.
+cudaError_t launch_score_fwd_f32(const ScoreArgs& a, int D, bool bf16, cudaStream_t s);
+cudaError_t launch_score_bwd_f32(const ScoreArgs& a, int D, bool bf16, cudaStream_t s);
+
+// The paged cache.
+constexpr int kPagedCtas = 304;     // decode CTAs: two on each of 152 multiprocessors
+constexpr int kPagedBlock = 64;     // keys of one work block
+constexpr int kPagedMaxBatch = 4096;
+struct PagedArgs {
+  int B, T, H, Hkv, G, D;
+  int num_pages, page_shift, max_pages;
+  const int* table;     // [B, max_pages]
+  const int* seq_lens;  // [B]
+  const int* new_lens;  // append: [B], or nullptr (all T)
+  const void *k_new, *v_new;  // append: [B, T, Hkv, D]
+  void *k_cache, *v_cache;    // [num_pages, page, Hkv, D]
+  const void* q;  // decode: [B, H, D]
+  void* out;
+  float* lse;  // [B, H]
+  int out_bf16;
+  float scale, cap;
+  const float* slopes;
+  float* partial;  // workspace: [kPagedCtas][2] partial results
+  int2* info;      // workspace: [B * Hkv * groups] which partials make up a unit
+  uint32_t* err;
+};
+// Query heads that share a key/value head are taken this many at a time.
+inline int paged_rows(bool bf16) { return bf16 ? 16 : 8; }
+cudaError_t launch_paged_append(const PagedArgs& a, int elem_bytes, cudaStream_t s);
+cudaError_t launch_paged_decode(const PagedArgs& a, bool bf16, cudaStream_t s);
+
+// From cp_api.cu: the checks and tensor maps that the host drivers share.
+// 0, or the cp_status of the current device's check.
+int host_device(uint32_t** err, int* sms);
+// bf16 [Bn, S, H, D] with 64-column x box_rows boxes of one head, 128-byte swizzle.
+bool host_tmap_bf16(CUtensorMap* m, const void* base, int D, int H, int S, int Bn, int box_rows);
+
+}  // namespace cp

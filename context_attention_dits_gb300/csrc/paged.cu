@@ -1,0 +1,603 @@
+// paged.cu — the paged key/value cache: rows of new tokens written into pages,
+// and attention of one new token per sequence over the pages.
+//
+// A cache is [num_pages, page, Hkv, D]; key j of sequence b is row j mod page
+// of page table[b][j / page]. With n = seq_lens[b] and q the sequence's new
+// token (position n - 1):
+//   x_j = scale q.k_j, capped to cap tanh(x / cap), less slope_h (n - 1 - j)
+//   out = sum_j softmax_j(x_j) v_j,  lse = ln sum_j exp(x_j),  j < n
+//
+// Decode reads every cached row once and computes 4 G D flop per row pair of
+// 4 D bytes (bf16): it is bound by HBM. What the split has to give is enough
+// bytes in flight on every multiprocessor whatever the batch: all work is laid
+// out as one list of 64-key blocks (sequence, key/value head, group of query
+// heads, block), cut into equal contiguous ranges, one per CTA. A CTA's range
+// holds at most one unit (sequence, head) that began in an earlier CTA and one
+// that goes on in the next; those leave a partial (O, m, l) each, which a
+// second launch joins. Units that lie within one CTA are written directly.
+// Each warp streams its own 16 keys of every block through kStages buffers of
+// its own with 16-byte asynchronous copies (one row of one head is 128 to 512
+// contiguous bytes), so no barrier of the CTA stands in the loop; the warps'
+// states are joined at the end of a unit.
+// bf16: Q K^T and P V on m16n8k16 matrix instructions (16 query heads, 16
+// keys); the tile is far too small for a 128-row tensor-memory MMA, and the
+// instruction's rate is not what bounds it. fp32: FMAs, 8 query heads.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <climits>
+#include <cmath>
+#include <cstdint>
+
+#include "cp_internal.h"
+#include "cp_ptx.cuh"
+#include "cp_score.h"
+
+namespace cp {
+namespace {
+
+constexpr float kL2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.69314718055994531f;
+
+// Row (page * page_size + row in page) of token pos of sequence b, or -1 (and
+// the error word) if its page is out of range.
+__device__ __forceinline__ int cache_row(const PagedArgs& a, int b, int pos) {
+  const int pg = pos >> a.page_shift;
+  const int id = a.table[static_cast<int64_t>(b) * a.max_pages + pg];
+  if (id < 0 || id >= a.num_pages) {
+    atomicOr(a.err, kDevErrPage);
+    return -1;
+  }
+  return (id << a.page_shift) + (pos & ((1 << a.page_shift) - 1));
+}
+
+// ----------------------------------------------------------------------------
+// Append. A row of a token is Hkv * D elements, contiguous on both sides; TPR
+// threads share a row, each moving 16 bytes of k and of v at a time.
+// ----------------------------------------------------------------------------
+template <int TPR>
+__global__ void __launch_bounds__(256) paged_append_kernel(const __grid_constant__ PagedArgs a, int pieces) {
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * (256 / TPR) + threadIdx.x / TPR;
+  if (row >= static_cast<int64_t>(a.B) * a.T) return;
+  const int b = static_cast<int>(row / a.T), t = static_cast<int>(row - static_cast<int64_t>(b) * a.T);
+  if (a.new_lens && t >= a.new_lens[b]) return;
+  const int64_t pos = static_cast<int64_t>(a.seq_lens[b]) + t;
+  if (a.seq_lens[b] < 0 || pos >= static_cast<int64_t>(a.max_pages) << a.page_shift) {
+    atomicOr(a.err, kDevErrPage);
+    return;
+  }
+  const int dst = cache_row(a, b, static_cast<int>(pos));
+  if (dst < 0) return;
+  const uint4* ks = static_cast<const uint4*>(a.k_new) + row * pieces;
+  const uint4* vs = static_cast<const uint4*>(a.v_new) + row * pieces;
+  uint4* kd = static_cast<uint4*>(a.k_cache) + static_cast<int64_t>(dst) * pieces;
+  uint4* vd = static_cast<uint4*>(a.v_cache) + static_cast<int64_t>(dst) * pieces;
+  for (int p = threadIdx.x % TPR; p < pieces; p += TPR) {
+    const uint4 x = ks[p], y = vs[p];
+    kd[p] = x;
+    vd[p] = y;
+  }
+}
+
+// ----------------------------------------------------------------------------
+// Decode
+// ----------------------------------------------------------------------------
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+constexpr int kDecThreads = 128;
+constexpr int kDecWarps = 4;
+constexpr int kChunk = 16;  // keys of a warp and step
+static_assert(kChunk * kDecWarps == kPagedBlock, "a block is a chunk of each warp");
+
+template <int D, typename T>
+struct DecCfg {
+  static constexpr bool kBf16 = sizeof(T) == 2;
+  static constexpr int kRows = kBf16 ? 16 : 8;          // query heads of a unit
+  static constexpr int kRowB = D * sizeof(T);           // bytes of a cached row
+  static constexpr int kPieces = kRowB / 16;            // 16-byte pieces of it
+  static constexpr int kTile = kChunk * kRowB;          // a chunk's k (or v)
+  static constexpr int kStages = kBf16 && D == 64 ? 4 : 3;
+  static constexpr int kWarpB = kStages * 2 * kTile;    // a warp's buffers
+  static constexpr int kSlot = kRows * (D + 2);         // floats of a partial: O, then m and l
+  static_assert(kStages <= 4, "have");
+  static_assert(kWarpB >= kSlot * 4, "a warp's buffers hold its state at the end of a unit");
+  static constexpr int kSmem = kDecWarps * kWarpB;
+  // two CTAs on a multiprocessor where their buffers fit
+  static constexpr int kCtas = kSmem <= 96 * 1024 ? kPagedCtas : kPagedCtas / 2;
+};
+
+// log2 of the score's weight: the cap's tanh from the exponential,
+// tanh z = 1 - 2 / (1 + e^2z); its error is ~2^-23 absolute, which is what the
+// exponent needs.
+struct DecScore {
+  float a0, capl2, sl2;  // scale (times 2 log2 e / cap if capped, log2 e otherwise); cap * log2 e; slope * log2 e
+  bool capped;
+  __device__ __forceinline__ float operator()(float dot, float slope, float dist) const {
+    float y = dot * a0;
+    if (capped) y = capl2 * (1.f - __fdividef(2.f, 1.f + ex2_approx(y)));
+    return fmaf(-slope, dist, y);
+  }
+};
+
+template <int D, typename T>
+__global__ void __launch_bounds__(kDecThreads) paged_decode_kernel(const __grid_constant__ PagedArgs a) {
+  using C = DecCfg<D, T>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int cum[kPagedMaxBatch + 1];  // blocks before sequence b
+  __shared__ int wsum[kDecWarps];
+  __shared__ uint32_t have[kDecWarps][4];  // the rows that a stage holds, a bit each
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int groups = (a.G + C::kRows - 1) / C::kRows;
+  const int HG = a.Hkv * groups;
+  const int cap_len = static_cast<int>(min(static_cast<int64_t>(a.max_pages) << a.page_shift, int64_t{INT_MAX - 64}));
+  auto seq_len = [&](int b) {
+    const int n = a.seq_lens[b];
+    if (n < 0 || n > cap_len) {
+      atomicOr(a.err, kDevErrPage);
+      return n < 0 ? 0 : cap_len;
+    }
+    return n;
+  };
+  // ---- the work list: an exclusive sum of the sequences' blocks ----
+  int carry = 0;
+  for (int b0 = 0; b0 < a.B; b0 += kDecThreads) {
+    const int b = b0 + threadIdx.x;
+    const int x = b < a.B ? (seq_len(b) + kPagedBlock - 1) / kPagedBlock * HG : 0;
+    int s = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += y;
+    }
+    if (lane == 31) wsum[warp] = s;
+    __syncthreads();
+    int before = carry;
+    for (int w = 0; w < kDecWarps; ++w) {
+      if (w < warp) before += wsum[w];
+      carry += wsum[w];
+    }
+    if (b < a.B) cum[b] = before + s - x;
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) cum[a.B] = carry;
+  __syncthreads();
+  const int total = carry;
+  // sequences without a token: out 0, lse -inf
+  for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+    if (cum[b + 1] != cum[b]) continue;
+    for (int i = threadIdx.x; i < a.H * D; i += kDecThreads) {
+      if (a.out_bf16)
+        static_cast<__nv_bfloat16*>(a.out)[static_cast<int64_t>(b) * a.H * D + i] = __float2bfloat16(0.f);
+      else
+        static_cast<float*>(a.out)[static_cast<int64_t>(b) * a.H * D + i] = 0.f;
+    }
+    for (int i = threadIdx.x; i < a.H; i += kDecThreads) a.lse[static_cast<int64_t>(b) * a.H + i] = -INFINITY;
+  }
+  const int share = (total + gridDim.x - 1) / gridDim.x;
+  const int begin = min(total, static_cast<int>(blockIdx.x) * share), end = min(total, begin + share);
+  if (begin >= end) return;
+
+  uint8_t* wbuf = smem + warp * C::kWarpB;
+  const uint32_t wb = smem_addr(wbuf);
+  const int64_t tok_b = static_cast<int64_t>(a.Hkv) * C::kRowB;  // bytes of a token's row of all heads
+  DecScore score;
+  score.capped = a.cap > 0.f;
+  score.a0 = a.scale * (score.capped ? 2.f * kL2e / a.cap : kL2e);
+  score.capl2 = a.cap * kL2e;
+
+  int b = 0;
+  {  // the sequence of the first block
+    int lo = 0, hi = a.B - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) / 2;
+      if (cum[mid] <= begin) lo = mid; else hi = mid - 1;
+    }
+    b = lo;
+  }
+  for (int at = begin; at < end;) {
+    while (cum[b + 1] <= at) ++b;
+    const int n = min(max(a.seq_lens[b], 0), cap_len);
+    const int nblk = (n + kPagedBlock - 1) / kPagedBlock;
+    const int u = (at - cum[b]) / nblk, blk0 = (at - cum[b]) - u * nblk;
+    const int blk1 = min(nblk, blk0 + end - at);
+    const int unit0 = at - blk0;  // the unit's first block in the list
+    const int hk = u / groups, hg = u - hk * groups;
+    const int h0 = hk * a.G + hg * C::kRows, nrow = min(C::kRows, a.G - hg * C::kRows);
+    const uint8_t* kc = static_cast<const uint8_t*>(a.k_cache) + static_cast<int64_t>(hk) * C::kRowB;
+    const uint8_t* vc = static_cast<const uint8_t*>(a.v_cache) + static_cast<int64_t>(hk) * C::kRowB;
+
+    // a chunk's rows: lane r < 16 finds row r (-1 past the end)
+    auto find = [&](int blk) {
+      const int j = blk * kPagedBlock + warp * kChunk + lane;
+      return lane < kChunk && blk < blk1 && j < n ? cache_row(a, b, j) : -1;
+    };
+    auto load = [&](int rows, int stage) {
+      const uint32_t base = wb + stage * 2 * C::kTile;
+      const uint32_t found = __ballot_sync(0xffffffffu, rows >= 0);
+      if (lane == 0) have[warp][stage] = found;
+#pragma unroll
+      for (int i = lane; i < kChunk * C::kPieces; i += 32) {
+        const int r = i / C::kPieces, p = i % C::kPieces;
+        const int row = __shfl_sync(0xffffffffu, rows, r);
+        const int64_t off = static_cast<int64_t>(max(row, 0)) * tok_b + p * 16;
+        const uint32_t d = base + r * C::kRowB + ((p ^ (r & 7)) * 16);
+        cp_async16(d, kc + off, row >= 0);
+        cp_async16(d + C::kTile, vc + off, row >= 0);
+      }
+    };
+
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    int rows_next = find(blk0);
+#pragma unroll
+    for (int st = 0; st < C::kStages - 1; ++st) {
+      if (blk0 + st < blk1) load(rows_next, st);
+      rows_next = find(blk0 + st + 1);
+      cp_async_commit();
+    }
+
+    if constexpr (C::kBf16) {
+      const int g = lane >> 2, tq = lane & 3;
+      uint32_t qf[D / 16][4];
+      {
+        const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + (static_cast<int64_t>(b) * a.H + h0) * D;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int r = g + (e & 1) * 8, d = kk * 16 + tq * 2 + (e >> 1) * 8;
+            qf[kk][e] = r < nrow ? *reinterpret_cast<const uint32_t*>(q + r * D + d) : 0u;
+          }
+      }
+      float slope[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) slope[e] = a.slopes && g + 8 * e < nrow ? a.slopes[h0 + g + 8 * e] * kL2e : 0.f;
+      float o[D / 8][4];
+#pragma unroll
+      for (int x = 0; x < D / 8; ++x)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[x][e] = 0.f;
+      const int lm = lane >> 3, lr = lane & 7;
+      const bool two = nrow > 8;
+      int stage = 0;
+      for (int blk = blk0; blk < blk1; ++blk) {
+        cp_async_wait<C::kStages - 2>();
+        __syncwarp();
+        {  // the stage that the last step read is free again
+          int st = stage + C::kStages - 1;
+          if (st >= C::kStages) st -= C::kStages;
+          if (blk + C::kStages - 1 < blk1) load(rows_next, st);
+          rows_next = find(blk + C::kStages);
+          cp_async_commit();
+        }
+        const uint32_t kb = wb + stage * 2 * C::kTile, vb = kb + C::kTile;
+        const uint32_t on = have[warp][stage];
+        float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+        const int krow = (lm >> 1) * 8 + lr;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          uint32_t f[4];
+          ldsm4(f, kb + krow * C::kRowB + (((2 * kk + (lm & 1)) ^ (krow & 7)) * 16));
+          mma16816(s[0], qf[kk], f[0], f[1]);
+          mma16816(s[1], qf[kk], f[2], f[3]);
+        }
+        const int j0 = blk * kPagedBlock + warp * kChunk + tq * 2;
+        uint32_t pf[4];
+        float fsc[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {  // rows g and g + 8
+          if (e == 1 && !two) {
+            pf[1] = pf[3] = 0u;
+            fsc[1] = 1.f;
+            break;
+          }
+          float x[4], mx = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int j = j0 + (c >> 1) * 8 + (c & 1);
+            x[c] = (on >> (tq * 2 + (c >> 1) * 8 + (c & 1))) & 1u ? score(s[c >> 1][2 * e + (c & 1)], slope[e], static_cast<float>(n - 1 - j)) : -INFINITY;
+            mx = fmaxf(mx, x[c]);
+          }
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          const float mn = fmaxf(m[e], mx), base = mn == -INFINITY ? 0.f : mn;
+          fsc[e] = ex2_approx(m[e] - base);
+          m[e] = mn;
+          float sum = 0.f;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            x[c] = ex2_approx(x[c] - base);
+            sum += x[c];
+          }
+          l[e] = l[e] * fsc[e] + sum;
+          // P rounded to bf16 for the matrix product; l sums it unrounded
+          pf[e] = pack_bf16x2(x[0], x[1]);
+          pf[2 + e] = pack_bf16x2(x[2], x[3]);
+        }
+        if (__any_sync(0xffffffffu, fsc[0] != 1.f || fsc[1] != 1.f)) {
+#pragma unroll
+          for (int x = 0; x < D / 8; ++x) {
+            o[x][0] *= fsc[0];
+            o[x][1] *= fsc[0];
+            o[x][2] *= fsc[1];
+            o[x][3] *= fsc[1];
+          }
+        }
+        const int vrow = (lm & 1) * 8 + lr;
+#pragma unroll
+        for (int x = 0; x < D / 16; ++x) {
+          uint32_t f[4];
+          ldsm4t(f, vb + vrow * C::kRowB + (((2 * x + (lm >> 1)) ^ (vrow & 7)) * 16));
+          mma16816(o[2 * x], pf, f[0], f[1]);
+          mma16816(o[2 * x + 1], pf, f[2], f[3]);
+        }
+        __syncwarp();
+        if (++stage == C::kStages) stage = 0;
+      }
+      // ---- this warp's state into its buffers: O [kRows][D], then m, l ----
+      cp_async_wait<0>();
+      __syncwarp();
+      float* w = reinterpret_cast<float*>(wbuf);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
+        l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
+        const int r = g + 8 * e;
+#pragma unroll
+        for (int x = 0; x < D / 8; ++x)
+          *reinterpret_cast<float2*>(w + r * D + x * 8 + tq * 2) = make_float2(o[x][2 * e], o[x][2 * e + 1]);
+        if (tq == 0) {
+          w[C::kRows * D + 2 * r] = m[e];
+          w[C::kRows * D + 2 * r + 1] = l[e];
+        }
+      }
+    } else {
+      // fp32: lane = (key lane % 16, half of D lane / 16) for the scores; then
+      // D / 32 columns a lane for the second product
+      constexpr int kCols = D / 32;
+      const int key = lane & 15, half = lane >> 4;
+      const float* q = static_cast<const float*>(a.q) + (static_cast<int64_t>(b) * a.H + h0) * D;
+      float o[C::kRows][kCols], mr[C::kRows], lr[C::kRows];
+#pragma unroll
+      for (int r = 0; r < C::kRows; ++r) {
+        mr[r] = -INFINITY;
+        lr[r] = 0.f;
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) o[r][c] = 0.f;
+      }
+      int stage = 0;
+      for (int blk = blk0; blk < blk1; ++blk) {
+        cp_async_wait<C::kStages - 2>();
+        __syncwarp();
+        {
+          int st = stage + C::kStages - 1;
+          if (st >= C::kStages) st -= C::kStages;
+          if (blk + C::kStages - 1 < blk1) load(rows_next, st);
+          rows_next = find(blk + C::kStages);
+          cp_async_commit();
+        }
+        const uint8_t* kb = wbuf + stage * 2 * C::kTile;
+        const uint8_t* vb = kb + C::kTile;
+        float s[C::kRows];
+#pragma unroll
+        for (int r = 0; r < C::kRows; ++r) s[r] = 0.f;
+#pragma unroll 4
+        for (int p = 0; p < C::kPieces / 2; ++p) {
+          const int pp = half * (C::kPieces / 2) + p;
+          const float4 x = *reinterpret_cast<const float4*>(kb + key * C::kRowB + ((pp ^ (key & 7)) * 16));
+#pragma unroll
+          for (int r = 0; r < C::kRows; ++r) {
+            if (r >= nrow) break;
+            const float4 y = *reinterpret_cast<const float4*>(q + r * D + pp * 4);
+            s[r] = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, s[r]))));
+          }
+        }
+        const int j = blk * kPagedBlock + warp * kChunk + key;
+        const bool on = (have[warp][stage] >> key) & 1u;
+#pragma unroll
+        for (int r = 0; r < C::kRows; ++r) {
+          if (r >= nrow) break;
+          s[r] += __shfl_xor_sync(0xffffffffu, s[r], 16);
+          const float slope = a.slopes ? a.slopes[h0 + r] * kL2e : 0.f;
+          float x = -INFINITY;
+          if (on) {
+            x = s[r] * a.scale;
+            if (score.capped) x = a.cap * tanhf(x / a.cap);
+            x = fmaf(x, kL2e, -slope * static_cast<float>(n - 1 - j));
+          }
+          float mx = x;
+#pragma unroll
+          for (int of = 8; of > 0; of >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, of));
+          const float mn = fmaxf(mr[r], mx), base = mn == -INFINITY ? 0.f : mn;
+          const float f = exp2f(mr[r] - base);
+          mr[r] = mn;
+          s[r] = exp2f(x - base);
+          lr[r] = lr[r] * f + s[r];  // over the lane's own keys, joined at the end
+#pragma unroll
+          for (int c = 0; c < kCols; ++c) o[r][c] *= f;
+        }
+#pragma unroll 4
+        for (int kx = 0; kx < kChunk; ++kx) {
+          float y[kCols];
+          const int p = lane * kCols / 4;
+          const float* src = reinterpret_cast<const float*>(vb + kx * C::kRowB + ((p ^ (kx & 7)) * 16)) + lane * kCols % 4;
+#pragma unroll
+          for (int c = 0; c < kCols; ++c) y[c] = src[c];
+#pragma unroll
+          for (int r = 0; r < C::kRows; ++r) {
+            if (r >= nrow) break;
+            const float w = __shfl_sync(0xffffffffu, s[r], kx);
+#pragma unroll
+            for (int c = 0; c < kCols; ++c) o[r][c] = fmaf(w, y[c], o[r][c]);
+          }
+        }
+        __syncwarp();
+        if (++stage == C::kStages) stage = 0;
+      }
+      cp_async_wait<0>();
+      __syncwarp();
+      float* w = reinterpret_cast<float*>(wbuf);
+#pragma unroll
+      for (int r = 0; r < C::kRows; ++r) {
+        float sum = lr[r];
+#pragma unroll
+        for (int of = 8; of > 0; of >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, of);
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) w[r * D + lane * kCols + c] = o[r][c];
+        if (lane == 0) {
+          w[C::kRows * D + 2 * r] = mr[r];
+          w[C::kRows * D + 2 * r + 1] = sum;
+        }
+      }
+    }
+
+    // ---- the warps' states joined: written out, or left as a partial ----
+    __syncthreads();
+    const bool whole = blk0 == 0 && blk1 == nblk;
+    const int slot = at == begin ? 0 : 1;
+    float* part = a.partial + (static_cast<int64_t>(blockIdx.x) * 2 + slot) * C::kSlot;
+    for (int i = threadIdx.x; i < nrow * D; i += kDecThreads) {
+      const int r = i / D;
+      float mw[kDecWarps], mx = -INFINITY, sum = 0.f, acc = 0.f;
+#pragma unroll
+      for (int w = 0; w < kDecWarps; ++w) {
+        mw[w] = reinterpret_cast<const float*>(smem + w * C::kWarpB)[C::kRows * D + 2 * r];
+        mx = fmaxf(mx, mw[w]);
+      }
+      const float base = mx == -INFINITY ? 0.f : mx;
+#pragma unroll
+      for (int w = 0; w < kDecWarps; ++w) {
+        const float* st = reinterpret_cast<const float*>(smem + w * C::kWarpB);
+        const float f = exp2f(mw[w] - base);
+        sum = fmaf(st[C::kRows * D + 2 * r + 1], f, sum);
+        acc = fmaf(st[i], f, acc);
+      }
+      if (whole) {
+        const int64_t row = static_cast<int64_t>(b) * a.H + h0 + r;
+        const float x = sum > 0.f ? acc / sum : 0.f;
+        if (a.out_bf16)
+          static_cast<__nv_bfloat16*>(a.out)[row * D + i % D] = __float2bfloat16(x);
+        else
+          static_cast<float*>(a.out)[row * D + i % D] = x;
+        if (i % D == 0) a.lse[row] = sum > 0.f ? (mx + log2f(sum)) * kLn2 : -INFINITY;
+      } else {
+        part[i] = acc;
+        if (i % D == 0) {
+          part[C::kRows * D + 2 * r] = mx;
+          part[C::kRows * D + 2 * r + 1] = sum;
+        }
+      }
+    }
+    if (threadIdx.x == 0 && blk0 == 0)  // the CTA that begins a unit says which partials make it up
+      a.info[static_cast<int64_t>(b) * HG + u] =
+          whole ? make_int2(0, -1) : make_int2(blockIdx.x * 2 + slot, (unit0 + nblk - 1) / share);
+    __syncthreads();  // the buffers are free for the next unit's copies
+    at += blk1 - blk0;
+  }
+}
+
+// Joins the partials of a unit that lay in more than one CTA: the first in the
+// slot that info names, the others in slot 0 of the CTAs up to info.y.
+template <int D>
+__global__ void __launch_bounds__(D) paged_join_kernel(const __grid_constant__ PagedArgs a, int rows) {
+  const int h = blockIdx.x, b = blockIdx.y, d = threadIdx.x;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (a.seq_lens[b] <= 0) return;
+  const int groups = (a.G + rows - 1) / rows;
+  const int hk = h / a.G, r = (h - hk * a.G) % rows, hg = (h - hk * a.G) / rows;
+  const int2 w = a.info[(static_cast<int64_t>(b) * a.Hkv + hk) * groups + hg];
+  if (w.y < 0) return;
+  const int slot_floats = rows * (D + 2);
+  float mx = -INFINITY, sum = 0.f, acc = 0.f;
+  for (int c = w.x >> 1; c <= w.y; ++c) {
+    const int slot = c == (w.x >> 1) ? w.x & 1 : 0;
+    const float* p = a.partial + (static_cast<int64_t>(c) * 2 + slot) * slot_floats;
+    const float pm = p[rows * D + 2 * r], pl = p[rows * D + 2 * r + 1], po = p[r * D + d];
+    const float mn = fmaxf(mx, pm), base = mn == -INFINITY ? 0.f : mn;
+    const float f = exp2f(mx - base), g = exp2f(pm - base);
+    sum = sum * f + pl * g;
+    acc = acc * f + po * g;
+    mx = mn;
+  }
+  const int64_t row = static_cast<int64_t>(b) * a.H + h;
+  const float x = sum > 0.f ? acc / sum : 0.f;
+  if (a.out_bf16)
+    static_cast<__nv_bfloat16*>(a.out)[row * D + d] = __float2bfloat16(x);
+  else
+    static_cast<float*>(a.out)[row * D + d] = x;
+  if (d == 0) a.lse[row] = sum > 0.f ? (mx + log2f(sum)) * kLn2 : -INFINITY;
+}
+
+template <int D, typename T>
+cudaError_t decode_d(const PagedArgs& a, cudaStream_t s) {
+  using C = DecCfg<D, T>;
+  static_assert(C::kSmem + (kPagedMaxBatch + 8) * 4 <= 227 * 1024, "shared memory budget");
+  cudaError_t e =
+      cudaFuncSetAttribute(paged_decode_kernel<D, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (e != cudaSuccess) return e;
+  // blocks of the list if every table were full; a unit of one block is never split
+  const int groups = (a.G + C::kRows - 1) / C::kRows;
+  const int64_t per_unit = ((static_cast<int64_t>(a.max_pages) << a.page_shift) + kPagedBlock - 1) / kPagedBlock;
+  const int64_t bound = per_unit * a.Hkv * groups * a.B;
+  const int ctas = static_cast<int>(bound < C::kCtas ? (bound > 0 ? bound : 1) : C::kCtas);
+  paged_decode_kernel<D, T><<<ctas, kDecThreads, C::kSmem, s>>>(a);
+  if ((e = cudaGetLastError()) != cudaSuccess || per_unit <= 1) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(a.H, a.B);
+  cfg.blockDim = dim3(D);
+  cfg.stream = s;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;  // its launch overlaps the decode kernel's end
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_join_kernel<D>, a, static_cast<int>(C::kRows));
+}
+
+}  // namespace
+
+cudaError_t launch_paged_append(const PagedArgs& a, int elem_bytes, cudaStream_t s) {
+  const int64_t rows = static_cast<int64_t>(a.B) * a.T;
+  if (rows == 0) return cudaSuccess;
+  const int pieces = a.Hkv * a.D * elem_bytes / 16;
+  // threads a row: enough for one piece each, where a row has as many
+  if (pieces <= 32) {
+    paged_append_kernel<32><<<static_cast<unsigned>((rows + 7) / 8), 256, 0, s>>>(a, pieces);
+  } else if (pieces <= 64) {
+    paged_append_kernel<64><<<static_cast<unsigned>((rows + 3) / 4), 256, 0, s>>>(a, pieces);
+  } else {
+    paged_append_kernel<128><<<static_cast<unsigned>((rows + 1) / 2), 256, 0, s>>>(a, pieces);
+  }
+  return cudaGetLastError();
+}
+
+cudaError_t launch_paged_decode(const PagedArgs& a, bool bf16, cudaStream_t s) {
+  if (a.D == 64) return bf16 ? decode_d<64, __nv_bfloat16>(a, s) : decode_d<64, float>(a, s);
+  return bf16 ? decode_d<128, __nv_bfloat16>(a, s) : decode_d<128, float>(a, s);
+}
+
+}  // namespace cp

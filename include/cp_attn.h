@@ -283,7 +283,8 @@ cp_status cp_attention_fwd_host(const void* q, const void* k, const void* v, flo
  * current device. Returns CP_OK if no kernel reported a problem since the
  * last call, CP_ERR_TIMEOUT if a kernel's bounded wait expired, CP_ERR_CUDA
  * if a kernel found its shared memory base misaligned (it then did no work)
- * or the read failed.
+ * or the read failed, CP_ERR_INVALID_ARG if a paged-cache kernel met a page
+ * index or a sequence length out of range.
  */
 cp_status cp_check_device_status(void* stream);
 
@@ -372,6 +373,124 @@ cp_status cp_attention_bwd(const void* q, const void* k, const void* v, const fl
                            const float* lse, float* dq, float* dk, float* dv, int B, int H, int S, int D,
                            float scale, int ring_degree, int ulysses_degree, int uneven_ok, void* workspace,
                            size_t ws_bytes, cp_dtype dt, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Attention with a score rule (language models): block attention as in
+ * cp_block_attn_fwd whose scores are capped by a tanh, get a bias that falls
+ * with distance and are masked by rule, with query heads that share key/value
+ * heads; its backward; and its serving form, one new token per sequence over a
+ * paged cache. The pages have no counterpart to these calls.
+ *
+ * For query row i (position q_pos0 + i) and key row j (position kv_pos0 + j)
+ * of query head h, which reads key/value head h / (H / Hkv):
+ *   x_ij = scale * q_i.k_j
+ *   x_ij = softcap * tanh(x_ij / softcap)              if softcap > 0
+ *   x_ij = x_ij - slopes[h] * |position i - position j| if slopes
+ * The pair takes part iff
+ *   !causal, or position j <= position i, or position j < prefix_lens[b]; and
+ *   no document ids, or q_docs[b,i] == kv_docs[b,j] >= 0.
+ * out_i = sum_j softmax_j(x_ij) v_j and lse_i = ln sum_j exp(x_ij) over the
+ * pairs that take part; a row without any gets out = 0, lse = -inf. Rows of a
+ * masked pair must still hold finite numbers: a weight of 0 meets them in the
+ * matrix products. Because positions are global, a ring's blocks are calls
+ * with their own q_pos0 and kv_pos0 whose fp32 (out, lse) cp_lse_merge joins.
+ * -------------------------------------------------------------------------*/
+typedef struct {
+  float softcap;              /* > 0: cap of the scores; 0: none */
+  const float* slopes;        /* device [H], fp32 (any sign, finite), or NULL */
+  int causal;                 /* nonzero: keys after the query take no part */
+  const int32_t* prefix_lens; /* device [B] or NULL; needs causal. Keys at positions below it are open to all rows */
+  const int32_t* q_docs;      /* device [B, Sq] or NULL: document ids in any order; negative: padding */
+  const int32_t* kv_docs;     /* device [B, Skv]; NULL iff q_docs is */
+  int64_t q_pos0, kv_pos0;    /* positions of row 0, 0 .. 2^30 */
+} cp_score_rule;
+
+/* Host-only: the status the two calls below return for these sizes before
+ * looking at a tensor's pointer. rule may be NULL (no cap, bias or mask). INVALID_ARG: a size, D not
+ * 64 or 128, more than 65535 batch entries or heads or 2^24 rows, a scale or
+ * softcap that is not finite (or a negative softcap), a position out of range,
+ * one of q_docs, kv_docs without the other; UNSUPPORTED_COMBO: prefix_lens
+ * without causal; NOT_DIVISIBLE: H % Hkv. */
+cp_status cp_scored_attn_validate(int B, int H, int Hkv, int Sq, int Skv, int D, float scale,
+                                  const cp_score_rule* rule, cp_dtype dt);
+
+/* Host-only: bytes of device workspace (256-byte aligned start); docs: whether
+ * the rule has document ids. The forward needs none without them. */
+size_t cp_scored_attn_workspace_size(int B, int H, int Sq, int Skv, int docs);
+size_t cp_scored_attn_bwd_workspace_size(int B, int H, int Sq, int Skv, int docs);
+
+/*
+ * Forward of one block.
+ *   q [B, Sq, H, D], k, v [B, Skv, Hkv, D] (dt, dense); out [B, Sq, H, D] of
+ *   out_dt: float32, or dt; lse [B, H, Sq] float32.
+ * Skv == 0 yields out = 0, lse = -inf; B == 0 or Sq == 0 launches nothing.
+ * Errors: those of cp_scored_attn_validate, INVALID_ARG (null pointers,
+ * out_dt), ALIGNMENT, WORKSPACE, CUDA, UNSUPPORTED_DEVICE.
+ */
+cp_status cp_scored_attn_fwd(const void* q, const void* k, const void* v, void* out, float* lse, int B, int H, int Hkv,
+                             int Sq, int Skv, int D, float scale, const cp_score_rule* rule, void* workspace,
+                             size_t ws_bytes, cp_dtype dt, cp_dtype out_dt, void* stream);
+
+/*
+ * Backward: gradients of L = sum(out * dout).
+ *   out (out_dt: float32 or dt), lse: the forward's results over ALL keys of a
+ *   row (for a ring's block: the merged ones); dout [B, Sq, H, D] (dt);
+ *   dq [B, Sq, H, D], dk, dv [B, Skv, Hkv, D] of grad_dt: float32, or dt;
+ *   written, not accumulated. dk and dv sum the query heads that share them.
+ * No atomics: results do not depend on the order of execution. A row with
+ * lse = -inf adds nothing. Errors: as cp_scored_attn_fwd.
+ */
+cp_status cp_scored_attn_bwd(const void* q, const void* k, const void* v, const void* out, const void* dout,
+                             const float* lse, void* dq, void* dk, void* dv, int B, int H, int Hkv, int Sq, int Skv,
+                             int D, float scale, const cp_score_rule* rule, void* workspace, size_t ws_bytes,
+                             cp_dtype dt, cp_dtype out_dt, cp_dtype grad_dt, void* stream);
+
+/*
+ * The paged cache: k_cache, v_cache [num_pages, page_size, Hkv, D] (dt,
+ * dense); page_size a power of two up to 65536; num_pages * page_size < 2^31.
+ * block_table [B, max_pages] int32: token j of sequence b lies in row
+ * j % page_size of page block_table[b, j / page_size]. Entries past a
+ * sequence's tokens are not read. At most 4096 sequences a call.
+ * A page index outside [0, num_pages), a sequence length below 0 or past
+ * max_pages * page_size is recorded in the device error word
+ * (cp_check_device_status then returns CP_ERR_INVALID_ARG) and what it names
+ * is left out: append skips the token, decode takes the key as masked and the
+ * length as clamped.
+ */
+
+/*
+ * Writes new tokens' rows into the cache.
+ *   k_new, v_new [B, T, Hkv, D] (dt, dense); seq_lens [B] int32: tokens in the
+ *   cache before the call; new_lens [B] int32 or NULL: the first new_lens[b]
+ *   of the T rows are tokens (all, if NULL), the others padding.
+ * Token t < new_lens[b] goes to position seq_lens[b] + t; every other row of
+ * the cache keeps its bytes. seq_lens is not changed. Two tokens of one call
+ * must not share a row of the cache. Errors: INVALID_ARG, ALIGNMENT, CUDA,
+ * UNSUPPORTED_DEVICE.
+ */
+cp_status cp_paged_kv_append(const void* k_new, const void* v_new, void* k_cache, void* v_cache,
+                             const int32_t* block_table, const int32_t* seq_lens, const int32_t* new_lens, int B, int T,
+                             int Hkv, int D, int num_pages, int page_size, int max_pages, cp_dtype dt, void* stream);
+
+/* Host-only: bytes of device workspace of cp_paged_attn_decode (256-byte
+ * aligned start; every byte used is written before it is read). */
+size_t cp_paged_attn_workspace_size(int B, int H, int Hkv, int D, cp_dtype dt);
+
+/*
+ * Attention of one new token per sequence, q [B, H, D] (dt), over its
+ * seq_lens[b] cached tokens (the new one among them, at position
+ * seq_lens[b] - 1), scores as above with softcap and slopes: out [B, H, D]
+ * (out_dt: float32 or dt), lse [B, H] float32. Several sequences may share
+ * pages. A sequence of length 0 gets out = 0, lse = -inf. Calls that may
+ * overlap on the GPU (and captured graphs replayed at the same time) need a
+ * workspace each. Errors: INVALID_ARG, NOT_DIVISIBLE (H % Hkv), ALIGNMENT,
+ * WORKSPACE, CUDA, UNSUPPORTED_DEVICE.
+ */
+cp_status cp_paged_attn_decode(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
+                               const int32_t* seq_lens, void* out, float* lse, int B, int H, int Hkv, int D,
+                               int num_pages, int page_size, int max_pages, float scale, float softcap,
+                               const float* slopes, void* workspace, size_t ws_bytes, cp_dtype dt, cp_dtype out_dt,
+                               void* stream);
 
 #ifdef __cplusplus
 }
