@@ -17,6 +17,7 @@ struct DocRange {
   int lo, hi, neg, pad;
 };
 constexpr int kDocBlock = 64;
+constexpr int kScoreMaxTokens = 1 << 21;  // query rows or keys of a call
 
 // A scored attention launch. Tensors are dense: q, out, dout, dq [B, Sq, H, D];
 // k, v, dk, dv [B, Skv, Hkv, D]; lse, delta [B, H, Sq].
@@ -68,8 +69,10 @@ __device__ __forceinline__ bool docs_same(const DocRange& q, const DocRange& k) 
 
 // Fills qrange and krange from qdoc and kdoc.
 cudaError_t launch_doc_ranges(const ScoreArgs& a, cudaStream_t s);
+// bf16 on the tensor cores.
+cudaError_t launch_score_fwd_tc(const ScoreArgs& a, int D, cudaStream_t s);
 // fp32 on the CUDA cores.
-cudaError_t launch_score_fwd_f32(const ScoreArgs& a, int D, bool bf16, cudaStream_t s);
+cudaError_t launch_score_fwd_f32(const ScoreArgs& a, int D, cudaStream_t s);
 cudaError_t launch_score_bwd_f32(const ScoreArgs& a, int D, bool bf16, cudaStream_t s);
 
 // The paged cache.

@@ -18,7 +18,6 @@ using cp::PagedArgs;
 using cp::ScoreArgs;
 
 constexpr uint64_t kWaitTimeoutNs = 1000000000ull;  // 1 s per device-side wait
-constexpr int kMaxTokens = 1 << 24;                 // query rows or keys of one call
 constexpr int64_t kMaxPos = 1 << 30;                // positions stay within 31 bits
 constexpr int kMaxGrid = 65535;                     // batch entries, heads
 
@@ -93,7 +92,7 @@ cp_status cp_scored_attn_validate(int B, int H, int Hkv, int Sq, int Skv, int D,
                                   const cp_score_rule* rule, cp_dtype dt) {
   const cp_score_rule& r = rule ? *rule : kPlainRule;
   if (B < 0 || H < 1 || Hkv < 1 || Sq < 0 || Skv < 0 || (D != 64 && D != 128) || !known(dt)) return CP_ERR_INVALID_ARG;
-  if (B > kMaxGrid || H > kMaxGrid || Sq > kMaxTokens || Skv > kMaxTokens) return CP_ERR_INVALID_ARG;
+  if (B > kMaxGrid || H > kMaxGrid || Sq > cp::kScoreMaxTokens || Skv > cp::kScoreMaxTokens) return CP_ERR_INVALID_ARG;
   if (!std::isfinite(scale) || !std::isfinite(r.softcap) || r.softcap < 0.f) return CP_ERR_INVALID_ARG;
   if (r.q_pos0 < 0 || r.kv_pos0 < 0 || r.q_pos0 > kMaxPos || r.kv_pos0 > kMaxPos) return CP_ERR_INVALID_ARG;
   if ((r.q_docs == nullptr) != (r.kv_docs == nullptr)) return CP_ERR_INVALID_ARG;
@@ -135,7 +134,8 @@ cp_status cp_scored_attn_fwd(const void* q, const void* k, const void* v, void* 
   a.lse = lse;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (a.qdoc && cp::launch_doc_ranges(a, s) != cudaSuccess) return CP_ERR_CUDA;
-  return cp::launch_score_fwd_f32(a, D, dt == CP_BF16, s) == cudaSuccess ? CP_OK : CP_ERR_CUDA;
+  const cudaError_t e = dt == CP_BF16 ? cp::launch_score_fwd_tc(a, D, s) : cp::launch_score_fwd_f32(a, D, s);
+  return e == cudaSuccess ? CP_OK : CP_ERR_CUDA;
 }
 
 cp_status cp_scored_attn_bwd(const void* q, const void* k, const void* v, const void* out, const void* dout,

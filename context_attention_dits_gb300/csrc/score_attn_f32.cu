@@ -520,9 +520,8 @@ cudaError_t launch_doc_ranges(const ScoreArgs& a, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-cudaError_t launch_score_fwd_f32(const ScoreArgs& a, int D, bool bf16, cudaStream_t s) {
-  if (D == 64) return bf16 ? fwd_d<64, __nv_bfloat16>(a, s) : fwd_d<64, float>(a, s);
-  return bf16 ? fwd_d<128, __nv_bfloat16>(a, s) : fwd_d<128, float>(a, s);
+cudaError_t launch_score_fwd_f32(const ScoreArgs& a, int D, cudaStream_t s) {
+  return D == 64 ? fwd_d<64, float>(a, s) : fwd_d<128, float>(a, s);
 }
 
 cudaError_t launch_score_bwd_f32(const ScoreArgs& a, int D, bool bf16, cudaStream_t s) {

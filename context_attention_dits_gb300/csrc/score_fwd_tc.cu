@@ -1,0 +1,641 @@
+// score_fwd_tc.cu — forward of attention with a score rule on the
+// 5th-generation tensor cores (tcgen05 + TMEM + TMA), bf16 q, k, v.
+//
+// With s = q.k: x = scale s, capped to cap tanh(x / cap), less slope |i - j|;
+// out = softmax(x) v and lse = ln sum exp x over the pairs that take part.
+// A CTA owns two 128-row query tiles of one (batch entry, query head) and walks
+// the 128-key tiles that any of their rows reach, with the running maximum m,
+// sum l and unnormalised O of the online softmax; S and O live in tensor
+// memory, P = 2^(x log2e - m) is rounded to bf16 over S for the second product
+// (l sums P before the rounding, so lse has fp32's accuracy and the rounding
+// errors of out average out over the keys).
+//
+// Warp roles, TMEM layout and the MMA issue order are those of the plain
+// forward kernel (320 threads: TMA producer, MMA issuer, two groups of four
+// softmax warps, one thread per query row). What the rule adds sits in the
+// softmax warps and in the choice of tiles:
+//   * masks: causal with an open prefix is a limit per row (keys below
+//     max(position + 1, prefix)), applied only in the tiles it cuts; documents
+//     compare ids only in tiles that hold more than one. Tiles that no row
+//     reaches are not loaded: past the last row's limit, and, with documents,
+//     those whose id range misses the rows' (a bitmap in shared memory, built
+//     from the ranges of 64-row blocks that a small launch has put down);
+//   * cap: an odd polynomial in s while every |x / cap| of a warp's tile stays
+//     below 1/2 (or 1), checked after the fact by the largest s^2; see
+//     score_math.cuh;
+//   * bias: one more FMA a score in tiles on one side of the diagonal.
+// After the first tile P is formed with the running maximum and checked
+// afterwards by the row's sum (<= 2^8) and largest s^2; a warp that fails
+// reloads S and takes the exact path (maximum first). Long causal rows are
+// launched first, so that the short ones fill the last wave.
+// Every wait is bounded (cp_ptx.cuh); on expiry the CTA drains its copies and
+// MMAs, frees TMEM and returns.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <climits>
+#include <cmath>
+#include <cstdint>
+#include <type_traits>
+
+#include "cp_internal.h"
+#include "cp_ptx.cuh"
+#include "cp_score.h"
+#include "score_math.cuh"
+
+namespace cp {
+namespace {
+
+constexpr int kThreads = 320;
+constexpr float kRescaleThreshold = 8.0f;  // log2 units: rescale only when the max grows by > 2^8
+constexpr uint32_t kTmemCols = 512;
+constexpr int kMapWords = kScoreMaxTokens / kTileN / 32;  // bitmap of key tiles
+
+template <int D>
+struct Smem {
+  static constexpr int kQTile = kTileM * D * 2;   // bytes of one bf16 Q tile
+  static constexpr int kKVTile = kTileN * D * 2;  // bytes of one bf16 K or V tile
+  static constexpr int kHalf = kTileM * 128;      // one 64-column (128-byte) box of a 128-row tile
+  static constexpr int kOffQ = 0;
+  static constexpr int kOffK = kOffQ + 2 * kQTile;
+  static constexpr int kOffV = kOffK + 2 * kKVTile;
+  static constexpr int kOffBar = kOffV + 2 * kKVTile;
+  static constexpr int kNumBars = 17;
+  static constexpr int kOffMisc = kOffBar + kNumBars * 8;
+  static constexpr int kOffMap = kOffMisc + 24;              // act, then which tiles are mixed for query tile 0, 1
+  static constexpr int kBytes = kOffMap + 3 * kMapWords * 4;
+  // slack to align the base to 1024 bytes; at least 116 KB so that two CTAs
+  // never share an SM (each allocates all 512 TMEM columns)
+  static constexpr int kAlloc = (kBytes + 1024) > 116 * 1024 ? (kBytes + 1024) : 116 * 1024;
+};
+
+// barrier indices
+enum : int {
+  kBarQFull = 0,
+  kBarKFull = 1,   // +stage
+  kBarKEmpty = 3,  // +stage
+  kBarVFull = 5,   // +stage
+  kBarVEmpty = 7,  // +stage
+  kBarSFull = 9,   // +tile
+  kBarPFull = 11,  // +tile
+  kBarOFull = 13,  // +tile
+  kBarDrain = 15,
+  kBarQFull1 = 16,  // Q tile 1 (Q tile 0 completes kBarQFull)
+};
+
+// Bounded wait that ignores the abort flag (used while draining).
+__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, uint64_t timeout_ns) {
+  const uint64_t t0 = global_timer_ns();
+  for (uint32_t n = 1; !mbar_try_wait(bar, parity); ++n) {
+    if ((n & 255u) == 0 && global_timer_ns() - t0 > timeout_ns) return;
+  }
+}
+
+__device__ __forceinline__ float u2f(uint32_t x) { return __uint_as_float(x); }
+
+// Holds the uses of loaded registers behind the wait that precedes it.
+__device__ __forceinline__ void tmem_pin(uint32_t (&r)[32]) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 8)
+    asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]),
+                 "+r"(r[i + 6]), "+r"(r[i + 7]));
+}
+
+template <int D, bool kCap, bool kBias>
+__global__ void __launch_bounds__(kThreads, 1)
+    score_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+                        const __grid_constant__ CUtensorMap tv, const __grid_constant__ ScoreArgs a,
+                        const __grid_constant__ CapCoef cc) {
+  using L = Smem<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sb = smem_addr(smem);
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  uint32_t* misc = reinterpret_cast<uint32_t*>(smem + L::kOffMisc);  // [0] TMEM base, [1] abort flag, [2] tiles
+  volatile uint32_t* abort_flag = misc + 1;
+  uint32_t* act = reinterpret_cast<uint32_t*>(smem + L::kOffMap);
+  uint32_t* mixed = act + kMapWords;  // [2][kMapWords]
+  auto bar = [&](int i) -> uint32_t { return sb + L::kOffBar + 8 * i; };
+
+  // ---- work item: a pair of query tiles (the last may be single); the pairs
+  // with the most causal keys first, heads fastest ----
+  const int npair = (a.Sq + 2 * kTileM - 1) / (2 * kTileM);
+  const int bh = blockIdx.x % (a.H * a.B);
+  const int pair = npair - 1 - static_cast<int>(blockIdx.x / (a.H * a.B));
+  const int h = bh % a.H, b = bh / a.H, hk = h / a.G;
+  const int row0 = pair * 2 * kTileM;
+  const int nrows = min(2 * kTileM, a.Sq - row0);
+  const int nq = nrows > kTileM ? 2 : 1;
+  const int plim = prefix_limit(a, b);
+  // key tiles that the last row (the largest limit) reaches
+  const int ntile = (max(0, min(a.Skv, key_limit(a, plim, row0 + nrows - 1))) + kTileN - 1) / kTileN;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < L::kNumBars; ++i) mbar_init(bar(i), (i == kBarPFull || i == kBarPFull + 1) ? 4 : 1);
+    misc[1] = 0;
+    misc[2] = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_addr(misc), kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  int NT = ntile;
+  if (a.qdoc) {
+    const int nqb = (a.Sq + kDocBlock - 1) / kDocBlock, nkb = (a.Skv + kDocBlock - 1) / kDocBlock;
+    const DocRange* qr = a.qrange + static_cast<int64_t>(b) * nqb;
+    const DocRange* kr = a.krange + static_cast<int64_t>(b) * nkb;
+    const DocRange q0 = doc_span(qr, nqb, row0 / kDocBlock, 2), q1 = doc_span(qr, nqb, row0 / kDocBlock + 2, 2);
+    for (int t0 = warp * 32; t0 < ntile; t0 += kThreads) {
+      const int t = t0 + lane;
+      const DocRange k = doc_span(kr, nkb, 2 * t, 2);
+      const uint32_t w = __ballot_sync(0xffffffffu, t < ntile && (docs_meet(q0, k) || docs_meet(q1, k)));
+      const uint32_t m0 = __ballot_sync(0xffffffffu, !docs_same(q0, k)), m1 = __ballot_sync(0xffffffffu, !docs_same(q1, k));
+      if (lane == 0) {
+        act[t0 >> 5] = w;
+        mixed[t0 >> 5] = m0;
+        mixed[kMapWords + (t0 >> 5)] = m1;
+        atomicAdd(&misc[2], __popc(w));
+      }
+    }
+    __syncthreads();
+    NT = static_cast<int>(misc[2]);
+  }
+  const uint32_t* bits = a.qdoc ? act : nullptr;
+  const uint32_t tmem = misc[0];
+  const uint64_t tmo = a.timeout_ns;
+
+  if (warp == 0) {
+    // ===================== TMA producer =====================
+    const bool leader = elect_one();
+    if (NT > 0) {
+      if (leader) {
+        tma_prefetch_desc(&tq);
+        tma_prefetch_desc(&tk);
+        tma_prefetch_desc(&tv);
+      }
+      int k_issued[2] = {0, 0}, v_issued[2] = {0, 0};
+      auto load_q = [&](int i) {
+        if (!leader) return;
+        const uint32_t qb = bar(i == 0 ? kBarQFull : kBarQFull1);
+        mbar_arrive_expect_tx(qb, L::kQTile);
+        for (int c = 0; c < D / 64; ++c)
+          tma_load_4d(sb + L::kOffQ + i * L::kQTile + c * L::kHalf, &tq, qb, c * 64, h, row0 + i * kTileM, b);
+      };
+      load_q(0);
+      TileWalk cur(bits, 0, ntile);
+      for (int it = 0; it < NT; ++it) {
+        const int s = it & 1;
+        const uint32_t ph = (it >> 1) & 1;
+        if (!mbar_wait_bounded(bar(kBarKEmpty + s), ph ^ 1, abort_flag, a.err, tmo)) break;
+        if (leader) {
+          mbar_arrive_expect_tx(bar(kBarKFull + s), L::kKVTile);
+          for (int c = 0; c < D / 64; ++c)
+            tma_load_4d(sb + L::kOffK + s * L::kKVTile + c * L::kHalf, &tk, bar(kBarKFull + s), c * 64, hk,
+                        cur.t * kTileN, b);
+        }
+        ++k_issued[s];
+        if (it == 0 && nq == 2) load_q(1);
+        if (!mbar_wait_bounded(bar(kBarVEmpty + s), ph ^ 1, abort_flag, a.err, tmo)) break;
+        if (leader) {
+          mbar_arrive_expect_tx(bar(kBarVFull + s), L::kKVTile);
+          for (int c = 0; c < D / 64; ++c)
+            tma_load_4d(sb + L::kOffV + s * L::kKVTile + c * L::kHalf, &tv, bar(kBarVFull + s), c * 64, hk,
+                        cur.t * kTileN, b);
+        }
+        ++v_issued[s];
+        cur.next();
+      }
+      if (*abort_flag) {
+        // let every issued copy land before the CTA's shared memory goes away
+        drain_wait(bar(kBarQFull), 0, tmo);
+        if (nq == 2 && k_issued[0] > 0) drain_wait(bar(kBarQFull1), 0, tmo);
+        for (int s = 0; s < 2; ++s) {
+          if (k_issued[s]) drain_wait(bar(kBarKFull + s), (k_issued[s] - 1) & 1, tmo);
+          if (v_issued[s]) drain_wait(bar(kBarVFull + s), (v_issued[s] - 1) & 1, tmo);
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ===================== MMA issuer =====================
+    // The whole warp runs the loop (every operand is warp-uniform); one
+    // elected lane issues the MMAs and commits.
+    const bool leader = elect_one();
+    if (NT > 0) {
+      constexpr uint32_t idesc_s = idesc_bf16_f32(kTileM, kTileN, false, false);
+      constexpr uint32_t idesc_o = idesc_bf16_f32(kTileM, D, false, true);
+      // Descriptor halves of every operand buffer, built once (see
+      // mma_ss_lohi: nothing but an add may sit between two MMAs).
+      const uint64_t dq = smem_desc_sw128(sb + L::kOffQ, 16, 1024);
+      const uint64_t dk = smem_desc_sw128(sb + L::kOffK, 16, 1024);
+      const uint64_t dv = smem_desc_sw128(sb + L::kOffV, L::kHalf, 1024);
+      const uint32_t qk_hi = static_cast<uint32_t>(dq >> 32);  // same for Q and K (SBO 1024, 128B swizzle)
+      const uint32_t v_hi = static_cast<uint32_t>(dv >> 32);
+      const uint32_t q_lo = static_cast<uint32_t>(dq), k_lo = static_cast<uint32_t>(dk);
+      const uint32_t v_lo = static_cast<uint32_t>(dv);
+      auto commit = [&](uint32_t bar_addr) {
+        if (leader) mma_commit(bar_addr);
+      };
+      auto issue_s = [&](int i, int stage) {
+        const uint32_t a0 = q_lo + ((i * L::kQTile) >> 4);
+        const uint32_t b0 = k_lo + ((stage * L::kKVTile) >> 4);
+        const uint32_t d_tmem = tmem + i * kTileN;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = ((kk >> 2) * L::kHalf + (kk & 3) * 32) >> 4;
+          if (leader) mma_ss_lohi(d_tmem, a0 + off, qk_hi, b0 + off, qk_hi, idesc_s, kk > 0 ? 1u : 0u);
+        }
+      };
+      auto issue_pv = [&](int i, int stage, bool acc) {
+        const uint32_t b0 = v_lo + ((stage * L::kKVTile) >> 4);
+        const uint32_t d_tmem = tmem + 256 + i * D;
+        const uint32_t a_tmem = tmem + i * kTileN;
+        const uint32_t acc0 = acc ? 1u : 0u;
+#pragma unroll
+        for (int kk = 0; kk < kTileN / 16; ++kk)
+          if (leader) mma_ts_lohi(d_tmem, a_tmem + kk * 8, b0 + ((kk * 2048) >> 4), v_hi, idesc_o, kk > 0 ? 1u : acc0);
+      };
+      bool ok = mbar_wait_bounded(bar(kBarQFull), 0, abort_flag, a.err, tmo) &&
+                mbar_wait_bounded(bar(kBarKFull), 0, abort_flag, a.err, tmo);
+      if (ok) {
+        for (int i = 0; i < nq && ok; ++i) {
+          if (i == 1 && !mbar_wait_bounded(bar(kBarQFull1), 0, abort_flag, a.err, tmo)) {
+            ok = false;
+            break;
+          }
+          issue_s(i, 0);
+          commit(bar(kBarSFull + i));
+        }
+        if (ok) commit(bar(kBarKEmpty));
+      }
+      // The tensor pipe queues about one MMA: whatever this thread does
+      // between two MMA groups leaves the pipe idle. Each step therefore
+      // waits at two points only: V(it), K(it+1) and P_0(it) before
+      // PV_0(it) + S_0(it+1); P_1(it) before PV_1(it) + S_1(it+1). The step
+      // is instantiated per tile count and ring stage so that every MMA
+      // operand is a compile-time offset from one base: a run-time tile or
+      // stage index in the issue sequence measurably stalls the pipe.
+      auto step = [&](auto nq_c, auto stage_c, int it) -> bool {
+        constexpr int kNq = decltype(nq_c)::value;
+        constexpr int s = decltype(stage_c)::value;
+        constexpr int s2 = s ^ 1;
+        const uint32_t ph = (it >> 1) & 1;
+        const bool more = it + 1 < NT;
+        if (!mbar_wait_bounded(bar(kBarVFull + s), ph, abort_flag, a.err, tmo) ||
+            (more && !mbar_wait_bounded(bar(kBarKFull + s2), ((it + 1) >> 1) & 1, abort_flag, a.err, tmo)))
+          return false;
+#pragma unroll
+        for (int i = 0; i < kNq; ++i) {
+          if (!mbar_wait_bounded(bar(kBarPFull + i), it & 1, abort_flag, a.err, tmo)) return false;
+          tc_fence_after();
+          issue_pv(i, s, it > 0);
+          if (more) {
+            issue_s(i, s2);
+            commit(bar(kBarSFull + i));
+          } else {
+            commit(bar(kBarOFull + i));
+          }
+          if (i == kNq - 1) {
+            commit(bar(kBarVEmpty + s));
+            if (more) commit(bar(kBarKEmpty + s2));
+          }
+        }
+        return true;
+      };
+      auto run_steps = [&](auto nq_c) {
+        for (int it = 0; ok && it < NT; it += 2) {
+          ok = step(nq_c, std::integral_constant<int, 0>{}, it);
+          if (ok && it + 1 < NT) ok = step(nq_c, std::integral_constant<int, 1>{}, it + 1);
+        }
+      };
+      if (nq == 2)
+        run_steps(std::integral_constant<int, 2>{});
+      else
+        run_steps(std::integral_constant<int, 1>{});
+      if (!ok) {
+        commit(bar(kBarDrain));
+        drain_wait(bar(kBarDrain), 0, tmo);
+      }
+    }
+  } else if (warp >= 2) {
+    // ===================== softmax + epilogue =====================
+    const int i = (warp - 2) >> 2;  // query tile of this warpgroup
+    const int wq = warp & 3;        // TMEM lane quadrant of this warp (warp id mod 4)
+    const int row = wq * 32 + lane;
+    if (i < nq) {
+      const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
+      const uint32_t t_s = tmem + lane_off + i * kTileN;
+      const uint32_t t_o = tmem + lane_off + 256 + i * D;
+      const float sl2 = a.scale * kLog2e;
+      const int tok0 = row0 + i * kTileM;   // first row of this query tile
+      const int rows_valid = min(kTileM, a.Sq - tok0);
+      const int lim = min(a.Skv, key_limit(a, plim, tok0 + row));
+      const int qd = a.qdoc && row < rows_valid ? a.qdoc[static_cast<int64_t>(b) * a.Sq + tok0 + row] : -1;
+      const int* kd = a.kdoc + static_cast<int64_t>(b) * a.Skv;
+      const float slope2 = kBias ? a.slopes[h] * kLog2e : 0.f;
+      float m_used = -INFINITY, l = 0.f;
+      int level = 0;  // of the cap's polynomial: 3, 6 terms' range, or neither
+      bool ok = true;
+      TileWalk cur(bits, 0, ntile);
+      for (int it = 0; it < NT; ++it) {
+        const int kv0 = cur.t * kTileN;
+        const bool mix = bits != nullptr && ((mixed[i * kMapWords + (cur.t >> 5)] >> (cur.t & 31)) & 1u);
+        const int nv = lim - kv0;                  // this row's keys of the tile: those below nv
+        const int dq = a.rel + tok0 + row - kv0;   // position of the row less that of the tile's first key
+        const bool cut = __any_sync(0xffffffffu, nv < kTileN);
+        // where every pair that takes part has the same order, the bias is linear in the key
+        const bool below = __all_sync(0xffffffffu, dq >= kTileN - 1 || nv <= dq + 1);
+        const bool above = __all_sync(0xffffffffu, dq <= 0);
+        // the places that take part, a bit each (found before the wait, which hides it)
+        const bool masked = cut || mix;
+        uint32_t on[4] = {~0u, ~0u, ~0u, ~0u};
+        if (masked) {
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const int n = nv - 32 * w;
+            on[w] = n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u;
+          }
+        }
+        if (mix) {
+          const int nk = a.Skv - kv0;
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            uint32_t same = 0;
+#pragma unroll
+            for (int c = 0; c < 32; ++c) {
+              const int id = 32 * w + c < nk ? __ldg(kd + kv0 + 32 * w + c) : -1;  // the same word for the whole warp
+              same |= (id == qd ? 1u : 0u) << c;
+            }
+            on[w] &= qd >= 0 ? same : 0u;
+          }
+        }
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar(kBarSFull + i), it & 1, abort_flag, a.err, tmo));
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t pk[kTileN / 2];
+        // P = 2^(x - m) in pairs, rounded to bf16 into pk, 32 columns at a time
+        // (the next columns' load is under way meanwhile); returns the row sum
+        // before the rounding. kMode 1: no cap; 3, 6: the polynomial of that
+        // degree, umax the largest s^2.
+        float umax = 0.f;
+        auto speculate = [&](auto mode_c, auto mask_c) -> float {
+          constexpr int kMode = decltype(mode_c)::value;
+          constexpr bool kMask = decltype(mask_c)::value;
+          float ls[4] = {0.f, 0.f, 0.f, 0.f};
+          float um[4] = {0.f, 0.f, 0.f, 0.f};
+          const float bs = kBias ? (below ? slope2 : -slope2) : 0.f;
+          const float bb = kBias ? fmaf(-bs, static_cast<float>(dq), -m_used) : -m_used;
+          uint32_t buf[2][32];
+          tmem_ld32(t_s, buf[0]);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t(&sr)[32] = buf[c & 1];
+            tmem_wait_ld();
+            tmem_pin(sr);
+            if (c < 3) tmem_ld32(t_s + (c + 1) * 32, buf[(c + 1) & 1]);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              float s0 = u2f(sr[2 * e]), s1 = u2f(sr[2 * e + 1]);
+              const bool on0 = !kMask || ((on[c] >> (2 * e)) & 1u), on1 = !kMask || ((on[c] >> (2 * e + 1)) & 1u);
+              float x0, x1, f0 = sl2, f1 = sl2;
+              if constexpr (kMode >= 3) {
+                if (kMask) {
+                  s0 = on0 ? s0 : 0.f;
+                  s1 = on1 ? s1 : 0.f;
+                }
+                float u0, u1;
+                fma2(u0, u1, s0, s1, s0, s1, 0.f, 0.f);
+                um[e & 3] = fmax3(um[e & 3], u0, u1);
+                cap_poly<kMode>(cc, u0, u1, f0, f1);
+              }
+              const float b0 = kBias ? fmaf(bs, static_cast<float>(32 * c + 2 * e), bb) : bb;
+              const float b1 = kBias ? fmaf(bs, static_cast<float>(32 * c + 2 * e + 1), bb) : bb;
+              fma2(x0, x1, s0, s1, f0, f1, b0, b1);
+              if (kMask) {
+                x0 = on0 ? x0 : -INFINITY;
+                x1 = on1 ? x1 : -INFINITY;
+              }
+              const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+              pk[16 * c + e] = pack_bf16x2(p0, p1);
+              const int w = (2 * e) & 3;
+              fma2(ls[w], ls[w + 1], p0, p1, 1.f, 1.f, ls[w], ls[w + 1]);
+            }
+          }
+          umax = fmaxf(fmaxf(um[0], um[1]), fmaxf(um[2], um[3]));
+          return (ls[0] + ls[1]) + (ls[2] + ls[3]);
+        };
+        float f = 1.f, lsum = INFINITY;
+        bool fits = false;
+        // speculatively with the running maximum: every P is at most the row
+        // sum, so a sum within 2^8 proves that the row maximum is within 2^8 of
+        // the running one (an overflow, or a row that has seen no key yet, fails
+        // the test too); and s^2 within the polynomial's range
+        if (it > 0 && (!kBias || below || above)) {
+          using std::integral_constant;
+          if constexpr (kCap) {
+            if (level == 0) {
+              lsum = masked ? speculate(integral_constant<int, 3>{}, std::true_type{})
+                            : speculate(integral_constant<int, 3>{}, std::false_type{});
+              fits = lsum <= 256.f && umax <= cc.u3;
+            } else if (level == 1 && !masked) {
+              lsum = speculate(integral_constant<int, 6>{}, std::false_type{});
+              fits = lsum <= 256.f && umax <= cc.u6;
+            }
+          } else {
+            lsum = masked ? speculate(integral_constant<int, 1>{}, std::true_type{})
+                          : speculate(integral_constant<int, 1>{}, std::false_type{});
+            fits = lsum <= 256.f;
+          }
+        }
+        if (__all_sync(0xffffffffu, fits)) {
+          tmem_st32(t_s, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));
+          tmem_st32(t_s + 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[32]));
+        } else {
+          // exactly, 32 columns at a time: scores in log2 units back over S and
+          // their maximum; move to it if it grew by more than 2^8, rescaling O
+          // and l by the same factor (O is idle here: PV of the previous tile
+          // completed before S of this tile was committed, and PV of this tile
+          // waits for P); then P. Columns [16 c, 16 c + 16) of P lie over
+          // columns of S that have been read. A row that has seen no key keeps
+          // m = -inf and P = 0.
+          float mxs = -INFINITY, um = 0.f;
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t onw = c == 0 ? on[0] : c == 1 ? on[1] : c == 2 ? on[2] : on[3];
+            const float dc = static_cast<float>(dq - 32 * c);
+            uint32_t sr[32];
+            tmem_ld32(t_s + c * 32, sr);
+            tmem_wait_ld();
+            tmem_pin(sr);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const float s = u2f(sr[e]);
+              float x = kCap ? cap_exact(cc, s) : s * sl2;
+              if (kBias) x = fmaf(-slope2, fabsf(dc - static_cast<float>(e)), x);
+              const bool live = (onw >> e) & 1u;
+              x = live ? x : -INFINITY;
+              if (kCap) um = fmaxf(um, live ? s * s : 0.f);
+              mxs = fmaxf(mxs, x);
+              sr[e] = __float_as_uint(x);
+            }
+            tmem_st32(t_s + c * 32, sr);
+          }
+          tmem_wait_st();
+          if (kCap) {
+            const float w = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(um)));
+            level = w <= cc.u3 ? 0 : w <= cc.u6 ? 1 : 2;
+          }
+          const bool need = mxs > m_used + kRescaleThreshold || (m_used == -INFINITY && mxs > -INFINITY);
+          if (need) {
+            f = ex2_approx(m_used - mxs);
+            m_used = mxs;
+          }
+          const float nm = m_used == -INFINITY ? 0.f : -m_used;
+          lsum = 0.f;
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t sr[32], pw[16];
+            tmem_ld32(t_s + c * 32, sr);
+            tmem_wait_ld();
+            tmem_pin(sr);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float p0 = ex2_approx(u2f(sr[2 * e]) + nm), p1 = ex2_approx(u2f(sr[2 * e + 1]) + nm);
+              pw[e] = pack_bf16x2(p0, p1);
+              lsum += p0 + p1;
+            }
+            tmem_st16(t_s + c * 16, pw);
+          }
+          if (it > 0 && __any_sync(0xffffffffu, need)) {
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[32];
+              tmem_ld32(t_o + c * 32, o);
+              tmem_wait_ld();
+              tmem_pin(o);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(u2f(o[e]) * f);
+              tmem_st32(t_o + c * 32, o);
+            }
+          }
+        }
+        l = l * f + lsum;
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarPFull + i));
+        cur.next();
+      }
+      if (ok && NT > 0) ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar(kBarOFull + i), 0, abort_flag, a.err, tmo));
+      if (ok) {
+        tc_fence_after();
+        // l = 0: no key -> out 0, lse -inf
+        const float inv_l = l != 0.f ? 1.f / l : 0.f;
+        if (row < rows_valid)
+          a.lse[(static_cast<int64_t>(b) * a.H + h) * a.Sq + tok0 + row] =
+              l != 0.f ? (m_used + log2f(l)) * kLn2 : -INFINITY;
+        uint32_t o[D];
+        if (NT > 0) {
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) tmem_ld32(t_o + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&o[c * 32]));
+          tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int e = 0; e < D; ++e) o[e] = 0u;
+        }
+        // 32 rows x 32 words a pass (32 fp32 columns, or 64 in bf16) staged in
+        // this tile's idle Q buffer, 128-byte swizzled, and stored 4 rows x 128
+        // contiguous bytes per warp instruction
+        const int64_t base = (static_cast<int64_t>(b) * a.Sq + tok0) * a.H + h;  // in rows of D
+        uint32_t* stage = reinterpret_cast<uint32_t*>(smem + L::kOffQ + i * L::kQTile + wq * 4096);
+        auto flush = [&](uint8_t* dst, int row_bytes) {
+          __syncwarp();
+#pragma unroll
+          for (int pass = 0; pass < 8; ++pass) {
+            const int rr = pass * 4 + (lane >> 3), q4 = lane & 7;
+            const uint4 val = *reinterpret_cast<const uint4*>(stage + rr * 32 + ((q4 ^ (rr & 7)) * 4));
+            if (wq * 32 + rr < rows_valid)
+              *reinterpret_cast<uint4*>(dst + (base + static_cast<int64_t>(wq * 32 + rr) * a.H) * row_bytes + q4 * 16) = val;
+          }
+          __syncwarp();  // the buffer is read before it is staged again
+        };
+        if (a.out_bf16) {
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c) {
+#pragma unroll
+            for (int q4 = 0; q4 < 8; ++q4) {
+              const uint32_t* oc = &o[c * 64 + 8 * q4];
+              uint4 val;
+              val.x = pack_bf16x2(u2f(oc[0]) * inv_l, u2f(oc[1]) * inv_l);
+              val.y = pack_bf16x2(u2f(oc[2]) * inv_l, u2f(oc[3]) * inv_l);
+              val.z = pack_bf16x2(u2f(oc[4]) * inv_l, u2f(oc[5]) * inv_l);
+              val.w = pack_bf16x2(u2f(oc[6]) * inv_l, u2f(oc[7]) * inv_l);
+              *reinterpret_cast<uint4*>(stage + lane * 32 + ((q4 ^ (lane & 7)) * 4)) = val;
+            }
+            flush(static_cast<uint8_t*>(a.out) + c * 128, D * 2);
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+#pragma unroll
+            for (int q4 = 0; q4 < 8; ++q4) {
+              const uint32_t* oc = &o[c * 32 + 4 * q4];
+              const float4 val = make_float4(u2f(oc[0]) * inv_l, u2f(oc[1]) * inv_l, u2f(oc[2]) * inv_l, u2f(oc[3]) * inv_l);
+              *reinterpret_cast<float4*>(stage + lane * 32 + ((q4 ^ (lane & 7)) * 4)) = val;
+            }
+            flush(static_cast<uint8_t*>(a.out) + c * 128, D * 4);
+          }
+        }
+      }
+    }
+  }
+
+  // ---- teardown: every thread of the CTA arrives here, aborted or not ----
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+template <int D, bool kCap, bool kBias>
+cudaError_t launch_rule(const ScoreArgs& a, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                        cudaStream_t s) {
+  using L = Smem<D>;
+  static_assert(L::kAlloc <= 227 * 1024, "shared memory budget");
+  auto kernel = score_fwd_tc_kernel<D, kCap, kBias>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
+  if (e != cudaSuccess) return e;
+  const int64_t items = static_cast<int64_t>((a.Sq + 2 * kTileM - 1) / (2 * kTileM)) * a.H * a.B;
+  if (items > 0x7fffffff) return cudaErrorInvalidValue;
+  kernel<<<dim3(static_cast<unsigned>(items)), kThreads, L::kAlloc, s>>>(tq, tk, tv, a, make_cap_coef(a.scale, a.cap));
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_d(const ScoreArgs& a, cudaStream_t s) {
+  CUtensorMap tq, tk, tv;
+  // without keys the maps of k and v are never read through
+  const bool none = a.Skv == 0;
+  if (!host_tmap_bf16(&tq, a.q, D, a.H, a.Sq, a.B, kTileM) ||
+      !host_tmap_bf16(&tk, none ? a.q : a.k, D, none ? a.H : a.Hkv, none ? a.Sq : a.Skv, a.B, kTileN) ||
+      !host_tmap_bf16(&tv, none ? a.q : a.v, D, none ? a.H : a.Hkv, none ? a.Sq : a.Skv, a.B, kTileN))
+    return cudaErrorInvalidValue;
+  if (a.cap > 0.f) return a.slopes ? launch_rule<D, true, true>(a, tq, tk, tv, s) : launch_rule<D, true, false>(a, tq, tk, tv, s);
+  return a.slopes ? launch_rule<D, false, true>(a, tq, tk, tv, s) : launch_rule<D, false, false>(a, tq, tk, tv, s);
+}
+
+}  // namespace
+
+cudaError_t launch_score_fwd_tc(const ScoreArgs& a, int D, cudaStream_t s) {
+  return D == 64 ? launch_d<64>(a, s) : launch_d<128>(a, s);
+}
+
+}  // namespace cp

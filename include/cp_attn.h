@@ -407,7 +407,7 @@ typedef struct {
 
 /* Host-only: the status the two calls below return for these sizes before
  * looking at a tensor's pointer. rule may be NULL (no cap, bias or mask). INVALID_ARG: a size, D not
- * 64 or 128, more than 65535 batch entries or heads or 2^24 rows, a scale or
+ * 64 or 128, more than 65535 batch entries or heads or 2^21 rows, a scale or
  * softcap that is not finite (or a negative softcap), a position out of range,
  * one of q_docs, kv_docs without the other; UNSUPPORTED_COMBO: prefix_lens
  * without causal; NOT_DIVISIBLE: H % Hkv. */
