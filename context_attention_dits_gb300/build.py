@@ -22,8 +22,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "libcpattn.so")
-SOURCES = ["attn_tc.cu", "attn_bwd.cu", "attn_bwd_tc.cu", "kernels_simt.cu", "score_fwd_tc.cu", "score_attn_f32.cu",
-           "paged.cu", "cp_score_api.cu", "cp_api.cu"]
+SOURCES = ["attn_tc.cu", "attn_bwd.cu", "attn_bwd_tc.cu", "kernels_simt.cu", "score_fwd_tc.cu", "score_bwd_tc.cu",
+           "score_attn_f32.cu", "paged.cu", "cp_score_api.cu", "cp_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -38,7 +38,9 @@ struct ScoreArgs {
   const void *o, *dout;  // backward: the forward's out, and its gradient
   void* out;             // forward
   float* lse;            // forward: written; backward: read
-  float* delta;          // backward
+  float* delta;          // backward, fp32 inputs: [B, H, Sq]
+  float* lse2p;          // backward, bf16: lse log2e and delta, each (batch entry, head) padded to 64 rows
+  float* dltp;
   void *dq, *dk, *dv;
   int out_bf16;   // type of out
   int grad_bf16;  // type of dq, dk, dv
@@ -71,9 +73,10 @@ __device__ __forceinline__ bool docs_same(const DocRange& q, const DocRange& k) 
 cudaError_t launch_doc_ranges(const ScoreArgs& a, cudaStream_t s);
 // bf16 on the tensor cores.
 cudaError_t launch_score_fwd_tc(const ScoreArgs& a, int D, cudaStream_t s);
+cudaError_t launch_score_bwd_tc(const ScoreArgs& a, int D, cudaStream_t s);
 // fp32 on the CUDA cores.
 cudaError_t launch_score_fwd_f32(const ScoreArgs& a, int D, cudaStream_t s);
-cudaError_t launch_score_bwd_f32(const ScoreArgs& a, int D, bool bf16, cudaStream_t s);
+cudaError_t launch_score_bwd_f32(const ScoreArgs& a, int D, cudaStream_t s);
 
 // The paged cache.
 constexpr int kPagedCtas = 304;     // decode CTAs: two on each of 152 multiprocessors

@@ -32,10 +32,11 @@ const cp_score_rule kPlainRule = {0.f, nullptr, 0, nullptr, nullptr, nullptr, 0,
 
 int64_t doc_blocks(int S) { return (static_cast<int64_t>(S) + cp::kDocBlock - 1) / cp::kDocBlock; }
 
-// Workspace of the forward: the document ranges of q and k. The backward adds
-// delta [B, H, Sq] in front.
+// Workspace of the forward: the document ranges of q and k. The backward has
+// lse log2e and delta in front, each (batch entry, head) padded to 64 rows
+// (fp32 inputs use delta alone, unpadded).
 struct ScoreWs {
-  size_t delta = 0, qr = 0, kr = 0, total = 0;
+  size_t lse = 0, delta = 0, qr = 0, kr = 0, total = 0;
 };
 ScoreWs score_ws(int B, int H, int Sq, int Skv, bool docs, bool bwd) {
   ScoreWs w;
@@ -45,7 +46,11 @@ ScoreWs score_ws(int B, int H, int Sq, int Skv, bool docs, bool bwd) {
     o = round_up(o + bytes, 256);
     return at;
   };
-  if (bwd) w.delta = take(static_cast<size_t>(B) * H * Sq * 4);
+  if (bwd) {
+    const size_t rows = static_cast<size_t>(B) * H * doc_blocks(Sq) * cp::kDocBlock;
+    w.lse = take(rows * 4);
+    w.delta = take(rows * 4);
+  }
   if (docs) {
     w.qr = take(static_cast<size_t>(B) * doc_blocks(Sq) * sizeof(DocRange));
     w.kr = take(static_cast<size_t>(B) * doc_blocks(Skv) * sizeof(DocRange));
@@ -170,13 +175,16 @@ cp_status cp_scored_attn_bwd(const void* q, const void* k, const void* v, const 
   a.dout = dout;
   a.lse = const_cast<float*>(lse);
   a.delta = reinterpret_cast<float*>(ws + w.delta);
+  a.lse2p = reinterpret_cast<float*>(ws + w.lse);
+  a.dltp = a.delta;
   a.dq = dq;
   a.dk = dk;
   a.dv = dv;
   a.grad_bf16 = grad_dt == CP_BF16;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (a.qdoc && cp::launch_doc_ranges(a, s) != cudaSuccess) return CP_ERR_CUDA;
-  return cp::launch_score_bwd_f32(a, D, dt == CP_BF16, s) == cudaSuccess ? CP_OK : CP_ERR_CUDA;
+  const cudaError_t e = dt == CP_BF16 ? cp::launch_score_bwd_tc(a, D, s) : cp::launch_score_bwd_f32(a, D, s);
+  return e == cudaSuccess ? CP_OK : CP_ERR_CUDA;
 }
 
 // ---------------------------------------------------------------------------

@@ -17,7 +17,6 @@
 // float4 column of 16 neighbouring rows then takes two wavefronts (the least
 // for 256 bytes), so one copy of K serves both Q K^T and dS K and nothing is
 // transposed. A 4 x 4 block costs 8 16-byte loads per 64 FMAs.
-#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <climits>
@@ -37,28 +36,15 @@ constexpr float kL2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.69314718055994531f;
 
 __device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
-  const uint2 v = *reinterpret_cast<const uint2*>(p);
-  const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v.x));
-  const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v.y));
-  return make_float4(a.x, a.y, b.x, b.y);
-}
-__device__ __forceinline__ void store4(void* base, int64_t i, bool bf16, float4 x) {
-  if (bf16) {
-    const __nv_bfloat162 lo = __floats2bfloat162_rn(x.x, x.y), hi = __floats2bfloat162_rn(x.z, x.w);
-    uint2 u;
-    u.x = *reinterpret_cast<const uint32_t*>(&lo);
-    u.y = *reinterpret_cast<const uint32_t*>(&hi);
-    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(base) + i) = u;
-  } else {
-    *reinterpret_cast<float4*>(static_cast<float*>(base) + i) = x;
-  }
+
+__device__ __forceinline__ void store4(void* base, int64_t i, float4 x) {
+  *reinterpret_cast<float4*>(static_cast<float*>(base) + i) = x;
 }
 
 // Rows row0 .. row0 + n - 1 (of `rows`; the others zero) of a [., S, heads, D]
 // tensor's head into dst, D + 4 floats a row.
-template <int D, typename T>
-__device__ __forceinline__ void load_rows(float* dst, const T* src, int64_t stride, int n, int rows) {
+template <int D>
+__device__ __forceinline__ void load_rows(float* dst, const float* src, int64_t stride, int n, int rows) {
   for (int e = threadIdx.x; e < rows * (D / 4); e += kThr) {
     const int r = e / (D / 4), d = (e % (D / 4)) * 4;
     const float4 x = r < n ? load4(src + r * stride + d) : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -141,7 +127,7 @@ constexpr int fwd_floats() {
   return (kR + 2 * kC) * (D + 4) + kC * kPT;
 }
 
-template <int D, typename T>
+template <int D>
 __global__ void __launch_bounds__(kThr) score_fwd_f32_kernel(const __grid_constant__ ScoreArgs a) {
   extern __shared__ __align__(16) float sm[];
   float* Q = sm;
@@ -155,7 +141,7 @@ __global__ void __launch_bounds__(kThr) score_fwd_f32_kernel(const __grid_consta
   const int64_t qs = static_cast<int64_t>(a.H) * D, ks = static_cast<int64_t>(a.Hkv) * D;
   const int64_t qo = (static_cast<int64_t>(b) * a.Sq + row0) * qs + static_cast<int64_t>(h) * D;
   const int64_t ko = static_cast<int64_t>(b) * a.Skv * ks + static_cast<int64_t>(hk) * D;
-  load_rows<D>(Q, static_cast<const T*>(a.q) + qo, qs, nrows, kR);
+  load_rows<D>(Q, static_cast<const float*>(a.q) + qo, qs, nrows, kR);
   const Scorer score(a, h);
   const int plim = prefix_limit(a, b);
   int lim[4], qd[4];
@@ -178,8 +164,8 @@ __global__ void __launch_bounds__(kThr) score_fwd_f32_kernel(const __grid_consta
     if (a.qdoc && !docs_meet(qr, doc_range(a.krange, b, a.Skv, k0))) continue;
     const int nk = min(kC, a.Skv - k0);
     __syncthreads();  // the last tile's readers are done
-    load_rows<D>(K, static_cast<const T*>(a.k) + ko + k0 * ks, ks, nk, kC);
-    load_rows<D>(V, static_cast<const T*>(a.v) + ko + k0 * ks, ks, nk, kC);
+    load_rows<D>(K, static_cast<const float*>(a.k) + ko + k0 * ks, ks, nk, kC);
+    load_rows<D>(V, static_cast<const float*>(a.v) + ko + k0 * ks, ks, nk, kC);
     __syncthreads();
     float s[4][4];
     dots<D>(s, Q, K, ti, tj);
@@ -232,7 +218,7 @@ __global__ void __launch_bounds__(kThr) score_fwd_f32_kernel(const __grid_consta
     const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;
 #pragma unroll
     for (int u = 0; u < D / 64; ++u)
-      store4(a.out, qo + r * qs + 4 * tj + 64 * u, a.out_bf16,
+      store4(a.out, qo + r * qs + 4 * tj + 64 * u,
              make_float4(acc[i][u].x * inv, acc[i][u].y * inv, acc[i][u].z * inv, acc[i][u].w * inv));
     if (tj == 0)
       a.lse[(static_cast<int64_t>(b) * a.H + h) * a.Sq + row0 + r] =
@@ -241,7 +227,7 @@ __global__ void __launch_bounds__(kThr) score_fwd_f32_kernel(const __grid_consta
 }
 
 // delta[b, h, i] = out_i . dout_i, a warp per row of [B, Sq, H, D]
-template <int D, typename T>
+template <int D>
 __global__ void __launch_bounds__(256) score_delta_kernel(const __grid_constant__ ScoreArgs a) {
   const int lane = threadIdx.x & 31;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
@@ -249,9 +235,8 @@ __global__ void __launch_bounds__(256) score_delta_kernel(const __grid_constant_
   const int64_t h = row % a.H, bs = row / a.H, s = bs % a.Sq, b = bs / a.Sq;
   float sum = 0.f;
   if (lane * 4 < D) {
-    const float4 g = load4(static_cast<const T*>(a.dout) + row * D + lane * 4);
-    const float4 o = a.out_bf16 ? load4(static_cast<const __nv_bfloat16*>(a.o) + row * D + lane * 4)
-                                : load4(static_cast<const float*>(a.o) + row * D + lane * 4);
+    const float4 g = load4(static_cast<const float*>(a.dout) + row * D + lane * 4);
+    const float4 o = load4(static_cast<const float*>(a.o) + row * D + lane * 4);
     sum = fmaf(g.x, o.x, fmaf(g.y, o.y, fmaf(g.z, o.z, g.w * o.w)));
   }
 #pragma unroll
@@ -272,7 +257,7 @@ constexpr int bwd_floats() {
   return (2 * kR + 2 * kC) * (D + 4) + kC * kPT + 2 * kC;
 }
 
-template <int D, typename T>
+template <int D>
 __global__ void __launch_bounds__(kThr) score_dq_f32_kernel(const __grid_constant__ ScoreArgs a) {
   extern __shared__ __align__(16) float sm[];
   float* Q = sm;
@@ -287,8 +272,8 @@ __global__ void __launch_bounds__(kThr) score_dq_f32_kernel(const __grid_constan
   const int64_t qs = static_cast<int64_t>(a.H) * D, ks = static_cast<int64_t>(a.Hkv) * D;
   const int64_t qo = (static_cast<int64_t>(b) * a.Sq + row0) * qs + static_cast<int64_t>(h) * D;
   const int64_t ko = static_cast<int64_t>(b) * a.Skv * ks + static_cast<int64_t>(hk) * D;
-  load_rows<D>(Q, static_cast<const T*>(a.q) + qo, qs, nrows, kR);
-  load_rows<D>(dO, static_cast<const T*>(a.dout) + qo, qs, nrows, kR);
+  load_rows<D>(Q, static_cast<const float*>(a.q) + qo, qs, nrows, kR);
+  load_rows<D>(dO, static_cast<const float*>(a.dout) + qo, qs, nrows, kR);
   const Scorer score(a, h);
   const int plim = prefix_limit(a, b);
   int lim[4], qd[4];
@@ -312,8 +297,8 @@ __global__ void __launch_bounds__(kThr) score_dq_f32_kernel(const __grid_constan
     if (a.qdoc && !docs_meet(qr, doc_range(a.krange, b, a.Skv, k0))) continue;
     const int nk = min(kC, a.Skv - k0);
     __syncthreads();
-    load_rows<D>(K, static_cast<const T*>(a.k) + ko + k0 * ks, ks, nk, kC);
-    load_rows<D>(V, static_cast<const T*>(a.v) + ko + k0 * ks, ks, nk, kC);
+    load_rows<D>(K, static_cast<const float*>(a.k) + ko + k0 * ks, ks, nk, kC);
+    load_rows<D>(V, static_cast<const float*>(a.v) + ko + k0 * ks, ks, nk, kC);
     __syncthreads();
     float s[4][4], dp[4][4];
     dots<D>(s, Q, K, ti, tj);
@@ -341,7 +326,7 @@ __global__ void __launch_bounds__(kThr) score_dq_f32_kernel(const __grid_constan
     if (r >= nrows) continue;
 #pragma unroll
     for (int u = 0; u < D / 64; ++u)
-      store4(a.dq, qo + r * qs + 4 * tj + 64 * u, a.grad_bf16,
+      store4(a.dq, qo + r * qs + 4 * tj + 64 * u,
              make_float4(acc[i][u].x * a.scale, acc[i][u].y * a.scale, acc[i][u].z * a.scale, acc[i][u].w * a.scale));
   }
 }
@@ -349,7 +334,7 @@ __global__ void __launch_bounds__(kThr) score_dq_f32_kernel(const __grid_constan
 // dk, dv of 32 keys: the streamed tiles are 64 query rows of each head that
 // shares the key/value head, head by head. Scores are formed transposed (rows
 // are keys), and P^T and then dS^T pass through one buffer.
-template <int D, typename T>
+template <int D>
 __global__ void __launch_bounds__(kThr) score_dkdv_f32_kernel(const __grid_constant__ ScoreArgs a) {
   extern __shared__ __align__(16) float sm[];
   float* K = sm;
@@ -365,8 +350,8 @@ __global__ void __launch_bounds__(kThr) score_dkdv_f32_kernel(const __grid_const
   const int nk = min(kR, a.Skv - key0);
   const int64_t qs = static_cast<int64_t>(a.H) * D, ks = static_cast<int64_t>(a.Hkv) * D;
   const int64_t ko = (static_cast<int64_t>(b) * a.Skv + key0) * ks + static_cast<int64_t>(hk) * D;
-  load_rows<D>(K, static_cast<const T*>(a.k) + ko, ks, nk, kR);
-  load_rows<D>(V, static_cast<const T*>(a.v) + ko, ks, nk, kR);
+  load_rows<D>(K, static_cast<const float*>(a.k) + ko, ks, nk, kR);
+  load_rows<D>(V, static_cast<const float*>(a.v) + ko, ks, nk, kR);
   const int plim = prefix_limit(a, b);
   int kd[4];
   float4 dk[4][D / 64], dv[4][D / 64];
@@ -390,8 +375,8 @@ __global__ void __launch_bounds__(kThr) score_dkdv_f32_kernel(const __grid_const
       const int64_t qo = (static_cast<int64_t>(b) * a.Sq + q0) * qs + static_cast<int64_t>(h) * D;
       const int64_t lo = (static_cast<int64_t>(b) * a.H + h) * a.Sq + q0;
       __syncthreads();
-      load_rows<D>(Q, static_cast<const T*>(a.q) + qo, qs, nq, kC);
-      load_rows<D>(dO, static_cast<const T*>(a.dout) + qo, qs, nq, kC);
+      load_rows<D>(Q, static_cast<const float*>(a.q) + qo, qs, nq, kC);
+      load_rows<D>(dO, static_cast<const float*>(a.dout) + qo, qs, nq, kC);
       if (threadIdx.x < kC) {
         const int r = threadIdx.x;
         lse2[r] = lse2_of(a, lo + r, r < nq);
@@ -435,9 +420,9 @@ __global__ void __launch_bounds__(kThr) score_dkdv_f32_kernel(const __grid_const
     if (r >= nk) continue;
 #pragma unroll
     for (int u = 0; u < D / 64; ++u) {
-      store4(a.dk, ko + r * ks + 4 * tj + 64 * u, a.grad_bf16,
+      store4(a.dk, ko + r * ks + 4 * tj + 64 * u,
              make_float4(dk[i][u].x * a.scale, dk[i][u].y * a.scale, dk[i][u].z * a.scale, dk[i][u].w * a.scale));
-      store4(a.dv, ko + r * ks + 4 * tj + 64 * u, a.grad_bf16, dv[i][u]);
+      store4(a.dv, ko + r * ks + 4 * tj + 64 * u, dv[i][u]);
     }
   }
 }
@@ -481,30 +466,30 @@ cudaError_t allow_smem(K kernel, int bytes) {
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
-template <int D, typename T>
+template <int D>
 cudaError_t fwd_d(const ScoreArgs& a, cudaStream_t s) {
   constexpr int bytes = fwd_floats<D>() * 4;
-  cudaError_t e = allow_smem(score_fwd_f32_kernel<D, T>, bytes);
+  cudaError_t e = allow_smem(score_fwd_f32_kernel<D>, bytes);
   if (e != cudaSuccess) return e;
-  score_fwd_f32_kernel<D, T><<<dim3((a.Sq + kR - 1) / kR, a.H, a.B), kThr, bytes, s>>>(a);
+  score_fwd_f32_kernel<D><<<dim3((a.Sq + kR - 1) / kR, a.H, a.B), kThr, bytes, s>>>(a);
   return cudaGetLastError();
 }
 
-template <int D, typename T>
+template <int D>
 cudaError_t bwd_d(const ScoreArgs& a, cudaStream_t s) {
   constexpr int bytes = bwd_floats<D>() * 4;
-  cudaError_t e = allow_smem(score_dq_f32_kernel<D, T>, bytes);
-  if (e == cudaSuccess) e = allow_smem(score_dkdv_f32_kernel<D, T>, bytes);
+  cudaError_t e = allow_smem(score_dq_f32_kernel<D>, bytes);
+  if (e == cudaSuccess) e = allow_smem(score_dkdv_f32_kernel<D>, bytes);
   if (e != cudaSuccess) return e;
   if (a.Sq > 0) {
     const int64_t rows = static_cast<int64_t>(a.B) * a.Sq * a.H;
-    score_delta_kernel<D, T><<<static_cast<unsigned>((rows + 7) / 8), 256, 0, s>>>(a);
+    score_delta_kernel<D><<<static_cast<unsigned>((rows + 7) / 8), 256, 0, s>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    score_dq_f32_kernel<D, T><<<dim3((a.Sq + kR - 1) / kR, a.H, a.B), kThr, bytes, s>>>(a);
+    score_dq_f32_kernel<D><<<dim3((a.Sq + kR - 1) / kR, a.H, a.B), kThr, bytes, s>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   if (a.Skv > 0) {
-    score_dkdv_f32_kernel<D, T><<<dim3((a.Skv + kR - 1) / kR, a.Hkv, a.B), kThr, bytes, s>>>(a);
+    score_dkdv_f32_kernel<D><<<dim3((a.Skv + kR - 1) / kR, a.Hkv, a.B), kThr, bytes, s>>>(a);
     e = cudaGetLastError();
   }
   return e;
@@ -521,12 +506,11 @@ cudaError_t launch_doc_ranges(const ScoreArgs& a, cudaStream_t s) {
 }
 
 cudaError_t launch_score_fwd_f32(const ScoreArgs& a, int D, cudaStream_t s) {
-  return D == 64 ? fwd_d<64, float>(a, s) : fwd_d<128, float>(a, s);
+  return D == 64 ? fwd_d<64>(a, s) : fwd_d<128>(a, s);
 }
 
-cudaError_t launch_score_bwd_f32(const ScoreArgs& a, int D, bool bf16, cudaStream_t s) {
-  if (D == 64) return bf16 ? bwd_d<64, __nv_bfloat16>(a, s) : bwd_d<64, float>(a, s);
-  return bf16 ? bwd_d<128, __nv_bfloat16>(a, s) : bwd_d<128, float>(a, s);
+cudaError_t launch_score_bwd_f32(const ScoreArgs& a, int D, cudaStream_t s) {
+  return D == 64 ? bwd_d<64>(a, s) : bwd_d<128>(a, s);
 }
 
 }  // namespace cp

@@ -1,0 +1,971 @@
+// score_bwd_tc.cu — backward of attention with a score rule on the
+// 5th-generation tensor cores (tcgen05, bf16 operands, fp32 accumulators in
+// tensor memory). With y = the capped score, x = y less the bias:
+//   p_ij = exp(x_ij - lse_i), ds_ij = p_ij (dout_i.v_j - delta_i) (1 - (y_ij / cap)^2),
+//   dv_j = sum p_ij dout_i, dk_j = scale sum ds_ij q_i (over rows i and the
+//   query heads that share the key/value head), dq_i = scale sum_j ds_ij k_j.
+//
+// Two kinds of CTA in one launch, neither with atomics, as in the plain
+// backward: dk/dv CTAs (128 keys of one key/value head; 64-row query sub-tiles
+// of each of its query heads stream by) and then dq CTAs (128 query rows; 64-key
+// sub-tiles stream by). S and dP are formed in both, 14 D flop a pair instead
+// of 10, in exchange for no reduction of dq across key tiles. TMEM and
+// shared-memory layout, the two TMEM slots that let the row pass of one
+// sub-step run beside the products of the other, and the issue order are those
+// of the plain backward. What the rule adds:
+//   * only the sub-tiles that hold a pair are walked: causal and prefix give a
+//     range, documents a bitmap built from the ranges of 64-row blocks;
+//   * the row pass, a thread per row and column half, masks the sub-tiles that
+//     a limit or a document border cuts, and forms y and its derivative by the
+//     cap's polynomial (score_math.cuh) while the warp's scores stay in its
+//     range, exactly otherwise;
+//   * lse log2e and delta come from copies padded to 64 rows a (batch entry,
+//     head), written by the delta kernel, so that a sub-tile's are one aligned
+//     bulk copy. Rows past the end, and rows that saw no key, hold +inf: p = 0.
+// P and dS are rounded to bf16 for their products; all sums are fp32.
+// Warp roles (320 threads): 0 = TMA producer, 1 = MMA issuer, 2-9 = row warps,
+// two per TMEM lane quarter, one per 32-column half of a sub-step.
+// The longest CTAs of each kind are launched first. Every wait is bounded; on
+// expiry the CTA records a timeout, lets its copies land, frees its tensor
+// memory and returns.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <climits>
+#include <cmath>
+#include <cstdint>
+#include <type_traits>
+
+#include "cp_internal.h"
+#include "cp_ptx.cuh"
+#include "cp_score.h"
+#include "score_math.cuh"
+
+namespace cp {
+namespace {
+
+constexpr int kRowWarps = 8;  // two per TMEM lane quarter, one per 32-column half of a sub-step
+constexpr int kThreadsB = 64 + 32 * kRowWarps;
+constexpr uint32_t kTmemColsB = 512;
+constexpr int kT = 128;         // keys per dk/dv CTA, query rows per dq CTA
+constexpr int kSub = 64;        // rows of a streamed sub-tile: query rows (dk/dv) or keys (dq) per sub-step
+constexpr int kSlots = 4;       // streamed sub-tile slots in shared memory
+constexpr int kMapWords = kScoreMaxTokens / kSub / 32;  // bitmap of sub-tiles
+static_assert(kSub == kDocBlock, "a sub-tile is a block of document ranges");
+
+// K-major operand of 128 rows: 16-element K steps within a 64-column box,
+// then the next box (boxes of 128 rows x 128 bytes)
+__device__ __forceinline__ uint32_t kstep128(int kk) {
+  return static_cast<uint32_t>(((kk >> 2) * (kT * 128) + (kk & 3) * 32) >> 4);
+}
+// the same for a 64-row sub-tile (boxes of 64 rows x 128 bytes)
+__device__ __forceinline__ uint32_t kstep64(int kk) {
+  return static_cast<uint32_t>(((kk >> 2) * (kSub * 128) + (kk & 3) * 32) >> 4);
+}
+
+template <int D>
+struct BSmem {
+  static constexpr int kTile = kT * D * 2;    // one bf16 128-row tile (K or V)
+  static constexpr int kSubT = kSub * D * 2;  // one bf16 64-row sub-tile (Q or dO)
+  static constexpr int kHalfS = kSub * 128;   // one 64-column box of a sub-tile
+  static constexpr int kOffK = 0;
+  static constexpr int kOffV = kOffK + kTile;
+  static constexpr int kOffQ = kOffV + kTile;            // kSlots sub-tiles
+  static constexpr int kOffO = kOffQ + kSlots * kSubT;   // dO, kSlots sub-tiles
+  static constexpr int kOffLse = kOffO + kSlots * kSubT;     // kSlots x 64 floats: lse * log2 e
+  static constexpr int kOffDlt = kOffLse + kSlots * kSub * 4; // kSlots x 64 floats: delta
+  static constexpr int kOffBar = kOffDlt + kSlots * kSub * 4;
+  static constexpr int kNumBars = 15;
+  static constexpr int kOffMisc = kOffBar + kNumBars * 8;
+  static constexpr int kOffMap = kOffMisc + 16;  // which sub-tiles are walked, and which are mixed
+  static constexpr int kBytes = kOffMap + 2 * kMapWords * 4;
+  // + room to align the base to 1024 bytes, as much as the 227 KB budget leaves
+  static constexpr int kMax = 227 * 1024;
+  static constexpr int kAlloc = kBytes + 1024 <= kMax ? kBytes + 1024 : kMax;
+};
+
+enum : int {
+  kBarKV = 0,      // K and V tiles landed
+  kBarQFull = 1,   // +slot (4): Q, dO, lse, delta of a sub-tile landed (TMA bytes)
+  kBarQEmpty = 5,  // +slot (4): MMAs done with the slot
+  kBarSFull = 9,   // +TMEM slot (2): S^T and dP^T of the sub-step in TMEM
+  kBarPFull = 11,  // +TMEM slot (2): P^T, dS^T written (every row warp arrives)
+  kBarDone = 13,   // every MMA of the CTA done: dK, dV final
+  kBarDrain = 14,
+};
+
+__device__ __forceinline__ void drain_wait_b(uint32_t bar, uint32_t parity, uint64_t timeout_ns) {
+  const uint64_t t0 = global_timer_ns();
+  for (uint32_t n = 1; !mbar_try_wait(bar, parity); ++n)
+    if ((n & 255u) == 0 && global_timer_ns() - t0 > timeout_ns) return;
+}
+
+__device__ __forceinline__ float u2f(uint32_t x) { return __uint_as_float(x); }
+
+// TMEM column (within S's or dP's 64) of the bf16 A operand for K step kk of
+// a sub-step: rows [32 h, 32 h + 32) of the sub-step (written by the row warps
+// of column half h) sit in columns [32 h, 32 h + 16), 8 columns per K step
+__device__ __forceinline__ uint32_t pcol(int kk) { return static_cast<uint32_t>((kk >> 1) * 32 + (kk & 1) * 8); }
+
+
+// Holds the uses of loaded registers behind the wait that precedes it.
+__device__ __forceinline__ void tmem_pin(uint32_t (&r)[32]) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 8)
+    asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]),
+                 "+r"(r[i + 6]), "+r"(r[i + 7]));
+}
+
+// The sub-tiles of [t0, t1) that meet the CTA's rows' documents (own: their
+// range), into the bitmaps act and mixed; returns how many. All threads call it.
+__device__ __forceinline__ int walk_map(const DocRange* other, int nblk, const DocRange& own, int t0, int t1,
+                                        uint32_t* act, uint32_t* count) {
+  uint32_t* mixed = act + kMapWords;
+  if (threadIdx.x == 0) *count = 0;
+  __syncthreads();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int w0 = (t0 & ~31) + warp * 32; w0 < t1; w0 += kThreadsB) {
+    const int t = w0 + lane;
+    const DocRange r = doc_span(other, nblk, t, 1);
+    const uint32_t w = __ballot_sync(0xffffffffu, t >= t0 && t < t1 && docs_meet(own, r));
+    const uint32_t m = __ballot_sync(0xffffffffu, !docs_same(own, r));
+    if (lane == 0) {
+      act[w0 >> 5] = w;
+      mixed[w0 >> 5] = m;
+      atomicAdd(count, __popc(w));
+    }
+  }
+  __syncthreads();
+  return static_cast<int>(*count);
+}
+
+// 32 scores of a row pass: p in place of s and ds in place of dp, packed as
+// bf16 pairs. Element e has the distance |d0 + step e| (step +1 or -1);
+// nl(e) = -lse log2e and nd(e) = -delta of its row; on: the pairs that take part.
+template <bool kCap, bool kBias, int kStep, typename NL, typename ND>
+__device__ __forceinline__ void row_pass(const uint32_t (&sr)[32], const uint32_t (&dr)[32], const CapCoef& cc,
+                                         float c2, float inv2, float slope2, float d0, uint32_t on, NL nl, ND nd,
+                                         uint32_t (&pp)[16], uint32_t (&dd)[16]) {
+  // kHow: 0 no cap, 3 and 6 the polynomials, 1 exact
+  auto pass = [&](auto how_c) {
+    constexpr int kHow = decltype(how_c)::value;
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) {
+      const float s0 = u2f(sr[e]), s1 = u2f(sr[e + 1]);
+      float b0, b1, n0, n1;
+      nl(e, b0, b1);
+      nd(e, n0, n1);
+      if constexpr (kBias) {
+        b0 = fmaf(-slope2, fabsf(d0 + static_cast<float>(kStep * e)), b0);
+        b1 = fmaf(-slope2, fabsf(d0 + static_cast<float>(kStep * (e + 1))), b1);
+      }
+      float t0, t1, g0, g1, c0 = 1.f, c1 = 1.f;
+      if constexpr (kHow == 0) {
+        fma2(t0, t1, s0, s1, c2, c2, b0, b1);
+      } else {
+        float y0, y1;
+        if constexpr (kHow >= 3) {
+          float u0, u1, f0, f1;
+          fma2(u0, u1, s0, s1, s0, s1, 0.f, 0.f);
+          cap_poly<kHow>(cc, u0, u1, f0, f1);
+          fma2(y0, y1, s0, s1, f0, f1, 0.f, 0.f);
+        } else {
+          y0 = cap_exact(cc, s0);
+          y1 = cap_exact(cc, s1);
+        }
+        float z0, z1;
+        fma2(z0, z1, y0, y1, y0, y1, 0.f, 0.f);
+        fma2(c0, c1, z0, z1, inv2, inv2, 1.f, 1.f);  // inv2 = -1 / (cap log2e)^2
+        t0 = y0 + b0;
+        t1 = y1 + b1;
+      }
+      fma2(g0, g1, u2f(dr[e]), u2f(dr[e + 1]), 1.f, 1.f, n0, n1);
+      float p0 = ex2_approx(t0), p1 = ex2_approx(t1), q0, q1;
+      fma2(q0, q1, p0, p1, g0, g1, 0.f, 0.f);
+      if constexpr (kHow != 0) fma2(q0, q1, q0, q1, c0, c1, 0.f, 0.f);
+      pp[e >> 1] = pack_bf16x2(p0, p1);
+      dd[e >> 1] = pack_bf16x2(q0, q1);
+    }
+  };
+  if constexpr (kCap) {
+    float um = 0.f;
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) {
+      float u0, u1;
+      fma2(u0, u1, u2f(sr[e]), u2f(sr[e + 1]), u2f(sr[e]), u2f(sr[e + 1]), 0.f, 0.f);
+      um = fmax3(um, u0, u1);
+    }
+    if (__all_sync(0xffffffffu, um <= cc.u3))
+      pass(std::integral_constant<int, 3>{});
+    else if (__all_sync(0xffffffffu, um <= cc.u6))
+      pass(std::integral_constant<int, 6>{});
+    else
+      pass(std::integral_constant<int, 1>{});
+  } else {
+    pass(std::integral_constant<int, 0>{});
+  }
+  if (__any_sync(0xffffffffu, on != ~0u)) {
+#pragma unroll
+    for (int x = 0; x < 16; ++x) {
+      const uint32_t keep = ((on >> (2 * x)) & 1u ? 0x0000ffffu : 0u) | ((on >> (2 * x + 1)) & 1u ? 0xffff0000u : 0u);
+      pp[x] &= keep;
+      dd[x] &= keep;
+    }
+  }
+}
+
+// 32 fp32 results of a row, times mul, to dst (fp32 or bf16) at element at.
+__device__ __forceinline__ void store_row32(void* dst, int64_t at, bool bf16, const uint32_t (&r)[32], float mul) {
+  if (bf16) {
+    __nv_bfloat16* d = static_cast<__nv_bfloat16*>(dst) + at;
+#pragma unroll
+    for (int x = 0; x < 32; x += 8) {
+      uint4 v;
+      v.x = pack_bf16x2(u2f(r[x]) * mul, u2f(r[x + 1]) * mul);
+      v.y = pack_bf16x2(u2f(r[x + 2]) * mul, u2f(r[x + 3]) * mul);
+      v.z = pack_bf16x2(u2f(r[x + 4]) * mul, u2f(r[x + 5]) * mul);
+      v.w = pack_bf16x2(u2f(r[x + 6]) * mul, u2f(r[x + 7]) * mul);
+      *reinterpret_cast<uint4*>(d + x) = v;
+    }
+  } else {
+    float* d = static_cast<float*>(dst) + at;
+#pragma unroll
+    for (int x = 0; x < 32; x += 4)
+      *reinterpret_cast<float4*>(d + x) = make_float4(u2f(r[x]) * mul, u2f(r[x + 1]) * mul, u2f(r[x + 2]) * mul, u2f(r[x + 3]) * mul);
+  }
+}
+
+// One dk/dv CTA: key tile bx of key/value head hk, batch entry b. tq64, to64: Q
+// and dO with 64-row boxes; tk, tv: K and V with 128-row boxes; smem_raw holds
+// alloc bytes of dynamic shared memory.
+template <int D, bool kCap, bool kBias>
+__device__ __forceinline__ void dkdv_cta(const CUtensorMap& tq64, const CUtensorMap& tk, const CUtensorMap& tv,
+                                         const CUtensorMap& to64, const ScoreArgs& a, const CapCoef& cc,
+                                         uint8_t* smem_raw, int alloc, int bx, int hk, int b) {
+  using L = BSmem<D>;
+  // the swizzled tiles need a 1024-byte aligned base; a base that would need
+  // more padding than the allocation holds is reported (uniformly, before any
+  // barrier or TMEM use) instead of used
+  const uint32_t pad = (1024u - (smem_addr(smem_raw) & 1023u)) & 1023u;
+  if (pad > static_cast<uint32_t>(alloc - L::kBytes)) {
+    if (threadIdx.x == 0) atomicOr(a.err, kDevErrLayout);
+    return;
+  }
+  uint8_t* smem = smem_raw + pad;
+  const uint32_t sb = smem_addr(smem);
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  uint32_t* misc = reinterpret_cast<uint32_t*>(smem + L::kOffMisc);  // [0] TMEM base, [1] abort flag, [2] count
+  volatile uint32_t* abort_flag = misc + 1;
+  auto bar = [&](int i) -> uint32_t { return sb + L::kOffBar + 8 * i; };
+  float* s_lse = reinterpret_cast<float*>(smem + L::kOffLse);
+  float* s_dlt = reinterpret_cast<float*>(smem + L::kOffDlt);
+
+  const int key0 = bx * kT;
+  const int nk = min(kT, a.Skv - key0);
+  const int plim = prefix_limit(a, b);
+  // query sub-tiles that reach a key of the tile: all, if it holds a prefix key
+  // or there is no causal rule, else from the first key's position on
+  const int ntq = (a.Sq + kSub - 1) / kSub;
+  const int t0 = a.causal && key0 >= plim ? min(ntq, max(0, key0 - a.rel) / kSub) : 0;
+  const int nqb = ntq, nkb = (a.Skv + kDocBlock - 1) / kDocBlock;
+  uint32_t* act = reinterpret_cast<uint32_t*>(smem + L::kOffMap);
+  const uint32_t* bits = a.qdoc ? act : nullptr;
+  int per_head = ntq - t0;
+  if (a.qdoc)
+    per_head = walk_map(a.qrange + static_cast<int64_t>(b) * nqb, nqb,
+                        doc_span(a.krange + static_cast<int64_t>(b) * nkb, nkb, bx * 2, 2), t0, ntq, act, misc + 2);
+  const int NJ = per_head * a.G;  // sub-steps: the sub-tiles of every query head, head by head
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < L::kNumBars; ++i) {
+      const bool four = i == kBarPFull || i == kBarPFull + 1;
+      mbar_init(bar(i), four ? kRowWarps : 1);
+    }
+    misc[1] = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_addr(misc), kTmemColsB);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = misc[0];
+  const uint64_t tmo = a.timeout_ns;
+
+  if (warp == 0) {
+    // ===================== TMA producer =====================
+    const bool leader = elect_one();
+    if (leader) {
+      tma_prefetch_desc(&tq64);
+      tma_prefetch_desc(&tk);
+      tma_prefetch_desc(&tv);
+      tma_prefetch_desc(&to64);
+      mbar_arrive_expect_tx(bar(kBarKV), 2 * L::kTile);
+      for (int c = 0; c < D / 64; ++c) {
+        tma_load_4d(sb + L::kOffK + c * (kT * 128), &tk, bar(kBarKV), c * 64, hk, key0, b);
+        tma_load_4d(sb + L::kOffV + c * (kT * 128), &tv, bar(kBarKV), c * 64, hk, key0, b);
+      }
+    }
+    int issued[kSlots] = {0, 0, 0, 0};
+    TileWalk cur(bits, t0, ntq);
+    int h = hk * a.G;
+    for (int j = 0; j < NJ; ++j) {
+      const int s = j & (kSlots - 1);
+      const uint32_t ph = (j >> 2) & 1;
+      if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar(kBarQEmpty + s), ph ^ 1, abort_flag, a.err, tmo))) break;
+      const int q0 = cur.t * kSub;
+      if (leader) {
+        mbar_arrive_expect_tx(bar(kBarQFull + s), 2 * L::kSubT + 2 * kSub * 4);
+        for (int c = 0; c < D / 64; ++c) {
+          tma_load_4d(sb + L::kOffQ + s * L::kSubT + c * L::kHalfS, &tq64, bar(kBarQFull + s), c * 64, h, q0, b);
+          tma_load_4d(sb + L::kOffO + s * L::kSubT + c * L::kHalfS, &to64, bar(kBarQFull + s), c * 64, h, q0, b);
+        }
+        const int64_t pr = ((static_cast<int64_t>(b) * a.H + h) * ntq + cur.t) * kSub;
+        bulk_g2s(smem_addr(s_lse + s * kSub), a.lse2p + pr, kSub * 4, bar(kBarQFull + s));
+        bulk_g2s(smem_addr(s_dlt + s * kSub), a.dltp + pr, kSub * 4, bar(kBarQFull + s));
+      }
+      __syncwarp();
+      ++issued[s];
+      cur.next();
+      if (cur.t >= ntq) {
+        cur = TileWalk(bits, t0, ntq);
+        ++h;
+      }
+    }
+    if (*abort_flag) {
+      // let every issued copy land before the CTA's shared memory goes away
+      drain_wait_b(bar(kBarKV), 0, tmo);
+      for (int s = 0; s < kSlots; ++s)
+        if (issued[s]) drain_wait_b(bar(kBarQFull + s), (issued[s] - 1) & 1, tmo);
+    }
+  } else if (warp == 1) {
+    // ===================== MMA issuer =====================
+    const bool leader = elect_one();
+    constexpr uint32_t idesc_s = idesc_bf16_f32(kT, kSub, false, false);  // S^T, dP^T: M = keys, N = 64 queries
+    constexpr uint32_t idesc_g = idesc_bf16_f32(kT, D, false, true);      // dV, dK: A in TMEM, B MN-major
+    const uint64_t k_km = smem_desc_sw128(sb + L::kOffK, 16, 1024);
+    const uint64_t v_km = smem_desc_sw128(sb + L::kOffV, 16, 1024);
+    const uint64_t q_km = smem_desc_sw128(sb + L::kOffQ, 16, 1024);
+    const uint64_t o_km = smem_desc_sw128(sb + L::kOffO, 16, 1024);
+    const uint64_t q_mn = smem_desc_sw128(sb + L::kOffQ, L::kHalfS, 1024);
+    const uint64_t o_mn = smem_desc_sw128(sb + L::kOffO, L::kHalfS, 1024);
+    const uint32_t km_hi = static_cast<uint32_t>(k_km >> 32), mn_hi = static_cast<uint32_t>(q_mn >> 32);
+    const uint32_t k_km_lo = static_cast<uint32_t>(k_km), v_km_lo = static_cast<uint32_t>(v_km);
+    const uint32_t q_km_lo = static_cast<uint32_t>(q_km), o_km_lo = static_cast<uint32_t>(o_km);
+    const uint32_t q_mn_lo = static_cast<uint32_t>(q_mn), o_mn_lo = static_cast<uint32_t>(o_mn);
+    auto commit = [&](uint32_t bar_addr) {
+      if (leader) mma_commit(bar_addr);
+    };
+    // S^T and dP^T of the sub-tile in smem slot q, into TMEM slot ts
+    auto issue_sdp = [&](int q, int ts) {
+      const uint32_t slot = static_cast<uint32_t>((q * L::kSubT) >> 4);
+      const uint32_t d = tmem + ts * 128;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk)
+        if (leader) mma_ss_lohi(d, k_km_lo + kstep128(kk), km_hi, q_km_lo + slot + kstep64(kk), km_hi, idesc_s, kk > 0);
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk)
+        if (leader)
+          mma_ss_lohi(d + kSub, v_km_lo + kstep128(kk), km_hi, o_km_lo + slot + kstep64(kk), km_hi, idesc_s, kk > 0);
+    };
+    // dV += P^T dO and dK += dS^T Q over the sub-tile's 64 query rows (K = rows:
+    // 16 rows = 2048 bytes of an MN-major sub-tile; the bf16 P^T / dS^T of
+    // rows [32 h, 32 h + 32) sit in TMEM columns [32 h, 32 h + 16) of theirs)
+    auto issue_g = [&](int q, int ts, bool acc) {
+      const uint32_t slot = static_cast<uint32_t>((q * L::kSubT) >> 4);
+      const uint32_t pa = tmem + ts * 128;
+#pragma unroll
+      for (int kk = 0; kk < kSub / 16; ++kk)
+        if (leader) mma_ts_lohi(tmem + 256, pa + pcol(kk), o_mn_lo + slot + ((kk * 2048) >> 4), mn_hi, idesc_g,
+                                (acc || kk > 0) ? 1u : 0u);
+#pragma unroll
+      for (int kk = 0; kk < kSub / 16; ++kk)
+        if (leader) mma_ts_lohi(tmem + 256 + D, pa + kSub + pcol(kk), q_mn_lo + slot + ((kk * 2048) >> 4), mn_hi,
+                                idesc_g, (acc || kk > 0) ? 1u : 0u);
+    };
+    auto wait_q = [&](int j) -> bool {
+      return mbar_wait_bounded(bar(kBarQFull + (j & (kSlots - 1))), (j >> 2) & 1, abort_flag, a.err, tmo);
+    };
+    bool ok = mbar_wait_bounded(bar(kBarKV), 0, abort_flag, a.err, tmo);
+    // prologue: S^T, dP^T of the first two sub-steps
+    for (int j = 0; ok && j < 2 && j < NJ; ++j) {
+      if (!wait_q(j)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      issue_sdp(j, j);
+      commit(bar(kBarSFull + j));
+    }
+    // sub-step j: once P^T, dS^T are in TMEM slot j mod 2, dV and dK consume
+    // them and S^T, dP^T of sub-step j + 2 go into the same slot; the step is
+    // instantiated per smem slot so every operand offset is a constant
+    auto step = [&](auto q_c, int j) -> bool {
+      constexpr int q = decltype(q_c)::value;
+      constexpr int ts = q & 1;
+      if (!mbar_wait_bounded(bar(kBarPFull + ts), (j >> 1) & 1, abort_flag, a.err, tmo)) return false;
+      tc_fence_after();
+      issue_g(q, ts, j > 0);
+      commit(bar(kBarQEmpty + q));
+      if (j + 2 < NJ) {
+        if (!wait_q(j + 2)) return false;
+        tc_fence_after();
+        issue_sdp((q + 2) & (kSlots - 1), ts);
+        commit(bar(kBarSFull + ts));
+      }
+      return true;
+    };
+    for (int j = 0; ok && j < NJ; j += kSlots) {
+      ok = step(std::integral_constant<int, 0>{}, j);
+      if (ok && j + 1 < NJ) ok = step(std::integral_constant<int, 1>{}, j + 1);
+      if (ok && j + 2 < NJ) ok = step(std::integral_constant<int, 2>{}, j + 2);
+      if (ok && j + 3 < NJ) ok = step(std::integral_constant<int, 3>{}, j + 3);
+    }
+    if (ok) {
+      commit(bar(kBarDone));
+    } else {
+      commit(bar(kBarDrain));
+      drain_wait_b(bar(kBarDrain), 0, tmo);
+    }
+  } else {
+    // ===================== row pass: one thread per key row and column half =====================
+    const int wq = warp & 3;
+    const int hc = (warp - 2) >> 2;  // this warp's 32 query columns of each sub-step
+    const int key = wq * 32 + lane;
+    const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
+    const bool kvalid = key < nk;
+    const float c2 = a.scale * kLog2e, inv2 = kCap ? -1.f / (cc.capl2 * cc.capl2) : 0.f;
+    const int jkey = key0 + key;
+    const bool open = !a.causal || jkey < plim;  // every row may see this key
+    const int kd = a.qdoc && kvalid ? a.kdoc[static_cast<int64_t>(b) * a.Skv + jkey] : -1;
+    const int* qdoc = a.qdoc + static_cast<int64_t>(b) * a.Sq;
+    bool ok = true;
+    TileWalk cur(bits, t0, ntq);
+    int h = hk * a.G;
+    float slope2 = kBias ? a.slopes[h] * kLog2e : 0.f;
+    for (int j = 0; j < NJ; ++j) {
+      const int q = j & (kSlots - 1), ts = j & 1;
+      const int i0 = cur.t * kSub + hc * 32;  // the query row of this warp's first column
+      const int d0 = a.rel + i0 - jkey;       // its position less the key's
+      uint32_t on = !kvalid ? 0u : open || d0 >= 0 ? ~0u : d0 <= -32 ? 0u : ~0u << -d0;
+      if (bits != nullptr && ((act[kMapWords + (cur.t >> 5)] >> (cur.t & 31)) & 1u)) {
+        uint32_t same = 0;
+#pragma unroll
+        for (int c = 0; c < 32; ++c) {
+          const int id = i0 + c < a.Sq ? __ldg(qdoc + i0 + c) : -1;  // the same word for the whole warp
+          same |= (id == kd ? 1u : 0u) << c;
+        }
+        on &= kd >= 0 ? same : 0u;
+      }
+      ok = __all_sync(0xffffffffu,
+                      mbar_wait_bounded(bar(kBarQFull + q), (j >> 2) & 1, abort_flag, a.err, tmo) &&
+                          mbar_wait_bounded(bar(kBarSFull + ts), (j >> 1) & 1, abort_flag, a.err, tmo));
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t t_s = tmem + lane_off + ts * 128 + hc * 32, t_dp = t_s + kSub;
+      uint32_t sr[32], dr[32], pp[16], dd[16];
+      tmem_ld32(t_s, sr);
+      tmem_ld32(t_dp, dr);
+      tmem_wait_ld();
+      tmem_pin(sr);
+      tmem_pin(dr);
+      const float* lse2 = s_lse + q * kSub + hc * 32;
+      const float* dlt = s_dlt + q * kSub + hc * 32;
+      row_pass<kCap, kBias, 1>(
+          sr, dr, cc, c2, inv2, slope2, static_cast<float>(d0), on,
+          [&](int e, float& x0, float& x1) {
+            const float2 v = *reinterpret_cast<const float2*>(lse2 + e);
+            x0 = -v.x;
+            x1 = -v.y;
+          },
+          [&](int e, float& x0, float& x1) {
+            const float2 v = *reinterpret_cast<const float2*>(dlt + e);
+            x0 = -v.x;
+            x1 = -v.y;
+          },
+          pp, dd);
+      // P^T over the first half of this warp's S^T columns, dS^T over those of dP^T
+      tmem_st16(t_s, pp);
+      tmem_st16(t_dp, dd);
+      cur.next();
+      if (cur.t >= ntq) {
+        cur = TileWalk(bits, t0, ntq);
+        ++h;
+        if (kBias && j + 1 < NJ) slope2 = a.slopes[h] * kLog2e;
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBarPFull + ts));
+    }
+    // ---- dk, dv of this CTA's keys ----
+    if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar(kBarDone), 0, abort_flag, a.err, tmo));
+    if (ok) {
+      tc_fence_after();
+      const int64_t at = ((static_cast<int64_t>(b) * a.Skv + key0 + key) * a.Hkv + hk) * D;
+      const int g = hc;  // column half 0 writes dv, half 1 dk
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t r[32];
+        tmem_ld32(tmem + lane_off + 256 + g * D + c * 32, r);
+        tmem_wait_ld();
+        tmem_pin(r);
+        if (NJ == 0) {  // no row reaches these keys: no product was formed
+#pragma unroll
+          for (int x = 0; x < 32; ++x) r[x] = 0u;
+        }
+        if (kvalid) store_row32(g == 0 ? a.dv : a.dk, at + c * 32, a.grad_bf16, r, g == 0 ? 1.f : a.scale);
+      }
+    }
+  }
+
+  // ---- teardown: every thread of the CTA arrives here, aborted or not ----
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemColsB);
+  }
+}
+
+// ----------------------------------------------------------------------------
+// dq: one CTA per 128 query rows of one (batch entry, head). The row warps
+// load the CTA's Q and dO rows once into TMEM (bf16 pairs, the A-operand
+// layout: columns [384, 384 + D/2) and [384 + D/2, 384 + D)); 64-key K and V
+// sub-tiles that the rows reach stream through kDqSlots shared-memory slots. Per sub-tile three MMAs (M = 128 rows):
+//   S  = Q K^T    (TS: Q in TMEM, K K-major; N = 64) -> TMEM slot j mod 2, [0, 64)
+//   dP = dO V^T   (TS)                               -> the same slot, [64, 128)
+//   dQ += dS K    (TS: dS over S's first 32 columns, K read MN-major)
+//                                                    -> TMEM [256, 256 + D)
+// Only K and V come from shared memory. S and dP of sub-step j + 2 are issued
+// right after dQ of sub-step j, so they run while the row warps (one thread
+// per query row and column half, lse and delta in registers) form
+// dS = p (dp - delta) of sub-step j + 1. dq is stored once, without atomics.
+// ----------------------------------------------------------------------------
+constexpr int kDqSlots = 6;  // K/V sub-tile slots of the dq kernel
+
+template <int D>
+struct DqSmem {
+  static constexpr int kSubT = kSub * D * 2;  // a K or V sub-tile: 64 keys
+  static constexpr int kHalfS = kSub * 128;
+  static constexpr int kOffK = 0;                          // kDqSlots sub-tiles
+  static constexpr int kOffV = kOffK + kDqSlots * kSubT;   // kDqSlots sub-tiles
+  static constexpr int kOffBar = kOffV + kDqSlots * kSubT;
+  static constexpr int kNumBars = 1 + 2 * kDqSlots + 6;
+  static constexpr int kOffMisc = kOffBar + kNumBars * 8;
+  static constexpr int kOffMap = kOffMisc + 16;
+  static constexpr int kBytes = kOffMap + 2 * kMapWords * 4;
+  static constexpr int kMax = 227 * 1024;
+  static constexpr int kAlloc = kBytes + 1024 <= kMax ? kBytes + 1024 : kMax;
+};
+
+enum : int {
+  kDqBarQ = 0,                             // Q and dO in TMEM (every row warp arrives)
+  kDqBarKVFull = 1,                        // +slot: K and V sub-tiles landed
+  kDqBarKVEmpty = 1 + kDqSlots,            // +slot: MMAs done with the slot
+  kDqBarSFull = 1 + 2 * kDqSlots,          // +TMEM slot (2): S and dP in TMEM
+  kDqBarPFull = kDqBarSFull + 2,           // +TMEM slot (2): dS written (every row warp arrives)
+  kDqBarDone = kDqBarPFull + 2,            // every MMA done: dQ final
+  kDqBarDrain = kDqBarDone + 1,
+};
+
+// One dq CTA: query tile bx of head h, batch entry b. tk64, tv64: K and V with
+// 64-row boxes.
+template <int D, bool kCap, bool kBias>
+__device__ __forceinline__ void dq_cta(const CUtensorMap& tk64, const CUtensorMap& tv64, const ScoreArgs& a,
+                                       const CapCoef& cc, uint8_t* smem_raw, int alloc, int bx, int h, int b) {
+  using L = DqSmem<D>;
+  const uint32_t pad = (1024u - (smem_addr(smem_raw) & 1023u)) & 1023u;
+  if (pad > static_cast<uint32_t>(alloc - L::kBytes)) {
+    if (threadIdx.x == 0) atomicOr(a.err, kDevErrLayout);
+    return;
+  }
+  uint8_t* smem = smem_raw + pad;
+  const uint32_t sb = smem_addr(smem);
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  uint32_t* misc = reinterpret_cast<uint32_t*>(smem + L::kOffMisc);  // [0] TMEM base, [1] abort flag, [2] count
+  volatile uint32_t* abort_flag = misc + 1;
+  auto bar = [&](int i) -> uint32_t { return sb + L::kOffBar + 8 * i; };
+
+  const int hk = h / a.G;
+  const int q0 = bx * kT;
+  const int nq = min(kT, a.Sq - q0);
+  const int plim = prefix_limit(a, b);
+  // key sub-tiles that the last row (the largest limit) reaches
+  const int ntk = (max(0, min(a.Skv, key_limit(a, plim, q0 + nq - 1))) + kSub - 1) / kSub;
+  const int nqb = (a.Sq + kDocBlock - 1) / kDocBlock, nkb = (a.Skv + kDocBlock - 1) / kDocBlock;
+  uint32_t* act = reinterpret_cast<uint32_t*>(smem + L::kOffMap);
+  const uint32_t* bits = a.qdoc ? act : nullptr;
+  int NJ = ntk;
+  if (a.qdoc)
+    NJ = walk_map(a.krange + static_cast<int64_t>(b) * nkb, nkb,
+                  doc_span(a.qrange + static_cast<int64_t>(b) * nqb, nqb, bx * 2, 2), 0, ntk, act, misc + 2);
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < L::kNumBars; ++i)
+      mbar_init(bar(i), (i == kDqBarQ || i == kDqBarPFull || i == kDqBarPFull + 1) ? kRowWarps : 1);
+    misc[1] = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_addr(misc), kTmemColsB);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = misc[0];
+  const uint64_t tmo = a.timeout_ns;
+
+  if (warp == 0) {
+    // ===================== TMA producer =====================
+    const bool leader = elect_one();
+    if (leader) {
+      tma_prefetch_desc(&tk64);
+      tma_prefetch_desc(&tv64);
+    }
+    int issued[kDqSlots] = {};
+    TileWalk cur(bits, 0, ntk);
+    for (int j = 0; j < NJ; ++j) {
+      const int s = j % kDqSlots;
+      const uint32_t ph = (j / kDqSlots) & 1;
+      if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar(kDqBarKVEmpty + s), ph ^ 1, abort_flag, a.err, tmo)))
+        break;
+      if (leader) {
+        mbar_arrive_expect_tx(bar(kDqBarKVFull + s), 2 * L::kSubT);
+        for (int c = 0; c < D / 64; ++c) {
+          tma_load_4d(sb + L::kOffK + s * L::kSubT + c * L::kHalfS, &tk64, bar(kDqBarKVFull + s), c * 64, hk,
+                      cur.t * kSub, b);
+          tma_load_4d(sb + L::kOffV + s * L::kSubT + c * L::kHalfS, &tv64, bar(kDqBarKVFull + s), c * 64, hk,
+                      cur.t * kSub, b);
+        }
+      }
+      ++issued[s];
+      cur.next();
+    }
+    if (*abort_flag) {
+      // let every issued copy land before the CTA's shared memory goes away
+      for (int s = 0; s < kDqSlots; ++s)
+        if (issued[s]) drain_wait_b(bar(kDqBarKVFull + s), (issued[s] - 1) & 1, tmo);
+    }
+  } else if (warp == 1) {
+    // ===================== MMA issuer =====================
+    const bool leader = elect_one();
+    constexpr uint32_t idesc_s = idesc_bf16_f32(kT, kSub, false, false);  // S, dP: M = query rows, N = 64 keys
+    constexpr uint32_t idesc_q = idesc_bf16_f32(kT, D, false, true);      // dQ: A (dS) in TMEM, B (K) MN-major
+    const uint64_t k_km = smem_desc_sw128(sb + L::kOffK, 16, 1024);
+    const uint64_t v_km = smem_desc_sw128(sb + L::kOffV, 16, 1024);
+    const uint64_t k_mn = smem_desc_sw128(sb + L::kOffK, L::kHalfS, 1024);
+    const uint32_t km_hi = static_cast<uint32_t>(k_km >> 32), mn_hi = static_cast<uint32_t>(k_mn >> 32);
+    const uint32_t k_lo = static_cast<uint32_t>(k_km), v_lo = static_cast<uint32_t>(v_km);
+    const uint32_t k_mn_lo = static_cast<uint32_t>(k_mn);
+    const uint32_t t_q = tmem + 384, t_o = tmem + 384 + D / 2;  // Q and dO rows in TMEM (8 columns per K step)
+    auto commit = [&](uint32_t bar_addr) {
+      if (leader) mma_commit(bar_addr);
+    };
+    // S and dP of the K/V sub-tile in smem slot q, into TMEM slot ts
+    auto issue_sdp = [&](int q, int ts) {
+      const uint32_t slot = static_cast<uint32_t>((q * L::kSubT) >> 4);
+      const uint32_t d = tmem + ts * 128;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk)
+        if (leader) mma_ts_lohi(d, t_q + kk * 8, k_lo + slot + kstep64(kk), km_hi, idesc_s, kk > 0 ? 1u : 0u);
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk)
+        if (leader) mma_ts_lohi(d + kSub, t_o + kk * 8, v_lo + slot + kstep64(kk), km_hi, idesc_s, kk > 0 ? 1u : 0u);
+    };
+    auto wait_kv = [&](int j) -> bool {
+      return mbar_wait_bounded(bar(kDqBarKVFull + (j % kDqSlots)), (j / kDqSlots) & 1, abort_flag, a.err, tmo);
+    };
+    bool ok = mbar_wait_bounded(bar(kDqBarQ), 0, abort_flag, a.err, tmo);
+    for (int j = 0; ok && j < 2 && j < NJ; ++j) {
+      if (!wait_kv(j)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      issue_sdp(j, j);
+      commit(bar(kDqBarSFull + j));
+    }
+    // sub-step j: dQ += dS K once dS is in TMEM slot j mod 2 (K = keys: 16 key
+    // rows = 2048 bytes of the MN-major sub-tile), then S, dP of sub-step j + 2
+    // into the same slot; instantiated per smem slot (kDqSlots is even, so the
+    // TMEM slot is the smem slot's parity)
+    static_assert(kDqSlots % 2 == 0, "TMEM slot = smem slot parity");
+    auto step = [&](auto q_c, int j) -> bool {
+      constexpr int q = decltype(q_c)::value;
+      constexpr int ts = q & 1;
+      if (!mbar_wait_bounded(bar(kDqBarPFull + ts), (j >> 1) & 1, abort_flag, a.err, tmo)) return false;
+      tc_fence_after();
+      const uint32_t slot = static_cast<uint32_t>((q * L::kSubT) >> 4);
+#pragma unroll
+      for (int kk = 0; kk < kSub / 16; ++kk)
+        if (leader) mma_ts_lohi(tmem + 256, tmem + ts * 128 + pcol(kk), k_mn_lo + slot + ((kk * 2048) >> 4), mn_hi,
+                                idesc_q, (j > 0 || kk > 0) ? 1u : 0u);
+      commit(bar(kDqBarKVEmpty + q));
+      if (j + 2 < NJ) {
+        if (!wait_kv(j + 2)) return false;
+        tc_fence_after();
+        issue_sdp((q + 2) % kDqSlots, ts);
+        commit(bar(kDqBarSFull + ts));
+      }
+      return true;
+    };
+    for (int j = 0; ok && j < NJ; j += kDqSlots) {
+      ok = step(std::integral_constant<int, 0>{}, j);
+      if (ok && j + 1 < NJ) ok = step(std::integral_constant<int, 1>{}, j + 1);
+      if (ok && j + 2 < NJ) ok = step(std::integral_constant<int, 2>{}, j + 2);
+      if (ok && j + 3 < NJ) ok = step(std::integral_constant<int, 3>{}, j + 3);
+      if (ok && j + 4 < NJ) ok = step(std::integral_constant<int, 4>{}, j + 4);
+      if (ok && j + 5 < NJ) ok = step(std::integral_constant<int, 5>{}, j + 5);
+    }
+    if (ok) {
+      commit(bar(kDqBarDone));
+    } else {
+      commit(bar(kDqBarDrain));
+      drain_wait_b(bar(kDqBarDrain), 0, tmo);
+    }
+  } else {
+    // ===================== dS: one thread per query row and column half =====================
+    const int wq = warp & 3;
+    const int hc = (warp - 2) >> 2;  // this warp's 32 key columns of each sub-step
+    const int row = wq * 32 + lane;
+    const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
+    const float c2 = a.scale * kLog2e, inv2 = kCap ? -1.f / (cc.capl2 * cc.capl2) : 0.f;
+    // the row's lse log2e and delta, from the padded copies (a row past the end holds +inf, 0)
+    float nl2 = -INFINITY, ndl = 0.f;
+    if (row < nq) {
+      const int64_t o = (static_cast<int64_t>(b) * a.H + h) * nqb * kDocBlock + q0 + row;
+      nl2 = -a.lse2p[o];
+      ndl = -a.dltp[o];
+    }
+    // this row's Q (column half 0) or dO (half 1) into TMEM as the A operand
+    // of S and dP: column c holds elements 2c and 2c + 1 of the row, which is
+    // the row's memory read as 32-bit words; rows past the shard are zero
+    // (they take no part)
+    {
+      const int64_t ro = ((static_cast<int64_t>(b) * a.Sq + q0 + row) * a.H + h) * D;
+      {
+        const int g = hc;
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(g == 0 ? a.q : a.dout) + ro);
+#pragma unroll 1
+        for (int c = 0; c < D / 64; ++c) {
+          uint32_t w[32];
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            const uint4 u = row < nq ? src[c * 8 + x] : make_uint4(0u, 0u, 0u, 0u);
+            w[4 * x] = u.x;
+            w[4 * x + 1] = u.y;
+            w[4 * x + 2] = u.z;
+            w[4 * x + 3] = u.w;
+          }
+          tmem_st32(tmem + lane_off + 384 + g * (D / 2) + c * 32, w);
+        }
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kDqBarQ));
+    }
+    bool ok = true;
+    const int lim = min(a.Skv, key_limit(a, plim, q0 + row));
+    const int qd = a.qdoc && row < nq ? a.qdoc[static_cast<int64_t>(b) * a.Sq + q0 + row] : -1;
+    const int* kdoc = a.kdoc + static_cast<int64_t>(b) * a.Skv;
+    const float slope2 = kBias ? a.slopes[h] * kLog2e : 0.f;
+    TileWalk cur(bits, 0, ntk);
+    for (int j = 0; j < NJ; ++j) {
+      const int ts = j & 1;
+      const int j0 = cur.t * kSub + hc * 32;  // the key of this warp's first column
+      const int n = lim - j0;
+      uint32_t on = n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u;
+      if (bits != nullptr && ((act[kMapWords + (cur.t >> 5)] >> (cur.t & 31)) & 1u)) {
+        uint32_t same = 0;
+#pragma unroll
+        for (int c = 0; c < 32; ++c) {
+          const int id = j0 + c < a.Skv ? __ldg(kdoc + j0 + c) : -1;  // the same word for the whole warp
+          same |= (id == qd ? 1u : 0u) << c;
+        }
+        on &= qd >= 0 ? same : 0u;
+      }
+      ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar(kDqBarSFull + ts), (j >> 1) & 1, abort_flag, a.err, tmo));
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t t_s = tmem + lane_off + ts * 128 + hc * 32, t_dp = t_s + kSub;  // this sub-step's slot
+      uint32_t sr[32], dr[32], pp[16], dd[16];
+      tmem_ld32(t_s, sr);
+      tmem_ld32(t_dp, dr);
+      tmem_wait_ld();
+      tmem_pin(sr);
+      tmem_pin(dr);
+      row_pass<kCap, kBias, -1>(
+          sr, dr, cc, c2, inv2, slope2, static_cast<float>(a.rel + q0 + row - j0), on,
+          [&](int, float& x0, float& x1) { x0 = x1 = nl2; }, [&](int, float& x0, float& x1) { x0 = x1 = ndl; }, pp, dd);
+      tmem_st16(t_s, dd);  // dS over the first half of this warp's S columns
+      cur.next();
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kDqBarPFull + ts));
+    }
+    // ---- dq of this CTA's rows ----
+    if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar(kDqBarDone), 0, abort_flag, a.err, tmo));
+    if (ok) {
+      tc_fence_after();
+      const int64_t at = ((static_cast<int64_t>(b) * a.Sq + q0 + row) * a.H + h) * D;
+#pragma unroll 1
+      for (int c = hc * (D / 64); c < (hc + 1) * (D / 64); ++c) {  // this half's D / 2 columns
+        uint32_t r[32];
+        tmem_ld32(tmem + lane_off + 256 + c * 32, r);
+        tmem_wait_ld();
+        tmem_pin(r);
+        if (NJ == 0) {  // these rows reach no key
+#pragma unroll
+          for (int x = 0; x < 32; ++x) r[x] = 0u;
+        }
+        if (row < nq) store_row32(a.dq, at + c * 32, a.grad_bf16, r, a.scale);
+      }
+    }
+  }
+
+  // ---- teardown: every thread of the CTA arrives here, aborted or not ----
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemColsB);
+  }
+}
+
+template <int D>
+__host__ __device__ constexpr int bwd_alloc() {
+  return BSmem<D>::kAlloc > DqSmem<D>::kAlloc ? BSmem<D>::kAlloc : DqSmem<D>::kAlloc;
+}
+
+// Both kinds of CTA in one launch: the dk/dv CTAs from the first keys (which
+// the most causal rows reach), then the dq CTAs from the last rows, heads
+// fastest, so that long CTAs start first and short ones fill the end.
+template <int D, bool kCap, bool kBias>
+__global__ void __launch_bounds__(kThreadsB, 1)
+    score_bwd_tc_kernel(const __grid_constant__ CUtensorMap tq64, const __grid_constant__ CUtensorMap tk,
+                        const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap to64,
+                        const __grid_constant__ CUtensorMap tk64, const __grid_constant__ CUtensorMap tv64,
+                        const __grid_constant__ ScoreArgs a, const __grid_constant__ CapCoef cc) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const int nkv = (a.Skv + kT - 1) / kT, nq = (a.Sq + kT - 1) / kT;
+  const int kv_ctas = nkv * a.Hkv * a.B;
+  const int id = static_cast<int>(blockIdx.x);
+  if (id < kv_ctas) {
+    const int bh = id % (a.Hkv * a.B);
+    dkdv_cta<D, kCap, kBias>(tq64, tk, tv, to64, a, cc, smem_raw, bwd_alloc<D>(), id / (a.Hkv * a.B), bh % a.Hkv,
+                             bh / a.Hkv);
+  } else {
+    const int i = id - kv_ctas, bh = i % (a.H * a.B);
+    dq_cta<D, kCap, kBias>(tk64, tv64, a, cc, smem_raw, bwd_alloc<D>(), nq - 1 - i / (a.H * a.B), bh % a.H, bh / a.H);
+  }
+}
+
+// delta_i = out_i . dout_i and lse_i log2e, 64 rows of one (batch entry, head) a
+// CTA, into copies padded to 64 rows: +inf and 0 past the end, +inf for a row
+// that saw no key. Bound by HBM (out and dout are read once).
+template <int D, bool kOutBf16>
+__global__ void __launch_bounds__(256) score_delta_tc_kernel(const __grid_constant__ ScoreArgs a) {
+  constexpr int kLanes = D / 8;        // lanes of a row, 8 elements each
+  constexpr int kRows = 256 / kLanes;  // rows a pass
+  const int sub = threadIdx.x % kLanes;
+  const int blk = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
+  const int64_t pad0 = ((static_cast<int64_t>(b) * a.H + h) * gridDim.x + blk) * kSub;
+#pragma unroll
+  for (int r0 = 0; r0 < kSub; r0 += kRows) {
+    const int r = r0 + threadIdx.x / kLanes, row = blk * kSub + r;
+    float sum = 0.f;
+    if (row < a.Sq) {
+      const int64_t at = ((static_cast<int64_t>(b) * a.Sq + row) * a.H + h) * D + sub * 8;
+      const uint4 g = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.dout) + at);
+      const uint32_t gw[4] = {g.x, g.y, g.z, g.w};
+      float o[8];
+      if constexpr (kOutBf16) {
+        const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.o) + at);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          o[2 * i] = __uint_as_float(w[i] << 16);
+          o[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+      } else {
+        const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.o) + at);
+        const float4 x = p[0], y = p[1];
+        o[0] = x.x; o[1] = x.y; o[2] = x.z; o[3] = x.w;
+        o[4] = y.x; o[5] = y.y; o[6] = y.z; o[7] = y.w;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        sum = fmaf(__uint_as_float(gw[i] << 16), o[2 * i], sum);
+        sum = fmaf(__uint_as_float(gw[i] & 0xffff0000u), o[2 * i + 1], sum);
+      }
+    }
+#pragma unroll
+    for (int s = kLanes / 2; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
+    if (sub == 0) {
+      const float l = row < a.Sq ? a.lse[(static_cast<int64_t>(b) * a.H + h) * a.Sq + row] : INFINITY;
+      a.lse2p[pad0 + r] = l == -INFINITY ? INFINITY : l * kLog2e;
+      a.dltp[pad0 + r] = row < a.Sq ? sum : 0.f;
+    }
+  }
+}
+
+struct BwdMaps {
+  CUtensorMap q64, k, v, o64, k64, v64;
+};
+
+template <int D, bool kCap, bool kBias>
+cudaError_t launch_rule(const ScoreArgs& a, const BwdMaps& m, cudaStream_t s) {
+  constexpr int kAlloc = bwd_alloc<D>();
+  static_assert(kAlloc <= 227 * 1024, "shared memory budget");
+  auto kernel = score_bwd_tc_kernel<D, kCap, kBias>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kAlloc);
+  if (e != cudaSuccess) return e;
+  const int64_t ctas = (static_cast<int64_t>((a.Skv + kT - 1) / kT) * a.Hkv + static_cast<int64_t>((a.Sq + kT - 1) / kT) * a.H) * a.B;
+  if (ctas > 0x7fffffff) return cudaErrorInvalidValue;
+  kernel<<<static_cast<unsigned>(ctas), kThreadsB, kAlloc, s>>>(m.q64, m.k, m.v, m.o64, m.k64, m.v64, a,
+                                                                make_cap_coef(a.scale, a.cap));
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_d(const ScoreArgs& a, cudaStream_t s) {
+  if (a.Sq > 0) {
+    const dim3 grid((a.Sq + kSub - 1) / kSub, a.H, a.B);
+    if (a.out_bf16)
+      score_delta_tc_kernel<D, true><<<grid, 256, 0, s>>>(a);
+    else
+      score_delta_tc_kernel<D, false><<<grid, 256, 0, s>>>(a);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  // one side may be empty: its maps stand on the other's memory and are never read through
+  const bool noq = a.Sq == 0, nok = a.Skv == 0;
+  const void *q = noq ? a.k : a.q, *o = noq ? a.k : a.dout, *k = nok ? a.q : a.k, *v = nok ? a.q : a.v;
+  const int hq = noq ? a.Hkv : a.H, sq = noq ? a.Skv : a.Sq, hk = nok ? a.H : a.Hkv, sk = nok ? a.Sq : a.Skv;
+  BwdMaps m;
+  if (!host_tmap_bf16(&m.q64, q, D, hq, sq, a.B, kSub) || !host_tmap_bf16(&m.o64, o, D, hq, sq, a.B, kSub) ||
+      !host_tmap_bf16(&m.k, k, D, hk, sk, a.B, kT) || !host_tmap_bf16(&m.v, v, D, hk, sk, a.B, kT) ||
+      !host_tmap_bf16(&m.k64, k, D, hk, sk, a.B, kSub) || !host_tmap_bf16(&m.v64, v, D, hk, sk, a.B, kSub))
+    return cudaErrorInvalidValue;
+  if (a.cap > 0.f) return a.slopes ? launch_rule<D, true, true>(a, m, s) : launch_rule<D, true, false>(a, m, s);
+  return a.slopes ? launch_rule<D, false, true>(a, m, s) : launch_rule<D, false, false>(a, m, s);
+}
+
+}  // namespace
+
+cudaError_t launch_score_bwd_tc(const ScoreArgs& a, int D, cudaStream_t s) {
+  return D == 64 ? launch_d<64>(a, s) : launch_d<128>(a, s);
+}
+
+}  // namespace cp
