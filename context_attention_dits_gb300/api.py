@@ -7,7 +7,6 @@ memory and the stream.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 
 import torch
@@ -291,11 +290,17 @@ def cp_attention_bwd(q, k, v, out, dout, lse, dq, dk, dv, scale: float, ring_deg
 # ---------------------------------------------------------------------------
 # attention with a score rule, and the paged cache
 # ---------------------------------------------------------------------------
+# The current stream's handle: by torch's own accessor of it where there is one (0.1 us; a torch.cuda.Stream object
+# costs 3 us, more than the launch of a kernel).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _place(dev, stream):
-    """The context (device, stream) that a call on tensors of `dev` runs in: its launches and the memory
-    allocated for it belong to `stream` (None: the device's current stream)."""
+    """The context (device, stream) that a call on tensors of `dev` runs in, or None if it is the present one: its
+    launches and the memory allocated for it belong to `stream` (None: the device's current stream)."""
     if stream is None:
-        return contextlib.nullcontext() if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+        return None if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=dev)
     if stream.device != dev:
@@ -303,12 +308,31 @@ def _place(dev, stream):
     return torch.cuda.stream(stream)
 
 
-def _dense_on(dev, **ts):
-    for name, t in ts.items():
+def _dense_on(dev, *ts):
+    for t in ts:
         if t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, q (or k_new) on {dev}: tensors must live on one CUDA device")
+            raise ValueError(f"a tensor is on {t.device}, the first one on {dev}: tensors must live on one CUDA device")
         if not t.is_contiguous():
-            raise ValueError(f"{name} must be dense")
+            raise ValueError("tensors must be dense")
+
+
+def _call(name, ctor, need, workspace, dev, stream):
+    """Calls ctor(workspace pointer, its bytes, raw stream) in the place that `stream` names; a workspace of `need`
+    bytes is allocated there when the caller gave none."""
+    place = _place(dev, stream)
+    if place is not None:
+        with place:
+            return _call(name, ctor, need, workspace, dev, None)
+    ptr, size = None, 0
+    if workspace is not None:
+        _dense_on(dev, workspace)
+        ptr, size = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    elif need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        ptr, size = workspace.data_ptr(), need
+    status = ctor(ptr, size, _raw_stream(dev.index))
+    if status:
+        raise CpError(status, name)
 
 
 def _i32(name, t, shape):
@@ -324,37 +348,26 @@ def _out_dt(name, t, like) -> int:
     return _DT[t.dtype]
 
 
-def _scratch(workspace, need, dev):
-    """Pointer, size and owner of the caller's workspace, or of one allocated here."""
-    if workspace is None:
-        if need == 0:
-            return None, 0, None
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    else:
-        _dense_on(dev, workspace=workspace)
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
-
-
 def _score_rule(q, k, softcap, slopes, causal, prefix_lens, q_docs, kv_docs, q_pos0, kv_pos0):
     B, Sq, H, _ = q.shape
     Skv = k.shape[1]
     dev = q.device
-    r = _lib.ScoreRule(softcap=float(softcap), causal=int(bool(causal)), q_pos0=int(q_pos0), kv_pos0=int(kv_pos0))
+    r = _lib.ScoreRule(float(softcap), None, bool(causal), None, None, None, int(q_pos0), int(kv_pos0))
     if slopes is not None:
         if slopes.dtype != torch.float32 or slopes.shape != (H,):
             raise ValueError("slopes must be float32 [H]")
-        _dense_on(dev, slopes=slopes)
+        _dense_on(dev, slopes)
         r.slopes = slopes.data_ptr()
     if prefix_lens is not None:
         _i32("prefix_lens", prefix_lens, (B,))
-        _dense_on(dev, prefix_lens=prefix_lens)
+        _dense_on(dev, prefix_lens)
         r.prefix_lens = prefix_lens.data_ptr() or 256  # an empty tensor has no address; no row reads it
     if (q_docs is None) != (kv_docs is None):
         raise ValueError("q_docs and kv_docs come together")
     if q_docs is not None:
         _i32("q_docs", q_docs, (B, Sq))
         _i32("kv_docs", kv_docs, (B, Skv))
-        _dense_on(dev, q_docs=q_docs, kv_docs=kv_docs)
+        _dense_on(dev, q_docs, kv_docs)
         r.q_docs, r.kv_docs = q_docs.data_ptr() or 256, kv_docs.data_ptr() or 256
     return r
 
@@ -404,14 +417,13 @@ def cp_scored_attn_fwd(q, k, v, out, lse, scale: float, softcap: float = 0.0, sl
     if out.shape != q.shape:
         raise ValueError("shape mismatch")
     dt, odt, dev = _dt(q), _out_dt("out", out, q), q.device
-    _dense_on(dev, q=q, k=k, v=v, out=out, lse=lse)
+    _dense_on(dev, q, k, v, out, lse)
     r = _score_rule(q, k, softcap, slopes, causal, prefix_lens, q_docs, kv_docs, q_pos0, kv_pos0)
-    with _place(dev, stream):
-        need = lib().cp_scored_attn_workspace_size(B, H, Sq, Skv, 1) if q_docs is not None else 0
-        ptr, size, _own = _scratch(workspace, need, dev)
-        st = lib().cp_scored_attn_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), B, H,
-                                      Hkv, Sq, Skv, D, float(scale), ctypes.byref(r), ptr, size, dt, odt, _stream(None))
-    check(st, "cp_scored_attn_fwd")
+    L = lib()
+    need = L.cp_scored_attn_workspace_size(B, H, Sq, Skv, 1) if q_docs is not None else 0
+    _call("cp_scored_attn_fwd", lambda ws, n, st: L.cp_scored_attn_fwd(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), B, H, Hkv, Sq, Skv, D,
+        float(scale), ctypes.byref(r), ws, n, dt, odt, st), need, workspace, dev, stream)
 
 
 def cp_scored_attn_bwd(q, k, v, out, dout, lse, dq, dk, dv, scale: float, softcap: float = 0.0, slopes=None,
@@ -429,15 +441,14 @@ def cp_scored_attn_bwd(q, k, v, out, dout, lse, dq, dk, dv, scale: float, softca
     if dout.dtype != q.dtype or dk.dtype != dq.dtype or dv.dtype != dq.dtype:
         raise TypeError("dout must have q's dtype; dq, dk and dv must share one")
     dt, odt, gdt, dev = _dt(q), _out_dt("out", out, q), _out_dt("dq", dq, q), q.device
-    _dense_on(dev, q=q, k=k, v=v, out=out, dout=dout, lse=lse, dq=dq, dk=dk, dv=dv)
+    _dense_on(dev, q, k, v, out, dout, lse, dq, dk, dv)
     r = _score_rule(q, k, softcap, slopes, causal, prefix_lens, q_docs, kv_docs, q_pos0, kv_pos0)
-    with _place(dev, stream):
-        need = lib().cp_scored_attn_bwd_workspace_size(B, H, Sq, Skv, int(q_docs is not None))
-        ptr, size, _own = _scratch(workspace, need, dev)
-        st = lib().cp_scored_attn_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), dout.data_ptr(),
-                                      lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, H, Hkv, Sq, Skv,
-                                      D, float(scale), ctypes.byref(r), ptr, size, dt, odt, gdt, _stream(None))
-    check(st, "cp_scored_attn_bwd")
+    L = lib()
+    need = L.cp_scored_attn_bwd_workspace_size(B, H, Sq, Skv, q_docs is not None)
+    _call("cp_scored_attn_bwd", lambda ws, n, st: L.cp_scored_attn_bwd(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), dout.data_ptr(), lse.data_ptr(), dq.data_ptr(),
+        dk.data_ptr(), dv.data_ptr(), B, H, Hkv, Sq, Skv, D, float(scale), ctypes.byref(r), ws, n, dt, odt, gdt, st),
+        need, workspace, dev, stream)
 
 
 def _paged_shapes(k_cache, v_cache, block_table, seq_lens, B, Hkv, D, like):
@@ -468,17 +479,16 @@ def cp_paged_kv_append(k_new, v_new, k_cache, v_cache, block_table, seq_lens, ne
     B, T, Hkv, D = k_new.shape
     dt, dev = _dt(k_new), k_new.device
     pages, page, max_pages = _paged_shapes(k_cache, v_cache, block_table, seq_lens, B, Hkv, D, k_new)
-    _dense_on(dev, k_new=k_new, v_new=v_new, k_cache=k_cache, v_cache=v_cache, block_table=block_table,
-              seq_lens=seq_lens)
+    _dense_on(dev, k_new, v_new, k_cache, v_cache, block_table, seq_lens)
+    news = None
     if new_lens is not None:
         _i32("new_lens", new_lens, (B,))
-        _dense_on(dev, new_lens=new_lens)
-    with _place(dev, stream):
-        st = lib().cp_paged_kv_append(k_new.data_ptr(), v_new.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-                                      block_table.data_ptr() or 256, seq_lens.data_ptr(),
-                                      new_lens.data_ptr() if new_lens is not None else None, B, T, Hkv, D, pages, page,
-                                      max_pages, dt, _stream(None))
-    check(st, "cp_paged_kv_append")
+        _dense_on(dev, new_lens)
+        news = new_lens.data_ptr()
+    L = lib()
+    _call("cp_paged_kv_append", lambda ws, n, st: L.cp_paged_kv_append(
+        k_new.data_ptr(), v_new.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr() or 256,
+        seq_lens.data_ptr(), news, B, T, Hkv, D, pages, page, max_pages, dt, st), 0, None, dev, stream)
 
 
 def cp_paged_attn_workspace_size(B, H, Hkv, D, dtype=torch.bfloat16) -> int:
@@ -505,20 +515,18 @@ def cp_paged_attn_decode(q, k_cache, v_cache, block_table, seq_lens, out, lse, s
         raise TypeError("lse must be float32")
     dt, odt, dev = _dt(q), _out_dt("out", out, q), q.device
     pages, page, max_pages = _paged_shapes(k_cache, v_cache, block_table, seq_lens, B, Hkv, D, q)
-    _dense_on(dev, q=q, k_cache=k_cache, v_cache=v_cache, block_table=block_table, seq_lens=seq_lens, out=out, lse=lse)
+    _dense_on(dev, q, k_cache, v_cache, block_table, seq_lens, out, lse)
+    slope = None
     if slopes is not None:
         if slopes.dtype != torch.float32 or slopes.shape != (H,):
             raise ValueError("slopes must be float32 [H]")
-        _dense_on(dev, slopes=slopes)
-    with _place(dev, stream):
-        need = lib().cp_paged_attn_workspace_size(B, H, Hkv, D, dt)
-        ptr, size, _own = _scratch(workspace, need, dev)
-        st = lib().cp_paged_attn_decode(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
-                                        seq_lens.data_ptr(), out.data_ptr(), lse.data_ptr(), B, H, Hkv, D, pages, page,
-                                        max_pages, float(scale), float(softcap),
-                                        slopes.data_ptr() if slopes is not None else None, ptr, size, dt, odt,
-                                        _stream(None))
-    check(st, "cp_paged_attn_decode")
+        _dense_on(dev, slopes)
+        slope = slopes.data_ptr()
+    L = lib()
+    _call("cp_paged_attn_decode", lambda ws, n, st: L.cp_paged_attn_decode(
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
+        out.data_ptr(), lse.data_ptr(), B, H, Hkv, D, pages, page, max_pages, float(scale), float(softcap),
+        slope, ws, n, dt, odt, st), L.cp_paged_attn_workspace_size(B, H, Hkv, D, dt), workspace, dev, stream)
 
 
 def cp_check_device_status(stream=None) -> int:

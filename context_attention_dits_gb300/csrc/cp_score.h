@@ -6,6 +6,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <climits>
 #include <cstdint>
 
@@ -104,6 +105,19 @@ struct PagedArgs {
 inline int paged_rows(bool bf16) { return bf16 ? 16 : 8; }
 cudaError_t launch_paged_append(const PagedArgs& a, int elem_bytes, cudaStream_t s);
 cudaError_t launch_paged_decode(const PagedArgs& a, bool bf16, cudaStream_t s);
+
+// Lets a kernel use `bytes` of dynamic shared memory, once per device (the call
+// costs as much host time as a launch).
+template <auto kKernel>
+cudaError_t allow_smem(int bytes) {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (dev < 64 && (done.load(std::memory_order_acquire) >> dev & 1))) return e;
+  e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev < 64) done.fetch_or(uint64_t{1} << dev, std::memory_order_release);
+  return e;
+}
 
 // From cp_api.cu: the checks and tensor maps that the host drivers share.
 // 0, or the cp_status of the current device's check.

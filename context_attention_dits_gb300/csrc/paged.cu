@@ -556,8 +556,7 @@ template <int D, typename T>
 cudaError_t decode_d(const PagedArgs& a, cudaStream_t s) {
   using C = DecCfg<D, T>;
   static_assert(C::kSmem + (kPagedMaxBatch + 8) * 4 <= 227 * 1024, "shared memory budget");
-  cudaError_t e =
-      cudaFuncSetAttribute(paged_decode_kernel<D, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  cudaError_t e = allow_smem<paged_decode_kernel<D, T>>(C::kSmem);
   if (e != cudaSuccess) return e;
   // blocks of the list if every table were full; a unit of one block is never split
   const int groups = (a.G + C::kRows - 1) / C::kRows;

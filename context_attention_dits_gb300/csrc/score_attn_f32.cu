@@ -461,15 +461,10 @@ __global__ void __launch_bounds__(256) doc_ranges_kernel(const __grid_constant__
   }
 }
 
-template <typename K>
-cudaError_t allow_smem(K kernel, int bytes) {
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-}
-
 template <int D>
 cudaError_t fwd_d(const ScoreArgs& a, cudaStream_t s) {
   constexpr int bytes = fwd_floats<D>() * 4;
-  cudaError_t e = allow_smem(score_fwd_f32_kernel<D>, bytes);
+  cudaError_t e = allow_smem<score_fwd_f32_kernel<D>>(bytes);
   if (e != cudaSuccess) return e;
   score_fwd_f32_kernel<D><<<dim3((a.Sq + kR - 1) / kR, a.H, a.B), kThr, bytes, s>>>(a);
   return cudaGetLastError();
@@ -478,8 +473,8 @@ cudaError_t fwd_d(const ScoreArgs& a, cudaStream_t s) {
 template <int D>
 cudaError_t bwd_d(const ScoreArgs& a, cudaStream_t s) {
   constexpr int bytes = bwd_floats<D>() * 4;
-  cudaError_t e = allow_smem(score_dq_f32_kernel<D>, bytes);
-  if (e == cudaSuccess) e = allow_smem(score_dkdv_f32_kernel<D>, bytes);
+  cudaError_t e = allow_smem<score_dq_f32_kernel<D>>(bytes);
+  if (e == cudaSuccess) e = allow_smem<score_dkdv_f32_kernel<D>>(bytes);
   if (e != cudaSuccess) return e;
   if (a.Sq > 0) {
     const int64_t rows = static_cast<int64_t>(a.B) * a.Sq * a.H;

@@ -929,7 +929,7 @@ cudaError_t launch_rule(const ScoreArgs& a, const BwdMaps& m, cudaStream_t s) {
   constexpr int kAlloc = bwd_alloc<D>();
   static_assert(kAlloc <= 227 * 1024, "shared memory budget");
   auto kernel = score_bwd_tc_kernel<D, kCap, kBias>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kAlloc);
+  cudaError_t e = allow_smem<score_bwd_tc_kernel<D, kCap, kBias>>(kAlloc);
   if (e != cudaSuccess) return e;
   const int64_t ctas = (static_cast<int64_t>((a.Skv + kT - 1) / kT) * a.Hkv + static_cast<int64_t>((a.Sq + kT - 1) / kT) * a.H) * a.B;
   if (ctas > 0x7fffffff) return cudaErrorInvalidValue;

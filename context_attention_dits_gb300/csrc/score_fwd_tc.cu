@@ -611,7 +611,7 @@ cudaError_t launch_rule(const ScoreArgs& a, const CUtensorMap& tq, const CUtenso
   using L = Smem<D>;
   static_assert(L::kAlloc <= 227 * 1024, "shared memory budget");
   auto kernel = score_fwd_tc_kernel<D, kCap, kBias>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
+  cudaError_t e = allow_smem<score_fwd_tc_kernel<D, kCap, kBias>>(L::kAlloc);
   if (e != cudaSuccess) return e;
   const int64_t items = static_cast<int64_t>((a.Sq + 2 * kTileM - 1) / (2 * kTileM)) * a.H * a.B;
   if (items > 0x7fffffff) return cudaErrorInvalidValue;
