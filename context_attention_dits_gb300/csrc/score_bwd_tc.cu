@@ -147,43 +147,39 @@ template <bool kCap, bool kBias, int kStep, typename NL, typename ND>
 __device__ __forceinline__ void row_pass(const uint32_t (&sr)[32], const uint32_t (&dr)[32], const CapCoef& cc,
                                          float c2, float inv2, float slope2, float d0, uint32_t on, NL nl, ND nd,
                                          uint32_t (&pp)[16], uint32_t (&dd)[16]) {
+  const f32x2 c22 = pair(c2, c2), inv22 = pair(inv2, inv2), one2 = pair(1.f, 1.f);
   // kHow: 0 no cap, 3 and 6 the polynomials, 1 exact
   auto pass = [&](auto how_c) {
     constexpr int kHow = decltype(how_c)::value;
 #pragma unroll
     for (int e = 0; e < 32; e += 2) {
-      const float s0 = u2f(sr[e]), s1 = u2f(sr[e + 1]);
-      float b0, b1, n0, n1;
-      nl(e, b0, b1);
-      nd(e, n0, n1);
+      const f32x2 s2 = pair_u(sr[e], sr[e + 1]);
+      f32x2 b2 = nl(e);
       if constexpr (kBias) {
-        b0 = fmaf(-slope2, fabsf(d0 + static_cast<float>(kStep * e)), b0);
-        b1 = fmaf(-slope2, fabsf(d0 + static_cast<float>(kStep * (e + 1))), b1);
+        const float a0 = fabsf(d0 + static_cast<float>(kStep * e)), a1 = fabsf(d0 + static_cast<float>(kStep * (e + 1)));
+        b2 = fma_x2(pair(-slope2, -slope2), pair(a0, a1), b2);
       }
-      float t0, t1, g0, g1, c0 = 1.f, c1 = 1.f;
+      f32x2 t2, c1 = one2;
       if constexpr (kHow == 0) {
-        fma2(t0, t1, s0, s1, c2, c2, b0, b1);
+        t2 = fma_x2(s2, c22, b2);
       } else {
-        float y0, y1;
+        f32x2 y2;
         if constexpr (kHow >= 3) {
-          float u0, u1, f0, f1;
-          fma2(u0, u1, s0, s1, s0, s1, 0.f, 0.f);
-          cap_poly<kHow>(cc, u0, u1, f0, f1);
-          fma2(y0, y1, s0, s1, f0, f1, 0.f, 0.f);
+          y2 = mul_x2(s2, cap_poly<kHow>(cc, mul_x2(s2, s2)));
         } else {
-          y0 = cap_exact(cc, s0);
-          y1 = cap_exact(cc, s1);
+          y2 = pair(cap_exact(cc, u2f(sr[e])), cap_exact(cc, u2f(sr[e + 1])));
         }
-        float z0, z1;
-        fma2(z0, z1, y0, y1, y0, y1, 0.f, 0.f);
-        fma2(c0, c1, z0, z1, inv2, inv2, 1.f, 1.f);  // inv2 = -1 / (cap log2e)^2
-        t0 = y0 + b0;
-        t1 = y1 + b1;
+        c1 = fma_x2(mul_x2(y2, y2), inv22, one2);  // 1 - (y / cap)^2; inv2 = -1 / (cap log2e)^2
+        t2 = add_x2(y2, b2);
       }
-      fma2(g0, g1, u2f(dr[e]), u2f(dr[e + 1]), 1.f, 1.f, n0, n1);
-      float p0 = ex2_approx(t0), p1 = ex2_approx(t1), q0, q1;
-      fma2(q0, q1, p0, p1, g0, g1, 0.f, 0.f);
-      if constexpr (kHow != 0) fma2(q0, q1, q0, q1, c0, c1, 0.f, 0.f);
+      const f32x2 g2 = add_x2(pair_u(dr[e], dr[e + 1]), nd(e));
+      float t0, t1;
+      split(t2, t0, t1);
+      const float p0 = ex2_approx(t0), p1 = ex2_approx(t1);
+      f32x2 q2 = mul_x2(pair(p0, p1), g2);
+      if constexpr (kHow != 0) q2 = mul_x2(q2, c1);
+      float q0, q1;
+      split(q2, q0, q1);
       pp[e >> 1] = pack_bf16x2(p0, p1);
       dd[e >> 1] = pack_bf16x2(q0, q1);
     }
@@ -191,11 +187,8 @@ __device__ __forceinline__ void row_pass(const uint32_t (&sr)[32], const uint32_
   if constexpr (kCap) {
     float um = 0.f;
 #pragma unroll
-    for (int e = 0; e < 32; e += 2) {
-      float u0, u1;
-      fma2(u0, u1, u2f(sr[e]), u2f(sr[e + 1]), u2f(sr[e]), u2f(sr[e + 1]), 0.f, 0.f);
-      um = fmax3(um, u0, u1);
-    }
+    for (int e = 0; e < 32; e += 4) um = fmax3(um, fmaxf(fabsf(u2f(sr[e])), fabsf(u2f(sr[e + 1]))), fmaxf(fabsf(u2f(sr[e + 2])), fabsf(u2f(sr[e + 3]))));
+    um *= um;
     if (__all_sync(0xffffffffu, um <= cc.u3))
       pass(std::integral_constant<int, 3>{});
     else if (__all_sync(0xffffffffu, um <= cc.u6))
@@ -311,7 +304,7 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap& tq64, const CUtensor
       }
     }
     int issued[kSlots] = {0, 0, 0, 0};
-    TileWalk cur(bits, t0, ntq);
+    TileWalk cur(bits, t0, ntq, t0 - 1);
     int h = hk * a.G;
     for (int j = 0; j < NJ; ++j) {
       const int s = j & (kSlots - 1);
@@ -331,8 +324,8 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap& tq64, const CUtensor
       __syncwarp();
       ++issued[s];
       cur.next();
-      if (cur.t >= ntq) {
-        cur = TileWalk(bits, t0, ntq);
+      if (cur.done()) {
+        cur = TileWalk(bits, t0, ntq, t0 - 1);
         ++h;
       }
     }
@@ -444,7 +437,7 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap& tq64, const CUtensor
     const int kd = a.qdoc && kvalid ? a.kdoc[static_cast<int64_t>(b) * a.Skv + jkey] : -1;
     const int* qdoc = a.qdoc + static_cast<int64_t>(b) * a.Sq;
     bool ok = true;
-    TileWalk cur(bits, t0, ntq);
+    TileWalk cur(bits, t0, ntq, t0 - 1);
     int h = hk * a.G;
     float slope2 = kBias ? a.slopes[h] * kLog2e : 0.f;
     for (int j = 0; j < NJ; ++j) {
@@ -477,23 +470,21 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap& tq64, const CUtensor
       const float* dlt = s_dlt + q * kSub + hc * 32;
       row_pass<kCap, kBias, 1>(
           sr, dr, cc, c2, inv2, slope2, static_cast<float>(d0), on,
-          [&](int e, float& x0, float& x1) {
+          [&](int e) {
             const float2 v = *reinterpret_cast<const float2*>(lse2 + e);
-            x0 = -v.x;
-            x1 = -v.y;
+            return pair(-v.x, -v.y);
           },
-          [&](int e, float& x0, float& x1) {
+          [&](int e) {
             const float2 v = *reinterpret_cast<const float2*>(dlt + e);
-            x0 = -v.x;
-            x1 = -v.y;
+            return pair(-v.x, -v.y);
           },
           pp, dd);
       // P^T over the first half of this warp's S^T columns, dS^T over those of dP^T
       tmem_st16(t_s, pp);
       tmem_st16(t_dp, dd);
       cur.next();
-      if (cur.t >= ntq) {
-        cur = TileWalk(bits, t0, ntq);
+      if (cur.done()) {
+        cur = TileWalk(bits, t0, ntq, t0 - 1);
         ++h;
         if (kBias && j + 1 < NJ) slope2 = a.slopes[h] * kLog2e;
       }
@@ -631,7 +622,7 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap& tk64, const CUtensorMa
       tma_prefetch_desc(&tv64);
     }
     int issued[kDqSlots] = {};
-    TileWalk cur(bits, 0, ntk);
+    TileWalk cur(bits, 0, ntk, -1);
     for (int j = 0; j < NJ; ++j) {
       const int s = j % kDqSlots;
       const uint32_t ph = (j / kDqSlots) & 1;
@@ -778,7 +769,7 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap& tk64, const CUtensorMa
     const int qd = a.qdoc && row < nq ? a.qdoc[static_cast<int64_t>(b) * a.Sq + q0 + row] : -1;
     const int* kdoc = a.kdoc + static_cast<int64_t>(b) * a.Skv;
     const float slope2 = kBias ? a.slopes[h] * kLog2e : 0.f;
-    TileWalk cur(bits, 0, ntk);
+    TileWalk cur(bits, 0, ntk, -1);
     for (int j = 0; j < NJ; ++j) {
       const int ts = j & 1;
       const int j0 = cur.t * kSub + hc * 32;  // the key of this warp's first column
@@ -805,7 +796,7 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap& tk64, const CUtensorMa
       tmem_pin(dr);
       row_pass<kCap, kBias, -1>(
           sr, dr, cc, c2, inv2, slope2, static_cast<float>(a.rel + q0 + row - j0), on,
-          [&](int, float& x0, float& x1) { x0 = x1 = nl2; }, [&](int, float& x0, float& x1) { x0 = x1 = ndl; }, pp, dd);
+          [&](int) { return pair(nl2, nl2); }, [&](int) { return pair(ndl, ndl); }, pp, dd);
       tmem_st16(t_s, dd);  // dS over the first half of this warp's S columns
       cur.next();
       tmem_wait_st();

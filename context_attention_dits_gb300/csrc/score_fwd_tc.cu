@@ -123,9 +123,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   // with the most causal keys first, heads fastest ----
   const int npair = (a.Sq + 2 * kTileM - 1) / (2 * kTileM);
   const int bh = blockIdx.x % (a.H * a.B);
-  const int pair = npair - 1 - static_cast<int>(blockIdx.x / (a.H * a.B));
+  const int item = npair - 1 - static_cast<int>(blockIdx.x / (a.H * a.B));
   const int h = bh % a.H, b = bh / a.H, hk = h / a.G;
-  const int row0 = pair * 2 * kTileM;
+  const int row0 = item * 2 * kTileM;
   const int nrows = min(2 * kTileM, a.Sq - row0);
   const int nq = nrows > kTileM ? 2 : 1;
   const int plim = prefix_limit(a, b);
@@ -167,6 +167,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     NT = static_cast<int>(misc[2]);
   }
   const uint32_t* bits = a.qdoc ? act : nullptr;
+  // with a bias the nearest keys weigh most: from the rows' own position
+  // outwards, so that the running maximum is found first and keeps
+  const int start = kBias ? min(ntile - 1, max(-1, (a.rel + row0 + nrows - 1) / kTileN)) : -1;
   const uint32_t tmem = misc[0];
   const uint64_t tmo = a.timeout_ns;
 
@@ -188,7 +191,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_load_4d(sb + L::kOffQ + i * L::kQTile + c * L::kHalf, &tq, qb, c * 64, h, row0 + i * kTileM, b);
       };
       load_q(0);
-      TileWalk cur(bits, 0, ntile);
+      TileWalk cur(bits, 0, ntile, start);
       for (int it = 0; it < NT; ++it) {
         const int s = it & 1;
         const uint32_t ph = (it >> 1) & 1;
@@ -341,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float m_used = -INFINITY, l = 0.f;
       int level = 0;  // of the cap's polynomial: 3, 6 terms' range, or neither
       bool ok = true;
-      TileWalk cur(bits, 0, ntile);
+      TileWalk cur(bits, 0, ntile, start);
       for (int it = 0; it < NT; ++it) {
         const int kv0 = cur.t * kTileN;
         const bool mix = bits != nullptr && ((mixed[i * kMapWords + (cur.t >> 5)] >> (cur.t & 31)) & 1u);
@@ -386,10 +389,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto speculate = [&](auto mode_c, auto mask_c) -> float {
           constexpr int kMode = decltype(mode_c)::value;
           constexpr bool kMask = decltype(mask_c)::value;
-          float ls[4] = {0.f, 0.f, 0.f, 0.f};
-          float um[4] = {0.f, 0.f, 0.f, 0.f};
+          f32x2 ls[2] = {0ull, 0ull};
+          float um[2] = {0.f, 0.f};
           const float bs = kBias ? (below ? slope2 : -slope2) : 0.f;
           const float bb = kBias ? fmaf(-bs, static_cast<float>(dq), -m_used) : -m_used;
+          const f32x2 bs2 = pair(bs, bs), bb2 = pair(bb, bb), sl22 = pair(sl2, sl2);
           uint32_t buf[2][32];
           tmem_ld32(t_s, buf[0]);
 #pragma unroll
@@ -400,34 +404,32 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (c < 3) tmem_ld32(t_s + (c + 1) * 32, buf[(c + 1) & 1]);
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              float s0 = u2f(sr[2 * e]), s1 = u2f(sr[2 * e + 1]);
               const bool on0 = !kMask || ((on[c] >> (2 * e)) & 1u), on1 = !kMask || ((on[c] >> (2 * e + 1)) & 1u);
-              float x0, x1, f0 = sl2, f1 = sl2;
+              f32x2 s2 = pair_u(sr[2 * e], sr[2 * e + 1]), fac = sl22;
               if constexpr (kMode >= 3) {
-                if (kMask) {
-                  s0 = on0 ? s0 : 0.f;
-                  s1 = on1 ? s1 : 0.f;
-                }
+                if (kMask) s2 = pair_u(on0 ? sr[2 * e] : 0u, on1 ? sr[2 * e + 1] : 0u);
+                const f32x2 u2 = mul_x2(s2, s2);
                 float u0, u1;
-                fma2(u0, u1, s0, s1, s0, s1, 0.f, 0.f);
-                um[e & 3] = fmax3(um[e & 3], u0, u1);
-                cap_poly<kMode>(cc, u0, u1, f0, f1);
+                split(u2, u0, u1);
+                um[e & 1] = fmax3(um[e & 1], u0, u1);
+                fac = cap_poly<kMode>(cc, u2);
               }
-              const float b0 = kBias ? fmaf(bs, static_cast<float>(32 * c + 2 * e), bb) : bb;
-              const float b1 = kBias ? fmaf(bs, static_cast<float>(32 * c + 2 * e + 1), bb) : bb;
-              fma2(x0, x1, s0, s1, f0, f1, b0, b1);
+              const f32x2 x2 = fma_x2(s2, fac, kBias ? fma_x2(bs2, columns(32 * c + 2 * e), bb2) : bb2);
+              float x0, x1;
+              split(x2, x0, x1);
               if (kMask) {
                 x0 = on0 ? x0 : -INFINITY;
                 x1 = on1 ? x1 : -INFINITY;
               }
               const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
               pk[16 * c + e] = pack_bf16x2(p0, p1);
-              const int w = (2 * e) & 3;
-              fma2(ls[w], ls[w + 1], p0, p1, 1.f, 1.f, ls[w], ls[w + 1]);
+              ls[e & 1] = add_x2(ls[e & 1], pair(p0, p1));
             }
           }
-          umax = fmaxf(fmaxf(um[0], um[1]), fmaxf(um[2], um[3]));
-          return (ls[0] + ls[1]) + (ls[2] + ls[3]);
+          umax = fmaxf(um[0], um[1]);
+          float l0, l1;
+          split(add_x2(ls[0], ls[1]), l0, l1);
+          return l0 + l1;
         };
         float f = 1.f, lsum = INFINITY;
         bool fits = false;

@@ -14,6 +14,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <cstring>
 
 #include "cp_ptx.cuh"
 #include "cp_score.h"
@@ -23,11 +24,44 @@ namespace cp {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.69314718055994531f;
 
+// Pairs of fp32 values in a 64-bit register pair, for the packed instructions
+// (one issue slot a pair). Coefficients are kept as pairs of equal values, so
+// that they are operands as they stand and no register pair is built for them.
+using f32x2 = unsigned long long;
+__device__ __forceinline__ f32x2 pair(float lo, float hi) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ f32x2 pair_u(uint32_t lo, uint32_t hi) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+__device__ __forceinline__ void split(f32x2 v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ f32x2 fma_x2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f32x2 mul_x2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 add_x2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 // Coefficients and limits of a launch's cap (host: make_cap_coef).
 struct CapCoef {
-  float p3[4], u3;  // for s^2 <= u3
-  float p6[7], u6;  // for s^2 <= u6
-  float a0, capl2;  // exact: capl2 (1 - 2 / (1 + 2^(s a0)))
+  f32x2 p3[4], p6[7];  // pairs of equal values
+  float u3, u6;        // the polynomials serve s^2 <= u3, u6
+  float a0, capl2;     // exact: capl2 (1 - 2 / (1 + 2^(s a0)))
 };
 
 inline CapCoef make_cap_coef(float scale, float cap) {
@@ -37,17 +71,24 @@ inline CapCoef make_cap_coef(float scale, float cap) {
   CapCoef c{};
   if (!(cap > 0.f)) return c;
   const double l2e = 1.4426950408889634, r = static_cast<double>(scale) / cap;
-  double pw = r;
+  auto twice = [](double x) {
+    const float f = static_cast<float>(x);
+    uint32_t u;
+    std::memcpy(&u, &f, 4);
+    return static_cast<f32x2>(u) << 32 | u;
+  };
   // a coefficient that fp32 cannot hold to full precision rules its polynomial out
   bool ok3 = true, ok6 = true;
+  double pw = r;
   for (int k = 0; k < 7; ++k, pw *= r * r) {
-    const double x = cap * l2e * pw;
+    const double x = cap * l2e * pw, ax = x < 0 ? -x : x;
+    const bool fits = r == 0.0 || (ax > 1e-30 && ax < 1e30);
     if (k < 4) {
-      c.p3[k] = static_cast<float>(x * t3[k]);
-      ok3 = ok3 && (pw == 0.0 || (x * t3[k] > 1e-30 || x * t3[k] < -1e-30)) && x < 1e30 && x > -1e30;
+      c.p3[k] = twice(x * t3[k]);
+      ok3 = ok3 && fits;
     }
-    c.p6[k] = static_cast<float>(x * t6[k]);
-    ok6 = ok6 && (pw == 0.0 || (x * t6[k] > 1e-30 || x * t6[k] < -1e-30)) && x < 1e30 && x > -1e30;
+    c.p6[k] = twice(x * t6[k]);
+    ok6 = ok6 && fits;
   }
   const double lim = r != 0.0 ? 1.0 / (r * r) : 3e38;
   c.u3 = ok3 ? static_cast<float>(lim * 0.25 < 3e38 ? lim * 0.25 : 3e38) : -1.f;
@@ -59,21 +100,29 @@ inline CapCoef make_cap_coef(float scale, float cap) {
 
 // The polynomials' factor of s, for a pair of scores with u = s^2.
 template <int kDeg>
-__device__ __forceinline__ void cap_poly(const CapCoef& c, float u0, float u1, float& f0, float& f1) {
-  if constexpr (kDeg == 3) {
-    f0 = f1 = c.p3[3];
+__device__ __forceinline__ f32x2 cap_poly(const CapCoef& c, f32x2 u) {
+  const f32x2* p = kDeg == 3 ? c.p3 : c.p6;
+  f32x2 f = fma_x2(p[kDeg], u, p[kDeg - 1]);
 #pragma unroll
-    for (int k = 2; k >= 0; --k) fma2(f0, f1, f0, f1, u0, u1, c.p3[k], c.p3[k]);
-  } else {
-    f0 = f1 = c.p6[6];
-#pragma unroll
-    for (int k = 5; k >= 0; --k) fma2(f0, f1, f0, f1, u0, u1, c.p6[k], c.p6[k]);
-  }
+  for (int k = kDeg - 2; k >= 0; --k) f = fma_x2(f, u, p[k]);
+  return f;
 }
 
 __device__ __forceinline__ float cap_exact(const CapCoef& c, float s) {
   return c.capl2 * (1.f - __fdividef(2.f, 1.f + ex2_approx(s * c.a0)));
 }
+
+// 0 .. 127 in pairs: the columns of a tile, for biases linear in the column.
+__constant__ float kColumn[128] = {
+    0.f, 1.f, 2.f, 3.f, 4.f, 5.f, 6.f, 7.f, 8.f, 9.f, 10.f, 11.f, 12.f, 13.f, 14.f, 15.f,
+    16.f, 17.f, 18.f, 19.f, 20.f, 21.f, 22.f, 23.f, 24.f, 25.f, 26.f, 27.f, 28.f, 29.f, 30.f, 31.f,
+    32.f, 33.f, 34.f, 35.f, 36.f, 37.f, 38.f, 39.f, 40.f, 41.f, 42.f, 43.f, 44.f, 45.f, 46.f, 47.f,
+    48.f, 49.f, 50.f, 51.f, 52.f, 53.f, 54.f, 55.f, 56.f, 57.f, 58.f, 59.f, 60.f, 61.f, 62.f, 63.f,
+    64.f, 65.f, 66.f, 67.f, 68.f, 69.f, 70.f, 71.f, 72.f, 73.f, 74.f, 75.f, 76.f, 77.f, 78.f, 79.f,
+    80.f, 81.f, 82.f, 83.f, 84.f, 85.f, 86.f, 87.f, 88.f, 89.f, 90.f, 91.f, 92.f, 93.f, 94.f, 95.f,
+    96.f, 97.f, 98.f, 99.f, 100.f, 101.f, 102.f, 103.f, 104.f, 105.f, 106.f, 107.f, 108.f, 109.f, 110.f, 111.f,
+    112.f, 113.f, 114.f, 115.f, 116.f, 117.f, 118.f, 119.f, 120.f, 121.f, 122.f, 123.f, 124.f, 125.f, 126.f, 127.f};
+__device__ __forceinline__ f32x2 columns(int c) { return *reinterpret_cast<const f32x2*>(kColumn + c); }
 
 // The row of document ranges of 64-row blocks, and the range of n consecutive
 // blocks (those past the row's end left out).
@@ -84,25 +133,63 @@ __device__ __forceinline__ DocRange doc_span(const DocRange* row, int nblk, int 
   return r;
 }
 
-// The tiles of a launch that meet a CTA's rows, as a bitmap in shared memory:
-// bit t of act, and whether the tile holds a pair of different documents.
-// Without documents every tile of [t0, t1) is taken.
+// The tiles of [lo, hi) that a CTA walks: all, or those whose bit is set in act
+// (a bitmap in shared memory). First from `start` down to lo, then from
+// start + 1 up; start < lo walks upwards only.
 struct TileWalk {
-  const uint32_t* act;  // nullptr: all of [t0, t1)
-  int t, t1;
-  __device__ __forceinline__ TileWalk(const uint32_t* bits, int t0, int end) : act(bits), t(t0 - 1), t1(end) { next(); }
+  const uint32_t* act;
+  int t, lo, hi, start;
+  bool down;
+  __device__ __forceinline__ TileWalk(const uint32_t* bits, int lo_, int hi_, int start_)
+      : act(bits), t(start_), lo(lo_), hi(hi_), start(start_ < lo_ ? lo_ - 1 : start_), down(start_ >= lo_) {
+    if (down) {
+      find_down();
+    } else {
+      t = lo - 1;
+      next();
+    }
+  }
+  __device__ __forceinline__ bool done() const { return t >= hi; }
   __device__ __forceinline__ void next() {
+    if (down) {
+      --t;
+      find_down();
+      return;
+    }
     ++t;
-    if (act == nullptr || t >= t1) return;
+    if (act == nullptr || t >= hi) return;
     uint32_t w = act[t >> 5] >> (t & 31);
     if (w) {
       t += __ffs(w) - 1;
       return;
     }
     int i = (t >> 5) + 1;
-    const int ni = (t1 + 31) >> 5;
+    const int ni = (hi + 31) >> 5;
     while (i < ni && (w = act[i]) == 0) ++i;
-    t = i < ni ? i * 32 + __ffs(w) - 1 : t1;
+    t = i < ni ? i * 32 + __ffs(w) - 1 : hi;
+  }
+  // the last set tile at or below t, else on to the upward part
+  __device__ __forceinline__ void find_down() {
+    if (act != nullptr && t >= lo) {
+      uint32_t w = act[t >> 5] << (31 - (t & 31));
+      if (w) {
+        t -= __clz(w);
+        return;
+      }
+      int i = (t >> 5) - 1;
+      const int i0 = lo >> 5;
+      while (i >= i0 && (w = act[i]) == 0) --i;
+      if (i >= i0) {
+        t = i * 32 + 31 - __clz(w);
+        return;
+      }
+      t = lo - 1;
+    }
+    if (t < lo) {
+      down = false;
+      t = start;
+      next();
+    }
   }
 };
 
