@@ -11,44 +11,82 @@
 // where h runs over the query heads that share the key/value head.
 //
 // Tiles: a CTA owns 32 rows (queries; keys for dk, dv) and walks 64-row tiles
-// of the other side. 128 threads; a thread forms a 4 x 4 block of scores (rows
-// 4 ti .. 4 ti + 3, columns tj + 16 c), then 4 rows x D/16 columns of the
-// second product. Every tile is kept row-major with D + 4 floats a row: a
+// of the other side. 128 threads form a group; a thread forms a 4 x 4 block of
+// scores (rows 4 ti .. 4 ti + 3, columns tj + 16 c), then 4 rows x D/16 columns
+// of the second product. Every tile is kept row-major with D + 4 floats a row: a
 // float4 column of 16 neighbouring rows then takes two wavefronts (the least
 // for 256 bytes), so one copy of K serves both Q K^T and dS K and nothing is
 // transposed. A 4 x 4 block costs 8 16-byte loads per 64 FMAs.
+// What bounds these kernels at the sizes fp32 is used for (a few hundred rows:
+// less than a CTA per multiprocessor) is the latency of a tile's chain of
+// copies, loads and barriers, so a CTA holds kGroups groups (as many as shared
+// memory holds tiles for: 4 at D = 64, 2 at D = 128) that take the tiles in
+// turn, each with its own buffers, barrier and running state, joined once at
+// the end; and a buffer's next tile is copied (16-byte asynchronous copies) as
+// soon as its last reader is through.
 #include <cuda_runtime.h>
 
 #include <climits>
 #include <cmath>
 #include <cstdint>
 
+#include "cp_ptx.cuh"
 #include "cp_score.h"
 
 namespace cp {
 namespace {
 
-constexpr int kThr = 128;
+constexpr int kGrp = 128;     // threads of a group
 constexpr int kR = 32;        // rows of the owned tile
 constexpr int kC = 64;        // rows of a streamed tile
 constexpr int kPT = kR + 4;   // row of the transposed probability tile
 constexpr float kL2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.69314718055994531f;
+constexpr float kLn2f = 0.69314718055994531f;
+
+template <int D>
+struct Cfg {
+  static constexpr int kGroups = 256 / D;
+  static constexpr int kThreads = kGroups * kGrp;
+  static constexpr int kRow = D + 4;                           // floats of a row
+  static constexpr int kOwn = kR * kRow, kTile = kC * kRow;    // floats of a tile
+  static constexpr int kP = kC * kPT;
+  static constexpr int kFwd = kOwn + kGroups * (2 * kTile + kP);
+  static constexpr int kBwd = 2 * kOwn + kGroups * (2 * kTile + kP + 2 * kC);
+  static_assert(2 * kOwn + 2 * kR <= 2 * kTile + kP, "a group's buffers hold its results at the end");
+};
 
 __device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-
 __device__ __forceinline__ void store4(void* base, int64_t i, float4 x) {
   *reinterpret_cast<float4*>(static_cast<float*>(base) + i) = x;
 }
+__device__ __forceinline__ float4 scaled(float4 x, float f) { return make_float4(x.x * f, x.y * f, x.z * f, x.w * f); }
+__device__ __forceinline__ void add4(float4& x, float4 y) {
+  x.x += y.x;
+  x.y += y.y;
+  x.z += y.z;
+  x.w += y.w;
+}
 
-// Rows row0 .. row0 + n - 1 (of `rows`; the others zero) of a [., S, heads, D]
-// tensor's head into dst, D + 4 floats a row.
+// Barrier of the caller's group.
+__device__ __forceinline__ void group_sync(int g) { asm volatile("bar.sync %0, %1;" ::"r"(g + 1), "n"(kGrp) : "memory"); }
+
+__device__ __forceinline__ void copy16(float* dst, const float* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(on ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// `rows` rows of a [., S, heads, D] tensor's head (the first n exist, the
+// others become zero) into dst, by threads t of nt.
 template <int D>
-__device__ __forceinline__ void load_rows(float* dst, const float* src, int64_t stride, int n, int rows) {
-  for (int e = threadIdx.x; e < rows * (D / 4); e += kThr) {
+__device__ __forceinline__ void copy_rows(float* dst, const float* src, int64_t stride, int n, int rows, int t, int nt) {
+  for (int e = t; e < rows * (D / 4); e += nt) {
     const int r = e / (D / 4), d = (e % (D / 4)) * 4;
-    const float4 x = r < n ? load4(src + r * stride + d) : make_float4(0.f, 0.f, 0.f, 0.f);
-    *reinterpret_cast<float4*>(dst + r * (D + 4) + d) = x;
+    copy16(dst + r * (D + 4) + d, src + (r < n ? r * stride + d : 0), r < n);
   }
 }
 
@@ -63,9 +101,9 @@ __device__ __forceinline__ void dots(float (&s)[4][4], const float* a, const flo
   for (int d = 0; d < D; d += 4) {
     float4 x[4], y[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const float4*>(a + (4 * ti + i) * (D + 4) + d);
+    for (int i = 0; i < 4; ++i) x[i] = load4(a + (4 * ti + i) * (D + 4) + d);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) y[c] = *reinterpret_cast<const float4*>(b + (tj + 16 * c) * (D + 4) + d);
+    for (int c = 0; c < 4; ++c) y[c] = load4(b + (tj + 16 * c) * (D + 4) + d);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -80,11 +118,11 @@ template <int D>
 __device__ __forceinline__ void second(float4 (&acc)[4][D / 64], const float* pt, const float* b, int ti, int tj) {
 #pragma unroll 4
   for (int j = 0; j < kC; ++j) {
-    const float4 p = *reinterpret_cast<const float4*>(pt + j * kPT + 4 * ti);
+    const float4 p = load4(pt + j * kPT + 4 * ti);
     const float w[4] = {p.x, p.y, p.z, p.w};
 #pragma unroll
     for (int u = 0; u < D / 64; ++u) {
-      const float4 y = *reinterpret_cast<const float4*>(b + j * (D + 4) + 4 * tj + 64 * u);
+      const float4 y = load4(b + j * (D + 4) + 4 * tj + 64 * u);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         acc[i][u].x = fmaf(w[i], y.x, acc[i][u].x);
@@ -94,6 +132,24 @@ __device__ __forceinline__ void second(float4 (&acc)[4][D / 64], const float* pt
       }
     }
   }
+}
+
+template <int D>
+__device__ __forceinline__ void clear(float4 (&acc)[4][D / 64]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int u = 0; u < D / 64; ++u) acc[i][u] = make_float4(0.f, 0.f, 0.f, 0.f);
+}
+
+// acc as a [kR][D] tile (rows of D + 4) in shared memory
+template <int D>
+__device__ __forceinline__ void put(const float4 (&acc)[4][D / 64], float* dst, int ti, int tj) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int u = 0; u < D / 64; ++u)
+      *reinterpret_cast<float4*>(dst + (4 * ti + i) * (D + 4) + 4 * tj + 64 * u) = acc[i][u];
 }
 
 // The score of a pair in units of log2, before the mask, and the derivative of
@@ -116,37 +172,67 @@ struct Scorer {
   }
 };
 
-// Document ranges of the owned tile [row0, row0 + 32) (one 64-row block) and
-// of a streamed 64-row tile starting at a multiple of 64.
+// The document range of the 64-row block that holds row `row`.
 __device__ __forceinline__ DocRange doc_range(const DocRange* r, int b, int S, int row) {
   return r[static_cast<int64_t>(b) * ((S + kDocBlock - 1) / kDocBlock) + row / kDocBlock];
 }
 
-template <int D>
-constexpr int fwd_floats() {
-  return (kR + 2 * kC) * (D + 4) + kC * kPT;
-}
+// The tiles (64 rows, from tile t0 to t1) of a walk that meet the owned rows'
+// documents; a group takes every kGroups-th of them.
+struct Walk {
+  const DocRange* r;  // of the batch entry; nullptr: no documents
+  DocRange own;
+  int t, t1;
+  __device__ __forceinline__ void skip() {
+    while (t < t1 && r != nullptr && !docs_meet(r[t], own)) ++t;
+  }
+  __device__ __forceinline__ void step(int n) {
+    for (int i = 0; i < n && t < t1; ++i) {
+      ++t;
+      skip();
+    }
+  }
+};
 
 template <int D>
-__global__ void __launch_bounds__(kThr) score_fwd_f32_kernel(const __grid_constant__ ScoreArgs a) {
+__global__ void __launch_bounds__(Cfg<D>::kThreads, 1) score_fwd_f32_kernel(const __grid_constant__ ScoreArgs a) {
+  using C = Cfg<D>;
   extern __shared__ __align__(16) float sm[];
+  const int g = threadIdx.x / kGrp, tid = threadIdx.x % kGrp;
   float* Q = sm;
-  float* K = Q + kR * (D + 4);
-  float* V = K + kC * (D + 4);
-  float* Pt = V + kC * (D + 4);
-  const int ti = threadIdx.x / 16, tj = threadIdx.x % 16;
+  float* K = sm + C::kOwn + g * (2 * C::kTile + C::kP);
+  float* V = K + C::kTile;
+  float* Pt = V + C::kTile;
+  const int ti = tid / 16, tj = tid % 16;
   const int h = blockIdx.y, b = blockIdx.z, hk = h / a.G;
   const int row0 = (gridDim.x - 1 - blockIdx.x) * kR;  // longest causal rows first
   const int nrows = min(kR, a.Sq - row0);
   const int64_t qs = static_cast<int64_t>(a.H) * D, ks = static_cast<int64_t>(a.Hkv) * D;
   const int64_t qo = (static_cast<int64_t>(b) * a.Sq + row0) * qs + static_cast<int64_t>(h) * D;
   const int64_t ko = static_cast<int64_t>(b) * a.Skv * ks + static_cast<int64_t>(hk) * D;
-  load_rows<D>(Q, static_cast<const float*>(a.q) + qo, qs, nrows, kR);
-  const Scorer score(a, h);
   const int plim = prefix_limit(a, b);
+  const int last = min(a.Skv, key_limit(a, plim, row0 + nrows - 1));
+  Walk cur{};
+  cur.t1 = (max(last, 0) + kC - 1) / kC;
+  if (a.qdoc) {
+    cur.r = a.krange + static_cast<int64_t>(b) * ((a.Skv + kDocBlock - 1) / kDocBlock);
+    cur.own = doc_range(a.qrange, b, a.Sq, row0);
+  }
+  cur.skip();
+  cur.step(g);
+  auto copy = [&](float* dst, const void* src, int t) {
+    if (t < cur.t1)
+      copy_rows<D>(dst, static_cast<const float*>(src) + ko + t * kC * ks, ks, min(kC, a.Skv - t * kC), kC, tid, kGrp);
+    copy_commit();
+  };
+  copy_rows<D>(Q, static_cast<const float*>(a.q) + qo, qs, nrows, kR, threadIdx.x, C::kThreads);
+  copy(K, a.k, cur.t);  // with Q
+  copy(V, a.v, cur.t);
+  const Scorer score(a, h);
   int lim[4], qd[4];
   float m[4], l[4];
   float4 acc[4][D / 64];
+  clear<D>(acc);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int r = 4 * ti + i;
@@ -154,21 +240,18 @@ __global__ void __launch_bounds__(kThr) score_fwd_f32_kernel(const __grid_consta
     qd[i] = a.qdoc && r < nrows ? a.qdoc[static_cast<int64_t>(b) * a.Sq + row0 + r] : -1;
     m[i] = -INFINITY;
     l[i] = 0.f;
-#pragma unroll
-    for (int u = 0; u < D / 64; ++u) acc[i][u] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
-  const int last = min(a.Skv, key_limit(a, plim, row0 + nrows - 1));
-  DocRange qr{};
-  if (a.qdoc) qr = doc_range(a.qrange, b, a.Sq, row0);
-  for (int k0 = 0; k0 < last; k0 += kC) {
-    if (a.qdoc && !docs_meet(qr, doc_range(a.krange, b, a.Skv, k0))) continue;
-    const int nk = min(kC, a.Skv - k0);
-    __syncthreads();  // the last tile's readers are done
-    load_rows<D>(K, static_cast<const float*>(a.k) + ko + k0 * ks, ks, nk, kC);
-    load_rows<D>(V, static_cast<const float*>(a.v) + ko + k0 * ks, ks, nk, kC);
-    __syncthreads();
+  copy_wait<1>();
+  __syncthreads();  // Q is every thread's
+  while (cur.t < cur.t1) {
+    const int k0 = cur.t * kC;
+    cur.step(C::kGroups);
+    copy_wait<1>();  // K
+    group_sync(g);
     float s[4][4];
     dots<D>(s, Q, K, ti, tj);
+    group_sync(g);
+    copy(K, a.k, cur.t);
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       const int j = k0 + tj + 16 * c;
@@ -196,33 +279,56 @@ __global__ void __launch_bounds__(kThr) score_fwd_f32_kernel(const __grid_consta
       }
       l[i] = l[i] * f + sum;
 #pragma unroll
-      for (int u = 0; u < D / 64; ++u) {
-        acc[i][u].x *= f;
-        acc[i][u].y *= f;
-        acc[i][u].z *= f;
-        acc[i][u].w *= f;
-      }
+      for (int u = 0; u < D / 64; ++u) acc[i][u] = scaled(acc[i][u], f);
     }
 #pragma unroll
     for (int c = 0; c < 4; ++c)
       *reinterpret_cast<float4*>(Pt + (tj + 16 * c) * kPT + 4 * ti) = make_float4(s[0][c], s[1][c], s[2][c], s[3][c]);
-    __syncthreads();
+    copy_wait<1>();  // V
+    group_sync(g);
     second<D>(acc, Pt, V, ti, tj);
+    group_sync(g);
+    copy(V, a.v, cur.t);
   }
+  copy_wait<0>();
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], o);
-    const int r = 4 * ti + i;
-    if (r >= nrows) continue;
-    const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;
+  // ---- the groups' states joined; group g stores the rows 4 ti + g (D = 64), or two of four ----
+  group_sync(g);
+  put<D>(acc, K, ti, tj);
+  if (tj == 0)
 #pragma unroll
-    for (int u = 0; u < D / 64; ++u)
-      store4(a.out, qo + r * qs + 4 * tj + 64 * u,
-             make_float4(acc[i][u].x * inv, acc[i][u].y * inv, acc[i][u].z * inv, acc[i][u].w * inv));
+    for (int i = 0; i < 4; ++i) {
+      K[C::kOwn + 2 * (4 * ti + i)] = m[i];
+      K[C::kOwn + 2 * (4 * ti + i) + 1] = l[i];
+    }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 4 / C::kGroups; ++i) {
+    const int r = 4 * ti + g * (4 / C::kGroups) + i;
+    if (r >= nrows) continue;
+    float mx = -INFINITY, sum = 0.f;
+    float4 o[D / 64];
+#pragma unroll
+    for (int u = 0; u < D / 64; ++u) o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int x = 0; x < C::kGroups; ++x) mx = fmaxf(mx, sm[C::kOwn + x * (2 * C::kTile + C::kP) + C::kOwn + 2 * r]);
+    const float base = mx == -INFINITY ? 0.f : mx;
+#pragma unroll
+    for (int x = 0; x < C::kGroups; ++x) {
+      const float* st = sm + C::kOwn + x * (2 * C::kTile + C::kP);
+      const float f = exp2f(st[C::kOwn + 2 * r] - base);
+      sum = fmaf(st[C::kOwn + 2 * r + 1], f, sum);
+#pragma unroll
+      for (int u = 0; u < D / 64; ++u) add4(o[u], scaled(load4(st + r * (D + 4) + 4 * tj + 64 * u), f));
+    }
+    const float inv = sum != 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+    for (int u = 0; u < D / 64; ++u) store4(a.out, qo + r * qs + 4 * tj + 64 * u, scaled(o[u], inv));
     if (tj == 0)
-      a.lse[(static_cast<int64_t>(b) * a.H + h) * a.Sq + row0 + r] =
-          l[i] > 0.f ? (m[i] + log2f(l[i])) * kLn2 : -INFINITY;
+      a.lse[(static_cast<int64_t>(b) * a.H + h) * a.Sq + row0 + r] = sum != 0.f ? (mx + log2f(sum)) * kLn2f : -INFINITY;
   }
 }
 
@@ -235,9 +341,9 @@ __global__ void __launch_bounds__(256) score_delta_kernel(const __grid_constant_
   const int64_t h = row % a.H, bs = row / a.H, s = bs % a.Sq, b = bs / a.Sq;
   float sum = 0.f;
   if (lane * 4 < D) {
-    const float4 g = load4(static_cast<const float*>(a.dout) + row * D + lane * 4);
+    const float4 x = load4(static_cast<const float*>(a.dout) + row * D + lane * 4);
     const float4 o = load4(static_cast<const float*>(a.o) + row * D + lane * 4);
-    sum = fmaf(g.x, o.x, fmaf(g.y, o.y, fmaf(g.z, o.z, g.w * o.w)));
+    sum = fmaf(x.x, o.x, fmaf(x.y, o.y, fmaf(x.z, o.z, x.w * o.w)));
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -252,33 +358,47 @@ __device__ __forceinline__ float lse2_of(const ScoreArgs& a, int64_t o, bool val
   return x == -INFINITY ? INFINITY : x * kL2e;
 }
 
+// dq of 32 query rows: key tiles stream by.
 template <int D>
-constexpr int bwd_floats() {
-  return (2 * kR + 2 * kC) * (D + 4) + kC * kPT + 2 * kC;
-}
-
-template <int D>
-__global__ void __launch_bounds__(kThr) score_dq_f32_kernel(const __grid_constant__ ScoreArgs a) {
-  extern __shared__ __align__(16) float sm[];
+__device__ __forceinline__ void dq_cta(const ScoreArgs& a, float* sm, int bx, int h, int b) {
+  using C = Cfg<D>;
+  constexpr int kStep = 2 * C::kTile + C::kP + 2 * kC;
+  const int g = threadIdx.x / kGrp, tid = threadIdx.x % kGrp;
   float* Q = sm;
-  float* dO = Q + kR * (D + 4);
-  float* K = dO + kR * (D + 4);
-  float* V = K + kC * (D + 4);
-  float* Pt = V + kC * (D + 4);
-  const int ti = threadIdx.x / 16, tj = threadIdx.x % 16;
-  const int h = blockIdx.y, b = blockIdx.z, hk = h / a.G;
-  const int row0 = (gridDim.x - 1 - blockIdx.x) * kR;
+  float* dO = Q + C::kOwn;
+  float* K = dO + C::kOwn + g * kStep;
+  float* V = K + C::kTile;
+  float* Pt = V + C::kTile;
+  const int ti = tid / 16, tj = tid % 16, hk = h / a.G;
+  const int row0 = bx * kR;
   const int nrows = min(kR, a.Sq - row0);
   const int64_t qs = static_cast<int64_t>(a.H) * D, ks = static_cast<int64_t>(a.Hkv) * D;
   const int64_t qo = (static_cast<int64_t>(b) * a.Sq + row0) * qs + static_cast<int64_t>(h) * D;
   const int64_t ko = static_cast<int64_t>(b) * a.Skv * ks + static_cast<int64_t>(hk) * D;
-  load_rows<D>(Q, static_cast<const float*>(a.q) + qo, qs, nrows, kR);
-  load_rows<D>(dO, static_cast<const float*>(a.dout) + qo, qs, nrows, kR);
-  const Scorer score(a, h);
   const int plim = prefix_limit(a, b);
+  const int last = min(a.Skv, key_limit(a, plim, row0 + nrows - 1));
+  Walk cur{};
+  cur.t1 = (max(last, 0) + kC - 1) / kC;
+  if (a.qdoc) {
+    cur.r = a.krange + static_cast<int64_t>(b) * ((a.Skv + kDocBlock - 1) / kDocBlock);
+    cur.own = doc_range(a.qrange, b, a.Sq, row0);
+  }
+  cur.skip();
+  cur.step(g);
+  auto copy = [&](float* dst, const void* src, int t) {
+    if (t < cur.t1)
+      copy_rows<D>(dst, static_cast<const float*>(src) + ko + t * kC * ks, ks, min(kC, a.Skv - t * kC), kC, tid, kGrp);
+    copy_commit();
+  };
+  copy_rows<D>(Q, static_cast<const float*>(a.q) + qo, qs, nrows, kR, threadIdx.x, C::kThreads);
+  copy_rows<D>(dO, static_cast<const float*>(a.dout) + qo, qs, nrows, kR, threadIdx.x, C::kThreads);
+  copy(V, a.v, cur.t);
+  copy(K, a.k, cur.t);
+  const Scorer score(a, h);
   int lim[4], qd[4];
   float lse2[4], dlt[4];
   float4 acc[4][D / 64];
+  clear<D>(acc);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int r = 4 * ti + i;
@@ -287,22 +407,17 @@ __global__ void __launch_bounds__(kThr) score_dq_f32_kernel(const __grid_constan
     qd[i] = a.qdoc && r < nrows ? a.qdoc[static_cast<int64_t>(b) * a.Sq + row0 + r] : -1;
     lse2[i] = lse2_of(a, o, r < nrows);
     dlt[i] = r < nrows ? a.delta[o] : 0.f;
-#pragma unroll
-    for (int u = 0; u < D / 64; ++u) acc[i][u] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
-  const int last = min(a.Skv, key_limit(a, plim, row0 + nrows - 1));
-  DocRange qr{};
-  if (a.qdoc) qr = doc_range(a.qrange, b, a.Sq, row0);
-  for (int k0 = 0; k0 < last; k0 += kC) {
-    if (a.qdoc && !docs_meet(qr, doc_range(a.krange, b, a.Skv, k0))) continue;
-    const int nk = min(kC, a.Skv - k0);
-    __syncthreads();
-    load_rows<D>(K, static_cast<const float*>(a.k) + ko + k0 * ks, ks, nk, kC);
-    load_rows<D>(V, static_cast<const float*>(a.v) + ko + k0 * ks, ks, nk, kC);
-    __syncthreads();
+  copy_wait<0>();
+  __syncthreads();
+  while (cur.t < cur.t1) {
+    const int k0 = cur.t * kC;
+    cur.step(C::kGroups);
+    copy_wait<0>();
+    group_sync(g);
     float s[4][4], dp[4][4];
-    dots<D>(s, Q, K, ti, tj);
     dots<D>(dp, dO, V, ti, tj);
+    dots<D>(s, Q, K, ti, tj);
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       const int j = k0 + tj + 16 * c;
@@ -317,17 +432,27 @@ __global__ void __launch_bounds__(kThr) score_dq_f32_kernel(const __grid_constan
       }
       *reinterpret_cast<float4*>(Pt + (tj + 16 * c) * kPT + 4 * ti) = make_float4(ds[0], ds[1], ds[2], ds[3]);
     }
-    __syncthreads();
+    group_sync(g);
+    copy(V, a.v, cur.t);
     second<D>(acc, Pt, K, ti, tj);
+    group_sync(g);
+    copy(K, a.k, cur.t);
   }
+  copy_wait<0>();
+  group_sync(g);
+  put<D>(acc, K, ti, tj);
+  __syncthreads();
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = 4 * ti + i;
+  for (int i = 0; i < 4 / C::kGroups; ++i) {
+    const int r = 4 * ti + g * (4 / C::kGroups) + i;
     if (r >= nrows) continue;
 #pragma unroll
-    for (int u = 0; u < D / 64; ++u)
-      store4(a.dq, qo + r * qs + 4 * tj + 64 * u,
-             make_float4(acc[i][u].x * a.scale, acc[i][u].y * a.scale, acc[i][u].z * a.scale, acc[i][u].w * a.scale));
+    for (int u = 0; u < D / 64; ++u) {
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int y = 0; y < C::kGroups; ++y) add4(x, load4(sm + 2 * C::kOwn + y * kStep + r * (D + 4) + 4 * tj + 64 * u));
+      store4(a.dq, qo + r * qs + 4 * tj + 64 * u, scaled(x, a.scale));
+    }
   }
 }
 
@@ -335,95 +460,157 @@ __global__ void __launch_bounds__(kThr) score_dq_f32_kernel(const __grid_constan
 // shares the key/value head, head by head. Scores are formed transposed (rows
 // are keys), and P^T and then dS^T pass through one buffer.
 template <int D>
-__global__ void __launch_bounds__(kThr) score_dkdv_f32_kernel(const __grid_constant__ ScoreArgs a) {
-  extern __shared__ __align__(16) float sm[];
+__device__ __forceinline__ void dkdv_cta(const ScoreArgs& a, float* sm, int bx, int hk, int b) {
+  using C = Cfg<D>;
+  constexpr int kStep = 2 * C::kTile + C::kP + 2 * kC;
+  const int g = threadIdx.x / kGrp, tid = threadIdx.x % kGrp;
   float* K = sm;
-  float* V = K + kR * (D + 4);
-  float* Q = V + kR * (D + 4);
-  float* dO = Q + kC * (D + 4);
-  float* Pt = dO + kC * (D + 4);
-  float* lse2 = Pt + kC * kPT;
+  float* V = K + C::kOwn;
+  float* Q = V + C::kOwn + g * kStep;
+  float* dO = Q + C::kTile;
+  float* Pt = dO + C::kTile;
+  float* lse2 = Pt + C::kP;
   float* dlt = lse2 + kC;
-  const int ti = threadIdx.x / 16, tj = threadIdx.x % 16;
-  const int hk = blockIdx.y, b = blockIdx.z;
-  const int key0 = blockIdx.x * kR;  // the first keys meet the most causal rows
+  const int ti = tid / 16, tj = tid % 16;
+  const int key0 = bx * kR;
   const int nk = min(kR, a.Skv - key0);
   const int64_t qs = static_cast<int64_t>(a.H) * D, ks = static_cast<int64_t>(a.Hkv) * D;
   const int64_t ko = (static_cast<int64_t>(b) * a.Skv + key0) * ks + static_cast<int64_t>(hk) * D;
-  load_rows<D>(K, static_cast<const float*>(a.k) + ko, ks, nk, kR);
-  load_rows<D>(V, static_cast<const float*>(a.v) + ko, ks, nk, kR);
+  copy_rows<D>(K, static_cast<const float*>(a.k) + ko, ks, nk, kR, threadIdx.x, C::kThreads);
+  copy_rows<D>(V, static_cast<const float*>(a.v) + ko, ks, nk, kR, threadIdx.x, C::kThreads);
+  copy_commit();
   const int plim = prefix_limit(a, b);
   int kd[4];
   float4 dk[4][D / 64], dv[4][D / 64];
+  clear<D>(dk);
+  clear<D>(dv);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int r = 4 * ti + i;
     kd[i] = a.qdoc && r < nk ? a.kdoc[static_cast<int64_t>(b) * a.Skv + key0 + r] : -1;
-#pragma unroll
-    for (int u = 0; u < D / 64; ++u) dk[i][u] = dv[i][u] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
-  // the first query row that reaches any key of the tile, down to a tile start
-  int first = 0;
-  if (a.causal && key0 >= plim) first = max(0, key0 - a.rel) / kC * kC;
-  DocRange kr{};
-  if (a.qdoc) kr = doc_range(a.krange, b, a.Skv, key0);
-  for (int h = hk * a.G; h < (hk + 1) * a.G; ++h) {
-    const Scorer score(a, h);
-    for (int q0 = first; q0 < a.Sq; q0 += kC) {
-      if (a.qdoc && !docs_meet(doc_range(a.qrange, b, a.Sq, q0), kr)) continue;
-      const int nq = min(kC, a.Sq - q0);
-      const int64_t qo = (static_cast<int64_t>(b) * a.Sq + q0) * qs + static_cast<int64_t>(h) * D;
-      const int64_t lo = (static_cast<int64_t>(b) * a.H + h) * a.Sq + q0;
-      __syncthreads();
-      load_rows<D>(Q, static_cast<const float*>(a.q) + qo, qs, nq, kC);
-      load_rows<D>(dO, static_cast<const float*>(a.dout) + qo, qs, nq, kC);
-      if (threadIdx.x < kC) {
-        const int r = threadIdx.x;
-        lse2[r] = lse2_of(a, lo + r, r < nq);
-        dlt[r] = r < nq ? a.delta[lo + r] : 0.f;
+  // query tiles from the first row that reaches a key of the tile
+  const int ntq = (a.Sq + kC - 1) / kC;
+  const int t0 = a.causal && key0 >= plim ? min(ntq, max(0, key0 - a.rel) / kC) : 0;
+  Walk first{};
+  first.t = t0;
+  first.t1 = ntq;
+  if (a.qdoc) {
+    first.r = a.qrange + static_cast<int64_t>(b) * ((a.Sq + kDocBlock - 1) / kDocBlock);
+    first.own = doc_range(a.krange, b, a.Skv, key0);
+  }
+  first.skip();
+  // (tile, head) pairs in turn: the next one is `n` further
+  Walk cur = first;
+  int h = hk * a.G;
+  const int h1 = h + a.G;
+  auto step = [&](int n) {
+    while (n > 0 && h < h1) {
+      if (cur.t < cur.t1) {
+        cur.step(1);
+        --n;
       }
-      __syncthreads();
-      float s[4][4], dp[4][4];
-      dots<D>(s, K, Q, ti, tj);
-      dots<D>(dp, V, dO, ti, tj);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int r = tj + 16 * c, i = q0 + r;
-        const int lim = key_limit(a, plim, i);
-        const int qd = a.qdoc && r < nq ? a.qdoc[static_cast<int64_t>(b) * a.Sq + i] : -1;
-        float p[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int j = key0 + 4 * ti + e;
-          float dcap;
-          const bool on = r < nq && j < lim && (!a.qdoc || (qd == kd[e] && qd >= 0));
-          const float x = exp2f(score(s[e][c], a.rel + i - j, dcap) - lse2[r]);
-          p[e] = on ? x : 0.f;
-          dp[e][c] = on ? x * (dp[e][c] - dlt[r]) * dcap : 0.f;
-        }
-        *reinterpret_cast<float4*>(Pt + r * kPT + 4 * ti) = make_float4(p[0], p[1], p[2], p[3]);
+      if (cur.t >= cur.t1) {
+        cur = first;
+        ++h;
+        if (first.t >= first.t1) h = h1;
       }
-      __syncthreads();
-      second<D>(dv, Pt, dO, ti, tj);
-      __syncthreads();
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-        *reinterpret_cast<float4*>(Pt + (tj + 16 * c) * kPT + 4 * ti) =
-            make_float4(dp[0][c], dp[1][c], dp[2][c], dp[3][c]);
-      __syncthreads();
-      second<D>(dk, Pt, Q, ti, tj);
     }
-  }
+  };
+  if (first.t >= first.t1) h = h1;
+  step(g);
+  auto copy = [&](float* dst, const void* src) {
+    if (h < h1) {
+      const int64_t qo = (static_cast<int64_t>(b) * a.Sq + cur.t * kC) * qs + static_cast<int64_t>(h) * D;
+      copy_rows<D>(dst, static_cast<const float*>(src) + qo, qs, min(kC, a.Sq - cur.t * kC), kC, tid, kGrp);
+    }
+    copy_commit();
+  };
+  copy(dO, a.dout);
+  copy(Q, a.q);
+  copy_wait<0>();
+  __syncthreads();
+  while (h < h1) {
+    const Scorer score(a, h);
+    const int q0 = cur.t * kC, nq = min(kC, a.Sq - q0);
+    const int64_t lo = (static_cast<int64_t>(b) * a.H + h) * a.Sq + q0;
+    if (tid < kC) {
+      lse2[tid] = lse2_of(a, lo + tid, tid < nq);
+      dlt[tid] = tid < nq ? a.delta[lo + tid] : 0.f;
+    }
+    step(C::kGroups);
+    copy_wait<0>();
+    group_sync(g);
+    float s[4][4], dp[4][4];
+    dots<D>(s, K, Q, ti, tj);
+    dots<D>(dp, V, dO, ti, tj);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = 4 * ti + i;
+    for (int c = 0; c < 4; ++c) {
+      const int r = tj + 16 * c, i = q0 + r;
+      const int lim = key_limit(a, plim, i);
+      const int qd = a.qdoc && r < nq ? a.qdoc[static_cast<int64_t>(b) * a.Sq + i] : -1;
+      float p[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int j = key0 + 4 * ti + e;
+        float dcap;
+        const bool on = r < nq && j < lim && (!a.qdoc || (qd == kd[e] && qd >= 0));
+        const float x = exp2f(score(s[e][c], a.rel + i - j, dcap) - lse2[r]);
+        p[e] = on ? x : 0.f;
+        dp[e][c] = on ? x * (dp[e][c] - dlt[r]) * dcap : 0.f;
+      }
+      *reinterpret_cast<float4*>(Pt + r * kPT + 4 * ti) = make_float4(p[0], p[1], p[2], p[3]);
+    }
+    group_sync(g);
+    second<D>(dv, Pt, dO, ti, tj);
+    group_sync(g);
+    copy(dO, a.dout);
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      *reinterpret_cast<float4*>(Pt + (tj + 16 * c) * kPT + 4 * ti) =
+          make_float4(dp[0][c], dp[1][c], dp[2][c], dp[3][c]);
+    group_sync(g);
+    second<D>(dk, Pt, Q, ti, tj);
+    group_sync(g);
+    copy(Q, a.q);
+  }
+  copy_wait<0>();
+  group_sync(g);
+  put<D>(dk, Q, ti, tj);
+  put<D>(dv, Q + C::kOwn, ti, tj);
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 4 / C::kGroups; ++i) {
+    const int r = 4 * ti + g * (4 / C::kGroups) + i;
     if (r >= nk) continue;
 #pragma unroll
     for (int u = 0; u < D / 64; ++u) {
-      store4(a.dk, ko + r * ks + 4 * tj + 64 * u,
-             make_float4(dk[i][u].x * a.scale, dk[i][u].y * a.scale, dk[i][u].z * a.scale, dk[i][u].w * a.scale));
-      store4(a.dv, ko + r * ks + 4 * tj + 64 * u, dv[i][u]);
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+#pragma unroll
+      for (int z = 0; z < C::kGroups; ++z) {
+        const float* st = sm + 2 * C::kOwn + z * kStep + r * (D + 4) + 4 * tj + 64 * u;
+        add4(x, load4(st));
+        add4(y, load4(st + C::kOwn));
+      }
+      store4(a.dk, ko + r * ks + 4 * tj + 64 * u, scaled(x, a.scale));
+      store4(a.dv, ko + r * ks + 4 * tj + 64 * u, y);
     }
+  }
+}
+
+// Both kinds of CTA in one launch: dk/dv CTAs (the first keys, which the most
+// causal rows reach, first), then dq CTAs (the last rows first).
+template <int D>
+__global__ void __launch_bounds__(Cfg<D>::kThreads, 1) score_bwd_f32_kernel(const __grid_constant__ ScoreArgs a) {
+  extern __shared__ __align__(16) float sm[];
+  const int kv_ctas = (a.Skv + kR - 1) / kR * a.Hkv * a.B, nq = (a.Sq + kR - 1) / kR;
+  const int id = static_cast<int>(blockIdx.x);
+  if (id < kv_ctas) {
+    const int bh = id % (a.Hkv * a.B);
+    dkdv_cta<D>(a, sm, id / (a.Hkv * a.B), bh % a.Hkv, bh / a.Hkv);
+  } else {
+    const int i = id - kv_ctas, bh = i % (a.H * a.B);
+    dq_cta<D>(a, sm, nq - 1 - i / (a.H * a.B), bh % a.H, bh / a.H);
   }
 }
 
@@ -463,31 +650,30 @@ __global__ void __launch_bounds__(256) doc_ranges_kernel(const __grid_constant__
 
 template <int D>
 cudaError_t fwd_d(const ScoreArgs& a, cudaStream_t s) {
-  constexpr int bytes = fwd_floats<D>() * 4;
+  constexpr int bytes = Cfg<D>::kFwd * 4;
+  static_assert(bytes <= 227 * 1024, "shared memory budget");
   cudaError_t e = allow_smem<score_fwd_f32_kernel<D>>(bytes);
   if (e != cudaSuccess) return e;
-  score_fwd_f32_kernel<D><<<dim3((a.Sq + kR - 1) / kR, a.H, a.B), kThr, bytes, s>>>(a);
+  score_fwd_f32_kernel<D><<<dim3((a.Sq + kR - 1) / kR, a.H, a.B), Cfg<D>::kThreads, bytes, s>>>(a);
   return cudaGetLastError();
 }
 
 template <int D>
 cudaError_t bwd_d(const ScoreArgs& a, cudaStream_t s) {
-  constexpr int bytes = bwd_floats<D>() * 4;
-  cudaError_t e = allow_smem<score_dq_f32_kernel<D>>(bytes);
-  if (e == cudaSuccess) e = allow_smem<score_dkdv_f32_kernel<D>>(bytes);
+  constexpr int bytes = Cfg<D>::kBwd * 4;
+  static_assert(bytes <= 227 * 1024, "shared memory budget");
+  cudaError_t e = allow_smem<score_bwd_f32_kernel<D>>(bytes);
   if (e != cudaSuccess) return e;
   if (a.Sq > 0) {
     const int64_t rows = static_cast<int64_t>(a.B) * a.Sq * a.H;
+    if ((rows + 7) / 8 > 0x7fffffff) return cudaErrorInvalidValue;
     score_delta_kernel<D><<<static_cast<unsigned>((rows + 7) / 8), 256, 0, s>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    score_dq_f32_kernel<D><<<dim3((a.Sq + kR - 1) / kR, a.H, a.B), kThr, bytes, s>>>(a);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
-  if (a.Skv > 0) {
-    score_dkdv_f32_kernel<D><<<dim3((a.Skv + kR - 1) / kR, a.Hkv, a.B), kThr, bytes, s>>>(a);
-    e = cudaGetLastError();
-  }
-  return e;
+  const int64_t ctas = (static_cast<int64_t>((a.Skv + kR - 1) / kR) * a.Hkv + static_cast<int64_t>((a.Sq + kR - 1) / kR) * a.H) * a.B;
+  if (ctas > 0x7fffffff) return cudaErrorInvalidValue;
+  score_bwd_f32_kernel<D><<<static_cast<unsigned>(ctas), Cfg<D>::kThreads, bytes, s>>>(a);
+  return cudaGetLastError();
 }
 
 }  // namespace

@@ -446,13 +446,10 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap& tq64, const CUtensor
       const int d0 = a.rel + i0 - jkey;       // its position less the key's
       uint32_t on = !kvalid ? 0u : open || d0 >= 0 ? ~0u : d0 <= -32 ? 0u : ~0u << -d0;
       if (bits != nullptr && ((act[kMapWords + (cur.t >> 5)] >> (cur.t & 31)) & 1u)) {
-        uint32_t same = 0;
-#pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          const int id = i0 + c < a.Sq ? __ldg(qdoc + i0 + c) : -1;  // the same word for the whole warp
-          same |= (id == kd ? 1u : 0u) << c;
-        }
-        on &= kd >= 0 ? same : 0u;
+        const int ids[1] = {i0 + lane < a.Sq ? __ldg(qdoc + i0 + lane) : -1};
+        uint32_t same[1];
+        same_docs<1>(kd, ids, same);
+        on &= same[0];
       }
       ok = __all_sync(0xffffffffu,
                       mbar_wait_bounded(bar(kBarQFull + q), (j >> 2) & 1, abort_flag, a.err, tmo) &&
@@ -776,13 +773,10 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap& tk64, const CUtensorMa
       const int n = lim - j0;
       uint32_t on = n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u;
       if (bits != nullptr && ((act[kMapWords + (cur.t >> 5)] >> (cur.t & 31)) & 1u)) {
-        uint32_t same = 0;
-#pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          const int id = j0 + c < a.Skv ? __ldg(kdoc + j0 + c) : -1;  // the same word for the whole warp
-          same |= (id == qd ? 1u : 0u) << c;
-        }
-        on &= qd >= 0 ? same : 0u;
+        const int ids[1] = {j0 + lane < a.Skv ? __ldg(kdoc + j0 + lane) : -1};
+        uint32_t same[1];
+        same_docs<1>(qd, ids, same);
+        on &= same[0];
       }
       ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar(kDqBarSFull + ts), (j >> 1) & 1, abort_flag, a.err, tmo));
       if (!ok) break;

@@ -365,17 +365,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (mix) {
-          const int nk = a.Skv - kv0;
+          int ids[4];
+          uint32_t same[4];
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
-            uint32_t same = 0;
-#pragma unroll
-            for (int c = 0; c < 32; ++c) {
-              const int id = 32 * w + c < nk ? __ldg(kd + kv0 + 32 * w + c) : -1;  // the same word for the whole warp
-              same |= (id == qd ? 1u : 0u) << c;
-            }
-            on[w] &= qd >= 0 ? same : 0u;
+            const int j = kv0 + 32 * w + lane;
+            ids[w] = j < a.Skv ? __ldg(kd + j) : -1;
           }
+          same_docs<4>(qd, ids, same);
+#pragma unroll
+          for (int w = 0; w < 4; ++w) on[w] &= same[w];
         }
         ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar(kBarSFull + i), it & 1, abort_flag, a.err, tmo));
         if (!ok) break;

@@ -133,6 +133,25 @@ __device__ __forceinline__ DocRange doc_span(const DocRange* row, int nblk, int 
   return r;
 }
 
+// Which of kWords x 32 document ids (lane c of word w holds id 32 w + c) are the
+// lane's own: a bit each; none for a negative one. One pass for each document
+// among the warp's own ids, which are rarely more than two.
+template <int kWords>
+__device__ __forceinline__ void same_docs(int own, const int (&ids)[kWords], uint32_t (&same)[kWords]) {
+#pragma unroll
+  for (int w = 0; w < kWords; ++w) same[w] = 0u;
+  uint32_t todo = __ballot_sync(0xffffffffu, own >= 0);
+  while (todo) {
+    const int d = __shfl_sync(0xffffffffu, own, __ffs(todo) - 1);
+#pragma unroll
+    for (int w = 0; w < kWords; ++w) {
+      const uint32_t b = __ballot_sync(0xffffffffu, ids[w] == d);
+      if (own == d) same[w] = b;
+    }
+    todo &= ~__ballot_sync(0xffffffffu, own == d);
+  }
+}
+
 // The tiles of [lo, hi) that a CTA walks: all, or those whose bit is set in act
 // (a bitmap in shared memory). First from `start` down to lo, then from
 // start + 1 up; start < lo walks upwards only.
