@@ -119,6 +119,25 @@ cudaError_t allow_smem(int bytes) {
   return e;
 }
 
+// Launches `items` clusters of `cluster` CTAs each.
+template <typename... P, typename... A>
+cudaError_t launch_clusters(void (*kernel)(P...), int64_t items, int cluster, int threads, int smem, cudaStream_t s,
+                            const A&... args) {
+  if (items * cluster > 0x7fffffff) return cudaErrorInvalidValue;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(items * cluster));
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = cluster;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = cluster > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
 // From cp_api.cu: the checks and tensor maps that the host drivers share.
 // 0, or the cp_status of the current device's check.
 int host_device(uint32_t** err, int* sms);

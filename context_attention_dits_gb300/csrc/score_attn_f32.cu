@@ -23,9 +23,12 @@
 // memory holds tiles for: 4 at D = 64, 2 at D = 128) that take the tiles in
 // turn, each with its own buffers, barrier and running state, joined once at
 // the end; and a buffer's next tile is copied (16-byte asynchronous copies) as
-// soon as its last reader is through.
+// soon as its last reader is through. Where that still leaves multiprocessors
+// idle, a cluster of 2, 4 or 8 CTAs shares the tiles of one item in the same way
+// and joins through distributed shared memory (see cluster_for).
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -204,8 +207,10 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) score_fwd_f32_kernel(cons
   float* V = K + C::kTile;
   float* Pt = V + C::kTile;
   const int ti = tid / 16, tj = tid % 16;
-  const int h = blockIdx.y, b = blockIdx.z, hk = h / a.G;
-  const int row0 = (gridDim.x - 1 - blockIdx.x) * kR;  // longest causal rows first
+  const int cs = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
+  const int item = blockIdx.x / cs, nrt = (a.Sq + kR - 1) / kR;
+  const int h = item % a.H, b = item / a.H % a.B, hk = h / a.G;
+  const int row0 = (nrt - 1 - item / (a.H * a.B)) * kR;  // longest causal rows first
   const int nrows = min(kR, a.Sq - row0);
   const int64_t qs = static_cast<int64_t>(a.H) * D, ks = static_cast<int64_t>(a.Hkv) * D;
   const int64_t qo = (static_cast<int64_t>(b) * a.Sq + row0) * qs + static_cast<int64_t>(h) * D;
@@ -219,7 +224,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) score_fwd_f32_kernel(cons
     cur.own = doc_range(a.qrange, b, a.Sq, row0);
   }
   cur.skip();
-  cur.step(g);
+  cur.step(rank * C::kGroups + g);
   auto copy = [&](float* dst, const void* src, int t) {
     if (t < cur.t1)
       copy_rows<D>(dst, static_cast<const float*>(src) + ko + t * kC * ks, ks, min(kC, a.Skv - t * kC), kC, tid, kGrp);
@@ -245,7 +250,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) score_fwd_f32_kernel(cons
   __syncthreads();  // Q is every thread's
   while (cur.t < cur.t1) {
     const int k0 = cur.t * kC;
-    cur.step(C::kGroups);
+    cur.step(cs * C::kGroups);
     copy_wait<1>();  // K
     group_sync(g);
     float s[4][4];
@@ -295,41 +300,41 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) score_fwd_f32_kernel(cons
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], o);
-  // ---- the groups' states joined; group g stores the rows 4 ti + g (D = 64), or two of four ----
+  // ---- the states of every CTA's groups joined: a CTA stores the rows of its share ----
   group_sync(g);
   put<D>(acc, K, ti, tj);
   if (tj == 0)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      K[C::kOwn + 2 * (4 * ti + i)] = m[i];
-      K[C::kOwn + 2 * (4 * ti + i) + 1] = l[i];
-    }
-  __syncthreads();
+    for (int i = 0; i < 4; ++i) *reinterpret_cast<float2*>(K + C::kOwn + 2 * (4 * ti + i)) = make_float2(m[i], l[i]);
+  cluster_sync();
+  const uint32_t st0 = smem_addr(sm + C::kOwn);
+  constexpr int kStep = (2 * C::kTile + C::kP) * 4;  // bytes from a group's buffers to the next's
+  const int share = kR / cs;
+  for (int e = threadIdx.x; e < share * (D / 4); e += C::kThreads) {
+    const int r = rank * share + e / (D / 4), d = (e % (D / 4)) * 4;
+    if (r >= nrows) break;
+    float mx = -INFINITY;
+    for (int x = 0; x < cs; ++x)
 #pragma unroll
-  for (int i = 0; i < 4 / C::kGroups; ++i) {
-    const int r = 4 * ti + g * (4 / C::kGroups) + i;
-    if (r >= nrows) continue;
-    float mx = -INFINITY, sum = 0.f;
-    float4 o[D / 64];
-#pragma unroll
-    for (int u = 0; u < D / 64; ++u) o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int x = 0; x < C::kGroups; ++x) mx = fmaxf(mx, sm[C::kOwn + x * (2 * C::kTile + C::kP) + C::kOwn + 2 * r]);
+      for (int y = 0; y < C::kGroups; ++y)
+        mx = fmaxf(mx, ld_peer2(cluster_peer(st0 + y * kStep + (C::kOwn + 2 * r) * 4, x)).x);
     const float base = mx == -INFINITY ? 0.f : mx;
+    float sum = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int x = 0; x < cs; ++x)
 #pragma unroll
-    for (int x = 0; x < C::kGroups; ++x) {
-      const float* st = sm + C::kOwn + x * (2 * C::kTile + C::kP);
-      const float f = exp2f(st[C::kOwn + 2 * r] - base);
-      sum = fmaf(st[C::kOwn + 2 * r + 1], f, sum);
-#pragma unroll
-      for (int u = 0; u < D / 64; ++u) add4(o[u], scaled(load4(st + r * (D + 4) + 4 * tj + 64 * u), f));
-    }
-    const float inv = sum != 0.f ? 1.f / sum : 0.f;
-#pragma unroll
-    for (int u = 0; u < D / 64; ++u) store4(a.out, qo + r * qs + 4 * tj + 64 * u, scaled(o[u], inv));
-    if (tj == 0)
+      for (int y = 0; y < C::kGroups; ++y) {
+        const uint32_t st = cluster_peer(st0 + y * kStep, x);
+        const float2 ml = ld_peer2(st + (C::kOwn + 2 * r) * 4);
+        const float f = exp2f(ml.x - base);
+        sum = fmaf(ml.y, f, sum);
+        add4(o, scaled(ld_peer4(st + (r * (D + 4) + d) * 4), f));
+      }
+    store4(a.out, qo + r * qs + d, scaled(o, sum != 0.f ? 1.f / sum : 0.f));
+    if (d == 0)
       a.lse[(static_cast<int64_t>(b) * a.H + h) * a.Sq + row0 + r] = sum != 0.f ? (mx + log2f(sum)) * kLn2f : -INFINITY;
   }
+  cluster_sync();  // no CTA leaves while another reads its shared memory
 }
 
 // delta[b, h, i] = out_i . dout_i, a warp per row of [B, Sq, H, D]
@@ -360,7 +365,7 @@ __device__ __forceinline__ float lse2_of(const ScoreArgs& a, int64_t o, bool val
 
 // dq of 32 query rows: key tiles stream by.
 template <int D>
-__device__ __forceinline__ void dq_cta(const ScoreArgs& a, float* sm, int bx, int h, int b) {
+__device__ __forceinline__ void dq_cta(const ScoreArgs& a, float* sm, int cs, int rank, int bx, int h, int b) {
   using C = Cfg<D>;
   constexpr int kStep = 2 * C::kTile + C::kP + 2 * kC;
   const int g = threadIdx.x / kGrp, tid = threadIdx.x % kGrp;
@@ -384,7 +389,7 @@ __device__ __forceinline__ void dq_cta(const ScoreArgs& a, float* sm, int bx, in
     cur.own = doc_range(a.qrange, b, a.Sq, row0);
   }
   cur.skip();
-  cur.step(g);
+  cur.step(rank * C::kGroups + g);
   auto copy = [&](float* dst, const void* src, int t) {
     if (t < cur.t1)
       copy_rows<D>(dst, static_cast<const float*>(src) + ko + t * kC * ks, ks, min(kC, a.Skv - t * kC), kC, tid, kGrp);
@@ -412,7 +417,7 @@ __device__ __forceinline__ void dq_cta(const ScoreArgs& a, float* sm, int bx, in
   __syncthreads();
   while (cur.t < cur.t1) {
     const int k0 = cur.t * kC;
-    cur.step(C::kGroups);
+    cur.step(cs * C::kGroups);
     copy_wait<0>();
     group_sync(g);
     float s[4][4], dp[4][4];
@@ -441,18 +446,17 @@ __device__ __forceinline__ void dq_cta(const ScoreArgs& a, float* sm, int bx, in
   copy_wait<0>();
   group_sync(g);
   put<D>(acc, K, ti, tj);
-  __syncthreads();
+  cluster_sync();
+  const uint32_t st0 = smem_addr(sm + 2 * C::kOwn);
+  const int share = kR / cs;
+  for (int e = threadIdx.x; e < share * (D / 4); e += C::kThreads) {
+    const int r = rank * share + e / (D / 4), d = (e % (D / 4)) * 4;
+    if (r >= nrows) break;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c = 0; c < cs; ++c)
 #pragma unroll
-  for (int i = 0; i < 4 / C::kGroups; ++i) {
-    const int r = 4 * ti + g * (4 / C::kGroups) + i;
-    if (r >= nrows) continue;
-#pragma unroll
-    for (int u = 0; u < D / 64; ++u) {
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int y = 0; y < C::kGroups; ++y) add4(x, load4(sm + 2 * C::kOwn + y * kStep + r * (D + 4) + 4 * tj + 64 * u));
-      store4(a.dq, qo + r * qs + 4 * tj + 64 * u, scaled(x, a.scale));
-    }
+      for (int y = 0; y < C::kGroups; ++y) add4(x, ld_peer4(cluster_peer(st0 + (y * kStep + r * (D + 4) + d) * 4, c)));
+    store4(a.dq, qo + r * qs + d, scaled(x, a.scale));
   }
 }
 
@@ -460,7 +464,7 @@ __device__ __forceinline__ void dq_cta(const ScoreArgs& a, float* sm, int bx, in
 // shares the key/value head, head by head. Scores are formed transposed (rows
 // are keys), and P^T and then dS^T pass through one buffer.
 template <int D>
-__device__ __forceinline__ void dkdv_cta(const ScoreArgs& a, float* sm, int bx, int hk, int b) {
+__device__ __forceinline__ void dkdv_cta(const ScoreArgs& a, float* sm, int cs, int rank, int bx, int hk, int b) {
   using C = Cfg<D>;
   constexpr int kStep = 2 * C::kTile + C::kP + 2 * kC;
   const int g = threadIdx.x / kGrp, tid = threadIdx.x % kGrp;
@@ -518,7 +522,7 @@ __device__ __forceinline__ void dkdv_cta(const ScoreArgs& a, float* sm, int bx, 
     }
   };
   if (first.t >= first.t1) h = h1;
-  step(g);
+  step(rank * C::kGroups + g);
   auto copy = [&](float* dst, const void* src) {
     if (h < h1) {
       const int64_t qo = (static_cast<int64_t>(b) * a.Sq + cur.t * kC) * qs + static_cast<int64_t>(h) * D;
@@ -538,7 +542,7 @@ __device__ __forceinline__ void dkdv_cta(const ScoreArgs& a, float* sm, int bx, 
       lse2[tid] = lse2_of(a, lo + tid, tid < nq);
       dlt[tid] = tid < nq ? a.delta[lo + tid] : 0.f;
     }
-    step(C::kGroups);
+    step(cs * C::kGroups);
     copy_wait<0>();
     group_sync(g);
     float s[4][4], dp[4][4];
@@ -578,23 +582,22 @@ __device__ __forceinline__ void dkdv_cta(const ScoreArgs& a, float* sm, int bx, 
   group_sync(g);
   put<D>(dk, Q, ti, tj);
   put<D>(dv, Q + C::kOwn, ti, tj);
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < 4 / C::kGroups; ++i) {
-    const int r = 4 * ti + g * (4 / C::kGroups) + i;
-    if (r >= nk) continue;
-#pragma unroll
-    for (int u = 0; u < D / 64; ++u) {
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+  cluster_sync();
+  const uint32_t st0 = smem_addr(sm + 2 * C::kOwn);
+  const int share = kR / cs;
+  for (int e = threadIdx.x; e < share * (D / 4); e += C::kThreads) {
+    const int r = rank * share + e / (D / 4), d = (e % (D / 4)) * 4;
+    if (r >= nk) break;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+    for (int c = 0; c < cs; ++c)
 #pragma unroll
       for (int z = 0; z < C::kGroups; ++z) {
-        const float* st = sm + 2 * C::kOwn + z * kStep + r * (D + 4) + 4 * tj + 64 * u;
-        add4(x, load4(st));
-        add4(y, load4(st + C::kOwn));
+        const uint32_t st = cluster_peer(st0 + (z * kStep + r * (D + 4) + d) * 4, c);
+        add4(x, ld_peer4(st));
+        add4(y, ld_peer4(st + C::kOwn * 4));
       }
-      store4(a.dk, ko + r * ks + 4 * tj + 64 * u, scaled(x, a.scale));
-      store4(a.dv, ko + r * ks + 4 * tj + 64 * u, y);
-    }
+    store4(a.dk, ko + r * ks + d, scaled(x, a.scale));
+    store4(a.dv, ko + r * ks + d, y);
   }
 }
 
@@ -603,15 +606,17 @@ __device__ __forceinline__ void dkdv_cta(const ScoreArgs& a, float* sm, int bx, 
 template <int D>
 __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) score_bwd_f32_kernel(const __grid_constant__ ScoreArgs a) {
   extern __shared__ __align__(16) float sm[];
-  const int kv_ctas = (a.Skv + kR - 1) / kR * a.Hkv * a.B, nq = (a.Sq + kR - 1) / kR;
-  const int id = static_cast<int>(blockIdx.x);
-  if (id < kv_ctas) {
+  const int cs = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
+  const int kv_items = (a.Skv + kR - 1) / kR * a.Hkv * a.B, nq = (a.Sq + kR - 1) / kR;
+  const int id = static_cast<int>(blockIdx.x) / cs;
+  if (id < kv_items) {
     const int bh = id % (a.Hkv * a.B);
-    dkdv_cta<D>(a, sm, id / (a.Hkv * a.B), bh % a.Hkv, bh / a.Hkv);
+    dkdv_cta<D>(a, sm, cs, rank, id / (a.Hkv * a.B), bh % a.Hkv, bh / a.Hkv);
   } else {
-    const int i = id - kv_ctas, bh = i % (a.H * a.B);
-    dq_cta<D>(a, sm, nq - 1 - i / (a.H * a.B), bh % a.H, bh / a.H);
+    const int i = id - kv_items, bh = i % (a.H * a.B);
+    dq_cta<D>(a, sm, cs, rank, nq - 1 - i / (a.H * a.B), bh % a.H, bh / a.H);
   }
+  cluster_sync();  // no CTA leaves while another reads its shared memory
 }
 
 // A warp per 64-row block of the document ids of q (the first nq blocks of a
@@ -648,14 +653,37 @@ __global__ void __launch_bounds__(256) doc_ranges_kernel(const __grid_constant__
   }
 }
 
+// CTAs that share an item, 1 to 8: the size with the least estimated time, in
+// steps (tiles taken by every group at once): the longest item's, or all items'
+// over 152 multiprocessors, with kOver steps of an item's own for its start and
+// join. A cluster pays where a few items are long (one key/value head under 32
+// query heads: ...) and costs where the items fill a wave (...).
+inline int cluster_for(int groups, int64_t items_a, int64_t tiles_a, int64_t items_b = 0, int64_t tiles_b = 0) {
+  constexpr double kOver = 1.5;
+  int best = 1;
+  double least = 0;
+  for (int cs = 1; cs <= 8; cs *= 2) {
+    const int64_t per = static_cast<int64_t>(cs) * groups;
+    const double ta = static_cast<double>((tiles_a + per - 1) / per) + kOver, tb = static_cast<double>((tiles_b + per - 1) / per) + kOver;
+    const double all = cs * (items_a * ta + items_b * tb) / 152.0;
+    const double t = std::max(std::max(items_a > 0 ? ta : 0.0, items_b > 0 ? tb : 0.0), all);
+    if (cs == 1 || t < 0.9 * least) {
+      best = cs;
+      least = t;
+    }
+  }
+  return best;
+}
+
 template <int D>
 cudaError_t fwd_d(const ScoreArgs& a, cudaStream_t s) {
   constexpr int bytes = Cfg<D>::kFwd * 4;
   static_assert(bytes <= 227 * 1024, "shared memory budget");
   cudaError_t e = allow_smem<score_fwd_f32_kernel<D>>(bytes);
   if (e != cudaSuccess) return e;
-  score_fwd_f32_kernel<D><<<dim3((a.Sq + kR - 1) / kR, a.H, a.B), Cfg<D>::kThreads, bytes, s>>>(a);
-  return cudaGetLastError();
+  const int64_t items = static_cast<int64_t>((a.Sq + kR - 1) / kR) * a.H * a.B;
+  return launch_clusters(score_fwd_f32_kernel<D>, items, cluster_for(Cfg<D>::kGroups, items, (a.Skv + kC - 1) / kC),
+                         Cfg<D>::kThreads, bytes, s, a);
 }
 
 template <int D>
@@ -670,10 +698,11 @@ cudaError_t bwd_d(const ScoreArgs& a, cudaStream_t s) {
     score_delta_kernel<D><<<static_cast<unsigned>((rows + 7) / 8), 256, 0, s>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
-  const int64_t ctas = (static_cast<int64_t>((a.Skv + kR - 1) / kR) * a.Hkv + static_cast<int64_t>((a.Sq + kR - 1) / kR) * a.H) * a.B;
-  if (ctas > 0x7fffffff) return cudaErrorInvalidValue;
-  score_bwd_f32_kernel<D><<<static_cast<unsigned>(ctas), Cfg<D>::kThreads, bytes, s>>>(a);
-  return cudaGetLastError();
+  const int64_t kv_items = static_cast<int64_t>((a.Skv + kR - 1) / kR) * a.Hkv * a.B;
+  const int64_t q_items = static_cast<int64_t>((a.Sq + kR - 1) / kR) * a.H * a.B;
+  const int cs = cluster_for(Cfg<D>::kGroups, kv_items, static_cast<int64_t>((a.Sq + kC - 1) / kC) * a.G, q_items,
+                             (a.Skv + kC - 1) / kC);
+  return launch_clusters(score_bwd_f32_kernel<D>, kv_items + q_items, cs, Cfg<D>::kThreads, bytes, s, a);
 }
 
 }  // namespace
