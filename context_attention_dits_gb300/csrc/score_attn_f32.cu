@@ -10,22 +10,26 @@
 //   dk_j  = scale sum_{h, i} ds_ij q_i,  dv_j = sum_{h, i} p_ij dout_i
 // where h runs over the query heads that share the key/value head.
 //
+// The products run on the tensor cores in three passes of tf32 (m16n8k8): with
+// x = hi + lo, hi its upper 11 bits, hi hi' + hi lo' + lo hi' leaves out 2^-22
+// of a product, and all sums are fp32. (As FMAs from shared memory the same
+// tiles were bound by its 128 bytes a cycle: a 4 x 4 block a thread needs half a
+// float an FMA where a quarter is the balance. 2048 tokens, 16 heads on 4, D =
+// 128, causal: forward 527 -> 444 us, backward 1611 -> 1283 us; the error
+// against 64 bits is below that of fp32 library products.)
 // Tiles: a CTA owns 32 rows (queries; keys for dk, dv) and walks 64-row tiles
-// of the other side. 128 threads form a group; a thread forms a 4 x 4 block of
-// scores (rows 4 ti .. 4 ti + 3, columns tj + 16 c), then 4 rows x D/16 columns
-// of the second product. Every tile is kept row-major with D + 4 floats a row: a
-// float4 column of 16 neighbouring rows then takes two wavefronts (the least
-// for 256 bytes), so one copy of K serves both Q K^T and dS K and nothing is
-// transposed. A 4 x 4 block costs 8 16-byte loads per 64 FMAs.
-// What bounds these kernels at the sizes fp32 is used for (a few hundred rows:
-// less than a CTA per multiprocessor) is the latency of a tile's chain of
-// copies, loads and barriers, so a CTA holds kGroups groups (as many as shared
-// memory holds tiles for: 4 at D = 64, 2 at D = 128) that take the tiles in
-// turn, each with its own buffers, barrier and running state, joined once at
-// the end; and a buffer's next tile is copied (16-byte asynchronous copies) as
-// soon as its last reader is through. Where that still leaves multiprocessors
-// idle, a cluster of 2, 4 or 8 CTAs shares the tiles of one item in the same way
-// and joins through distributed shared memory (see cluster_for).
+// of the other side. Four warps form a group; a warp takes 16 of the rows
+// against 32 rows of the tile, and keeps its own running state, so that the
+// weights never leave registers: accumulator columns 2t, 2t + 1 of a lane are
+// the A operand's columns t, t + 4 of the second product once the tile's rows
+// are taken in that order. Every tile is row-major with D + 4 floats a row, which
+// serves both products without bank conflicts and without a transposed copy.
+// A CTA holds kGroups groups (4 at D = 64, 2 at D = 128) that take the tiles in
+// turn, each with its own buffers and barrier, joined once at the end; a
+// buffer's next tile is copied (16-byte asynchronous copies) as soon as its last
+// reader is through. Where that still leaves multiprocessors idle, a cluster of
+// 2, 4 or 8 CTAs shares the tiles of one item in the same way and joins through
+// distributed shared memory (see cluster_for).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -42,7 +46,6 @@ namespace {
 constexpr int kGrp = 128;     // threads of a group
 constexpr int kR = 32;        // rows of the owned tile
 constexpr int kC = 64;        // rows of a streamed tile
-constexpr int kPT = kR + 4;   // row of the transposed probability tile
 constexpr float kL2e = 1.4426950408889634f;
 constexpr float kLn2f = 0.69314718055994531f;
 
@@ -52,10 +55,9 @@ struct Cfg {
   static constexpr int kThreads = kGroups * kGrp;
   static constexpr int kRow = D + 4;                           // floats of a row
   static constexpr int kOwn = kR * kRow, kTile = kC * kRow;    // floats of a tile
-  static constexpr int kP = kC * kPT;
-  static constexpr int kFwd = kOwn + kGroups * (2 * kTile + kP);
-  static constexpr int kBwd = 2 * kOwn + kGroups * (2 * kTile + kP + 2 * kC);
-  static_assert(2 * kOwn + 2 * kR <= 2 * kTile + kP, "a group's buffers hold its results at the end");
+  static constexpr int kStep = 2 * kTile + 4 * kC;             // a group's: two tiles, then row statistics
+  static constexpr int kFwd = kOwn + kGroups * kStep;
+  static constexpr int kBwd = 2 * kOwn + kGroups * kStep;
 };
 
 __device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
@@ -93,66 +95,109 @@ __device__ __forceinline__ void copy_rows(float* dst, const float* src, int64_t 
   }
 }
 
-// s[i][c] = row (4 ti + i) of a . row (tj + 16 c) of b
-template <int D>
-__device__ __forceinline__ void dots(float (&s)[4][4], const float* a, const float* b, int ti, int tj) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int c = 0; c < 4; ++c) s[i][c] = 0.f;
-#pragma unroll 4
-  for (int d = 0; d < D; d += 4) {
-    float4 x[4], y[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = load4(a + (4 * ti + i) * (D + 4) + d);
-#pragma unroll
-    for (int c = 0; c < 4; ++c) y[c] = load4(b + (tj + 16 * c) * (D + 4) + d);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-        s[i][c] = fmaf(x[i].w, y[c].w, fmaf(x[i].z, y[c].z, fmaf(x[i].y, y[c].y, fmaf(x[i].x, y[c].x, s[i][c]))));
-  }
+// x = hi + lo: hi rounded to tf32's 11 bits (half away from zero), so that lo has
+// either sign and what the multiplier does not read of it (2^-22 of x at most)
+// averages out over a sum.
+__device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
+  hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
+  lo = __float_as_uint(x - __uint_as_float(hi));
+}
+__device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// big += hi hi', small += hi lo' + lo hi'. The accumulators' additions truncate,
+// which adds up along a long sum (3.9e-6 of dq over 700 keys), so big is started
+// anew every four steps and added up by rounding additions (4e-7).
+__device__ __forceinline__ void mma3(float (&big)[4], float (&small)[4], const uint32_t (&ah)[4], const uint32_t (&al)[4],
+                                     float b0, float b1) {
+  uint32_t h0, l0, h1, l1;
+  split_tf32(b0, h0, l0);
+  split_tf32(b1, h1, l1);
+  mma_tf32(small, al, h0, h1);
+  mma_tf32(big, ah, h0, h1);
+  mma_tf32(small, ah, l0, l1);
 }
 
-// acc[i][.] += sum over the streamed tile's rows j of pt[j][4 ti + i] * b[j][columns of tj]
-// (columns 4 tj + 64 u, u < D / 64)
+// s[n][.] = 16 rows of a . rows 8 n .. 8 n + 7 of b, as accumulator fragments:
+// elements 0, 1 are row g, columns 2 t, 2 t + 1; 2, 3 row g + 8 (g = lane / 4, t = lane % 4)
 template <int D>
-__device__ __forceinline__ void second(float4 (&acc)[4][D / 64], const float* pt, const float* b, int ti, int tj) {
-#pragma unroll 4
-  for (int j = 0; j < kC; ++j) {
-    const float4 p = load4(pt + j * kPT + 4 * ti);
-    const float w[4] = {p.x, p.y, p.z, p.w};
+__device__ __forceinline__ void dots(float (&s)[4][4], const float* a, const float* b, int g, int t) {
+  float small[4][4];
 #pragma unroll
-    for (int u = 0; u < D / 64; ++u) {
-      const float4 y = load4(b + j * (D + 4) + 4 * tj + 64 * u);
+  for (int n = 0; n < 4; ++n)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        acc[i][u].x = fmaf(w[i], y.x, acc[i][u].x);
-        acc[i][u].y = fmaf(w[i], y.y, acc[i][u].y);
-        acc[i][u].z = fmaf(w[i], y.z, acc[i][u].z);
-        acc[i][u].w = fmaf(w[i], y.w, acc[i][u].w);
+    for (int e = 0; e < 4; ++e) s[n][e] = small[n][e] = 0.f;
+#pragma unroll 1
+  for (int k0 = 0; k0 < D; k0 += 32) {
+    float big[4][4];
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) big[n][e] = 0.f;
+#pragma unroll
+    for (int k = k0; k < k0 + 32; k += 8) {
+      uint32_t ah[4], al[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) split_tf32(a[(g + (e & 1) * 8) * (D + 4) + k + t + (e >> 1) * 4], ah[e], al[e]);
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        const float* r = b + (8 * n + g) * (D + 4) + k + t;
+        mma3(big[n], small[n], ah, al, r[0], r[4]);
       }
     }
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[n][e] += big[n][e];
+  }
+#pragma unroll
+  for (int n = 0; n < 4; ++n)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s[n][e] += small[n][e];
+}
+
+// acc += w b: w the 16 x 32 weights as the fragments of dots, b the tile's 32
+// rows; acc[n] columns 8 n .. 8 n + 7
+template <int D>
+__device__ __forceinline__ void second(float (&acc)[D / 8][4], const float (&w)[4][4], const float* b, int g, int t) {
+  uint32_t ah[4][4], al[4][4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) split_tf32(w[k][(e & 1) * 2 + (e >> 1)], ah[k][e], al[k][e]);
+  b += 2 * t * (D + 4) + g;
+#pragma unroll
+  for (int n = 0; n < D / 8; ++n) {
+    float big[4] = {0.f, 0.f, 0.f, 0.f}, small[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float* r = b + 8 * k * (D + 4) + 8 * n;
+      mma3(big, small, ah[k], al[k], r[0], r[D + 4]);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[n][e] += big[e] + small[e];
   }
 }
 
 template <int D>
-__device__ __forceinline__ void clear(float4 (&acc)[4][D / 64]) {
+__device__ __forceinline__ void clear(float (&acc)[D / 8][4]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int n = 0; n < D / 8; ++n)
 #pragma unroll
-    for (int u = 0; u < D / 64; ++u) acc[i][u] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
 }
 
-// acc as a [kR][D] tile (rows of D + 4) in shared memory
+// acc as 16 rows of D + 4 floats in shared memory
 template <int D>
-__device__ __forceinline__ void put(const float4 (&acc)[4][D / 64], float* dst, int ti, int tj) {
+__device__ __forceinline__ void put(const float (&acc)[D / 8][4], float* dst, int g, int t) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int u = 0; u < D / 64; ++u)
-      *reinterpret_cast<float4*>(dst + (4 * ti + i) * (D + 4) + 4 * tj + 64 * u) = acc[i][u];
+  for (int n = 0; n < D / 8; ++n) {
+    *reinterpret_cast<float2*>(dst + g * (D + 4) + 8 * n + 2 * t) = make_float2(acc[n][0], acc[n][1]);
+    *reinterpret_cast<float2*>(dst + (g + 8) * (D + 4) + 8 * n + 2 * t) = make_float2(acc[n][2], acc[n][3]);
+  }
 }
 
 // The score of a pair in units of log2, before the mask, and the derivative of
@@ -201,12 +246,12 @@ template <int D>
 __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) score_fwd_f32_kernel(const __grid_constant__ ScoreArgs a) {
   using C = Cfg<D>;
   extern __shared__ __align__(16) float sm[];
-  const int g = threadIdx.x / kGrp, tid = threadIdx.x % kGrp;
+  const int grp = threadIdx.x / kGrp, tid = threadIdx.x % kGrp;
+  const int r16 = (tid >> 5 & 1) * 16, c32 = (tid >> 6) * 32;  // the warp's rows and columns
+  const int g = (tid & 31) >> 2, t = tid & 3;
   float* Q = sm;
-  float* K = sm + C::kOwn + g * (2 * C::kTile + C::kP);
+  float* K = sm + C::kOwn + grp * C::kStep;
   float* V = K + C::kTile;
-  float* Pt = V + C::kTile;
-  const int ti = tid / 16, tj = tid % 16;
   const int cs = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
   const int item = blockIdx.x / cs, nrt = (a.Sq + kR - 1) / kR;
   const int h = item % a.H, b = item / a.H % a.B, hk = h / a.G;
@@ -224,23 +269,23 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) score_fwd_f32_kernel(cons
     cur.own = doc_range(a.qrange, b, a.Sq, row0);
   }
   cur.skip();
-  cur.step(rank * C::kGroups + g);
-  auto copy = [&](float* dst, const void* src, int t) {
-    if (t < cur.t1)
-      copy_rows<D>(dst, static_cast<const float*>(src) + ko + t * kC * ks, ks, min(kC, a.Skv - t * kC), kC, tid, kGrp);
+  cur.step(rank * C::kGroups + grp);
+  auto copy = [&](float* dst, const void* src, int at) {
+    if (at < cur.t1)
+      copy_rows<D>(dst, static_cast<const float*>(src) + ko + at * kC * ks, ks, min(kC, a.Skv - at * kC), kC, tid, kGrp);
     copy_commit();
   };
   copy_rows<D>(Q, static_cast<const float*>(a.q) + qo, qs, nrows, kR, threadIdx.x, C::kThreads);
   copy(K, a.k, cur.t);  // with Q
   copy(V, a.v, cur.t);
   const Scorer score(a, h);
-  int lim[4], qd[4];
-  float m[4], l[4];
-  float4 acc[4][D / 64];
+  int lim[2], qd[2];
+  float m[2], l[2];
+  float acc[D / 8][4];
   clear<D>(acc);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = 4 * ti + i;
+  for (int i = 0; i < 2; ++i) {  // rows g and g + 8 of the warp's
+    const int r = r16 + g + 8 * i;
     lim[i] = min(a.Skv, key_limit(a, plim, row0 + r));
     qd[i] = a.qdoc && r < nrows ? a.qdoc[static_cast<int64_t>(b) * a.Sq + row0 + r] : -1;
     m[i] = -INFINITY;
@@ -249,66 +294,72 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) score_fwd_f32_kernel(cons
   copy_wait<1>();
   __syncthreads();  // Q is every thread's
   while (cur.t < cur.t1) {
-    const int k0 = cur.t * kC;
+    const int j0 = cur.t * kC + c32 + 2 * t;
     cur.step(cs * C::kGroups);
     copy_wait<1>();  // K
-    group_sync(g);
+    group_sync(grp);
     float s[4][4];
-    dots<D>(s, Q, K, ti, tj);
-    group_sync(g);
+    dots<D>(s, Q + r16 * C::kRow, K + c32 * C::kRow, g, t);
+    group_sync(grp);
     copy(K, a.k, cur.t);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const int j = k0 + tj + 16 * c;
-      const int kd = a.qdoc && j < a.Skv ? a.kdoc[static_cast<int64_t>(b) * a.Skv + j] : -1;
+    for (int n = 0; n < 4; ++n)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float unused;
-        const bool on = j < lim[i] && (!a.qdoc || (qd[i] == kd && kd >= 0));
-        s[i][c] = on ? score(s[i][c], a.rel + row0 + 4 * ti + i - j, unused) : -INFINITY;
+      for (int c = 0; c < 2; ++c) {
+        const int j = j0 + 8 * n + c;
+        const int kd = a.qdoc && j < a.Skv ? a.kdoc[static_cast<int64_t>(b) * a.Skv + j] : -1;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float unused;
+          const bool on = j < lim[i] && (!a.qdoc || (qd[i] == kd && kd >= 0));
+          float& x = s[n][2 * i + c];
+          x = on ? score(x, a.rel + row0 + r16 + g + 8 * i - j, unused) : -INFINITY;
+        }
       }
-    }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float mx = fmaxf(fmaxf(s[i][0], s[i][1]), fmaxf(s[i][2], s[i][3]));
+    for (int i = 0; i < 2; ++i) {
+      float mx = -INFINITY;
 #pragma unroll
-      for (int o = 8; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      for (int n = 0; n < 4; ++n) mx = fmaxf(mx, fmaxf(s[n][2 * i], s[n][2 * i + 1]));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
       const float mn = fmaxf(m[i], mx), base = mn == -INFINITY ? 0.f : mn;
       const float f = exp2f(m[i] - base);  // 0 while m is -inf
       m[i] = mn;
       float sum = 0.f;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        s[i][c] = exp2f(s[i][c] - base);
-        sum += s[i][c];
-      }
+      for (int n = 0; n < 4; ++n)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          s[n][2 * i + c] = exp2f(s[n][2 * i + c] - base);
+          sum += s[n][2 * i + c];
+        }
       l[i] = l[i] * f + sum;
 #pragma unroll
-      for (int u = 0; u < D / 64; ++u) acc[i][u] = scaled(acc[i][u], f);
+      for (int n = 0; n < D / 8; ++n) {
+        acc[n][2 * i] *= f;
+        acc[n][2 * i + 1] *= f;
+      }
     }
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-      *reinterpret_cast<float4*>(Pt + (tj + 16 * c) * kPT + 4 * ti) = make_float4(s[0][c], s[1][c], s[2][c], s[3][c]);
     copy_wait<1>();  // V
-    group_sync(g);
-    second<D>(acc, Pt, V, ti, tj);
-    group_sync(g);
+    group_sync(grp);
+    second<D>(acc, s, V + c32 * C::kRow, g, t);
+    group_sync(grp);
     copy(V, a.v, cur.t);
   }
   copy_wait<0>();
+  // ---- the states of every CTA's warps joined: a CTA stores the rows of its
+  // share. K holds O of the two column halves, [2][32 rows]; then m, l ----
+  group_sync(grp);
+  put<D>(acc, K + (c32 + r16) * C::kRow, g, t);
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], o);
-  // ---- the states of every CTA's groups joined: a CTA stores the rows of its share ----
-  group_sync(g);
-  put<D>(acc, K, ti, tj);
-  if (tj == 0)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) *reinterpret_cast<float2*>(K + C::kOwn + 2 * (4 * ti + i)) = make_float2(m[i], l[i]);
+  for (int i = 0; i < 2; ++i) {
+    l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+    l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+    if (t == 0) *reinterpret_cast<float2*>(K + 2 * C::kTile + 2 * (c32 + r16 + g + 8 * i)) = make_float2(m[i], l[i]);
+  }
   cluster_sync();
   const uint32_t st0 = smem_addr(sm + C::kOwn);
-  constexpr int kStep = (2 * C::kTile + C::kP) * 4;  // bytes from a group's buffers to the next's
   const int share = kR / cs;
   for (int e = threadIdx.x; e < share * (D / 4); e += C::kThreads) {
     const int r = rank * share + e / (D / 4), d = (e % (D / 4)) * 4;
@@ -316,19 +367,20 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) score_fwd_f32_kernel(cons
     float mx = -INFINITY;
     for (int x = 0; x < cs; ++x)
 #pragma unroll
-      for (int y = 0; y < C::kGroups; ++y)
-        mx = fmaxf(mx, ld_peer2(cluster_peer(st0 + y * kStep + (C::kOwn + 2 * r) * 4, x)).x);
+      for (int y = 0; y < 2 * C::kGroups; ++y)
+        mx = fmaxf(mx, ld_peer2(cluster_peer(st0 + ((y >> 1) * C::kStep + 2 * C::kTile + 2 * ((y & 1) * kR + r)) * 4, x)).x);
     const float base = mx == -INFINITY ? 0.f : mx;
     float sum = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int x = 0; x < cs; ++x)
 #pragma unroll
-      for (int y = 0; y < C::kGroups; ++y) {
-        const uint32_t st = cluster_peer(st0 + y * kStep, x);
-        const float2 ml = ld_peer2(st + (C::kOwn + 2 * r) * 4);
+      for (int y = 0; y < 2 * C::kGroups; ++y) {
+        const uint32_t st = cluster_peer(st0 + (y >> 1) * C::kStep * 4, x);
+        const int rr = (y & 1) * kR + r;
+        const float2 ml = ld_peer2(st + (2 * C::kTile + 2 * rr) * 4);
         const float f = exp2f(ml.x - base);
         sum = fmaf(ml.y, f, sum);
-        add4(o, scaled(ld_peer4(st + (r * (D + 4) + d) * 4), f));
+        add4(o, scaled(ld_peer4(st + (rr * C::kRow + d) * 4), f));
       }
     store4(a.out, qo + r * qs + d, scaled(o, sum != 0.f ? 1.f / sum : 0.f));
     if (d == 0)
@@ -363,18 +415,38 @@ __device__ __forceinline__ float lse2_of(const ScoreArgs& a, int64_t o, bool val
   return x == -INFINITY ? INFINITY : x * kL2e;
 }
 
+// Sum over every CTA's warps of the 32 x D results that put has left at `at`
+// floats into each group's buffers, times mul, to dst (row r at r * stride).
+template <int D>
+__device__ __forceinline__ void join(const float* sm, int at, int cs, int rank, int n, float mul, void* dst, int64_t to,
+                                     int64_t stride) {
+  using C = Cfg<D>;
+  const uint32_t st0 = smem_addr(sm + 2 * C::kOwn + at);
+  const int share = kR / cs;
+  for (int e = threadIdx.x; e < share * (D / 4); e += C::kThreads) {
+    const int r = rank * share + e / (D / 4), d = (e % (D / 4)) * 4;
+    if (r >= n) break;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c = 0; c < cs; ++c)
+#pragma unroll
+      for (int y = 0; y < 2 * C::kGroups; ++y)
+        add4(x, ld_peer4(cluster_peer(st0 + ((y >> 1) * C::kStep + ((y & 1) * kR + r) * C::kRow + d) * 4, c)));
+    store4(dst, to + r * stride + d, scaled(x, mul));
+  }
+}
+
 // dq of 32 query rows: key tiles stream by.
 template <int D>
 __device__ __forceinline__ void dq_cta(const ScoreArgs& a, float* sm, int cs, int rank, int bx, int h, int b) {
   using C = Cfg<D>;
-  constexpr int kStep = 2 * C::kTile + C::kP + 2 * kC;
-  const int g = threadIdx.x / kGrp, tid = threadIdx.x % kGrp;
+  const int grp = threadIdx.x / kGrp, tid = threadIdx.x % kGrp;
+  const int r16 = (tid >> 5 & 1) * 16, c32 = (tid >> 6) * 32;
+  const int g = (tid & 31) >> 2, t = tid & 3;
   float* Q = sm;
   float* dO = Q + C::kOwn;
-  float* K = dO + C::kOwn + g * kStep;
+  float* K = dO + C::kOwn + grp * C::kStep;
   float* V = K + C::kTile;
-  float* Pt = V + C::kTile;
-  const int ti = tid / 16, tj = tid % 16, hk = h / a.G;
+  const int hk = h / a.G;
   const int row0 = bx * kR;
   const int nrows = min(kR, a.Sq - row0);
   const int64_t qs = static_cast<int64_t>(a.H) * D, ks = static_cast<int64_t>(a.Hkv) * D;
@@ -389,10 +461,10 @@ __device__ __forceinline__ void dq_cta(const ScoreArgs& a, float* sm, int cs, in
     cur.own = doc_range(a.qrange, b, a.Sq, row0);
   }
   cur.skip();
-  cur.step(rank * C::kGroups + g);
-  auto copy = [&](float* dst, const void* src, int t) {
-    if (t < cur.t1)
-      copy_rows<D>(dst, static_cast<const float*>(src) + ko + t * kC * ks, ks, min(kC, a.Skv - t * kC), kC, tid, kGrp);
+  cur.step(rank * C::kGroups + grp);
+  auto copy = [&](float* dst, const void* src, int at) {
+    if (at < cur.t1)
+      copy_rows<D>(dst, static_cast<const float*>(src) + ko + at * kC * ks, ks, min(kC, a.Skv - at * kC), kC, tid, kGrp);
     copy_commit();
   };
   copy_rows<D>(Q, static_cast<const float*>(a.q) + qo, qs, nrows, kR, threadIdx.x, C::kThreads);
@@ -400,13 +472,13 @@ __device__ __forceinline__ void dq_cta(const ScoreArgs& a, float* sm, int cs, in
   copy(V, a.v, cur.t);
   copy(K, a.k, cur.t);
   const Scorer score(a, h);
-  int lim[4], qd[4];
-  float lse2[4], dlt[4];
-  float4 acc[4][D / 64];
+  int lim[2], qd[2];
+  float lse2[2], dlt[2];
+  float acc[D / 8][4];
   clear<D>(acc);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = 4 * ti + i;
+  for (int i = 0; i < 2; ++i) {
+    const int r = r16 + g + 8 * i;
     const int64_t o = (static_cast<int64_t>(b) * a.H + h) * a.Sq + row0 + r;
     lim[i] = min(a.Skv, key_limit(a, plim, row0 + r));
     qd[i] = a.qdoc && r < nrows ? a.qdoc[static_cast<int64_t>(b) * a.Sq + row0 + r] : -1;
@@ -416,66 +488,56 @@ __device__ __forceinline__ void dq_cta(const ScoreArgs& a, float* sm, int cs, in
   copy_wait<0>();
   __syncthreads();
   while (cur.t < cur.t1) {
-    const int k0 = cur.t * kC;
+    const int j0 = cur.t * kC + c32 + 2 * t;
     cur.step(cs * C::kGroups);
     copy_wait<0>();
-    group_sync(g);
+    group_sync(grp);
     float s[4][4], dp[4][4];
-    dots<D>(dp, dO, V, ti, tj);
-    dots<D>(s, Q, K, ti, tj);
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const int j = k0 + tj + 16 * c;
-      const int kd = a.qdoc && j < a.Skv ? a.kdoc[static_cast<int64_t>(b) * a.Skv + j] : -1;
-      float ds[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float dcap;
-        const bool on = j < lim[i] && (!a.qdoc || (qd[i] == kd && kd >= 0));
-        const float p = exp2f(score(s[i][c], a.rel + row0 + 4 * ti + i - j, dcap) - lse2[i]);
-        ds[i] = on ? p * (dp[i][c] - dlt[i]) * dcap : 0.f;
-      }
-      *reinterpret_cast<float4*>(Pt + (tj + 16 * c) * kPT + 4 * ti) = make_float4(ds[0], ds[1], ds[2], ds[3]);
-    }
-    group_sync(g);
+    dots<D>(dp, dO + r16 * C::kRow, V + c32 * C::kRow, g, t);
+    dots<D>(s, Q + r16 * C::kRow, K + c32 * C::kRow, g, t);
+    group_sync(grp);
     copy(V, a.v, cur.t);
-    second<D>(acc, Pt, K, ti, tj);
-    group_sync(g);
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int j = j0 + 8 * n + c;
+        const int kd = a.qdoc && j < a.Skv ? a.kdoc[static_cast<int64_t>(b) * a.Skv + j] : -1;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float dcap;
+          const bool on = j < lim[i] && (!a.qdoc || (qd[i] == kd && kd >= 0));
+          const int e = 2 * i + c;
+          const float p = exp2f(score(s[n][e], a.rel + row0 + r16 + g + 8 * i - j, dcap) - lse2[i]);
+          s[n][e] = on ? p * (dp[n][e] - dlt[i]) * dcap : 0.f;
+        }
+      }
+    second<D>(acc, s, K + c32 * C::kRow, g, t);
+    group_sync(grp);
     copy(K, a.k, cur.t);
   }
   copy_wait<0>();
-  group_sync(g);
-  put<D>(acc, K, ti, tj);
+  group_sync(grp);
+  put<D>(acc, K + (c32 + r16) * C::kRow, g, t);
   cluster_sync();
-  const uint32_t st0 = smem_addr(sm + 2 * C::kOwn);
-  const int share = kR / cs;
-  for (int e = threadIdx.x; e < share * (D / 4); e += C::kThreads) {
-    const int r = rank * share + e / (D / 4), d = (e % (D / 4)) * 4;
-    if (r >= nrows) break;
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c = 0; c < cs; ++c)
-#pragma unroll
-      for (int y = 0; y < C::kGroups; ++y) add4(x, ld_peer4(cluster_peer(st0 + (y * kStep + r * (D + 4) + d) * 4, c)));
-    store4(a.dq, qo + r * qs + d, scaled(x, a.scale));
-  }
+  join<D>(sm, 0, cs, rank, nrows, a.scale, a.dq, qo, qs);
 }
 
 // dk, dv of 32 keys: the streamed tiles are 64 query rows of each head that
 // shares the key/value head, head by head. Scores are formed transposed (rows
-// are keys), and P^T and then dS^T pass through one buffer.
+// are keys).
 template <int D>
 __device__ __forceinline__ void dkdv_cta(const ScoreArgs& a, float* sm, int cs, int rank, int bx, int hk, int b) {
   using C = Cfg<D>;
-  constexpr int kStep = 2 * C::kTile + C::kP + 2 * kC;
-  const int g = threadIdx.x / kGrp, tid = threadIdx.x % kGrp;
+  const int grp = threadIdx.x / kGrp, tid = threadIdx.x % kGrp;
+  const int r16 = (tid >> 5 & 1) * 16, c32 = (tid >> 6) * 32;
+  const int g = (tid & 31) >> 2, t = tid & 3;
   float* K = sm;
   float* V = K + C::kOwn;
-  float* Q = V + C::kOwn + g * kStep;
+  float* Q = V + C::kOwn + grp * C::kStep;
   float* dO = Q + C::kTile;
-  float* Pt = dO + C::kTile;
-  float* lse2 = Pt + C::kP;
+  float* lse2 = dO + C::kTile;
   float* dlt = lse2 + kC;
-  const int ti = tid / 16, tj = tid % 16;
   const int key0 = bx * kR;
   const int nk = min(kR, a.Skv - key0);
   const int64_t qs = static_cast<int64_t>(a.H) * D, ks = static_cast<int64_t>(a.Hkv) * D;
@@ -484,13 +546,13 @@ __device__ __forceinline__ void dkdv_cta(const ScoreArgs& a, float* sm, int cs, 
   copy_rows<D>(V, static_cast<const float*>(a.v) + ko, ks, nk, kR, threadIdx.x, C::kThreads);
   copy_commit();
   const int plim = prefix_limit(a, b);
-  int kd[4];
-  float4 dk[4][D / 64], dv[4][D / 64];
+  int kd[2];
+  float dk[D / 8][4], dv[D / 8][4];
   clear<D>(dk);
   clear<D>(dv);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = 4 * ti + i;
+  for (int i = 0; i < 2; ++i) {
+    const int r = r16 + g + 8 * i;
     kd[i] = a.qdoc && r < nk ? a.kdoc[static_cast<int64_t>(b) * a.Skv + key0 + r] : -1;
   }
   // query tiles from the first row that reaches a key of the tile
@@ -517,12 +579,11 @@ __device__ __forceinline__ void dkdv_cta(const ScoreArgs& a, float* sm, int cs, 
       if (cur.t >= cur.t1) {
         cur = first;
         ++h;
-        if (first.t >= first.t1) h = h1;
       }
     }
   };
   if (first.t >= first.t1) h = h1;
-  step(rank * C::kGroups + g);
+  step(rank * C::kGroups + grp);
   auto copy = [&](float* dst, const void* src) {
     if (h < h1) {
       const int64_t qo = (static_cast<int64_t>(b) * a.Sq + cur.t * kC) * qs + static_cast<int64_t>(h) * D;
@@ -544,61 +605,42 @@ __device__ __forceinline__ void dkdv_cta(const ScoreArgs& a, float* sm, int cs, 
     }
     step(cs * C::kGroups);
     copy_wait<0>();
-    group_sync(g);
+    group_sync(grp);
     float s[4][4], dp[4][4];
-    dots<D>(s, K, Q, ti, tj);
-    dots<D>(dp, V, dO, ti, tj);
+    dots<D>(s, K + r16 * C::kRow, Q + c32 * C::kRow, g, t);
+    dots<D>(dp, V + r16 * C::kRow, dO + c32 * C::kRow, g, t);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const int r = tj + 16 * c, i = q0 + r;
-      const int lim = key_limit(a, plim, i);
-      const int qd = a.qdoc && r < nq ? a.qdoc[static_cast<int64_t>(b) * a.Sq + i] : -1;
-      float p[4];
+    for (int n = 0; n < 4; ++n)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int j = key0 + 4 * ti + e;
-        float dcap;
-        const bool on = r < nq && j < lim && (!a.qdoc || (qd == kd[e] && qd >= 0));
-        const float x = exp2f(score(s[e][c], a.rel + i - j, dcap) - lse2[r]);
-        p[e] = on ? x : 0.f;
-        dp[e][c] = on ? x * (dp[e][c] - dlt[r]) * dcap : 0.f;
+      for (int c = 0; c < 2; ++c) {
+        const int r = c32 + 8 * n + 2 * t + c, i = q0 + r;
+        const int lim = key_limit(a, plim, i);
+        const int qd = a.qdoc && r < nq ? a.qdoc[static_cast<int64_t>(b) * a.Sq + i] : -1;
+        const float l2 = lse2[r], dl = dlt[r];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int j = key0 + r16 + g + 8 * u, e = 2 * u + c;
+          float dcap;
+          const bool on = r < nq && j < lim && (!a.qdoc || (qd == kd[u] && qd >= 0));
+          const float p = exp2f(score(s[n][e], a.rel + i - j, dcap) - l2);
+          s[n][e] = on ? p : 0.f;
+          dp[n][e] = on ? p * (dp[n][e] - dl) * dcap : 0.f;
+        }
       }
-      *reinterpret_cast<float4*>(Pt + r * kPT + 4 * ti) = make_float4(p[0], p[1], p[2], p[3]);
-    }
-    group_sync(g);
-    second<D>(dv, Pt, dO, ti, tj);
-    group_sync(g);
+    second<D>(dv, s, dO + c32 * C::kRow, g, t);
+    group_sync(grp);
     copy(dO, a.dout);
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-      *reinterpret_cast<float4*>(Pt + (tj + 16 * c) * kPT + 4 * ti) =
-          make_float4(dp[0][c], dp[1][c], dp[2][c], dp[3][c]);
-    group_sync(g);
-    second<D>(dk, Pt, Q, ti, tj);
-    group_sync(g);
+    second<D>(dk, dp, Q + c32 * C::kRow, g, t);
+    group_sync(grp);
     copy(Q, a.q);
   }
   copy_wait<0>();
-  group_sync(g);
-  put<D>(dk, Q, ti, tj);
-  put<D>(dv, Q + C::kOwn, ti, tj);
+  group_sync(grp);
+  put<D>(dk, Q + (c32 + r16) * C::kRow, g, t);
+  put<D>(dv, dO + (c32 + r16) * C::kRow, g, t);
   cluster_sync();
-  const uint32_t st0 = smem_addr(sm + 2 * C::kOwn);
-  const int share = kR / cs;
-  for (int e = threadIdx.x; e < share * (D / 4); e += C::kThreads) {
-    const int r = rank * share + e / (D / 4), d = (e % (D / 4)) * 4;
-    if (r >= nk) break;
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
-    for (int c = 0; c < cs; ++c)
-#pragma unroll
-      for (int z = 0; z < C::kGroups; ++z) {
-        const uint32_t st = cluster_peer(st0 + (z * kStep + r * (D + 4) + d) * 4, c);
-        add4(x, ld_peer4(st));
-        add4(y, ld_peer4(st + C::kOwn * 4));
-      }
-    store4(a.dk, ko + r * ks + d, scaled(x, a.scale));
-    store4(a.dv, ko + r * ks + d, y);
-  }
+  join<D>(sm, 0, cs, rank, nk, a.scale, a.dk, ko, ks);
+  join<D>(sm, C::kTile, cs, rank, nk, 1.f, a.dv, ko, ks);
 }
 
 // Both kinds of CTA in one launch: dk/dv CTAs (the first keys, which the most
