@@ -92,6 +92,14 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity,
 }
 
 // ----------------------------------------------------------------------------
+// Overlap of a launch with its predecessor's end (programmatic launches): the
+// predecessor lets its successor start; the successor waits for all of the
+// predecessor's work, visible after. Both do nothing in ordinary launches.
+// ----------------------------------------------------------------------------
+__device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// ----------------------------------------------------------------------------
 // Clusters (a launch without the attribute has clusters of one CTA)
 // ----------------------------------------------------------------------------
 __device__ __forceinline__ uint32_t cluster_rank() {

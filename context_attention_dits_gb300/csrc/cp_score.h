@@ -119,22 +119,57 @@ cudaError_t allow_smem(int bytes) {
   return e;
 }
 
-// Launches `items` clusters of `cluster` CTAs each.
+// CTAs that share an item, 1 to 8: the size with the least estimated time. Items
+// of kind a (taken by clusters) and b (by clusters too if b_clusters, else by
+// single CTAs) have up to tiles_a and tiles_b steps, `over` steps of their own
+// for start and join, and a part `fill` of the steps on average; the estimate is
+// the longest item's time or all items' over 152 multiprocessors. Where items
+// fill a wave of their own a cluster only adds starts and joins (fp32, 104 items
+// of 7 tiles: 22 us alone, 29 in clusters of 2); it pays where a few are long
+// (fp32, 32 query heads on one: backward 2544 us alone, 1288 in clusters of 2).
+inline int cluster_for(double over, int64_t items_a, int64_t tiles_a, int64_t items_b, int64_t tiles_b, double fill,
+                       bool b_clusters) {
+  int best = 1;
+  double least = 0;
+  for (int cs = 1; cs <= 8; cs *= 2) {
+    const int cb = b_clusters ? cs : 1;
+    const double ta = static_cast<double>((tiles_a + cs - 1) / cs), tb = static_cast<double>((tiles_b + cb - 1) / cb);
+    const double all = (items_a * cs * (fill * ta + over) + items_b * cb * (fill * tb + over)) / 152.0;
+    double t = all;
+    if (items_a > 0 && ta + over > t) t = ta + over;
+    if (items_b > 0 && tb + over > t) t = tb + over;
+    if (cs == 1 || t < 0.9 * least) {
+      best = cs;
+      least = t;
+    }
+  }
+  return best;
+}
+
+// Launches `items` clusters of `cluster` CTAs each; `after`: the launch may start
+// while its predecessor in the stream ends (the kernel calls grid_wait).
 template <typename... P, typename... A>
-cudaError_t launch_clusters(void (*kernel)(P...), int64_t items, int cluster, int threads, int smem, cudaStream_t s,
-                            const A&... args) {
+cudaError_t launch_clusters(void (*kernel)(P...), int64_t items, int cluster, int threads, int smem, bool after,
+                            cudaStream_t s, const A&... args) {
   if (items * cluster > 0x7fffffff) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(items * cluster));
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim.x = cluster;
-  at.val.clusterDim.y = at.val.clusterDim.z = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = cluster > 1 ? 1 : 0;
+  cudaLaunchAttribute at[2]{};
+  cfg.attrs = at;
+  if (cluster > 1) {
+    at[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+    at[cfg.numAttrs].val.clusterDim.x = cluster;
+    at[cfg.numAttrs].val.clusterDim.y = at[cfg.numAttrs].val.clusterDim.z = 1;
+    ++cfg.numAttrs;
+  }
+  if (after) {
+    at[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
+    ++cfg.numAttrs;
+  }
   return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
 }
 

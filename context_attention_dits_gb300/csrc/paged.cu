@@ -525,7 +525,7 @@ __global__ void __launch_bounds__(kDecThreads) paged_decode_kernel(const __grid_
 template <int D>
 __global__ void __launch_bounds__(D) paged_join_kernel(const __grid_constant__ PagedArgs a, int rows) {
   const int h = blockIdx.x, b = blockIdx.y, d = threadIdx.x;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  grid_wait();
   if (a.seq_lens[b] <= 0) return;
   const int groups = (a.G + rows - 1) / rows;
   const int hk = h / a.G, r = (h - hk * a.G) % rows, hg = (h - hk * a.G) / rows;

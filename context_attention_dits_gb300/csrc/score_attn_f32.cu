@@ -252,6 +252,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) score_fwd_f32_kernel(cons
   float* Q = sm;
   float* K = sm + C::kOwn + grp * C::kStep;
   float* V = K + C::kTile;
+  grid_wait();  // the document ranges
   const int cs = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
   const int item = blockIdx.x / cs, nrt = (a.Sq + kR - 1) / kR;
   const int h = item % a.H, b = item / a.H % a.B, hk = h / a.G;
@@ -392,6 +393,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) score_fwd_f32_kernel(cons
 // delta[b, h, i] = out_i . dout_i, a warp per row of [B, Sq, H, D]
 template <int D>
 __global__ void __launch_bounds__(256) score_delta_kernel(const __grid_constant__ ScoreArgs a) {
+  grid_release();
   const int lane = threadIdx.x & 31;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
   if (row >= static_cast<int64_t>(a.B) * a.Sq * a.H) return;
@@ -649,6 +651,7 @@ template <int D>
 __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) score_bwd_f32_kernel(const __grid_constant__ ScoreArgs a) {
   extern __shared__ __align__(16) float sm[];
   const int cs = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
+  grid_wait();  // the delta kernel's results
   const int kv_items = (a.Skv + kR - 1) / kR * a.Hkv * a.B, nq = (a.Sq + kR - 1) / kR;
   const int id = static_cast<int>(blockIdx.x) / cs;
   if (id < kv_items) {
@@ -664,6 +667,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) score_bwd_f32_kernel(cons
 // A warp per 64-row block of the document ids of q (the first nq blocks of a
 // batch entry) and k.
 __global__ void __launch_bounds__(256) doc_ranges_kernel(const __grid_constant__ ScoreArgs a, int nq, int nk) {
+  grid_release();
   const int lane = threadIdx.x & 31;
   const int64_t w = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
   if (w >= static_cast<int64_t>(a.B) * (nq + nk)) return;
@@ -695,28 +699,6 @@ __global__ void __launch_bounds__(256) doc_ranges_kernel(const __grid_constant__
   }
 }
 
-// CTAs that share an item, 1 to 8: the size with the least estimated time, in
-// steps (tiles taken by every group at once): the longest item's, or all items'
-// over 152 multiprocessors, with kOver steps of an item's own for its start and
-// join. A cluster pays where a few items are long (one key/value head under 32
-// query heads: ...) and costs where the items fill a wave (...).
-inline int cluster_for(int groups, int64_t items_a, int64_t tiles_a, int64_t items_b = 0, int64_t tiles_b = 0) {
-  constexpr double kOver = 1.5;
-  int best = 1;
-  double least = 0;
-  for (int cs = 1; cs <= 8; cs *= 2) {
-    const int64_t per = static_cast<int64_t>(cs) * groups;
-    const double ta = static_cast<double>((tiles_a + per - 1) / per) + kOver, tb = static_cast<double>((tiles_b + per - 1) / per) + kOver;
-    const double all = cs * (items_a * ta + items_b * tb) / 152.0;
-    const double t = std::max(std::max(items_a > 0 ? ta : 0.0, items_b > 0 ? tb : 0.0), all);
-    if (cs == 1 || t < 0.9 * least) {
-      best = cs;
-      least = t;
-    }
-  }
-  return best;
-}
-
 template <int D>
 cudaError_t fwd_d(const ScoreArgs& a, cudaStream_t s) {
   constexpr int bytes = Cfg<D>::kFwd * 4;
@@ -724,8 +706,10 @@ cudaError_t fwd_d(const ScoreArgs& a, cudaStream_t s) {
   cudaError_t e = allow_smem<score_fwd_f32_kernel<D>>(bytes);
   if (e != cudaSuccess) return e;
   const int64_t items = static_cast<int64_t>((a.Sq + kR - 1) / kR) * a.H * a.B;
-  return launch_clusters(score_fwd_f32_kernel<D>, items, cluster_for(Cfg<D>::kGroups, items, (a.Skv + kC - 1) / kC),
-                         Cfg<D>::kThreads, bytes, s, a);
+  // steps: tiles taken by every group at once
+  const int64_t steps = ((a.Skv + kC - 1) / kC + Cfg<D>::kGroups - 1) / Cfg<D>::kGroups;
+  return launch_clusters(score_fwd_f32_kernel<D>, items, cluster_for(1.5, items, steps, 0, 0, a.causal ? 0.5 : 1.0, true),
+                         Cfg<D>::kThreads, bytes, a.qdoc != nullptr, s, a);
 }
 
 template <int D>
@@ -742,9 +726,10 @@ cudaError_t bwd_d(const ScoreArgs& a, cudaStream_t s) {
   }
   const int64_t kv_items = static_cast<int64_t>((a.Skv + kR - 1) / kR) * a.Hkv * a.B;
   const int64_t q_items = static_cast<int64_t>((a.Sq + kR - 1) / kR) * a.H * a.B;
-  const int cs = cluster_for(Cfg<D>::kGroups, kv_items, static_cast<int64_t>((a.Sq + kC - 1) / kC) * a.G, q_items,
-                             (a.Skv + kC - 1) / kC);
-  return launch_clusters(score_bwd_f32_kernel<D>, kv_items + q_items, cs, Cfg<D>::kThreads, bytes, s, a);
+  constexpr int G = Cfg<D>::kGroups;
+  const int cs = cluster_for(1.5, kv_items, (static_cast<int64_t>((a.Sq + kC - 1) / kC) * a.G + G - 1) / G, q_items,
+                             ((a.Skv + kC - 1) / kC + G - 1) / G, a.causal ? 0.5 : 1.0, true);
+  return launch_clusters(score_bwd_f32_kernel<D>, kv_items + q_items, cs, Cfg<D>::kThreads, bytes, a.Sq > 0, s, a);
 }
 
 }  // namespace

@@ -231,11 +231,13 @@ __device__ __forceinline__ void store_row32(void* dst, int64_t at, bool bf16, co
 
 // One dk/dv CTA: key tile bx of key/value head hk, batch entry b. tq64, to64: Q
 // and dO with 64-row boxes; tk, tv: K and V with 128-row boxes; smem_raw holds
-// alloc bytes of dynamic shared memory.
+// alloc bytes of dynamic shared memory. The cs CTAs of a cluster take equal
+// ranges of the sub-steps, and each sums the rows of its share over all of them
+// (in the order of their ranks) through distributed shared memory.
 template <int D, bool kCap, bool kBias>
 __device__ __forceinline__ void dkdv_cta(const CUtensorMap& tq64, const CUtensorMap& tk, const CUtensorMap& tv,
                                          const CUtensorMap& to64, const ScoreArgs& a, const CapCoef& cc,
-                                         uint8_t* smem_raw, int alloc, int bx, int hk, int b) {
+                                         uint8_t* smem_raw, int alloc, int cs, int rank, int bx, int hk, int b) {
   using L = BSmem<D>;
   // the swizzled tiles need a 1024-byte aligned base; a base that would need
   // more padding than the allocation holds is reported (uniformly, before any
@@ -269,7 +271,27 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap& tq64, const CUtensor
   if (a.qdoc)
     per_head = walk_map(a.qrange + static_cast<int64_t>(b) * nqb, nqb,
                         doc_span(a.krange + static_cast<int64_t>(b) * nkb, nkb, bx * 2, 2), t0, ntq, act, misc + 2);
-  const int NJ = per_head * a.G;  // sub-steps: the sub-tiles of every query head, head by head
+  // sub-steps: the sub-tiles of every query head, head by head; this CTA's part of them
+  const int all = per_head * a.G, j0 = static_cast<int>(static_cast<int64_t>(all) * rank / cs);
+  const int NJ = static_cast<int>(static_cast<int64_t>(all) * (rank + 1) / cs) - j0;
+  struct HeadWalk {
+    TileWalk first, w;
+    int h;
+    __device__ __forceinline__ HeadWalk(const uint32_t* bits, int t0, int t1, int per_head, int h0, int j)
+        : first(bits, t0, t1, t0 - 1), w(first), h(h0) {
+      if (per_head > 0) {
+        h += j / per_head;
+        for (int i = j % per_head; i > 0; --i) w.next();
+      }
+    }
+    __device__ __forceinline__ void next() {
+      w.next();
+      if (w.done()) {
+        w = first;
+        ++h;
+      }
+    }
+  };
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < L::kNumBars; ++i) {
@@ -304,30 +326,25 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap& tq64, const CUtensor
       }
     }
     int issued[kSlots] = {0, 0, 0, 0};
-    TileWalk cur(bits, t0, ntq, t0 - 1);
-    int h = hk * a.G;
+    HeadWalk cur(bits, t0, ntq, per_head, hk * a.G, j0);
     for (int j = 0; j < NJ; ++j) {
       const int s = j & (kSlots - 1);
       const uint32_t ph = (j >> 2) & 1;
       if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar(kBarQEmpty + s), ph ^ 1, abort_flag, a.err, tmo))) break;
-      const int q0 = cur.t * kSub;
+      const int q0 = cur.w.t * kSub, h = cur.h;
       if (leader) {
         mbar_arrive_expect_tx(bar(kBarQFull + s), 2 * L::kSubT + 2 * kSub * 4);
         for (int c = 0; c < D / 64; ++c) {
           tma_load_4d(sb + L::kOffQ + s * L::kSubT + c * L::kHalfS, &tq64, bar(kBarQFull + s), c * 64, h, q0, b);
           tma_load_4d(sb + L::kOffO + s * L::kSubT + c * L::kHalfS, &to64, bar(kBarQFull + s), c * 64, h, q0, b);
         }
-        const int64_t pr = ((static_cast<int64_t>(b) * a.H + h) * ntq + cur.t) * kSub;
+        const int64_t pr = ((static_cast<int64_t>(b) * a.H + h) * ntq + cur.w.t) * kSub;
         bulk_g2s(smem_addr(s_lse + s * kSub), a.lse2p + pr, kSub * 4, bar(kBarQFull + s));
         bulk_g2s(smem_addr(s_dlt + s * kSub), a.dltp + pr, kSub * 4, bar(kBarQFull + s));
       }
       __syncwarp();
       ++issued[s];
       cur.next();
-      if (cur.done()) {
-        cur = TileWalk(bits, t0, ntq, t0 - 1);
-        ++h;
-      }
     }
     if (*abort_flag) {
       // let every issued copy land before the CTA's shared memory goes away
@@ -437,15 +454,14 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap& tq64, const CUtensor
     const int kd = a.qdoc && kvalid ? a.kdoc[static_cast<int64_t>(b) * a.Skv + jkey] : -1;
     const int* qdoc = a.qdoc + static_cast<int64_t>(b) * a.Sq;
     bool ok = true;
-    TileWalk cur(bits, t0, ntq, t0 - 1);
-    int h = hk * a.G;
-    float slope2 = kBias ? a.slopes[h] * kLog2e : 0.f;
+    HeadWalk cur(bits, t0, ntq, per_head, hk * a.G, j0);
     for (int j = 0; j < NJ; ++j) {
       const int q = j & (kSlots - 1), ts = j & 1;
-      const int i0 = cur.t * kSub + hc * 32;  // the query row of this warp's first column
+      const float slope2 = kBias ? __ldg(a.slopes + cur.h) * kLog2e : 0.f;
+      const int i0 = cur.w.t * kSub + hc * 32;  // the query row of this warp's first column
       const int d0 = a.rel + i0 - jkey;       // its position less the key's
       uint32_t on = !kvalid ? 0u : open || d0 >= 0 ? ~0u : d0 <= -32 ? 0u : ~0u << -d0;
-      if (bits != nullptr && ((act[kMapWords + (cur.t >> 5)] >> (cur.t & 31)) & 1u)) {
+      if (bits != nullptr && ((act[kMapWords + (cur.w.t >> 5)] >> (cur.w.t & 31)) & 1u)) {
         const int ids[1] = {i0 + lane < a.Sq ? __ldg(qdoc + i0 + lane) : -1};
         uint32_t same[1];
         same_docs<1>(kd, ids, same);
@@ -480,11 +496,6 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap& tq64, const CUtensor
       tmem_st16(t_s, pp);
       tmem_st16(t_dp, dd);
       cur.next();
-      if (cur.done()) {
-        cur = TileWalk(bits, t0, ntq, t0 - 1);
-        ++h;
-        if (kBias && j + 1 < NJ) slope2 = a.slopes[h] * kLog2e;
-      }
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -506,9 +517,45 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap& tq64, const CUtensor
 #pragma unroll
           for (int x = 0; x < 32; ++x) r[x] = 0u;
         }
-        if (kvalid) store_row32(g == 0 ? a.dv : a.dk, at + c * 32, a.grad_bf16, r, g == 0 ? 1.f : a.scale);
+        if (cs > 1) {  // this CTA's part, over the idle tiles: [dv, dk][key][D], 16-byte pieces permuted by row
+          float* part = reinterpret_cast<float*>(smem) + (g * kT + key) * D;
+#pragma unroll
+          for (int x = 0; x < 8; ++x)
+            *reinterpret_cast<float4*>(part + (((c * 8 + x) ^ (key & 7)) * 4)) =
+                make_float4(u2f(r[4 * x]), u2f(r[4 * x + 1]), u2f(r[4 * x + 2]), u2f(r[4 * x + 3]));
+        } else if (kvalid) {
+          store_row32(g == 0 ? a.dv : a.dk, at + c * 32, a.grad_bf16, r, g == 0 ? 1.f : a.scale);
+        }
       }
     }
+  }
+  if (cs > 1) {
+    static_assert(2 * kT * D * 4 <= L::kOffLse, "the parts lie over the tiles");
+    __syncwarp();
+    cluster_sync();
+    const int share = kT / cs;
+    for (int e = threadIdx.x; e < 2 * share * (D / 4); e += kThreadsB) {
+      const int g = e / (share * (D / 4)), k = rank * share + e / (D / 4) % share, p = e % (D / 4);
+      if (k >= nk) continue;
+      const uint32_t at = sb + static_cast<uint32_t>(((g * kT + k) * D + ((p ^ (k & 7)) * 4)) * 4);
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int c = 0; c < cs; ++c) {
+        const float4 y = ld_peer4(cluster_peer(at, c));
+        x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+      }
+      const float mul = g == 0 ? 1.f : a.scale;
+      void* dst = g == 0 ? a.dv : a.dk;
+      const int64_t o = ((static_cast<int64_t>(b) * a.Skv + key0 + k) * a.Hkv + hk) * D + p * 4;
+      if (a.grad_bf16) {
+        uint2 v;
+        v.x = pack_bf16x2(x.x * mul, x.y * mul);
+        v.y = pack_bf16x2(x.z * mul, x.w * mul);
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(dst) + o) = v;
+      } else {
+        *reinterpret_cast<float4*>(static_cast<float*>(dst) + o) = make_float4(x.x * mul, x.y * mul, x.z * mul, x.w * mul);
+      }
+    }
+    cluster_sync();  // no CTA leaves while another reads its shared memory
   }
 
   // ---- teardown: every thread of the CTA arrives here, aborted or not ----
@@ -833,9 +880,10 @@ __host__ __device__ constexpr int bwd_alloc() {
   return BSmem<D>::kAlloc > DqSmem<D>::kAlloc ? BSmem<D>::kAlloc : DqSmem<D>::kAlloc;
 }
 
-// Both kinds of CTA in one launch: the dk/dv CTAs from the first keys (which
-// the most causal rows reach), then the dq CTAs from the last rows, heads
-// fastest, so that long CTAs start first and short ones fill the end.
+// Both kinds of CTA in one launch: the dk/dv items from the first keys (which
+// the most causal rows reach), each taken by the CTAs of one cluster; then the
+// dq CTAs from the last rows, heads fastest, so that long CTAs start first and
+// short ones fill the end.
 template <int D, bool kCap, bool kBias>
 __global__ void __launch_bounds__(kThreadsB, 1)
     score_bwd_tc_kernel(const __grid_constant__ CUtensorMap tq64, const __grid_constant__ CUtensorMap tk,
@@ -843,16 +891,19 @@ __global__ void __launch_bounds__(kThreadsB, 1)
                         const __grid_constant__ CUtensorMap tk64, const __grid_constant__ CUtensorMap tv64,
                         const __grid_constant__ ScoreArgs a, const __grid_constant__ CapCoef cc) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const int cs = static_cast<int>(cluster_size());
   const int nkv = (a.Skv + kT - 1) / kT, nq = (a.Sq + kT - 1) / kT;
-  const int kv_ctas = nkv * a.Hkv * a.B;
+  const int kv_ctas = nkv * a.Hkv * a.B * cs;
   const int id = static_cast<int>(blockIdx.x);
+  grid_wait();  // the delta kernel's results
   if (id < kv_ctas) {
-    const int bh = id % (a.Hkv * a.B);
-    dkdv_cta<D, kCap, kBias>(tq64, tk, tv, to64, a, cc, smem_raw, bwd_alloc<D>(), id / (a.Hkv * a.B), bh % a.Hkv,
-                             bh / a.Hkv);
+    const int item = id / cs, bh = item % (a.Hkv * a.B);
+    dkdv_cta<D, kCap, kBias>(tq64, tk, tv, to64, a, cc, smem_raw, bwd_alloc<D>(), cs, id % cs, item / (a.Hkv * a.B),
+                             bh % a.Hkv, bh / a.Hkv);
   } else {
     const int i = id - kv_ctas, bh = i % (a.H * a.B);
-    dq_cta<D, kCap, kBias>(tk64, tv64, a, cc, smem_raw, bwd_alloc<D>(), nq - 1 - i / (a.H * a.B), bh % a.H, bh / a.H);
+    if (i < nq * a.H * a.B)  // the last cluster may have CTAs without work
+      dq_cta<D, kCap, kBias>(tk64, tv64, a, cc, smem_raw, bwd_alloc<D>(), nq - 1 - i / (a.H * a.B), bh % a.H, bh / a.H);
   }
 }
 
@@ -863,6 +914,7 @@ template <int D, bool kOutBf16>
 __global__ void __launch_bounds__(256) score_delta_tc_kernel(const __grid_constant__ ScoreArgs a) {
   constexpr int kLanes = D / 8;        // lanes of a row, 8 elements each
   constexpr int kRows = 256 / kLanes;  // rows a pass
+  grid_release();
   const int sub = threadIdx.x % kLanes;
   const int blk = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
   const int64_t pad0 = ((static_cast<int64_t>(b) * a.H + h) * gridDim.x + blk) * kSub;
@@ -913,14 +965,17 @@ template <int D, bool kCap, bool kBias>
 cudaError_t launch_rule(const ScoreArgs& a, const BwdMaps& m, cudaStream_t s) {
   constexpr int kAlloc = bwd_alloc<D>();
   static_assert(kAlloc <= 227 * 1024, "shared memory budget");
-  auto kernel = score_bwd_tc_kernel<D, kCap, kBias>;
   cudaError_t e = allow_smem<score_bwd_tc_kernel<D, kCap, kBias>>(kAlloc);
   if (e != cudaSuccess) return e;
-  const int64_t ctas = (static_cast<int64_t>((a.Skv + kT - 1) / kT) * a.Hkv + static_cast<int64_t>((a.Sq + kT - 1) / kT) * a.H) * a.B;
-  if (ctas > 0x7fffffff) return cudaErrorInvalidValue;
-  kernel<<<static_cast<unsigned>(ctas), kThreadsB, kAlloc, s>>>(m.q64, m.k, m.v, m.o64, m.k64, m.v64, a,
-                                                                make_cap_coef(a.scale, a.cap));
-  return cudaGetLastError();
+  const int64_t ntq = (a.Sq + kSub - 1) / kSub, ntk = (a.Skv + kSub - 1) / kSub;
+  const int64_t kv_items = static_cast<int64_t>((a.Skv + kT - 1) / kT) * a.Hkv * a.B;
+  const int64_t q_ctas = static_cast<int64_t>((a.Sq + kT - 1) / kT) * a.H * a.B;
+  // sub-steps: a dq CTA's take 3/4 of a dk/dv CTA's; some 8 of them go by before
+  // the first and after the last
+  const int cs = cluster_for(8.0, kv_items, ntq * a.G, q_ctas, ntk * 3 / 4, a.causal ? 0.5 : 1.0, false);
+  const int64_t ctas = kv_items * cs + (q_ctas + cs - 1) / cs * cs;
+  return launch_clusters(score_bwd_tc_kernel<D, kCap, kBias>, ctas / cs, cs, kThreadsB, kAlloc, a.Sq > 0, s, m.q64, m.k,
+                         m.v, m.o64, m.k64, m.v64, a, make_cap_coef(a.scale, a.cap));
 }
 
 template <int D>

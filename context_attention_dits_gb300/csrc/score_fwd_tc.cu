@@ -30,6 +30,10 @@
 // launched first, so that the short ones fill the last wave.
 // Every wait is bounded (cp_ptx.cuh); on expiry the CTA drains its copies and
 // MMAs, frees TMEM and returns.
+// A few rows against many keys (a chunk of a long prompt) are too few items for
+// the multiprocessors: then the CTAs of a cluster take equal ranges of an item's
+// key tiles, leave their (m, l, O) in shared memory, and each joins and stores
+// the rows of its share.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -63,7 +67,8 @@ struct Smem {
   static constexpr int kOffBar = kOffV + 2 * kKVTile;
   static constexpr int kNumBars = 17;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
-  static constexpr int kOffMap = kOffMisc + 24;              // act, then which tiles are mixed for query tile 0, 1
+  static constexpr int kOffStat = kOffMisc + 24;             // [256] rows' m, l (clusters)
+  static constexpr int kOffMap = kOffStat + 2 * kTileM * 8;              // act, then which tiles are mixed for query tile 0, 1
   static constexpr int kBytes = kOffMap + 3 * kMapWords * 4;
   // slack to align the base to 1024 bytes; at least 116 KB so that two CTAs
   // never share an SM (each allocates all 512 TMEM columns)
@@ -121,9 +126,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // ---- work item: a pair of query tiles (the last may be single); the pairs
   // with the most causal keys first, heads fastest ----
-  const int npair = (a.Sq + 2 * kTileM - 1) / (2 * kTileM);
-  const int bh = blockIdx.x % (a.H * a.B);
-  const int item = npair - 1 - static_cast<int>(blockIdx.x / (a.H * a.B));
+  const int cs = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
+  const int npair = (a.Sq + 2 * kTileM - 1) / (2 * kTileM), id = static_cast<int>(blockIdx.x) / cs;
+  const int bh = id % (a.H * a.B);
+  const int item = npair - 1 - id / (a.H * a.B);
   const int h = bh % a.H, b = bh / a.H, hk = h / a.G;
   const int row0 = item * 2 * kTileM;
   const int nrows = min(2 * kTileM, a.Sq - row0);
@@ -147,6 +153,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   int NT = ntile;
   if (a.qdoc) {
+    grid_wait();  // the document ranges
     const int nqb = (a.Sq + kDocBlock - 1) / kDocBlock, nkb = (a.Skv + kDocBlock - 1) / kDocBlock;
     const DocRange* qr = a.qrange + static_cast<int64_t>(b) * nqb;
     const DocRange* kr = a.krange + static_cast<int64_t>(b) * nkb;
@@ -167,6 +174,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     NT = static_cast<int>(misc[2]);
   }
   const uint32_t* bits = a.qdoc ? act : nullptr;
+  // this CTA's part of the walk: NT tiles from the n0-th on
+  const int n0 = static_cast<int>(static_cast<int64_t>(NT) * rank / cs);
+  NT = static_cast<int>(static_cast<int64_t>(NT) * (rank + 1) / cs) - n0;
   // with a bias the nearest keys weigh most: from the rows' own position
   // outwards, so that the running maximum is found first and keeps
   const int start = kBias ? min(ntile - 1, max(-1, (a.rel + row0 + nrows - 1) / kTileN)) : -1;
@@ -192,6 +202,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       load_q(0);
       TileWalk cur(bits, 0, ntile, start);
+      for (int n = 0; n < n0; ++n) cur.next();
       for (int it = 0; it < NT; ++it) {
         const int s = it & 1;
         const uint32_t ph = (it >> 1) & 1;
@@ -345,6 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int level = 0;  // of the cap's polynomial: 3, 6 terms' range, or neither
       bool ok = true;
       TileWalk cur(bits, 0, ntile, start);
+      for (int n = 0; n < n0; ++n) cur.next();
       for (int it = 0; it < NT; ++it) {
         const int kv0 = cur.t * kTileN;
         const bool mix = bits != nullptr && ((mixed[i * kMapWords + (cur.t >> 5)] >> (cur.t & 31)) & 1u);
@@ -535,11 +547,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok && NT > 0) ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar(kBarOFull + i), 0, abort_flag, a.err, tmo));
       if (ok) {
         tc_fence_after();
-        // l = 0: no key -> out 0, lse -inf
-        const float inv_l = l != 0.f ? 1.f / l : 0.f;
-        if (row < rows_valid)
-          a.lse[(static_cast<int64_t>(b) * a.H + h) * a.Sq + tok0 + row] =
-              l != 0.f ? (m_used + log2f(l)) * kLn2 : -INFINITY;
         uint32_t o[D];
         if (NT > 0) {
 #pragma unroll
@@ -549,51 +556,101 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int e = 0; e < D; ++e) o[e] = 0u;
         }
-        // 32 rows x 32 words a pass (32 fp32 columns, or 64 in bf16) staged in
-        // this tile's idle Q buffer, 128-byte swizzled, and stored 4 rows x 128
-        // contiguous bytes per warp instruction
-        const int64_t base = (static_cast<int64_t>(b) * a.Sq + tok0) * a.H + h;  // in rows of D
-        uint32_t* stage = reinterpret_cast<uint32_t*>(smem + L::kOffQ + i * L::kQTile + wq * 4096);
-        auto flush = [&](uint8_t* dst, int row_bytes) {
-          __syncwarp();
+        if (cs > 1) {
+          // this CTA's part over the idle tiles: [256 rows][D], 16-byte pieces permuted by row
+          const int r = i * kTileM + row;
+          *reinterpret_cast<float2*>(smem + L::kOffStat + r * 8) = make_float2(m_used, l);
+          float* part = reinterpret_cast<float*>(smem) + r * D;
 #pragma unroll
-          for (int pass = 0; pass < 8; ++pass) {
-            const int rr = pass * 4 + (lane >> 3), q4 = lane & 7;
-            const uint4 val = *reinterpret_cast<const uint4*>(stage + rr * 32 + ((q4 ^ (rr & 7)) * 4));
-            if (wq * 32 + rr < rows_valid)
-              *reinterpret_cast<uint4*>(dst + (base + static_cast<int64_t>(wq * 32 + rr) * a.H) * row_bytes + q4 * 16) = val;
-          }
-          __syncwarp();  // the buffer is read before it is staged again
-        };
-        if (a.out_bf16) {
-#pragma unroll
-          for (int c = 0; c < D / 64; ++c) {
-#pragma unroll
-            for (int q4 = 0; q4 < 8; ++q4) {
-              const uint32_t* oc = &o[c * 64 + 8 * q4];
-              uint4 val;
-              val.x = pack_bf16x2(u2f(oc[0]) * inv_l, u2f(oc[1]) * inv_l);
-              val.y = pack_bf16x2(u2f(oc[2]) * inv_l, u2f(oc[3]) * inv_l);
-              val.z = pack_bf16x2(u2f(oc[4]) * inv_l, u2f(oc[5]) * inv_l);
-              val.w = pack_bf16x2(u2f(oc[6]) * inv_l, u2f(oc[7]) * inv_l);
-              *reinterpret_cast<uint4*>(stage + lane * 32 + ((q4 ^ (lane & 7)) * 4)) = val;
-            }
-            flush(static_cast<uint8_t*>(a.out) + c * 128, D * 2);
-          }
+          for (int x = 0; x < D / 4; ++x)
+            *reinterpret_cast<float4*>(part + ((x ^ (r & 7)) * 4)) =
+                make_float4(u2f(o[4 * x]), u2f(o[4 * x + 1]), u2f(o[4 * x + 2]), u2f(o[4 * x + 3]));
         } else {
+          // l = 0: no key -> out 0, lse -inf
+          const float inv_l = l != 0.f ? 1.f / l : 0.f;
+          if (row < rows_valid)
+            a.lse[(static_cast<int64_t>(b) * a.H + h) * a.Sq + tok0 + row] =
+                l != 0.f ? (m_used + log2f(l)) * kLn2 : -INFINITY;
+          // 32 rows x 32 words a pass (32 fp32 columns, or 64 in bf16) staged in
+          // this tile's idle Q buffer, 128-byte swizzled, and stored 4 rows x 128
+          // contiguous bytes per warp instruction
+          const int64_t base = (static_cast<int64_t>(b) * a.Sq + tok0) * a.H + h;  // in rows of D
+          uint32_t* stage = reinterpret_cast<uint32_t*>(smem + L::kOffQ + i * L::kQTile + wq * 4096);
+          auto flush = [&](uint8_t* dst, int row_bytes) {
+            __syncwarp();
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-#pragma unroll
-            for (int q4 = 0; q4 < 8; ++q4) {
-              const uint32_t* oc = &o[c * 32 + 4 * q4];
-              const float4 val = make_float4(u2f(oc[0]) * inv_l, u2f(oc[1]) * inv_l, u2f(oc[2]) * inv_l, u2f(oc[3]) * inv_l);
-              *reinterpret_cast<float4*>(stage + lane * 32 + ((q4 ^ (lane & 7)) * 4)) = val;
+            for (int pass = 0; pass < 8; ++pass) {
+              const int rr = pass * 4 + (lane >> 3), q4 = lane & 7;
+              const uint4 val = *reinterpret_cast<const uint4*>(stage + rr * 32 + ((q4 ^ (rr & 7)) * 4));
+              if (wq * 32 + rr < rows_valid)
+                *reinterpret_cast<uint4*>(dst + (base + static_cast<int64_t>(wq * 32 + rr) * a.H) * row_bytes + q4 * 16) = val;
             }
-            flush(static_cast<uint8_t*>(a.out) + c * 128, D * 4);
+            __syncwarp();  // the buffer is read before it is staged again
+          };
+          if (a.out_bf16) {
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c) {
+#pragma unroll
+              for (int q4 = 0; q4 < 8; ++q4) {
+                const uint32_t* oc = &o[c * 64 + 8 * q4];
+                uint4 val;
+                val.x = pack_bf16x2(u2f(oc[0]) * inv_l, u2f(oc[1]) * inv_l);
+                val.y = pack_bf16x2(u2f(oc[2]) * inv_l, u2f(oc[3]) * inv_l);
+                val.z = pack_bf16x2(u2f(oc[4]) * inv_l, u2f(oc[5]) * inv_l);
+                val.w = pack_bf16x2(u2f(oc[6]) * inv_l, u2f(oc[7]) * inv_l);
+                *reinterpret_cast<uint4*>(stage + lane * 32 + ((q4 ^ (lane & 7)) * 4)) = val;
+              }
+              flush(static_cast<uint8_t*>(a.out) + c * 128, D * 2);
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+#pragma unroll
+              for (int q4 = 0; q4 < 8; ++q4) {
+                const uint32_t* oc = &o[c * 32 + 4 * q4];
+                const float4 val = make_float4(u2f(oc[0]) * inv_l, u2f(oc[1]) * inv_l, u2f(oc[2]) * inv_l, u2f(oc[3]) * inv_l);
+                *reinterpret_cast<float4*>(stage + lane * 32 + ((q4 ^ (lane & 7)) * 4)) = val;
+              }
+              flush(static_cast<uint8_t*>(a.out) + c * 128, D * 4);
+            }
           }
         }
       }
     }
+  }
+  if (cs > 1) {
+    static_assert(2 * kTileM * D * 4 <= L::kOffBar, "the parts lie over the tiles");
+    __syncwarp();
+    cluster_sync();
+    const int share = 2 * kTileM / cs;
+    for (int e = threadIdx.x; e < share * (D / 4); e += kThreads) {
+      const int r = rank * share + e / (D / 4), x = e % (D / 4);
+      if (r >= nrows) break;
+      float mx = -INFINITY, sum = 0.f;
+      for (int c = 0; c < cs; ++c) mx = fmaxf(mx, ld_peer2(cluster_peer(sb + L::kOffStat + r * 8, c)).x);
+      const float base = mx == -INFINITY ? 0.f : mx;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int c = 0; c < cs; ++c) {
+        const float2 ml = ld_peer2(cluster_peer(sb + L::kOffStat + r * 8, c));
+        const float f = ex2_approx(ml.x - base);
+        const float4 y = ld_peer4(cluster_peer(sb + (r * D + ((x ^ (r & 7)) * 4)) * 4, c));
+        sum = fmaf(ml.y, f, sum);
+        o = make_float4(fmaf(y.x, f, o.x), fmaf(y.y, f, o.y), fmaf(y.z, f, o.z), fmaf(y.w, f, o.w));
+      }
+      const float inv = sum != 0.f ? 1.f / sum : 0.f;
+      const int64_t at = ((static_cast<int64_t>(b) * a.Sq + row0 + r) * a.H + h) * D + x * 4;
+      if (a.out_bf16) {
+        uint2 v;
+        v.x = pack_bf16x2(o.x * inv, o.y * inv);
+        v.y = pack_bf16x2(o.z * inv, o.w * inv);
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + at) = v;
+      } else {
+        *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+      }
+      if (x == 0)
+        a.lse[(static_cast<int64_t>(b) * a.H + h) * a.Sq + row0 + r] = sum != 0.f ? (mx + log2f(sum)) * kLn2 : -INFINITY;
+    }
+    cluster_sync();  // no CTA leaves while another reads its shared memory
   }
 
   // ---- teardown: every thread of the CTA arrives here, aborted or not ----
@@ -611,13 +668,13 @@ cudaError_t launch_rule(const ScoreArgs& a, const CUtensorMap& tq, const CUtenso
                         cudaStream_t s) {
   using L = Smem<D>;
   static_assert(L::kAlloc <= 227 * 1024, "shared memory budget");
-  auto kernel = score_fwd_tc_kernel<D, kCap, kBias>;
   cudaError_t e = allow_smem<score_fwd_tc_kernel<D, kCap, kBias>>(L::kAlloc);
   if (e != cudaSuccess) return e;
   const int64_t items = static_cast<int64_t>((a.Sq + 2 * kTileM - 1) / (2 * kTileM)) * a.H * a.B;
-  if (items > 0x7fffffff) return cudaErrorInvalidValue;
-  kernel<<<dim3(static_cast<unsigned>(items)), kThreads, L::kAlloc, s>>>(tq, tk, tv, a, make_cap_coef(a.scale, a.cap));
-  return cudaGetLastError();
+  // steps: key tiles; some 8 of them go by before the first and after the last
+  const int cs = cluster_for(8.0, items, (a.Skv + kTileN - 1) / kTileN, 0, 0, a.causal ? 0.5 : 1.0, true);
+  return launch_clusters(score_fwd_tc_kernel<D, kCap, kBias>, items, cs, kThreads, L::kAlloc, a.qdoc != nullptr, s, tq, tk,
+                         tv, a, make_cap_coef(a.scale, a.cap));
 }
 
 template <int D>

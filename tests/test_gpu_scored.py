@@ -177,6 +177,13 @@ CASES = {
                                                    kv_docs=torch.full((1, 130), -1, dtype=torch.int32))),
     "wide": (1, 520, 1030, 6, 3, 128, dict(causal=True, q_pos0=510, softcap=50.0)),
     "five heads on one": (2, 129, 64, 5, 1, 64, dict(softcap=10.0, slopes=slopes(5))),
+    "sixteen heads on one": (1, 300, 300, 16, 1, 128, dict(causal=True, softcap=20.0)),
+    "sixteen heads on one, documents": (1, 260, 260, 16, 1, 64, dict(causal=True, q_docs=docs(1, 260, 3, 11, 5),
+                                                                     kv_docs=docs(1, 260, 3, 11, 5), slopes=slopes(16))),
+    "few rows, many keys": (1, 20, 1500, 2, 1, 128, dict(causal=True, q_pos0=1480, softcap=30.0)),
+    "few rows, many keys, documents": (1, 130, 1100, 2, 2, 64, dict(causal=True, q_pos0=970, q_docs=docs(1, 1100, 3, 5, 6)[:, 970:].contiguous(),
+                                                                    kv_docs=docs(1, 1100, 3, 5, 6))),
+    "few rows, distance": (1, 40, 900, 3, 3, 64, dict(slopes=slopes(3), q_pos0=430)),
     "no keys": (1, 9, 0, 2, 2, 64, dict(softcap=10.0)),
 }
 
