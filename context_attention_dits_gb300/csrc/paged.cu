@@ -21,7 +21,8 @@
 // states are joined at the end of a unit.
 // bf16: Q K^T and P V on m16n8k16 matrix instructions (16 query heads, 16
 // keys); the tile is far too small for a 128-row tensor-memory MMA, and the
-// instruction's rate is not what bounds it. fp32: FMAs, 8 query heads.
+// instruction's rate is not what bounds it. fp32: the same in three passes of
+// tf32, 8 query heads.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -32,6 +33,7 @@
 #include "cp_internal.h"
 #include "cp_ptx.cuh"
 #include "cp_score.h"
+#include "tf32.cuh"
 
 namespace cp {
 namespace {
@@ -53,29 +55,42 @@ __device__ __forceinline__ int cache_row(const PagedArgs& a, int b, int pos) {
 
 // ----------------------------------------------------------------------------
 // Append. A row of a token is Hkv * D elements, contiguous on both sides; TPR
-// threads share a row, each moving 16 bytes of k and of v at a time.
+// threads share a row, each moving 16 bytes of k and of v at a time. Bound by
+// HBM where there are many rows, by the launch where there are few. The first
+// pieces are on their way before the row's place is looked up (a length, then a
+// page), whose latency is as long as theirs.
 // ----------------------------------------------------------------------------
 template <int TPR>
 __global__ void __launch_bounds__(256) paged_append_kernel(const __grid_constant__ PagedArgs a, int pieces) {
   const int64_t row = static_cast<int64_t>(blockIdx.x) * (256 / TPR) + threadIdx.x / TPR;
   if (row >= static_cast<int64_t>(a.B) * a.T) return;
-  const int b = static_cast<int>(row / a.T), t = static_cast<int>(row - static_cast<int64_t>(b) * a.T);
+  const int b = static_cast<int>(row) / a.T, t = static_cast<int>(row) - b * a.T;  // B * T < 2^31
+  const int n = a.seq_lens[b];
   if (a.new_lens && t >= a.new_lens[b]) return;
-  const int64_t pos = static_cast<int64_t>(a.seq_lens[b]) + t;
-  if (a.seq_lens[b] < 0 || pos >= static_cast<int64_t>(a.max_pages) << a.page_shift) {
+  const uint4* ks = static_cast<const uint4*>(a.k_new) + row * pieces;
+  const uint4* vs = static_cast<const uint4*>(a.v_new) + row * pieces;
+  int p = threadIdx.x % TPR;
+  uint4 x, y;
+  if (p < pieces) {
+    x = ks[p];
+    y = vs[p];
+  }
+  const int64_t pos = static_cast<int64_t>(n) + t;
+  if (n < 0 || pos >= static_cast<int64_t>(a.max_pages) << a.page_shift) {
     atomicOr(a.err, kDevErrPage);
     return;
   }
   const int dst = cache_row(a, b, static_cast<int>(pos));
   if (dst < 0) return;
-  const uint4* ks = static_cast<const uint4*>(a.k_new) + row * pieces;
-  const uint4* vs = static_cast<const uint4*>(a.v_new) + row * pieces;
   uint4* kd = static_cast<uint4*>(a.k_cache) + static_cast<int64_t>(dst) * pieces;
   uint4* vd = static_cast<uint4*>(a.v_cache) + static_cast<int64_t>(dst) * pieces;
-  for (int p = threadIdx.x % TPR; p < pieces; p += TPR) {
-    const uint4 x = ks[p], y = vs[p];
+  while (p < pieces) {
     kd[p] = x;
     vd[p] = y;
+    if ((p += TPR) < pieces) {
+      x = ks[p];
+      y = vs[p];
+    }
   }
 }
 
@@ -376,19 +391,24 @@ __global__ void __launch_bounds__(kDecThreads) paged_decode_kernel(const __grid_
         }
       }
     } else {
-      // fp32: lane = (key lane % 16, half of D lane / 16) for the scores; then
-      // D / 32 columns a lane for the second product
-      constexpr int kCols = D / 32;
-      const int key = lane & 15, half = lane >> 4;
-      const float* q = static_cast<const float*>(a.q) + (static_cast<int64_t>(b) * a.H + h0) * D;
-      float o[C::kRows][kCols], mr[C::kRows], lr[C::kRows];
+      // fp32 in three passes of tf32 (tf32.cuh), keys as the rows: S^T = K Q^T
+      // (16 keys x 8 heads), then O^T = V^T P^T (D x 8 heads, 16 keys); a lane
+      // holds the statistics of heads 2 tq and 2 tq + 1
+      const int g = lane >> 2, tq = lane & 3;
+      const float* q = static_cast<const float*>(a.q) + (static_cast<int64_t>(b) * a.H + h0 + g) * D;
+      uint32_t qh[D / 8][2], ql[D / 8][2];
 #pragma unroll
-      for (int r = 0; r < C::kRows; ++r) {
-        mr[r] = -INFINITY;
-        lr[r] = 0.f;
+      for (int kk = 0; kk < D / 8; ++kk)
 #pragma unroll
-        for (int c = 0; c < kCols; ++c) o[r][c] = 0.f;
-      }
+        for (int e = 0; e < 2; ++e) split_tf32(g < nrow ? q[8 * kk + tq + 4 * e] : 0.f, qh[kk][e], ql[kk][e]);
+      float slope[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) slope[e] = a.slopes && 2 * tq + e < nrow ? a.slopes[h0 + 2 * tq + e] * kL2e : 0.f;
+      float o[D / 16][4];
+#pragma unroll
+      for (int x = 0; x < D / 16; ++x)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[x][e] = 0.f;
       int stage = 0;
       for (int blk = blk0; blk < blk1; ++blk) {
         cp_async_wait<C::kStages - 2>();
@@ -402,58 +422,73 @@ __global__ void __launch_bounds__(kDecThreads) paged_decode_kernel(const __grid_
         }
         const uint8_t* kb = wbuf + stage * 2 * C::kTile;
         const uint8_t* vb = kb + C::kTile;
-        float s[C::kRows];
+        const uint32_t on = have[warp][stage];
+        // element d of row r of a tile
+        auto at = [&](const uint8_t* tile, int r, int d) {
+          return *reinterpret_cast<const float*>(tile + r * C::kRowB + (((d >> 2) ^ (r & 7)) * 16) + (d & 3) * 4);
+        };
+        float s[4] = {0.f, 0.f, 0.f, 0.f}, small[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int r = 0; r < C::kRows; ++r) s[r] = 0.f;
-#pragma unroll 4
-        for (int p = 0; p < C::kPieces / 2; ++p) {
-          const int pp = half * (C::kPieces / 2) + p;
-          const float4 x = *reinterpret_cast<const float4*>(kb + key * C::kRowB + ((pp ^ (key & 7)) * 16));
+        for (int k0 = 0; k0 < D / 8; k0 += 4) {
+          float big[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int r = 0; r < C::kRows; ++r) {
-            if (r >= nrow) break;
-            const float4 y = *reinterpret_cast<const float4*>(q + r * D + pp * 4);
-            s[r] = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, s[r]))));
+          for (int kk = k0; kk < k0 + 4; ++kk) {
+            uint32_t ah[4], al[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) split_tf32(at(kb, g + (e & 1) * 8, 8 * kk + tq + (e >> 1) * 4), ah[e], al[e]);
+            mma3_tf32(big, small, ah, al, qh[kk], ql[kk]);
           }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[e] += big[e];
         }
-        const int j = blk * kPagedBlock + warp * kChunk + key;
-        const bool on = (have[warp][stage] >> key) & 1u;
+        // rows (keys) g and g + 8: elements 0, 1 and 2, 3; columns (heads) 2 tq, 2 tq + 1
+        const int j0 = blk * kPagedBlock + warp * kChunk + g;
+        float f[2];
 #pragma unroll
-        for (int r = 0; r < C::kRows; ++r) {
-          if (r >= nrow) break;
-          s[r] += __shfl_xor_sync(0xffffffffu, s[r], 16);
-          const float slope = a.slopes ? a.slopes[h0 + r] * kL2e : 0.f;
-          float x = -INFINITY;
-          if (on) {
-            x = s[r] * a.scale;
-            if (score.capped) x = a.cap * tanhf(x / a.cap);
-            x = fmaf(x, kL2e, -slope * static_cast<float>(n - 1 - j));
+        for (int e = 0; e < 2; ++e) {
+          float x[2], mx = -INFINITY;
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            x[u] = -INFINITY;
+            if ((on >> (g + 8 * u)) & 1u) {
+              float y = (s[2 * u + e] + small[2 * u + e]) * a.scale;
+              if (score.capped) y = a.cap * tanhf(y / a.cap);
+              x[u] = fmaf(y, kL2e, -slope[e] * static_cast<float>(n - 1 - j0 - 8 * u));
+            }
+            mx = fmaxf(mx, x[u]);
           }
-          float mx = x;
 #pragma unroll
-          for (int of = 8; of > 0; of >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, of));
-          const float mn = fmaxf(mr[r], mx), base = mn == -INFINITY ? 0.f : mn;
-          const float f = exp2f(mr[r] - base);
-          mr[r] = mn;
-          s[r] = exp2f(x - base);
-          lr[r] = lr[r] * f + s[r];  // over the lane's own keys, joined at the end
-#pragma unroll
-          for (int c = 0; c < kCols; ++c) o[r][c] *= f;
+          for (int of = 16; of > 2; of >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, of));
+          const float mn = fmaxf(m[e], mx), base = mn == -INFINITY ? 0.f : mn;
+          f[e] = exp2f(m[e] - base);
+          m[e] = mn;
+          s[e] = exp2f(x[0] - base);
+          s[2 + e] = exp2f(x[1] - base);
+          l[e] = l[e] * f[e] + s[e] + s[2 + e];
         }
-#pragma unroll 4
-        for (int kx = 0; kx < kChunk; ++kx) {
-          float y[kCols];
-          const int p = lane * kCols / 4;
-          const float* src = reinterpret_cast<const float*>(vb + kx * C::kRowB + ((p ^ (kx & 7)) * 16)) + lane * kCols % 4;
+        // P^T as the B operand: key tq (+ 4, 8, 12), head g, from lane 4 key + head / 2
+        uint32_t ph[2][2], pl[2][2];
 #pragma unroll
-          for (int c = 0; c < kCols; ++c) y[c] = src[c];
+        for (int u = 0; u < 2; ++u)
 #pragma unroll
-          for (int r = 0; r < C::kRows; ++r) {
-            if (r >= nrow) break;
-            const float w = __shfl_sync(0xffffffffu, s[r], kx);
-#pragma unroll
-            for (int c = 0; c < kCols; ++c) o[r][c] = fmaf(w, y[c], o[r][c]);
+          for (int e = 0; e < 2; ++e) {
+            const int src = (tq + 4 * e) * 4 + (g >> 1);
+            const float y0 = __shfl_sync(0xffffffffu, s[2 * u], src), y1 = __shfl_sync(0xffffffffu, s[2 * u + 1], src);
+            split_tf32(g & 1 ? y1 : y0, ph[u][e], pl[u][e]);
           }
+#pragma unroll
+        for (int x = 0; x < D / 16; ++x) {
+          float big[4] = {0.f, 0.f, 0.f, 0.f}, sm[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            uint32_t ah[4], al[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              split_tf32(at(vb, 8 * u + tq + (e >> 1) * 4, 16 * x + g + (e & 1) * 8), ah[e], al[e]);
+            mma3_tf32(big, sm, ah, al, ph[u], pl[u]);
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[x][e] = fmaf(o[x][e], f[e & 1], big[e] + sm[e]);
         }
         __syncwarp();
         if (++stage == C::kStages) stage = 0;
@@ -462,15 +497,18 @@ __global__ void __launch_bounds__(kDecThreads) paged_decode_kernel(const __grid_
       __syncwarp();
       float* w = reinterpret_cast<float*>(wbuf);
 #pragma unroll
-      for (int r = 0; r < C::kRows; ++r) {
-        float sum = lr[r];
+      for (int e = 0; e < 2; ++e) {
 #pragma unroll
-        for (int of = 8; of > 0; of >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, of);
+        for (int of = 16; of > 2; of >>= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], of);
+        const int r = 2 * tq + e;
 #pragma unroll
-        for (int c = 0; c < kCols; ++c) w[r * D + lane * kCols + c] = o[r][c];
-        if (lane == 0) {
-          w[C::kRows * D + 2 * r] = mr[r];
-          w[C::kRows * D + 2 * r + 1] = sum;
+        for (int x = 0; x < D / 16; ++x) {
+          w[r * D + 16 * x + g] = o[x][e];
+          w[r * D + 16 * x + g + 8] = o[x][2 + e];
+        }
+        if (g == 0) {
+          w[C::kRows * D + 2 * r] = m[e];
+          w[C::kRows * D + 2 * r + 1] = l[e];
         }
       }
     }
@@ -498,12 +536,12 @@ __global__ void __launch_bounds__(kDecThreads) paged_decode_kernel(const __grid_
       }
       if (whole) {
         const int64_t row = static_cast<int64_t>(b) * a.H + h0 + r;
-        const float x = sum > 0.f ? acc / sum : 0.f;
+        const float x = sum != 0.f ? acc / sum : 0.f;
         if (a.out_bf16)
           static_cast<__nv_bfloat16*>(a.out)[row * D + i % D] = __float2bfloat16(x);
         else
           static_cast<float*>(a.out)[row * D + i % D] = x;
-        if (i % D == 0) a.lse[row] = sum > 0.f ? (mx + log2f(sum)) * kLn2 : -INFINITY;
+        if (i % D == 0) a.lse[row] = sum != 0.f ? (mx + log2f(sum)) * kLn2 : -INFINITY;
       } else {
         part[i] = acc;
         if (i % D == 0) {
@@ -521,35 +559,90 @@ __global__ void __launch_bounds__(kDecThreads) paged_decode_kernel(const __grid_
 }
 
 // Joins the partials of a unit that lay in more than one CTA: the first in the
-// slot that info names, the others in slot 0 of the CTAs up to info.y.
+// slot that info names, the others in slot 0 of the CTAs up to info.y. A thread
+// per column; the partials' weights first, a thread each, then the columns with
+// eight loads under way (a dependent walk over 32 partials took 10 us).
 template <int D>
 __global__ void __launch_bounds__(D) paged_join_kernel(const __grid_constant__ PagedArgs a, int rows) {
-  const int h = blockIdx.x, b = blockIdx.y, d = threadIdx.x;
+  __shared__ float weight[kPagedCtas];
+  __shared__ float red[2][D / 32];
+  const int h = blockIdx.x, b = blockIdx.y, d = threadIdx.x, warp = d >> 5;
   grid_wait();
   if (a.seq_lens[b] <= 0) return;
   const int groups = (a.G + rows - 1) / rows;
   const int hk = h / a.G, r = (h - hk * a.G) % rows, hg = (h - hk * a.G) / rows;
   const int2 w = a.info[(static_cast<int64_t>(b) * a.Hkv + hk) * groups + hg];
   if (w.y < 0) return;
-  const int slot_floats = rows * (D + 2);
+  const int c0 = w.x >> 1, n = w.y - c0 + 1, slot_floats = rows * (D + 2);
+  auto part = [&](int i) {
+    return a.partial + (static_cast<int64_t>(c0 + i) * 2 + (i == 0 ? w.x & 1 : 0)) * slot_floats;
+  };
   float mx = -INFINITY, sum = 0.f, acc = 0.f;
-  for (int c = w.x >> 1; c <= w.y; ++c) {
-    const int slot = c == (w.x >> 1) ? w.x & 1 : 0;
-    const float* p = a.partial + (static_cast<int64_t>(c) * 2 + slot) * slot_floats;
-    const float pm = p[rows * D + 2 * r], pl = p[rows * D + 2 * r + 1], po = p[r * D + d];
-    const float mn = fmaxf(mx, pm), base = mn == -INFINITY ? 0.f : mn;
-    const float f = exp2f(mx - base), g = exp2f(pm - base);
-    sum = sum * f + pl * g;
-    acc = acc * f + po * g;
-    mx = mn;
+  auto store = [&]() {
+    const int64_t row = static_cast<int64_t>(b) * a.H + h;
+    const float x = sum != 0.f ? acc / sum : 0.f;
+    if (a.out_bf16)
+      static_cast<__nv_bfloat16*>(a.out)[row * D + d] = __float2bfloat16(x);
+    else
+      static_cast<float*>(a.out)[row * D + d] = x;
+    if (d == 0) a.lse[row] = sum != 0.f ? (mx + log2f(sum)) * kLn2 : -INFINITY;
+  };
+  if (n <= 4) {  // every load at once
+    float pm[4], pl[4], po[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      pm[i] = -INFINITY;
+      pl[i] = po[i] = 0.f;
+      if (i < n) {
+        const float2 ml = *reinterpret_cast<const float2*>(part(i) + rows * D + 2 * r);
+        pm[i] = ml.x;
+        pl[i] = ml.y;
+        po[i] = part(i)[r * D + d];
+      }
+      mx = fmaxf(mx, pm[i]);
+    }
+    const float base = mx == -INFINITY ? 0.f : mx;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float f = exp2f(pm[i] - base);
+      sum = fmaf(pl[i], f, sum);
+      acc = fmaf(po[i], f, acc);
+    }
+    store();
+    return;
   }
-  const int64_t row = static_cast<int64_t>(b) * a.H + h;
-  const float x = sum > 0.f ? acc / sum : 0.f;
-  if (a.out_bf16)
-    static_cast<__nv_bfloat16*>(a.out)[row * D + d] = __float2bfloat16(x);
-  else
-    static_cast<float*>(a.out)[row * D + d] = x;
-  if (d == 0) a.lse[row] = sum > 0.f ? (mx + log2f(sum)) * kLn2 : -INFINITY;
+  for (int i = d; i < n; i += D) {
+    weight[i] = part(i)[rows * D + 2 * r];
+    mx = fmaxf(mx, weight[i]);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  if ((d & 31) == 0) red[0][warp] = mx;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) mx = fmaxf(mx, red[0][i]);
+  const float base = mx == -INFINITY ? 0.f : mx;
+  for (int i = d; i < n; i += D) {
+    weight[i] = exp2f(weight[i] - base);
+    sum = fmaf(part(i)[rows * D + 2 * r + 1], weight[i], sum);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if ((d & 31) == 0) red[1][warp] = sum;
+  __syncthreads();
+  sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) sum += red[1][i];
+  int i = 0;
+  for (; i + 8 <= n; i += 8) {
+    float x[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) x[u] = part(i + u)[r * D + d];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) acc = fmaf(x[u], weight[i + u], acc);
+  }
+  for (; i < n; ++i) acc = fmaf(part(i)[r * D + d], weight[i], acc);
+  store();
 }
 
 template <int D, typename T>
@@ -584,13 +677,12 @@ cudaError_t launch_paged_append(const PagedArgs& a, int elem_bytes, cudaStream_t
   if (rows == 0) return cudaSuccess;
   const int pieces = a.Hkv * a.D * elem_bytes / 16;
   // threads a row: enough for one piece each, where a row has as many
-  if (pieces <= 32) {
+  if (pieces <= 32)
     paged_append_kernel<32><<<static_cast<unsigned>((rows + 7) / 8), 256, 0, s>>>(a, pieces);
-  } else if (pieces <= 64) {
+  else if (pieces <= 64)
     paged_append_kernel<64><<<static_cast<unsigned>((rows + 3) / 4), 256, 0, s>>>(a, pieces);
-  } else {
+  else
     paged_append_kernel<128><<<static_cast<unsigned>((rows + 1) / 2), 256, 0, s>>>(a, pieces);
-  }
   return cudaGetLastError();
 }
 

@@ -39,6 +39,7 @@
 
 #include "cp_ptx.cuh"
 #include "cp_score.h"
+#include "tf32.cuh"
 
 namespace cp {
 namespace {
@@ -95,30 +96,12 @@ __device__ __forceinline__ void copy_rows(float* dst, const float* src, int64_t 
   }
 }
 
-// x = hi + lo: hi rounded to tf32's 11 bits (half away from zero), so that lo has
-// either sign and what the multiplier does not read of it (2^-22 of x at most)
-// averages out over a sum.
-__device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
-  hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
-  lo = __float_as_uint(x - __uint_as_float(hi));
-}
-__device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-// big += hi hi', small += hi lo' + lo hi'. The accumulators' additions truncate,
-// which adds up along a long sum (3.9e-6 of dq over 700 keys), so big is started
-// anew every four steps and added up by rounding additions (4e-7).
 __device__ __forceinline__ void mma3(float (&big)[4], float (&small)[4], const uint32_t (&ah)[4], const uint32_t (&al)[4],
                                      float b0, float b1) {
-  uint32_t h0, l0, h1, l1;
-  split_tf32(b0, h0, l0);
-  split_tf32(b1, h1, l1);
-  mma_tf32(small, al, h0, h1);
-  mma_tf32(big, ah, h0, h1);
-  mma_tf32(small, ah, l0, l1);
+  uint32_t bh[2], bl[2];
+  split_tf32(b0, bh[0], bl[0]);
+  split_tf32(b1, bh[1], bl[1]);
+  mma3_tf32(big, small, ah, al, bh, bl);
 }
 
 // s[n][.] = 16 rows of a . rows 8 n .. 8 n + 7 of b, as accumulator fragments:
