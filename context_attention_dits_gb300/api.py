@@ -290,49 +290,55 @@ def cp_attention_bwd(q, k, v, out, dout, lse, dq, dk, dv, scale: float, ring_deg
 # ---------------------------------------------------------------------------
 # attention with a score rule, and the paged cache
 # ---------------------------------------------------------------------------
-# The current stream's handle: by torch's own accessor of it where there is one (0.1 us; a torch.cuda.Stream object
-# costs 3 us, more than the launch of a kernel).
+# A call's host time is a large part of a short one's, so the wrappers below look each thing up once, and take the
+# current stream's handle by torch's own accessor where there is one (0.1 us; a torch.cuda.Stream object costs 3 us,
+# as much as the launch of a kernel).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                       lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _place(dev, stream):
-    """The context (device, stream) that a call on tensors of `dev` runs in, or None if it is the present one: its
-    launches and the memory allocated for it belong to `stream` (None: the device's current stream)."""
-    if stream is None:
-        return None if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
-    if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream), device=dev)
-    if stream.device != dev:
-        raise ValueError(f"the stream is of {stream.device}, the tensors are on {dev}")
-    return torch.cuda.stream(stream)
+def _index(t) -> int:
+    """The CUDA device of the call's first tensor."""
+    index = t.get_device()
+    if index < 0:
+        raise ValueError("tensors must live on a CUDA device")
+    return index
 
 
-def _dense_on(dev, *ts):
+def _dense_on(index, *ts):
     for t in ts:
-        if t.device != dev:
-            raise ValueError(f"a tensor is on {t.device}, the first one on {dev}: tensors must live on one CUDA device")
+        if t.get_device() != index:
+            raise ValueError(f"a tensor is on {t.device}, the first one on cuda:{index}: all must live on one device")
         if not t.is_contiguous():
             raise ValueError("tensors must be dense")
 
 
-def _call(name, ctor, need, workspace, dev, stream):
-    """Calls ctor(workspace pointer, its bytes, raw stream) in the place that `stream` names; a workspace of `need`
-    bytes is allocated there when the caller gave none."""
-    place = _place(dev, stream)
-    if place is not None:
+def _call(fn, args, need, workspace, after, index, stream):
+    """fn(*args, workspace, its bytes, *after, stream) on `stream` (None: the current one of the tensors' device),
+    where a workspace of `need` bytes is allocated if the caller gave none; need None: the call takes no workspace."""
+    if stream is not None or torch.cuda.current_device() != index:
+        if stream is None:
+            place = torch.cuda.device(index)
+        else:
+            if not hasattr(stream, "cuda_stream"):
+                stream = torch.cuda.ExternalStream(int(stream), device=index)
+            if stream.device.index != index:
+                raise ValueError(f"the stream is of {stream.device}, the tensors are on cuda:{index}")
+            place = torch.cuda.stream(stream)
         with place:
-            return _call(name, ctor, need, workspace, dev, None)
-    ptr, size = None, 0
-    if workspace is not None:
-        _dense_on(dev, workspace)
-        ptr, size = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+            return _call(fn, args, need, workspace, after, index, None)
+    if need is None:
+        status = fn(*args, *after, _raw_stream(index))
+    elif workspace is not None:
+        _dense_on(index, workspace)
+        status = fn(*args, workspace.data_ptr(), workspace.numel() * workspace.element_size(), *after, _raw_stream(index))
     elif need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        ptr, size = workspace.data_ptr(), need
-    status = ctor(ptr, size, _raw_stream(dev.index))
+        workspace = torch.empty(need, dtype=torch.uint8, device=index)
+        status = fn(*args, workspace.data_ptr(), need, *after, _raw_stream(index))
+    else:
+        status = fn(*args, None, 0, *after, _raw_stream(index))
     if status:
-        raise CpError(status, name)
+        raise CpError(status, fn.__name__)
 
 
 def _i32(name, t, shape):
@@ -342,47 +348,30 @@ def _i32(name, t, shape):
         raise ValueError(f"{name} must have the shape {tuple(shape)}")
 
 
-def _out_dt(name, t, like) -> int:
-    if t.dtype != torch.float32 and t.dtype != like.dtype:
-        raise TypeError(f"{name} must be float32 or {like.dtype}")
-    return _DT[t.dtype]
+def _slopes(slopes, H, index):
+    if slopes.dtype != torch.float32 or slopes.shape != (H,):
+        raise ValueError("slopes must be float32 [H]")
+    _dense_on(index, slopes)
+    return slopes.data_ptr()
 
 
-def _score_rule(q, k, softcap, slopes, causal, prefix_lens, q_docs, kv_docs, q_pos0, kv_pos0):
-    B, Sq, H, _ = q.shape
-    Skv = k.shape[1]
-    dev = q.device
+def _score_rule(B, H, Sq, Skv, index, softcap, slopes, causal, prefix_lens, q_docs, kv_docs, q_pos0, kv_pos0):
     r = _lib.ScoreRule(float(softcap), None, bool(causal), None, None, None, int(q_pos0), int(kv_pos0))
     if slopes is not None:
-        if slopes.dtype != torch.float32 or slopes.shape != (H,):
-            raise ValueError("slopes must be float32 [H]")
-        _dense_on(dev, slopes)
-        r.slopes = slopes.data_ptr()
+        r.slopes = _slopes(slopes, H, index)
+    # an empty tensor has no address; no row reads it
     if prefix_lens is not None:
         _i32("prefix_lens", prefix_lens, (B,))
-        _dense_on(dev, prefix_lens)
-        r.prefix_lens = prefix_lens.data_ptr() or 256  # an empty tensor has no address; no row reads it
-    if (q_docs is None) != (kv_docs is None):
-        raise ValueError("q_docs and kv_docs come together")
-    if q_docs is not None:
+        _dense_on(index, prefix_lens)
+        r.prefix_lens = prefix_lens.data_ptr() or 256
+    if q_docs is not None or kv_docs is not None:
+        if q_docs is None or kv_docs is None:
+            raise ValueError("q_docs and kv_docs come together")
         _i32("q_docs", q_docs, (B, Sq))
         _i32("kv_docs", kv_docs, (B, Skv))
-        _dense_on(dev, q_docs, kv_docs)
+        _dense_on(index, q_docs, kv_docs)
         r.q_docs, r.kv_docs = q_docs.data_ptr() or 256, kv_docs.data_ptr() or 256
-    return r
-
-
-def _scored_shapes(q, k, v, lse):
-    _cuda(q, k, v, lse)
-    if q.dim() != 4 or k.dim() != 4:
-        raise ValueError("q must be [B, Sq, H, D], k and v [B, Skv, Hkv, D]")
-    B, Sq, H, D = q.shape
-    Skv, Hkv = k.shape[1], k.shape[2]
-    if k.shape != (B, Skv, Hkv, D) or v.shape != k.shape or lse.shape != (B, H, Sq):
-        raise ValueError("shape mismatch")
-    if k.dtype != q.dtype or v.dtype != q.dtype or lse.dtype != torch.float32:
-        raise TypeError("q, k, v must share a dtype; lse must be float32")
-    return B, Sq, H, D, Skv, Hkv
+    return ctypes.byref(r)
 
 
 def cp_scored_attn_validate(B, H, Hkv, Sq, Skv, D, scale=1.0, softcap=0.0, causal=False, prefix=False,
@@ -413,17 +402,24 @@ def cp_scored_attn_fwd(q, k, v, out, lse, scale: float, softcap: float = 0.0, sl
     Row 0 of q and of k has the position q_pos0 and kv_pos0. workspace: a CUDA tensor of at least
     cp_scored_attn_workspace_size(...) bytes; allocated here through torch when None.
     """
-    B, Sq, H, D, Skv, Hkv = _scored_shapes(q, k, v, lse)
-    if out.shape != q.shape:
+    index, dtype = _index(q), q.dtype
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q must be [B, Sq, H, D], k and v [B, Skv, Hkv, D]")
+    B, Sq, H, D = q.shape
+    _, Skv, Hkv, _ = k.shape
+    if k.shape != (B, Skv, Hkv, D) or v.shape != k.shape or out.shape != q.shape or lse.shape != (B, H, Sq):
         raise ValueError("shape mismatch")
-    dt, odt, dev = _dt(q), _out_dt("out", out, q), q.device
-    _dense_on(dev, q, k, v, out, lse)
-    r = _score_rule(q, k, softcap, slopes, causal, prefix_lens, q_docs, kv_docs, q_pos0, kv_pos0)
+    if k.dtype != dtype or v.dtype != dtype or lse.dtype != torch.float32:
+        raise TypeError("q, k, v must share a dtype; lse must be float32")
+    if out.dtype != dtype and out.dtype != torch.float32:
+        raise TypeError(f"out must be float32 or {dtype}")
+    _dense_on(index, q, k, v, out, lse)
+    rule = _score_rule(B, H, Sq, Skv, index, softcap, slopes, causal, prefix_lens, q_docs, kv_docs, q_pos0, kv_pos0)
     L = lib()
-    need = L.cp_scored_attn_workspace_size(B, H, Sq, Skv, 1) if q_docs is not None else 0
-    _call("cp_scored_attn_fwd", lambda ws, n, st: L.cp_scored_attn_fwd(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), B, H, Hkv, Sq, Skv, D,
-        float(scale), ctypes.byref(r), ws, n, dt, odt, st), need, workspace, dev, stream)
+    _call(L.cp_scored_attn_fwd, (q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), B, H, Hkv, Sq,
+                                 Skv, D, float(scale), rule),
+          0 if q_docs is None else L.cp_scored_attn_workspace_size(B, H, Sq, Skv, 1), workspace,
+          (_dt(q), _DT[out.dtype]), index, stream)
 
 
 def cp_scored_attn_bwd(q, k, v, out, dout, lse, dq, dk, dv, scale: float, softcap: float = 0.0, slopes=None,
@@ -435,33 +431,49 @@ def cp_scored_attn_bwd(q, k, v, out, dout, lse, dq, dk, dv, scale: float, softca
     For a block of a ring, out and lse are the row's results over all blocks, and the blocks' gradients add up.
     workspace: a CUDA tensor of at least cp_scored_attn_bwd_workspace_size(...) bytes; allocated here when None.
     """
-    B, Sq, H, D, Skv, Hkv = _scored_shapes(q, k, v, lse)
-    if out.shape != q.shape or dout.shape != q.shape or dq.shape != q.shape or dk.shape != k.shape or dv.shape != k.shape:
+    index, dtype = _index(q), q.dtype
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q must be [B, Sq, H, D], k and v [B, Skv, Hkv, D]")
+    qs, ks = q.shape, k.shape
+    B, Sq, H, D = qs
+    _, Skv, Hkv, _ = ks
+    if ks != (B, Skv, Hkv, D) or v.shape != ks or dk.shape != ks or dv.shape != ks or lse.shape != (B, H, Sq):
         raise ValueError("shape mismatch")
-    if dout.dtype != q.dtype or dk.dtype != dq.dtype or dv.dtype != dq.dtype:
-        raise TypeError("dout must have q's dtype; dq, dk and dv must share one")
-    dt, odt, gdt, dev = _dt(q), _out_dt("out", out, q), _out_dt("dq", dq, q), q.device
-    _dense_on(dev, q, k, v, out, dout, lse, dq, dk, dv)
-    r = _score_rule(q, k, softcap, slopes, causal, prefix_lens, q_docs, kv_docs, q_pos0, kv_pos0)
+    if out.shape != qs or dout.shape != qs or dq.shape != qs:
+        raise ValueError("shape mismatch")
+    if k.dtype != dtype or v.dtype != dtype or dout.dtype != dtype or lse.dtype != torch.float32:
+        raise TypeError("q, k, v and dout must share a dtype; lse must be float32")
+    gtype = dq.dtype
+    if dk.dtype != gtype or dv.dtype != gtype:
+        raise TypeError("dq, dk and dv must share a dtype")
+    for t in (out.dtype, gtype):
+        if t != dtype and t != torch.float32:
+            raise TypeError(f"out and the gradients must be float32 or {dtype}")
+    _dense_on(index, q, k, v, out, dout, lse, dq, dk, dv)
+    rule = _score_rule(B, H, Sq, Skv, index, softcap, slopes, causal, prefix_lens, q_docs, kv_docs, q_pos0, kv_pos0)
     L = lib()
-    need = L.cp_scored_attn_bwd_workspace_size(B, H, Sq, Skv, q_docs is not None)
-    _call("cp_scored_attn_bwd", lambda ws, n, st: L.cp_scored_attn_bwd(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), dout.data_ptr(), lse.data_ptr(), dq.data_ptr(),
-        dk.data_ptr(), dv.data_ptr(), B, H, Hkv, Sq, Skv, D, float(scale), ctypes.byref(r), ws, n, dt, odt, gdt, st),
-        need, workspace, dev, stream)
+    _call(L.cp_scored_attn_bwd, (q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), dout.data_ptr(),
+                                 lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, H, Hkv, Sq, Skv, D,
+                                 float(scale), rule),
+          L.cp_scored_attn_bwd_workspace_size(B, H, Sq, Skv, q_docs is not None), workspace,
+          (_dt(q), _DT[out.dtype], _DT[gtype]), index, stream)
 
 
-def _paged_shapes(k_cache, v_cache, block_table, seq_lens, B, Hkv, D, like):
-    _cuda(k_cache, v_cache, block_table, seq_lens)
-    if k_cache.dim() != 4 or k_cache.shape[2:] != (Hkv, D) or v_cache.shape != k_cache.shape:
+def _paged_shapes(k_cache, v_cache, block_table, seq_lens, B, Hkv, D, dtype):
+    """(num_pages, page_size, max_pages)"""
+    if k_cache.dim() != 4 or block_table.dim() != 2:
+        raise ValueError("k_cache and v_cache must be [num_pages, page_size, Hkv, D], block_table [B, max_pages]")
+    pages, page, heads, width = k_cache.shape
+    if heads != Hkv or width != D or v_cache.shape != k_cache.shape:
         raise ValueError("k_cache and v_cache must be [num_pages, page_size, Hkv, D]")
-    if k_cache.dtype != like.dtype or v_cache.dtype != like.dtype:
+    if k_cache.dtype != dtype or v_cache.dtype != dtype:
         raise TypeError("the caches must have the dtype of the other tensors")
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be [B, max_pages]")
-    _i32("block_table", block_table, (B, block_table.shape[1]))
-    _i32("seq_lens", seq_lens, (B,))
-    return k_cache.shape[0], k_cache.shape[1], block_table.shape[1]
+    rows, most = block_table.shape
+    if rows != B or seq_lens.shape != (B,):
+        raise ValueError("block_table must be [B, max_pages], seq_lens [B]")
+    if block_table.dtype != torch.int32 or seq_lens.dtype != torch.int32:
+        raise TypeError("block_table and seq_lens must be int32")
+    return pages, page, most
 
 
 def cp_paged_kv_append(k_new, v_new, k_cache, v_cache, block_table, seq_lens, new_lens=None, stream=None):
@@ -471,24 +483,22 @@ def cp_paged_kv_append(k_new, v_new, k_cache, v_cache, block_table, seq_lens, ne
     position % page of page block_table[b, position // page]. seq_lens (int32 [B], the lengths before the call) is not
     changed. A position or page out of range is skipped and reported by cp_check_device_status.
     """
-    _cuda(k_new, v_new)
+    index, dtype = _index(k_new), k_new.dtype
     if k_new.dim() != 4 or v_new.shape != k_new.shape:
         raise ValueError("k_new and v_new must be [B, T, Hkv, D]")
-    if v_new.dtype != k_new.dtype:
+    if v_new.dtype != dtype:
         raise TypeError("k_new and v_new must share a dtype")
     B, T, Hkv, D = k_new.shape
-    dt, dev = _dt(k_new), k_new.device
-    pages, page, max_pages = _paged_shapes(k_cache, v_cache, block_table, seq_lens, B, Hkv, D, k_new)
-    _dense_on(dev, k_new, v_new, k_cache, v_cache, block_table, seq_lens)
+    pages, page, most = _paged_shapes(k_cache, v_cache, block_table, seq_lens, B, Hkv, D, dtype)
+    _dense_on(index, k_new, v_new, k_cache, v_cache, block_table, seq_lens)
     news = None
     if new_lens is not None:
         _i32("new_lens", new_lens, (B,))
-        _dense_on(dev, new_lens)
+        _dense_on(index, new_lens)
         news = new_lens.data_ptr()
-    L = lib()
-    _call("cp_paged_kv_append", lambda ws, n, st: L.cp_paged_kv_append(
-        k_new.data_ptr(), v_new.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr() or 256,
-        seq_lens.data_ptr(), news, B, T, Hkv, D, pages, page, max_pages, dt, st), 0, None, dev, stream)
+    _call(lib().cp_paged_kv_append, (k_new.data_ptr(), v_new.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                                     block_table.data_ptr() or 256, seq_lens.data_ptr(), news, B, T, Hkv, D, pages,
+                                     page, most, _dt(k_new)), None, None, (), index, stream)
 
 
 def cp_paged_attn_workspace_size(B, H, Hkv, D, dtype=torch.bfloat16) -> int:
@@ -504,7 +514,7 @@ def cp_paged_attn_decode(q, k_cache, v_cache, block_table, seq_lens, out, lse, s
     gets out 0, lse -inf. workspace: a CUDA tensor of at least cp_paged_attn_workspace_size(...) bytes, one for each
     call that may run at the same time; allocated here through torch when None.
     """
-    _cuda(q, lse)
+    index, dtype = _index(q), q.dtype
     if q.dim() != 3 or k_cache.dim() != 4:
         raise ValueError("q must be [B, H, D], the caches [num_pages, page_size, Hkv, D]")
     B, H, D = q.shape
@@ -513,20 +523,15 @@ def cp_paged_attn_decode(q, k_cache, v_cache, block_table, seq_lens, out, lse, s
         raise ValueError("shape mismatch")
     if lse.dtype != torch.float32:
         raise TypeError("lse must be float32")
-    dt, odt, dev = _dt(q), _out_dt("out", out, q), q.device
-    pages, page, max_pages = _paged_shapes(k_cache, v_cache, block_table, seq_lens, B, Hkv, D, q)
-    _dense_on(dev, q, k_cache, v_cache, block_table, seq_lens, out, lse)
-    slope = None
-    if slopes is not None:
-        if slopes.dtype != torch.float32 or slopes.shape != (H,):
-            raise ValueError("slopes must be float32 [H]")
-        _dense_on(dev, slopes)
-        slope = slopes.data_ptr()
-    L = lib()
-    _call("cp_paged_attn_decode", lambda ws, n, st: L.cp_paged_attn_decode(
-        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
-        out.data_ptr(), lse.data_ptr(), B, H, Hkv, D, pages, page, max_pages, float(scale), float(softcap),
-        slope, ws, n, dt, odt, st), L.cp_paged_attn_workspace_size(B, H, Hkv, D, dt), workspace, dev, stream)
+    if out.dtype != dtype and out.dtype != torch.float32:
+        raise TypeError(f"out must be float32 or {dtype}")
+    pages, page, most = _paged_shapes(k_cache, v_cache, block_table, seq_lens, B, Hkv, D, dtype)
+    _dense_on(index, q, k_cache, v_cache, block_table, seq_lens, out, lse)
+    L, dt = lib(), _dt(q)
+    _call(L.cp_paged_attn_decode, (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
+                                   seq_lens.data_ptr(), out.data_ptr(), lse.data_ptr(), B, H, Hkv, D, pages, page, most,
+                                   float(scale), float(softcap), None if slopes is None else _slopes(slopes, H, index)),
+          L.cp_paged_attn_workspace_size(B, H, Hkv, D, dt), workspace, (dt, _DT[out.dtype]), index, stream)
 
 
 def cp_check_device_status(stream=None) -> int:

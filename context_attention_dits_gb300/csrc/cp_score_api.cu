@@ -236,15 +236,16 @@ cp_status cp_paged_kv_append(const void* k_new, const void* v_new, void* k_cache
 }
 
 // Partials of the CTAs, then which of them make up each unit.
-static size_t paged_partial_bytes(int D, cp_dtype dt) {
-  return round_up(static_cast<size_t>(cp::kPagedCtas) * 2 * cp::paged_rows(dt == CP_BF16) * (D + 2) * 4, 256);
+static size_t paged_partial_bytes(int G, int D, cp_dtype dt) {
+  const int rows = cp::paged_rows(dt == CP_BF16);
+  return round_up(static_cast<size_t>(cp::kPagedCtas) * 2 * (G < rows ? G : rows) * (D + 2) * 4, 256);
 }
 
 size_t cp_paged_attn_workspace_size(int B, int H, int Hkv, int D, cp_dtype dt) {
   if (B < 1 || H < 1 || Hkv < 1 || D < 1 || H % Hkv) return 0;
   const int rows = cp::paged_rows(dt == CP_BF16);
   const size_t groups = (H / Hkv + rows - 1) / rows;
-  return paged_partial_bytes(D, dt) + round_up(static_cast<size_t>(B) * Hkv * groups * sizeof(int2), 256);
+  return paged_partial_bytes(H / Hkv, D, dt) + round_up(static_cast<size_t>(B) * Hkv * groups * sizeof(int2), 256);
 }
 
 cp_status cp_paged_attn_decode(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
@@ -291,7 +292,7 @@ cp_status cp_paged_attn_decode(const void* q, const void* k_cache, const void* v
   a.cap = softcap;
   a.slopes = slopes;
   a.partial = static_cast<float*>(workspace);
-  a.info = reinterpret_cast<int2*>(static_cast<char*>(workspace) + paged_partial_bytes(D, dt));
+  a.info = reinterpret_cast<int2*>(static_cast<char*>(workspace) + paged_partial_bytes(a.G, D, dt));
   int sms = 0;
   if ((st = static_cast<cp_status>(cp::host_device(&a.err, &sms))) != CP_OK) return st;
   return cp::launch_paged_decode(a, dt == CP_BF16, static_cast<cudaStream_t>(stream)) == cudaSuccess ? CP_OK

@@ -138,9 +138,9 @@ struct DecCfg {
   static constexpr int kTile = kChunk * kRowB;          // a chunk's k (or v)
   static constexpr int kStages = kBf16 && D == 64 ? 4 : 3;
   static constexpr int kWarpB = kStages * 2 * kTile;    // a warp's buffers
-  static constexpr int kSlot = kRows * (D + 2);         // floats of a partial: O, then m and l
+  static constexpr int kState = kRows * (D + 2);        // floats of a warp's state: O, then m and l
   static_assert(kStages <= 4, "have");
-  static_assert(kWarpB >= kSlot * 4, "a warp's buffers hold its state at the end of a unit");
+  static_assert(kWarpB >= kState * 4, "a warp's buffers hold its state at the end of a unit");
   static constexpr int kSmem = kDecWarps * kWarpB;
   // two CTAs on a multiprocessor where their buffers fit
   static constexpr int kCtas = kSmem <= 96 * 1024 ? kPagedCtas : kPagedCtas / 2;
@@ -517,7 +517,8 @@ __global__ void __launch_bounds__(kDecThreads) paged_decode_kernel(const __grid_
     __syncthreads();
     const bool whole = blk0 == 0 && blk1 == nblk;
     const int slot = at == begin ? 0 : 1;
-    float* part = a.partial + (static_cast<int64_t>(blockIdx.x) * 2 + slot) * C::kSlot;
+    const int width = min(C::kRows, a.G);  // heads of a partial: O, then m and l
+    float* part = a.partial + (static_cast<int64_t>(blockIdx.x) * 2 + slot) * width * (D + 2);
     for (int i = threadIdx.x; i < nrow * D; i += kDecThreads) {
       const int r = i / D;
       float mw[kDecWarps], mx = -INFINITY, sum = 0.f, acc = 0.f;
@@ -545,8 +546,8 @@ __global__ void __launch_bounds__(kDecThreads) paged_decode_kernel(const __grid_
       } else {
         part[i] = acc;
         if (i % D == 0) {
-          part[C::kRows * D + 2 * r] = mx;
-          part[C::kRows * D + 2 * r + 1] = sum;
+          part[width * D + 2 * r] = mx;
+          part[width * D + 2 * r + 1] = sum;
         }
       }
     }
@@ -573,7 +574,7 @@ __global__ void __launch_bounds__(D) paged_join_kernel(const __grid_constant__ P
   const int hk = h / a.G, r = (h - hk * a.G) % rows, hg = (h - hk * a.G) / rows;
   const int2 w = a.info[(static_cast<int64_t>(b) * a.Hkv + hk) * groups + hg];
   if (w.y < 0) return;
-  const int c0 = w.x >> 1, n = w.y - c0 + 1, slot_floats = rows * (D + 2);
+  const int c0 = w.x >> 1, n = w.y - c0 + 1, width = min(rows, a.G), slot_floats = width * (D + 2);
   auto part = [&](int i) {
     return a.partial + (static_cast<int64_t>(c0 + i) * 2 + (i == 0 ? w.x & 1 : 0)) * slot_floats;
   };
@@ -594,7 +595,7 @@ __global__ void __launch_bounds__(D) paged_join_kernel(const __grid_constant__ P
       pm[i] = -INFINITY;
       pl[i] = po[i] = 0.f;
       if (i < n) {
-        const float2 ml = *reinterpret_cast<const float2*>(part(i) + rows * D + 2 * r);
+        const float2 ml = *reinterpret_cast<const float2*>(part(i) + width * D + 2 * r);
         pm[i] = ml.x;
         pl[i] = ml.y;
         po[i] = part(i)[r * D + d];
@@ -612,7 +613,7 @@ __global__ void __launch_bounds__(D) paged_join_kernel(const __grid_constant__ P
     return;
   }
   for (int i = d; i < n; i += D) {
-    weight[i] = part(i)[rows * D + 2 * r];
+    weight[i] = part(i)[width * D + 2 * r];
     mx = fmaxf(mx, weight[i]);
   }
 #pragma unroll
@@ -624,7 +625,7 @@ __global__ void __launch_bounds__(D) paged_join_kernel(const __grid_constant__ P
   const float base = mx == -INFINITY ? 0.f : mx;
   for (int i = d; i < n; i += D) {
     weight[i] = exp2f(weight[i] - base);
-    sum = fmaf(part(i)[rows * D + 2 * r + 1], weight[i], sum);
+    sum = fmaf(part(i)[width * D + 2 * r + 1], weight[i], sum);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);

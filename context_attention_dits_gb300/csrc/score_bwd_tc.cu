@@ -229,13 +229,12 @@ __device__ __forceinline__ void store_row32(void* dst, int64_t at, bool bf16, co
   }
 }
 
-// One dk/dv CTA: key tile bx of key/value head hk, batch entry b. tq64, to64: Q
-// and dO with 64-row boxes; tk, tv: K and V with 128-row boxes; smem_raw holds
-// alloc bytes of dynamic shared memory. The cs CTAs of a cluster take equal
+// One dk/dv CTA: key tile bx of key/value head hk, batch entry b. The maps have
+// 64-row boxes; smem_raw holds alloc bytes of dynamic shared memory. The cs CTAs of a cluster take equal
 // ranges of the sub-steps, and each sums the rows of its share over all of them
 // (in the order of their ranks) through distributed shared memory.
 template <int D, bool kCap, bool kBias>
-__device__ __forceinline__ void dkdv_cta(const CUtensorMap& tq64, const CUtensorMap& tk, const CUtensorMap& tv,
+__device__ __forceinline__ void dkdv_cta(const CUtensorMap& tq64, const CUtensorMap& tk64, const CUtensorMap& tv64,
                                          const CUtensorMap& to64, const ScoreArgs& a, const CapCoef& cc,
                                          uint8_t* smem_raw, int alloc, int cs, int rank, int bx, int hk, int b) {
   using L = BSmem<D>;
@@ -316,14 +315,15 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap& tq64, const CUtensor
     const bool leader = elect_one();
     if (leader) {
       tma_prefetch_desc(&tq64);
-      tma_prefetch_desc(&tk);
-      tma_prefetch_desc(&tv);
+      tma_prefetch_desc(&tk64);
+      tma_prefetch_desc(&tv64);
       tma_prefetch_desc(&to64);
       mbar_arrive_expect_tx(bar(kBarKV), 2 * L::kTile);
-      for (int c = 0; c < D / 64; ++c) {
-        tma_load_4d(sb + L::kOffK + c * (kT * 128), &tk, bar(kBarKV), c * 64, hk, key0, b);
-        tma_load_4d(sb + L::kOffV + c * (kT * 128), &tv, bar(kBarKV), c * 64, hk, key0, b);
-      }
+      for (int c = 0; c < D / 64; ++c)
+        for (int r = 0; r < kT; r += kSub) {  // two boxes of 64 rows lie as one of 128 would
+          tma_load_4d(sb + L::kOffK + c * (kT * 128) + r * 128, &tk64, bar(kBarKV), c * 64, hk, key0 + r, b);
+          tma_load_4d(sb + L::kOffV + c * (kT * 128) + r * 128, &tv64, bar(kBarKV), c * 64, hk, key0 + r, b);
+        }
     }
     int issued[kSlots] = {0, 0, 0, 0};
     HeadWalk cur(bits, t0, ntq, per_head, hk * a.G, j0);
@@ -609,8 +609,7 @@ enum : int {
   kDqBarDrain = kDqBarDone + 1,
 };
 
-// One dq CTA: query tile bx of head h, batch entry b. tk64, tv64: K and V with
-// 64-row boxes.
+// One dq CTA: query tile bx of head h, batch entry b.
 template <int D, bool kCap, bool kBias>
 __device__ __forceinline__ void dq_cta(const CUtensorMap& tk64, const CUtensorMap& tv64, const ScoreArgs& a,
                                        const CapCoef& cc, uint8_t* smem_raw, int alloc, int bx, int h, int b) {
@@ -886,8 +885,7 @@ __host__ __device__ constexpr int bwd_alloc() {
 // short ones fill the end.
 template <int D, bool kCap, bool kBias>
 __global__ void __launch_bounds__(kThreadsB, 1)
-    score_bwd_tc_kernel(const __grid_constant__ CUtensorMap tq64, const __grid_constant__ CUtensorMap tk,
-                        const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap to64,
+    score_bwd_tc_kernel(const __grid_constant__ CUtensorMap tq64, const __grid_constant__ CUtensorMap to64,
                         const __grid_constant__ CUtensorMap tk64, const __grid_constant__ CUtensorMap tv64,
                         const __grid_constant__ ScoreArgs a, const __grid_constant__ CapCoef cc) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -898,7 +896,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
   grid_wait();  // the delta kernel's results
   if (id < kv_ctas) {
     const int item = id / cs, bh = item % (a.Hkv * a.B);
-    dkdv_cta<D, kCap, kBias>(tq64, tk, tv, to64, a, cc, smem_raw, bwd_alloc<D>(), cs, id % cs, item / (a.Hkv * a.B),
+    dkdv_cta<D, kCap, kBias>(tq64, tk64, tv64, to64, a, cc, smem_raw, bwd_alloc<D>(), cs, id % cs, item / (a.Hkv * a.B),
                              bh % a.Hkv, bh / a.Hkv);
   } else {
     const int i = id - kv_ctas, bh = i % (a.H * a.B);
@@ -958,7 +956,7 @@ __global__ void __launch_bounds__(256) score_delta_tc_kernel(const __grid_consta
 }
 
 struct BwdMaps {
-  CUtensorMap q64, k, v, o64, k64, v64;
+  CUtensorMap q64, o64, k64, v64;
 };
 
 template <int D, bool kCap, bool kBias>
@@ -974,8 +972,8 @@ cudaError_t launch_rule(const ScoreArgs& a, const BwdMaps& m, cudaStream_t s) {
   // the first and after the last
   const int cs = cluster_for(8.0, kv_items, ntq * a.G, q_ctas, ntk * 3 / 4, a.causal ? 0.5 : 1.0, false);
   const int64_t ctas = kv_items * cs + (q_ctas + cs - 1) / cs * cs;
-  return launch_clusters(score_bwd_tc_kernel<D, kCap, kBias>, ctas / cs, cs, kThreadsB, kAlloc, a.Sq > 0, s, m.q64, m.k,
-                         m.v, m.o64, m.k64, m.v64, a, make_cap_coef(a.scale, a.cap));
+  return launch_clusters(score_bwd_tc_kernel<D, kCap, kBias>, ctas / cs, cs, kThreadsB, kAlloc, a.Sq > 0, s, m.q64,
+                         m.o64, m.k64, m.v64, a, make_cap_coef(a.scale, a.cap));
 }
 
 template <int D>
@@ -995,7 +993,6 @@ cudaError_t launch_d(const ScoreArgs& a, cudaStream_t s) {
   const int hq = noq ? a.Hkv : a.H, sq = noq ? a.Skv : a.Sq, hk = nok ? a.H : a.Hkv, sk = nok ? a.Sq : a.Skv;
   BwdMaps m;
   if (!host_tmap_bf16(&m.q64, q, D, hq, sq, a.B, kSub) || !host_tmap_bf16(&m.o64, o, D, hq, sq, a.B, kSub) ||
-      !host_tmap_bf16(&m.k, k, D, hk, sk, a.B, kT) || !host_tmap_bf16(&m.v, v, D, hk, sk, a.B, kT) ||
       !host_tmap_bf16(&m.k64, k, D, hk, sk, a.B, kSub) || !host_tmap_bf16(&m.v64, v, D, hk, sk, a.B, kSub))
     return cudaErrorInvalidValue;
   if (a.cap > 0.f) return a.slopes ? launch_rule<D, true, true>(a, m, s) : launch_rule<D, true, false>(a, m, s);
