@@ -533,28 +533,50 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap& tq64, const CUtensor
     static_assert(2 * kT * D * 4 <= L::kOffLse, "the parts lie over the tiles");
     __syncwarp();
     cluster_sync();
-    const int share = kT / cs;
-    for (int e = threadIdx.x; e < 2 * share * (D / 4); e += kThreadsB) {
-      const int g = e / (share * (D / 4)), k = rank * share + e / (D / 4) % share, p = e % (D / 4);
-      if (k >= nk) continue;
-      const uint32_t at = sb + static_cast<uint32_t>(((g * kT + k) * D + ((p ^ (k & 7)) * 4)) * 4);
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int c = 0; c < cs; ++c) {
-        const float4 y = ld_peer4(cluster_peer(at, c));
-        x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+    // a row's D / 4 pieces on neighbouring lanes, kIn rows a thread at once: every
+    // load of a step is under way before the first is used
+    auto join = [&](auto cs_c) {
+      constexpr int kCs = decltype(cs_c)::value, kIn = 16 / kCs;
+      constexpr int kStep = kThreadsB / (D / 4);  // rows side by side
+      const int share = kT / kCs, p = threadIdx.x % (D / 4);
+      for (int e0 = threadIdx.x / (D / 4); e0 < 2 * share; e0 += kStep * kIn) {  // dv's rows, then dk's
+        float4 y[kIn][kCs];
+#pragma unroll
+        for (int u = 0; u < kIn; ++u) {
+          const int e = min(e0 + u * kStep, 2 * share - 1), g = e / share, k = rank * share + e % share;
+#pragma unroll
+          for (int c = 0; c < kCs; ++c)
+            y[u][c] = ld_peer4(cluster_peer(sb + static_cast<uint32_t>(((g * kT + k) * D + ((p ^ (k & 7)) * 4)) * 4), c));
+        }
+#pragma unroll
+        for (int u = 0; u < kIn; ++u) {
+          const int e = e0 + u * kStep, g = e / share, k = rank * share + e % share;
+          if (e >= 2 * share) break;
+          if (k >= nk) continue;
+          float4 x = y[u][0];
+#pragma unroll
+          for (int c = 1; c < kCs; ++c) x = make_float4(x.x + y[u][c].x, x.y + y[u][c].y, x.z + y[u][c].z, x.w + y[u][c].w);
+          const float mul = g == 0 ? 1.f : a.scale;
+          void* dst = g == 0 ? a.dv : a.dk;
+          const int64_t o = ((static_cast<int64_t>(b) * a.Skv + key0 + k) * a.Hkv + hk) * D + p * 4;
+          if (a.grad_bf16) {
+            uint2 v;
+            v.x = pack_bf16x2(x.x * mul, x.y * mul);
+            v.y = pack_bf16x2(x.z * mul, x.w * mul);
+            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(dst) + o) = v;
+          } else {
+            *reinterpret_cast<float4*>(static_cast<float*>(dst) + o) =
+                make_float4(x.x * mul, x.y * mul, x.z * mul, x.w * mul);
+          }
+        }
       }
-      const float mul = g == 0 ? 1.f : a.scale;
-      void* dst = g == 0 ? a.dv : a.dk;
-      const int64_t o = ((static_cast<int64_t>(b) * a.Skv + key0 + k) * a.Hkv + hk) * D + p * 4;
-      if (a.grad_bf16) {
-        uint2 v;
-        v.x = pack_bf16x2(x.x * mul, x.y * mul);
-        v.y = pack_bf16x2(x.z * mul, x.w * mul);
-        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(dst) + o) = v;
-      } else {
-        *reinterpret_cast<float4*>(static_cast<float*>(dst) + o) = make_float4(x.x * mul, x.y * mul, x.z * mul, x.w * mul);
-      }
-    }
+    };
+    if (cs == 2)
+      join(std::integral_constant<int, 2>{});
+    else if (cs == 4)
+      join(std::integral_constant<int, 4>{});
+    else
+      join(std::integral_constant<int, 8>{});
     cluster_sync();  // no CTA leaves while another reads its shared memory
   }
 

@@ -622,34 +622,63 @@ __global__ void __launch_bounds__(kThreads, 1)
     static_assert(2 * kTileM * D * 4 <= L::kOffBar, "the parts lie over the tiles");
     __syncwarp();
     cluster_sync();
-    const int share = 2 * kTileM / cs;
-    for (int e = threadIdx.x; e < share * (D / 4); e += kThreads) {
-      const int r = rank * share + e / (D / 4), x = e % (D / 4);
-      if (r >= nrows) break;
-      float mx = -INFINITY, sum = 0.f;
-      for (int c = 0; c < cs; ++c) mx = fmaxf(mx, ld_peer2(cluster_peer(sb + L::kOffStat + r * 8, c)).x);
-      const float base = mx == -INFINITY ? 0.f : mx;
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int c = 0; c < cs; ++c) {
-        const float2 ml = ld_peer2(cluster_peer(sb + L::kOffStat + r * 8, c));
-        const float f = ex2_approx(ml.x - base);
-        const float4 y = ld_peer4(cluster_peer(sb + (r * D + ((x ^ (r & 7)) * 4)) * 4, c));
-        sum = fmaf(ml.y, f, sum);
-        o = make_float4(fmaf(y.x, f, o.x), fmaf(y.y, f, o.y), fmaf(y.z, f, o.z), fmaf(y.w, f, o.w));
+    // a row's D / 4 pieces on neighbouring lanes, kIn rows a thread at once: every
+    // load of a step is under way before the first is used
+    auto join = [&](auto cs_c) {
+      constexpr int kCs = decltype(cs_c)::value, kIn = 16 / kCs;
+      constexpr int kStep = kThreads / (D / 4);  // rows side by side
+      const int share = 2 * kTileM / kCs, x = threadIdx.x % (D / 4);
+      for (int r0 = threadIdx.x / (D / 4); r0 < share; r0 += kStep * kIn) {
+        float2 ml[kIn][kCs];
+        float4 y[kIn][kCs];
+#pragma unroll
+        for (int u = 0; u < kIn; ++u) {
+          const int r = rank * share + min(r0 + u * kStep, share - 1);
+#pragma unroll
+          for (int c = 0; c < kCs; ++c) {
+            ml[u][c] = ld_peer2(cluster_peer(sb + L::kOffStat + r * 8, c));
+            y[u][c] = ld_peer4(cluster_peer(sb + (r * D + ((x ^ (r & 7)) * 4)) * 4, c));
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < kIn; ++u) {
+          const int r = rank * share + r0 + u * kStep;
+          if (r0 + u * kStep >= share || r >= nrows) break;
+          float mx = -INFINITY, sum = 0.f;
+#pragma unroll
+          for (int c = 0; c < kCs; ++c) mx = fmaxf(mx, ml[u][c].x);
+          const float base = mx == -INFINITY ? 0.f : mx;
+          float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int c = 0; c < kCs; ++c) {
+            const float f = ex2_approx(ml[u][c].x - base);
+            sum = fmaf(ml[u][c].y, f, sum);
+            o = make_float4(fmaf(y[u][c].x, f, o.x), fmaf(y[u][c].y, f, o.y), fmaf(y[u][c].z, f, o.z),
+                            fmaf(y[u][c].w, f, o.w));
+          }
+          const float inv = sum != 0.f ? 1.f / sum : 0.f;
+          const int64_t at = ((static_cast<int64_t>(b) * a.Sq + row0 + r) * a.H + h) * D + x * 4;
+          if (a.out_bf16) {
+            uint2 v;
+            v.x = pack_bf16x2(o.x * inv, o.y * inv);
+            v.y = pack_bf16x2(o.z * inv, o.w * inv);
+            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + at) = v;
+          } else {
+            *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) =
+                make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+          }
+          if (x == 0)
+            a.lse[(static_cast<int64_t>(b) * a.H + h) * a.Sq + row0 + r] =
+                sum != 0.f ? (mx + log2f(sum)) * kLn2 : -INFINITY;
+        }
       }
-      const float inv = sum != 0.f ? 1.f / sum : 0.f;
-      const int64_t at = ((static_cast<int64_t>(b) * a.Sq + row0 + r) * a.H + h) * D + x * 4;
-      if (a.out_bf16) {
-        uint2 v;
-        v.x = pack_bf16x2(o.x * inv, o.y * inv);
-        v.y = pack_bf16x2(o.z * inv, o.w * inv);
-        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + at) = v;
-      } else {
-        *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-      }
-      if (x == 0)
-        a.lse[(static_cast<int64_t>(b) * a.H + h) * a.Sq + row0 + r] = sum != 0.f ? (mx + log2f(sum)) * kLn2 : -INFINITY;
-    }
+    };
+    if (cs == 2)
+      join(std::integral_constant<int, 2>{});
+    else if (cs == 4)
+      join(std::integral_constant<int, 4>{});
+    else
+      join(std::integral_constant<int, 8>{});
     cluster_sync();  // no CTA leaves while another reads its shared memory
   }
 
