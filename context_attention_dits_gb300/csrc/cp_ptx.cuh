@@ -112,6 +112,10 @@ __device__ __forceinline__ uint32_t cluster_size() {
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
   return r;
 }
+// The first of n things that rank's equal part of them begins with; size a power of two.
+__device__ __forceinline__ int cluster_part(int n, int rank, int size) {
+  return static_cast<int>(static_cast<int64_t>(n) * rank >> (__ffs(size) - 1));
+}
 // Every thread of every CTA of the cluster comes here; shared memory written
 // before is visible after.
 __device__ __forceinline__ void cluster_sync() {
@@ -252,6 +256,13 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
       "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
       "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
       : CP_R8(0), CP_R8(8), CP_R8(16), CP_R8(24)
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : CP_R8(0), CP_R8(8)
       : "r"(taddr));
 }
 #undef CP_R8

@@ -146,14 +146,14 @@ inline int cluster_for(double over, int64_t items_a, int64_t tiles_a, int64_t it
   return best;
 }
 
-// Launches `items` clusters of `cluster` CTAs each; `after`: the launch may start
-// while its predecessor in the stream ends (the kernel calls grid_wait).
+// Launches items x y x z clusters of `cluster` CTAs each; `after`: the launch may
+// start while its predecessor in the stream ends (the kernel calls grid_wait).
 template <typename... P, typename... A>
-cudaError_t launch_clusters(void (*kernel)(P...), int64_t items, int cluster, int threads, int smem, bool after,
-                            cudaStream_t s, const A&... args) {
-  if (items * cluster > 0x7fffffff) return cudaErrorInvalidValue;
+cudaError_t launch_clusters(void (*kernel)(P...), int64_t items, unsigned y, unsigned z, int cluster, int threads,
+                            int smem, bool after, cudaStream_t s, const A&... args) {
+  if (items * cluster > 0x7fffffff || y > 65535 || z > 65535) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(items * cluster));
+  cfg.gridDim = dim3(static_cast<unsigned>(items * cluster), y, z);
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;

@@ -271,8 +271,7 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap& tq64, const CUtensor
     per_head = walk_map(a.qrange + static_cast<int64_t>(b) * nqb, nqb,
                         doc_span(a.krange + static_cast<int64_t>(b) * nkb, nkb, bx * 2, 2), t0, ntq, act, misc + 2);
   // sub-steps: the sub-tiles of every query head, head by head; this CTA's part of them
-  const int all = per_head * a.G, j0 = static_cast<int>(static_cast<int64_t>(all) * rank / cs);
-  const int NJ = static_cast<int>(static_cast<int64_t>(all) * (rank + 1) / cs) - j0;
+  const int all = per_head * a.G, j0 = cluster_part(all, rank, cs), NJ = cluster_part(all, rank + 1, cs) - j0;
   struct HeadWalk {
     TileWalk first, w;
     int h;
@@ -994,7 +993,7 @@ cudaError_t launch_rule(const ScoreArgs& a, const BwdMaps& m, cudaStream_t s) {
   // the first and after the last
   const int cs = cluster_for(8.0, kv_items, ntq * a.G, q_ctas, ntk * 3 / 4, a.causal ? 0.5 : 1.0, false);
   const int64_t ctas = kv_items * cs + (q_ctas + cs - 1) / cs * cs;
-  return launch_clusters(score_bwd_tc_kernel<D, kCap, kBias>, ctas / cs, cs, kThreadsB, kAlloc, a.Sq > 0, s, m.q64,
+  return launch_clusters(score_bwd_tc_kernel<D, kCap, kBias>, ctas / cs, 1, 1, cs, kThreadsB, kAlloc, a.Sq > 0, s, m.q64,
                          m.o64, m.k64, m.v64, a, make_cap_coef(a.scale, a.cap));
 }
 

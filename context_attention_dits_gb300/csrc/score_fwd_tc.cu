@@ -100,9 +100,10 @@ __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, uint64
 __device__ __forceinline__ float u2f(uint32_t x) { return __uint_as_float(x); }
 
 // Holds the uses of loaded registers behind the wait that precedes it.
-__device__ __forceinline__ void tmem_pin(uint32_t (&r)[32]) {
+template <int N>
+__device__ __forceinline__ void tmem_pin(uint32_t (&r)[N]) {
 #pragma unroll
-  for (int i = 0; i < 32; i += 8)
+  for (int i = 0; i < N; i += 8)
     asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]),
                  "+r"(r[i + 6]), "+r"(r[i + 7]));
 }
@@ -126,11 +127,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // ---- work item: a pair of query tiles (the last may be single); the pairs
   // with the most causal keys first, heads fastest ----
+  // (head and rank in x, batch entry in y, pair in z: no index needs a division)
   const int cs = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
-  const int npair = (a.Sq + 2 * kTileM - 1) / (2 * kTileM), id = static_cast<int>(blockIdx.x) / cs;
-  const int bh = id % (a.H * a.B);
-  const int item = npair - 1 - id / (a.H * a.B);
-  const int h = bh % a.H, b = bh / a.H, hk = h / a.G;
+  const int h = static_cast<int>(blockIdx.x) >> (__ffs(cs) - 1), b = blockIdx.y, hk = h / a.G;
+  const int item = gridDim.z - 1 - blockIdx.z;
   const int row0 = item * 2 * kTileM;
   const int nrows = min(2 * kTileM, a.Sq - row0);
   const int nq = nrows > kTileM ? 2 : 1;
@@ -175,8 +175,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const uint32_t* bits = a.qdoc ? act : nullptr;
   // this CTA's part of the walk: NT tiles from the n0-th on
-  const int n0 = static_cast<int>(static_cast<int64_t>(NT) * rank / cs);
-  NT = static_cast<int>(static_cast<int64_t>(NT) * (rank + 1) / cs) - n0;
+  const int n0 = cluster_part(NT, rank, cs);
+  NT = cluster_part(NT, rank + 1, cs) - n0;
   // with a bias the nearest keys weigh most: from the rows' own position
   // outwards, so that the running maximum is found first and keeps
   const int start = kBias ? min(ntile - 1, max(-1, (a.rel + row0 + nrows - 1) / kTileN)) : -1;
@@ -392,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         tc_fence_after();
         uint32_t pk[kTileN / 2];
-        // P = 2^(x - m) in pairs, rounded to bf16 into pk, 32 columns at a time
+        // P = 2^(x - m) in pairs, rounded to bf16 into pk, 16 columns at a time
         // (the next columns' load is under way meanwhile); returns the row sum
         // before the rounding. kMode 1: no cap; 3, 6: the polynomial of that
         // degree, umax the largest s^2.
@@ -405,17 +405,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float bs = kBias ? (below ? slope2 : -slope2) : 0.f;
           const float bb = kBias ? fmaf(-bs, static_cast<float>(dq), -m_used) : -m_used;
           const f32x2 bs2 = pair(bs, bs), bb2 = pair(bb, bb), sl22 = pair(sl2, sl2);
-          uint32_t buf[2][32];
-          tmem_ld32(t_s, buf[0]);
+          uint32_t buf[2][16];
+          tmem_ld16(t_s, buf[0]);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t(&sr)[32] = buf[c & 1];
+          for (int c = 0; c < 8; ++c) {
+            uint32_t(&sr)[16] = buf[c & 1];
             tmem_wait_ld();
             tmem_pin(sr);
-            if (c < 3) tmem_ld32(t_s + (c + 1) * 32, buf[(c + 1) & 1]);
+            if (c < 7) tmem_ld16(t_s + (c + 1) * 16, buf[(c + 1) & 1]);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const bool on0 = !kMask || ((on[c] >> (2 * e)) & 1u), on1 = !kMask || ((on[c] >> (2 * e + 1)) & 1u);
+            for (int e = 0; e < 8; ++e) {
+              const int col = 16 * c + 2 * e;
+              const bool on0 = !kMask || ((on[c >> 1] >> (col & 31)) & 1u);
+              const bool on1 = !kMask || ((on[c >> 1] >> ((col & 31) + 1)) & 1u);
               f32x2 s2 = pair_u(sr[2 * e], sr[2 * e + 1]), fac = sl22;
               if constexpr (kMode >= 3) {
                 if (kMask) s2 = pair_u(on0 ? sr[2 * e] : 0u, on1 ? sr[2 * e + 1] : 0u);
@@ -425,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 um[e & 1] = fmax3(um[e & 1], u0, u1);
                 fac = cap_poly<kMode>(cc, u2);
               }
-              const f32x2 x2 = fma_x2(s2, fac, kBias ? fma_x2(bs2, columns(32 * c + 2 * e), bb2) : bb2);
+              const f32x2 x2 = fma_x2(s2, fac, kBias ? fma_x2(bs2, columns(col), bb2) : bb2);
               float x0, x1;
               split(x2, x0, x1);
               if (kMask) {
@@ -433,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 x1 = on1 ? x1 : -INFINITY;
               }
               const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
-              pk[16 * c + e] = pack_bf16x2(p0, p1);
+              pk[8 * c + e] = pack_bf16x2(p0, p1);
               ls[e & 1] = add_x2(ls[e & 1], pair(p0, p1));
             }
           }
@@ -479,22 +481,55 @@ __global__ void __launch_bounds__(kThreads, 1)
           float mxs = -INFINITY, um = 0.f;
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
-            const uint32_t onw = c == 0 ? on[0] : c == 1 ? on[1] : c == 2 ? on[2] : on[3];
-            const float dc = static_cast<float>(dq - 32 * c);
             uint32_t sr[32];
             tmem_ld32(t_s + c * 32, sr);
             tmem_wait_ld();
             tmem_pin(sr);
+            const uint32_t onw = c == 0 ? on[0] : c == 1 ? on[1] : c == 2 ? on[2] : on[3];
+            const f32x2 sl22 = pair(sl2, sl2);
+            bool poly = false;  // (a masked place may only cost the polynomial)
+            if (kCap) {
+              float u = 0.f;
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const float s = u2f(sr[e]);
-              float x = kCap ? cap_exact(cc, s) : s * sl2;
-              if (kBias) x = fmaf(-slope2, fabsf(dc - static_cast<float>(e)), x);
-              const bool live = (onw >> e) & 1u;
-              x = live ? x : -INFINITY;
-              if (kCap) um = fmaxf(um, live ? s * s : 0.f);
-              mxs = fmaxf(mxs, x);
-              sr[e] = __float_as_uint(x);
+              for (int e = 0; e < 32; e += 2) u = fmax3(u, fabsf(u2f(sr[e])), fabsf(u2f(sr[e + 1])));
+              um = fmaxf(um, u * u);
+              poly = __all_sync(0xffffffffu, u * u <= cc.u3);
+            }
+            const float dc = static_cast<float>(dq - 32 * c);
+            if (kBias && !kCap) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                float x = fmaf(-slope2, fabsf(dc - static_cast<float>(e)), u2f(sr[e]) * sl2);
+                x = (onw >> e) & 1u ? x : -INFINITY;
+                mxs = fmaxf(mxs, x);
+                sr[e] = __float_as_uint(x);
+              }
+            } else {
+              if (!kCap || poly) {
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) {
+                  const f32x2 s2 = pair_u(sr[e], sr[e + 1]);
+                  float x0, x1;
+                  split(mul_x2(s2, kCap ? cap_poly<3>(cc, mul_x2(s2, s2)) : sl22), x0, x1);
+                  sr[e] = __float_as_uint(x0);
+                  sr[e + 1] = __float_as_uint(x1);
+                }
+              } else {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) sr[e] = __float_as_uint(cap_exact(cc, u2f(sr[e])));
+              }
+              if (kBias) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  sr[e] = __float_as_uint(fmaf(-slope2, fabsf(dc - static_cast<float>(e)), u2f(sr[e])));
+              }
+              if (masked) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  if (!((onw >> e) & 1u)) sr[e] = __float_as_uint(-INFINITY);
+              }
+#pragma unroll
+              for (int e = 0; e < 32; e += 2) mxs = fmax3(mxs, u2f(sr[e]), u2f(sr[e + 1]));
             }
             tmem_st32(t_s + c * 32, sr);
           }
@@ -509,21 +544,27 @@ __global__ void __launch_bounds__(kThreads, 1)
             m_used = mxs;
           }
           const float nm = m_used == -INFINITY ? 0.f : -m_used;
-          lsum = 0.f;
+          f32x2 ls[2] = {0ull, 0ull};
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
             uint32_t sr[32], pw[16];
             tmem_ld32(t_s + c * 32, sr);
             tmem_wait_ld();
             tmem_pin(sr);
+            const f32x2 nm2 = pair(nm, nm);
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              const float p0 = ex2_approx(u2f(sr[2 * e]) + nm), p1 = ex2_approx(u2f(sr[2 * e + 1]) + nm);
+              float x0, x1;
+              split(add_x2(pair_u(sr[2 * e], sr[2 * e + 1]), nm2), x0, x1);
+              const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
               pw[e] = pack_bf16x2(p0, p1);
-              lsum += p0 + p1;
+              ls[e & 1] = add_x2(ls[e & 1], pair(p0, p1));
             }
             tmem_st16(t_s + c * 16, pw);
           }
+          float l0, l1;
+          split(add_x2(ls[0], ls[1]), l0, l1);
+          lsum = l0 + l1;
           if (it > 0 && __any_sync(0xffffffffu, need)) {
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
@@ -544,6 +585,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(bar(kBarPFull + i));
         cur.next();
       }
+      // l = 0: no key -> out 0, lse -inf (found while the last product runs)
+      const float inv_l = l != 0.f ? 1.f / l : 0.f;
+      const float lse_v = l != 0.f ? (m_used + log2f(l)) * kLn2 : -INFINITY;
       if (ok && NT > 0) ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar(kBarOFull + i), 0, abort_flag, a.err, tmo));
       if (ok) {
         tc_fence_after();
@@ -566,11 +610,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             *reinterpret_cast<float4*>(part + ((x ^ (r & 7)) * 4)) =
                 make_float4(u2f(o[4 * x]), u2f(o[4 * x + 1]), u2f(o[4 * x + 2]), u2f(o[4 * x + 3]));
         } else {
-          // l = 0: no key -> out 0, lse -inf
-          const float inv_l = l != 0.f ? 1.f / l : 0.f;
-          if (row < rows_valid)
-            a.lse[(static_cast<int64_t>(b) * a.H + h) * a.Sq + tok0 + row] =
-                l != 0.f ? (m_used + log2f(l)) * kLn2 : -INFINITY;
+          if (row < rows_valid) a.lse[(static_cast<int64_t>(b) * a.H + h) * a.Sq + tok0 + row] = lse_v;
           // 32 rows x 32 words a pass (32 fp32 columns, or 64 in bf16) staged in
           // this tile's idle Q buffer, 128-byte swizzled, and stored 4 rows x 128
           // contiguous bytes per warp instruction
@@ -702,7 +742,7 @@ cudaError_t launch_rule(const ScoreArgs& a, const CUtensorMap& tq, const CUtenso
   const int64_t items = static_cast<int64_t>((a.Sq + 2 * kTileM - 1) / (2 * kTileM)) * a.H * a.B;
   // steps: key tiles; some 8 of them go by before the first and after the last
   const int cs = cluster_for(8.0, items, (a.Skv + kTileN - 1) / kTileN, 0, 0, a.causal ? 0.5 : 1.0, true);
-  return launch_clusters(score_fwd_tc_kernel<D, kCap, kBias>, items, cs, kThreads, L::kAlloc, a.qdoc != nullptr, s, tq, tk,
+  return launch_clusters(score_fwd_tc_kernel<D, kCap, kBias>, a.H, a.B, (a.Sq + 2 * kTileM - 1) / (2 * kTileM), cs, kThreads, L::kAlloc, a.qdoc != nullptr, s, tq, tk,
                          tv, a, make_cap_coef(a.scale, a.cap));
 }
 
