@@ -28,6 +28,12 @@ bool known(cp_dtype t) { return t == CP_BF16 || t == CP_F32; }
 // An output is fp32 or of the inputs' type.
 bool out_type_ok(cp_dtype out, cp_dtype in) { return known(out) && (out == CP_F32 || out == in); }
 
+// A scale and a cap whose quotient and coefficients fp32 holds.
+bool scores_ok(float scale, float softcap) {
+  if (!std::isfinite(scale) || !std::isfinite(softcap) || softcap < 0.f) return false;
+  return softcap == 0.f || (softcap >= 1e-30f && softcap >= std::fabs(scale) * 1e-30f);
+}
+
 const cp_score_rule kPlainRule = {0.f, nullptr, 0, nullptr, nullptr, nullptr, 0, 0};
 
 int64_t doc_blocks(int S) { return (static_cast<int64_t>(S) + cp::kDocBlock - 1) / cp::kDocBlock; }
@@ -98,7 +104,7 @@ cp_status cp_scored_attn_validate(int B, int H, int Hkv, int Sq, int Skv, int D,
   const cp_score_rule& r = rule ? *rule : kPlainRule;
   if (B < 0 || H < 1 || Hkv < 1 || Sq < 0 || Skv < 0 || (D != 64 && D != 128) || !known(dt)) return CP_ERR_INVALID_ARG;
   if (B > kMaxGrid || H > kMaxGrid || Sq > cp::kScoreMaxTokens || Skv > cp::kScoreMaxTokens) return CP_ERR_INVALID_ARG;
-  if (!std::isfinite(scale) || !std::isfinite(r.softcap) || r.softcap < 0.f) return CP_ERR_INVALID_ARG;
+  if (!scores_ok(scale, r.softcap)) return CP_ERR_INVALID_ARG;
   if (r.q_pos0 < 0 || r.kv_pos0 < 0 || r.q_pos0 > kMaxPos || r.kv_pos0 > kMaxPos) return CP_ERR_INVALID_ARG;
   if ((r.q_docs == nullptr) != (r.kv_docs == nullptr)) return CP_ERR_INVALID_ARG;
   if (r.prefix_lens && !r.causal) return CP_ERR_UNSUPPORTED_COMBO;
@@ -258,7 +264,7 @@ cp_status cp_paged_attn_decode(const void* q, const void* k_cache, const void* v
   cp_status st = check_paged(B, Hkv, D, num_pages, page_size, max_pages, dt, &a.page_shift);
   if (st != CP_OK) return st;
   if (H < 1 || H > kMaxGrid || !out_type_ok(out_dt, dt)) return CP_ERR_INVALID_ARG;
-  if (!std::isfinite(scale) || !std::isfinite(softcap) || softcap < 0.f) return CP_ERR_INVALID_ARG;
+  if (!scores_ok(scale, softcap)) return CP_ERR_INVALID_ARG;
   if (H % Hkv) return CP_ERR_NOT_DIVISIBLE;
   const int rows = cp::paged_rows(dt == CP_BF16), groups = (H / Hkv + rows - 1) / rows;
   // the list of 64-key blocks is indexed in 32 bits

@@ -146,16 +146,13 @@ struct DecCfg {
   static constexpr int kCtas = kSmem <= 96 * 1024 ? kPagedCtas : kPagedCtas / 2;
 };
 
-// log2 of the score's weight: the cap's tanh from the exponential,
-// tanh z = 1 - 2 / (1 + e^2z); its error is ~2^-23 absolute, which is what the
-// exponent needs.
+// A score in units of log2, dist keys back.
 struct DecScore {
-  float a0, capl2, sl2;  // scale (times 2 log2 e / cap if capped, log2 e otherwise); cap * log2 e; slope * log2 e
-  bool capped;
-  __device__ __forceinline__ float operator()(float dot, float slope, float dist) const {
-    float y = dot * a0;
-    if (capped) y = capl2 * (1.f - __fdividef(2.f, 1.f + ex2_approx(y)));
-    return fmaf(-slope, dist, y);
+  float scale, cap, inv_cap;
+  __device__ __forceinline__ float operator()(float dot, float slope2, float dist) const {
+    float x = dot * scale;
+    if (cap > 0.f) x = cap * tanhf(x * inv_cap);
+    return fmaf(x, kL2e, -slope2 * dist);
   }
 };
 
@@ -221,9 +218,9 @@ __global__ void __launch_bounds__(kDecThreads) paged_decode_kernel(const __grid_
   const uint32_t wb = smem_addr(wbuf);
   const int64_t tok_b = static_cast<int64_t>(a.Hkv) * C::kRowB;  // bytes of a token's row of all heads
   DecScore score;
-  score.capped = a.cap > 0.f;
-  score.a0 = a.scale * (score.capped ? 2.f * kL2e / a.cap : kL2e);
-  score.capl2 = a.cap * kL2e;
+  score.scale = a.scale;
+  score.cap = a.cap;
+  score.inv_cap = a.cap > 0.f ? 1.f / a.cap : 0.f;
 
   int b = 0;
   {  // the sequence of the first block
@@ -451,9 +448,7 @@ __global__ void __launch_bounds__(kDecThreads) paged_decode_kernel(const __grid_
           for (int u = 0; u < 2; ++u) {
             x[u] = -INFINITY;
             if ((on >> (g + 8 * u)) & 1u) {
-              float y = (s[2 * u + e] + small[2 * u + e]) * a.scale;
-              if (score.capped) y = a.cap * tanhf(y / a.cap);
-              x[u] = fmaf(y, kL2e, -slope[e] * static_cast<float>(n - 1 - j0 - 8 * u));
+              x[u] = score(s[2 * u + e] + small[2 * u + e], slope[e], static_cast<float>(n - 1 - j0 - 8 * u));
             }
             mx = fmaxf(mx, x[u]);
           }

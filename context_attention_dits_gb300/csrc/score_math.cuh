@@ -13,6 +13,7 @@
 
 #include <cuda_runtime.h>
 
+#include <cmath>
 #include <cstdint>
 #include <cstring>
 
@@ -77,22 +78,34 @@ inline CapCoef make_cap_coef(float scale, float cap) {
     std::memcpy(&u, &f, 4);
     return static_cast<f32x2>(u) << 32 | u;
   };
-  // a coefficient that fp32 cannot hold to full precision rules its polynomial out
-  bool ok3 = true, ok6 = true;
-  double pw = r;
+  // Coefficients below fp32's normal numbers (a wide cap) become 0, and their
+  // polynomial then serves only the x for which they do not count; one above its
+  // range (a narrow cap) rules its polynomial out. x3, x6: the largest x^2.
+  double x3 = 0.25, x6 = 1.0, pw = r;
   for (int k = 0; k < 7; ++k, pw *= r * r) {
-    const double x = cap * l2e * pw, ax = x < 0 ? -x : x;
-    const bool fits = r == 0.0 || (ax > 1e-30 && ax < 1e30);
-    if (k < 4) {
-      c.p3[k] = twice(x * t3[k]);
-      ok3 = ok3 && fits;
-    }
-    c.p6[k] = twice(x * t6[k]);
-    ok6 = ok6 && fits;
+    const double x = cap * l2e * pw;
+    auto put = [&](const double* t, int deg, f32x2* p, double* most) {
+      if (k > deg) return;
+      double v = x * t[k];
+      const double av = v < 0 ? -v : v;
+      if (av < 2e-38 && r != 0.0 && k > 0) {
+        v = 0.0;
+        const double only = std::pow(1e-7 / std::fabs(t[k]), 1.0 / k);
+        if (only < *most) *most = only;
+      }
+      if (av > 1e38) *most = -1.0;
+      p[k] = twice(v);
+    };
+    put(t3, 3, c.p3, &x3);
+    put(t6, 6, c.p6, &x6);
   }
-  const double lim = r != 0.0 ? 1.0 / (r * r) : 3e38;
-  c.u3 = ok3 ? static_cast<float>(lim * 0.25 < 3e38 ? lim * 0.25 : 3e38) : -1.f;
-  c.u6 = ok6 ? static_cast<float>(lim < 3e38 ? lim : 3e38) : -1.f;
+  auto limit = [&](double most) {
+    if (most < 0) return -1.f;
+    const double u = r != 0.0 ? most / (r * r) : 3e38;
+    return static_cast<float>(u < 3e38 ? u : 3e38);
+  };
+  c.u3 = limit(x3);
+  c.u6 = limit(x6);
   c.a0 = static_cast<float>(2.0 * l2e * r);
   c.capl2 = static_cast<float>(cap * l2e);
   return c;

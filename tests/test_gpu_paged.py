@@ -109,7 +109,7 @@ def test_decode(name, H, Hkv, D, page, dt, out_dt):
 
 
 @pytest.mark.parametrize("dt", [BF, F4])
-@pytest.mark.parametrize("cap,bias", [(30.0, False), (0.5, False), (0.0, True), (20.0, True)])
+@pytest.mark.parametrize("cap,bias", [(30.0, False), (0.5, False), (0.0, True), (20.0, True), (1e5, False)])
 def test_decode_score_rule(dt, cap, bias):
     H, Hkv, D = 8, 2, 64
     s = make([700, 33, 1, 200], H, Hkv, D, 16, dt, seed=3)

@@ -153,6 +153,9 @@ CASES = {
     "plain, shared heads": (2, 70, 70, 4, 2, 64, {}),
     "cap": (1, 130, 130, 2, 2, 128, dict(softcap=30.0)),
     "tight cap": (1, 97, 97, 2, 1, 64, dict(softcap=0.75)),
+    "narrow cap": (1, 140, 140, 2, 2, 128, dict(softcap=1e-3, causal=True)),
+    "wide cap": (1, 300, 300, 2, 2, 128, dict(softcap=1e5, causal=True)),
+    "cap without effect": (1, 140, 140, 2, 2, 64, dict(softcap=1e30)),
     "bias both ways": (1, 200, 200, 3, 3, 64, dict(slopes=slopes(3))),
     "negative slope": (1, 65, 129, 2, 2, 128, dict(slopes=torch.tensor([-0.01, 0.02]), softcap=5.0)),
     "causal": (2, 257, 257, 2, 1, 128, dict(causal=True)),
@@ -206,7 +209,7 @@ def test_large_scores_and_growing_maxima(dt):
     B, S, H, D = 1, 390, 2, 64
     q, k, v, dout = draw(B, S, S, H, H, D, dt, seed=5)
     k = (k.float() * torch.linspace(0.1, 12.0, S)[None, :, None, None]).to(dt)
-    for rule in ({}, dict(softcap=40.0), dict(causal=True, slopes=torch.tensor([0.3, -0.2]))):
+    for rule in ({}, dict(softcap=40.0), dict(softcap=2000.0), dict(causal=True, slopes=torch.tensor([0.3, -0.2]))):
         out, lse = run_fwd(q, k, v, 0.6, rule, dt)
         check_fwd(q, k, v, 0.6, rule, out, lse, f"growing {sorted(rule)}")
         grads = run_bwd(q, k, v, out, dout, lse, 0.6, rule, dt)

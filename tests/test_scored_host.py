@@ -27,7 +27,7 @@ def test_validate():
     assert f() == 0 and f(Sq=0, Skv=0, B=0) == 0 and f(softcap=30.0, causal=True, prefix=True, dtype=torch.float32) == 0
     for bad in (dict(D=96), dict(B=-1), dict(H=0), dict(Hkv=0), dict(Sq=-1), dict(Skv=-1), dict(B=65536), dict(H=65536),
                 dict(Sq=(1 << 21) + 1), dict(Skv=(1 << 21) + 1), dict(scale=float("nan")), dict(scale=float("inf")),
-                dict(softcap=-1.0), dict(softcap=float("nan")), dict(q_pos0=-1), dict(kv_pos0=(1 << 30) + 1)):
+                dict(softcap=-1.0), dict(softcap=float("nan")), dict(softcap=1e-31), dict(scale=1e25, softcap=1e-6), dict(q_pos0=-1), dict(kv_pos0=(1 << 30) + 1)):
         assert f(**bad) == _lib.CP_ERR_INVALID_ARG, bad
     assert f(H=7) == _lib.CP_ERR_NOT_DIVISIBLE
     assert f(prefix=True) == _lib.CP_ERR_UNSUPPORTED_COMBO
