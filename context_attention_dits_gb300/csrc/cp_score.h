@@ -40,7 +40,7 @@ struct ScoreArgs {
   void* out;             // forward
   float* lse;            // forward: written; backward: read
   float* delta;          // backward, fp32 inputs: [B, H, Sq]
-  float* lse2p;          // backward, bf16: lse log2e and delta, each (batch entry, head) padded to 64 rows
+  float* lse2p;          // backward, bf16: -lse log2e and delta, each (batch entry, head) padded to 64 rows
   float* dltp;
   void *dq, *dk, *dv;
   int out_bf16;   // type of out

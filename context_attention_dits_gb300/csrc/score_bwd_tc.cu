@@ -19,9 +19,9 @@
 //     a limit or a document border cuts, and forms y and its derivative by the
 //     cap's polynomial (score_math.cuh) while the warp's scores stay in its
 //     range, exactly otherwise;
-//   * lse log2e and delta come from copies padded to 64 rows a (batch entry,
+//   * -lse log2e and delta come from copies padded to 64 rows a (batch entry,
 //     head), written by the delta kernel, so that a sub-tile's are one aligned
-//     bulk copy. Rows past the end, and rows that saw no key, hold +inf: p = 0.
+//     bulk copy. Rows past the end, and rows that saw no key, hold -inf: p = 0.
 // P and dS are rounded to bf16 for their products; all sums are fp32.
 // Warp roles (320 threads): 0 = TMA producer, 1 = MMA issuer, 2-9 = row warps,
 // two per TMEM lane quarter, one per 32-column half of a sub-step.
@@ -73,7 +73,7 @@ struct BSmem {
   static constexpr int kOffV = kOffK + kTile;
   static constexpr int kOffQ = kOffV + kTile;            // kSlots sub-tiles
   static constexpr int kOffO = kOffQ + kSlots * kSubT;   // dO, kSlots sub-tiles
-  static constexpr int kOffLse = kOffO + kSlots * kSubT;     // kSlots x 64 floats: lse * log2 e
+  static constexpr int kOffLse = kOffO + kSlots * kSubT;     // kSlots x 64 floats: -lse log2 e
   static constexpr int kOffDlt = kOffLse + kSlots * kSub * 4; // kSlots x 64 floats: delta
   static constexpr int kOffBar = kOffDlt + kSlots * kSub * 4;
   static constexpr int kNumBars = 15;
@@ -140,14 +140,17 @@ __device__ __forceinline__ int walk_map(const DocRange* other, int nblk, const D
   return static_cast<int>(*count);
 }
 
-// 32 scores of a row pass: p in place of s and ds in place of dp, packed as
+// 32 scores of a row pass: p in place of s and -ds in place of dp, packed as
 // bf16 pairs. Element e has the distance |d0 + step e| (step +1 or -1);
-// nl(e) = -lse log2e and nd(e) = -delta of its row; on: the pairs that take part.
+// nl(e) = -lse log2e and dl(e) = delta of its row; on: the pairs that take part.
+// The signs are such that no packed operand has to be negated (an instruction
+// each): -ds = p (delta - dp), or with a cap p (delta - dp)(1 - tanh^2) from
+// p (dp - delta)(tanh^2 - 1); the epilogues multiply by -scale.
 template <bool kCap, bool kBias, int kStep, typename NL, typename ND>
 __device__ __forceinline__ void row_pass(const uint32_t (&sr)[32], const uint32_t (&dr)[32], const CapCoef& cc,
-                                         float c2, float inv2, float slope2, float d0, uint32_t on, NL nl, ND nd,
+                                         float c2, float capl2, float slope2, float d0, uint32_t on, NL nl, ND dl,
                                          uint32_t (&pp)[16], uint32_t (&dd)[16]) {
-  const f32x2 c22 = pair(c2, c2), inv22 = pair(inv2, inv2), one2 = pair(1.f, 1.f);
+  const f32x2 c22 = pair(c2, c2), cap2 = pair(capl2, capl2), minus = pair(-1.f, -1.f);
   // kHow: 0 no cap, 3 and 6 the polynomials, 1 exact
   auto pass = [&](auto how_c) {
     constexpr int kHow = decltype(how_c)::value;
@@ -159,25 +162,25 @@ __device__ __forceinline__ void row_pass(const uint32_t (&sr)[32], const uint32_
         const float a0 = fabsf(d0 + static_cast<float>(kStep * e)), a1 = fabsf(d0 + static_cast<float>(kStep * (e + 1)));
         b2 = fma_x2(pair(-slope2, -slope2), pair(a0, a1), b2);
       }
-      f32x2 t2, c1 = one2;
+      const f32x2 dp2 = pair_u(dr[e], dr[e + 1]);
+      f32x2 t2, q2;
       if constexpr (kHow == 0) {
         t2 = fma_x2(s2, c22, b2);
+        q2 = fma_x2(dp2, minus, dl(e));
       } else {
-        f32x2 y2;
+        f32x2 th;  // tanh
         if constexpr (kHow >= 3) {
-          y2 = mul_x2(s2, cap_poly<kHow>(cc, mul_x2(s2, s2)));
+          th = mul_x2(s2, cap_poly<kHow>(cc, mul_x2(s2, s2)));
         } else {
-          y2 = pair(cap_exact(cc, u2f(sr[e])), cap_exact(cc, u2f(sr[e + 1])));
+          th = pair(cap_exact(cc, u2f(sr[e])), cap_exact(cc, u2f(sr[e + 1])));
         }
-        c1 = fma_x2(mul_x2(y2, y2), inv22, one2);  // 1 - (y / cap)^2; inv2 = -1 / (cap log2e)^2
-        t2 = add_x2(y2, b2);
+        t2 = fma_x2(th, cap2, b2);
+        q2 = mul_x2(fma_x2(dl(e), minus, dp2), fma_x2(th, th, minus));
       }
-      const f32x2 g2 = add_x2(pair_u(dr[e], dr[e + 1]), nd(e));
       float t0, t1;
       split(t2, t0, t1);
       const float p0 = ex2_approx(t0), p1 = ex2_approx(t1);
-      f32x2 q2 = mul_x2(pair(p0, p1), g2);
-      if constexpr (kHow != 0) q2 = mul_x2(q2, c1);
+      q2 = mul_x2(pair(p0, p1), q2);
       float q0, q1;
       split(q2, q0, q1);
       pp[e >> 1] = pack_bf16x2(p0, p1);
@@ -447,7 +450,7 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap& tq64, const CUtensor
     const int key = wq * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
     const bool kvalid = key < nk;
-    const float c2 = a.scale * kLog2e, inv2 = kCap ? -1.f / (cc.capl2 * cc.capl2) : 0.f;
+    const float c2 = a.scale * kLog2e, capl2 = a.cap * kLog2e;
     const int jkey = key0 + key;
     const bool open = !a.causal || jkey < plim;  // every row may see this key
     const int kd = a.qdoc && kvalid ? a.kdoc[static_cast<int64_t>(b) * a.Skv + jkey] : -1;
@@ -478,18 +481,12 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap& tq64, const CUtensor
       tmem_wait_ld();
       tmem_pin(sr);
       tmem_pin(dr);
-      const float* lse2 = s_lse + q * kSub + hc * 32;
+      const float* nlse2 = s_lse + q * kSub + hc * 32;
       const float* dlt = s_dlt + q * kSub + hc * 32;
       row_pass<kCap, kBias, 1>(
-          sr, dr, cc, c2, inv2, slope2, static_cast<float>(d0), on,
-          [&](int e) {
-            const float2 v = *reinterpret_cast<const float2*>(lse2 + e);
-            return pair(-v.x, -v.y);
-          },
-          [&](int e) {
-            const float2 v = *reinterpret_cast<const float2*>(dlt + e);
-            return pair(-v.x, -v.y);
-          },
+          sr, dr, cc, c2, capl2, slope2, static_cast<float>(d0), on,
+          [&](int e) { return *reinterpret_cast<const f32x2*>(nlse2 + e); },
+          [&](int e) { return *reinterpret_cast<const f32x2*>(dlt + e); },
           pp, dd);
       // P^T over the first half of this warp's S^T columns, dS^T over those of dP^T
       tmem_st16(t_s, pp);
@@ -523,7 +520,7 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap& tq64, const CUtensor
             *reinterpret_cast<float4*>(part + (((c * 8 + x) ^ (key & 7)) * 4)) =
                 make_float4(u2f(r[4 * x]), u2f(r[4 * x + 1]), u2f(r[4 * x + 2]), u2f(r[4 * x + 3]));
         } else if (kvalid) {
-          store_row32(g == 0 ? a.dv : a.dk, at + c * 32, a.grad_bf16, r, g == 0 ? 1.f : a.scale);
+          store_row32(g == 0 ? a.dv : a.dk, at + c * 32, a.grad_bf16, r, g == 0 ? 1.f : -a.scale);
         }
       }
     }
@@ -555,7 +552,7 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap& tq64, const CUtensor
           float4 x = y[u][0];
 #pragma unroll
           for (int c = 1; c < kCs; ++c) x = make_float4(x.x + y[u][c].x, x.y + y[u][c].y, x.z + y[u][c].z, x.w + y[u][c].w);
-          const float mul = g == 0 ? 1.f : a.scale;
+          const float mul = g == 0 ? 1.f : -a.scale;
           void* dst = g == 0 ? a.dv : a.dk;
           const int64_t o = ((static_cast<int64_t>(b) * a.Skv + key0 + k) * a.Hkv + hk) * D + p * 4;
           if (a.grad_bf16) {
@@ -792,13 +789,13 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap& tk64, const CUtensorMa
     const int hc = (warp - 2) >> 2;  // this warp's 32 key columns of each sub-step
     const int row = wq * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
-    const float c2 = a.scale * kLog2e, inv2 = kCap ? -1.f / (cc.capl2 * cc.capl2) : 0.f;
-    // the row's lse log2e and delta, from the padded copies (a row past the end holds +inf, 0)
-    float nl2 = -INFINITY, ndl = 0.f;
+    const float c2 = a.scale * kLog2e, capl2 = a.cap * kLog2e;
+    // the row's -lse log2e and delta, from the padded copies (a row past the end holds -inf, 0)
+    float nl2 = -INFINITY, dlt = 0.f;
     if (row < nq) {
       const int64_t o = (static_cast<int64_t>(b) * a.H + h) * nqb * kDocBlock + q0 + row;
-      nl2 = -a.lse2p[o];
-      ndl = -a.dltp[o];
+      nl2 = a.lse2p[o];
+      dlt = a.dltp[o];
     }
     // this row's Q (column half 0) or dO (half 1) into TMEM as the A operand
     // of S and dP: column c holds elements 2c and 2c + 1 of the row, which is
@@ -856,8 +853,8 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap& tk64, const CUtensorMa
       tmem_pin(sr);
       tmem_pin(dr);
       row_pass<kCap, kBias, -1>(
-          sr, dr, cc, c2, inv2, slope2, static_cast<float>(a.rel + q0 + row - j0), on,
-          [&](int) { return pair(nl2, nl2); }, [&](int) { return pair(ndl, ndl); }, pp, dd);
+          sr, dr, cc, c2, capl2, slope2, static_cast<float>(a.rel + q0 + row - j0), on,
+          [&](int) { return pair(nl2, nl2); }, [&](int) { return pair(dlt, dlt); }, pp, dd);
       tmem_st16(t_s, dd);  // dS over the first half of this warp's S columns
       cur.next();
       tmem_wait_st();
@@ -880,7 +877,7 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap& tk64, const CUtensorMa
 #pragma unroll
           for (int x = 0; x < 32; ++x) r[x] = 0u;
         }
-        if (row < nq) store_row32(a.dq, at + c * 32, a.grad_bf16, r, a.scale);
+        if (row < nq) store_row32(a.dq, at + c * 32, a.grad_bf16, r, -a.scale);
       }
     }
   }
@@ -926,8 +923,8 @@ __global__ void __launch_bounds__(kThreadsB, 1)
   }
 }
 
-// delta_i = out_i . dout_i and lse_i log2e, 64 rows of one (batch entry, head) a
-// CTA, into copies padded to 64 rows: +inf and 0 past the end, +inf for a row
+// delta_i = out_i . dout_i and -lse_i log2e, 64 rows of one (batch entry, head) a
+// CTA, into copies padded to 64 rows: -inf and 0 past the end, -inf for a row
 // that saw no key. Bound by HBM (out and dout are read once).
 template <int D, bool kOutBf16>
 __global__ void __launch_bounds__(256) score_delta_tc_kernel(const __grid_constant__ ScoreArgs a) {
@@ -969,8 +966,8 @@ __global__ void __launch_bounds__(256) score_delta_tc_kernel(const __grid_consta
 #pragma unroll
     for (int s = kLanes / 2; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
     if (sub == 0) {
-      const float l = row < a.Sq ? a.lse[(static_cast<int64_t>(b) * a.H + h) * a.Sq + row] : INFINITY;
-      a.lse2p[pad0 + r] = l == -INFINITY ? INFINITY : l * kLog2e;
+      const float l = row < a.Sq ? a.lse[(static_cast<int64_t>(b) * a.H + h) * a.Sq + row] : -INFINITY;
+      a.lse2p[pad0 + r] = l == -INFINITY ? -INFINITY : -l * kLog2e;
       a.dltp[pad0 + r] = row < a.Sq ? sum : 0.f;
     }
   }
@@ -994,7 +991,7 @@ cudaError_t launch_rule(const ScoreArgs& a, const BwdMaps& m, cudaStream_t s) {
   const int cs = cluster_for(8.0, kv_items, ntq * a.G, q_ctas, ntk * 3 / 4, a.causal ? 0.5 : 1.0, false);
   const int64_t ctas = kv_items * cs + (q_ctas + cs - 1) / cs * cs;
   return launch_clusters(score_bwd_tc_kernel<D, kCap, kBias>, ctas / cs, 1, 1, cs, kThreadsB, kAlloc, a.Sq > 0, s, m.q64,
-                         m.o64, m.k64, m.v64, a, make_cap_coef(a.scale, a.cap));
+                         m.o64, m.k64, m.v64, a, make_cap_coef(a.scale, a.cap, true));
 }
 
 template <int D>

@@ -743,7 +743,7 @@ cudaError_t launch_rule(const ScoreArgs& a, const CUtensorMap& tq, const CUtenso
   // steps: key tiles; some 8 of them go by before the first and after the last
   const int cs = cluster_for(8.0, items, (a.Skv + kTileN - 1) / kTileN, 0, 0, a.causal ? 0.5 : 1.0, true);
   return launch_clusters(score_fwd_tc_kernel<D, kCap, kBias>, a.H, a.B, (a.Sq + 2 * kTileM - 1) / (2 * kTileM), cs, kThreads, L::kAlloc, a.qdoc != nullptr, s, tq, tk,
-                         tv, a, make_cap_coef(a.scale, a.cap));
+                         tv, a, make_cap_coef(a.scale, a.cap, false));
 }
 
 template <int D>

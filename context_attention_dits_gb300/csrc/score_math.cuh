@@ -65,7 +65,8 @@ struct CapCoef {
   float a0, capl2;     // exact: capl2 (1 - 2 / (1 + 2^(s a0)))
 };
 
-inline CapCoef make_cap_coef(float scale, float cap) {
+// unit: the coefficients give tanh itself, without cap log2e.
+inline CapCoef make_cap_coef(float scale, float cap, bool unit) {
   static const double t3[4] = {0.9999994558, -0.3332631794, 0.131902966, -0.04440222613};
   static const double t6[7] = {0.9999999502,  -0.3333283915,  0.1332520408, -0.05345702957,
                                0.02028998042, -0.006203379104, 0.001041022634};
@@ -83,7 +84,7 @@ inline CapCoef make_cap_coef(float scale, float cap) {
   // range (a narrow cap) rules its polynomial out. x3, x6: the largest x^2.
   double x3 = 0.25, x6 = 1.0, pw = r;
   for (int k = 0; k < 7; ++k, pw *= r * r) {
-    const double x = cap * l2e * pw;
+    const double x = (unit ? 1.0 : cap * l2e) * pw;
     auto put = [&](const double* t, int deg, f32x2* p, double* most) {
       if (k > deg) return;
       double v = x * t[k];
@@ -107,7 +108,7 @@ inline CapCoef make_cap_coef(float scale, float cap) {
   c.u3 = limit(x3);
   c.u6 = limit(x6);
   c.a0 = static_cast<float>(2.0 * l2e * r);
-  c.capl2 = static_cast<float>(cap * l2e);
+  c.capl2 = unit ? 1.f : static_cast<float>(cap * l2e);
   return c;
 }
 
