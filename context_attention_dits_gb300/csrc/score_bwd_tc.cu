@@ -211,24 +211,67 @@ __device__ __forceinline__ void row_pass(const uint32_t (&sr)[32], const uint32_
   }
 }
 
-// 32 fp32 results of a row, times mul, to dst (fp32 or bf16) at element at.
-__device__ __forceinline__ void store_row32(void* dst, int64_t at, bool bf16, const uint32_t (&r)[32], float mul) {
-  if (bf16) {
-    __nv_bfloat16* d = static_cast<__nv_bfloat16*>(dst) + at;
+// A warp's 32 rows (a lane each) of kP 16-byte pieces to dst, `pitch` bytes from
+// row to row, the first `rows` of them: through 512 kP bytes of shared memory,
+// so that a warp instruction stores whole lines (a lane storing its own row
+// took 7000 cycles a tile, this ...).
+template <int kP>
+__device__ __forceinline__ void store_rows(uint8_t* stage, int lane, const uint4 (&v)[kP], uint8_t* dst, int64_t pitch,
+                                           int rows) {
 #pragma unroll
-    for (int x = 0; x < 32; x += 8) {
-      uint4 v;
-      v.x = pack_bf16x2(u2f(r[x]) * mul, u2f(r[x + 1]) * mul);
-      v.y = pack_bf16x2(u2f(r[x + 2]) * mul, u2f(r[x + 3]) * mul);
-      v.z = pack_bf16x2(u2f(r[x + 4]) * mul, u2f(r[x + 5]) * mul);
-      v.w = pack_bf16x2(u2f(r[x + 6]) * mul, u2f(r[x + 7]) * mul);
-      *reinterpret_cast<uint4*>(d + x) = v;
+  for (int q = 0; q < kP; ++q)
+    *reinterpret_cast<uint4*>(stage + lane * kP * 16 + ((q ^ (lane & (kP - 1))) * 16)) = v[q];
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < kP; ++i) {
+    const int r = (i * 32 + lane) / kP, q = lane % kP;
+    const uint4 x = *reinterpret_cast<const uint4*>(stage + r * kP * 16 + ((q ^ (r & (kP - 1))) * 16));
+    if (r < rows) *reinterpret_cast<uint4*>(dst + r * pitch + q * 16) = x;
+  }
+  __syncwarp();  // the stage is read before it is filled again
+}
+
+// kCols2 columns from TMEM column t_acc of a warp's rows, times mul, to dst (fp32
+// or bf16, element `at` of the first row, `pitch` elements from row to row);
+// none: there are zeros instead.
+template <int kCols2>
+__device__ __forceinline__ void store_acc(uint32_t t_acc, bool none, float mul, uint8_t* stage, int lane, void* dst,
+                                          int64_t at, int64_t pitch, int rows, bool bf16) {
+  if (bf16) {
+    constexpr int kStep = kCols2 < 64 ? kCols2 : 64;  // columns of a pass
+#pragma unroll 1
+    for (int c = 0; c < kCols2; c += kStep) {
+      uint4 v[kStep / 8];
+#pragma unroll
+      for (int u = 0; u < kStep / 32; ++u) {
+        uint32_t r[32];
+        tmem_ld32(t_acc + c + u * 32, r);
+        tmem_wait_ld();
+        tmem_pin(r);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const float m = none ? 0.f : mul;
+          auto w = [&](int e) { return none ? 0u : pack_bf16x2(u2f(r[8 * x + e]) * m, u2f(r[8 * x + e + 1]) * m); };
+          v[u * 4 + x] = make_uint4(w(0), w(2), w(4), w(6));
+        }
+      }
+      store_rows<kStep / 8>(stage, lane, v, static_cast<uint8_t*>(dst) + (at + c) * 2, pitch * 2, rows);
     }
   } else {
-    float* d = static_cast<float*>(dst) + at;
+#pragma unroll 1
+    for (int c = 0; c < kCols2; c += 32) {
+      uint32_t r[32];
+      tmem_ld32(t_acc + c, r);
+      tmem_wait_ld();
+      tmem_pin(r);
+      uint4 v[8];
 #pragma unroll
-    for (int x = 0; x < 32; x += 4)
-      *reinterpret_cast<float4*>(d + x) = make_float4(u2f(r[x]) * mul, u2f(r[x + 1]) * mul, u2f(r[x + 2]) * mul, u2f(r[x + 3]) * mul);
+      for (int x = 0; x < 8; ++x) {
+        auto w = [&](int e) { return none ? 0u : __float_as_uint(u2f(r[4 * x + e]) * mul); };
+        v[x] = make_uint4(w(0), w(1), w(2), w(3));
+      }
+      store_rows<8>(stage, lane, v, static_cast<uint8_t*>(dst) + (at + c) * 4, pitch * 4, rows);
+    }
   }
 }
 
@@ -501,27 +544,25 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap& tq64, const CUtensor
     if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar(kBarDone), 0, abort_flag, a.err, tmo));
     if (ok) {
       tc_fence_after();
-      const int64_t at = ((static_cast<int64_t>(b) * a.Skv + key0 + key) * a.Hkv + hk) * D;
-      const int g = hc;  // column half 0 writes dv, half 1 dk
+      const int g = hc;  // column half 0 writes dv, half 1 dk; NJ == 0: no row reaches these keys
+      if (cs > 1) {  // this CTA's part, over the idle tiles: [dv, dk][key][D], 16-byte pieces permuted by row
+        float* part = reinterpret_cast<float*>(smem) + (g * kT + key) * D;
 #pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t r[32];
-        tmem_ld32(tmem + lane_off + 256 + g * D + c * 32, r);
-        tmem_wait_ld();
-        tmem_pin(r);
-        if (NJ == 0) {  // no row reaches these keys: no product was formed
-#pragma unroll
-          for (int x = 0; x < 32; ++x) r[x] = 0u;
-        }
-        if (cs > 1) {  // this CTA's part, over the idle tiles: [dv, dk][key][D], 16-byte pieces permuted by row
-          float* part = reinterpret_cast<float*>(smem) + (g * kT + key) * D;
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t r[32];
+          tmem_ld32(tmem + lane_off + 256 + g * D + c * 32, r);
+          tmem_wait_ld();
+          tmem_pin(r);
 #pragma unroll
           for (int x = 0; x < 8; ++x)
             *reinterpret_cast<float4*>(part + (((c * 8 + x) ^ (key & 7)) * 4)) =
-                make_float4(u2f(r[4 * x]), u2f(r[4 * x + 1]), u2f(r[4 * x + 2]), u2f(r[4 * x + 3]));
-        } else if (kvalid) {
-          store_row32(g == 0 ? a.dv : a.dk, at + c * 32, a.grad_bf16, r, g == 0 ? 1.f : -a.scale);
+                NJ == 0 ? make_float4(0.f, 0.f, 0.f, 0.f)
+                        : make_float4(u2f(r[4 * x]), u2f(r[4 * x + 1]), u2f(r[4 * x + 2]), u2f(r[4 * x + 3]));
         }
+      } else {
+        store_acc<D>(tmem + lane_off + 256 + g * D, NJ == 0, g == 0 ? 1.f : -a.scale, smem + L::kOffQ + (warp - 2) * 4096,
+                     lane, g == 0 ? a.dv : a.dk, ((static_cast<int64_t>(b) * a.Skv + key0 + wq * 32) * a.Hkv + hk) * D,
+                     static_cast<int64_t>(a.Hkv) * D, nk - wq * 32, a.grad_bf16);
       }
     }
   }
@@ -609,7 +650,7 @@ struct DqSmem {
   static constexpr int kOffK = 0;                          // kDqSlots sub-tiles
   static constexpr int kOffV = kOffK + kDqSlots * kSubT;   // kDqSlots sub-tiles
   static constexpr int kOffBar = kOffV + kDqSlots * kSubT;
-  static constexpr int kNumBars = 1 + 2 * kDqSlots + 6;
+  static constexpr int kNumBars = 1 + 2 * kDqSlots + 7;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
   static constexpr int kOffMap = kOffMisc + 16;
   static constexpr int kBytes = kOffMap + 2 * kMapWords * 4;
@@ -625,11 +666,13 @@ enum : int {
   kDqBarPFull = kDqBarSFull + 2,           // +TMEM slot (2): dS written (every row warp arrives)
   kDqBarDone = kDqBarPFull + 2,            // every MMA done: dQ final
   kDqBarDrain = kDqBarDone + 1,
+  kDqBarLoad = kDqBarDrain + 1,            // Q and dO landed in the last two slots
 };
 
 // One dq CTA: query tile bx of head h, batch entry b.
 template <int D, bool kCap, bool kBias>
-__device__ __forceinline__ void dq_cta(const CUtensorMap& tk64, const CUtensorMap& tv64, const ScoreArgs& a,
+__device__ __forceinline__ void dq_cta(const CUtensorMap& tq64, const CUtensorMap& to64, const CUtensorMap& tk64,
+                                       const CUtensorMap& tv64, const ScoreArgs& a,
                                        const CapCoef& cc, uint8_t* smem_raw, int alloc, int bx, int h, int b) {
   using L = DqSmem<D>;
   const uint32_t pad = (1024u - (smem_addr(smem_raw) & 1023u)) & 1023u;
@@ -678,15 +721,23 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap& tk64, const CUtensorMa
   if (warp == 0) {
     // ===================== TMA producer =====================
     const bool leader = elect_one();
+    // Q and dO first, through the last two K and the last two V slots: the row
+    // warps take them to TMEM before those are needed
     if (leader) {
-      tma_prefetch_desc(&tk64);
-      tma_prefetch_desc(&tv64);
+      mbar_arrive_expect_tx(bar(kDqBarLoad), 2 * kT * D * 2);
+      for (int c = 0; c < D / 64; ++c)
+        for (int r = 0; r < kT; r += kSub) {
+          const uint32_t at = (kDqSlots - 2) * L::kSubT + c * (kT * 128) + r * 128;
+          tma_load_4d(sb + L::kOffK + at, &tq64, bar(kDqBarLoad), c * 64, h, q0 + r, b);
+          tma_load_4d(sb + L::kOffV + at, &to64, bar(kDqBarLoad), c * 64, h, q0 + r, b);
+        }
     }
     int issued[kDqSlots] = {};
     TileWalk cur(bits, 0, ntk, -1);
     for (int j = 0; j < NJ; ++j) {
       const int s = j % kDqSlots;
       const uint32_t ph = (j / kDqSlots) & 1;
+      if (j == kDqSlots - 2 && !__all_sync(0xffffffffu, mbar_wait_bounded(bar(kDqBarQ), 0, abort_flag, a.err, tmo))) break;
       if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar(kDqBarKVEmpty + s), ph ^ 1, abort_flag, a.err, tmo)))
         break;
       if (leader) {
@@ -703,6 +754,7 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap& tk64, const CUtensorMa
     }
     if (*abort_flag) {
       // let every issued copy land before the CTA's shared memory goes away
+      drain_wait_b(bar(kDqBarLoad), 0, tmo);
       for (int s = 0; s < kDqSlots; ++s)
         if (issued[s]) drain_wait_b(bar(kDqBarKVFull + s), (issued[s] - 1) & 1, tmo);
     }
@@ -799,39 +851,35 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap& tk64, const CUtensorMa
     }
     // this row's Q (column half 0) or dO (half 1) into TMEM as the A operand
     // of S and dP: column c holds elements 2c and 2c + 1 of the row, which is
-    // the row's memory read as 32-bit words; rows past the shard are zero
-    // (they take no part)
-    {
-      const int64_t ro = ((static_cast<int64_t>(b) * a.Sq + q0 + row) * a.H + h) * D;
-      {
-        const int g = hc;
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(g == 0 ? a.q : a.dout) + ro);
+    // the row's memory read as 32-bit words; rows past the end were filled with
+    // zeros (read from global memory a row a lane, this took 7000 cycles)
+    bool ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar(kDqBarLoad), 0, abort_flag, a.err, tmo));
+    if (ok) {
+      const uint8_t* src = smem + (hc == 0 ? L::kOffK : L::kOffV) + (kDqSlots - 2) * L::kSubT + row * 128;
 #pragma unroll 1
-        for (int c = 0; c < D / 64; ++c) {
-          uint32_t w[32];
+      for (int c = 0; c < D / 64; ++c) {
+        uint32_t w[32];
 #pragma unroll
-          for (int x = 0; x < 8; ++x) {
-            const uint4 u = row < nq ? src[c * 8 + x] : make_uint4(0u, 0u, 0u, 0u);
-            w[4 * x] = u.x;
-            w[4 * x + 1] = u.y;
-            w[4 * x + 2] = u.z;
-            w[4 * x + 3] = u.w;
-          }
-          tmem_st32(tmem + lane_off + 384 + g * (D / 2) + c * 32, w);
+        for (int x = 0; x < 8; ++x) {
+          const uint4 u = *reinterpret_cast<const uint4*>(src + c * (kT * 128) + ((x ^ (row & 7)) * 16));
+          w[4 * x] = u.x;
+          w[4 * x + 1] = u.y;
+          w[4 * x + 2] = u.z;
+          w[4 * x + 3] = u.w;
         }
+        tmem_st32(tmem + lane_off + 384 + hc * (D / 2) + c * 32, w);
       }
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kDqBarQ));
     }
-    bool ok = true;
     const int lim = min(a.Skv, key_limit(a, plim, q0 + row));
     const int qd = a.qdoc && row < nq ? a.qdoc[static_cast<int64_t>(b) * a.Sq + q0 + row] : -1;
     const int* kdoc = a.kdoc + static_cast<int64_t>(b) * a.Skv;
     const float slope2 = kBias ? a.slopes[h] * kLog2e : 0.f;
     TileWalk cur(bits, 0, ntk, -1);
-    for (int j = 0; j < NJ; ++j) {
+    for (int j = 0; ok && j < NJ; ++j) {
       const int ts = j & 1;
       const int j0 = cur.t * kSub + hc * 32;  // the key of this warp's first column
       const int n = lim - j0;
@@ -866,19 +914,10 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap& tk64, const CUtensorMa
     if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar(kDqBarDone), 0, abort_flag, a.err, tmo));
     if (ok) {
       tc_fence_after();
-      const int64_t at = ((static_cast<int64_t>(b) * a.Sq + q0 + row) * a.H + h) * D;
-#pragma unroll 1
-      for (int c = hc * (D / 64); c < (hc + 1) * (D / 64); ++c) {  // this half's D / 2 columns
-        uint32_t r[32];
-        tmem_ld32(tmem + lane_off + 256 + c * 32, r);
-        tmem_wait_ld();
-        tmem_pin(r);
-        if (NJ == 0) {  // these rows reach no key
-#pragma unroll
-          for (int x = 0; x < 32; ++x) r[x] = 0u;
-        }
-        if (row < nq) store_row32(a.dq, at + c * 32, a.grad_bf16, r, -a.scale);
-      }
+      // this half's D / 2 columns; NJ == 0: these rows reach no key
+      store_acc<D / 2>(tmem + lane_off + 256 + hc * (D / 2), NJ == 0, -a.scale, smem + L::kOffK + (warp - 2) * 4096, lane,
+                       a.dq, ((static_cast<int64_t>(b) * a.Sq + q0 + wq * 32) * a.H + h) * D + hc * (D / 2),
+                       static_cast<int64_t>(a.H) * D, nq - wq * 32, a.grad_bf16);
     }
   }
 
@@ -919,7 +958,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
   } else {
     const int i = id - kv_ctas, bh = i % (a.H * a.B);
     if (i < nq * a.H * a.B)  // the last cluster may have CTAs without work
-      dq_cta<D, kCap, kBias>(tk64, tv64, a, cc, smem_raw, bwd_alloc<D>(), nq - 1 - i / (a.H * a.B), bh % a.H, bh / a.H);
+      dq_cta<D, kCap, kBias>(tq64, to64, tk64, tv64, a, cc, smem_raw, bwd_alloc<D>(), nq - 1 - i / (a.H * a.B), bh % a.H, bh / a.H);
   }
 }
 
