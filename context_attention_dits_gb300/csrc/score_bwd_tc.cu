@@ -36,6 +36,7 @@
 #include <cmath>
 #include <cstdint>
 #include <type_traits>
+#include <utility>
 
 #include "cp_internal.h"
 #include "cp_ptx.cuh"
@@ -50,7 +51,24 @@ constexpr int kThreadsB = 64 + 32 * kRowWarps;
 constexpr uint32_t kTmemColsB = 512;
 constexpr int kT = 128;         // keys per dk/dv CTA, query rows per dq CTA
 constexpr int kSub = 64;        // rows of a streamed sub-tile: query rows (dk/dv) or keys (dq) per sub-step
-constexpr int kSlots = 4;       // streamed sub-tile slots in shared memory
+
+// Depth of the rings. A TMEM slot holds a sub-step's S and dP, and the row pass of
+// one sub-step runs while the tensor cores work on the others': two slots are what
+// 512 columns leave at D = 128. At D = 64, where the products take half as long and
+// a sub-step's chain (S, row pass, gradients) would set the pace, there are three.
+template <int D>
+struct Ring {
+  static constexpr int kTS = D == 64 ? 3 : 2;     // TMEM slots of 128 columns
+  static constexpr int kSlots = D == 64 ? 6 : 4;  // dk/dv: streamed query sub-tiles in shared memory (a multiple of kTS)
+  static constexpr int kAcc = kTS * 128;          // TMEM column of the accumulators
+  static_assert(kSlots % kTS == 0 && kAcc + 2 * D <= 512, "the TMEM slot is the smem slot modulo kTS");
+};
+
+// f(0) && f(1) && ... with the indexes as constants
+template <typename F, int... I>
+__device__ __forceinline__ bool each(std::integer_sequence<int, I...>, F&& f) {
+  return (f(std::integral_constant<int, I>{}) && ...);
+}
 constexpr int kMapWords = kScoreMaxTokens / kSub / 32;  // bitmap of sub-tiles
 static_assert(kSub == kDocBlock, "a sub-tile is a block of document ranges");
 
@@ -66,6 +84,7 @@ __device__ __forceinline__ uint32_t kstep64(int kk) {
 
 template <int D>
 struct BSmem {
+  static constexpr int kSlots = Ring<D>::kSlots;
   static constexpr int kTile = kT * D * 2;    // one bf16 128-row tile (K or V)
   static constexpr int kSubT = kSub * D * 2;  // one bf16 64-row sub-tile (Q or dO)
   static constexpr int kHalfS = kSub * 128;   // one 64-column box of a sub-tile
@@ -76,7 +95,7 @@ struct BSmem {
   static constexpr int kOffLse = kOffO + kSlots * kSubT;     // kSlots x 64 floats: -lse log2 e
   static constexpr int kOffDlt = kOffLse + kSlots * kSub * 4; // kSlots x 64 floats: delta
   static constexpr int kOffBar = kOffDlt + kSlots * kSub * 4;
-  static constexpr int kNumBars = 15;
+  static constexpr int kNumBars = 21;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
   static constexpr int kOffMap = kOffMisc + 16;  // which sub-tiles are walked, and which are mixed
   static constexpr int kBytes = kOffMap + 2 * kMapWords * 4;
@@ -87,12 +106,12 @@ struct BSmem {
 
 enum : int {
   kBarKV = 0,      // K and V tiles landed
-  kBarQFull = 1,   // +slot (4): Q, dO, lse, delta of a sub-tile landed (TMA bytes)
-  kBarQEmpty = 5,  // +slot (4): MMAs done with the slot
-  kBarSFull = 9,   // +TMEM slot (2): S^T and dP^T of the sub-step in TMEM
-  kBarPFull = 11,  // +TMEM slot (2): P^T, dS^T written (every row warp arrives)
-  kBarDone = 13,   // every MMA of the CTA done: dK, dV final
-  kBarDrain = 14,
+  kBarQFull = 1,   // +slot (6): Q, dO, lse, delta of a sub-tile landed (TMA bytes)
+  kBarQEmpty = 7,  // +slot (6): MMAs done with the slot
+  kBarSFull = 13,  // +TMEM slot (3): S^T and dP^T of the sub-step in TMEM
+  kBarPFull = 16,  // +TMEM slot (3): P^T, dS^T written (every row warp arrives)
+  kBarDone = 19,   // every MMA of the CTA done: dK, dV final
+  kBarDrain = 20,
 };
 
 __device__ __forceinline__ void drain_wait_b(uint32_t bar, uint32_t parity, uint64_t timeout_ns) {
@@ -284,6 +303,7 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap& tq64, const CUtensor
                                          const CUtensorMap& to64, const ScoreArgs& a, const CapCoef& cc,
                                          uint8_t* smem_raw, int alloc, int cs, int rank, int bx, int hk, int b) {
   using L = BSmem<D>;
+  constexpr int kSlots = Ring<D>::kSlots, kTS = Ring<D>::kTS, kAcc = Ring<D>::kAcc;
   // the swizzled tiles need a 1024-byte aligned base; a base that would need
   // more padding than the allocation holds is reported (uniformly, before any
   // barrier or TMEM use) instead of used
@@ -339,8 +359,7 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap& tq64, const CUtensor
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < L::kNumBars; ++i) {
-      const bool four = i == kBarPFull || i == kBarPFull + 1;
-      mbar_init(bar(i), four ? kRowWarps : 1);
+      mbar_init(bar(i), i >= kBarPFull && i < kBarDone ? kRowWarps : 1);
     }
     misc[1] = 0;
     fence_mbar_init();
@@ -370,11 +389,11 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap& tq64, const CUtensor
           tma_load_4d(sb + L::kOffV + c * (kT * 128) + r * 128, &tv64, bar(kBarKV), c * 64, hk, key0 + r, b);
         }
     }
-    int issued[kSlots] = {0, 0, 0, 0};
+    int issued[kSlots] = {};
     HeadWalk cur(bits, t0, ntq, per_head, hk * a.G, j0);
     for (int j = 0; j < NJ; ++j) {
-      const int s = j & (kSlots - 1);
-      const uint32_t ph = (j >> 2) & 1;
+      const int s = j % kSlots;
+      const uint32_t ph = (j / kSlots) & 1;
       if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar(kBarQEmpty + s), ph ^ 1, abort_flag, a.err, tmo))) break;
       const int q0 = cur.w.t * kSub, h = cur.h;
       if (leader) {
@@ -435,19 +454,19 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap& tq64, const CUtensor
       const uint32_t pa = tmem + ts * 128;
 #pragma unroll
       for (int kk = 0; kk < kSub / 16; ++kk)
-        if (leader) mma_ts_lohi(tmem + 256, pa + pcol(kk), o_mn_lo + slot + ((kk * 2048) >> 4), mn_hi, idesc_g,
+        if (leader) mma_ts_lohi(tmem + kAcc, pa + pcol(kk), o_mn_lo + slot + ((kk * 2048) >> 4), mn_hi, idesc_g,
                                 (acc || kk > 0) ? 1u : 0u);
 #pragma unroll
       for (int kk = 0; kk < kSub / 16; ++kk)
-        if (leader) mma_ts_lohi(tmem + 256 + D, pa + kSub + pcol(kk), q_mn_lo + slot + ((kk * 2048) >> 4), mn_hi,
+        if (leader) mma_ts_lohi(tmem + kAcc + D, pa + kSub + pcol(kk), q_mn_lo + slot + ((kk * 2048) >> 4), mn_hi,
                                 idesc_g, (acc || kk > 0) ? 1u : 0u);
     };
     auto wait_q = [&](int j) -> bool {
-      return mbar_wait_bounded(bar(kBarQFull + (j & (kSlots - 1))), (j >> 2) & 1, abort_flag, a.err, tmo);
+      return mbar_wait_bounded(bar(kBarQFull + j % kSlots), (j / kSlots) & 1, abort_flag, a.err, tmo);
     };
     bool ok = mbar_wait_bounded(bar(kBarKV), 0, abort_flag, a.err, tmo);
-    // prologue: S^T, dP^T of the first two sub-steps
-    for (int j = 0; ok && j < 2 && j < NJ; ++j) {
+    // prologue: S^T, dP^T of the first kTS sub-steps
+    for (int j = 0; ok && j < kTS && j < NJ; ++j) {
       if (!wait_q(j)) {
         ok = false;
         break;
@@ -456,30 +475,26 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap& tq64, const CUtensor
       issue_sdp(j, j);
       commit(bar(kBarSFull + j));
     }
-    // sub-step j: once P^T, dS^T are in TMEM slot j mod 2, dV and dK consume
-    // them and S^T, dP^T of sub-step j + 2 go into the same slot; the step is
+    // sub-step j: once P^T, dS^T are in TMEM slot j mod kTS, dV and dK consume
+    // them and S^T, dP^T of sub-step j + kTS go into the same slot; the step is
     // instantiated per smem slot so every operand offset is a constant
     auto step = [&](auto q_c, int j) -> bool {
       constexpr int q = decltype(q_c)::value;
-      constexpr int ts = q & 1;
-      if (!mbar_wait_bounded(bar(kBarPFull + ts), (j >> 1) & 1, abort_flag, a.err, tmo)) return false;
+      constexpr int ts = q % kTS;
+      if (!mbar_wait_bounded(bar(kBarPFull + ts), (j / kTS) & 1, abort_flag, a.err, tmo)) return false;
       tc_fence_after();
       issue_g(q, ts, j > 0);
       commit(bar(kBarQEmpty + q));
-      if (j + 2 < NJ) {
-        if (!wait_q(j + 2)) return false;
+      if (j + kTS < NJ) {
+        if (!wait_q(j + kTS)) return false;
         tc_fence_after();
-        issue_sdp((q + 2) & (kSlots - 1), ts);
+        issue_sdp((q + kTS) % kSlots, ts);
         commit(bar(kBarSFull + ts));
       }
       return true;
     };
-    for (int j = 0; ok && j < NJ; j += kSlots) {
-      ok = step(std::integral_constant<int, 0>{}, j);
-      if (ok && j + 1 < NJ) ok = step(std::integral_constant<int, 1>{}, j + 1);
-      if (ok && j + 2 < NJ) ok = step(std::integral_constant<int, 2>{}, j + 2);
-      if (ok && j + 3 < NJ) ok = step(std::integral_constant<int, 3>{}, j + 3);
-    }
+    for (int j = 0; ok && j < NJ; j += kSlots)
+      ok = each(std::make_integer_sequence<int, kSlots>{}, [&](auto q) { return j + q >= NJ || step(q, j + q); });
     if (ok) {
       commit(bar(kBarDone));
     } else {
@@ -501,7 +516,7 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap& tq64, const CUtensor
     bool ok = true;
     HeadWalk cur(bits, t0, ntq, per_head, hk * a.G, j0);
     for (int j = 0; j < NJ; ++j) {
-      const int q = j & (kSlots - 1), ts = j & 1;
+      const int q = j % kSlots, ts = j % kTS;
       const float slope2 = kBias ? __ldg(a.slopes + cur.h) * kLog2e : 0.f;
       const int i0 = cur.w.t * kSub + hc * 32;  // the query row of this warp's first column
       const int d0 = a.rel + i0 - jkey;       // its position less the key's
@@ -513,8 +528,8 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap& tq64, const CUtensor
         on &= same[0];
       }
       ok = __all_sync(0xffffffffu,
-                      mbar_wait_bounded(bar(kBarQFull + q), (j >> 2) & 1, abort_flag, a.err, tmo) &&
-                          mbar_wait_bounded(bar(kBarSFull + ts), (j >> 1) & 1, abort_flag, a.err, tmo));
+                      mbar_wait_bounded(bar(kBarQFull + q), (j / kSlots) & 1, abort_flag, a.err, tmo) &&
+                          mbar_wait_bounded(bar(kBarSFull + ts), (j / kTS) & 1, abort_flag, a.err, tmo));
       if (!ok) break;
       tc_fence_after();
       const uint32_t t_s = tmem + lane_off + ts * 128 + hc * 32, t_dp = t_s + kSub;
@@ -550,7 +565,7 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap& tq64, const CUtensor
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t r[32];
-          tmem_ld32(tmem + lane_off + 256 + g * D + c * 32, r);
+          tmem_ld32(tmem + lane_off + kAcc + g * D + c * 32, r);
           tmem_wait_ld();
           tmem_pin(r);
 #pragma unroll
@@ -560,7 +575,7 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap& tq64, const CUtensor
                         : make_float4(u2f(r[4 * x]), u2f(r[4 * x + 1]), u2f(r[4 * x + 2]), u2f(r[4 * x + 3]));
         }
       } else {
-        store_acc<D>(tmem + lane_off + 256 + g * D, NJ == 0, g == 0 ? 1.f : -a.scale, smem + L::kOffQ + (warp - 2) * 4096,
+        store_acc<D>(tmem + lane_off + kAcc + g * D, NJ == 0, g == 0 ? 1.f : -a.scale, smem + L::kOffQ + (warp - 2) * 4096,
                      lane, g == 0 ? a.dv : a.dk, ((static_cast<int64_t>(b) * a.Skv + key0 + wq * 32) * a.Hkv + hk) * D,
                      static_cast<int64_t>(a.Hkv) * D, nk - wq * 32, a.grad_bf16);
       }
@@ -630,13 +645,13 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap& tq64, const CUtensor
 // ----------------------------------------------------------------------------
 // dq: one CTA per 128 query rows of one (batch entry, head). The row warps
 // load the CTA's Q and dO rows once into TMEM (bf16 pairs, the A-operand
-// layout: columns [384, 384 + D/2) and [384 + D/2, 384 + D)); 64-key K and V
+// layout: D columns behind dQ); 64-key K and V
 // sub-tiles that the rows reach stream through kDqSlots shared-memory slots. Per sub-tile three MMAs (M = 128 rows):
-//   S  = Q K^T    (TS: Q in TMEM, K K-major; N = 64) -> TMEM slot j mod 2, [0, 64)
+//   S  = Q K^T    (TS: Q in TMEM, K K-major; N = 64) -> TMEM slot j mod kTS, [0, 64)
 //   dP = dO V^T   (TS)                               -> the same slot, [64, 128)
 //   dQ += dS K    (TS: dS over S's first 32 columns, K read MN-major)
-//                                                    -> TMEM [256, 256 + D)
-// Only K and V come from shared memory. S and dP of sub-step j + 2 are issued
+//                                                    -> TMEM [kAcc, kAcc + D)
+// Only K and V come from shared memory. S and dP of sub-step j + kTS are issued
 // right after dQ of sub-step j, so they run while the row warps (one thread
 // per query row and column half, lse and delta in registers) form
 // dS = p (dp - delta) of sub-step j + 1. dq is stored once, without atomics.
@@ -650,7 +665,7 @@ struct DqSmem {
   static constexpr int kOffK = 0;                          // kDqSlots sub-tiles
   static constexpr int kOffV = kOffK + kDqSlots * kSubT;   // kDqSlots sub-tiles
   static constexpr int kOffBar = kOffV + kDqSlots * kSubT;
-  static constexpr int kNumBars = 1 + 2 * kDqSlots + 7;
+  static constexpr int kNumBars = 1 + 2 * kDqSlots + 9;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
   static constexpr int kOffMap = kOffMisc + 16;
   static constexpr int kBytes = kOffMap + 2 * kMapWords * 4;
@@ -662,9 +677,9 @@ enum : int {
   kDqBarQ = 0,                             // Q and dO in TMEM (every row warp arrives)
   kDqBarKVFull = 1,                        // +slot: K and V sub-tiles landed
   kDqBarKVEmpty = 1 + kDqSlots,            // +slot: MMAs done with the slot
-  kDqBarSFull = 1 + 2 * kDqSlots,          // +TMEM slot (2): S and dP in TMEM
-  kDqBarPFull = kDqBarSFull + 2,           // +TMEM slot (2): dS written (every row warp arrives)
-  kDqBarDone = kDqBarPFull + 2,            // every MMA done: dQ final
+  kDqBarSFull = 1 + 2 * kDqSlots,          // +TMEM slot (3): S and dP in TMEM
+  kDqBarPFull = kDqBarSFull + 3,           // +TMEM slot (3): dS written (every row warp arrives)
+  kDqBarDone = kDqBarPFull + 3,            // every MMA done: dQ final
   kDqBarDrain = kDqBarDone + 1,
   kDqBarLoad = kDqBarDrain + 1,            // Q and dO landed in the last two slots
 };
@@ -675,6 +690,8 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap& tq64, const CUtensorMa
                                        const CUtensorMap& tv64, const ScoreArgs& a,
                                        const CapCoef& cc, uint8_t* smem_raw, int alloc, int bx, int h, int b) {
   using L = DqSmem<D>;
+  // TMEM: the slots, dQ, then Q and dO (D / 2 columns each)
+  constexpr int kTS = Ring<D>::kTS, kAcc = Ring<D>::kAcc, kOp = kAcc + D;
   const uint32_t pad = (1024u - (smem_addr(smem_raw) & 1023u)) & 1023u;
   if (pad > static_cast<uint32_t>(alloc - L::kBytes)) {
     if (threadIdx.x == 0) atomicOr(a.err, kDevErrLayout);
@@ -704,7 +721,7 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap& tq64, const CUtensorMa
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < L::kNumBars; ++i)
-      mbar_init(bar(i), (i == kDqBarQ || i == kDqBarPFull || i == kDqBarPFull + 1) ? kRowWarps : 1);
+      mbar_init(bar(i), i == kDqBarQ || (i >= kDqBarPFull && i < kDqBarDone) ? kRowWarps : 1);
     misc[1] = 0;
     fence_mbar_init();
   }
@@ -769,7 +786,7 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap& tq64, const CUtensorMa
     const uint32_t km_hi = static_cast<uint32_t>(k_km >> 32), mn_hi = static_cast<uint32_t>(k_mn >> 32);
     const uint32_t k_lo = static_cast<uint32_t>(k_km), v_lo = static_cast<uint32_t>(v_km);
     const uint32_t k_mn_lo = static_cast<uint32_t>(k_mn);
-    const uint32_t t_q = tmem + 384, t_o = tmem + 384 + D / 2;  // Q and dO rows in TMEM (8 columns per K step)
+    const uint32_t t_q = tmem + kOp, t_o = tmem + kOp + D / 2;  // Q and dO rows in TMEM (8 columns per K step)
     auto commit = [&](uint32_t bar_addr) {
       if (leader) mma_commit(bar_addr);
     };
@@ -788,7 +805,7 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap& tq64, const CUtensorMa
       return mbar_wait_bounded(bar(kDqBarKVFull + (j % kDqSlots)), (j / kDqSlots) & 1, abort_flag, a.err, tmo);
     };
     bool ok = mbar_wait_bounded(bar(kDqBarQ), 0, abort_flag, a.err, tmo);
-    for (int j = 0; ok && j < 2 && j < NJ; ++j) {
+    for (int j = 0; ok && j < kTS && j < NJ; ++j) {
       if (!wait_kv(j)) {
         ok = false;
         break;
@@ -797,38 +814,32 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap& tq64, const CUtensorMa
       issue_sdp(j, j);
       commit(bar(kDqBarSFull + j));
     }
-    // sub-step j: dQ += dS K once dS is in TMEM slot j mod 2 (K = keys: 16 key
-    // rows = 2048 bytes of the MN-major sub-tile), then S, dP of sub-step j + 2
-    // into the same slot; instantiated per smem slot (kDqSlots is even, so the
-    // TMEM slot is the smem slot's parity)
-    static_assert(kDqSlots % 2 == 0, "TMEM slot = smem slot parity");
+    // sub-step j: dQ += dS K once dS is in TMEM slot j mod kTS (K = keys: 16 key
+    // rows = 2048 bytes of the MN-major sub-tile), then S, dP of sub-step j + kTS
+    // into the same slot; instantiated per smem slot (a multiple of kTS of them, so
+    // the TMEM slot is the smem slot modulo kTS)
+    static_assert(kDqSlots % kTS == 0, "TMEM slot = smem slot modulo kTS");
     auto step = [&](auto q_c, int j) -> bool {
       constexpr int q = decltype(q_c)::value;
-      constexpr int ts = q & 1;
-      if (!mbar_wait_bounded(bar(kDqBarPFull + ts), (j >> 1) & 1, abort_flag, a.err, tmo)) return false;
+      constexpr int ts = q % kTS;
+      if (!mbar_wait_bounded(bar(kDqBarPFull + ts), (j / kTS) & 1, abort_flag, a.err, tmo)) return false;
       tc_fence_after();
       const uint32_t slot = static_cast<uint32_t>((q * L::kSubT) >> 4);
 #pragma unroll
       for (int kk = 0; kk < kSub / 16; ++kk)
-        if (leader) mma_ts_lohi(tmem + 256, tmem + ts * 128 + pcol(kk), k_mn_lo + slot + ((kk * 2048) >> 4), mn_hi,
+        if (leader) mma_ts_lohi(tmem + kAcc, tmem + ts * 128 + pcol(kk), k_mn_lo + slot + ((kk * 2048) >> 4), mn_hi,
                                 idesc_q, (j > 0 || kk > 0) ? 1u : 0u);
       commit(bar(kDqBarKVEmpty + q));
-      if (j + 2 < NJ) {
-        if (!wait_kv(j + 2)) return false;
+      if (j + kTS < NJ) {
+        if (!wait_kv(j + kTS)) return false;
         tc_fence_after();
-        issue_sdp((q + 2) % kDqSlots, ts);
+        issue_sdp((q + kTS) % kDqSlots, ts);
         commit(bar(kDqBarSFull + ts));
       }
       return true;
     };
-    for (int j = 0; ok && j < NJ; j += kDqSlots) {
-      ok = step(std::integral_constant<int, 0>{}, j);
-      if (ok && j + 1 < NJ) ok = step(std::integral_constant<int, 1>{}, j + 1);
-      if (ok && j + 2 < NJ) ok = step(std::integral_constant<int, 2>{}, j + 2);
-      if (ok && j + 3 < NJ) ok = step(std::integral_constant<int, 3>{}, j + 3);
-      if (ok && j + 4 < NJ) ok = step(std::integral_constant<int, 4>{}, j + 4);
-      if (ok && j + 5 < NJ) ok = step(std::integral_constant<int, 5>{}, j + 5);
-    }
+    for (int j = 0; ok && j < NJ; j += kDqSlots)
+      ok = each(std::make_integer_sequence<int, kDqSlots>{}, [&](auto q) { return j + q >= NJ || step(q, j + q); });
     if (ok) {
       commit(bar(kDqBarDone));
     } else {
@@ -867,7 +878,7 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap& tq64, const CUtensorMa
           w[4 * x + 2] = u.z;
           w[4 * x + 3] = u.w;
         }
-        tmem_st32(tmem + lane_off + 384 + hc * (D / 2) + c * 32, w);
+        tmem_st32(tmem + lane_off + kOp + hc * (D / 2) + c * 32, w);
       }
       tmem_wait_st();
       tc_fence_before();
@@ -880,7 +891,7 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap& tq64, const CUtensorMa
     const float slope2 = kBias ? a.slopes[h] * kLog2e : 0.f;
     TileWalk cur(bits, 0, ntk, -1);
     for (int j = 0; ok && j < NJ; ++j) {
-      const int ts = j & 1;
+      const int ts = j % kTS;
       const int j0 = cur.t * kSub + hc * 32;  // the key of this warp's first column
       const int n = lim - j0;
       uint32_t on = n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u;
@@ -890,7 +901,7 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap& tq64, const CUtensorMa
         same_docs<1>(qd, ids, same);
         on &= same[0];
       }
-      ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar(kDqBarSFull + ts), (j >> 1) & 1, abort_flag, a.err, tmo));
+      ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar(kDqBarSFull + ts), (j / kTS) & 1, abort_flag, a.err, tmo));
       if (!ok) break;
       tc_fence_after();
       const uint32_t t_s = tmem + lane_off + ts * 128 + hc * 32, t_dp = t_s + kSub;  // this sub-step's slot
@@ -915,7 +926,7 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap& tq64, const CUtensorMa
     if (ok) {
       tc_fence_after();
       // this half's D / 2 columns; NJ == 0: these rows reach no key
-      store_acc<D / 2>(tmem + lane_off + 256 + hc * (D / 2), NJ == 0, -a.scale, smem + L::kOffK + (warp - 2) * 4096, lane,
+      store_acc<D / 2>(tmem + lane_off + kAcc + hc * (D / 2), NJ == 0, -a.scale, smem + L::kOffK + (warp - 2) * 4096, lane,
                        a.dq, ((static_cast<int64_t>(b) * a.Sq + q0 + wq * 32) * a.H + h) * D + hc * (D / 2),
                        static_cast<int64_t>(a.H) * D, nq - wq * 32, a.grad_bf16);
     }
