@@ -72,6 +72,7 @@ SIGNATURES = {
                                 _sz, _i, _i, _i, _vp]),
     "cp_paged_kv_append": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _vp]),
     "cp_paged_attn_workspace_size": (_sz, [_i, _i, _i, _i, _i]),
+    "cp_paged_attn_workspace_size_for": (_sz, [_i, _i, _i, _i, _i, _i, _i]),
     "cp_paged_attn_decode": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _f, _f, _vp, _vp, _sz,
                                   _i, _i, _vp]),
 }

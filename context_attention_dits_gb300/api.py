@@ -501,8 +501,12 @@ def cp_paged_kv_append(k_new, v_new, k_cache, v_cache, block_table, seq_lens, ne
                                      page, most, _dt(k_new)), None, None, (), index, stream)
 
 
-def cp_paged_attn_workspace_size(B, H, Hkv, D, dtype=torch.bfloat16) -> int:
-    return int(lib().cp_paged_attn_workspace_size(B, H, Hkv, D, _DT[dtype]))
+def cp_paged_attn_workspace_size(B, H, Hkv, D, dtype=torch.bfloat16, page_size=None, max_pages=None) -> int:
+    """Workspace bytes of cp_paged_attn_decode for any table, or for tables of max_pages pages of page_size rows (0
+    where such a call needs none)."""
+    if page_size is None or max_pages is None:
+        return int(lib().cp_paged_attn_workspace_size(B, H, Hkv, D, _DT[dtype]))
+    return int(lib().cp_paged_attn_workspace_size_for(B, H, Hkv, D, page_size, max_pages, _DT[dtype]))
 
 
 def cp_paged_attn_decode(q, k_cache, v_cache, block_table, seq_lens, out, lse, scale: float, softcap: float = 0.0,
@@ -531,7 +535,7 @@ def cp_paged_attn_decode(q, k_cache, v_cache, block_table, seq_lens, out, lse, s
     _call(L.cp_paged_attn_decode, (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
                                    seq_lens.data_ptr(), out.data_ptr(), lse.data_ptr(), B, H, Hkv, D, pages, page, most,
                                    float(scale), float(softcap), None if slopes is None else _slopes(slopes, H, index)),
-          L.cp_paged_attn_workspace_size(B, H, Hkv, D, dt), workspace, (dt, _DT[out.dtype]), index, stream)
+          L.cp_paged_attn_workspace_size_for(B, H, Hkv, D, page, most, dt), workspace, (dt, _DT[out.dtype]), index, stream)
 
 
 def cp_check_device_status(stream=None) -> int:

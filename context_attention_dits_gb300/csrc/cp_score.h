@@ -102,7 +102,26 @@ struct PagedArgs {
   uint32_t* err;
 };
 // Query heads that share a key/value head are taken this many at a time.
-inline int paged_rows(bool bf16) { return bf16 ? 16 : 8; }
+constexpr int paged_rows(bool bf16) { return bf16 ? 16 : 8; }
+// CTAs that run at once: two on a multiprocessor where their buffers fit.
+constexpr int paged_ctas(int D, bool bf16) { return D * (bf16 ? 2 : 4) <= 256 ? kPagedCtas : kPagedCtas / 2; }
+// Decode in one launch: the CTAs (1 to 8, a cluster) that share a unit (a
+// sequence's key/value head and group of query heads), or 0 where the list of all
+// blocks is cut among the CTAs instead. Clusters save the second launch and the
+// workspace, but a unit has 8 CTAs at most and idle ones take no other's work. So:
+// two blocks a CTA where all units' CTAs run at once, more where they would not,
+// up to 8 (bf16) or 4 (fp32, whose blocks are twice the bytes). Clusters against
+// the list, 24 heads on 8, D = 128, device us: bf16 1 x 1000 keys 5.6 / 8.4,
+// 1 x 4096 10.0 / 11.7, 8 x 1000 8.7 / 10.4, 4 x 4096 11.7 / 15.9, 1 x 8000
+// (16 blocks a CTA) 15.9 / 15.1; fp32 1 x 1000 8.2 / 9.9, 1 x 4096 (8) 18.1 / 15.0.
+inline int paged_cluster(int D, bool bf16, int B, int Hkv, int G, int max_pages, int page_shift) {
+  const int64_t blocks = ((static_cast<int64_t>(max_pages) << page_shift) + kPagedBlock - 1) / kPagedBlock;
+  const int64_t units = static_cast<int64_t>(B) * Hkv * ((G + paged_rows(bf16) - 1) / paged_rows(bf16));
+  const int ctas = paged_ctas(D, bf16);
+  int cs = 1;
+  while (cs < 8 && blocks > 2 * cs && units * cs * 2 <= ctas) cs *= 2;
+  return units <= ctas && blocks <= cs * (bf16 ? 8 : 4) ? cs : 0;
+}
 cudaError_t launch_paged_append(const PagedArgs& a, int elem_bytes, cudaStream_t s);
 cudaError_t launch_paged_decode(const PagedArgs& a, bool bf16, cudaStream_t s);
 

@@ -254,6 +254,14 @@ size_t cp_paged_attn_workspace_size(int B, int H, int Hkv, int D, cp_dtype dt) {
   return paged_partial_bytes(H / Hkv, D, dt) + round_up(static_cast<size_t>(B) * Hkv * groups * sizeof(int2), 256);
 }
 
+size_t cp_paged_attn_workspace_size_for(int B, int H, int Hkv, int D, int page_size, int max_pages, cp_dtype dt) {
+  if (page_size < 1 || page_size > 65536 || max_pages < 0) return 0;
+  const size_t most = cp_paged_attn_workspace_size(B, H, Hkv, D, dt);
+  int shift = 0;
+  while ((2 << shift) <= page_size) ++shift;
+  return most && cp::paged_cluster(D, dt == CP_BF16, B, Hkv, H / Hkv, max_pages, shift) > 0 ? 0 : most;
+}
+
 cp_status cp_paged_attn_decode(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
                                const int32_t* seq_lens, void* out, float* lse, int B, int H, int Hkv, int D,
                                int num_pages, int page_size, int max_pages, float scale, float softcap,
@@ -277,7 +285,8 @@ cp_status cp_paged_attn_decode(const void* q, const void* k_cache, const void* v
   if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16) || !aligned(lse, 4) ||
       !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(slopes, 4))
     return CP_ERR_ALIGNMENT;
-  if (!workspace || ws_bytes < cp_paged_attn_workspace_size(B, H, Hkv, D, dt)) return CP_ERR_WORKSPACE;
+  const size_t need = cp_paged_attn_workspace_size_for(B, H, Hkv, D, page_size, max_pages, dt);
+  if (need && (!workspace || ws_bytes < need)) return CP_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return CP_ERR_ALIGNMENT;
   a.B = B;
   a.H = H;
@@ -297,8 +306,10 @@ cp_status cp_paged_attn_decode(const void* q, const void* k_cache, const void* v
   a.scale = scale;
   a.cap = softcap;
   a.slopes = slopes;
-  a.partial = static_cast<float*>(workspace);
-  a.info = reinterpret_cast<int2*>(static_cast<char*>(workspace) + paged_partial_bytes(a.G, D, dt));
+  if (need) {
+    a.partial = static_cast<float*>(workspace);
+    a.info = reinterpret_cast<int2*>(static_cast<char*>(workspace) + paged_partial_bytes(a.G, D, dt));
+  }
   int sms = 0;
   if ((st = static_cast<cp_status>(cp::host_device(&a.err, &sms))) != CP_OK) return st;
   return cp::launch_paged_decode(a, dt == CP_BF16, static_cast<cudaStream_t>(stream)) == cudaSuccess ? CP_OK

@@ -15,6 +15,8 @@
 // holds at most one unit (sequence, head) that began in an earlier CTA and one
 // that goes on in the next; those leave a partial (O, m, l) each, which a
 // second launch joins. Units that lie within one CTA are written directly.
+// Where the tables are short and the units few (paged_cluster), a unit is taken
+// by a cluster of CTAs instead, which joins its parts itself: one launch.
 // Each warp streams its own 16 keys of every block through kStages buffers of
 // its own with 16-byte asynchronous copies (one row of one head is 128 to 512
 // contiguous bytes), so no barrier of the CTA stands in the loop; the warps'
@@ -140,10 +142,10 @@ struct DecCfg {
   static constexpr int kWarpB = kStages * 2 * kTile;    // a warp's buffers
   static constexpr int kState = kRows * (D + 2);        // floats of a warp's state: O, then m and l
   static_assert(kStages <= 4, "have");
-  static_assert(kWarpB >= kState * 4, "a warp's buffers hold its state at the end of a unit");
+  static_assert(kWarpB >= 2 * kState * 4, "a warp's buffers hold its state at the end of a unit, the first's the CTA's too");
   static constexpr int kSmem = kDecWarps * kWarpB;
-  // two CTAs on a multiprocessor where their buffers fit
-  static constexpr int kCtas = kSmem <= 96 * 1024 ? kPagedCtas : kPagedCtas / 2;
+  static constexpr int kCtas = paged_ctas(D, kBf16);
+  static_assert(kCtas == 152 || 2 * (kSmem + kPagedMaxBatch * 4 + 2048) <= 228 * 1024, "two CTAs on a multiprocessor");
 };
 
 // A score in units of log2, dist keys back.
@@ -156,6 +158,338 @@ struct DecScore {
   }
 };
 
+// The length of sequence b, held within what its row of the table can address.
+__device__ __forceinline__ int table_len(const PagedArgs& a) {
+  return static_cast<int>(min(static_cast<int64_t>(a.max_pages) << a.page_shift, int64_t{INT_MAX - 64}));
+}
+__device__ __forceinline__ int seq_len(const PagedArgs& a, int b) {
+  const int n = a.seq_lens[b], most = table_len(a);
+  if (n < 0 || n > most) {
+    atomicOr(a.err, kDevErrPage);
+    return n < 0 ? 0 : most;
+  }
+  return n;
+}
+
+__device__ __forceinline__ void put_out(const PagedArgs& a, int64_t at, float x) {
+  if (a.out_bf16)
+    static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16(x);
+  else
+    static_cast<float*>(a.out)[at] = x;
+}
+__device__ __forceinline__ float natural_lse(float mx, float sum) {
+  return sum != 0.f ? (mx + log2f(sum)) * kLn2 : -INFINITY;
+}
+
+// Blocks [blk0, blk1) of group hg of key/value head hk's query heads, sequence b
+// of n tokens: each warp's state into its buffers, O [kRows][D], then m and l.
+template <int D, typename T>
+__device__ __forceinline__ void decode_unit(const PagedArgs& a, int b, int n, int hk, int hg, int blk0, int blk1,
+                                            uint8_t* smem, uint32_t (*have)[4]) {
+  using C = DecCfg<D, T>;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint8_t* wbuf = smem + warp * C::kWarpB;
+  const uint32_t wb = smem_addr(wbuf);
+  const int64_t tok_b = static_cast<int64_t>(a.Hkv) * C::kRowB;  // bytes of a token's row of all heads
+  DecScore score;
+  score.scale = a.scale;
+  score.cap = a.cap;
+  score.inv_cap = a.cap > 0.f ? 1.f / a.cap : 0.f;
+  const int h0 = hk * a.G + hg * C::kRows, nrow = min(C::kRows, a.G - hg * C::kRows);
+  const uint8_t* kc = static_cast<const uint8_t*>(a.k_cache) + static_cast<int64_t>(hk) * C::kRowB;
+  const uint8_t* vc = static_cast<const uint8_t*>(a.v_cache) + static_cast<int64_t>(hk) * C::kRowB;
+
+  // a chunk's rows: lane r < 16 finds row r (-1 past the end)
+  auto find = [&](int blk) {
+    const int j = blk * kPagedBlock + warp * kChunk + lane;
+    return lane < kChunk && blk < blk1 && j < n ? cache_row(a, b, j) : -1;
+  };
+  auto load = [&](int rows, int stage) {
+    const uint32_t base = wb + stage * 2 * C::kTile;
+    const uint32_t found = __ballot_sync(0xffffffffu, rows >= 0);
+    if (lane == 0) have[warp][stage] = found;
+#pragma unroll
+    for (int i = lane; i < kChunk * C::kPieces; i += 32) {
+      const int r = i / C::kPieces, p = i % C::kPieces;
+      const int row = __shfl_sync(0xffffffffu, rows, r);
+      const int64_t off = static_cast<int64_t>(max(row, 0)) * tok_b + p * 16;
+      const uint32_t d = base + r * C::kRowB + ((p ^ (r & 7)) * 16);
+      cp_async16(d, kc + off, row >= 0);
+      cp_async16(d + C::kTile, vc + off, row >= 0);
+    }
+  };
+
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  int rows_next = find(blk0);
+#pragma unroll
+  for (int st = 0; st < C::kStages - 1; ++st) {
+    if (blk0 + st < blk1) load(rows_next, st);
+    rows_next = find(blk0 + st + 1);
+    cp_async_commit();
+  }
+
+  if constexpr (C::kBf16) {
+    const int g = lane >> 2, tq = lane & 3;
+    uint32_t qf[D / 16][4];
+    {
+      const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + (static_cast<int64_t>(b) * a.H + h0) * D;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int r = g + (e & 1) * 8, d = kk * 16 + tq * 2 + (e >> 1) * 8;
+          qf[kk][e] = r < nrow ? *reinterpret_cast<const uint32_t*>(q + r * D + d) : 0u;
+        }
+    }
+    float slope[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) slope[e] = a.slopes && g + 8 * e < nrow ? a.slopes[h0 + g + 8 * e] * kL2e : 0.f;
+    float o[D / 8][4];
+#pragma unroll
+    for (int x = 0; x < D / 8; ++x)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[x][e] = 0.f;
+    const int lm = lane >> 3, lr = lane & 7;
+    const bool two = nrow > 8;
+    int stage = 0;
+    for (int blk = blk0; blk < blk1; ++blk) {
+      cp_async_wait<C::kStages - 2>();
+      __syncwarp();
+      {  // the stage that the last step read is free again
+        int st = stage + C::kStages - 1;
+        if (st >= C::kStages) st -= C::kStages;
+        if (blk + C::kStages - 1 < blk1) load(rows_next, st);
+        rows_next = find(blk + C::kStages);
+        cp_async_commit();
+      }
+      const uint32_t kb = wb + stage * 2 * C::kTile, vb = kb + C::kTile;
+      const uint32_t on = have[warp][stage];
+      float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+      const int krow = (lm >> 1) * 8 + lr;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        uint32_t f[4];
+        ldsm4(f, kb + krow * C::kRowB + (((2 * kk + (lm & 1)) ^ (krow & 7)) * 16));
+        mma16816(s[0], qf[kk], f[0], f[1]);
+        mma16816(s[1], qf[kk], f[2], f[3]);
+      }
+      const int j0 = blk * kPagedBlock + warp * kChunk + tq * 2;
+      uint32_t pf[4];
+      float fsc[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {  // rows g and g + 8
+        if (e == 1 && !two) {
+          pf[1] = pf[3] = 0u;
+          fsc[1] = 1.f;
+          break;
+        }
+        float x[4], mx = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int j = j0 + (c >> 1) * 8 + (c & 1);
+          x[c] = (on >> (tq * 2 + (c >> 1) * 8 + (c & 1))) & 1u ? score(s[c >> 1][2 * e + (c & 1)], slope[e], static_cast<float>(n - 1 - j)) : -INFINITY;
+          mx = fmaxf(mx, x[c]);
+        }
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const float mn = fmaxf(m[e], mx), base = mn == -INFINITY ? 0.f : mn;
+        fsc[e] = ex2_approx(m[e] - base);
+        m[e] = mn;
+        float sum = 0.f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          x[c] = ex2_approx(x[c] - base);
+          sum += x[c];
+        }
+        l[e] = l[e] * fsc[e] + sum;
+        // P rounded to bf16 for the matrix product; l sums it unrounded
+        pf[e] = pack_bf16x2(x[0], x[1]);
+        pf[2 + e] = pack_bf16x2(x[2], x[3]);
+      }
+      if (__any_sync(0xffffffffu, fsc[0] != 1.f || fsc[1] != 1.f)) {
+#pragma unroll
+        for (int x = 0; x < D / 8; ++x) {
+          o[x][0] *= fsc[0];
+          o[x][1] *= fsc[0];
+          o[x][2] *= fsc[1];
+          o[x][3] *= fsc[1];
+        }
+      }
+      const int vrow = (lm & 1) * 8 + lr;
+#pragma unroll
+      for (int x = 0; x < D / 16; ++x) {
+        uint32_t f[4];
+        ldsm4t(f, vb + vrow * C::kRowB + (((2 * x + (lm >> 1)) ^ (vrow & 7)) * 16));
+        mma16816(o[2 * x], pf, f[0], f[1]);
+        mma16816(o[2 * x + 1], pf, f[2], f[3]);
+      }
+      __syncwarp();
+      if (++stage == C::kStages) stage = 0;
+    }
+    // ---- this warp's state into its buffers: O [kRows][D], then m, l ----
+    cp_async_wait<0>();
+    __syncwarp();
+    float* w = reinterpret_cast<float*>(wbuf);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
+      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
+      const int r = g + 8 * e;
+#pragma unroll
+      for (int x = 0; x < D / 8; ++x)
+        *reinterpret_cast<float2*>(w + r * D + x * 8 + tq * 2) = make_float2(o[x][2 * e], o[x][2 * e + 1]);
+      if (tq == 0) {
+        w[C::kRows * D + 2 * r] = m[e];
+        w[C::kRows * D + 2 * r + 1] = l[e];
+      }
+    }
+  } else {
+    // fp32 in three passes of tf32 (tf32.cuh), keys as the rows: S^T = K Q^T
+    // (16 keys x 8 heads), then O^T = V^T P^T (D x 8 heads, 16 keys); a lane
+    // holds the statistics of heads 2 tq and 2 tq + 1
+    const int g = lane >> 2, tq = lane & 3;
+    const float* q = static_cast<const float*>(a.q) + (static_cast<int64_t>(b) * a.H + h0 + g) * D;
+    uint32_t qh[D / 8][2], ql[D / 8][2];
+#pragma unroll
+    for (int kk = 0; kk < D / 8; ++kk)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) split_tf32(g < nrow ? q[8 * kk + tq + 4 * e] : 0.f, qh[kk][e], ql[kk][e]);
+    float slope[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) slope[e] = a.slopes && 2 * tq + e < nrow ? a.slopes[h0 + 2 * tq + e] * kL2e : 0.f;
+    float o[D / 16][4];
+#pragma unroll
+    for (int x = 0; x < D / 16; ++x)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[x][e] = 0.f;
+    int stage = 0;
+    for (int blk = blk0; blk < blk1; ++blk) {
+      cp_async_wait<C::kStages - 2>();
+      __syncwarp();
+      {
+        int st = stage + C::kStages - 1;
+        if (st >= C::kStages) st -= C::kStages;
+        if (blk + C::kStages - 1 < blk1) load(rows_next, st);
+        rows_next = find(blk + C::kStages);
+        cp_async_commit();
+      }
+      const uint8_t* kb = wbuf + stage * 2 * C::kTile;
+      const uint8_t* vb = kb + C::kTile;
+      const uint32_t on = have[warp][stage];
+      // element d of row r of a tile
+      auto at = [&](const uint8_t* tile, int r, int d) {
+        return *reinterpret_cast<const float*>(tile + r * C::kRowB + (((d >> 2) ^ (r & 7)) * 16) + (d & 3) * 4);
+      };
+      float s[4] = {0.f, 0.f, 0.f, 0.f}, small[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int k0 = 0; k0 < D / 8; k0 += 4) {
+        float big[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int kk = k0; kk < k0 + 4; ++kk) {
+          uint32_t ah[4], al[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) split_tf32(at(kb, g + (e & 1) * 8, 8 * kk + tq + (e >> 1) * 4), ah[e], al[e]);
+          mma3_tf32(big, small, ah, al, qh[kk], ql[kk]);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[e] += big[e];
+      }
+      // rows (keys) g and g + 8: elements 0, 1 and 2, 3; columns (heads) 2 tq, 2 tq + 1
+      const int j0 = blk * kPagedBlock + warp * kChunk + g;
+      float f[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float x[2], mx = -INFINITY;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          x[u] = -INFINITY;
+          if ((on >> (g + 8 * u)) & 1u) {
+            x[u] = score(s[2 * u + e] + small[2 * u + e], slope[e], static_cast<float>(n - 1 - j0 - 8 * u));
+          }
+          mx = fmaxf(mx, x[u]);
+        }
+#pragma unroll
+        for (int of = 16; of > 2; of >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, of));
+        const float mn = fmaxf(m[e], mx), base = mn == -INFINITY ? 0.f : mn;
+        f[e] = exp2f(m[e] - base);
+        m[e] = mn;
+        s[e] = exp2f(x[0] - base);
+        s[2 + e] = exp2f(x[1] - base);
+        l[e] = l[e] * f[e] + s[e] + s[2 + e];
+      }
+      // P^T as the B operand: key tq (+ 4, 8, 12), head g, from lane 4 key + head / 2
+      uint32_t ph[2][2], pl[2][2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int src = (tq + 4 * e) * 4 + (g >> 1);
+          const float y0 = __shfl_sync(0xffffffffu, s[2 * u], src), y1 = __shfl_sync(0xffffffffu, s[2 * u + 1], src);
+          split_tf32(g & 1 ? y1 : y0, ph[u][e], pl[u][e]);
+        }
+#pragma unroll
+      for (int x = 0; x < D / 16; ++x) {
+        float big[4] = {0.f, 0.f, 0.f, 0.f}, sm[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          uint32_t ah[4], al[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            split_tf32(at(vb, 8 * u + tq + (e >> 1) * 4, 16 * x + g + (e & 1) * 8), ah[e], al[e]);
+          mma3_tf32(big, sm, ah, al, ph[u], pl[u]);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[x][e] = fmaf(o[x][e], f[e & 1], big[e] + sm[e]);
+      }
+      __syncwarp();
+      if (++stage == C::kStages) stage = 0;
+    }
+    cp_async_wait<0>();
+    __syncwarp();
+    float* w = reinterpret_cast<float*>(wbuf);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+#pragma unroll
+      for (int of = 16; of > 2; of >>= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], of);
+      const int r = 2 * tq + e;
+#pragma unroll
+      for (int x = 0; x < D / 16; ++x) {
+        w[r * D + 16 * x + g] = o[x][e];
+        w[r * D + 16 * x + g + 8] = o[x][2 + e];
+      }
+      if (g == 0) {
+        w[C::kRows * D + 2 * r] = m[e];
+        w[C::kRows * D + 2 * r + 1] = l[e];
+      }
+    }
+  }
+}
+
+// Element i of a unit's O over the CTA's four warps, relative to the largest
+// maximum mx of its head; sum: the weights'.
+template <int D, typename T>
+__device__ __forceinline__ float join_warps(const uint8_t* smem, int i, float& mx, float& sum) {
+  using C = DecCfg<D, T>;
+  const int r = i / D;
+  float mw[kDecWarps], acc = 0.f;
+  mx = -INFINITY;
+  sum = 0.f;
+#pragma unroll
+  for (int w = 0; w < kDecWarps; ++w) {
+    mw[w] = reinterpret_cast<const float*>(smem + w * C::kWarpB)[C::kRows * D + 2 * r];
+    mx = fmaxf(mx, mw[w]);
+  }
+  const float base = mx == -INFINITY ? 0.f : mx;
+#pragma unroll
+  for (int w = 0; w < kDecWarps; ++w) {
+    const float* st = reinterpret_cast<const float*>(smem + w * C::kWarpB);
+    const float f = exp2f(mw[w] - base);
+    sum = fmaf(st[C::kRows * D + 2 * r + 1], f, sum);
+    acc = fmaf(st[i], f, acc);
+  }
+  return acc;
+}
+
 template <int D, typename T>
 __global__ void __launch_bounds__(kDecThreads) paged_decode_kernel(const __grid_constant__ PagedArgs a) {
   using C = DecCfg<D, T>;
@@ -166,20 +500,11 @@ __global__ void __launch_bounds__(kDecThreads) paged_decode_kernel(const __grid_
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int groups = (a.G + C::kRows - 1) / C::kRows;
   const int HG = a.Hkv * groups;
-  const int cap_len = static_cast<int>(min(static_cast<int64_t>(a.max_pages) << a.page_shift, int64_t{INT_MAX - 64}));
-  auto seq_len = [&](int b) {
-    const int n = a.seq_lens[b];
-    if (n < 0 || n > cap_len) {
-      atomicOr(a.err, kDevErrPage);
-      return n < 0 ? 0 : cap_len;
-    }
-    return n;
-  };
   // ---- the work list: an exclusive sum of the sequences' blocks ----
   int carry = 0;
   for (int b0 = 0; b0 < a.B; b0 += kDecThreads) {
     const int b = b0 + threadIdx.x;
-    const int x = b < a.B ? (seq_len(b) + kPagedBlock - 1) / kPagedBlock * HG : 0;
+    const int x = b < a.B ? (seq_len(a, b) + kPagedBlock - 1) / kPagedBlock * HG : 0;
     int s = x;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -202,25 +527,12 @@ __global__ void __launch_bounds__(kDecThreads) paged_decode_kernel(const __grid_
   // sequences without a token: out 0, lse -inf
   for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
     if (cum[b + 1] != cum[b]) continue;
-    for (int i = threadIdx.x; i < a.H * D; i += kDecThreads) {
-      if (a.out_bf16)
-        static_cast<__nv_bfloat16*>(a.out)[static_cast<int64_t>(b) * a.H * D + i] = __float2bfloat16(0.f);
-      else
-        static_cast<float*>(a.out)[static_cast<int64_t>(b) * a.H * D + i] = 0.f;
-    }
+    for (int i = threadIdx.x; i < a.H * D; i += kDecThreads) put_out(a, static_cast<int64_t>(b) * a.H * D + i, 0.f);
     for (int i = threadIdx.x; i < a.H; i += kDecThreads) a.lse[static_cast<int64_t>(b) * a.H + i] = -INFINITY;
   }
   const int share = (total + gridDim.x - 1) / gridDim.x;
   const int begin = min(total, static_cast<int>(blockIdx.x) * share), end = min(total, begin + share);
   if (begin >= end) return;
-
-  uint8_t* wbuf = smem + warp * C::kWarpB;
-  const uint32_t wb = smem_addr(wbuf);
-  const int64_t tok_b = static_cast<int64_t>(a.Hkv) * C::kRowB;  // bytes of a token's row of all heads
-  DecScore score;
-  score.scale = a.scale;
-  score.cap = a.cap;
-  score.inv_cap = a.cap > 0.f ? 1.f / a.cap : 0.f;
 
   int b = 0;
   {  // the sequence of the first block
@@ -233,281 +545,14 @@ __global__ void __launch_bounds__(kDecThreads) paged_decode_kernel(const __grid_
   }
   for (int at = begin; at < end;) {
     while (cum[b + 1] <= at) ++b;
-    const int n = min(max(a.seq_lens[b], 0), cap_len);
+    const int n = min(max(a.seq_lens[b], 0), table_len(a));
     const int nblk = (n + kPagedBlock - 1) / kPagedBlock;
     const int u = (at - cum[b]) / nblk, blk0 = (at - cum[b]) - u * nblk;
     const int blk1 = min(nblk, blk0 + end - at);
     const int unit0 = at - blk0;  // the unit's first block in the list
     const int hk = u / groups, hg = u - hk * groups;
     const int h0 = hk * a.G + hg * C::kRows, nrow = min(C::kRows, a.G - hg * C::kRows);
-    const uint8_t* kc = static_cast<const uint8_t*>(a.k_cache) + static_cast<int64_t>(hk) * C::kRowB;
-    const uint8_t* vc = static_cast<const uint8_t*>(a.v_cache) + static_cast<int64_t>(hk) * C::kRowB;
-
-    // a chunk's rows: lane r < 16 finds row r (-1 past the end)
-    auto find = [&](int blk) {
-      const int j = blk * kPagedBlock + warp * kChunk + lane;
-      return lane < kChunk && blk < blk1 && j < n ? cache_row(a, b, j) : -1;
-    };
-    auto load = [&](int rows, int stage) {
-      const uint32_t base = wb + stage * 2 * C::kTile;
-      const uint32_t found = __ballot_sync(0xffffffffu, rows >= 0);
-      if (lane == 0) have[warp][stage] = found;
-#pragma unroll
-      for (int i = lane; i < kChunk * C::kPieces; i += 32) {
-        const int r = i / C::kPieces, p = i % C::kPieces;
-        const int row = __shfl_sync(0xffffffffu, rows, r);
-        const int64_t off = static_cast<int64_t>(max(row, 0)) * tok_b + p * 16;
-        const uint32_t d = base + r * C::kRowB + ((p ^ (r & 7)) * 16);
-        cp_async16(d, kc + off, row >= 0);
-        cp_async16(d + C::kTile, vc + off, row >= 0);
-      }
-    };
-
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-    int rows_next = find(blk0);
-#pragma unroll
-    for (int st = 0; st < C::kStages - 1; ++st) {
-      if (blk0 + st < blk1) load(rows_next, st);
-      rows_next = find(blk0 + st + 1);
-      cp_async_commit();
-    }
-
-    if constexpr (C::kBf16) {
-      const int g = lane >> 2, tq = lane & 3;
-      uint32_t qf[D / 16][4];
-      {
-        const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + (static_cast<int64_t>(b) * a.H + h0) * D;
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int r = g + (e & 1) * 8, d = kk * 16 + tq * 2 + (e >> 1) * 8;
-            qf[kk][e] = r < nrow ? *reinterpret_cast<const uint32_t*>(q + r * D + d) : 0u;
-          }
-      }
-      float slope[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) slope[e] = a.slopes && g + 8 * e < nrow ? a.slopes[h0 + g + 8 * e] * kL2e : 0.f;
-      float o[D / 8][4];
-#pragma unroll
-      for (int x = 0; x < D / 8; ++x)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[x][e] = 0.f;
-      const int lm = lane >> 3, lr = lane & 7;
-      const bool two = nrow > 8;
-      int stage = 0;
-      for (int blk = blk0; blk < blk1; ++blk) {
-        cp_async_wait<C::kStages - 2>();
-        __syncwarp();
-        {  // the stage that the last step read is free again
-          int st = stage + C::kStages - 1;
-          if (st >= C::kStages) st -= C::kStages;
-          if (blk + C::kStages - 1 < blk1) load(rows_next, st);
-          rows_next = find(blk + C::kStages);
-          cp_async_commit();
-        }
-        const uint32_t kb = wb + stage * 2 * C::kTile, vb = kb + C::kTile;
-        const uint32_t on = have[warp][stage];
-        float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-        const int krow = (lm >> 1) * 8 + lr;
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          uint32_t f[4];
-          ldsm4(f, kb + krow * C::kRowB + (((2 * kk + (lm & 1)) ^ (krow & 7)) * 16));
-          mma16816(s[0], qf[kk], f[0], f[1]);
-          mma16816(s[1], qf[kk], f[2], f[3]);
-        }
-        const int j0 = blk * kPagedBlock + warp * kChunk + tq * 2;
-        uint32_t pf[4];
-        float fsc[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {  // rows g and g + 8
-          if (e == 1 && !two) {
-            pf[1] = pf[3] = 0u;
-            fsc[1] = 1.f;
-            break;
-          }
-          float x[4], mx = -INFINITY;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int j = j0 + (c >> 1) * 8 + (c & 1);
-            x[c] = (on >> (tq * 2 + (c >> 1) * 8 + (c & 1))) & 1u ? score(s[c >> 1][2 * e + (c & 1)], slope[e], static_cast<float>(n - 1 - j)) : -INFINITY;
-            mx = fmaxf(mx, x[c]);
-          }
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-          const float mn = fmaxf(m[e], mx), base = mn == -INFINITY ? 0.f : mn;
-          fsc[e] = ex2_approx(m[e] - base);
-          m[e] = mn;
-          float sum = 0.f;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            x[c] = ex2_approx(x[c] - base);
-            sum += x[c];
-          }
-          l[e] = l[e] * fsc[e] + sum;
-          // P rounded to bf16 for the matrix product; l sums it unrounded
-          pf[e] = pack_bf16x2(x[0], x[1]);
-          pf[2 + e] = pack_bf16x2(x[2], x[3]);
-        }
-        if (__any_sync(0xffffffffu, fsc[0] != 1.f || fsc[1] != 1.f)) {
-#pragma unroll
-          for (int x = 0; x < D / 8; ++x) {
-            o[x][0] *= fsc[0];
-            o[x][1] *= fsc[0];
-            o[x][2] *= fsc[1];
-            o[x][3] *= fsc[1];
-          }
-        }
-        const int vrow = (lm & 1) * 8 + lr;
-#pragma unroll
-        for (int x = 0; x < D / 16; ++x) {
-          uint32_t f[4];
-          ldsm4t(f, vb + vrow * C::kRowB + (((2 * x + (lm >> 1)) ^ (vrow & 7)) * 16));
-          mma16816(o[2 * x], pf, f[0], f[1]);
-          mma16816(o[2 * x + 1], pf, f[2], f[3]);
-        }
-        __syncwarp();
-        if (++stage == C::kStages) stage = 0;
-      }
-      // ---- this warp's state into its buffers: O [kRows][D], then m, l ----
-      cp_async_wait<0>();
-      __syncwarp();
-      float* w = reinterpret_cast<float*>(wbuf);
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
-        l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
-        const int r = g + 8 * e;
-#pragma unroll
-        for (int x = 0; x < D / 8; ++x)
-          *reinterpret_cast<float2*>(w + r * D + x * 8 + tq * 2) = make_float2(o[x][2 * e], o[x][2 * e + 1]);
-        if (tq == 0) {
-          w[C::kRows * D + 2 * r] = m[e];
-          w[C::kRows * D + 2 * r + 1] = l[e];
-        }
-      }
-    } else {
-      // fp32 in three passes of tf32 (tf32.cuh), keys as the rows: S^T = K Q^T
-      // (16 keys x 8 heads), then O^T = V^T P^T (D x 8 heads, 16 keys); a lane
-      // holds the statistics of heads 2 tq and 2 tq + 1
-      const int g = lane >> 2, tq = lane & 3;
-      const float* q = static_cast<const float*>(a.q) + (static_cast<int64_t>(b) * a.H + h0 + g) * D;
-      uint32_t qh[D / 8][2], ql[D / 8][2];
-#pragma unroll
-      for (int kk = 0; kk < D / 8; ++kk)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) split_tf32(g < nrow ? q[8 * kk + tq + 4 * e] : 0.f, qh[kk][e], ql[kk][e]);
-      float slope[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) slope[e] = a.slopes && 2 * tq + e < nrow ? a.slopes[h0 + 2 * tq + e] * kL2e : 0.f;
-      float o[D / 16][4];
-#pragma unroll
-      for (int x = 0; x < D / 16; ++x)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[x][e] = 0.f;
-      int stage = 0;
-      for (int blk = blk0; blk < blk1; ++blk) {
-        cp_async_wait<C::kStages - 2>();
-        __syncwarp();
-        {
-          int st = stage + C::kStages - 1;
-          if (st >= C::kStages) st -= C::kStages;
-          if (blk + C::kStages - 1 < blk1) load(rows_next, st);
-          rows_next = find(blk + C::kStages);
-          cp_async_commit();
-        }
-        const uint8_t* kb = wbuf + stage * 2 * C::kTile;
-        const uint8_t* vb = kb + C::kTile;
-        const uint32_t on = have[warp][stage];
-        // element d of row r of a tile
-        auto at = [&](const uint8_t* tile, int r, int d) {
-          return *reinterpret_cast<const float*>(tile + r * C::kRowB + (((d >> 2) ^ (r & 7)) * 16) + (d & 3) * 4);
-        };
-        float s[4] = {0.f, 0.f, 0.f, 0.f}, small[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int k0 = 0; k0 < D / 8; k0 += 4) {
-          float big[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int kk = k0; kk < k0 + 4; ++kk) {
-            uint32_t ah[4], al[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) split_tf32(at(kb, g + (e & 1) * 8, 8 * kk + tq + (e >> 1) * 4), ah[e], al[e]);
-            mma3_tf32(big, small, ah, al, qh[kk], ql[kk]);
-          }
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s[e] += big[e];
-        }
-        // rows (keys) g and g + 8: elements 0, 1 and 2, 3; columns (heads) 2 tq, 2 tq + 1
-        const int j0 = blk * kPagedBlock + warp * kChunk + g;
-        float f[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float x[2], mx = -INFINITY;
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            x[u] = -INFINITY;
-            if ((on >> (g + 8 * u)) & 1u) {
-              x[u] = score(s[2 * u + e] + small[2 * u + e], slope[e], static_cast<float>(n - 1 - j0 - 8 * u));
-            }
-            mx = fmaxf(mx, x[u]);
-          }
-#pragma unroll
-          for (int of = 16; of > 2; of >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, of));
-          const float mn = fmaxf(m[e], mx), base = mn == -INFINITY ? 0.f : mn;
-          f[e] = exp2f(m[e] - base);
-          m[e] = mn;
-          s[e] = exp2f(x[0] - base);
-          s[2 + e] = exp2f(x[1] - base);
-          l[e] = l[e] * f[e] + s[e] + s[2 + e];
-        }
-        // P^T as the B operand: key tq (+ 4, 8, 12), head g, from lane 4 key + head / 2
-        uint32_t ph[2][2], pl[2][2];
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int src = (tq + 4 * e) * 4 + (g >> 1);
-            const float y0 = __shfl_sync(0xffffffffu, s[2 * u], src), y1 = __shfl_sync(0xffffffffu, s[2 * u + 1], src);
-            split_tf32(g & 1 ? y1 : y0, ph[u][e], pl[u][e]);
-          }
-#pragma unroll
-        for (int x = 0; x < D / 16; ++x) {
-          float big[4] = {0.f, 0.f, 0.f, 0.f}, sm[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            uint32_t ah[4], al[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              split_tf32(at(vb, 8 * u + tq + (e >> 1) * 4, 16 * x + g + (e & 1) * 8), ah[e], al[e]);
-            mma3_tf32(big, sm, ah, al, ph[u], pl[u]);
-          }
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[x][e] = fmaf(o[x][e], f[e & 1], big[e] + sm[e]);
-        }
-        __syncwarp();
-        if (++stage == C::kStages) stage = 0;
-      }
-      cp_async_wait<0>();
-      __syncwarp();
-      float* w = reinterpret_cast<float*>(wbuf);
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-#pragma unroll
-        for (int of = 16; of > 2; of >>= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], of);
-        const int r = 2 * tq + e;
-#pragma unroll
-        for (int x = 0; x < D / 16; ++x) {
-          w[r * D + 16 * x + g] = o[x][e];
-          w[r * D + 16 * x + g + 8] = o[x][2 + e];
-        }
-        if (g == 0) {
-          w[C::kRows * D + 2 * r] = m[e];
-          w[C::kRows * D + 2 * r + 1] = l[e];
-        }
-      }
-    }
-
+    decode_unit<D, T>(a, b, n, hk, hg, blk0, blk1, smem, have);
     // ---- the warps' states joined: written out, or left as a partial ----
     __syncthreads();
     const bool whole = blk0 == 0 && blk1 == nblk;
@@ -516,28 +561,12 @@ __global__ void __launch_bounds__(kDecThreads) paged_decode_kernel(const __grid_
     float* part = a.partial + (static_cast<int64_t>(blockIdx.x) * 2 + slot) * width * (D + 2);
     for (int i = threadIdx.x; i < nrow * D; i += kDecThreads) {
       const int r = i / D;
-      float mw[kDecWarps], mx = -INFINITY, sum = 0.f, acc = 0.f;
-#pragma unroll
-      for (int w = 0; w < kDecWarps; ++w) {
-        mw[w] = reinterpret_cast<const float*>(smem + w * C::kWarpB)[C::kRows * D + 2 * r];
-        mx = fmaxf(mx, mw[w]);
-      }
-      const float base = mx == -INFINITY ? 0.f : mx;
-#pragma unroll
-      for (int w = 0; w < kDecWarps; ++w) {
-        const float* st = reinterpret_cast<const float*>(smem + w * C::kWarpB);
-        const float f = exp2f(mw[w] - base);
-        sum = fmaf(st[C::kRows * D + 2 * r + 1], f, sum);
-        acc = fmaf(st[i], f, acc);
-      }
+      float mx, sum;
+      const float acc = join_warps<D, T>(smem, i, mx, sum);
       if (whole) {
         const int64_t row = static_cast<int64_t>(b) * a.H + h0 + r;
-        const float x = sum != 0.f ? acc / sum : 0.f;
-        if (a.out_bf16)
-          static_cast<__nv_bfloat16*>(a.out)[row * D + i % D] = __float2bfloat16(x);
-        else
-          static_cast<float*>(a.out)[row * D + i % D] = x;
-        if (i % D == 0) a.lse[row] = sum != 0.f ? (mx + log2f(sum)) * kLn2 : -INFINITY;
+        put_out(a, row * D + i % D, sum != 0.f ? acc / sum : 0.f);
+        if (i % D == 0) a.lse[row] = natural_lse(mx, sum);
       } else {
         part[i] = acc;
         if (i % D == 0) {
@@ -576,12 +605,8 @@ __global__ void __launch_bounds__(D) paged_join_kernel(const __grid_constant__ P
   float mx = -INFINITY, sum = 0.f, acc = 0.f;
   auto store = [&]() {
     const int64_t row = static_cast<int64_t>(b) * a.H + h;
-    const float x = sum != 0.f ? acc / sum : 0.f;
-    if (a.out_bf16)
-      static_cast<__nv_bfloat16*>(a.out)[row * D + d] = __float2bfloat16(x);
-    else
-      static_cast<float*>(a.out)[row * D + d] = x;
-    if (d == 0) a.lse[row] = sum != 0.f ? (mx + log2f(sum)) * kLn2 : -INFINITY;
+    put_out(a, row * D + d, sum != 0.f ? acc / sum : 0.f);
+    if (d == 0) a.lse[row] = natural_lse(mx, sum);
   };
   if (n <= 4) {  // every load at once
     float pm[4], pl[4], po[4];
@@ -641,12 +666,91 @@ __global__ void __launch_bounds__(D) paged_join_kernel(const __grid_constant__ P
   store();
 }
 
+// A unit by a cluster of CTAs, each with an equal part of its blocks; the parts
+// are joined through distributed shared memory. One launch and no workspace, for
+// short tables (paged_cluster).
+template <int D, typename T>
+__global__ void __launch_bounds__(kDecThreads) paged_decode_cluster_kernel(const __grid_constant__ PagedArgs a) {
+  using C = DecCfg<D, T>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ uint32_t have[kDecWarps][4];
+  const int cs = cluster_size(), rank = cluster_rank();
+  const int groups = (a.G + C::kRows - 1) / C::kRows;
+  const int u = blockIdx.x / cs, b = blockIdx.y, hk = u / groups, hg = u - hk * groups;
+  const int h0 = hk * a.G + hg * C::kRows, nrow = min(C::kRows, a.G - hg * C::kRows);
+  const int64_t row0 = static_cast<int64_t>(b) * a.H + h0;
+  const int n = seq_len(a, b);
+  if (n == 0) {  // the whole cluster leaves
+    for (int i = threadIdx.x; rank == 0 && i < nrow * D; i += kDecThreads) put_out(a, row0 * D + i, 0.f);
+    for (int r = threadIdx.x; rank == 0 && r < nrow; r += kDecThreads) a.lse[row0 + r] = -INFINITY;
+    return;
+  }
+  const int nblk = (n + kPagedBlock - 1) / kPagedBlock;
+  decode_unit<D, T>(a, b, n, hk, hg, cluster_part(nblk, rank, cs), cluster_part(nblk, rank + 1, cs), smem, have);
+  __syncthreads();
+  // this CTA's state, behind the first warp's
+  float* part = reinterpret_cast<float*>(smem) + C::kState;
+  for (int i = threadIdx.x; i < nrow * D; i += kDecThreads) {
+    float mx, sum;
+    const float acc = join_warps<D, T>(smem, i, mx, sum);
+    if (cs == 1) {
+      put_out(a, row0 * D + i, sum != 0.f ? acc / sum : 0.f);
+      if (i % D == 0) a.lse[row0 + i / D] = natural_lse(mx, sum);
+    } else {
+      part[i] = acc;
+      if (i % D == 0) {
+        part[C::kRows * D + 2 * (i / D)] = mx;
+        part[C::kRows * D + 2 * (i / D) + 1] = sum;
+      }
+    }
+  }
+  if (cs == 1) return;
+  cluster_sync();
+  const uint32_t mine = smem_addr(part);
+  const int end = 2 * cluster_part(nrow * D / 2, rank + 1, cs);
+  for (int i = 2 * (cluster_part(nrow * D / 2, rank, cs) + threadIdx.x); i < end; i += 2 * kDecThreads) {
+    const int r = i / D;
+    float2 ml[8], o[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      ml[c] = make_float2(-INFINITY, 0.f);
+      o[c] = make_float2(0.f, 0.f);
+      if (c < cs) {  // every load under way at once
+        const uint32_t at = cluster_peer(mine, c);
+        ml[c] = ld_peer2(at + (C::kRows * D + 2 * r) * 4);
+        o[c] = ld_peer2(at + i * 4);
+      }
+    }
+    float mx = -INFINITY, sum = 0.f, x = 0.f, y = 0.f;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) mx = fmaxf(mx, ml[c].x);
+    const float base = mx == -INFINITY ? 0.f : mx;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      const float f = exp2f(ml[c].x - base);
+      sum = fmaf(ml[c].y, f, sum);
+      x = fmaf(o[c].x, f, x);
+      y = fmaf(o[c].y, f, y);
+    }
+    put_out(a, row0 * D + i, sum != 0.f ? x / sum : 0.f);
+    put_out(a, row0 * D + i + 1, sum != 0.f ? y / sum : 0.f);
+    if (i % D == 0) a.lse[row0 + r] = natural_lse(mx, sum);
+  }
+  cluster_sync();  // a CTA's shared memory stays until its peers have read it
+}
+
 template <int D, typename T>
 cudaError_t decode_d(const PagedArgs& a, cudaStream_t s) {
   using C = DecCfg<D, T>;
   static_assert(C::kSmem + (kPagedMaxBatch + 8) * 4 <= 227 * 1024, "shared memory budget");
-  cudaError_t e = allow_smem<paged_decode_kernel<D, T>>(C::kSmem);
-  if (e != cudaSuccess) return e;
+  cudaError_t e;
+  const int cs = paged_cluster(D, C::kBf16, a.B, a.Hkv, a.G, a.max_pages, a.page_shift);
+  if (cs > 0) {
+    if ((e = allow_smem<paged_decode_cluster_kernel<D, T>>(C::kSmem)) != cudaSuccess) return e;
+    const int units = a.Hkv * ((a.G + C::kRows - 1) / C::kRows);
+    return launch_clusters(paged_decode_cluster_kernel<D, T>, units, a.B, 1, cs, kDecThreads, C::kSmem, false, s, a);
+  }
+  if ((e = allow_smem<paged_decode_kernel<D, T>>(C::kSmem)) != cudaSuccess) return e;
   // blocks of the list if every table were full; a unit of one block is never split
   const int groups = (a.G + C::kRows - 1) / C::kRows;
   const int64_t per_unit = ((static_cast<int64_t>(a.max_pages) << a.page_shift) + kPagedBlock - 1) / kPagedBlock;

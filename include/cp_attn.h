@@ -475,6 +475,9 @@ cp_status cp_paged_kv_append(const void* k_new, const void* v_new, void* k_cache
 /* Host-only: bytes of device workspace of cp_paged_attn_decode (256-byte
  * aligned start; every byte used is written before it is read). */
 size_t cp_paged_attn_workspace_size(int B, int H, int Hkv, int D, cp_dtype dt);
+/* Host-only: the same for one size of table: 0 where the call takes one launch
+ * (short tables) and needs none, else cp_paged_attn_workspace_size's bytes. */
+size_t cp_paged_attn_workspace_size_for(int B, int H, int Hkv, int D, int page_size, int max_pages, cp_dtype dt);
 
 /*
  * Attention of one new token per sequence, q [B, H, D] (dt), over its

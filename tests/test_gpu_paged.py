@@ -108,6 +108,41 @@ def test_decode(name, H, Hkv, D, page, dt, out_dt):
     assert cpa().cp_check_device_status() == 0
 
 
+def widened(s, tokens):
+    """The table with room for more tokens; the columns behind hold no page and are not read."""
+    s = dict(s)
+    B, pages = s["table"].shape
+    extra = max(0, tokens // s["k"].shape[1] - pages)
+    s["table"] = torch.cat([s["table"], torch.full((B, extra), -1, dtype=torch.int32)], 1).contiguous()
+    return s
+
+
+# tables of up to 2, 4, 8, 16, 64 blocks of 64 tokens, and one that only the list of blocks takes
+@pytest.mark.parametrize("tokens", [128, 256, 512, 1024, 4096, 40000])
+@pytest.mark.parametrize("H,Hkv,D,page,dt,out_dt", [
+    (24, 8, 128, 16, BF, BF),
+    (20, 1, 128, 1, BF, F4),
+    (8, 1, 64, 128, BF, BF),
+    (6, 3, 128, 32, F4, F4),
+    (18, 2, 64, 64, F4, F4),
+])
+def test_decode_whatever_the_table_holds(tokens, H, Hkv, D, page, dt, out_dt):
+    from context_attention_dits_gb300 import cp_paged_attn_workspace_size as size
+    lens = [min(tokens, n) for n in (128, 0, 1, 65, 127)]
+    s = widened(make(lens, H, Hkv, D, page, dt, seed=tokens), tokens)
+    if tokens <= 128 or tokens == 40000:
+        assert (size(5, H, Hkv, D, dt, page_size=page, max_pages=s["table"].shape[1]) > 0) == (tokens == 40000)
+    out, lse = decode(s, D ** -0.5, out_dt, softcap=20.0)
+    check_decode(s, D ** -0.5, out, lse, f"{tokens}", 20.0)
+    assert cpa().cp_check_device_status() == 0
+    s["table"][3, 0] = -7   # sequence 3 loses its first page (all of it, where pages are of 128), the others nothing
+    bad, bl = decode(s, D ** -0.5, out_dt, softcap=20.0)
+    assert cpa().cp_check_device_status() == -1
+    rest = [0, 1, 2, 4]
+    assert torch.equal(bad[rest], out[rest]) and torch.equal(bl[rest], lse[rest])
+    assert (bl[3] < lse[3]).all() and (page < 65 or ((bad[3] == 0).all() and torch.isneginf(bl[3]).all()))
+
+
 @pytest.mark.parametrize("dt", [BF, F4])
 @pytest.mark.parametrize("cap,bias", [(30.0, False), (0.5, False), (0.0, True), (20.0, True), (1e5, False)])
 def test_decode_score_rule(dt, cap, bias):
@@ -288,7 +323,7 @@ def test_wrapper_refusals():
         with pytest.raises(TypeError):
             f(**bad)
     with pytest.raises(cpa().CpError):
-        f(workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+        f(t=s["table"].repeat(1, 4096), workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
     new = torch.zeros((2, 1, 2, 64), dtype=BF, device="cuda")
     with pytest.raises(ValueError):
         cpa().cp_paged_kv_append(new, new[:, :0], s["k"], s["v"], s["table"], s["lens"])

@@ -96,7 +96,11 @@ def test_paged_calls_reject_before_launch():
                 dict(most=1 << 30, page=16), dict(B=4096, most=1 << 20, page=64, Hkv=8)):
         assert decode(**bad) == inv, bad
     need = cpa.cp_paged_attn_workspace_size(2, 8, 2, 64)
-    assert need > 0 and decode(n=need - 1) == _lib.CP_ERR_WORKSPACE and decode(ws=0) == _lib.CP_ERR_WORKSPACE
+    assert need > 0 and decode(n=need - 1, most=4096) == _lib.CP_ERR_WORKSPACE
+    assert decode(ws=0, most=4096) == _lib.CP_ERR_WORKSPACE
+    # a short table takes one launch and no workspace, a long one what the size without a table says
+    assert cpa.cp_paged_attn_workspace_size(2, 8, 2, 64, page_size=16, max_pages=4) == 0
+    assert cpa.cp_paged_attn_workspace_size(2, 8, 2, 64, page_size=16, max_pages=4096) == need
     assert decode(ws=P + 16) == _lib.CP_ERR_ALIGNMENT
     assert decode(B=0) == 0
 
