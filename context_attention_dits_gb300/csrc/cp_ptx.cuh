@@ -127,6 +127,35 @@ __device__ __forceinline__ uint32_t cluster_peer(uint32_t addr, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
 }
+// Asks for the block index of a block of this grid that has not started (it will
+// not start then): 16 bytes at dst, complete on the mbarrier. Not to be asked
+// again once it has found none.
+__device__ __forceinline__ void next_block_ask(uint32_t dst, uint32_t bar) {
+  asm volatile(
+      "fence.proxy.async.shared::cta;\n\t"  // (the last answer has been read)
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(dst),
+      "r"(bar)
+      : "memory");
+}
+// The answer: false if there was none.
+__device__ __forceinline__ bool next_block(uint32_t at, int& x, int& y, int& z) {
+  uint32_t found, bx, by, bz;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b128 a;\n\t.reg .b64 lo, hi;\n\t"
+      "ld.shared.v2.b64 {lo, hi}, [%4];\n\t"
+      "mov.b128 a, {lo, hi};\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, a;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t"
+      "mov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\tmov.u32 %3, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, %2, %3, _}, a;\n\t}"
+      : "=&r"(found), "=&r"(bx), "=&r"(by), "=&r"(bz)
+      : "r"(at)
+      : "memory");
+  x = bx;
+  y = by;
+  z = bz;
+  return found != 0;
+}
 __device__ __forceinline__ float4 ld_peer4(uint32_t addr) {
   float4 v;
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
@@ -153,6 +182,20 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, uint
       "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
       : "memory");
 }
+
+// The way back: the part of the box that lies within the tensor, from shared
+// memory that this thread's fence_async has put in order. One bulk group each.
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void tma_store_4d(const void* tmap, uint32_t src, int c0, int c1, int c2, int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3, %4}], [%5];\n\t"
+      "cp.async.bulk.commit_group;" ::"l"(reinterpret_cast<uint64_t>(tmap)),
+      "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(src)
+      : "memory");
+}
+// This thread's stores have read their shared memory; have been carried out.
+__device__ __forceinline__ void tma_store_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void tma_store_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 // Untiled bulk copy of `bytes` (a multiple of 16) from global memory to this
 // CTA's shared memory, both addresses 16-byte aligned, completing on an

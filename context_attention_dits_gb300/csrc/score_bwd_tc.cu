@@ -339,7 +339,7 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap& tq64, const CUtensor
   // sub-steps: the sub-tiles of every query head, head by head; this CTA's part of them
   const int all = per_head * a.G, j0 = cluster_part(all, rank, cs), NJ = cluster_part(all, rank + 1, cs) - j0;
   struct HeadWalk {
-    TileWalk first, w;
+    TileWalk<> first, w;
     int h;
     __device__ __forceinline__ HeadWalk(const uint32_t* bits, int t0, int t1, int per_head, int h0, int j)
         : first(bits, t0, t1, t0 - 1), w(first), h(h0) {
@@ -750,7 +750,7 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap& tq64, const CUtensorMa
         }
     }
     int issued[kDqSlots] = {};
-    TileWalk cur(bits, 0, ntk, -1);
+    TileWalk<> cur(bits, 0, ntk, -1);
     for (int j = 0; j < NJ; ++j) {
       const int s = j % kDqSlots;
       const uint32_t ph = (j / kDqSlots) & 1;
@@ -889,7 +889,7 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap& tq64, const CUtensorMa
     const int qd = a.qdoc && row < nq ? a.qdoc[static_cast<int64_t>(b) * a.Sq + q0 + row] : -1;
     const int* kdoc = a.kdoc + static_cast<int64_t>(b) * a.Skv;
     const float slope2 = kBias ? a.slopes[h] * kLog2e : 0.f;
-    TileWalk cur(bits, 0, ntk, -1);
+    TileWalk<> cur(bits, 0, ntk, -1);
     for (int j = 0; ok && j < NJ; ++j) {
       const int ts = j % kTS;
       const int j0 = cur.t * kSub + hc * 32;  // the key of this warp's first column

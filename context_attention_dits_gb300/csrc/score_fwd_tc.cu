@@ -24,10 +24,10 @@
 //     below 1/2 (or 1), checked after the fact by the largest s^2; see
 //     score_math.cuh;
 //   * bias: one more FMA a score in tiles on one side of the diagonal.
-// After the first tile P is formed with the running maximum and checked
-// afterwards by the row's sum (<= 2^8) and largest s^2; a warp that fails
-// reloads S and takes the exact path (maximum first). Long causal rows are
-// launched first, so that the short ones fill the last wave.
+// P is formed with whatever reference the row has, 0 at first, in place of the
+// running maximum, and checked afterwards by the row's sum (2^-32 to 2^32, far
+// from where fp32 or bf16 end) and largest s^2; a warp that fails reloads S and
+// takes the exact path (maximum first).
 // Every wait is bounded (cp_ptx.cuh); on expiry the CTA drains its copies and
 // MMAs, frees TMEM and returns.
 // A few rows against many keys (a chunk of a long prompt) are too few items for
@@ -51,10 +51,14 @@
 namespace cp {
 namespace {
 
-constexpr int kThreads = 320;
+constexpr int kThreads = 352;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: rescale only when the max grows by > 2^8
+constexpr float kSumMost = 4294967296.f;   // of a row's P over a tile
 constexpr uint32_t kTmemCols = 512;
-constexpr int kMapWords = kScoreMaxTokens / kTileN / 32;  // bitmap of key tiles
+// Words of a bitmap of key tiles: a bit for a tile up to 262144 keys, for 2, 4
+// or 8 neighbours beyond.
+constexpr int kMapWords = 64;
+static_assert(kScoreMaxTokens / kTileN <= kMapWords * 32 * 8, "groups of 8 at most");
 
 template <int D>
 struct Smem {
@@ -64,29 +68,46 @@ struct Smem {
   static constexpr int kOffQ = 0;
   static constexpr int kOffK = kOffQ + 2 * kQTile;
   static constexpr int kOffV = kOffK + 2 * kKVTile;
-  static constexpr int kOffBar = kOffV + 2 * kKVTile;
-  static constexpr int kNumBars = 17;
-  static constexpr int kOffMisc = kOffBar + kNumBars * 8;
-  static constexpr int kOffStat = kOffMisc + 24;             // [256] rows' m, l (clusters)
-  static constexpr int kOffMap = kOffStat + 2 * kTileM * 8;              // act, then which tiles are mixed for query tile 0, 1
-  static constexpr int kBytes = kOffMap + 3 * kMapWords * 4;
+  static constexpr int kOffStage = kOffV + 2 * kKVTile;  // a softmax warp's 32 rows x 128 bytes of out on their way
+  static constexpr int kOffStat = kOffStage;             // (clusters) [256] rows' m, l
+  static constexpr int kOffBar = kOffStage + 8 * 4096;
+  static constexpr int kNumBars = 25;
+  static constexpr int kOffNext = (kOffBar + kNumBars * 8 + 15) / 16 * 16;  // the next block's index
+  static constexpr int kOffItem = kOffNext + 16;                          // [2] Item
+  static constexpr int kOffMisc = kOffItem + 2 * 32;
+  static constexpr int kOffMap = kOffMisc + 16;  // [2] act, then which tiles are mixed for query tile 0, 1
+  static constexpr int kBytes = kOffMap + 2 * 3 * kMapWords * 4;
   // slack to align the base to 1024 bytes; at least 116 KB so that two CTAs
   // never share an SM (each allocates all 512 TMEM columns)
   static constexpr int kAlloc = (kBytes + 1024) > 116 * 1024 ? (kBytes + 1024) : 116 * 1024;
 };
 
+// A work item: a pair of query tiles (the last may be single) of one head, and
+// this CTA's part of the walk over its key tiles.
+struct Item {
+  int valid;  // 0: there are no more
+  int h, b, row0;
+  int plim, ntile;  // prefix_limit; key tiles that the last row reaches
+  int n0, NT;       // this CTA's tiles: NT of those that take part, from the n0-th on
+};
+static_assert(sizeof(Item) == 32, "kOffMisc");
+
 // barrier indices
 enum : int {
-  kBarQFull = 0,
-  kBarKFull = 1,   // +stage
-  kBarKEmpty = 3,  // +stage
-  kBarVFull = 5,   // +stage
-  kBarVEmpty = 7,  // +stage
-  kBarSFull = 9,   // +tile
-  kBarPFull = 11,  // +tile
-  kBarOFull = 13,  // +tile
-  kBarDrain = 15,
-  kBarQFull1 = 16,  // Q tile 1 (Q tile 0 completes kBarQFull)
+  kBarQFull = 0,      // +tile
+  kBarQEmpty = 2,     // +tile: the item's last S has read Q
+  kBarKFull = 4,      // +stage
+  kBarKEmpty = 6,     // +stage
+  kBarVFull = 8,      // +stage
+  kBarVEmpty = 10,    // +stage
+  kBarSFull = 12,     // +tile
+  kBarPFull = 14,     // +tile
+  kBarOFull = 16,     // +tile
+  kBarItemFull = 18,  // +slot: an Item and its bitmaps are set
+  kBarItemEmpty = 20, // +slot: producer, issuer and the softmax warps have read them
+  kBarNear = 22,      // the item's last tiles are being loaded
+  kBarNext = 23,      // the next block's index is there
+  kBarDrain = 24,
 };
 
 // Bounded wait that ignores the abort flag (used while draining).
@@ -111,7 +132,7 @@ __device__ __forceinline__ void tmem_pin(uint32_t (&r)[N]) {
 template <int D, bool kCap, bool kBias>
 __global__ void __launch_bounds__(kThreads, 1)
     score_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
-                        const __grid_constant__ CUtensorMap tv, const __grid_constant__ ScoreArgs a,
+                        const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap to, const __grid_constant__ ScoreArgs a,
                         const __grid_constant__ CapCoef cc) {
   using L = Smem<D>;
   extern __shared__ uint8_t smem_raw[];
@@ -121,27 +142,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int lane = threadIdx.x & 31;
   uint32_t* misc = reinterpret_cast<uint32_t*>(smem + L::kOffMisc);  // [0] TMEM base, [1] abort flag, [2] tiles
   volatile uint32_t* abort_flag = misc + 1;
-  uint32_t* act = reinterpret_cast<uint32_t*>(smem + L::kOffMap);
-  uint32_t* mixed = act + kMapWords;  // [2][kMapWords]
   auto bar = [&](int i) -> uint32_t { return sb + L::kOffBar + 8 * i; };
-
-  // ---- work item: a pair of query tiles (the last may be single); the pairs
-  // with the most causal keys first, heads fastest ----
-  // (head and rank in x, batch entry in y, pair in z: no index needs a division)
+  auto item_at = [&](int slot) { return reinterpret_cast<Item*>(smem + L::kOffItem) + slot; };
+  auto map_at = [&](int slot) { return reinterpret_cast<uint32_t*>(smem + L::kOffMap) + slot * 3 * kMapWords; };
   const int cs = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
-  const int h = static_cast<int>(blockIdx.x) >> (__ffs(cs) - 1), b = blockIdx.y, hk = h / a.G;
-  const int item = gridDim.z - 1 - blockIdx.z;
-  const int row0 = item * 2 * kTileM;
-  const int nrows = min(2 * kTileM, a.Sq - row0);
-  const int nq = nrows > kTileM ? 2 : 1;
-  const int plim = prefix_limit(a, b);
-  // key tiles that the last row (the largest limit) reaches
-  const int ntile = (max(0, min(a.Skv, key_limit(a, plim, row0 + nrows - 1))) + kTileN - 1) / kTileN;
+  int shift = 0;  // a bit of the bitmaps is for 2^shift key tiles
+  while (((a.Skv + kTileN - 1) / kTileN) >> shift > kMapWords * 32) ++shift;
+  // with a bias the nearest keys weigh most: from the rows' own position
+  // outwards, so that the running maximum is found first and keeps
+  auto walk_start = [&](const Item& t) {
+    return kBias ? min(t.ntile - 1, max(-1, (a.rel + min(t.row0 + 2 * kTileM, a.Sq) - 1) / kTileN)) : -1;
+  };
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < L::kNumBars; ++i) mbar_init(bar(i), (i == kBarPFull || i == kBarPFull + 1) ? 4 : 1);
+    for (int i = 0; i < L::kNumBars; ++i)
+      mbar_init(bar(i), (i == kBarPFull || i == kBarPFull + 1) ? 4 : (i == kBarItemEmpty || i == kBarItemEmpty + 1) ? 10 : 1);
     misc[1] = 0;
-    misc[2] = 0;
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -151,88 +167,146 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  int NT = ntile;
-  if (a.qdoc) {
-    grid_wait();  // the document ranges
-    const int nqb = (a.Sq + kDocBlock - 1) / kDocBlock, nkb = (a.Skv + kDocBlock - 1) / kDocBlock;
-    const DocRange* qr = a.qrange + static_cast<int64_t>(b) * nqb;
-    const DocRange* kr = a.krange + static_cast<int64_t>(b) * nkb;
-    const DocRange q0 = doc_span(qr, nqb, row0 / kDocBlock, 2), q1 = doc_span(qr, nqb, row0 / kDocBlock + 2, 2);
-    for (int t0 = warp * 32; t0 < ntile; t0 += kThreads) {
-      const int t = t0 + lane;
-      const DocRange k = doc_span(kr, nkb, 2 * t, 2);
-      const uint32_t w = __ballot_sync(0xffffffffu, t < ntile && (docs_meet(q0, k) || docs_meet(q1, k)));
-      const uint32_t m0 = __ballot_sync(0xffffffffu, !docs_same(q0, k)), m1 = __ballot_sync(0xffffffffu, !docs_same(q1, k));
-      if (lane == 0) {
-        act[t0 >> 5] = w;
-        mixed[t0 >> 5] = m0;
-        mixed[kMapWords + (t0 >> 5)] = m1;
-        atomicAdd(&misc[2], __popc(w));
-      }
-    }
-    __syncthreads();
-    NT = static_cast<int>(misc[2]);
-  }
-  const uint32_t* bits = a.qdoc ? act : nullptr;
-  // this CTA's part of the walk: NT tiles from the n0-th on
-  const int n0 = cluster_part(NT, rank, cs);
-  NT = cluster_part(NT, rank + 1, cs) - n0;
-  // with a bias the nearest keys weigh most: from the rows' own position
-  // outwards, so that the running maximum is found first and keeps
-  const int start = kBias ? min(ntile - 1, max(-1, (a.rel + row0 + nrows - 1) / kTileN)) : -1;
   const uint32_t tmem = misc[0];
   const uint64_t tmo = a.timeout_ns;
 
-  if (warp == 0) {
+  if (warp == kThreads / 32 - 1) {
+    // ===================== items =====================
+    // The first is this block's own; then, once the last tiles of an item are
+    // being loaded, a block that has not started gives up its own: setting up
+    // and the first loads of an item then go by under the last products and the
+    // stores of the one before. In a cluster there is the one item.
+    if (a.qdoc) grid_wait();  // the document ranges
+    // (head and rank in x, batch entry in y, pair in z, the pairs with the most
+    // causal keys first, heads fastest: no index needs a division)
+    int x = static_cast<int>(blockIdx.x) >> (__ffs(cs) - 1), y = blockIdx.y, z = blockIdx.z;
+    bool more = true;
+    for (int n = 0;; ++n) {
+      const int slot = n & 1;
+      if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar(kBarItemEmpty + slot), ((n >> 1) & 1) ^ 1, abort_flag, a.err, tmo)))
+        break;
+      Item t{};
+      if (more) {
+        t.valid = 1;
+        t.h = x;
+        t.b = y;
+        t.row0 = (static_cast<int>(gridDim.z) - 1 - z) * 2 * kTileM;
+        t.plim = prefix_limit(a, t.b);
+        // key tiles that the last row (the largest limit) reaches
+        t.ntile = (max(0, min(a.Skv, key_limit(a, t.plim, min(t.row0 + 2 * kTileM, a.Sq) - 1))) + kTileN - 1) / kTileN;
+        int tiles = t.ntile;
+        if (a.qdoc) {
+          uint32_t* act = map_at(slot);
+          const int nqb = (a.Sq + kDocBlock - 1) / kDocBlock, nkb = (a.Skv + kDocBlock - 1) / kDocBlock;
+          const DocRange* qr = a.qrange + static_cast<int64_t>(t.b) * nqb;
+          const DocRange* kr = a.krange + static_cast<int64_t>(t.b) * nkb;
+          const DocRange q0 = doc_span(qr, nqb, t.row0 / kDocBlock, 2), q1 = doc_span(qr, nqb, t.row0 / kDocBlock + 2, 2);
+          tiles = 0;
+          const int groups = (t.ntile + (1 << shift) - 1) >> shift;
+#pragma unroll 4
+          for (int g0 = 0; g0 < groups; g0 += 32) {
+            const int gr = g0 + lane;
+            const DocRange k = doc_span(kr, nkb, (2 * gr) << shift, 2 << shift);
+            const bool on = gr < groups && (docs_meet(q0, k) || docs_meet(q1, k));
+            const uint32_t w = __ballot_sync(0xffffffffu, on);
+            const uint32_t m0 = __ballot_sync(0xffffffffu, !docs_same(q0, k)), m1 = __ballot_sync(0xffffffffu, !docs_same(q1, k));
+            if (lane == 0) {
+              act[g0 >> 5] = w;
+              act[kMapWords + (g0 >> 5)] = m0;
+              act[2 * kMapWords + (g0 >> 5)] = m1;
+            }
+            tiles += on ? min(1 << shift, t.ntile - (gr << shift)) : 0;
+          }
+          tiles = __reduce_add_sync(0xffffffffu, tiles);
+        }
+        // this CTA's part of the walk
+        t.n0 = cluster_part(tiles, rank, cs);
+        t.NT = cluster_part(tiles, rank + 1, cs) - t.n0;
+      }
+      if (lane == 0) {
+        *item_at(slot) = t;
+        mbar_arrive(bar(kBarItemFull + slot));
+      }
+      if (!more) break;
+      more = false;
+      if (cs > 1) continue;
+      if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar(kBarNear), n & 1, abort_flag, a.err, tmo))) break;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(bar(kBarNext), 16);
+        next_block_ask(sb + L::kOffNext, bar(kBarNext));
+      }
+      if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar(kBarNext), n & 1, abort_flag, a.err, tmo))) {
+        drain_wait(bar(kBarNext), n & 1, tmo);
+        break;
+      }
+      more = next_block(sb + L::kOffNext, x, y, z);
+      __syncwarp();  // every lane has read the answer
+    }
+  } else if (warp == 0) {
     // ===================== TMA producer =====================
     const bool leader = elect_one();
-    if (NT > 0) {
-      if (leader) {
-        tma_prefetch_desc(&tq);
-        tma_prefetch_desc(&tk);
-        tma_prefetch_desc(&tv);
-      }
-      int k_issued[2] = {0, 0}, v_issued[2] = {0, 0};
-      auto load_q = [&](int i) {
-        if (!leader) return;
-        const uint32_t qb = bar(i == 0 ? kBarQFull : kBarQFull1);
-        mbar_arrive_expect_tx(qb, L::kQTile);
-        for (int c = 0; c < D / 64; ++c)
-          tma_load_4d(sb + L::kOffQ + i * L::kQTile + c * L::kHalf, &tq, qb, c * 64, h, row0 + i * kTileM, b);
+    if (leader) {
+      tma_prefetch_desc(&tq);
+      tma_prefetch_desc(&tk);
+      tma_prefetch_desc(&tv);
+    }
+    int k_issued[2] = {0, 0}, v_issued[2] = {0, 0}, q_issued[2] = {0, 0};
+    int g = 0;  // key tiles so far, of all items
+    bool ok = true;
+    for (int n = 0; ok; ++n) {
+      const int slot = n & 1;
+      if (!mbar_wait_bounded(bar(kBarItemFull + slot), (n >> 1) & 1, abort_flag, a.err, tmo)) break;
+      const Item t = *item_at(slot);
+      if (!t.valid) break;
+      const int hk = t.h / a.G;
+      auto load_q = [&](int i) -> bool {
+        const uint32_t qb = bar(kBarQFull + i);
+        if (!mbar_wait_bounded(bar(kBarQEmpty + i), (q_issued[i] & 1) ^ 1, abort_flag, a.err, tmo)) return false;
+        if (leader) {
+          mbar_arrive_expect_tx(qb, L::kQTile);
+          for (int c = 0; c < D / 64; ++c)
+            tma_load_4d(sb + L::kOffQ + i * L::kQTile + c * L::kHalf, &tq, qb, c * 64, t.h, t.row0 + i * kTileM, t.b);
+        }
+        ++q_issued[i];
+        return true;
       };
-      load_q(0);
-      TileWalk cur(bits, 0, ntile, start);
-      for (int n = 0; n < n0; ++n) cur.next();
-      for (int it = 0; it < NT; ++it) {
-        const int s = it & 1;
-        const uint32_t ph = (it >> 1) & 1;
-        if (!mbar_wait_bounded(bar(kBarKEmpty + s), ph ^ 1, abort_flag, a.err, tmo)) break;
+      const int near = max(0, t.NT - 3);
+      if (t.NT == 0 && leader) mbar_arrive(bar(kBarNear));
+      if (t.NT > 0) ok = load_q(0);
+      TileWalk<true> cur(a.qdoc ? map_at(slot) : nullptr, 0, t.ntile, walk_start(t), shift);
+      for (int k = 0; k < t.n0; ++k) cur.next();
+      for (int it = 0; ok && it < t.NT; ++it, ++g) {
+        const int s = g & 1;
+        const uint32_t ph = (g >> 1) & 1;
+        if (it == near && leader) mbar_arrive(bar(kBarNear));
+        if (!(ok = mbar_wait_bounded(bar(kBarKEmpty + s), ph ^ 1, abort_flag, a.err, tmo))) break;
         if (leader) {
           mbar_arrive_expect_tx(bar(kBarKFull + s), L::kKVTile);
           for (int c = 0; c < D / 64; ++c)
             tma_load_4d(sb + L::kOffK + s * L::kKVTile + c * L::kHalf, &tk, bar(kBarKFull + s), c * 64, hk,
-                        cur.t * kTileN, b);
+                        cur.t * kTileN, t.b);
         }
         ++k_issued[s];
-        if (it == 0 && nq == 2) load_q(1);
-        if (!mbar_wait_bounded(bar(kBarVEmpty + s), ph ^ 1, abort_flag, a.err, tmo)) break;
+        if (it == 0 && t.row0 + kTileM < a.Sq && !(ok = load_q(1))) break;
+        if (!(ok = mbar_wait_bounded(bar(kBarVEmpty + s), ph ^ 1, abort_flag, a.err, tmo))) break;
         if (leader) {
           mbar_arrive_expect_tx(bar(kBarVFull + s), L::kKVTile);
           for (int c = 0; c < D / 64; ++c)
             tma_load_4d(sb + L::kOffV + s * L::kKVTile + c * L::kHalf, &tv, bar(kBarVFull + s), c * 64, hk,
-                        cur.t * kTileN, b);
+                        cur.t * kTileN, t.b);
         }
         ++v_issued[s];
         cur.next();
       }
-      if (*abort_flag) {
-        // let every issued copy land before the CTA's shared memory goes away
-        drain_wait(bar(kBarQFull), 0, tmo);
-        if (nq == 2 && k_issued[0] > 0) drain_wait(bar(kBarQFull1), 0, tmo);
-        for (int s = 0; s < 2; ++s) {
-          if (k_issued[s]) drain_wait(bar(kBarKFull + s), (k_issued[s] - 1) & 1, tmo);
-          if (v_issued[s]) drain_wait(bar(kBarVFull + s), (v_issued[s] - 1) & 1, tmo);
-        }
+      __syncwarp();
+      if (leader) mbar_arrive(bar(kBarItemEmpty + slot));
+    }
+    if (*abort_flag) {
+      // let every issued copy land before the CTA's shared memory goes away
+      for (int s = 0; s < 2; ++s) {
+        if (q_issued[s]) drain_wait(bar(kBarQFull + s), (q_issued[s] - 1) & 1, tmo);
+        if (k_issued[s]) drain_wait(bar(kBarKFull + s), (k_issued[s] - 1) & 1, tmo);
+        if (v_issued[s]) drain_wait(bar(kBarVFull + s), (v_issued[s] - 1) & 1, tmo);
       }
     }
   } else if (warp == 1) {
@@ -240,77 +314,91 @@ __global__ void __launch_bounds__(kThreads, 1)
     // The whole warp runs the loop (every operand is warp-uniform); one
     // elected lane issues the MMAs and commits.
     const bool leader = elect_one();
-    if (NT > 0) {
-      constexpr uint32_t idesc_s = idesc_bf16_f32(kTileM, kTileN, false, false);
-      constexpr uint32_t idesc_o = idesc_bf16_f32(kTileM, D, false, true);
-      // Descriptor halves of every operand buffer, built once (see
-      // mma_ss_lohi: nothing but an add may sit between two MMAs).
-      const uint64_t dq = smem_desc_sw128(sb + L::kOffQ, 16, 1024);
-      const uint64_t dk = smem_desc_sw128(sb + L::kOffK, 16, 1024);
-      const uint64_t dv = smem_desc_sw128(sb + L::kOffV, L::kHalf, 1024);
-      const uint32_t qk_hi = static_cast<uint32_t>(dq >> 32);  // same for Q and K (SBO 1024, 128B swizzle)
-      const uint32_t v_hi = static_cast<uint32_t>(dv >> 32);
-      const uint32_t q_lo = static_cast<uint32_t>(dq), k_lo = static_cast<uint32_t>(dk);
-      const uint32_t v_lo = static_cast<uint32_t>(dv);
-      auto commit = [&](uint32_t bar_addr) {
-        if (leader) mma_commit(bar_addr);
-      };
-      auto issue_s = [&](int i, int stage) {
-        const uint32_t a0 = q_lo + ((i * L::kQTile) >> 4);
-        const uint32_t b0 = k_lo + ((stage * L::kKVTile) >> 4);
-        const uint32_t d_tmem = tmem + i * kTileN;
+    constexpr uint32_t idesc_s = idesc_bf16_f32(kTileM, kTileN, false, false);
+    constexpr uint32_t idesc_o = idesc_bf16_f32(kTileM, D, false, true);
+    // Descriptor halves of every operand buffer, built once (see
+    // mma_ss_lohi: nothing but an add may sit between two MMAs).
+    const uint64_t dq = smem_desc_sw128(sb + L::kOffQ, 16, 1024);
+    const uint64_t dk = smem_desc_sw128(sb + L::kOffK, 16, 1024);
+    const uint64_t dv = smem_desc_sw128(sb + L::kOffV, L::kHalf, 1024);
+    const uint32_t qk_hi = static_cast<uint32_t>(dq >> 32);  // same for Q and K (SBO 1024, 128B swizzle)
+    const uint32_t v_hi = static_cast<uint32_t>(dv >> 32);
+    const uint32_t q_lo = static_cast<uint32_t>(dq), k_lo = static_cast<uint32_t>(dk);
+    const uint32_t v_lo = static_cast<uint32_t>(dv);
+    auto commit = [&](uint32_t bar_addr) {
+      if (leader) mma_commit(bar_addr);
+    };
+    auto issue_s = [&](int i, int stage) {
+      const uint32_t a0 = q_lo + ((i * L::kQTile) >> 4);
+      const uint32_t b0 = k_lo + ((stage * L::kKVTile) >> 4);
+      const uint32_t d_tmem = tmem + i * kTileN;
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = ((kk >> 2) * L::kHalf + (kk & 3) * 32) >> 4;
-          if (leader) mma_ss_lohi(d_tmem, a0 + off, qk_hi, b0 + off, qk_hi, idesc_s, kk > 0 ? 1u : 0u);
-        }
-      };
-      auto issue_pv = [&](int i, int stage, bool acc) {
-        const uint32_t b0 = v_lo + ((stage * L::kKVTile) >> 4);
-        const uint32_t d_tmem = tmem + 256 + i * D;
-        const uint32_t a_tmem = tmem + i * kTileN;
-        const uint32_t acc0 = acc ? 1u : 0u;
-#pragma unroll
-        for (int kk = 0; kk < kTileN / 16; ++kk)
-          if (leader) mma_ts_lohi(d_tmem, a_tmem + kk * 8, b0 + ((kk * 2048) >> 4), v_hi, idesc_o, kk > 0 ? 1u : acc0);
-      };
-      bool ok = mbar_wait_bounded(bar(kBarQFull), 0, abort_flag, a.err, tmo) &&
-                mbar_wait_bounded(bar(kBarKFull), 0, abort_flag, a.err, tmo);
-      if (ok) {
-        for (int i = 0; i < nq && ok; ++i) {
-          if (i == 1 && !mbar_wait_bounded(bar(kBarQFull1), 0, abort_flag, a.err, tmo)) {
-            ok = false;
-            break;
-          }
-          issue_s(i, 0);
-          commit(bar(kBarSFull + i));
-        }
-        if (ok) commit(bar(kBarKEmpty));
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t off = ((kk >> 2) * L::kHalf + (kk & 3) * 32) >> 4;
+        if (leader) mma_ss_lohi(d_tmem, a0 + off, qk_hi, b0 + off, qk_hi, idesc_s, kk > 0 ? 1u : 0u);
       }
+    };
+    auto issue_pv = [&](int i, int stage, bool acc) {
+      const uint32_t b0 = v_lo + ((stage * L::kKVTile) >> 4);
+      const uint32_t d_tmem = tmem + 256 + i * D;
+      const uint32_t a_tmem = tmem + i * kTileN;
+      const uint32_t acc0 = acc ? 1u : 0u;
+#pragma unroll
+      for (int kk = 0; kk < kTileN / 16; ++kk)
+        if (leader) mma_ts_lohi(d_tmem, a_tmem + kk * 8, b0 + ((kk * 2048) >> 4), v_hi, idesc_o, kk > 0 ? 1u : acc0);
+    };
+    int g = 0;              // key tiles so far, of all items
+    int pc[2] = {0, 0};     // and those of each query tile
+    int qc[2] = {0, 0};     // items of each query tile
+    bool ok = true;
+    for (int n = 0; ok; ++n) {
+      if (!(ok = mbar_wait_bounded(bar(kBarItemFull + (n & 1)), (n >> 1) & 1, abort_flag, a.err, tmo))) break;
+      const Item* t = item_at(n & 1);
+      const int valid = t->valid, NT = t->NT, nq = t->row0 + kTileM < a.Sq ? 2 : 1;
+      __syncwarp();
+      if (leader) mbar_arrive(bar(kBarItemEmpty + (n & 1)));
+      if (!valid) break;
+      if (NT == 0) continue;
+      // S of the first tile: behind the last products of the item before, whose P
+      // it writes over
+      ok = mbar_wait_bounded(bar(kBarQFull), qc[0] & 1, abort_flag, a.err, tmo) &&
+           mbar_wait_bounded(bar(kBarKFull + (g & 1)), (g >> 1) & 1, abort_flag, a.err, tmo);
+      for (int i = 0; i < nq && ok; ++i) {
+        if (i == 1 && !mbar_wait_bounded(bar(kBarQFull + 1), qc[1] & 1, abort_flag, a.err, tmo)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        issue_s(i, g & 1);
+        commit(bar(kBarSFull + i));
+        if (NT == 1) commit(bar(kBarQEmpty + i));
+      }
+      if (ok) commit(bar(kBarKEmpty + (g & 1)));
       // The tensor pipe queues about one MMA: whatever this thread does
       // between two MMA groups leaves the pipe idle. Each step therefore
       // waits at two points only: V(it), K(it+1) and P_0(it) before
       // PV_0(it) + S_0(it+1); P_1(it) before PV_1(it) + S_1(it+1). The step
       // is instantiated per tile count and ring stage so that every MMA
       // operand is a compile-time offset from one base: a run-time tile or
-      // stage index in the issue sequence measurably stalls the pipe.
+      // stage index in the issue sequence measurably stalls the pipe. P of an
+      // item's first tile comes after its softmax warps have read the O before.
       auto step = [&](auto nq_c, auto stage_c, int it) -> bool {
         constexpr int kNq = decltype(nq_c)::value;
         constexpr int s = decltype(stage_c)::value;
         constexpr int s2 = s ^ 1;
-        const uint32_t ph = (it >> 1) & 1;
         const bool more = it + 1 < NT;
-        if (!mbar_wait_bounded(bar(kBarVFull + s), ph, abort_flag, a.err, tmo) ||
-            (more && !mbar_wait_bounded(bar(kBarKFull + s2), ((it + 1) >> 1) & 1, abort_flag, a.err, tmo)))
+        if (!mbar_wait_bounded(bar(kBarVFull + s), ((g + it) >> 1) & 1, abort_flag, a.err, tmo) ||
+            (more && !mbar_wait_bounded(bar(kBarKFull + s2), ((g + it + 1) >> 1) & 1, abort_flag, a.err, tmo)))
           return false;
 #pragma unroll
         for (int i = 0; i < kNq; ++i) {
-          if (!mbar_wait_bounded(bar(kBarPFull + i), it & 1, abort_flag, a.err, tmo)) return false;
+          if (!mbar_wait_bounded(bar(kBarPFull + i), (pc[i] + it) & 1, abort_flag, a.err, tmo)) return false;
           tc_fence_after();
           issue_pv(i, s, it > 0);
           if (more) {
             issue_s(i, s2);
             commit(bar(kBarSFull + i));
+            if (it + 2 == NT) commit(bar(kBarQEmpty + i));
           } else {
             commit(bar(kBarOFull + i));
           }
@@ -322,7 +410,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         return true;
       };
       auto run_steps = [&](auto nq_c) {
-        for (int it = 0; ok && it < NT; it += 2) {
+        int it = 0;
+        if (ok && (g & 1)) ok = step(nq_c, std::integral_constant<int, 1>{}, it++);
+        for (; ok && it < NT; it += 2) {
           ok = step(nq_c, std::integral_constant<int, 0>{}, it);
           if (ok && it + 1 < NT) ok = step(nq_c, std::integral_constant<int, 1>{}, it + 1);
         }
@@ -331,35 +421,54 @@ __global__ void __launch_bounds__(kThreads, 1)
         run_steps(std::integral_constant<int, 2>{});
       else
         run_steps(std::integral_constant<int, 1>{});
-      if (!ok) {
-        commit(bar(kBarDrain));
-        drain_wait(bar(kBarDrain), 0, tmo);
+      g += NT;
+      for (int i = 0; i < nq; ++i) {
+        pc[i] += NT;
+        ++qc[i];
       }
     }
-  } else if (warp >= 2) {
+    if (!ok) {
+      commit(bar(kBarDrain));
+      drain_wait(bar(kBarDrain), 0, tmo);
+    }
+  } else {
     // ===================== softmax + epilogue =====================
     const int i = (warp - 2) >> 2;  // query tile of this warpgroup
     const int wq = warp & 3;        // TMEM lane quadrant of this warp (warp id mod 4)
     const int row = wq * 32 + lane;
-    if (i < nq) {
-      const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
-      const uint32_t t_s = tmem + lane_off + i * kTileN;
-      const uint32_t t_o = tmem + lane_off + 256 + i * D;
-      const float sl2 = a.scale * kLog2e;
-      const int tok0 = row0 + i * kTileM;   // first row of this query tile
+    const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
+    const uint32_t t_s = tmem + lane_off + i * kTileN;
+    const uint32_t t_o = tmem + lane_off + 256 + i * D;
+    const float sl2 = a.scale * kLog2e;
+    int pc = 0, oc = 0;  // key tiles and items with any so far
+    int level = 0;       // of the cap's polynomial: 3, 6 terms' range, or neither
+    bool guess = true;   // an item's first P may be formed with the reference 0
+    bool ok = true;
+    for (int n = 0; ok; ++n) {
+      ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar(kBarItemFull + (n & 1)), (n >> 1) & 1, abort_flag, a.err, tmo));
+      if (!ok) break;
+      const Item t = *item_at(n & 1);
+      if (!t.valid) break;
+      const int tok0 = t.row0 + i * kTileM;   // first row of this query tile
+      if (tok0 >= a.Sq) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarItemEmpty + (n & 1)));
+        continue;
+      }
+      const int h = t.h, b = t.b, NT = t.NT;
+      const uint32_t* bits = a.qdoc ? map_at(n & 1) : nullptr;
+      const uint32_t* mixed = map_at(n & 1) + (1 + i) * kMapWords;
       const int rows_valid = min(kTileM, a.Sq - tok0);
-      const int lim = min(a.Skv, key_limit(a, plim, tok0 + row));
+      const int lim = min(a.Skv, key_limit(a, t.plim, tok0 + row));
       const int qd = a.qdoc && row < rows_valid ? a.qdoc[static_cast<int64_t>(b) * a.Sq + tok0 + row] : -1;
       const int* kd = a.kdoc + static_cast<int64_t>(b) * a.Skv;
       const float slope2 = kBias ? a.slopes[h] * kLog2e : 0.f;
       float m_used = -INFINITY, l = 0.f;
-      int level = 0;  // of the cap's polynomial: 3, 6 terms' range, or neither
-      bool ok = true;
-      TileWalk cur(bits, 0, ntile, start);
-      for (int n = 0; n < n0; ++n) cur.next();
+      TileWalk<true> cur(bits, 0, t.ntile, walk_start(t), shift);
+      for (int k = 0; k < t.n0; ++k) cur.next();
       for (int it = 0; it < NT; ++it) {
         const int kv0 = cur.t * kTileN;
-        const bool mix = bits != nullptr && ((mixed[i * kMapWords + (cur.t >> 5)] >> (cur.t & 31)) & 1u);
+        const bool mix = bits != nullptr && cur.in(mixed);
         const int nv = lim - kv0;                  // this row's keys of the tile: those below nv
         const int dq = a.rel + tok0 + row - kv0;   // position of the row less that of the tile's first key
         const bool cut = __any_sync(0xffffffffu, nv < kTileN);
@@ -388,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int w = 0; w < 4; ++w) on[w] &= same[w];
         }
-        ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar(kBarSFull + i), it & 1, abort_flag, a.err, tmo));
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar(kBarSFull + i), (pc + it) & 1, abort_flag, a.err, tmo));
         if (!ok) break;
         tc_fence_after();
         uint32_t pk[kTileN / 2];
@@ -403,7 +512,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           f32x2 ls[2] = {0ull, 0ull};
           float um[2] = {0.f, 0.f};
           const float bs = kBias ? (below ? slope2 : -slope2) : 0.f;
-          const float bb = kBias ? fmaf(-bs, static_cast<float>(dq), -m_used) : -m_used;
+          const float ref = m_used == -INFINITY ? 0.f : m_used;
+          const float bb = kBias ? fmaf(-bs, static_cast<float>(dq), -ref) : -ref;
           const f32x2 bs2 = pair(bs, bs), bb2 = pair(bb, bb), sl22 = pair(sl2, sl2);
           uint32_t buf[2][16];
           tmem_ld16(t_s, buf[0]);
@@ -446,30 +556,33 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         float f = 1.f, lsum = INFINITY;
         bool fits = false;
-        // speculatively with the running maximum: every P is at most the row
-        // sum, so a sum within 2^8 proves that the row maximum is within 2^8 of
-        // the running one (an overflow, or a row that has seen no key yet, fails
-        // the test too); and s^2 within the polynomial's range
-        if (it > 0 && (!kBias || below || above)) {
+        // speculatively with the reference that the row has (0 before it has one):
+        // any will do that keeps its sums far from overflow, which a row sum
+        // within 2^32 proves (every P is at most that), and from underflow, where
+        // the first sum is above 2^-32; and s^2 within the polynomial's range
+        const bool none = masked && (on[0] | on[1] | on[2] | on[3]) == 0u;
+        auto holds = [&](float sum) { return sum <= kSumMost && (m_used != -INFINITY || sum >= 1.f / kSumMost || none); };
+        if ((it > 0 || guess) && (!kBias || below || above)) {
           using std::integral_constant;
           if constexpr (kCap) {
             if (level == 0) {
               lsum = masked ? speculate(integral_constant<int, 3>{}, std::true_type{})
                             : speculate(integral_constant<int, 3>{}, std::false_type{});
-              fits = lsum <= 256.f && umax <= cc.u3;
+              fits = holds(lsum) && umax <= cc.u3;
             } else if (level == 1 && !masked) {
               lsum = speculate(integral_constant<int, 6>{}, std::false_type{});
-              fits = lsum <= 256.f && umax <= cc.u6;
+              fits = holds(lsum) && umax <= cc.u6;
             }
           } else {
             lsum = masked ? speculate(integral_constant<int, 1>{}, std::true_type{})
                           : speculate(integral_constant<int, 1>{}, std::false_type{});
-            fits = lsum <= 256.f;
+            fits = holds(lsum);
           }
         }
         if (__all_sync(0xffffffffu, fits)) {
           tmem_st32(t_s, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));
           tmem_st32(t_s + 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[32]));
+          if (m_used == -INFINITY && !none) m_used = 0.f;
         } else {
           // exactly, 32 columns at a time: scores in log2 units back over S and
           // their maximum; move to it if it grew by more than 2^8, rescaling O
@@ -543,6 +656,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             f = ex2_approx(m_used - mxs);
             m_used = mxs;
           }
+          guess = __all_sync(0xffffffffu, m_used == -INFINITY || fabsf(m_used) <= 24.f);
           const float nm = m_used == -INFINITY ? 0.f : -m_used;
           f32x2 ls[2] = {0ull, 0ull};
 #pragma unroll 1
@@ -585,81 +699,81 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(bar(kBarPFull + i));
         cur.next();
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBarItemEmpty + (n & 1)));
       // l = 0: no key -> out 0, lse -inf (found while the last product runs)
       const float inv_l = l != 0.f ? 1.f / l : 0.f;
       const float lse_v = l != 0.f ? (m_used + log2f(l)) * kLn2 : -INFINITY;
-      if (ok && NT > 0) ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar(kBarOFull + i), 0, abort_flag, a.err, tmo));
+      if (ok && NT > 0) ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar(kBarOFull + i), oc & 1, abort_flag, a.err, tmo));
+      pc += NT;
+      oc += NT > 0;
       if (ok) {
         tc_fence_after();
-        uint32_t o[D];
-        if (NT > 0) {
-#pragma unroll
-          for (int c = 0; c < D / 32; ++c) tmem_ld32(t_o + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&o[c * 32]));
-          tmem_wait_ld();
-        } else {
-#pragma unroll
-          for (int e = 0; e < D; ++e) o[e] = 0u;
-        }
-        if (cs > 1) {
-          // this CTA's part over the idle tiles: [256 rows][D], 16-byte pieces permuted by row
-          const int r = i * kTileM + row;
-          *reinterpret_cast<float2*>(smem + L::kOffStat + r * 8) = make_float2(m_used, l);
-          float* part = reinterpret_cast<float*>(smem) + r * D;
-#pragma unroll
-          for (int x = 0; x < D / 4; ++x)
-            *reinterpret_cast<float4*>(part + ((x ^ (r & 7)) * 4)) =
-                make_float4(u2f(o[4 * x]), u2f(o[4 * x + 1]), u2f(o[4 * x + 2]), u2f(o[4 * x + 3]));
-        } else {
-          if (row < rows_valid) a.lse[(static_cast<int64_t>(b) * a.H + h) * a.Sq + tok0 + row] = lse_v;
-          // 32 rows x 32 words a pass (32 fp32 columns, or 64 in bf16) staged in
-          // this tile's idle Q buffer, 128-byte swizzled, and stored 4 rows x 128
-          // contiguous bytes per warp instruction
-          const int64_t base = (static_cast<int64_t>(b) * a.Sq + tok0) * a.H + h;  // in rows of D
-          uint32_t* stage = reinterpret_cast<uint32_t*>(smem + L::kOffQ + i * L::kQTile + wq * 4096);
-          auto flush = [&](uint8_t* dst, int row_bytes) {
-            __syncwarp();
-#pragma unroll
-            for (int pass = 0; pass < 8; ++pass) {
-              const int rr = pass * 4 + (lane >> 3), q4 = lane & 7;
-              const uint4 val = *reinterpret_cast<const uint4*>(stage + rr * 32 + ((q4 ^ (rr & 7)) * 4));
-              if (wq * 32 + rr < rows_valid)
-                *reinterpret_cast<uint4*>(dst + (base + static_cast<int64_t>(wq * 32 + rr) * a.H) * row_bytes + q4 * 16) = val;
-            }
-            __syncwarp();  // the buffer is read before it is staged again
-          };
-          if (a.out_bf16) {
-#pragma unroll
-            for (int c = 0; c < D / 64; ++c) {
-#pragma unroll
-              for (int q4 = 0; q4 < 8; ++q4) {
-                const uint32_t* oc = &o[c * 64 + 8 * q4];
-                uint4 val;
-                val.x = pack_bf16x2(u2f(oc[0]) * inv_l, u2f(oc[1]) * inv_l);
-                val.y = pack_bf16x2(u2f(oc[2]) * inv_l, u2f(oc[3]) * inv_l);
-                val.z = pack_bf16x2(u2f(oc[4]) * inv_l, u2f(oc[5]) * inv_l);
-                val.w = pack_bf16x2(u2f(oc[6]) * inv_l, u2f(oc[7]) * inv_l);
-                *reinterpret_cast<uint4*>(stage + lane * 32 + ((q4 ^ (lane & 7)) * 4)) = val;
-              }
-              flush(static_cast<uint8_t*>(a.out) + c * 128, D * 2);
-            }
+        if (cs > 1)
+          *reinterpret_cast<float2*>(smem + L::kOffStat + (i * kTileM + row) * 8) = make_float2(m_used, l);
+        else if (row < rows_valid)
+          a.lse[(static_cast<int64_t>(b) * a.H + h) * a.Sq + tok0 + row] = lse_v;
+        // 32 rows x 128 bytes (64 columns in bf16, 32 in fp32) are staged in this
+        // warp's buffer, 128-byte swizzled, and stored by TMA, which cuts the rows
+        // past the end: the stores of all multiprocessors come at about the same
+        // time, and ordinary ones would hold up this warp's next item behind them
+        const uint32_t stage = sb + L::kOffStage + (warp - 2) * 4096;
+        auto place = [&](int q4, uint32_t x, uint32_t y, uint32_t z, uint32_t u) {
+          *reinterpret_cast<uint4*>(smem + L::kOffStage + (warp - 2) * 4096 + lane * 128 + ((q4 ^ (lane & 7)) * 16)) =
+              make_uint4(x, y, z, u);
+        };
+        auto stage_free = [&]() {
+          if (lane == 0) tma_store_wait_read();
+          __syncwarp();
+        };
+        auto flush = [&](int col) {
+          fence_async();
+          __syncwarp();
+          if (lane == 0 && wq * 32 < rows_valid) tma_store_4d(&to, stage, col, h, tok0 + wq * 32, b);
+        };
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          if (NT > 0) {
+            tmem_ld32(t_o + c * 32, o);
+            tmem_wait_ld();
+            tmem_pin(o);
           } else {
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
+            for (int e = 0; e < 32; ++e) o[e] = 0u;
+          }
+          auto w = [&](int e) { return __float_as_uint(u2f(o[e]) * inv_l); };
+          auto w2 = [&](int e) { return pack_bf16x2(u2f(o[e]) * inv_l, u2f(o[e + 1]) * inv_l); };
+          if (cs > 1) {
+            // this CTA's part over the idle tiles: [256 rows][D], 16-byte pieces permuted by row
+            const int r = i * kTileM + row;
+            float* part = reinterpret_cast<float*>(smem) + r * D;
 #pragma unroll
-              for (int q4 = 0; q4 < 8; ++q4) {
-                const uint32_t* oc = &o[c * 32 + 4 * q4];
-                const float4 val = make_float4(u2f(oc[0]) * inv_l, u2f(oc[1]) * inv_l, u2f(oc[2]) * inv_l, u2f(oc[3]) * inv_l);
-                *reinterpret_cast<float4*>(stage + lane * 32 + ((q4 ^ (lane & 7)) * 4)) = val;
-              }
-              flush(static_cast<uint8_t*>(a.out) + c * 128, D * 4);
-            }
+            for (int x = 0; x < 8; ++x)
+              *reinterpret_cast<uint4*>(part + (((c * 8 + x) ^ (r & 7)) * 4)) =
+                  make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+          } else if (a.out_bf16) {
+            if ((c & 1) == 0) stage_free();
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              place((c & 1) * 4 + x, w2(8 * x), w2(8 * x + 2), w2(8 * x + 4), w2(8 * x + 6));
+            if (c & 1) flush((c >> 1) * 64);
+          } else {
+            stage_free();
+#pragma unroll
+            for (int x = 0; x < 8; ++x) place(x, w(4 * x), w(4 * x + 1), w(4 * x + 2), w(4 * x + 3));
+            flush(c * 64);
           }
         }
       }
     }
+    if (lane == 0) tma_store_wait();
   }
   if (cs > 1) {
-    static_assert(2 * kTileM * D * 4 <= L::kOffBar, "the parts lie over the tiles");
+    static_assert(2 * kTileM * D * 4 <= L::kOffStage, "the parts lie over the tiles");
+    const int h = static_cast<int>(blockIdx.x) >> (__ffs(cs) - 1), b = blockIdx.y;
+    const int row0 = (static_cast<int>(gridDim.z) - 1 - static_cast<int>(blockIdx.z)) * 2 * kTileM;
+    const int nrows = min(2 * kTileM, a.Sq - row0);
     __syncwarp();
     cluster_sync();
     // a row's D / 4 pieces on neighbouring lanes, kIn rows a thread at once: every
@@ -734,7 +848,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <int D, bool kCap, bool kBias>
 cudaError_t launch_rule(const ScoreArgs& a, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                        cudaStream_t s) {
+                        const CUtensorMap& to, cudaStream_t s) {
   using L = Smem<D>;
   static_assert(L::kAlloc <= 227 * 1024, "shared memory budget");
   cudaError_t e = allow_smem<score_fwd_tc_kernel<D, kCap, kBias>>(L::kAlloc);
@@ -743,20 +857,22 @@ cudaError_t launch_rule(const ScoreArgs& a, const CUtensorMap& tq, const CUtenso
   // steps: key tiles; some 8 of them go by before the first and after the last
   const int cs = cluster_for(8.0, items, (a.Skv + kTileN - 1) / kTileN, 0, 0, a.causal ? 0.5 : 1.0, true);
   return launch_clusters(score_fwd_tc_kernel<D, kCap, kBias>, a.H, a.B, (a.Sq + 2 * kTileM - 1) / (2 * kTileM), cs, kThreads, L::kAlloc, a.qdoc != nullptr, s, tq, tk,
-                         tv, a, make_cap_coef(a.scale, a.cap, false));
+                         tv, to, a, make_cap_coef(a.scale, a.cap, false));
 }
 
 template <int D>
 cudaError_t launch_d(const ScoreArgs& a, cudaStream_t s) {
-  CUtensorMap tq, tk, tv;
+  CUtensorMap tq, tk, tv, to;
   // without keys the maps of k and v are never read through
   const bool none = a.Skv == 0;
   if (!host_tmap_bf16(&tq, a.q, D, a.H, a.Sq, a.B, kTileM) ||
       !host_tmap_bf16(&tk, none ? a.q : a.k, D, none ? a.H : a.Hkv, none ? a.Sq : a.Skv, a.B, kTileN) ||
-      !host_tmap_bf16(&tv, none ? a.q : a.v, D, none ? a.H : a.Hkv, none ? a.Sq : a.Skv, a.B, kTileN))
+      !host_tmap_bf16(&tv, none ? a.q : a.v, D, none ? a.H : a.Hkv, none ? a.Sq : a.Skv, a.B, kTileN) ||
+      // fp32 rows as twice as many 16-bit columns
+      !host_tmap_bf16(&to, a.out, a.out_bf16 ? D : 2 * D, a.H, a.Sq, a.B, 32))
     return cudaErrorInvalidValue;
-  if (a.cap > 0.f) return a.slopes ? launch_rule<D, true, true>(a, tq, tk, tv, s) : launch_rule<D, true, false>(a, tq, tk, tv, s);
-  return a.slopes ? launch_rule<D, false, true>(a, tq, tk, tv, s) : launch_rule<D, false, false>(a, tq, tk, tv, s);
+  if (a.cap > 0.f) return a.slopes ? launch_rule<D, true, true>(a, tq, tk, tv, to, s) : launch_rule<D, true, false>(a, tq, tk, tv, to, s);
+  return a.slopes ? launch_rule<D, false, true>(a, tq, tk, tv, to, s) : launch_rule<D, false, false>(a, tq, tk, tv, to, s);
 }
 
 }  // namespace

@@ -167,14 +167,17 @@ __device__ __forceinline__ void same_docs(int own, const int (&ids)[kWords], uin
 }
 
 // The tiles of [lo, hi) that a CTA walks: all, or those whose bit is set in act
-// (a bitmap in shared memory). First from `start` down to lo, then from
-// start + 1 up; start < lo walks upwards only.
+// (a bitmap in shared memory, a bit for a tile, or for 2^shift where kGroups).
+// First from `start` down to lo, then from start + 1 up; start < lo
+// walks upwards only.
+template <bool kGroups = false>
 struct TileWalk {
   const uint32_t* act;
-  int t, lo, hi, start;
+  int t, lo, hi, start, shift;
   bool down;
-  __device__ __forceinline__ TileWalk(const uint32_t* bits, int lo_, int hi_, int start_)
-      : act(bits), t(start_), lo(lo_), hi(hi_), start(start_ < lo_ ? lo_ - 1 : start_), down(start_ >= lo_) {
+  __device__ __forceinline__ TileWalk(const uint32_t* bits, int lo_, int hi_, int start_, int shift_ = 0)
+      : act(bits), t(start_), lo(lo_), hi(hi_), start(start_ < lo_ ? lo_ - 1 : start_), shift(kGroups ? shift_ : 0),
+        down(start_ >= lo_) {
     if (down) {
       find_down();
     } else {
@@ -183,6 +186,11 @@ struct TileWalk {
     }
   }
   __device__ __forceinline__ bool done() const { return t >= hi; }
+  // whether the tile's bit is set in another bitmap of the same kind
+  __device__ __forceinline__ bool in(const uint32_t* map) const {
+    const int g = t >> shift;
+    return (map[g >> 5] >> (g & 31)) & 1u;
+  }
   __device__ __forceinline__ void next() {
     if (down) {
       --t;
@@ -191,29 +199,34 @@ struct TileWalk {
     }
     ++t;
     if (act == nullptr || t >= hi) return;
-    uint32_t w = act[t >> 5] >> (t & 31);
+    const int g = t >> shift;
+    uint32_t w = act[g >> 5] >> (g & 31);
+    if (w & 1u) return;
     if (w) {
-      t += __ffs(w) - 1;
+      t = (g + __ffs(w) - 1) << shift;
       return;
     }
-    int i = (t >> 5) + 1;
-    const int ni = (hi + 31) >> 5;
+    int i = (g >> 5) + 1;
+    const int ni = (((hi - 1) >> shift) >> 5) + 1;
     while (i < ni && (w = act[i]) == 0) ++i;
-    t = i < ni ? i * 32 + __ffs(w) - 1 : hi;
+    t = i < ni ? (i * 32 + __ffs(w) - 1) << shift : hi;
   }
   // the last set tile at or below t, else on to the upward part
   __device__ __forceinline__ void find_down() {
     if (act != nullptr && t >= lo) {
-      uint32_t w = act[t >> 5] << (31 - (t & 31));
+      const int g = t >> shift;
+      uint32_t w = act[g >> 5] << (31 - (g & 31));
+      if (w >> 31) return;
+      auto last = [&](int group) { return kGroups ? ((group + 1) << shift) - 1 : group; };
       if (w) {
-        t -= __clz(w);
+        t = last(g - __clz(w));
         return;
       }
-      int i = (t >> 5) - 1;
-      const int i0 = lo >> 5;
+      int i = (g >> 5) - 1;
+      const int i0 = (lo >> shift) >> 5;
       while (i >= i0 && (w = act[i]) == 0) --i;
       if (i >= i0) {
-        t = i * 32 + 31 - __clz(w);
+        t = last(i * 32 + 31 - __clz(w));
         return;
       }
       t = lo - 1;
