@@ -249,6 +249,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tma_prefetch_desc(&tq);
       tma_prefetch_desc(&tk);
       tma_prefetch_desc(&tv);
+      tma_prefetch_desc(&to);
     }
     int k_issued[2] = {0, 0}, v_issued[2] = {0, 0}, q_issued[2] = {0, 0};
     int g = 0;  // key tiles so far, of all items
@@ -447,30 +448,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int n = 0; ok; ++n) {
       ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar(kBarItemFull + (n & 1)), (n >> 1) & 1, abort_flag, a.err, tmo));
       if (!ok) break;
-      const Item t = *item_at(n & 1);
-      if (!t.valid) break;
-      const int tok0 = t.row0 + i * kTileM;   // first row of this query tile
-      if (tok0 >= a.Sq) {
+      const Item* item = item_at(n & 1);
+      if (!item->valid) break;
+      if (item->row0 + i * kTileM >= a.Sq) {
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kBarItemEmpty + (n & 1)));
         continue;
       }
-      const int h = t.h, b = t.b, NT = t.NT;
-      const uint32_t* bits = a.qdoc ? map_at(n & 1) : nullptr;
-      const uint32_t* mixed = map_at(n & 1) + (1 + i) * kMapWords;
-      const int rows_valid = min(kTileM, a.Sq - tok0);
-      const int lim = min(a.Skv, key_limit(a, t.plim, tok0 + row));
-      const int qd = a.qdoc && row < rows_valid ? a.qdoc[static_cast<int64_t>(b) * a.Sq + tok0 + row] : -1;
-      const int* kd = a.kdoc + static_cast<int64_t>(b) * a.Skv;
-      const float slope2 = kBias ? a.slopes[h] * kLog2e : 0.f;
+      const int NT = item->NT;
+      const int at = item->row0 + i * kTileM + row;  // this thread's query row
+      const int lim = min(a.Skv, key_limit(a, item->plim, at));
+      const int qd = a.qdoc && at < a.Sq ? a.qdoc[static_cast<int64_t>(item->b) * a.Sq + at] : -1;
+      const float slope2 = kBias ? a.slopes[item->h] * kLog2e : 0.f;
       float m_used = -INFINITY, l = 0.f;
-      TileWalk<true> cur(bits, 0, t.ntile, walk_start(t), shift);
-      for (int k = 0; k < t.n0; ++k) cur.next();
+      TileWalk<true> cur(a.qdoc ? map_at(n & 1) : nullptr, 0, item->ntile, walk_start(*item), shift);
+      for (int k = item->n0; k > 0; --k) cur.next();
       for (int it = 0; it < NT; ++it) {
         const int kv0 = cur.t * kTileN;
-        const bool mix = bits != nullptr && cur.in(mixed);
+        const bool mix = a.qdoc && cur.in(map_at(n & 1) + (1 + i) * kMapWords);
         const int nv = lim - kv0;                  // this row's keys of the tile: those below nv
-        const int dq = a.rel + tok0 + row - kv0;   // position of the row less that of the tile's first key
+        const int dq = a.rel + at - kv0;   // position of the row less that of the tile's first key
         const bool cut = __any_sync(0xffffffffu, nv < kTileN);
         // where every pair that takes part has the same order, the bias is linear in the key
         const bool below = __all_sync(0xffffffffu, dq >= kTileN - 1 || nv <= dq + 1);
@@ -486,6 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (mix) {
+          const int* kd = a.kdoc + static_cast<int64_t>(item->b) * a.Skv;
           int ids[4];
           uint32_t same[4];
 #pragma unroll
@@ -699,14 +697,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(bar(kBarPFull + i));
         cur.next();
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kBarItemEmpty + (n & 1)));
       // l = 0: no key -> out 0, lse -inf (found while the last product runs)
       const float inv_l = l != 0.f ? 1.f / l : 0.f;
       const float lse_v = l != 0.f ? (m_used + log2f(l)) * kLn2 : -INFINITY;
       if (ok && NT > 0) ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar(kBarOFull + i), oc & 1, abort_flag, a.err, tmo));
       pc += NT;
       oc += NT > 0;
+      const int h = item->h, b = item->b, tok0 = item->row0 + i * kTileM;
+      const int rows_valid = a.Sq - tok0;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBarItemEmpty + (n & 1)));
       if (ok) {
         tc_fence_after();
         if (cs > 1)
@@ -767,7 +767,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-    if (lane == 0) tma_store_wait();
+    if (lane == 0) tma_store_wait_read();
   }
   if (cs > 1) {
     static_assert(2 * kTileM * D * 4 <= L::kOffStage, "the parts lie over the tiles");
