@@ -46,7 +46,10 @@
 namespace cp {
 namespace {
 
-constexpr int kRowWarps = 8;  // two per TMEM lane quarter, one per 32-column half of a sub-step
+// Row warps: two groups, which take the sub-steps in turn, so that the waits and
+// tensor-memory latencies of one group's pass go by under the other's. In a group
+// two per TMEM lane quarter, one per 32-column half of a sub-step.
+constexpr int kGroupWarps = 8, kRowWarps = 2 * kGroupWarps;
 constexpr int kThreadsB = 64 + 32 * kRowWarps;
 constexpr uint32_t kTmemColsB = 512;
 constexpr int kT = 128;         // keys per dk/dv CTA, query rows per dq CTA
@@ -129,9 +132,10 @@ __device__ __forceinline__ uint32_t pcol(int kk) { return static_cast<uint32_t>(
 
 
 // Holds the uses of loaded registers behind the wait that precedes it.
-__device__ __forceinline__ void tmem_pin(uint32_t (&r)[32]) {
+template <int N>
+__device__ __forceinline__ void tmem_pin(uint32_t (&r)[N]) {
 #pragma unroll
-  for (int i = 0; i < 32; i += 8)
+  for (int i = 0; i < N; i += 8)
     asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]),
                  "+r"(r[i + 6]), "+r"(r[i + 7]));
 }
@@ -159,22 +163,22 @@ __device__ __forceinline__ int walk_map(const DocRange* other, int nblk, const D
   return static_cast<int>(*count);
 }
 
-// 32 scores of a row pass: p in place of s and -ds in place of dp, packed as
+// 16 scores of a row pass: p in place of s and -ds in place of dp, packed as
 // bf16 pairs. Element e has the distance |d0 + step e| (step +1 or -1);
 // nl(e) = -lse log2e and dl(e) = delta of its row; on: the pairs that take part.
 // The signs are such that no packed operand has to be negated (an instruction
 // each): -ds = p (delta - dp), or with a cap p (delta - dp)(1 - tanh^2) from
 // p (dp - delta)(tanh^2 - 1); the epilogues multiply by -scale.
 template <bool kCap, bool kBias, int kStep, typename NL, typename ND>
-__device__ __forceinline__ void row_pass(const uint32_t (&sr)[32], const uint32_t (&dr)[32], const CapCoef& cc,
+__device__ __forceinline__ void row_pass(const uint32_t (&sr)[16], const uint32_t (&dr)[16], const CapCoef& cc,
                                          float c2, float capl2, float slope2, float d0, uint32_t on, NL nl, ND dl,
-                                         uint32_t (&pp)[16], uint32_t (&dd)[16]) {
+                                         uint32_t (&pp)[8], uint32_t (&dd)[8]) {
   const f32x2 c22 = pair(c2, c2), cap2 = pair(capl2, capl2), minus = pair(-1.f, -1.f);
   // kHow: 0 no cap, 3 and 6 the polynomials, 1 exact
   auto pass = [&](auto how_c) {
     constexpr int kHow = decltype(how_c)::value;
 #pragma unroll
-    for (int e = 0; e < 32; e += 2) {
+    for (int e = 0; e < 16; e += 2) {
       const f32x2 s2 = pair_u(sr[e], sr[e + 1]);
       f32x2 b2 = nl(e);
       if constexpr (kBias) {
@@ -209,7 +213,7 @@ __device__ __forceinline__ void row_pass(const uint32_t (&sr)[32], const uint32_
   if constexpr (kCap) {
     float um = 0.f;
 #pragma unroll
-    for (int e = 0; e < 32; e += 4) um = fmax3(um, fmaxf(fabsf(u2f(sr[e])), fabsf(u2f(sr[e + 1]))), fmaxf(fabsf(u2f(sr[e + 2])), fabsf(u2f(sr[e + 3]))));
+    for (int e = 0; e < 16; e += 4) um = fmax3(um, fmaxf(fabsf(u2f(sr[e])), fabsf(u2f(sr[e + 1]))), fmaxf(fabsf(u2f(sr[e + 2])), fabsf(u2f(sr[e + 3]))));
     um *= um;
     if (__all_sync(0xffffffffu, um <= cc.u3))
       pass(std::integral_constant<int, 3>{});
@@ -220,9 +224,9 @@ __device__ __forceinline__ void row_pass(const uint32_t (&sr)[32], const uint32_
   } else {
     pass(std::integral_constant<int, 0>{});
   }
-  if (__any_sync(0xffffffffu, on != ~0u)) {
+  if (__any_sync(0xffffffffu, (on & 0xffffu) != 0xffffu)) {
 #pragma unroll
-    for (int x = 0; x < 16; ++x) {
+    for (int x = 0; x < 8; ++x) {
       const uint32_t keep = ((on >> (2 * x)) & 1u ? 0x0000ffffu : 0u) | ((on >> (2 * x + 1)) & 1u ? 0xffff0000u : 0u);
       pp[x] &= keep;
       dd[x] &= keep;
@@ -359,7 +363,7 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap& tq64, const CUtensor
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < L::kNumBars; ++i) {
-      mbar_init(bar(i), i >= kBarPFull && i < kBarDone ? kRowWarps : 1);
+      mbar_init(bar(i), i >= kBarPFull && i < kBarDone ? kGroupWarps : 1);
     }
     misc[1] = 0;
     fence_mbar_init();
@@ -504,7 +508,8 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap& tq64, const CUtensor
   } else {
     // ===================== row pass: one thread per key row and column half =====================
     const int wq = warp & 3;
-    const int hc = (warp - 2) >> 2;  // this warp's 32 query columns of each sub-step
+    const int group = (warp - 2) / kGroupWarps;  // takes the sub-steps j = group mod 2
+    const int hc = ((warp - 2) >> 2) & 1;        // this warp's 32 query columns of each
     const int key = wq * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
     const bool kvalid = key < nk;
@@ -514,8 +519,8 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap& tq64, const CUtensor
     const int kd = a.qdoc && kvalid ? a.kdoc[static_cast<int64_t>(b) * a.Skv + jkey] : -1;
     const int* qdoc = a.qdoc + static_cast<int64_t>(b) * a.Sq;
     bool ok = true;
-    HeadWalk cur(bits, t0, ntq, per_head, hk * a.G, j0);
-    for (int j = 0; j < NJ; ++j) {
+    HeadWalk cur(bits, t0, ntq, per_head, hk * a.G, j0 + group);
+    for (int j = group; j < NJ; j += 2) {
       const int q = j % kSlots, ts = j % kTS;
       const float slope2 = kBias ? __ldg(a.slopes + cur.h) * kLog2e : 0.f;
       const int i0 = cur.w.t * kSub + hc * 32;  // the query row of this warp's first column
@@ -533,22 +538,30 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap& tq64, const CUtensor
       if (!ok) break;
       tc_fence_after();
       const uint32_t t_s = tmem + lane_off + ts * 128 + hc * 32, t_dp = t_s + kSub;
-      uint32_t sr[32], dr[32], pp[16], dd[16];
-      tmem_ld32(t_s, sr);
-      tmem_ld32(t_dp, dr);
-      tmem_wait_ld();
-      tmem_pin(sr);
-      tmem_pin(dr);
       const float* nlse2 = s_lse + q * kSub + hc * 32;
       const float* dlt = s_dlt + q * kSub + hc * 32;
-      row_pass<kCap, kBias, 1>(
-          sr, dr, cc, c2, capl2, slope2, static_cast<float>(d0), on,
-          [&](int e) { return *reinterpret_cast<const f32x2*>(nlse2 + e); },
-          [&](int e) { return *reinterpret_cast<const f32x2*>(dlt + e); },
-          pp, dd);
-      // P^T over the first half of this warp's S^T columns, dS^T over those of dP^T
-      tmem_st16(t_s, pp);
-      tmem_st16(t_dp, dd);
+      // P^T over the first half of this warp's S^T columns, dS^T over those of
+      // dP^T, 16 columns at a time, the next ones' loads under way meanwhile
+      uint32_t sr[2][16], dr[2][16], pp[8], dd[8];
+      tmem_ld16(t_s, sr[0]);
+      tmem_ld16(t_dp, dr[0]);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        tmem_wait_ld();
+        tmem_pin(sr[c]);
+        tmem_pin(dr[c]);
+        if (c == 0) {
+          tmem_ld16(t_s + 16, sr[1]);
+          tmem_ld16(t_dp + 16, dr[1]);
+        }
+        row_pass<kCap, kBias, 1>(
+            sr[c], dr[c], cc, c2, capl2, slope2, static_cast<float>(d0 + 16 * c), on >> (16 * c),
+            [&](int e) { return *reinterpret_cast<const f32x2*>(nlse2 + 16 * c + e); },
+            [&](int e) { return *reinterpret_cast<const f32x2*>(dlt + 16 * c + e); }, pp, dd);
+        tmem_st8(t_s + 8 * c, pp);
+        tmem_st8(t_dp + 8 * c, dd);
+      }
+      cur.next();
       cur.next();
       tmem_wait_st();
       tc_fence_before();
@@ -563,7 +576,7 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap& tq64, const CUtensor
       if (cs > 1) {  // this CTA's part, over the idle tiles: [dv, dk][key][D], 16-byte pieces permuted by row
         float* part = reinterpret_cast<float*>(smem) + (g * kT + key) * D;
 #pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
+        for (int c = group * (D / 64); c < (group + 1) * (D / 64); ++c) {
           uint32_t r[32];
           tmem_ld32(tmem + lane_off + kAcc + g * D + c * 32, r);
           tmem_wait_ld();
@@ -575,8 +588,10 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap& tq64, const CUtensor
                         : make_float4(u2f(r[4 * x]), u2f(r[4 * x + 1]), u2f(r[4 * x + 2]), u2f(r[4 * x + 3]));
         }
       } else {
-        store_acc<D>(tmem + lane_off + kAcc + g * D, NJ == 0, g == 0 ? 1.f : -a.scale, smem + L::kOffQ + (warp - 2) * 4096,
-                     lane, g == 0 ? a.dv : a.dk, ((static_cast<int64_t>(b) * a.Skv + key0 + wq * 32) * a.Hkv + hk) * D,
+        const int c = group * (D / 2);  // half the columns each
+        store_acc<D / 2>(tmem + lane_off + kAcc + g * D + c, NJ == 0, g == 0 ? 1.f : -a.scale,
+                     smem + L::kOffQ + (warp - 2) * 4096, lane, g == 0 ? a.dv : a.dk,
+                     ((static_cast<int64_t>(b) * a.Skv + key0 + wq * 32) * a.Hkv + hk) * D + c,
                      static_cast<int64_t>(a.Hkv) * D, nk - wq * 32, a.grad_bf16);
       }
     }
@@ -721,7 +736,7 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap& tq64, const CUtensorMa
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < L::kNumBars; ++i)
-      mbar_init(bar(i), i == kDqBarQ || (i >= kDqBarPFull && i < kDqBarDone) ? kRowWarps : 1);
+      mbar_init(bar(i), i == kDqBarQ ? kRowWarps : i >= kDqBarPFull && i < kDqBarDone ? kGroupWarps : 1);
     misc[1] = 0;
     fence_mbar_init();
   }
@@ -849,7 +864,8 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap& tq64, const CUtensorMa
   } else {
     // ===================== dS: one thread per query row and column half =====================
     const int wq = warp & 3;
-    const int hc = (warp - 2) >> 2;  // this warp's 32 key columns of each sub-step
+    const int group = (warp - 2) / kGroupWarps;  // takes the sub-steps j = group mod 2
+    const int hc = ((warp - 2) >> 2) & 1;        // this warp's 32 key columns of each
     const int row = wq * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
     const float c2 = a.scale * kLog2e, capl2 = a.cap * kLog2e;
@@ -860,15 +876,15 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap& tq64, const CUtensorMa
       nl2 = a.lse2p[o];
       dlt = a.dltp[o];
     }
-    // this row's Q (column half 0) or dO (half 1) into TMEM as the A operand
+    // this row's Q (column half 0) or dO (half 1; half the columns by each group) into TMEM as the A operand
     // of S and dP: column c holds elements 2c and 2c + 1 of the row, which is
     // the row's memory read as 32-bit words; rows past the end were filled with
     // zeros (read from global memory a row a lane, this took 7000 cycles)
     bool ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar(kDqBarLoad), 0, abort_flag, a.err, tmo));
     if (ok) {
       const uint8_t* src = smem + (hc == 0 ? L::kOffK : L::kOffV) + (kDqSlots - 2) * L::kSubT + row * 128;
-#pragma unroll 1
-      for (int c = 0; c < D / 64; ++c) {
+      if (D == 128 || group == 0) {
+        const int c = D == 128 ? group : 0;
         uint32_t w[32];
 #pragma unroll
         for (int x = 0; x < 8; ++x) {
@@ -890,7 +906,8 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap& tq64, const CUtensorMa
     const int* kdoc = a.kdoc + static_cast<int64_t>(b) * a.Skv;
     const float slope2 = kBias ? a.slopes[h] * kLog2e : 0.f;
     TileWalk<> cur(bits, 0, ntk, -1);
-    for (int j = 0; ok && j < NJ; ++j) {
+    if (group == 1) cur.next();
+    for (int j = group; ok && j < NJ; j += 2) {
       const int ts = j % kTS;
       const int j0 = cur.t * kSub + hc * 32;  // the key of this warp's first column
       const int n = lim - j0;
@@ -905,16 +922,24 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap& tq64, const CUtensorMa
       if (!ok) break;
       tc_fence_after();
       const uint32_t t_s = tmem + lane_off + ts * 128 + hc * 32, t_dp = t_s + kSub;  // this sub-step's slot
-      uint32_t sr[32], dr[32], pp[16], dd[16];
-      tmem_ld32(t_s, sr);
-      tmem_ld32(t_dp, dr);
-      tmem_wait_ld();
-      tmem_pin(sr);
-      tmem_pin(dr);
-      row_pass<kCap, kBias, -1>(
-          sr, dr, cc, c2, capl2, slope2, static_cast<float>(a.rel + q0 + row - j0), on,
-          [&](int) { return pair(nl2, nl2); }, [&](int) { return pair(dlt, dlt); }, pp, dd);
-      tmem_st16(t_s, dd);  // dS over the first half of this warp's S columns
+      uint32_t sr[2][16], dr[2][16], pp[8], dd[8];
+      tmem_ld16(t_s, sr[0]);
+      tmem_ld16(t_dp, dr[0]);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        tmem_wait_ld();
+        tmem_pin(sr[c]);
+        tmem_pin(dr[c]);
+        if (c == 0) {
+          tmem_ld16(t_s + 16, sr[1]);
+          tmem_ld16(t_dp + 16, dr[1]);
+        }
+        row_pass<kCap, kBias, -1>(
+            sr[c], dr[c], cc, c2, capl2, slope2, static_cast<float>(a.rel + q0 + row - j0 - 16 * c), on >> (16 * c),
+            [&](int) { return pair(nl2, nl2); }, [&](int) { return pair(dlt, dlt); }, pp, dd);
+        tmem_st8(t_s + 8 * c, dd);  // dS over the first half of this warp's S columns
+      }
+      cur.next();
       cur.next();
       tmem_wait_st();
       tc_fence_before();
@@ -925,10 +950,12 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap& tq64, const CUtensorMa
     if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar(kDqBarDone), 0, abort_flag, a.err, tmo));
     if (ok) {
       tc_fence_after();
-      // this half's D / 2 columns; NJ == 0: these rows reach no key
-      store_acc<D / 2>(tmem + lane_off + kAcc + hc * (D / 2), NJ == 0, -a.scale, smem + L::kOffK + (warp - 2) * 4096, lane,
-                       a.dq, ((static_cast<int64_t>(b) * a.Sq + q0 + wq * 32) * a.H + h) * D + hc * (D / 2),
-                       static_cast<int64_t>(a.H) * D, nq - wq * 32, a.grad_bf16);
+      // 32 columns a warp; NJ == 0: these rows reach no key
+      const int c = (hc * (D / 64) + (D == 128 ? group : 0)) * 32;
+      if (D == 128 || group == 0)
+        store_acc<32>(tmem + lane_off + kAcc + c, NJ == 0, -a.scale, smem + L::kOffK + (warp - 2) * 4096, lane, a.dq,
+                      ((static_cast<int64_t>(b) * a.Sq + q0 + wq * 32) * a.H + h) * D + c, static_cast<int64_t>(a.H) * D,
+                      nq - wq * 32, a.grad_bf16);
     }
   }
 
