@@ -23,8 +23,7 @@
 //     head), written by the delta kernel, so that a sub-tile's are one aligned
 //     bulk copy. Rows past the end, and rows that saw no key, hold -inf: p = 0.
 // P and dS are rounded to bf16 for their products; all sums are fp32.
-// Warp roles (320 threads): 0 = TMA producer, 1 = MMA issuer, 2-9 = row warps,
-// two per TMEM lane quarter, one per 32-column half of a sub-step.
+// Warp roles: 0 = TMA producer, 1 = MMA issuer, then the row warps.
 // The longest CTAs of each kind are launched first. Every wait is bounded; on
 // expiry the CTA records a timeout, lets its copies land, frees its tensor
 // memory and returns.
@@ -46,11 +45,20 @@
 namespace cp {
 namespace {
 
-// Row warps: two groups, which take the sub-steps in turn, so that the waits and
-// tensor-memory latencies of one group's pass go by under the other's. In a group
-// two per TMEM lane quarter, one per 32-column half of a sub-step.
-constexpr int kGroupWarps = 8, kRowWarps = 2 * kGroupWarps;
-constexpr int kThreadsB = 64 + 32 * kRowWarps;
+// Row warps come in groups of 8: two per TMEM lane quarter, one per 32-column
+// half of a sub-step. At D = 64 two groups take the sub-steps in turn, so that the
+// waits and tensor-memory latencies of one group's pass go by under the other's
+// (4608 tokens, 24 heads: plain 442 -> 412 us, cap 50 704 -> 607). At D = 128, where
+// the tensor cores set the pace, one group is faster (567 us against 588): its warps
+// have the registers for 32 columns at once.
+constexpr int kGroupWarps = 8;
+template <int D>
+struct Rows {
+  static constexpr int kGroups = D == 64 ? 2 : 1;
+  static constexpr int kWarps = kGroups * kGroupWarps;
+  static constexpr int kThreads = 64 + 32 * kWarps;
+  static constexpr int kN = 32 / kGroups;  // columns of a row pass
+};
 constexpr uint32_t kTmemColsB = 512;
 constexpr int kT = 128;         // keys per dk/dv CTA, query rows per dq CTA
 constexpr int kSub = 64;        // rows of a streamed sub-tile: query rows (dk/dv) or keys (dq) per sub-step
@@ -140,6 +148,11 @@ __device__ __forceinline__ void tmem_pin(uint32_t (&r)[N]) {
                  "+r"(r[i + 6]), "+r"(r[i + 7]));
 }
 
+__device__ __forceinline__ void tmem_ld(uint32_t t, uint32_t (&r)[32]) { tmem_ld32(t, r); }
+__device__ __forceinline__ void tmem_ld(uint32_t t, uint32_t (&r)[16]) { tmem_ld16(t, r); }
+__device__ __forceinline__ void tmem_st(uint32_t t, const uint32_t (&r)[16]) { tmem_st16(t, r); }
+__device__ __forceinline__ void tmem_st(uint32_t t, const uint32_t (&r)[8]) { tmem_st8(t, r); }
+
 // The sub-tiles of [t0, t1) that meet the CTA's rows' documents (own: their
 // range), into the bitmaps act and mixed; returns how many. All threads call it.
 __device__ __forceinline__ int walk_map(const DocRange* other, int nblk, const DocRange& own, int t0, int t1,
@@ -148,7 +161,7 @@ __device__ __forceinline__ int walk_map(const DocRange* other, int nblk, const D
   if (threadIdx.x == 0) *count = 0;
   __syncthreads();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int w0 = (t0 & ~31) + warp * 32; w0 < t1; w0 += kThreadsB) {
+  for (int w0 = (t0 & ~31) + warp * 32; w0 < t1; w0 += static_cast<int>(blockDim.x)) {
     const int t = w0 + lane;
     const DocRange r = doc_span(other, nblk, t, 1);
     const uint32_t w = __ballot_sync(0xffffffffu, t >= t0 && t < t1 && docs_meet(own, r));
@@ -163,22 +176,22 @@ __device__ __forceinline__ int walk_map(const DocRange* other, int nblk, const D
   return static_cast<int>(*count);
 }
 
-// 16 scores of a row pass: p in place of s and -ds in place of dp, packed as
+// N scores of a row pass: p in place of s and -ds in place of dp, packed as
 // bf16 pairs. Element e has the distance |d0 + step e| (step +1 or -1);
 // nl(e) = -lse log2e and dl(e) = delta of its row; on: the pairs that take part.
 // The signs are such that no packed operand has to be negated (an instruction
 // each): -ds = p (delta - dp), or with a cap p (delta - dp)(1 - tanh^2) from
 // p (dp - delta)(tanh^2 - 1); the epilogues multiply by -scale.
-template <bool kCap, bool kBias, int kStep, typename NL, typename ND>
-__device__ __forceinline__ void row_pass(const uint32_t (&sr)[16], const uint32_t (&dr)[16], const CapCoef& cc,
+template <bool kCap, bool kBias, int kStep, int N, typename NL, typename ND>
+__device__ __forceinline__ void row_pass(const uint32_t (&sr)[N], const uint32_t (&dr)[N], const CapCoef& cc,
                                          float c2, float capl2, float slope2, float d0, uint32_t on, NL nl, ND dl,
-                                         uint32_t (&pp)[8], uint32_t (&dd)[8]) {
+                                         uint32_t (&pp)[N / 2], uint32_t (&dd)[N / 2]) {
   const f32x2 c22 = pair(c2, c2), cap2 = pair(capl2, capl2), minus = pair(-1.f, -1.f);
   // kHow: 0 no cap, 3 and 6 the polynomials, 1 exact
   auto pass = [&](auto how_c) {
     constexpr int kHow = decltype(how_c)::value;
 #pragma unroll
-    for (int e = 0; e < 16; e += 2) {
+    for (int e = 0; e < N; e += 2) {
       const f32x2 s2 = pair_u(sr[e], sr[e + 1]);
       f32x2 b2 = nl(e);
       if constexpr (kBias) {
@@ -213,7 +226,7 @@ __device__ __forceinline__ void row_pass(const uint32_t (&sr)[16], const uint32_
   if constexpr (kCap) {
     float um = 0.f;
 #pragma unroll
-    for (int e = 0; e < 16; e += 4) um = fmax3(um, fmaxf(fabsf(u2f(sr[e])), fabsf(u2f(sr[e + 1]))), fmaxf(fabsf(u2f(sr[e + 2])), fabsf(u2f(sr[e + 3]))));
+    for (int e = 0; e < N; e += 4) um = fmax3(um, fmaxf(fabsf(u2f(sr[e])), fabsf(u2f(sr[e + 1]))), fmaxf(fabsf(u2f(sr[e + 2])), fabsf(u2f(sr[e + 3]))));
     um *= um;
     if (__all_sync(0xffffffffu, um <= cc.u3))
       pass(std::integral_constant<int, 3>{});
@@ -224,9 +237,9 @@ __device__ __forceinline__ void row_pass(const uint32_t (&sr)[16], const uint32_
   } else {
     pass(std::integral_constant<int, 0>{});
   }
-  if (__any_sync(0xffffffffu, (on & 0xffffu) != 0xffffu)) {
+  if (__any_sync(0xffffffffu, (on | ~(~0u >> (32 - N))) != ~0u)) {
 #pragma unroll
-    for (int x = 0; x < 8; ++x) {
+    for (int x = 0; x < N / 2; ++x) {
       const uint32_t keep = ((on >> (2 * x)) & 1u ? 0x0000ffffu : 0u) | ((on >> (2 * x + 1)) & 1u ? 0xffff0000u : 0u);
       pp[x] &= keep;
       dd[x] &= keep;
@@ -308,6 +321,7 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap& tq64, const CUtensor
                                          uint8_t* smem_raw, int alloc, int cs, int rank, int bx, int hk, int b) {
   using L = BSmem<D>;
   constexpr int kSlots = Ring<D>::kSlots, kTS = Ring<D>::kTS, kAcc = Ring<D>::kAcc;
+  constexpr int kGroups = Rows<D>::kGroups, kN = Rows<D>::kN, kThreadsB = Rows<D>::kThreads;
   // the swizzled tiles need a 1024-byte aligned base; a base that would need
   // more padding than the allocation holds is reported (uniformly, before any
   // barrier or TMEM use) instead of used
@@ -508,7 +522,7 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap& tq64, const CUtensor
   } else {
     // ===================== row pass: one thread per key row and column half =====================
     const int wq = warp & 3;
-    const int group = (warp - 2) / kGroupWarps;  // takes the sub-steps j = group mod 2
+    const int group = (warp - 2) / kGroupWarps;  // takes the sub-steps j = group mod kGroups
     const int hc = ((warp - 2) >> 2) & 1;        // this warp's 32 query columns of each
     const int key = wq * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
@@ -520,7 +534,7 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap& tq64, const CUtensor
     const int* qdoc = a.qdoc + static_cast<int64_t>(b) * a.Sq;
     bool ok = true;
     HeadWalk cur(bits, t0, ntq, per_head, hk * a.G, j0 + group);
-    for (int j = group; j < NJ; j += 2) {
+    for (int j = group; j < NJ; j += kGroups) {
       const int q = j % kSlots, ts = j % kTS;
       const float slope2 = kBias ? __ldg(a.slopes + cur.h) * kLog2e : 0.f;
       const int i0 = cur.w.t * kSub + hc * 32;  // the query row of this warp's first column
@@ -541,28 +555,28 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap& tq64, const CUtensor
       const float* nlse2 = s_lse + q * kSub + hc * 32;
       const float* dlt = s_dlt + q * kSub + hc * 32;
       // P^T over the first half of this warp's S^T columns, dS^T over those of
-      // dP^T, 16 columns at a time, the next ones' loads under way meanwhile
-      uint32_t sr[2][16], dr[2][16], pp[8], dd[8];
-      tmem_ld16(t_s, sr[0]);
-      tmem_ld16(t_dp, dr[0]);
+      // dP^T, kN columns at a time, the next ones' loads under way meanwhile
+      uint32_t sr[kGroups][kN], dr[kGroups][kN], pp[kN / 2], dd[kN / 2];
+      tmem_ld(t_s, sr[0]);
+      tmem_ld(t_dp, dr[0]);
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
+      for (int c = 0; c < kGroups; ++c) {
         tmem_wait_ld();
         tmem_pin(sr[c]);
         tmem_pin(dr[c]);
-        if (c == 0) {
-          tmem_ld16(t_s + 16, sr[1]);
-          tmem_ld16(t_dp + 16, dr[1]);
+        if (c + 1 < kGroups) {
+          tmem_ld(t_s + (c + 1) * kN, sr[(c + 1) % kGroups]);
+          tmem_ld(t_dp + (c + 1) * kN, dr[(c + 1) % kGroups]);
         }
         row_pass<kCap, kBias, 1>(
-            sr[c], dr[c], cc, c2, capl2, slope2, static_cast<float>(d0 + 16 * c), on >> (16 * c),
-            [&](int e) { return *reinterpret_cast<const f32x2*>(nlse2 + 16 * c + e); },
-            [&](int e) { return *reinterpret_cast<const f32x2*>(dlt + 16 * c + e); }, pp, dd);
-        tmem_st8(t_s + 8 * c, pp);
-        tmem_st8(t_dp + 8 * c, dd);
+            sr[c], dr[c], cc, c2, capl2, slope2, static_cast<float>(d0 + kN * c), on >> (kN * c),
+            [&](int e) { return *reinterpret_cast<const f32x2*>(nlse2 + kN * c + e); },
+            [&](int e) { return *reinterpret_cast<const f32x2*>(dlt + kN * c + e); }, pp, dd);
+        tmem_st(t_s + kN / 2 * c, pp);
+        tmem_st(t_dp + kN / 2 * c, dd);
       }
-      cur.next();
-      cur.next();
+#pragma unroll
+      for (int c = 0; c < kGroups; ++c) cur.next();
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -576,7 +590,7 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap& tq64, const CUtensor
       if (cs > 1) {  // this CTA's part, over the idle tiles: [dv, dk][key][D], 16-byte pieces permuted by row
         float* part = reinterpret_cast<float*>(smem) + (g * kT + key) * D;
 #pragma unroll 1
-        for (int c = group * (D / 64); c < (group + 1) * (D / 64); ++c) {
+        for (int c = group * (D / 32 / kGroups); c < (group + 1) * (D / 32 / kGroups); ++c) {
           uint32_t r[32];
           tmem_ld32(tmem + lane_off + kAcc + g * D + c * 32, r);
           tmem_wait_ld();
@@ -588,8 +602,9 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap& tq64, const CUtensor
                         : make_float4(u2f(r[4 * x]), u2f(r[4 * x + 1]), u2f(r[4 * x + 2]), u2f(r[4 * x + 3]));
         }
       } else {
-        const int c = group * (D / 2);  // half the columns each
-        store_acc<D / 2>(tmem + lane_off + kAcc + g * D + c, NJ == 0, g == 0 ? 1.f : -a.scale,
+        constexpr int kCols = D / kGroups;
+        const int c = group * kCols;
+        store_acc<kCols>(tmem + lane_off + kAcc + g * D + c, NJ == 0, g == 0 ? 1.f : -a.scale,
                      smem + L::kOffQ + (warp - 2) * 4096, lane, g == 0 ? a.dv : a.dk,
                      ((static_cast<int64_t>(b) * a.Skv + key0 + wq * 32) * a.Hkv + hk) * D + c,
                      static_cast<int64_t>(a.Hkv) * D, nk - wq * 32, a.grad_bf16);
@@ -707,6 +722,7 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap& tq64, const CUtensorMa
   using L = DqSmem<D>;
   // TMEM: the slots, dQ, then Q and dO (D / 2 columns each)
   constexpr int kTS = Ring<D>::kTS, kAcc = Ring<D>::kAcc, kOp = kAcc + D;
+  constexpr int kGroups = Rows<D>::kGroups, kN = Rows<D>::kN;
   const uint32_t pad = (1024u - (smem_addr(smem_raw) & 1023u)) & 1023u;
   if (pad > static_cast<uint32_t>(alloc - L::kBytes)) {
     if (threadIdx.x == 0) atomicOr(a.err, kDevErrLayout);
@@ -736,7 +752,7 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap& tq64, const CUtensorMa
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < L::kNumBars; ++i)
-      mbar_init(bar(i), i == kDqBarQ ? kRowWarps : i >= kDqBarPFull && i < kDqBarDone ? kGroupWarps : 1);
+      mbar_init(bar(i), i == kDqBarQ ? Rows<D>::kWarps : i >= kDqBarPFull && i < kDqBarDone ? kGroupWarps : 1);
     misc[1] = 0;
     fence_mbar_init();
   }
@@ -864,7 +880,7 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap& tq64, const CUtensorMa
   } else {
     // ===================== dS: one thread per query row and column half =====================
     const int wq = warp & 3;
-    const int group = (warp - 2) / kGroupWarps;  // takes the sub-steps j = group mod 2
+    const int group = (warp - 2) / kGroupWarps;  // takes the sub-steps j = group mod kGroups
     const int hc = ((warp - 2) >> 2) & 1;        // this warp's 32 key columns of each
     const int row = wq * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
@@ -876,15 +892,15 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap& tq64, const CUtensorMa
       nl2 = a.lse2p[o];
       dlt = a.dltp[o];
     }
-    // this row's Q (column half 0) or dO (half 1; half the columns by each group) into TMEM as the A operand
+    // this row's Q (column half 0) or dO (half 1) into TMEM as the A operand
     // of S and dP: column c holds elements 2c and 2c + 1 of the row, which is
     // the row's memory read as 32-bit words; rows past the end were filled with
     // zeros (read from global memory a row a lane, this took 7000 cycles)
     bool ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar(kDqBarLoad), 0, abort_flag, a.err, tmo));
     if (ok) {
       const uint8_t* src = smem + (hc == 0 ? L::kOffK : L::kOffV) + (kDqSlots - 2) * L::kSubT + row * 128;
-      if (D == 128 || group == 0) {
-        const int c = D == 128 ? group : 0;
+#pragma unroll 1
+      for (int c = group; c < D / 64; c += kGroups) {
         uint32_t w[32];
 #pragma unroll
         for (int x = 0; x < 8; ++x) {
@@ -907,7 +923,7 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap& tq64, const CUtensorMa
     const float slope2 = kBias ? a.slopes[h] * kLog2e : 0.f;
     TileWalk<> cur(bits, 0, ntk, -1);
     if (group == 1) cur.next();
-    for (int j = group; ok && j < NJ; j += 2) {
+    for (int j = group; ok && j < NJ; j += kGroups) {
       const int ts = j % kTS;
       const int j0 = cur.t * kSub + hc * 32;  // the key of this warp's first column
       const int n = lim - j0;
@@ -922,25 +938,25 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap& tq64, const CUtensorMa
       if (!ok) break;
       tc_fence_after();
       const uint32_t t_s = tmem + lane_off + ts * 128 + hc * 32, t_dp = t_s + kSub;  // this sub-step's slot
-      uint32_t sr[2][16], dr[2][16], pp[8], dd[8];
-      tmem_ld16(t_s, sr[0]);
-      tmem_ld16(t_dp, dr[0]);
+      uint32_t sr[kGroups][kN], dr[kGroups][kN], pp[kN / 2], dd[kN / 2];
+      tmem_ld(t_s, sr[0]);
+      tmem_ld(t_dp, dr[0]);
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
+      for (int c = 0; c < kGroups; ++c) {
         tmem_wait_ld();
         tmem_pin(sr[c]);
         tmem_pin(dr[c]);
-        if (c == 0) {
-          tmem_ld16(t_s + 16, sr[1]);
-          tmem_ld16(t_dp + 16, dr[1]);
+        if (c + 1 < kGroups) {
+          tmem_ld(t_s + (c + 1) * kN, sr[(c + 1) % kGroups]);
+          tmem_ld(t_dp + (c + 1) * kN, dr[(c + 1) % kGroups]);
         }
         row_pass<kCap, kBias, -1>(
-            sr[c], dr[c], cc, c2, capl2, slope2, static_cast<float>(a.rel + q0 + row - j0 - 16 * c), on >> (16 * c),
+            sr[c], dr[c], cc, c2, capl2, slope2, static_cast<float>(a.rel + q0 + row - j0 - kN * c), on >> (kN * c),
             [&](int) { return pair(nl2, nl2); }, [&](int) { return pair(dlt, dlt); }, pp, dd);
-        tmem_st8(t_s + 8 * c, dd);  // dS over the first half of this warp's S columns
+        tmem_st(t_s + kN / 2 * c, dd);  // dS over the first half of this warp's S columns
       }
-      cur.next();
-      cur.next();
+#pragma unroll
+      for (int c = 0; c < kGroups; ++c) cur.next();
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -950,12 +966,11 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap& tq64, const CUtensorMa
     if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar(kDqBarDone), 0, abort_flag, a.err, tmo));
     if (ok) {
       tc_fence_after();
-      // 32 columns a warp; NJ == 0: these rows reach no key
-      const int c = (hc * (D / 64) + (D == 128 ? group : 0)) * 32;
-      if (D == 128 || group == 0)
-        store_acc<32>(tmem + lane_off + kAcc + c, NJ == 0, -a.scale, smem + L::kOffK + (warp - 2) * 4096, lane, a.dq,
-                      ((static_cast<int64_t>(b) * a.Sq + q0 + wq * 32) * a.H + h) * D + c, static_cast<int64_t>(a.H) * D,
-                      nq - wq * 32, a.grad_bf16);
+      // half the columns by each column half (of the first group); NJ == 0: these rows reach no key
+      if (group == 0)
+        store_acc<D / 2>(tmem + lane_off + kAcc + hc * (D / 2), NJ == 0, -a.scale, smem + L::kOffK + (warp - 2) * 4096, lane,
+                         a.dq, ((static_cast<int64_t>(b) * a.Sq + q0 + wq * 32) * a.H + h) * D + hc * (D / 2),
+                         static_cast<int64_t>(a.H) * D, nq - wq * 32, a.grad_bf16);
     }
   }
 
@@ -979,7 +994,7 @@ __host__ __device__ constexpr int bwd_alloc() {
 // dq CTAs from the last rows, heads fastest, so that long CTAs start first and
 // short ones fill the end.
 template <int D, bool kCap, bool kBias>
-__global__ void __launch_bounds__(kThreadsB, 1)
+__global__ void __launch_bounds__(Rows<D>::kThreads, 1)
     score_bwd_tc_kernel(const __grid_constant__ CUtensorMap tq64, const __grid_constant__ CUtensorMap to64,
                         const __grid_constant__ CUtensorMap tk64, const __grid_constant__ CUtensorMap tv64,
                         const __grid_constant__ ScoreArgs a, const __grid_constant__ CapCoef cc) {
@@ -1067,7 +1082,7 @@ cudaError_t launch_rule(const ScoreArgs& a, const BwdMaps& m, cudaStream_t s) {
   // the first and after the last
   const int cs = cluster_for(8.0, kv_items, ntq * a.G, q_ctas, ntk * 3 / 4, a.causal ? 0.5 : 1.0, false);
   const int64_t ctas = kv_items * cs + (q_ctas + cs - 1) / cs * cs;
-  return launch_clusters(score_bwd_tc_kernel<D, kCap, kBias>, ctas / cs, 1, 1, cs, kThreadsB, kAlloc, a.Sq > 0, s, m.q64,
+  return launch_clusters(score_bwd_tc_kernel<D, kCap, kBias>, ctas / cs, 1, 1, cs, Rows<D>::kThreads, kAlloc, a.Sq > 0, s, m.q64,
                          m.o64, m.k64, m.v64, a, make_cap_coef(a.scale, a.cap, true));
 }
 
