@@ -143,6 +143,13 @@ def test_decode_whatever_the_table_holds(tokens, H, Hkv, D, page, dt, out_dt):
     assert (bl[3] < lse[3]).all() and (page < 65 or ((bad[3] == 0).all() and torch.isneginf(bl[3]).all()))
 
 
+def test_decode_of_an_empty_table():
+    s = make([0, 0], 4, 2, 64, 16, BF, seed=0)
+    s["table"] = s["table"][:, :0].contiguous()
+    out, lse = decode(s, 0.1, BF)
+    assert (out == 0).all() and torch.isneginf(lse).all() and cpa().cp_check_device_status() == 0
+
+
 @pytest.mark.parametrize("dt", [BF, F4])
 @pytest.mark.parametrize("cap,bias", [(30.0, False), (0.5, False), (0.0, True), (20.0, True), (1e5, False)])
 def test_decode_score_rule(dt, cap, bias):

@@ -216,6 +216,88 @@ def test_large_scores_and_growing_maxima(dt):
         check_bwd(q, k, v, out, dout, lse, 0.6, rule, grads, f"growing {sorted(rule)}")
 
 
+MANY = {  # more items than run at once, so that CTAs go on from one to the next: rule of (B, S)
+    "plain": lambda B, S: {},
+    "causal, cap": lambda B, S: dict(causal=True, softcap=15.0),
+    "slopes both ways": lambda B, S: dict(slopes=slopes(40)),
+    "prefix, slopes, cap": lambda B, S: dict(causal=True, softcap=30.0, slopes=slopes(40),
+                                             prefix_lens=(torch.arange(B, dtype=torch.int32) * 97)),
+    # items without a key among the others: the whole second pair of entry 1, all of entry 2
+    "documents": lambda B, S: dict(causal=True, **{n: torch.where(
+        (torch.arange(B)[:, None] == 2) | ((torch.arange(B)[:, None] == 1) & (torch.arange(S)[None] >= 256)),
+        -1, docs(B, S, 4, 5, 7)).to(torch.int32) for n in ("q_docs", "kv_docs")}),
+}
+
+
+@pytest.mark.parametrize("D,out_dt", [(64, BF), (128, BF), (128, F4)])
+@pytest.mark.parametrize("name", list(MANY))
+def test_more_items_than_multiprocessors(name, D, out_dt):
+    B, S, H, Hkv = 4, 300, 40, 8
+    rule = MANY[name](B, S)
+    q, k, v, dout = draw(B, S, S, H, Hkv, D, BF, seed=D, qmul=1.5)
+    out, lse = run_fwd(q, k, v, D ** -0.5, rule, out_dt)
+    check_fwd(q, k, v, D ** -0.5, rule, out, lse, name)
+    if D == 64:
+        grads = run_bwd(q, k, v, out, dout, lse, D ** -0.5, rule, out_dt)
+        check_bwd(q, k, v, out, dout, lse, D ** -0.5, rule, grads, name)
+    again, al = run_fwd(q, k, v, D ** -0.5, rule, out_dt)
+    assert torch.equal(out, again) and torch.equal(lse, al)
+
+
+@pytest.mark.parametrize("dt", [F4, BF])
+@pytest.mark.parametrize("rule", [{}, dict(causal=True), dict(causal=True, slopes=torch.tensor([0.05, -0.05])),
+                                  dict(softcap=400.0)], ids=["plain", "causal", "slopes", "cap"])
+def test_rows_and_tiles_at_any_level(rule, dt):
+    """Scores whose level differs from row to row (within a warp) and from one stretch of keys to the next, from far
+    below to far above what exp2 can hold."""
+    B, S, H, D = 1, 600, 2, 64
+    q, k, v, dout = draw(B, S, S, H, H, D, dt, seed=11)
+    u = torch.ones(D) / 8
+    rows = torch.tensor([0.0, -1.0, 1.0, -0.2, 0.2, -4.0, 4.0, 0.02])[torch.arange(S) % 8]
+    tiles = torch.tensor([3.0, -3.0, 40.0, 0.0, -40.0])[torch.arange(S) // 128]
+    q = (0.1 * q.float() + rows[None, :, None, None] * u).to(dt)
+    k = (0.1 * k.float() + tiles[None, :, None, None] * u).to(dt)
+    out, lse = run_fwd(q, k, v, 1.5, rule, dt)
+    check_fwd(q, k, v, 1.5, rule, out, lse, "levels")
+    grads = run_bwd(q, k, v, out, dout, lse, 1.5, rule, dt)
+    check_bwd(q, k, v, out, dout, lse, 1.5, rule, grads, "levels")
+
+
+@pytest.mark.parametrize("n", [262144, 262145, 600000, 1 << 21])
+def test_documents_among_more_keys_than_one_bitmap_bit_each(n):
+    """A few rows against very many keys of many documents, bf16, against float64 on the same GPU: (w + e) p|v| with
+    the pairs that take part for n in e."""
+    B, S, H, D, every = 1, 150, 2, 64, 64 * 1024
+    g = torch.Generator(device="cuda").manual_seed(n)
+    r = lambda *s: torch.randn(s, generator=g, device="cuda").to(BF)
+    q, k, v = r(B, S, H, D), r(B, n, 1, D), r(B, n, 1, D)
+    pos = torch.arange(n, device="cuda")
+    # stretches of 300 keys at every 65536th of document i mod 3; the others' documents are nobody's
+    kd = torch.where(pos % every < 300, (pos // every) % 3, 10 + pos // 1000).to(torch.int32)[None].contiguous()
+    qd = (torch.arange(S, device="cuda") // 10 % 4).to(torch.int32)[None].contiguous()   # 3: no key at all
+    out, lse = torch.empty_like(q, dtype=F4), torch.empty((B, H, S), device="cuda")
+    cpa().cp_scored_attn_fwd(q, k, v, out, lse, D ** -0.5, causal=True, q_pos0=n - S, q_docs=qd, kv_docs=kd)
+    assert cpa().cp_check_device_status() == 0
+    at = (kd[0] < 3).nonzero()[:, 0]     # the keys that any row sees
+    kf, vf = k[0, at, 0].double(), v[0, at, 0].double()
+    keep = (qd[0][:, None] == kd[0, at][None]) & (at[None] <= (n - S + torch.arange(S, device="cuda"))[:, None])
+    m = len(at)
+    for h in range(H):
+        x = (q[0, :, h].double() @ kf.T) * D ** -0.5
+        big = (q[0, :, h].double().abs() @ kf.abs().T).max().item() * D ** -0.5
+        x = x.masked_fill(~keep, -float("inf"))
+        wl = torch.logsumexp(x, 1)
+        none = torch.isneginf(wl)
+        assert none.any() and torch.equal(torch.isneginf(lse[0, h]), none) and (out[0, none, h] == 0).all()
+        p = torch.exp(x - torch.where(none, torch.zeros_like(wl), wl)[:, None])
+        d = (D + 20) * U * big
+        e = 2 * (2 * d + 2.0 ** -21 + m * U)
+        over = (out[0, :, h].double() - p @ vf).abs() - (2.0 ** -8 + e) * (p @ vf.abs()) - 2 * U * (p @ vf).abs()
+        assert over.max().item() <= 0
+        ok = ~none
+        assert ((lse[0, h].double() - wl)[ok].abs() <= 2 * d + 2.0 ** -20 + m * U + 4 * U * wl[ok].abs()).all()
+
+
 def test_gradients_match_differences():
     """fp32 gradients against central differences of the library's own forward."""
     B, S, H, Hkv, D = 1, 70, 4, 2, 64
