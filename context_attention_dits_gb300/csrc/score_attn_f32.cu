@@ -1,5 +1,5 @@
-// score_attn_f32.cu — attention with a score rule on the CUDA cores, fp32
-// throughout: forward and backward.
+// score_attn_f32.cu — attention with a score rule, fp32 inputs, results and
+// sums: forward and backward.
 //
 // With x_ij = scale q_i.k_j, capped to cap tanh(x / cap) if there is a cap,
 // less slope_h |i - j| if there are slopes, -inf where a mask rules the pair
