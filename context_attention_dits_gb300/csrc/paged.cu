@@ -66,9 +66,9 @@ __device__ __forceinline__ int cache_row(const PagedArgs& a, int b, int pos) {
 // threads share a row, each moving 16 bytes of k and of v at a time. Bound by
 // HBM where there are many rows, by the launch where there are few. The first
 // pieces are on their way before the row's place is looked up (a length, then a
-// page), whose latency is as long as theirs. 6 x 4607 tokens of 8 heads of 128,
-// bf16: 21.6 us, 113 MB read and as many written, of which L2 keeps a part; a
-// token of one sequence 1.9 us.
+// page), whose latency is as long as theirs. 6 sequences with up to 4607 new
+// tokens of 8 heads of 128, bf16, 113 MB read and written in all: 21.2 us; one
+// token of 64 sequences 1.7 us.
 // ----------------------------------------------------------------------------
 template <int TPR>
 __global__ void __launch_bounds__(256) paged_append_kernel(const __grid_constant__ PagedArgs a, int pieces) {
