@@ -25,8 +25,8 @@
 //     score_math.cuh;
 //   * bias: one more FMA a score in tiles on one side of the diagonal.
 // P is formed with whatever reference the row has, 0 at first, in place of the
-// running maximum, and checked afterwards by the row's sum (2^-32 to 2^32, far
-// from where fp32 or bf16 end) and largest s^2; a warp that fails reloads S and
+// running maximum, and checked afterwards by the row's sum (2^-20 to 2^20, which
+// leaves v up to 1e30 and down to 1e-30) and largest s^2; a warp that fails reloads S and
 // takes the exact path (maximum first).
 //
 // What bounds it: a query tile's step is a chain of S (512 cycles of the tensor
@@ -66,7 +66,7 @@ namespace {
 
 constexpr int kThreads = 352;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: rescale only when the max grows by > 2^8
-constexpr float kSumMost = 4294967296.f;   // of a row's P over a tile
+constexpr float kSumMost = 1048576.f;      // of a row's P over a tile
 constexpr uint32_t kTmemCols = 512;
 // Words of a bitmap of key tiles: a bit for a tile up to 262144 keys, for 2, 4
 // or 8 neighbours beyond.
@@ -569,8 +569,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool fits = false;
         // speculatively with the reference that the row has (0 before it has one):
         // any will do that keeps its sums far from overflow, which a row sum
-        // within 2^32 proves (every P is at most that), and from underflow, where
-        // the first sum is above 2^-32; and s^2 within the polynomial's range
+        // within 2^20 proves (every P is at most that), and from underflow, where
+        // the first sum is above 2^-20; and s^2 within the polynomial's range
         const bool none = masked && (on[0] | on[1] | on[2] | on[3]) == 0u;
         auto holds = [&](float sum) { return sum <= kSumMost && (m_used != -INFINITY || sum >= 1.f / kSumMost || none); };
         if (!kBias || below || above) {

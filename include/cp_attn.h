@@ -486,7 +486,8 @@ size_t cp_paged_attn_workspace_size_for(int B, int H, int Hkv, int D, int page_s
  * (out_dt: float32 or dt), lse [B, H] float32. Several sequences may share
  * pages. A sequence of length 0 gets out = 0, lse = -inf. Calls that may
  * overlap on the GPU (and captured graphs replayed at the same time) need a
- * workspace each. Errors: INVALID_ARG, NOT_DIVISIBLE (H % Hkv), ALIGNMENT,
+ * workspace each; it may be NULL where cp_paged_attn_workspace_size_for is 0.
+ * Errors: INVALID_ARG, NOT_DIVISIBLE (H % Hkv), ALIGNMENT,
  * WORKSPACE, CUDA, UNSUPPORTED_DEVICE.
  */
 cp_status cp_paged_attn_decode(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,

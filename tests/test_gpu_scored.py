@@ -298,6 +298,22 @@ def test_documents_among_more_keys_than_one_bitmap_bit_each(n):
         assert ((lse[0, h].double() - wl)[ok].abs() <= 2 * d + 2.0 ** -20 + m * U + 4 * U * wl[ok].abs()).all()
 
 
+@pytest.mark.parametrize("dt", [F4, BF])
+def test_values_of_any_size(dt):
+    """out is linear in v and the gradients are in dout: powers of two come out bit for bit."""
+    B, S, H, Hkv, D = 1, 500, 4, 2, 128
+    q, k, v, dout = draw(B, S, S, H, Hkv, D, dt, seed=13, qmul=2.0)
+    rule = dict(causal=True, softcap=30.0, slopes=slopes(4))
+    out, lse = run_fwd(q, k, v, D ** -0.5, rule, dt)
+    for e in (90, -60):
+        far, same = run_fwd(q, k, v * 2.0 ** e, D ** -0.5, rule, dt)
+        assert torch.equal(far, out * 2.0 ** e) and torch.equal(same, lse)
+    grads = run_bwd(q, k, v, out, dout, lse, D ** -0.5, rule, dt)
+    for e in (60, -30):
+        far = run_bwd(q, k, v, out, dout * 2.0 ** e, lse, D ** -0.5, rule, dt)
+        assert all(torch.equal(x, y * 2.0 ** e) for x, y in zip(far, grads))
+
+
 def test_gradients_match_differences():
     """fp32 gradients against central differences of the library's own forward."""
     B, S, H, Hkv, D = 1, 70, 4, 2, 64
