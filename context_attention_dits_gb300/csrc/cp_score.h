@@ -1,5 +1,5 @@
 // cp_score.h — launch parameters of the score-rule attention (forward,
-// backward) and of the paged cache, shared by their kernels and host drivers.
+// backward) and of the paged cache, shared by their kernels and entry points.
 // Not part of the public ABI.
 #pragma once
 
@@ -192,7 +192,7 @@ cudaError_t launch_clusters(void (*kernel)(P...), int64_t items, unsigned y, uns
   return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
 }
 
-// From cp_api.cu: the checks and tensor maps that the host drivers share.
+// From cp_api.cu: the checks and tensor maps that the entry points share.
 // 0, or the cp_status of the current device's check.
 int host_device(uint32_t** err, int* sms);
 // bf16 [Bn, S, H, D] with 64-column x box_rows boxes of one head, 128-byte swizzle.
