@@ -105,21 +105,27 @@ struct PagedArgs {
 constexpr int paged_rows(bool bf16) { return bf16 ? 16 : 8; }
 // CTAs that run at once: two on a multiprocessor where their buffers fit.
 constexpr int paged_ctas(int D, bool bf16) { return D * (bf16 ? 2 : 4) <= 256 ? kPagedCtas : kPagedCtas / 2; }
-// Decode in one launch: the CTAs (1 to 8, a cluster) that share a unit (a
+// Decode in one launch: the CTAs (1 to 16, a cluster) that share a unit (a
 // sequence's key/value head and group of query heads), or 0 where the list of all
 // blocks is cut among the CTAs instead. Clusters save the second launch and the
-// workspace, but a unit has 8 CTAs at most and idle ones take no other's work. So:
+// workspace, but a unit has 8 or 16 CTAs at most and idle ones take no other's work. So:
 // two blocks a CTA where all units' CTAs run at once, more where they would not,
 // up to 8 (bf16) or 4 (fp32, whose blocks are twice the bytes). Clusters against
 // the list, 24 heads on 8, D = 128, device us: bf16 1 x 1000 keys 5.6 / 8.4,
 // 1 x 4096 10.0 / 11.7, 8 x 1000 8.7 / 10.4, 4 x 4096 11.7 / 15.9, 1 x 8000
 // (16 blocks a CTA) 15.9 / 15.1; fp32 1 x 1000 8.2 / 9.9, 1 x 4096 (8) 18.1 / 15.0.
+// Clusters of 16 find room beside each other for some 8 units, and only where two
+// CTAs fit a multiprocessor: against clusters of 8, bf16 1 x 4096 8.7 / 10.0,
+// 1 x 8192 12.1 / 13.7, 1 x 2000 6.7 / 6.9, 1 x 1500 6.8 / 6.2, but 2 x 2000 (16
+// units) 12.5 / 7.9, fp32 1 x 2000 16.1 / 11.3.
+constexpr int kPagedCluster = 16;
 inline int paged_cluster(int D, bool bf16, int B, int Hkv, int G, int max_pages, int page_shift) {
   const int64_t blocks = ((static_cast<int64_t>(max_pages) << page_shift) + kPagedBlock - 1) / kPagedBlock;
   const int64_t units = static_cast<int64_t>(B) * Hkv * ((G + paged_rows(bf16) - 1) / paged_rows(bf16));
   const int ctas = paged_ctas(D, bf16);
   int cs = 1;
-  while (cs < 8 && blocks > 2 * cs && units * cs * 2 <= ctas) cs *= 2;
+  const int most = units <= 8 && ctas == kPagedCtas ? kPagedCluster : kPagedCluster / 2;
+  while (cs < most && blocks > (cs < 8 ? 2 : 4) * cs && units * cs * 2 <= ctas) cs *= 2;
   return units <= ctas && blocks <= cs * (bf16 ? 8 : 4) ? cs : 0;
 }
 cudaError_t launch_paged_append(const PagedArgs& a, int elem_bytes, cudaStream_t s);
@@ -127,13 +133,14 @@ cudaError_t launch_paged_decode(const PagedArgs& a, bool bf16, cudaStream_t s);
 
 // Lets a kernel use `bytes` of dynamic shared memory, once per device (the call
 // costs as much host time as a launch).
-template <auto kKernel>
+template <auto kKernel, bool kClusters16 = false>
 cudaError_t allow_smem(int bytes) {
   static std::atomic<uint64_t> done{0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess || (dev < 64 && (done.load(std::memory_order_acquire) >> dev & 1))) return e;
   e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (kClusters16 && e == cudaSuccess) e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e == cudaSuccess && dev < 64) done.fetch_or(uint64_t{1} << dev, std::memory_order_release);
   return e;
 }

@@ -37,6 +37,7 @@
 #include <climits>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "cp_internal.h"
 #include "cp_ptx.cuh"
@@ -715,35 +716,42 @@ __global__ void __launch_bounds__(kDecThreads) paged_decode_cluster_kernel(const
   if (cs == 1) return;
   cluster_sync();
   const uint32_t mine = smem_addr(part);
-  const int end = 2 * cluster_part(nrow * D / 2, rank + 1, cs);
-  for (int i = 2 * (cluster_part(nrow * D / 2, rank, cs) + threadIdx.x); i < end; i += 2 * kDecThreads) {
-    const int r = i / D;
-    float2 ml[8], o[8];
+  auto join = [&](auto most_c) {
+    constexpr int kMost = decltype(most_c)::value;
+    const int end = 2 * cluster_part(nrow * D / 2, rank + 1, cs);
+    for (int i = 2 * (cluster_part(nrow * D / 2, rank, cs) + threadIdx.x); i < end; i += 2 * kDecThreads) {
+      const int r = i / D;
+      float2 ml[kMost], o[kMost];
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      ml[c] = make_float2(-INFINITY, 0.f);
-      o[c] = make_float2(0.f, 0.f);
-      if (c < cs) {  // every load under way at once
-        const uint32_t at = cluster_peer(mine, c);
-        ml[c] = ld_peer2(at + (C::kRows * D + 2 * r) * 4);
-        o[c] = ld_peer2(at + i * 4);
+      for (int c = 0; c < kMost; ++c) {
+        ml[c] = make_float2(-INFINITY, 0.f);
+        o[c] = make_float2(0.f, 0.f);
+        if (c < cs) {  // every load under way at once
+          const uint32_t at = cluster_peer(mine, c);
+          ml[c] = ld_peer2(at + (C::kRows * D + 2 * r) * 4);
+          o[c] = ld_peer2(at + i * 4);
+        }
       }
-    }
-    float mx = -INFINITY, sum = 0.f, x = 0.f, y = 0.f;
+      float mx = -INFINITY, sum = 0.f, x = 0.f, y = 0.f;
 #pragma unroll
-    for (int c = 0; c < 8; ++c) mx = fmaxf(mx, ml[c].x);
-    const float base = mx == -INFINITY ? 0.f : mx;
+      for (int c = 0; c < kMost; ++c) mx = fmaxf(mx, ml[c].x);
+      const float base = mx == -INFINITY ? 0.f : mx;
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      const float f = exp2f(ml[c].x - base);
-      sum = fmaf(ml[c].y, f, sum);
-      x = fmaf(o[c].x, f, x);
-      y = fmaf(o[c].y, f, y);
+      for (int c = 0; c < kMost; ++c) {
+        const float f = exp2f(ml[c].x - base);
+        sum = fmaf(ml[c].y, f, sum);
+        x = fmaf(o[c].x, f, x);
+        y = fmaf(o[c].y, f, y);
+      }
+      put_out(a, row0 * D + i, sum != 0.f ? x / sum : 0.f);
+      put_out(a, row0 * D + i + 1, sum != 0.f ? y / sum : 0.f);
+      if (i % D == 0) a.lse[row0 + r] = natural_lse(mx, sum);
     }
-    put_out(a, row0 * D + i, sum != 0.f ? x / sum : 0.f);
-    put_out(a, row0 * D + i + 1, sum != 0.f ? y / sum : 0.f);
-    if (i % D == 0) a.lse[row0 + r] = natural_lse(mx, sum);
-  }
+  };
+  if (cs <= 8)
+    join(std::integral_constant<int, 8>{});
+  else
+    join(std::integral_constant<int, kPagedCluster>{});
   cluster_sync();  // a CTA's shared memory stays until its peers have read it
 }
 
@@ -754,7 +762,7 @@ cudaError_t decode_d(const PagedArgs& a, cudaStream_t s) {
   cudaError_t e;
   const int cs = paged_cluster(D, C::kBf16, a.B, a.Hkv, a.G, a.max_pages, a.page_shift);
   if (cs > 0) {
-    if ((e = allow_smem<paged_decode_cluster_kernel<D, T>>(C::kSmem)) != cudaSuccess) return e;
+    if ((e = allow_smem<paged_decode_cluster_kernel<D, T>, true>(C::kSmem)) != cudaSuccess) return e;
     const int units = a.Hkv * ((a.G + C::kRows - 1) / C::kRows);
     return launch_clusters(paged_decode_cluster_kernel<D, T>, units, a.B, 1, cs, kDecThreads, C::kSmem, false, s, a);
   }
