@@ -24,8 +24,8 @@
 //     below 1/2 (or 1), checked after the fact by the largest s^2; see
 //     score_math.cuh;
 //   * bias: one more FMA a score in tiles on one side of the diagonal.
-// P is formed with whatever reference the row has, 0 at first, in place of the
-// running maximum, and checked afterwards by the row's sum (2^-20 to 2^20, which
+// P is formed with whatever reference the row has, 0 at first (the maximum in
+// rows of few keys), in place of the running maximum, and checked afterwards by the row's sum (2^-20 to 2^20, which
 // leaves v up to 1e30 and down to 1e-30) and largest s^2; a warp that fails reloads S and
 // takes the exact path (maximum first).
 //
@@ -67,6 +67,7 @@ namespace {
 constexpr int kThreads = 352;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: rescale only when the max grows by > 2^8
 constexpr float kSumMost = 1048576.f;      // of a row's P over a tile
+constexpr int kFewKeys = 32;
 constexpr uint32_t kTmemCols = 512;
 // Words of a bitmap of key tiles: a bit for a tile up to 262144 keys, for 2, 4
 // or 8 neighbours beyond.
@@ -472,8 +473,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int qd = a.qdoc && at < a.Sq ? a.qdoc[static_cast<int64_t>(item->b) * a.Sq + at] : -1;
       const float slope2 = kBias ? a.slopes[item->h] * kLog2e : 0.f;
       float m_used = -INFINITY, l = 0.f;
-      int level = 0;  // of the cap's polynomial: 3, 6 terms' range, or neither (each item's own: which CTA
-                      // takes it, and after which, must not show in its bits)
+      // 0: as below; with a cap, of whose polynomial these are the 3 terms' range, 1: the
+      // 6 terms' range; 2: the next tile exactly. Each item's own: which CTA takes it,
+      // and after which, must not show in its bits. With the reference 0 the heaviest
+      // key's P is rounded, with the maximum it is 1: rows of few keys, whose result
+      // hangs on that one, begin exactly (their error would be up to twice that of out's
+      // own rounding; so it is below 1.4 of it)
+      int level = __any_sync(0xffffffffu, lim < kFewKeys) ? 2 : 0;
       TileWalk<true> cur(a.qdoc ? map_at(n & 1) : nullptr, 0, item->ntile, walk_start(*item), shift);
       for (int k = item->n0; k > 0; --k) cur.next();
       for (int it = 0; it < NT; ++it) {
@@ -507,6 +513,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           same_docs<4>(qd, ids, same);
 #pragma unroll
           for (int w = 0; w < 4; ++w) on[w] &= same[w];
+        }
+        if (masked && a.qdoc) {
+          const int keys = __popc(on[0]) + __popc(on[1]) + __popc(on[2]) + __popc(on[3]);
+          if (__any_sync(0xffffffffu, m_used == -INFINITY && keys > 0 && keys < kFewKeys)) level = 2;
         }
         ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar(kBarSFull + i), (pc + it) & 1, abort_flag, a.err, tmo));
         if (!ok) break;
@@ -584,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               lsum = speculate(integral_constant<int, 6>{}, std::false_type{});
               fits = holds(lsum) && umax <= cc.u6;
             }
-          } else {
+          } else if (level == 0) {
             lsum = masked ? speculate(integral_constant<int, 1>{}, std::true_type{})
                           : speculate(integral_constant<int, 1>{}, std::false_type{});
             fits = holds(lsum);
@@ -658,6 +668,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_st32(t_s + c * 32, sr);
           }
           tmem_wait_st();
+          level = 0;
           if (kCap) {
             const float w = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(um)));
             level = w <= cc.u3 ? 0 : w <= cc.u6 ? 1 : 2;

@@ -314,6 +314,25 @@ def test_values_of_any_size(dt):
         assert all(torch.equal(x, y * 2.0 ** e) for x, y in zip(far, grads))
 
 
+@pytest.mark.parametrize("rule", [{}, dict(softcap=20.0), dict(slopes=slopes(4)), dict(softcap=20.0, slopes=slopes(4))],
+                         ids=["plain", "cap", "slopes", "both"])
+def test_rows_of_few_keys_are_exact_to_the_rounding_of_out(rule):
+    """bf16: a row of one key is that key's value bit for bit (P = 1). Rows of up to 31 keys: rounding P adds at most
+    what out's own rounding is off by, in the 2-norm, less the heaviest key's part, whose P is exact: below sqrt(2)."""
+    B, S, H, D = 2, 300, 4, 64
+    q, k, v, _ = draw(B, S, S, H, H, D, BF, seed=17, qmul=3.0)
+    own = torch.arange(S, dtype=torch.int32).repeat(B, 1)
+    out, _ = run_fwd(q, k, v, D ** -0.5, dict(rule, q_docs=own, kv_docs=own), BF)
+    assert torch.equal(out, v)
+    out, _ = run_fwd(q, k, v, D ** -0.5, dict(rule, causal=True), BF)
+    assert torch.equal(out[:, 0], v[:, 0])
+    for n, ids in ((3, own // 3), (20, own // 20), (31, own // 31)):
+        r = dict(rule, causal=True, q_docs=ids, kv_docs=ids)
+        out, _ = run_fwd(q, k, v, D ** -0.5, r, BF)
+        want = torch.from_numpy(so.scored_attention(q, k, v, D ** -0.5, **r)[0])
+        assert (out.double() - want).norm() <= 2 ** 0.5 * (want.to(BF).double() - want).norm(), n
+
+
 def test_gradients_match_differences():
     """fp32 gradients against central differences of the library's own forward."""
     B, S, H, Hkv, D = 1, 70, 4, 2, 64
