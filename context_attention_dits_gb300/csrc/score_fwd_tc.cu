@@ -37,10 +37,10 @@
 // out, which come from all multiprocessors at once. A CTA therefore goes on to
 // the item of a block that has not started, and the loads and S of its first tile
 // go by under the stores of the last (900 cycles from item to item); longest
-// items first. Measured, 4608 tokens, 24 heads on 8, bf16, D = 128: plain 161 us
-// (1617 TFLOP/s; the plain kernel 166), causal 93.5, cap 50 210, causal with it
-// 127, slopes 167, causal with them 96, causal with both 143; documents of 512 34.
-// D = 64: 124, 75, 191, 116, 146, 83, 141.
+// items first. Measured, 4608 tokens, 24 heads on 8, bf16, D = 128: plain 160 us
+// (1626 TFLOP/s; the plain kernel 165), causal 93.4, cap 50 216, causal with it
+// 130, slopes 170, causal with them 99, causal with both 144; documents of 512 35.
+// D = 64: 124, 77, 196, 118, 150, 87, 144.
 // Every wait is bounded (cp_ptx.cuh); on expiry the CTA drains its copies and
 // MMAs, frees TMEM and returns.
 // A few rows against many keys (a chunk of a long prompt) are too few items for
