@@ -117,8 +117,10 @@ __device__ __forceinline__ int cluster_part(int n, int rank, int size) {
   return static_cast<int>(static_cast<int64_t>(n) * rank >> (__ffs(size) - 1));
 }
 // Every thread of every CTA of the cluster comes here; shared memory written
-// before is visible after.
+// before is visible after. (The aligned forms ask for converged warps, which a
+// loop or branch that lanes leave apart does not promise.)
 __device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // The address of this CTA's shared-memory address in CTA `rank` of the cluster.

@@ -211,7 +211,9 @@ __device__ __forceinline__ void decode_unit(const PagedArgs& a, int b, int n, in
   // a chunk's rows: lane r < 16 finds row r (-1 past the end)
   auto find = [&](int blk) {
     const int j = blk * kPagedBlock + warp * kChunk + lane;
-    return lane < kChunk && blk < blk1 && j < n ? cache_row(a, b, j) : -1;
+    const int row = lane < kChunk && blk < blk1 && j < n ? cache_row(a, b, j) : -1;
+    __syncwarp();  // the matrix loads and products that follow want the warp converged
+    return row;
   };
   auto load = [&](int rows, int stage) {
     const uint32_t base = wb + stage * 2 * C::kTile;

@@ -73,8 +73,12 @@ __device__ __forceinline__ void add4(float4& x, float4 y) {
   x.w += y.w;
 }
 
-// Barrier of the caller's group.
-__device__ __forceinline__ void group_sync(int g) { asm volatile("bar.sync %0, %1;" ::"r"(g + 1), "n"(kGrp) : "memory"); }
+// Barrier of the caller's group, whose warps converge for it (and for the matrix
+// instructions behind it).
+__device__ __forceinline__ void group_sync(int g) {
+  __syncwarp();
+  asm volatile("bar.sync %0, %1;" ::"r"(g + 1), "n"(kGrp) : "memory");
+}
 
 __device__ __forceinline__ void copy16(float* dst, const float* src, bool on) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(on ? 16 : 0)
@@ -497,6 +501,7 @@ __device__ __forceinline__ void dq_cta(const ScoreArgs& a, float* sm, int cs, in
           s[n][e] = on ? p * (dp[n][e] - dlt[i]) * dcap : 0.f;
         }
       }
+    __syncwarp();  // lanes may have parted over masks and the cap; matrix instructions want the warp converged
     second<D>(acc, s, K + c32 * C::kRow, g, t);
     group_sync(grp);
     copy(K, a.k, cur.t);
@@ -612,6 +617,7 @@ __device__ __forceinline__ void dkdv_cta(const ScoreArgs& a, float* sm, int cs, 
           dp[n][e] = on ? p * (dp[n][e] - dl) * dcap : 0.f;
         }
       }
+    __syncwarp();
     second<D>(dv, s, dO + c32 * C::kRow, g, t);
     group_sync(grp);
     copy(dO, a.dout);

@@ -623,7 +623,6 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap& tq64, const CUtensor
   }
   if (cs > 1) {
     static_assert(2 * kT * D * 4 <= L::kOffLse, "the parts lie over the tiles");
-    __syncwarp();
     cluster_sync();
     // a row's D / 4 pieces on neighbouring lanes, kIn rows a thread at once: every
     // load of a step is under way before the first is used

@@ -603,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (__all_sync(0xffffffffu, fits)) {
           tmem_st32(t_s, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));
           tmem_st32(t_s + 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[32]));
-          if (m_used == -INFINITY && !none) m_used = 0.f;
+          m_used = m_used == -INFINITY && !none ? 0.f : m_used;
         } else {
           // exactly, 32 columns at a time: scores in log2 units back over S and
           // their maximum; move to it if it grew by more than 2^8, rescaling O
@@ -665,6 +665,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int e = 0; e < 32; e += 2) mxs = fmax3(mxs, u2f(sr[e]), u2f(sr[e + 1]));
             }
+            __syncwarp();  // (tensor-memory accesses want the warp converged, here and below)
             tmem_st32(t_s + c * 32, sr);
           }
           tmem_wait_st();
@@ -678,6 +679,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             f = ex2_approx(m_used - mxs);
             m_used = mxs;
           }
+          __syncwarp();
           const float nm = m_used == -INFINITY ? 0.f : -m_used;
           f32x2 ls[2] = {0ull, 0ull};
 #pragma unroll 1
@@ -736,6 +738,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           *reinterpret_cast<float2*>(smem + L::kOffStat + (i * kTileM + row) * 8) = make_float2(m_used, l);
         else if (row < rows_valid)
           a.lse[(static_cast<int64_t>(b) * a.H + h) * a.Sq + tok0 + row] = lse_v;
+        __syncwarp();
         // 32 rows x 128 bytes (64 columns in bf16, 32 in fp32) are staged in this
         // warp's buffer, 128-byte swizzled, and stored by TMA, which cuts the rows
         // past the end: the stores of all multiprocessors come at about the same
@@ -797,7 +800,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int h = static_cast<int>(blockIdx.x) >> (__ffs(cs) - 1), b = blockIdx.y;
     const int row0 = (static_cast<int>(gridDim.z) - 1 - static_cast<int>(blockIdx.z)) * 2 * kTileM;
     const int nrows = min(2 * kTileM, a.Sq - row0);
-    __syncwarp();
     cluster_sync();
     // a row's D / 4 pieces on neighbouring lanes, kIn rows a thread at once: every
     // load of a step is under way before the first is used

@@ -339,3 +339,15 @@ def test_wrapper_refusals():
     with pytest.raises(cpa().CpError):   # a page of 12 rows
         bad = torch.zeros((4, 12, 2, 64), dtype=BF, device="cuda")
         cpa().cp_paged_kv_append(new, new, bad, bad, s["table"], s["lens"])
+
+
+@pytest.mark.parametrize("dt", [BF, F4])
+@pytest.mark.parametrize("H,Hkv,D", [(1, 1, 64), (3, 1, 64), (1, 1, 128)])
+def test_decode_of_few_heads_by_wide_clusters(H, Hkv, D, dt):
+    """A unit of one to three heads shared by 8 or 16 CTAs: most threads have nothing to join."""
+    s = make([4000, 1, 0], H, Hkv, D, 16, dt, seed=H + D, most=4096)
+    one = {n: (t[:1].contiguous() if n in ("q", "table", "lens") else t) for n, t in s.items()}
+    for x in (one, s):
+        out, lse = decode(x, D ** -0.5, dt, softcap=30.0)
+        check_decode(x, D ** -0.5, out, lse, "wide clusters", 30.0)
+    assert cpa().cp_check_device_status() == 0

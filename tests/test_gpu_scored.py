@@ -450,3 +450,16 @@ def test_wrapper_refusals():
         cpa().cp_scored_attn_bwd(q, k, k, q, q, lse, g[0].float(), g[1], g[2], 0.1)
     with pytest.raises(ValueError):
         cpa().cp_scored_attn_bwd(q, k, k, q, q, lse, g[0], g[1][:, :4], g[2], 0.1)
+
+
+@pytest.mark.parametrize("dt", [F4, BF])
+@pytest.mark.parametrize("Sq,Skv,H,Hkv,D", [(1, 1500, 2, 1, 64), (5, 1100, 1, 1, 128), (1500, 3, 16, 1, 64),
+                                            (700, 1, 8, 1, 128)])
+def test_clusters_on_a_handful_of_rows_or_keys(Sq, Skv, H, Hkv, D, dt):
+    """Clusters that join fewer rows than they have CTAs or threads."""
+    rule = dict(softcap=20.0, slopes=slopes(H), q_pos0=max(Skv - Sq, 0))
+    q, k, v, dout = draw(1, Sq, Skv, H, Hkv, D, dt, seed=Sq + Skv)
+    out, lse = run_fwd(q, k, v, D ** -0.5, rule, dt)
+    check_fwd(q, k, v, D ** -0.5, rule, out, lse, "handful")
+    grads = run_bwd(q, k, v, out, dout, lse, D ** -0.5, rule, dt)
+    check_bwd(q, k, v, out, dout, lse, D ** -0.5, rule, grads, "handful")
