@@ -452,9 +452,9 @@ cp_status cp_scored_attn_bwd(const void* q, const void* k, const void* v, const 
  * j % page_size of page block_table[b, j / page_size]. Entries past a
  * sequence's tokens are not read. At most 4096 sequences a call.
  * A page index outside [0, num_pages), a sequence length below 0 or past
- * max_pages * page_size is recorded in the device error word
- * (cp_check_device_status then returns CP_ERR_INVALID_ARG) and what it names
- * is left out: append skips the token, decode takes the key as masked and the
+ * max_pages * page_size, a position of 2^31 or more is recorded in the device
+ * error word (cp_check_device_status then returns CP_ERR_INVALID_ARG) and what
+ * it names is left out: append skips the token, decode takes the key as masked and the
  * length as clamped.
  */
 

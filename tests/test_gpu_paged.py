@@ -351,3 +351,20 @@ def test_decode_of_few_heads_by_wide_clusters(H, Hkv, D, dt):
         out, lse = decode(x, D ** -0.5, dt, softcap=30.0)
         check_decode(x, D ** -0.5, out, lse, "wide clusters", 30.0)
     assert cpa().cp_check_device_status() == 0
+
+
+def test_append_past_the_last_position_an_int_holds():
+    """A table for more than 2^31 tokens: the token at position 2^31 - 1 is written, those behind are reported."""
+    cache = torch.zeros((2, 65536, 1, 64), dtype=BF, device="cuda")
+    k, v = cache.clone(), cache.clone()
+    table = torch.zeros((2, 40000), dtype=torch.int32, device="cuda")
+    table[0, 32767] = 1
+    new = torch.randn((2, 3, 1, 64), generator=torch.Generator().manual_seed(1)).to(BF).cuda()
+    lens = torch.tensor([2 ** 31 - 1, 7], dtype=torch.int32, device="cuda")
+    cpa().cp_paged_kv_append(new, -new, k, v, table, lens)
+    assert cpa().cp_check_device_status() == -1 and cpa().cp_check_device_status() == 0
+    for got, x in ((k, new), (v, -new)):
+        want = cache.clone()
+        want[1, 65535] = x[0, 0]
+        want[0, 7:10] = x[1]
+        assert torch.equal(got, want)
