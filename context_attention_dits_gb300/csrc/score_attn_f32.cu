@@ -199,9 +199,11 @@ struct Scorer {
     float x = dot * scale;
     dcap = 1.f;
     if (capped) {
-      const float t = tanhf(x * inv_cap);
-      x = cap * t;
-      dcap = 1.f - t * t;
+      const float y = x * inv_cap;
+      x = cap * tanhf(y);
+      // 1 - tanh^2 without its cancellation
+      const float e = ex2_approx(-2.f * kL2e * fabsf(y)), r = rcp_approx(1.f + e);
+      dcap = 4.f * e * r * r;
     }
     return fmaf(x, kL2e, -slope2 * static_cast<float>(abs(dist)));
   }

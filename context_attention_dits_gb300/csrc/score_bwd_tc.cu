@@ -214,14 +214,15 @@ __device__ __forceinline__ void row_pass(const uint32_t (&sr)[N], const uint32_t
         t2 = fma_x2(s2, c22, b2);
         q2 = fma_x2(dp2, minus, dl(e));
       } else {
-        f32x2 th;  // tanh
+        f32x2 th, nd;  // tanh, tanh^2 - 1
         if constexpr (kHow >= 3) {
           th = mul_x2(s2, cap_poly<kHow>(cc, mul_x2(s2, s2)));
+          nd = fma_x2(th, th, minus);
         } else {
-          th = pair(cap_exact(cc, u2f(sr[e])), cap_exact(cc, u2f(sr[e + 1])));
+          tanh_exact(cc, s2, th, nd);
         }
         t2 = fma_x2(th, cap2, b2);
-        q2 = mul_x2(fma_x2(dl(e), minus, dp2), fma_x2(th, th, minus));
+        q2 = mul_x2(fma_x2(dl(e), minus, dp2), nd);
       }
       float t0, t1;
       split(t2, t0, t1);

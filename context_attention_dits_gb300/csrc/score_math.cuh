@@ -8,7 +8,10 @@
 // (5.0e-8); the host folds cap, log2 e and (scale / cap)^(2k+1) into the
 // coefficients. Beyond |x| = 1 the exact form 1 - 2 / (1 + e^2x) is taken: two
 // more results of the special-function unit a score, which is what the softmax
-// is short of (16 a cycle and multiprocessor against 128 FMAs).
+// is short of (16 a cycle and multiprocessor against 128 FMAs). The derivative
+// 1 - tanh^2 is formed from the tanh only below |x| = 1: beyond, where it
+// cancels (2e-3 of it lost at 6.5, all at 9), it is 4 e / (1 + e)^2 with
+// e = e^-2|x|, by the same two results.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -124,6 +127,18 @@ __device__ __forceinline__ f32x2 cap_poly(const CapCoef& c, f32x2 u) {
 
 __device__ __forceinline__ float cap_exact(const CapCoef& c, float s) {
   return c.capl2 * (1.f - __fdividef(2.f, 1.f + ex2_approx(s * c.a0)));
+}
+
+// tanh and tanh^2 - 1 of a pair of scores (coefficients with unit set).
+__device__ __forceinline__ void tanh_exact(const CapCoef& c, f32x2 s, f32x2& th, f32x2& neg_d) {
+  float x0, x1;
+  split(mul_x2(s, pair(c.a0, c.a0)), x0, x1);
+  const float e0 = ex2_approx(-fabsf(x0)), e1 = ex2_approx(-fabsf(x1));
+  const f32x2 r = pair(rcp_approx(1.f + e0), rcp_approx(1.f + e1)), er = mul_x2(pair(e0, e1), r);
+  float t0, t1;
+  split(fma_x2(er, pair(-2.f, -2.f), pair(1.f, 1.f)), t0, t1);
+  th = pair(copysignf(t0, x0), copysignf(t1, x1));
+  neg_d = mul_x2(mul_x2(er, r), pair(-4.f, -4.f));
 }
 
 // 0 .. 127 in pairs: the columns of a tile, for biases linear in the column.

@@ -463,3 +463,46 @@ def test_clusters_on_a_handful_of_rows_or_keys(Sq, Skv, H, Hkv, D, dt):
     check_fwd(q, k, v, D ** -0.5, rule, out, lse, "handful")
     grads = run_bwd(q, k, v, out, dout, lse, D ** -0.5, rule, dt)
     check_bwd(q, k, v, out, dout, lse, D ** -0.5, rule, grads, "handful")
+
+
+@pytest.mark.parametrize("dt", [F4, BF])
+@pytest.mark.parametrize("D,slope", [(64, False), (128, True)])
+@pytest.mark.parametrize("low,high", [(0.3, 1.5), (4.0, 4.0), (6.5, 6.5), (9.0, 9.0), (4.0, 9.0)])
+def test_gradients_of_saturated_scores(low, high, D, slope, dt):
+    """Every pair far into the cap's flat part, |x / cap| from low to high: the gradients are small there, and hold
+    their digits. With y = x / cap known to (D + 20) u |y| the derivative 1 - tanh^2, whose logarithm's slope in y is
+    at most 2, is off by 2 (D + 20) u |y| relative, and by 8 |y| u + 32 u for its own evaluation (an exponential of 2 |y|,
+    a quotient, three products); the rest is as in the module's E, the second term times the derivative."""
+    B, S, H, Hkv, cap = 1, 200, 4, 2, 2.0
+    scale = D ** -0.5
+    q, k, v, dout = draw(B, S, S, H, Hkv, D, dt, seed=int(10 * high) + D)
+    level = torch.linspace(low, high, S)[torch.randperm(S, generator=torch.Generator().manual_seed(3))]
+    sign = torch.where(torch.arange(S) % 3 == 0, -1.0, 1.0)
+    q = ((level * sign * cap / (scale * D))[None, :, None, None] + 0.02 * q.float()).to(dt)
+    k = (1.0 + 0.03 * k.float()).to(dt)
+    rule = dict(softcap=cap, causal=True)
+    if slope:
+        rule["slopes"] = slopes(H)
+    out, lse = run_fwd(q, k, v, scale, rule, dt)
+    check_fwd(q, k, v, scale, rule, out, lse, "saturated")
+    grads = run_bwd(q, k, v, out, dout, lse, scale, rule, F4)
+    want = so.scored_attention_bwd(q, k, v, out, dout, lse, scale, **rule)
+    d, e, n = errors_of(q, k, scale, rule)
+    w = 2.0 ** -8 if dt == BF else 0.0
+    qf, kf, vf, of, gf, lf = (t.double().numpy() for t in (q, k, v, out, dout, lse))
+    bound = [np.zeros_like(x) for x in want[:2]]
+    for h in range(H):
+        p, dcap = probs(q, k, lf, 0, h, scale, rule)
+        g, vv = gf[0, :, h], vf[0, :, h // 2]
+        y = np.abs(scale * qf[0, :, h] @ kf[0, :, h // 2].T) / cap
+        rel = 2 * (D + 20) * U * (scale * np.abs(qf[0, :, h]) @ np.abs(kf[0, :, h // 2]).T) / cap + (8 * y + 32) * U
+        ds = p * (g @ vv.T - np.sum(g * of[0, :, h], 1)[:, None]) * dcap
+        ga = np.abs(g)
+        E = (w + e + rel) * np.abs(ds) + p * dcap * (D + 8) * U * (ga @ np.abs(vv).T + np.sum(ga * np.abs(of[0, :, h]), 1)[:, None])
+        bound[0][0, :, h] = scale * (E @ np.abs(kf[0, :, h // 2]))
+        bound[1][0, :, h // 2] += scale * (E.T @ np.abs(qf[0, :, h]))
+    for name, x, z, bd in zip(("dq", "dk"), grads, want, bound):
+        x = x.double().numpy()
+        over = np.abs(x - z) - bd - 2 * U * np.abs(z)
+        assert np.all(np.isfinite(x)) and over.max() <= 0, (
+            f"{name}: past its bound by {over.max():.3e} of {bd.flat[over.argmax()]:.3e}")
