@@ -28,9 +28,9 @@ bool known(cp_dtype t) { return t == CP_BF16 || t == CP_F32; }
 // An output is fp32 or of the inputs' type.
 bool out_type_ok(cp_dtype out, cp_dtype in) { return known(out) && (out == CP_F32 || out == in); }
 
-// A scale and a cap whose quotient and coefficients fp32 holds.
+// A scale and a cap whose quotient, products with log2 e and coefficients fp32 holds.
 bool scores_ok(float scale, float softcap) {
-  if (!std::isfinite(scale) || !std::isfinite(softcap) || softcap < 0.f) return false;
+  if (!(std::fabs(scale) <= 1e30f) || !(softcap >= 0.f && softcap <= 1e30f)) return false;
   return softcap == 0.f || (softcap >= 1e-30f && softcap >= std::fabs(scale) * 1e-30f);
 }
 

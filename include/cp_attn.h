@@ -396,7 +396,7 @@ cp_status cp_attention_bwd(const void* q, const void* k, const void* v, const fl
  * with their own q_pos0 and kv_pos0 whose fp32 (out, lse) cp_lse_merge joins.
  * -------------------------------------------------------------------------*/
 typedef struct {
-  float softcap;              /* > 0: cap of the scores, at least 1e-30 and 1e-30 |scale|; 0: none */
+  float softcap;              /* > 0: cap of the scores, at least 1e-30 and 1e-30 |scale|, at most 1e30; 0: none */
   const float* slopes;        /* device [H], fp32 (any sign, finite), or NULL */
   int causal;                 /* nonzero: keys after the query take no part */
   const int32_t* prefix_lens; /* device [B] or NULL; needs causal. Keys at positions below it are open to all rows */
@@ -407,8 +407,8 @@ typedef struct {
 
 /* Host-only: the status the two calls below return for these sizes before
  * looking at a tensor's pointer. rule may be NULL (no cap, bias or mask). INVALID_ARG: a size, D not
- * 64 or 128, more than 65535 batch entries or heads or 2^21 rows, a scale or
- * softcap that is not finite, a softcap out of its range, a position out of range,
+ * 64 or 128, more than 65535 batch entries or heads or 2^21 rows, a scale beyond
+ * +-1e30 or not a number, a softcap out of its range, a position out of range,
  * one of q_docs, kv_docs without the other; UNSUPPORTED_COMBO: prefix_lens
  * without causal; NOT_DIVISIBLE: H % Hkv. */
 cp_status cp_scored_attn_validate(int B, int H, int Hkv, int Sq, int Skv, int D, float scale,

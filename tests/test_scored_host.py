@@ -114,3 +114,17 @@ def test_python_wrappers_reject_host_tensors():
     with pytest.raises(ValueError):
         cpa.cp_paged_attn_decode(q[0], q, q, torch.zeros((1, 1), dtype=torch.int32), torch.zeros(1, dtype=torch.int32),
                                  q[0], l[0], 0.1)
+
+
+def test_scales_and_caps_whose_products_would_overflow():
+    """cap log2 e past fp32's range made NaN of a zero score in the bf16 backward."""
+    f = lambda **kw: cpa.cp_scored_attn_validate(2, 8, 2, 5, 7, 64, **kw)
+    assert f(softcap=1e30) == 0 and f(scale=1e30) == 0 and f(scale=-1e30, softcap=1.0) == 0
+    for bad in (dict(softcap=1.1e30), dict(softcap=3e38), dict(scale=1.1e30), dict(scale=-3e38), dict(scale=float("-inf")),
+                dict(softcap=float("inf"))):
+        for dt in (torch.bfloat16, torch.float32):
+            assert f(**bad, dtype=dt) == _lib.CP_ERR_INVALID_ARG, bad
+    L = _lib.lib()
+    for scale, cap in ((0.1, 3e38), (3e38, 0.0), (float("nan"), 0.0)):
+        assert L.cp_paged_attn_decode(P, P, P, P, P, P, P, 1, 2, 2, 64, 8, 16, 4, scale, cap, None, None, 0, 0, 0,
+                                      None) == _lib.CP_ERR_INVALID_ARG
