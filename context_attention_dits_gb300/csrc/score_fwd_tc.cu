@@ -25,9 +25,10 @@
 //     score_math.cuh;
 //   * bias: one more FMA a score in tiles on one side of the diagonal.
 // P is formed with whatever reference the row has, 0 at first (the maximum in
-// rows of few keys), in place of the running maximum, and checked afterwards by the row's sum (2^-20 to 2^20, which
-// leaves v up to 1e30 and down to 1e-30) and largest s^2; a warp that fails reloads S and
-// takes the exact path (maximum first).
+// rows of few keys), in place of the running maximum, and checked afterwards by
+// the row's sum over the tile (2^-20 to 2^20) and up to it (at most 2^26, which
+// leaves v up to 2^96 in rows of any length, and down to 2^-96), and the largest
+// s^2; a warp that fails reloads S and takes the exact path (maximum first).
 //
 // What bounds it: a query tile's step is a chain of S (512 cycles of the tensor
 // pipe at D = 128), the softmax (some 1050: 128 exponentials a thread), P V (512)
@@ -67,6 +68,7 @@ namespace {
 constexpr int kThreads = 352;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: rescale only when the max grows by > 2^8
 constexpr float kSumMost = 1048576.f;      // of a row's P over a tile
+constexpr float kTotalMost = 67108864.f;   // 2^26, over its tiles: beyond, the reference moves up as far
 constexpr int kFewKeys = 32;
 constexpr uint32_t kTmemCols = 512;
 // Words of a bitmap of key tiles: a bit for a tile up to 262144 keys, for 2, 4
@@ -579,10 +581,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool fits = false;
         // speculatively with the reference that the row has (0 before it has one):
         // any will do that keeps its sums far from overflow, which a row sum
-        // within 2^20 proves (every P is at most that), and from underflow, where
-        // the first sum is above 2^-20; and s^2 within the polynomial's range
+        // within 2^20 and those before within 2^26 prove (every P is at most that),
+        // and from underflow, where the first sum is above 2^-20; and s^2 within the
+        // polynomial's range
         const bool none = masked && (on[0] | on[1] | on[2] | on[3]) == 0u;
-        auto holds = [&](float sum) { return sum <= kSumMost && (m_used != -INFINITY || sum >= 1.f / kSumMost || none); };
+        auto holds = [&](float sum) {
+          return sum <= kSumMost && l <= kTotalMost && (m_used != -INFINITY || sum >= 1.f / kSumMost || none);
+        };
         if (!kBias || below || above) {
           using std::integral_constant;
           if constexpr (kCap) {
@@ -606,7 +611,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           m_used = m_used == -INFINITY && !none ? 0.f : m_used;
         } else {
           // exactly, 32 columns at a time: scores in log2 units back over S and
-          // their maximum; move to it if it grew by more than 2^8, rescaling O
+          // their maximum; move to it if it grew by more than 2^8 (and by 2^26 at
+          // least where the sum has reached that), rescaling O
           // and l by the same factor (O is idle here: PV of the previous tile
           // completed before S of this tile was committed, and PV of this tile
           // waits for P); then P. Columns [16 c, 16 c + 16) of P lie over
@@ -674,10 +680,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float w = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(um)));
             level = w <= cc.u3 ? 0 : w <= cc.u6 ? 1 : 2;
           }
-          const bool need = mxs > m_used + kRescaleThreshold || (m_used == -INFINITY && mxs > -INFINITY);
+          const bool full = l > kTotalMost;
+          const bool need = full || mxs > m_used + kRescaleThreshold || (m_used == -INFINITY && mxs > -INFINITY);
           if (need) {
-            f = ex2_approx(m_used - mxs);
-            m_used = mxs;
+            const float to = full ? fmaxf(mxs, m_used + 26.f) : mxs;
+            f = ex2_approx(m_used - to);
+            m_used = to;
           }
           __syncwarp();
           const float nm = m_used == -INFINITY ? 0.f : -m_used;

@@ -390,10 +390,15 @@ cp_status cp_attention_bwd(const void* q, const void* k, const void* v, const fl
  *   !causal, or position j <= position i, or position j < prefix_lens[b]; and
  *   no document ids, or q_docs[b,i] == kv_docs[b,j] >= 0.
  * out_i = sum_j softmax_j(x_ij) v_j and lse_i = ln sum_j exp(x_ij) over the
- * pairs that take part; a row without any gets out = 0, lse = -inf. Rows of a
- * masked pair must still hold finite numbers: a weight of 0 meets them in the
- * matrix products. Because positions are global, a ring's blocks are calls
- * with their own q_pos0 and kv_pos0 whose fp32 (out, lse) cp_lse_merge joins.
+ * pairs that take part; a row without any gets out = 0, lse = -inf. q, k, v (and
+ * out, dout) hold finite numbers, those of masked pairs too: a weight of 0 meets
+ * them in the matrix products, and an infinity in fp32 is NaN once it is split
+ * for its three products. |v| is at most 2^96 (8e28; sums are formed before they
+ * are divided by the weights'), other fp32 inputs at most 2^127. x is held in
+ * fp32, so a weight is as far off as fp32's rounding of the row's largest |x|,
+ * slopes and distances included. Because positions are global, a ring's blocks
+ * are calls with their own q_pos0 and kv_pos0 whose fp32 (out, lse)
+ * cp_lse_merge joins.
  * -------------------------------------------------------------------------*/
 typedef struct {
   float softcap;              /* > 0: cap of the scores, at least 1e-30 and 1e-30 |scale|, at most 1e30; 0: none */
@@ -423,8 +428,9 @@ size_t cp_scored_attn_bwd_workspace_size(int B, int H, int Sq, int Skv, int docs
  * Forward of one block.
  *   q [B, Sq, H, D], k, v [B, Skv, Hkv, D] (dt, dense); out [B, Sq, H, D] of
  *   out_dt: float32, or dt; lse [B, H, Sq] float32.
- * Skv == 0 yields out = 0, lse = -inf; B == 0 or Sq == 0 launches nothing.
- * Errors: those of cp_scored_attn_validate, INVALID_ARG (null pointers,
+ * Skv == 0 yields out = 0, lse = -inf; B == 0 or Sq == 0 launches nothing. Calls
+ * that may overlap on the GPU (and captured graphs replayed at the same time) need
+ * a workspace each. Errors: those of cp_scored_attn_validate, INVALID_ARG (null pointers,
  * out_dt), ALIGNMENT, WORKSPACE, CUDA, UNSUPPORTED_DEVICE.
  */
 cp_status cp_scored_attn_fwd(const void* q, const void* k, const void* v, void* out, float* lse, int B, int H, int Hkv,

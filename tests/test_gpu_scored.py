@@ -506,3 +506,22 @@ def test_gradients_of_saturated_scores(low, high, D, slope, dt):
         over = np.abs(x - z) - bd - 2 * U * np.abs(z)
         assert np.all(np.isfinite(x)) and over.max() <= 0, (
             f"{name}: past its bound by {over.max():.3e} of {bd.flat[over.argmax()]:.3e}")
+
+
+def test_a_long_row_of_heavy_weights_and_large_values():
+    """2^21 keys, each of weight 2^12.9 before the division, and v = 2^96, the largest that the header allows: the
+    sum of the products would pass fp32's range with the reference of the first tile. All keys are alike, so out is v
+    but for the roundings of P and of itself, and lse the score plus ln 2^21 (within the module's bound, whose n u is
+    taken for the 2^14 tiles' sums of 2^7 keys each)."""
+    n, D = 1 << 21, 64
+    q = torch.full((1, 1, 1, D), 1.1171875, dtype=BF, device="cuda")
+    k, v = torch.ones((1, n, 1, D), dtype=BF, device="cuda"), torch.full((1, n, 1, D), 2.0 ** 96, dtype=BF, device="cuda")
+    out, lse = torch.empty((1, 1, 1, D), device="cuda"), torch.empty((1, 1, 1), device="cuda")
+    cpa().cp_scored_attn_fwd(q, k, v, out, lse, D ** -0.5)
+    assert cpa().cp_check_device_status() == 0
+    x = 1.1171875 * D * D ** -0.5
+    want = x + n.bit_length() * np.log(2.0) - np.log(2.0)
+    d, sums = (D + 20) * U * x, (2 ** 14 + 2 ** 7) * U
+    assert abs(lse.item() - want) <= 2 * d + 2.0 ** -20 + sums + 4 * U * want
+    off = (out.double() / 2.0 ** 96 - 1).abs().max().item()
+    assert off <= 2.0 ** -8 + 2 * (2 * d + 2.0 ** -21 + sums) + 2 * U, off
