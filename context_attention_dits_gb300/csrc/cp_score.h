@@ -45,6 +45,7 @@ struct ScoreArgs {
   void *dq, *dk, *dv;
   int out_bf16;   // type of out
   int grad_bf16;  // type of dq, dk, dv
+  int sms;        // multiprocessors of the device
   uint32_t* err;  // tensor-core kernels: device error word and the bound on each wait
   uint64_t timeout_ns;
 };
@@ -75,12 +76,12 @@ cudaError_t launch_doc_ranges(const ScoreArgs& a, cudaStream_t s);
 // bf16 on the tensor cores.
 cudaError_t launch_score_fwd_tc(const ScoreArgs& a, int D, cudaStream_t s);
 cudaError_t launch_score_bwd_tc(const ScoreArgs& a, int D, cudaStream_t s);
-// fp32 on the CUDA cores.
+// fp32, its products in three passes of tf32.
 cudaError_t launch_score_fwd_f32(const ScoreArgs& a, int D, cudaStream_t s);
 cudaError_t launch_score_bwd_f32(const ScoreArgs& a, int D, cudaStream_t s);
 
 // The paged cache.
-constexpr int kPagedCtas = 304;     // decode CTAs: two on each of 152 multiprocessors
+constexpr int kPagedCtas = 304;     // decode CTAs at most: two on each of 152 multiprocessors
 constexpr int kPagedBlock = 64;     // keys of one work block
 constexpr int kPagedMaxBatch = 4096;
 struct PagedArgs {
@@ -99,19 +100,27 @@ struct PagedArgs {
   const float* slopes;
   float* partial;  // workspace: [kPagedCtas][2] partial results
   int2* info;      // workspace: [B * Hkv * groups] which partials make up a unit
+  int sms;         // multiprocessors of the device
   uint32_t* err;
 };
 // Query heads that share a key/value head are taken this many at a time.
 constexpr int paged_rows(bool bf16) { return bf16 ? 16 : 8; }
-// CTAs that run at once: two on a multiprocessor where their buffers fit.
+// CTAs that run at once on 152 multiprocessors: two on each where their buffers fit.
 constexpr int paged_ctas(int D, bool bf16) { return D * (bf16 ? 2 : 4) <= 256 ? kPagedCtas : kPagedCtas / 2; }
+// CTAs that share a list of `blocks` blocks: as many as run at once, so that no
+// second wave of equal ranges follows, on a device with fewer multiprocessors too.
+inline int paged_grid(int D, bool bf16, int64_t blocks, int sms) {
+  const int most = paged_ctas(D, bf16), at_once = most / 152 * sms, ctas = at_once < most ? at_once : most;
+  return blocks < 1 ? 1 : blocks < ctas ? static_cast<int>(blocks) : ctas;
+}
 // Decode in one launch: the CTAs (1 to 16, a cluster) that share a unit (a
 // sequence's key/value head and group of query heads), or 0 where the list of all
 // blocks is cut among the CTAs instead. Clusters save the second launch and the
 // workspace, but a unit has 8 or 16 CTAs at most and idle ones take no other's work. So:
-// two blocks a CTA where all units' CTAs run at once, more where they would not,
-// up to 8 (bf16) or 4 (fp32, whose blocks are twice the bytes). Clusters against
-// the list, 24 heads on 8, D = 128, device us: bf16 1 x 1000 keys 5.6 / 8.4,
+// two blocks a CTA where all units' CTAs run at once (on 152 multiprocessors: the
+// workspace's size, which hangs on this, is asked for without a device), more
+// where they would not, up to 8 (bf16) or 4 (fp32, whose blocks are twice the
+// bytes). Clusters against the list, 24 heads on 8, D = 128, device us: bf16 1 x 1000 keys 5.6 / 8.4,
 // 1 x 4096 10.0 / 11.7, 8 x 1000 8.7 / 10.4, 4 x 4096 11.7 / 15.9, 1 x 8000
 // (16 blocks a CTA) 15.9 / 15.1; fp32 1 x 1000 8.2 / 9.9, 1 x 4096 (8) 18.1 / 15.0.
 // Clusters of 16 find room beside each other for some 8 units, and only where two
@@ -149,18 +158,18 @@ cudaError_t allow_smem(int bytes) {
 // of kind a (taken by clusters) and b (by clusters too if b_clusters, else by
 // single CTAs) have up to tiles_a and tiles_b steps, `over` steps of their own
 // for start and join, and a part `fill` of the steps on average; the estimate is
-// the longest item's time or all items' over 152 multiprocessors. Where items
+// the longest item's time or all items' over the multiprocessors. Where items
 // fill a wave of their own a cluster only adds starts and joins (fp32, 104 items
 // of 7 tiles: 22 us alone, 29 in clusters of 2); it pays where a few are long
 // (fp32, 32 query heads on one: backward 2544 us alone, 1288 in clusters of 2).
 inline int cluster_for(double over, int64_t items_a, int64_t tiles_a, int64_t items_b, int64_t tiles_b, double fill,
-                       bool b_clusters) {
+                       bool b_clusters, int sms) {
   int best = 1;
   double least = 0;
   for (int cs = 1; cs <= 8; cs *= 2) {
     const int cb = b_clusters ? cs : 1;
     const double ta = static_cast<double>((tiles_a + cs - 1) / cs), tb = static_cast<double>((tiles_b + cb - 1) / cb);
-    const double all = (items_a * cs * (fill * ta + over) + items_b * cb * (fill * tb + over)) / 152.0;
+    const double all = (items_a * cs * (fill * ta + over) + items_b * cb * (fill * tb + over)) / sms;
     double t = all;
     if (items_a > 0 && ta + over > t) t = ta + over;
     if (items_b > 0 && tb + over > t) t = tb + over;

@@ -91,8 +91,7 @@ cp_status fill_args(ScoreArgs* a, const cp_score_rule& r, const void* q, const v
     a->krange = reinterpret_cast<DocRange*>(ws + w.kr);
   }
   a->timeout_ns = kWaitTimeoutNs;
-  int sms = 0;
-  return static_cast<cp_status>(cp::host_device(&a->err, &sms));
+  return static_cast<cp_status>(cp::host_device(&a->err, &a->sms));
 }
 
 }  // namespace
@@ -234,8 +233,7 @@ cp_status cp_paged_kv_append(const void* k_new, const void* v_new, void* k_cache
   a.v_new = v_new;
   a.k_cache = k_cache;
   a.v_cache = v_cache;
-  int sms = 0;
-  if ((st = static_cast<cp_status>(cp::host_device(&a.err, &sms))) != CP_OK) return st;
+  if ((st = static_cast<cp_status>(cp::host_device(&a.err, &a.sms))) != CP_OK) return st;
   return cp::launch_paged_append(a, dt == CP_BF16 ? 2 : 4, static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? CP_OK
              : CP_ERR_CUDA;
@@ -310,8 +308,7 @@ cp_status cp_paged_attn_decode(const void* q, const void* k_cache, const void* v
     a.partial = static_cast<float*>(workspace);
     a.info = reinterpret_cast<int2*>(static_cast<char*>(workspace) + paged_partial_bytes(a.G, D, dt));
   }
-  int sms = 0;
-  if ((st = static_cast<cp_status>(cp::host_device(&a.err, &sms))) != CP_OK) return st;
+  if ((st = static_cast<cp_status>(cp::host_device(&a.err, &a.sms))) != CP_OK) return st;
   return cp::launch_paged_decode(a, dt == CP_BF16, static_cast<cudaStream_t>(stream)) == cudaSuccess ? CP_OK
                                                                                                        : CP_ERR_CUDA;
 }

@@ -773,8 +773,7 @@ cudaError_t decode_d(const PagedArgs& a, cudaStream_t s) {
   const int groups = (a.G + C::kRows - 1) / C::kRows;
   const int64_t per_unit = ((static_cast<int64_t>(a.max_pages) << a.page_shift) + kPagedBlock - 1) / kPagedBlock;
   const int64_t bound = per_unit * a.Hkv * groups * a.B;
-  const int ctas = static_cast<int>(bound < C::kCtas ? (bound > 0 ? bound : 1) : C::kCtas);
-  paged_decode_kernel<D, T><<<ctas, kDecThreads, C::kSmem, s>>>(a);
+  paged_decode_kernel<D, T><<<paged_grid(D, C::kBf16, bound, a.sms), kDecThreads, C::kSmem, s>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess || per_unit <= 1) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(a.H, a.B);

@@ -699,8 +699,8 @@ cudaError_t fwd_d(const ScoreArgs& a, cudaStream_t s) {
   const int64_t items = static_cast<int64_t>((a.Sq + kR - 1) / kR) * a.H * a.B;
   // steps: tiles taken by every group at once
   const int64_t steps = ((a.Skv + kC - 1) / kC + Cfg<D>::kGroups - 1) / Cfg<D>::kGroups;
-  return launch_clusters(score_fwd_f32_kernel<D>, items, 1, 1, cluster_for(1.5, items, steps, 0, 0, a.causal ? 0.5 : 1.0, true),
-                         Cfg<D>::kThreads, bytes, a.qdoc != nullptr, s, a);
+  const int cs = cluster_for(1.5, items, steps, 0, 0, a.causal ? 0.5 : 1.0, true, a.sms);
+  return launch_clusters(score_fwd_f32_kernel<D>, items, 1, 1, cs, Cfg<D>::kThreads, bytes, a.qdoc != nullptr, s, a);
 }
 
 template <int D>
@@ -719,7 +719,7 @@ cudaError_t bwd_d(const ScoreArgs& a, cudaStream_t s) {
   const int64_t q_items = static_cast<int64_t>((a.Sq + kR - 1) / kR) * a.H * a.B;
   constexpr int G = Cfg<D>::kGroups;
   const int cs = cluster_for(1.5, kv_items, (static_cast<int64_t>((a.Sq + kC - 1) / kC) * a.G + G - 1) / G, q_items,
-                             ((a.Skv + kC - 1) / kC + G - 1) / G, a.causal ? 0.5 : 1.0, true);
+                             ((a.Skv + kC - 1) / kC + G - 1) / G, a.causal ? 0.5 : 1.0, true, a.sms);
   return launch_clusters(score_bwd_f32_kernel<D>, kv_items + q_items, 1, 1, cs, Cfg<D>::kThreads, bytes, a.Sq > 0, s, a);
 }
 

@@ -1090,7 +1090,7 @@ cudaError_t launch_rule(const ScoreArgs& a, const BwdMaps& m, cudaStream_t s) {
   const int64_t q_ctas = static_cast<int64_t>((a.Sq + kT - 1) / kT) * a.H * a.B;
   // sub-steps: a dq CTA's take 3/4 of a dk/dv CTA's; some 8 of them go by before
   // the first and after the last
-  const int cs = cluster_for(8.0, kv_items, ntq * a.G, q_ctas, ntk * 3 / 4, a.causal ? 0.5 : 1.0, false);
+  const int cs = cluster_for(8.0, kv_items, ntq * a.G, q_ctas, ntk * 3 / 4, a.causal ? 0.5 : 1.0, false, a.sms);
   const int64_t ctas = kv_items * cs + (q_ctas + cs - 1) / cs * cs;
   return launch_clusters(score_bwd_tc_kernel<D, kCap, kBias>, ctas / cs, 1, 1, cs, Rows<D>::kThreads, kAlloc, a.Sq > 0, s, m.q64,
                          m.o64, m.k64, m.v64, a, make_cap_coef(a.scale, a.cap, true));

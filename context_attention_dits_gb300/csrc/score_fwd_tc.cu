@@ -888,7 +888,7 @@ cudaError_t launch_rule(const ScoreArgs& a, const CUtensorMap& tq, const CUtenso
   if (e != cudaSuccess) return e;
   const int64_t items = static_cast<int64_t>((a.Sq + 2 * kTileM - 1) / (2 * kTileM)) * a.H * a.B;
   // steps: key tiles; some 8 of them go by before the first and after the last
-  const int cs = cluster_for(8.0, items, (a.Skv + kTileN - 1) / kTileN, 0, 0, a.causal ? 0.5 : 1.0, true);
+  const int cs = cluster_for(8.0, items, (a.Skv + kTileN - 1) / kTileN, 0, 0, a.causal ? 0.5 : 1.0, true, a.sms);
   return launch_clusters(score_fwd_tc_kernel<D, kCap, kBias>, a.H, a.B, (a.Sq + 2 * kTileM - 1) / (2 * kTileM), cs, kThreads, L::kAlloc, a.qdoc != nullptr, s, tq, tk,
                          tv, to, a, make_cap_coef(a.scale, a.cap, false));
 }
