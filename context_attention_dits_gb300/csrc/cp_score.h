@@ -87,6 +87,7 @@ constexpr int kPagedMaxBatch = 4096;
 struct PagedArgs {
   int B, T, H, Hkv, G, D;
   int num_pages, page_shift, max_pages;
+  uint32_t positions;  // append: what the tables hold a place for, 2^31 at most (a 64-bit test took 7% more)
   const int* table;     // [B, max_pages]
   const int* seq_lens;  // [B]
   const int* new_lens;  // append: [B], or nullptr (all T)

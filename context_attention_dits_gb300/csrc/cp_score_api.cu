@@ -226,6 +226,8 @@ cp_status cp_paged_kv_append(const void* k_new, const void* v_new, void* k_cache
   a.D = D;
   a.num_pages = num_pages;
   a.max_pages = max_pages;
+  const int64_t positions = static_cast<int64_t>(max_pages) * page_size;
+  a.positions = static_cast<uint32_t>(positions < (int64_t{1} << 31) ? positions : int64_t{1} << 31);
   a.table = block_table;
   a.seq_lens = seq_lens;
   a.new_lens = new_lens;

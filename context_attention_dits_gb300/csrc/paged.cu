@@ -86,8 +86,8 @@ __global__ void __launch_bounds__(256) paged_append_kernel(const __grid_constant
     x = ks[p];
     y = vs[p];
   }
-  const int64_t pos = static_cast<int64_t>(n) + t;  // (below 2^31 in the lookup, however wide the table)
-  if (n < 0 || pos > INT_MAX || pos >= static_cast<int64_t>(a.max_pages) << a.page_shift) {
+  const uint32_t pos = static_cast<uint32_t>(n) + static_cast<uint32_t>(t);  // (both below 2^31)
+  if (n < 0 || pos >= a.positions) {
     atomicOr(a.err, kDevErrPage);
     return;
   }
