@@ -368,3 +368,18 @@ def test_append_past_the_last_position_an_int_holds():
         want[1, 65535] = x[0, 0]
         want[0, 7:10] = x[1]
         assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("dt", [BF, F4])
+@pytest.mark.parametrize("B,most", [(129, 400), (300, 200), (4096, 70)])
+def test_decode_of_more_sequences_than_one_pass_of_the_work_list(B, most, dt):
+    """The list of blocks is summed 128 sequences at a time: ragged lengths, every fifth sequence empty."""
+    H, Hkv, D, page = 4, 2, 64, 16
+    g = torch.Generator().manual_seed(B)
+    lens = torch.randint(1, most + 1, (B,), generator=g)
+    lens[::5] = 0
+    s = widened(make(lens.tolist(), H, Hkv, D, page, dt, seed=B), 4096)
+    assert cpa().cp_paged_attn_workspace_size(B, H, Hkv, D, dt, page_size=page, max_pages=s["table"].shape[1]) > 0
+    out, lse = decode(s, D ** -0.5, dt, softcap=20.0)
+    check_decode(s, D ** -0.5, out, lse, f"{B} sequences", 20.0)
+    assert cpa().cp_check_device_status() == 0

@@ -525,3 +525,44 @@ def test_a_long_row_of_heavy_weights_and_large_values():
     assert abs(lse.item() - want) <= 2 * d + 2.0 ** -20 + sums + 4 * U * want
     off = (out.double() / 2.0 ** 96 - 1).abs().max().item()
     assert off <= 2.0 ** -8 + 2 * (2 * d + 2.0 ** -21 + sums) + 2 * U, off
+
+
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("n,at", [(300000, 150001), (600000, 393300), (1 << 21, (1 << 20) + 700), (1 << 21, 0),
+                                  (1 << 21, (1 << 21) - 150)])
+def test_documents_and_slopes_among_more_keys_than_one_bitmap_bit_each(n, at, causal):
+    """With slopes the tiles are walked from the rows' position outwards, here with a bit of the bitmap for 2, 4 or 8
+    tiles, from the middle of a group, the first key and the last; bounds as without slopes, with 4 u of the bias."""
+    B, S, H, D, every = 1, 150, 2, 64, 64 * 1024
+    g = torch.Generator(device="cuda").manual_seed(n + at)
+    r = lambda *s: torch.randn(s, generator=g, device="cuda").to(BF)
+    q, k, v = r(B, S, H, D), r(B, n, 1, D), r(B, n, 1, D)
+    slope = torch.tensor([2e-6, -1e-6], device="cuda")
+    pos, rows = torch.arange(n, device="cuda"), torch.arange(S, device="cuda")
+    near = (pos >= at - 700) & (pos < at + 900)   # keys around the rows are of the rows' documents too
+    kd = torch.where((pos % every < 300) | near, (pos // 50) % 3, 10 + pos // 1000).to(torch.int32)[None].contiguous()
+    qd = (rows // 10 % 4).to(torch.int32)[None].contiguous()   # 3: no key at all
+    out, lse = torch.empty_like(q, dtype=F4), torch.empty((B, H, S), device="cuda")
+    cpa().cp_scored_attn_fwd(q, k, v, out, lse, D ** -0.5, slopes=slope, causal=causal, q_pos0=at, q_docs=qd, kv_docs=kd)
+    assert cpa().cp_check_device_status() == 0
+    keys = (kd[0] < 3).nonzero()[:, 0]
+    kf, vf = k[0, keys, 0].double(), v[0, keys, 0].double()
+    back = (at + rows)[:, None] - keys[None]
+    keep = qd[0][:, None] == kd[0, keys][None]
+    if causal:
+        keep &= back >= 0
+    m = len(keys)
+    for h in range(H):
+        x = (q[0, :, h].double() @ kf.T) * D ** -0.5 - slope[h].double() * back.abs().double()
+        big = (q[0, :, h].double().abs() @ kf.abs().T).max().item() * D ** -0.5 + 2e-6 * n
+        x = x.masked_fill(~keep, -float("inf"))
+        wl = torch.logsumexp(x, 1)
+        none = torch.isneginf(wl)
+        assert none.any() and torch.equal(torch.isneginf(lse[0, h]), none) and (out[0, none, h] == 0).all()
+        p = torch.exp(x - torch.where(none, torch.zeros_like(wl), wl)[:, None])
+        d = (D + 20) * U * big
+        e = 2 * (2 * d + 2.0 ** -21 + m * U)
+        over = (out[0, :, h].double() - p @ vf).abs() - (2.0 ** -8 + e) * (p @ vf.abs()) - 2 * U * (p @ vf).abs()
+        assert over.max().item() <= 0
+        ok = ~none
+        assert ((lse[0, h].double() - wl)[ok].abs() <= 2 * d + 2.0 ** -20 + m * U + 4 * U * wl[ok].abs()).all()
