@@ -386,12 +386,17 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap& tq64, const CUtensor
     }
   };
 
+  // No copy, product or wait meets a barrier before this: initialised, the
+  // initialisation fenced for the cluster and for the async proxy (the copies' and
+  // the commits' arrivals), then the CTA's barrier. No peer's shared memory is
+  // touched before the first cluster_sync.
   if (threadIdx.x == 0) {
     for (int i = 0; i < L::kNumBars; ++i) {
       mbar_init(bar(i), i >= kBarPFull && i < kBarDone ? kGroupWarps : 1);
     }
     misc[1] = 0;
     fence_mbar_init();
+    fence_async();
   }
   if (warp == 1) {
     tmem_alloc(smem_addr(misc), kTmemColsB);
@@ -760,11 +765,12 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap& tq64, const CUtensorMa
     NJ = walk_map(a.krange + static_cast<int64_t>(b) * nkb, nkb,
                   doc_span(a.qrange + static_cast<int64_t>(b) * nqb, nqb, bx * 2, 2), 0, ntk, act, misc + 2);
 
-  if (threadIdx.x == 0) {
+  if (threadIdx.x == 0) {  // (in the order that dkdv_cta states)
     for (int i = 0; i < L::kNumBars; ++i)
       mbar_init(bar(i), i == kDqBarQ ? Rows<D>::kWarps : i >= kDqBarPFull && i < kDqBarDone ? kGroupWarps : 1);
     misc[1] = 0;
     fence_mbar_init();
+    fence_async();
   }
   if (warp == 1) {
     tmem_alloc(smem_addr(misc), kTmemColsB);

@@ -170,11 +170,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     return kBias ? min(t.ntile - 1, max(-1, (a.rel + min(t.row0 + 2 * kTileM, a.Sq) - 1) / kTileN)) : -1;
   };
 
+  // No copy, product or wait meets a barrier before this: initialised, the
+  // initialisation fenced for the cluster and for the async proxy (the copies' and
+  // the commits' arrivals), then the CTA's barrier. No peer's shared memory is
+  // touched before the first cluster_sync.
   if (threadIdx.x == 0) {
     for (int i = 0; i < L::kNumBars; ++i)
       mbar_init(bar(i), (i == kBarPFull || i == kBarPFull + 1) ? 4 : (i == kBarItemEmpty || i == kBarItemEmpty + 1) ? 10 : 1);
     misc[1] = 0;
     fence_mbar_init();
+    fence_async();
   }
   if (warp == 1) {
     tmem_alloc(smem_addr(misc), kTmemCols);

@@ -24,3 +24,18 @@ def test_warps_converge_before_aligned_barriers():
                            ("score_attn_f32.cu", "group_sync", "bar.sync")):
         body = functions(name)[fn]
         assert what in body and "__syncwarp();" in body and body.index("__syncwarp();") < body.index(what), (name, fn)
+
+
+def test_barriers_are_set_up_before_anything_meets_them():
+    """From a kernel's first mbar_init to the CTA's barrier: both fences, and no copy, product or wait."""
+    for name, kernels in (("score_fwd_tc.cu", 1), ("score_bwd_tc.cu", 2)):
+        text = open(os.path.join(CSRC, name)).read()
+        starts = [m.start() for m in re.finditer(r"for \(int i = 0; i < L::kNumBars; \+\+i\)", text)]
+        assert len(starts) == kernels
+        for at in starts:
+            part = text[at:text.index("__syncthreads();", at)]
+            assert part.index("mbar_init(") < part.index("fence_mbar_init();") < part.index("fence_async();"), name
+            assert not re.search(r"tma_load|bulk_g2s|expect_tx|mma_|mbar_wait|cluster_peer|next_block", part), name
+            # and none earlier in the same function
+            head = text[text.rindex("\ntemplate <int D", 0, at):at]
+            assert not re.search(r"tma_load\w*\(|bulk_g2s\(|expect_tx\(|mma_\w+\(|mbar_wait\w*\(|cluster_peer\(", head), name
