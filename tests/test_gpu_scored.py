@@ -566,3 +566,55 @@ def test_documents_and_slopes_among_more_keys_than_one_bitmap_bit_each(n, at, ca
         assert over.max().item() <= 0
         ok = ~none
         assert ((lse[0, h].double() - wl)[ok].abs() <= 2 * d + 2.0 ** -20 + m * U + 4 * U * wl[ok].abs()).all()
+
+
+def test_two_streams_at_once():
+    """Forward, backward and decode of two users on two streams at the same time: the bits of each alone."""
+    D, page = 64, 16
+
+    def user(seed, S, H, Hkv):
+        x = [t.cuda() for t in draw(2, S, S, H, Hkv, D, BF, seed=seed)]
+        ids = docs(2, S, 3, 9, seed).cuda()
+        tab = torch.arange(2 * (-(-S // page)), dtype=torch.int32, device="cuda").view(2, -1)
+        kc, vc = (torch.zeros((tab.numel(), page, Hkv, D), dtype=BF, device="cuda") for _ in range(2))
+        zero, full = (torch.full((2,), n, dtype=torch.int32, device="cuda") for n in (0, S))
+        return dict(x=x, rule=dict(causal=True, softcap=10.0, q_docs=ids, kv_docs=ids), tab=tab, cache=(kc, vc), zero=zero,
+                    full=full)
+
+    def step(u):
+        q, k, v, g = u["x"]
+        out, lse = torch.empty_like(q), torch.empty((2, q.shape[2], q.shape[1]), device="cuda")
+        grads = [torch.empty_like(t) for t in (q, k, v)]
+        cpa().cp_scored_attn_fwd(q, k, v, out, lse, 0.1, **u["rule"])
+        cpa().cp_scored_attn_bwd(q, k, v, out, g, lse, *grads, 0.1, **u["rule"])
+        cpa().cp_paged_kv_append(k, v, *u["cache"], u["tab"], u["zero"])
+        o, l = torch.empty_like(q[:, -1].contiguous()), torch.empty((2, q.shape[2]), device="cuda")
+        cpa().cp_paged_attn_decode(q[:, -1].contiguous(), *u["cache"], u["tab"], u["full"], o, l, 0.1, softcap=10.0)
+        return [out, lse, *grads, o, l]
+
+    users = [user(31, 700, 8, 2), user(32, 1500, 4, 4)]
+    want = [step(u) for u in users]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in users]
+    got = []
+    for _ in range(10):
+        for u, s in zip(users, streams):
+            with torch.cuda.stream(s):
+                got.append(step(u))
+    torch.cuda.synchronize()
+    assert cpa().cp_check_device_status() == 0
+    for i, y in enumerate(got):
+        assert all(torch.equal(a, b) for a, b in zip(y, want[i % 2]))
+
+
+@pytest.mark.parametrize("name", ["causal, cap", "documents"])
+def test_gradients_of_more_items_than_multiprocessors_repeat(name):
+    """The backward at D = 128 with more items than run at once, against its bounds, and the same bits again."""
+    B, S, H, Hkv, D = 4, 300, 40, 8, 128
+    rule = MANY[name](B, S)
+    q, k, v, dout = draw(B, S, S, H, Hkv, D, BF, seed=D, qmul=1.5)
+    out, lse = run_fwd(q, k, v, D ** -0.5, rule, BF)
+    grads = run_bwd(q, k, v, out, dout, lse, D ** -0.5, rule, BF)
+    check_bwd(q, k, v, out, dout, lse, D ** -0.5, rule, grads, name)
+    again = run_bwd(q, k, v, out, dout, lse, D ** -0.5, rule, BF)
+    assert all(torch.equal(x, y) for x, y in zip(grads, again))
