@@ -25,12 +25,14 @@
 // keys); the tile is far too small for a 128-row tensor-memory MMA, and the
 // instruction's rate is not what bounds it. fp32: the same in three passes of
 // tf32, 8 query heads.
-// Measured, device time: 2 x 262144 keys, 32 heads on 4, D = 128, bf16 167 us
-// (6.4 TB/s), 48 x 4096 keys, 24 on 8 123 us (6.5), 48 ragged ones of 512 to 8192
-// 88 us (5.8: units end inside the ranges, and a pipeline starts anew with each);
-// fp32 8 x 16384 keys 184 us (5.8); 1 x 1000 keys 5.6 us. More than 16 query heads
-// on one (8 in fp32) read its rows once for each 16: 32 on one 3.0 TB/s of the
-// cache's bytes.
+// Measured, device time: 2 x 262144 keys, 32 heads on 4, D = 128, bf16 170 us
+// (6.3 TB/s), 48 x 4096 keys, 24 on 8 125 us (6.4), 48 ragged ones, log-uniform
+// from 512 to 8192, 90 us for one draw of 131167 keys (6.0; 5.2 to 6.0 by the
+// draw: units end inside the ranges, and a pipeline starts anew with each); fp32
+// 8 x 16384 keys 183 us (5.9); 1 x 1000 keys 5.9 us under a table for 1000, 9.1
+// under one for 65536 tokens (the path goes by the table's width, all that the
+// host knows). More than 16 query heads on one (8 in fp32) read its rows once for
+// each 16: 32 on one 3.0 TB/s of the cache's bytes.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -780,7 +782,9 @@ cudaError_t decode_d(const PagedArgs& a, cudaStream_t s) {
   cfg.blockDim = dim3(D);
   cfg.stream = s;
   cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;  // its launch overlaps the decode kernel's end
+  // prepared while the decode kernel runs, which does not release it early: the
+  // join's CTAs start when the last of decode's have left
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;

@@ -31,9 +31,9 @@
 // in place of 32); a dq sub-step 919, of which 768. Starts and ends are 12000
 // cycles of a dk/dv CTA and 9000 of a dq CTA. With a cap the row pass of D = 64 is
 // as long as the products. Measured, 4608 tokens, 24 heads on 8, D = 128: plain
-// 583 us (1119 TFLOP/s of 10 D flop a pair), causal 315, cap 50 740, causal with it
-// 394, slopes 586, causal with them 319, causal with both 425; documents of 512
-// 118. D = 64: 415, 222, 605, 321, 444, 241, 365.
+// 581 us (1123 TFLOP/s of 10 D flop a pair), causal 316, cap 50 744, causal with it
+// 397, slopes 584, causal with them 320, causal with both 425; documents of 512
+// 97 (24 heads on 24: 117). D = 64: 409, 222, 607, 322, 444, 240, 361.
 // Every wait is bounded; on
 // expiry the CTA records a timeout, lets its copies land, frees its tensor
 // memory and returns.
@@ -135,28 +135,10 @@ enum : int {
   kBarDrain = 20,
 };
 
-__device__ __forceinline__ void drain_wait_b(uint32_t bar, uint32_t parity, uint64_t timeout_ns) {
-  const uint64_t t0 = global_timer_ns();
-  for (uint32_t n = 1; !mbar_try_wait(bar, parity); ++n)
-    if ((n & 255u) == 0 && global_timer_ns() - t0 > timeout_ns) return;
-}
-
-__device__ __forceinline__ float u2f(uint32_t x) { return __uint_as_float(x); }
-
 // TMEM column (within S's or dP's 64) of the bf16 A operand for K step kk of
 // a sub-step: rows [32 h, 32 h + 32) of the sub-step (written by the row warps
 // of column half h) sit in columns [32 h, 32 h + 16), 8 columns per K step
 __device__ __forceinline__ uint32_t pcol(int kk) { return static_cast<uint32_t>((kk >> 1) * 32 + (kk & 1) * 8); }
-
-
-// Holds the uses of loaded registers behind the wait that precedes it.
-template <int N>
-__device__ __forceinline__ void tmem_pin(uint32_t (&r)[N]) {
-#pragma unroll
-  for (int i = 0; i < N; i += 8)
-    asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]),
-                 "+r"(r[i + 6]), "+r"(r[i + 7]));
-}
 
 __device__ __forceinline__ void tmem_ld(uint32_t t, uint32_t (&r)[32]) { tmem_ld32(t, r); }
 __device__ __forceinline__ void tmem_ld(uint32_t t, uint32_t (&r)[16]) { tmem_ld16(t, r); }
@@ -219,7 +201,11 @@ __device__ __forceinline__ void row_pass(const uint32_t (&sr)[N], const uint32_t
           th = mul_x2(s2, cap_poly<kHow>(cc, mul_x2(s2, s2)));
           nd = fma_x2(th, th, minus);
         } else {
-          tanh_exact(cc, s2, th, nd);
+          float h0, h1, n0, n1;
+          tanh_exact(cc, u2f(sr[e]), h0, n0);
+          tanh_exact(cc, u2f(sr[e + 1]), h1, n1);
+          th = pair(h0, h1);
+          nd = pair(n0, n1);
         }
         t2 = fma_x2(th, cap2, b2);
         q2 = mul_x2(fma_x2(dl(e), minus, dp2), nd);
@@ -446,9 +432,9 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap& tq64, const CUtensor
     }
     if (*abort_flag) {
       // let every issued copy land before the CTA's shared memory goes away
-      drain_wait_b(bar(kBarKV), 0, tmo);
+      drain_wait(bar(kBarKV), 0, tmo);
       for (int s = 0; s < kSlots; ++s)
-        if (issued[s]) drain_wait_b(bar(kBarQFull + s), (issued[s] - 1) & 1, tmo);
+        if (issued[s]) drain_wait(bar(kBarQFull + s), (issued[s] - 1) & 1, tmo);
     }
   } else if (warp == 1) {
     // ===================== MMA issuer =====================
@@ -533,7 +519,7 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap& tq64, const CUtensor
       commit(bar(kBarDone));
     } else {
       commit(bar(kBarDrain));
-      drain_wait_b(bar(kBarDrain), 0, tmo);
+      drain_wait(bar(kBarDrain), 0, tmo);
     }
   } else {
     // ===================== row pass: one thread per key row and column half =====================
@@ -818,9 +804,9 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap& tq64, const CUtensorMa
     }
     if (*abort_flag) {
       // let every issued copy land before the CTA's shared memory goes away
-      drain_wait_b(bar(kDqBarLoad), 0, tmo);
+      drain_wait(bar(kDqBarLoad), 0, tmo);
       for (int s = 0; s < kDqSlots; ++s)
-        if (issued[s]) drain_wait_b(bar(kDqBarKVFull + s), (issued[s] - 1) & 1, tmo);
+        if (issued[s]) drain_wait(bar(kDqBarKVFull + s), (issued[s] - 1) & 1, tmo);
     }
   } else if (warp == 1) {
     // ===================== MMA issuer =====================
@@ -891,7 +877,7 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap& tq64, const CUtensorMa
       commit(bar(kDqBarDone));
     } else {
       commit(bar(kDqBarDrain));
-      drain_wait_b(bar(kDqBarDrain), 0, tmo);
+      drain_wait(bar(kDqBarDrain), 0, tmo);
     }
   } else {
     // ===================== dS: one thread per query row and column half =====================

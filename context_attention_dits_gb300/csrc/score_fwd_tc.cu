@@ -37,11 +37,13 @@
 // ends: the first loads and S (5000 cycles after a cold start) and the stores of
 // out, which come from all multiprocessors at once. A CTA therefore goes on to
 // the item of a block that has not started, and the loads and S of its first tile
-// go by under the stores of the last (900 cycles from item to item); longest
-// items first. Measured, 4608 tokens, 24 heads on 8, bf16, D = 128: plain 160 us
-// (1626 TFLOP/s; the plain kernel 165), causal 93.4, cap 50 216, causal with it
-// 130, slopes 170, causal with them 99, causal with both 144; documents of 512 35.
-// D = 64: 124, 77, 196, 118, 150, 87, 144.
+// go by under the stores of the last (900 cycles from item to item); those with
+// the most causal keys first. Measured, 4608 tokens, 24 heads on 8, bf16, D =
+// 128: plain 161 us (1618 TFLOP/s; the plain kernel 165), causal 94, cap 50 217,
+// causal with it 130, slopes 171, causal with them 99, causal with both 145;
+// documents of 512 32 (24 heads on 24: 35). D = 64: 123, 76, 194, 119, 150, 86,
+// 145. The eleven warps leave 168 registers a thread; every form spills 28 to 98
+// bytes.
 // Every wait is bounded (cp_ptx.cuh); on expiry the CTA drains its copies and
 // MMAs, frees TMEM and returns.
 // A few rows against many keys (a chunk of a long prompt) are too few items for
@@ -125,25 +127,6 @@ enum : int {
   kBarNext = 23,      // the next block's index is there
   kBarDrain = 24,
 };
-
-// Bounded wait that ignores the abort flag (used while draining).
-__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, uint64_t timeout_ns) {
-  const uint64_t t0 = global_timer_ns();
-  for (uint32_t n = 1; !mbar_try_wait(bar, parity); ++n) {
-    if ((n & 255u) == 0 && global_timer_ns() - t0 > timeout_ns) return;
-  }
-}
-
-__device__ __forceinline__ float u2f(uint32_t x) { return __uint_as_float(x); }
-
-// Holds the uses of loaded registers behind the wait that precedes it.
-template <int N>
-__device__ __forceinline__ void tmem_pin(uint32_t (&r)[N]) {
-#pragma unroll
-  for (int i = 0; i < N; i += 8)
-    asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]),
-                 "+r"(r[i + 6]), "+r"(r[i + 7]));
-}
 
 template <int D, bool kCap, bool kBias>
 __global__ void __launch_bounds__(kThreads, 1)

@@ -28,6 +28,26 @@ namespace cp {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.69314718055994531f;
 
+// Bounded wait that ignores the abort flag, for a CTA that gives up and lets its
+// copies and products end.
+__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, uint64_t timeout_ns) {
+  const uint64_t t0 = global_timer_ns();
+  for (uint32_t n = 1; !mbar_try_wait(bar, parity); ++n) {
+    if ((n & 255u) == 0 && global_timer_ns() - t0 > timeout_ns) return;
+  }
+}
+
+__device__ __forceinline__ float u2f(uint32_t x) { return __uint_as_float(x); }
+
+// Holds the uses of loaded registers behind the wait that precedes it.
+template <int N>
+__device__ __forceinline__ void tmem_pin(uint32_t (&r)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; i += 8)
+    asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]),
+                 "+r"(r[i + 6]), "+r"(r[i + 7]));
+}
+
 // Pairs of fp32 values in a 64-bit register pair, for the packed instructions
 // (one issue slot a pair). Coefficients are kept as pairs of equal values, so
 // that they are operands as they stand and no register pair is built for them.
@@ -129,16 +149,12 @@ __device__ __forceinline__ float cap_exact(const CapCoef& c, float s) {
   return c.capl2 * (1.f - __fdividef(2.f, 1.f + ex2_approx(s * c.a0)));
 }
 
-// tanh and tanh^2 - 1 of a pair of scores (coefficients with unit set).
-__device__ __forceinline__ void tanh_exact(const CapCoef& c, f32x2 s, f32x2& th, f32x2& neg_d) {
-  float x0, x1;
-  split(mul_x2(s, pair(c.a0, c.a0)), x0, x1);
-  const float e0 = ex2_approx(-fabsf(x0)), e1 = ex2_approx(-fabsf(x1));
-  const f32x2 r = pair(rcp_approx(1.f + e0), rcp_approx(1.f + e1)), er = mul_x2(pair(e0, e1), r);
-  float t0, t1;
-  split(fma_x2(er, pair(-2.f, -2.f), pair(1.f, 1.f)), t0, t1);
-  th = pair(copysignf(t0, x0), copysignf(t1, x1));
-  neg_d = mul_x2(mul_x2(er, r), pair(-4.f, -4.f));
+// tanh and tanh^2 - 1 (coefficients with unit set). One score at a time: in pairs
+// the constants' register pairs cost the polynomials' passes 1.5%.
+__device__ __forceinline__ void tanh_exact(const CapCoef& c, float s, float& th, float& neg_d) {
+  const float x2 = s * c.a0, e = ex2_approx(-fabsf(x2)), r = rcp_approx(1.f + e), er = e * r;
+  th = copysignf(fmaf(-2.f, er, 1.f), x2);
+  neg_d = -4.f * er * r;
 }
 
 // 0 .. 127 in pairs: the columns of a tile, for biases linear in the column.
