@@ -39,9 +39,9 @@
 // the item of a block that has not started, and the loads and S of its first tile
 // go by under the stores of the last (900 cycles from item to item); those with
 // the most causal keys first. Measured, 4608 tokens, 24 heads on 8, bf16, D =
-// 128: plain 161 us (1618 TFLOP/s; the plain kernel 165), causal 94, cap 50 217,
+// 128: plain 161 us (1618 TFLOP/s; the plain kernel 165), causal 94, cap 50 219,
 // causal with it 130, slopes 171, causal with them 99, causal with both 145;
-// documents of 512 32 (24 heads on 24: 35). D = 64: 123, 76, 194, 119, 150, 86,
+// documents of 512 32 (24 heads on 24: 35). D = 64: 123, 76, 194, 121, 149, 87,
 // 145. The eleven warps leave 168 registers a thread; every form spills 28 to 98
 // bytes.
 // Every wait is bounded (cp_ptx.cuh); on expiry the CTA drains its copies and
