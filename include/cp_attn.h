@@ -395,10 +395,10 @@ cp_status cp_attention_bwd(const void* q, const void* k, const void* v, const fl
  * them in the matrix products, and an infinity in fp32 is NaN once it is split
  * for its three products. |v| is at most 2^96 (8e28; sums are formed before they
  * are divided by the weights'), other fp32 inputs at most 2^127. x is held in
- * fp32, so a weight is as far off as fp32's rounding of the row's largest |x|,
- * slopes and distances included. Because positions are global, a ring's blocks
- * are calls with their own q_pos0 and kv_pos0 whose fp32 (out, lse)
- * cp_lse_merge joins.
+ * fp32, and so is lse: a row's weights and gradients are off by some 2^-22 of its
+ * largest |x|, relative, and say nothing where slope times distance nears 2^22.
+ * Because positions are global, a ring's blocks are calls with their own q_pos0
+ * and kv_pos0 whose fp32 (out, lse) cp_lse_merge joins.
  * -------------------------------------------------------------------------*/
 typedef struct {
   float softcap;              /* > 0: cap of the scores, at least 1e-30 and 1e-30 |scale|, at most 1e30; 0: none */
