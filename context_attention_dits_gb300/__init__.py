@@ -22,6 +22,9 @@ from .api import (  # noqa: F401
     cp_paged_attn_decode,
     cp_paged_attn_workspace_size,
     cp_paged_kv_append,
+    cp_qk_norm_rope_bwd,
+    cp_qk_norm_rope_bwd_workspace_size,
+    cp_qk_norm_rope_fwd,
     cp_ring_shard_table,
     cp_scored_attn_bwd,
     cp_scored_attn_bwd_workspace_size,

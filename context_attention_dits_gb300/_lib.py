@@ -34,10 +34,20 @@ class ScoreRule(ctypes.Structure):
                 ("q_pos0", ctypes.c_int64), ("kv_pos0", ctypes.c_int64)]
 
 
+class QkRule(ctypes.Structure):
+    """cp_qk_rule."""
+    _fields_ = [("norm", ctypes.c_int), ("eps", ctypes.c_float), ("q_weight", ctypes.c_void_p),
+                ("k_weight", ctypes.c_void_p), ("weight_dt", ctypes.c_int), ("pairs", ctypes.c_int),
+                ("interleaved", ctypes.c_int), ("freqs", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+                ("positions_shared", ctypes.c_int), ("axes", ctypes.c_int), ("pair_axis", ctypes.c_char_p)]
+
+
 # every symbol include/cp_attn.h declares, with (restype, argtypes)
 _vp, _i, _i64, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
 _ip = ctypes.POINTER(ctypes.c_int)
 _rule = ctypes.POINTER(ScoreRule)
+_qk = ctypes.POINTER(QkRule)
+_i64p = ctypes.POINTER(ctypes.c_int64)
 SIGNATURES = {
     "cp_status_string": (ctypes.c_char_p, [_i]),
     "cp_version": (_i, []),
@@ -75,6 +85,10 @@ SIGNATURES = {
     "cp_paged_attn_workspace_size_for": (_sz, [_i, _i, _i, _i, _i, _i, _i]),
     "cp_paged_attn_decode": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _f, _f, _vp, _vp, _sz,
                                   _i, _i, _vp]),
+    "cp_qk_norm_rope_fwd": (_i, [_vp, _vp, _vp, _vp, _i64p, _i, _i, _i, _i, _i, _qk, _i, _vp]),
+    "cp_qk_norm_rope_bwd_workspace_size": (_sz, [_i]),
+    "cp_qk_norm_rope_bwd": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64p, _i, _i, _i, _i, _i, _qk, _vp, _sz, _i, _i,
+                                 _vp]),
 }
 CP_NO_ALLOC_WORKSPACE_BYTES = 64 * 1024 * 1024
 

@@ -502,6 +502,69 @@ cp_status cp_paged_attn_decode(const void* q, const void* k_cache, const void* v
                                const float* slopes, void* workspace, size_t ws_bytes, cp_dtype dt, cp_dtype out_dt,
                                void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Queries and keys normalised for each head and rotated by their positions, as
+ * diffusion transformers and language models do between a projection and the
+ * attention, in one pass over both; and the gradients. The pages have no
+ * counterpart to these calls.
+ *
+ * For one head x of one token, D values:
+ *   y = x w / sqrt(mean(x^2) + eps)     (norm; w = 1 without weights; no norm: y = x)
+ *   pair p < pairs, (u, v) = (y_2p, y_2p+1) if interleaved, else (y_p, y_(pairs + p)),
+ *   turned by t = positions[b, s, pair_axis[p]] * freqs[p] radians:
+ *   (u, v) -> (u cos t - v sin t, u sin t + v cos t)
+ * and the values behind the 2 pairs first ones stay as they are. The angle is formed
+ * in 64-bit fixed point of a turn: it is as good at position 2^30 as at 1. Sums and
+ * rotation are fp32, results rounded once.
+ * -------------------------------------------------------------------------*/
+typedef struct {
+  int norm;                 /* nonzero: root-mean-square norm of each head */
+  float eps;                /* with norm: 0 .. 1e30 */
+  const void* q_weight;     /* device [D] of weight_dt, or NULL (1); need norm */
+  const void* k_weight;
+  cp_dtype weight_dt;       /* float32, or the rows' type */
+  int pairs;                /* a multiple of 4, 2 pairs <= D; 0: no rotation */
+  int interleaved;
+  const double* freqs;      /* device [pairs], radians a position (below 2^-1022 or not finite: 0) */
+  const int32_t* positions; /* device [B, S, axes], or [S, axes] if positions_shared; any sign */
+  int positions_shared;
+  int axes;                 /* 1 .. 4 */
+  const uint8_t* pair_axis; /* HOST [pairs], each below axes, read during the call; NULL: all 0 */
+} cp_qk_rule;
+
+/*
+ * Forward: q [B, S, H, D], k [B, S, Hkv, D] -> q_out, k_out of the same shapes and
+ * type. Hkv == 0: no keys (k, k_out not read). strides: HOST [4][3] elements from
+ * batch entry to batch entry, token to token and head to head of q, k, q_out, k_out
+ * (a packed projection's parts, [B, H, S, D] layouts), or NULL: all dense. D is dense;
+ * strides of sizes above 1 are multiples of 16 bytes, 0 .. 2^40, and the rows of a
+ * result do not overlap. A result may be its own input (the same address and
+ * strides); anything else must not overlap. B * S below 2^25.
+ * Errors: INVALID_ARG, ALIGNMENT, CUDA, UNSUPPORTED_DEVICE. B or S 0: nothing is launched.
+ */
+cp_status cp_qk_norm_rope_fwd(const void* q, const void* k, void* q_out, void* k_out, const int64_t* strides, int B,
+                              int S, int H, int Hkv, int D, const cp_qk_rule* rule, cp_dtype dt, void* stream);
+
+/* Host-only: bytes of device workspace of the backward where it writes the
+ * gradient of a weight (256-byte aligned start; written before it is read). */
+size_t cp_qk_norm_rope_bwd_workspace_size(int D);
+
+/*
+ * Backward: from q, k (the rows before, not read without norm) and the results'
+ * gradients dq_out, dk_out (grad_dt: float32, or dt) the gradients dq, dk (dt) and
+ * those of the weights, fp32 [D] (dq_weight, dk_weight; either may be NULL, both need
+ * norm; a weight that is NULL counts as 1). All written, not accumulated. strides:
+ * HOST [6][3] of q, k, dq_out, dk_out, dq, dk, or NULL; as above. dq may be dq_out or
+ * q, dk may be dk_out or k (same address, strides and type). No atomics: results
+ * repeat. Calls that may overlap on the GPU (and captured graphs replayed at the same
+ * time) need a workspace each. Errors: as above, and WORKSPACE. With B or S 0 the
+ * weights' gradients are written as 0.
+ */
+cp_status cp_qk_norm_rope_bwd(const void* q, const void* k, const void* dq_out, const void* dk_out, void* dq, void* dk,
+                              float* dq_weight, float* dk_weight, const int64_t* strides, int B, int S, int H, int Hkv,
+                              int D, const cp_qk_rule* rule, void* workspace, size_t ws_bytes, cp_dtype dt,
+                              cp_dtype grad_dt, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
