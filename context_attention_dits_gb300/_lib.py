@@ -6,10 +6,12 @@ implementation of these calls.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import threading
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "lib", "libcpattn.so")
+BIND_PATH = os.path.join(os.path.dirname(LIB_PATH), "_cpbind.so")
 
 # status codes (cp_status)
 CP_OK = 0
@@ -92,8 +94,9 @@ SIGNATURES = {
 }
 CP_NO_ALLOC_WORKSPACE_BYTES = 64 * 1024 * 1024
 
-_lock = threading.Lock()
+_lock = threading.RLock()
 _lib = None
+_bind = None
 
 
 class CpError(RuntimeError):
@@ -118,6 +121,24 @@ def lib() -> ctypes.CDLL:
                     fn.argtypes = args
                 _lib = L
     return _lib
+
+
+def bind():
+    """The compiled marshalling of the calls whose host time counts, over the library that lib() loads."""
+    global _bind
+    if _bind is None:
+        with _lock:
+            if _bind is None:
+                if not os.path.exists(BIND_PATH):
+                    raise RuntimeError(f"_cpbind.so is not built ({BIND_PATH}); run "
+                                       "`python -m context_attention_dits_gb300.build`")
+                import torch  # noqa: F401  (its libraries)
+                spec = importlib.util.spec_from_file_location("_cpbind", BIND_PATH)
+                module = importlib.util.module_from_spec(spec)
+                spec.loader.exec_module(module)
+                module.init(lib()._handle)
+                _bind = module
+    return _bind
 
 
 def status_string(status: int) -> str:

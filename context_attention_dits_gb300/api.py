@@ -541,61 +541,18 @@ def cp_paged_attn_decode(q, k_cache, v_cache, block_table, seq_lens, out, lse, s
 # ---------------------------------------------------------------------------
 # queries and keys between their projections and the attention
 # ---------------------------------------------------------------------------
-def _heads(index, dtype, shape, *ts):
-    """Checks of [B,S,heads,D] tensors whose values of a head are dense; their strides, three each."""
-    got = []
-    for t in ts:
-        if t.get_device() != index:
-            raise ValueError(f"a tensor is on {t.device}, the first one on cuda:{index}: all must live on one device")
-        if t.shape != shape:
-            raise ValueError(f"a tensor has the shape {tuple(t.shape)}, {tuple(shape)} is wanted")
-        if t.dtype != dtype:
-            raise TypeError(f"a tensor is {t.dtype}, {dtype} is wanted")
-        st = t.stride()
-        if st[3] != 1:
-            raise ValueError("the values of a head must be dense")
-        got += st[:3]
-    return got
-
-
-def _qk_rule(index, dtype, B, S, D, positions, freqs, axes, interleaved, eps, q_weight, k_weight):
-    r = _lib.QkRule()
-    if eps is not None:
-        r.norm, r.eps = 1, float(eps)
-    kind = None
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is None:
-            continue
-        if eps is None:
-            raise ValueError("weights need a norm (eps)")
-        if w.shape != (D,) or w.dtype not in (dtype, torch.float32) or w.dtype != (kind or w.dtype):
-            raise ValueError(f"weights must be [D], both float32 or both {dtype}")
-        kind = w.dtype
-        _dense_on(index, w)
-        setattr(r, name, w.data_ptr())
-    r.weight_dt = _DT[kind or dtype]
-    if freqs is None:
-        if positions is not None or axes is not None:
-            raise ValueError("positions and axes need freqs")
-        return ctypes.byref(r)
-    if positions is None:
-        raise ValueError("freqs need positions")
-    if freqs.dtype != torch.float64 or freqs.dim() != 1:
-        raise ValueError("freqs must be float64 [pairs]")
-    if positions.dtype != torch.int32:
-        raise TypeError("positions must be int32")
-    shape = positions.shape
-    if len(shape) not in (2, 3) or shape[-2] != S or (len(shape) == 3 and shape[0] != B):
-        raise ValueError("positions must be [B, S, axes] or [S, axes]")
-    _dense_on(index, freqs, positions)
-    r.pairs, r.axes, r.interleaved = freqs.shape[0], shape[-1], bool(interleaved)
-    r.freqs, r.positions, r.positions_shared = freqs.data_ptr(), positions.data_ptr(), len(shape) == 2
-    if axes is not None:
-        axes = bytes(axes)
-        if len(axes) != r.pairs:
-            raise ValueError("axes must name an axis for each pair")
-        r.pair_axis = axes
-    return ctypes.byref(r)
+# These calls are checked and marshalled by compiled code (csrc/bind.cpp), which takes their arguments by position.
+def _bound(name, args, first, stream):
+    if stream is not None:
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), device=_index(first))
+        if stream.device.index != _index(first):
+            raise ValueError(f"the stream is of {stream.device}, the tensors are on cuda:{_index(first)}")
+        with torch.cuda.stream(stream):
+            return _bound(name, args, first, None)
+    status = getattr(_lib.bind(), name)(*args)
+    if status:
+        raise CpError(status, "cp_" + name)
 
 
 def cp_qk_norm_rope_fwd(q, k, q_out, k_out, positions=None, freqs=None, axes=None, interleaved: bool = False, eps=None,
@@ -610,24 +567,9 @@ def cp_qk_norm_rope_fwd(q, k, q_out, k_out, positions=None, freqs=None, axes=Non
     bytes([0] * 8 + [1] * 28 + [2] * 28). Tensors may be strided (the parts of a packed projection) as long as the
     values of a head are dense and strides are multiples of 16 bytes.
     """
-    index, dtype = _index(q), q.dtype
-    if q.dim() != 4:
-        raise ValueError("q must be [B, S, H, D]")
-    if (k is None) != (k_out is None):
-        raise ValueError("k and k_out come together")
-    B, S, H, D = q.shape
-    sq, sqo = _heads(index, dtype, q.shape, q), _heads(index, dtype, q.shape, q_out)
-    Hkv, kp, kop, sk = 0, None, None, [0] * 6
-    if k is not None:
-        if k.dim() != 4:
-            raise ValueError("k must be [B, S, Hkv, D]")
-        Hkv = k.shape[2]
-        sk = _heads(index, dtype, (B, S, Hkv, D), k, k_out)
-        kp, kop = k.data_ptr(), k_out.data_ptr()
-    rule = _qk_rule(index, dtype, B, S, D, positions, freqs, axes, interleaved, eps, q_weight, k_weight)
-    _call(lib().cp_qk_norm_rope_fwd, (q.data_ptr(), kp, q_out.data_ptr(), kop,
-                                      (ctypes.c_int64 * 12)(*sq, *sk[:3], *sqo, *sk[3:]), B, S, H, Hkv, D, rule, _dt(q)),
-          None, None, (), index, stream)
+    if axes is not None:
+        axes = bytes(axes)
+    _bound("qk_norm_rope_fwd", (q, k, q_out, k_out, positions, freqs, axes, interleaved, eps, q_weight, k_weight), q, stream)
 
 
 def cp_qk_norm_rope_bwd_workspace_size(D) -> int:
@@ -644,36 +586,10 @@ def cp_qk_norm_rope_bwd(q, k, dq_out, dk_out, dq, dk, positions=None, freqs=None
     workspace (only with a weight's gradient): a CUDA tensor of at least cp_qk_norm_rope_bwd_workspace_size(D) bytes,
     one for each call that may run at the same time; allocated here through torch when None.
     """
-    index, dtype = _index(q), q.dtype
-    if q.dim() != 4:
-        raise ValueError("q must be [B, S, H, D]")
-    if (k is None) != (dk_out is None) or (k is None) != (dk is None):
-        raise ValueError("k, dk_out and dk come together")
-    B, S, H, D = q.shape
-    gtype = dq_out.dtype
-    if gtype != dtype and gtype != torch.float32:
-        raise TypeError(f"dq_out and dk_out must be float32 or {dtype}")
-    sq, sg = _heads(index, dtype, q.shape, q, dq), _heads(index, gtype, q.shape, dq_out)
-    Hkv, kp, gp, dkp, sk, sgk = 0, None, None, None, [0] * 6, [0] * 3
-    if k is not None:
-        if k.dim() != 4:
-            raise ValueError("k must be [B, S, Hkv, D]")
-        Hkv = k.shape[2]
-        sk, sgk = _heads(index, dtype, (B, S, Hkv, D), k, dk), _heads(index, gtype, (B, S, Hkv, D), dk_out)
-        kp, gp, dkp = k.data_ptr(), dk_out.data_ptr(), dk.data_ptr()
-    rule = _qk_rule(index, dtype, B, S, D, positions, freqs, axes, interleaved, eps, q_weight, k_weight)
-    ws = [None, None]
-    for i, w in enumerate((dq_weight, dk_weight)):
-        if w is not None:
-            if w.shape != (D,) or w.dtype != torch.float32:
-                raise ValueError("weights' gradients must be float32 [D]")
-            _dense_on(index, w)
-            ws[i] = w.data_ptr()
-    L = lib()
-    need = 0 if ws == [None, None] else L.cp_qk_norm_rope_bwd_workspace_size(D)
-    _call(L.cp_qk_norm_rope_bwd, (q.data_ptr(), kp, dq_out.data_ptr(), gp, dq.data_ptr(), dkp, *ws,
-                                  (ctypes.c_int64 * 18)(*sq[:3], *sk[:3], *sg, *sgk, *sq[3:], *sk[3:]), B, S, H, Hkv, D,
-                                  rule), need, workspace, (_dt(q), _DT[gtype]), index, stream)
+    if axes is not None:
+        axes = bytes(axes)
+    _bound("qk_norm_rope_bwd", (q, k, dq_out, dk_out, dq, dk, positions, freqs, axes, interleaved, eps, q_weight, k_weight,
+                                dq_weight, dk_weight, workspace), q, stream)
 
 
 def cp_check_device_status(stream=None) -> int:

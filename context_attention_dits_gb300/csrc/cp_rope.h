@@ -23,7 +23,7 @@ struct RopeRows {
 struct RopeArgs {
   int S, H, Hkv;    // Hkv = 0: no keys
   int tokens;       // B * S
-  int parts;        // units of a token (a unit is a warp's: a part of the token's heads)
+  int parts, parts_q;  // each token's heads are cut into parts, the first parts_q of q
   RopeRows q, k;    // the rows before
   RopeRows qo, ko;  // forward: the rows after; backward: their gradients
   RopeRows dq, dk;  // backward: the gradients of q and k
@@ -36,16 +36,10 @@ struct RopeArgs {
   const int* pos;  // [B, S, axes], or [S, axes] with pos_sb = 0
   int64_t pos_sb;
   int axes;
-  float* partial;  // backward: [CTAs][2][D], or nullptr
+  float* partial;  // backward: [CTAs][D], or nullptr
   float *dwq, *dwk;
   uint8_t axis[kRopeMaxPairs];  // of each pair
 };
-
-// Row steps of a token: a warp takes 256 / D rows at once, of q or of k.
-inline int rope_steps(int D, int H, int Hkv) {
-  const int rows = 256 / D;
-  return (H + rows - 1) / rows + (Hkv + rows - 1) / rows;
-}
 
 cudaError_t launch_rope_fwd(RopeArgs& a, int D, bool bf16, bool interleaved, int sms, cudaStream_t s);
 // g_f32: the gradients qo, ko are float32 (else of the rows' type).

@@ -120,7 +120,7 @@ cp_status cp_qk_norm_rope_fwd(const void* q, const void* k, void* q_out, void* k
 }
 
 size_t cp_qk_norm_rope_bwd_workspace_size(int D) {
-  return D == 64 || D == 128 ? static_cast<size_t>(cp::kRopeCtas) * 2 * D * sizeof(float) : 0;
+  return D == 64 || D == 128 ? static_cast<size_t>(cp::kRopeCtas) * D * sizeof(float) : 0;
 }
 
 cp_status cp_qk_norm_rope_bwd(const void* q, const void* k, const void* dq_out, const void* dk_out, void* dq, void* dk,

@@ -23,6 +23,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 
 #include "cp_ptx.cuh"
@@ -32,6 +33,8 @@ namespace cp {
 namespace {
 
 constexpr int kThreads = kRopeWarps * 32;
+constexpr int kFwdCtas = 4, kBwdCtas = 2;  // on a multiprocessor
+constexpr int kRopeSteps = 16;             // row steps of a part at most, while tokens are many
 
 // f 2^64 / 2 pi, whole turns dropped; f as m 2^(e - 1075), m its 53 bits. 2^66 / 2 pi
 // rounded to 64 bits is off by 2^-65 of itself. Subnormal and not finite: 0.
@@ -86,6 +89,31 @@ __device__ __forceinline__ uint2 ld8(const void* p) {
   return v;
 }
 
+// Packed pairs of fp32 (half the issue slots, the same roundings).
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+
+// 8 values of a row as the first and the second members of four pairs: neighbours,
+// or the two fours against each other; and back.
+template <bool kNext>
+__device__ __forceinline__ void apart(const float (&x)[8], float2 (&u)[2], float2 (&v)[2]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    u[i] = kNext ? make_float2(x[4 * i], x[4 * i + 2]) : make_float2(x[2 * i], x[2 * i + 1]);
+    v[i] = kNext ? make_float2(x[4 * i + 1], x[4 * i + 3]) : make_float2(x[4 + 2 * i], x[4 + 2 * i + 1]);
+  }
+}
+template <bool kNext>
+__device__ __forceinline__ void together(const float2 (&u)[2], const float2 (&v)[2], float (&x)[8]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    x[kNext ? 4 * i : 2 * i] = u[i].x;
+    x[kNext ? 4 * i + 2 : 2 * i + 1] = u[i].y;
+    x[kNext ? 4 * i + 1 : 4 + 2 * i] = v[i].x;
+    x[kNext ? 4 * i + 3 : 4 + 2 * i + 1] = v[i].y;
+  }
+}
+
 // A lane's 8 values of a row as they lie in memory: 4 from element e0, 4 from e1.
 template <typename T>
 struct Raw;
@@ -101,22 +129,28 @@ struct Raw<__nv_bfloat16> {
       w[0] = x.x, w[1] = x.y, w[2] = y.x, w[3] = y.y;
     }
   }
-  __device__ __forceinline__ void get(float (&x)[8]) const {
+  template <bool kNext>
+  __device__ __forceinline__ void get(float2 (&u)[2], float2 (&v)[2]) const {
+    float x[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       x[2 * i] = __uint_as_float(w[i] << 16);
       x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
+    apart<kNext>(x, u, v);
   }
-  static __device__ __forceinline__ void store(__nv_bfloat16* row, int e0, int e1, bool one, const float (&x)[8]) {
-    uint32_t v[4];
+  template <bool kNext>
+  static __device__ __forceinline__ void store(__nv_bfloat16* row, int e0, int e1, const float2 (&u)[2], const float2 (&v)[2]) {
+    float x[8];
+    together<kNext>(u, v, x);
+    uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
-    if (one) {
-      *reinterpret_cast<uint4*>(row + e0) = make_uint4(v[0], v[1], v[2], v[3]);
+    for (int i = 0; i < 4; ++i) w[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+    if (kNext) {
+      *reinterpret_cast<uint4*>(row + e0) = make_uint4(w[0], w[1], w[2], w[3]);
     } else {
-      *reinterpret_cast<uint2*>(row + e0) = make_uint2(v[0], v[1]);
-      *reinterpret_cast<uint2*>(row + e1) = make_uint2(v[2], v[3]);
+      *reinterpret_cast<uint2*>(row + e0) = make_uint2(w[0], w[1]);
+      *reinterpret_cast<uint2*>(row + e1) = make_uint2(w[2], w[3]);
     }
   }
 };
@@ -128,27 +162,21 @@ struct Raw<float> {
     w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
     w[4] = y.x, w[5] = y.y, w[6] = y.z, w[7] = y.w;
   }
-  __device__ __forceinline__ void get(float (&x)[8]) const {
+  template <bool kNext>
+  __device__ __forceinline__ void get(float2 (&u)[2], float2 (&v)[2]) const {
+    float x[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(w[i]);
+    apart<kNext>(x, u, v);
   }
-  static __device__ __forceinline__ void store(float* row, int e0, int e1, bool, const float (&x)[8]) {
+  template <bool kNext>
+  static __device__ __forceinline__ void store(float* row, int e0, int e1, const float2 (&u)[2], const float2 (&v)[2]) {
+    float x[8];
+    together<kNext>(u, v, x);
     *reinterpret_cast<float4*>(row + e0) = make_float4(x[0], x[1], x[2], x[3]);
     *reinterpret_cast<float4*>(row + e1) = make_float4(x[4], x[5], x[6], x[7]);
   }
 };
-
-// The four pairs of 8 values turned by (c, s): neighbours, or the two fours against each other.
-template <bool kNext>
-__device__ __forceinline__ void rotate(float (&x)[8], const float (&c)[4], const float (&s)[4]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float &u = x[kNext ? 2 * i : i], &v = x[kNext ? 2 * i + 1 : 4 + i];
-    const float y = fmaf(u, c[i], -v * s[i]);
-    v = fmaf(u, s[i], v * c[i]);
-    u = y;
-  }
-}
 
 // What a lane is: its place in its row, its values, its weights and its own pairs' steps.
 template <int D, typename T, bool kNext>
@@ -176,24 +204,29 @@ struct Lane {
     }
   }
   // cos and sin of the lane's four pairs for the token at pos
-  __device__ __forceinline__ void angles(const int* pos, float (&c)[4], float (&s)[4]) const {
-    float oc[kOwn], os[kOwn];
+  __device__ __forceinline__ void angles(const int* pos, float2 (&c)[2], float2 (&s)[2]) const {
+    float oc[kOwn], os[kOwn], ac[4], as[4];
 #pragma unroll
     for (int i = 0; i < kOwn; ++i) cos_sin(step[i], pos[axis[i]], oc[i], os[i]);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int from = i / kOwn * kLanes + l;
-      c[i] = __shfl_sync(0xffffffffu, oc[i % kOwn], from);
-      s[i] = __shfl_sync(0xffffffffu, os[i % kOwn], from);
+      ac[i] = __shfl_sync(0xffffffffu, oc[i % kOwn], from);
+      as[i] = __shfl_sync(0xffffffffu, os[i % kOwn], from);
     }
+    c[0] = make_float2(ac[0], ac[1]), c[1] = make_float2(ac[2], ac[3]);
+    s[0] = make_float2(as[0], as[1]), s[1] = make_float2(as[2], as[3]);
   }
-  __device__ __forceinline__ void weights(const RopeArgs& a, const void* w, float (&x)[8]) const {
+  __device__ __forceinline__ void weights(const RopeArgs& a, const void* w, float2 (&u)[2], float2 (&v)[2]) const {
+    float x[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const int e = j < 4 ? e0 + j : e1 + j - 4;
+      const int e = element(j);
       x[j] = !w ? 1.f : a.w_f32 ? static_cast<const float*>(w)[e] : static_cast<float>(static_cast<const T*>(w)[e]);
     }
+    apart<kNext>(x, u, v);
   }
+  __device__ __forceinline__ int element(int j) const { return j < 4 ? e0 + j : e1 + j - 4; }
   static __device__ __forceinline__ float row_sum(float x) {
 #pragma unroll
     for (int o = kLanes / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
@@ -201,192 +234,248 @@ struct Lane {
   }
 };
 
-// The row steps of one unit: [q0, q1) of q, [k0, k1) of k, of token (b, s).
-struct Unit {
-  int b, s, q0, q1, k0, k1;
-  __device__ __forceinline__ Unit(const RopeArgs& a, int unit, int rows) {
-    const int token = unit / a.parts, part = unit - token * a.parts;
-    const int nq = (a.H + rows - 1) / rows, n = nq + (a.Hkv + rows - 1) / rows;
-    const int first = part * n / a.parts, last = (part + 1) * n / a.parts;
-    b = token / a.S;
-    s = token - b * a.S;
-    q0 = first;
-    q1 = min(last, nq);
-    k0 = max(first - nq, 0);
-    k1 = last - nq;
+// A CTA's part of every token: rows of q or of k, steps [first, last) of them. Its
+// warps take the tokens in turn.
+struct Part {
+  bool k;
+  int first, last, heads, token, stride;
+  __device__ __forceinline__ Part(const RopeArgs& a, int rows) {
+    const int group = blockIdx.x / a.parts, part = blockIdx.x - group * a.parts;
+    k = part >= a.parts_q;
+    heads = k ? a.Hkv : a.H;
+    const int n = (heads + rows - 1) / rows, of = k ? a.parts - a.parts_q : a.parts_q, at = k ? part - a.parts_q : part;
+    first = static_cast<int>(static_cast<int64_t>(at) * n / of);
+    last = static_cast<int>(static_cast<int64_t>(at + 1) * n / of);
+    token = group * kRopeWarps + (threadIdx.x >> 5);
+    stride = gridDim.x / a.parts * kRopeWarps;
   }
 };
 
 template <typename T>
-__device__ __forceinline__ T* row_of(const RopeRows& x, const Unit& u, int head) {
-  return static_cast<T*>(x.p) + u.b * x.sb + u.s * x.ss + head * x.sh;
+__device__ __forceinline__ T* row_of(const RopeRows& x, int b, int s, int head) {
+  return static_cast<T*>(x.p) + b * x.sb + s * x.ss + head * x.sh;
 }
 
 template <int D, typename T, bool kNext>
-__global__ void __launch_bounds__(kThreads) rope_fwd_kernel(const __grid_constant__ RopeArgs a) {
+__global__ void __launch_bounds__(kThreads, kFwdCtas) rope_fwd_kernel(const __grid_constant__ RopeArgs a) {
   using L = Lane<D, T, kNext>;
   constexpr int kAhead = sizeof(T) == 2 ? 4 : 2;  // rows whose loads are under way at once
   const L me(a);
-  float wq[8], wk[8];
-  me.weights(a, a.wq, wq);
-  me.weights(a, a.wk, wk);
-  const int units = a.tokens * a.parts, stride = gridDim.x * kRopeWarps;
-  for (int unit = blockIdx.x * kRopeWarps + (threadIdx.x >> 5); unit < units; unit += stride) {
-    const Unit u(a, unit, L::kRows);
-    float c[4] = {1.f, 1.f, 1.f, 1.f}, s[4] = {0.f, 0.f, 0.f, 0.f};
-    if (a.pairs) me.angles(a.pos + u.b * a.pos_sb + static_cast<int64_t>(u.s) * a.axes, c, s);
-    auto rows = [&](const RopeRows& in, const RopeRows& to, const float (&w)[8], int heads, int first, int last) {
-      for (int at = first; at < last; at += kAhead) {
-        Raw<T> raw[kAhead];
+  const Part part(a, L::kRows);
+  const RopeRows &in = part.k ? a.k : a.q, &to = part.k ? a.ko : a.qo;
+  const int64_t in_step = L::kRows * in.sh, to_step = L::kRows * to.sh;
+  float2 wu[2], wv[2];
+  me.weights(a, part.k ? a.wk : a.wq, wu, wv);
+  for (int token = part.token; token < a.tokens; token += part.stride) {
+    const int b = token / a.S, s = token - b * a.S;
+    const int h0 = part.first * L::kRows + me.r;
+    const T* from = row_of<T>(in, b, s, h0);
+    T* dest = row_of<T>(to, b, s, h0);
+    Raw<T> raw[kAhead];
+    auto load = [&](int at) {
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-          const int h = (at + i) * L::kRows + me.r;
-          if (at + i < last && h < heads)
-            raw[i].load(row_of<T>(in, u, h), me.e0, me.e1, kNext);
-          else
-            raw[i] = {};
-        }
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-          if (at + i >= last) break;
-          const int h = (at + i) * L::kRows + me.r;
-          float x[8];
-          raw[i].get(x);
-          if (a.norm) {
-            float sq = 0.f;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) sq = fmaf(x[j], x[j], sq);
-            const float n = rsqrtf(fmaf(L::row_sum(sq), 1.f / D, a.eps));
-#pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] *= n * w[j];
-          }
-          rotate<kNext>(x, c, s);
-          if (h < heads) Raw<T>::store(row_of<T>(to, u, h), me.e0, me.e1, kNext, x);
-        }
+      for (int i = 0; i < kAhead; ++i) {
+        raw[i] = {};
+        if (at + i < part.last && (at + i) * L::kRows + me.r < part.heads) raw[i].load(from + i * in_step, me.e0, me.e1, kNext);
       }
+      from += kAhead * in_step;
     };
-    rows(a.q, a.qo, wq, a.H, u.q0, u.q1);
-    rows(a.k, a.ko, wk, a.Hkv, u.k0, u.k1);
+    load(part.first);  // on their way while the angles are formed
+    // (u, v) -> n (u au - v bv, u bu + v av): weights and angles as one
+    float2 au[2], av[2], bu[2], bv[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      au[i] = wu[i];
+      av[i] = wv[i];
+      bu[i] = bv[i] = make_float2(0.f, 0.f);
+    }
+    if (a.pairs) {
+      float2 c[2], sn[2];
+      me.angles(a.pos + b * a.pos_sb + static_cast<int64_t>(s) * a.axes, c, sn);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        au[i] = mul2(wu[i], c[i]);
+        av[i] = mul2(wv[i], c[i]);
+        bu[i] = mul2(wu[i], sn[i]);
+        bv[i] = mul2(wv[i], make_float2(-sn[i].x, -sn[i].y));
+      }
+    }
+    for (int at = part.first; at < part.last;) {
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        if (at + i >= part.last) break;
+        float2 u[2], v[2];
+        raw[i].template get<kNext>(u, v);
+        float n = 1.f;
+        if (a.norm) {
+          const float2 sq = fma2(v[1], v[1], fma2(v[0], v[0], fma2(u[1], u[1], mul2(u[0], u[0]))));
+          n = rsqrtf(fmaf(L::row_sum(sq.x + sq.y), 1.f / D, a.eps));
+        }
+        const float2 nn = make_float2(n, n);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float2 y = mul2(fma2(u[j], au[j], mul2(v[j], bv[j])), nn);
+          v[j] = mul2(fma2(v[j], av[j], mul2(u[j], bu[j])), nn);
+          u[j] = y;
+        }
+        if ((at + i) * L::kRows + me.r < part.heads) Raw<T>::template store<kNext>(dest + i * to_step, me.e0, me.e1, u, v);
+      }
+      dest += kAhead * to_step;
+      at += kAhead;
+      if (at < part.last) load(at);
+    }
   }
 }
 
 template <int D, typename T, typename G, bool kNext>
-__global__ void __launch_bounds__(kThreads) rope_bwd_kernel(const __grid_constant__ RopeArgs a) {
+__global__ void __launch_bounds__(kThreads, kBwdCtas) rope_bwd_kernel(const __grid_constant__ RopeArgs a) {
   using L = Lane<D, T, kNext>;
-  constexpr int kAhead = 2;
+  constexpr int kAhead = sizeof(T) + sizeof(G) == 4 ? 4 : 2;
   const L me(a);
-  float wq[8], wk[8], aq[8], ak[8];
-  me.weights(a, a.wq, wq);
-  me.weights(a, a.wk, wk);
+  const Part part(a, L::kRows);
+  const RopeRows &in = part.k ? a.k : a.q, &grad = part.k ? a.ko : a.qo, &to = part.k ? a.dk : a.dq;
+  const int64_t in_step = L::kRows * in.sh, grad_step = L::kRows * grad.sh, to_step = L::kRows * to.sh;
+  float2 wu[2], wv[2], accu[2], accv[2];
+  me.weights(a, part.k ? a.wk : a.wq, wu, wv);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) aq[j] = ak[j] = 0.f;
-  const int units = a.tokens * a.parts, stride = gridDim.x * kRopeWarps;
-  for (int unit = blockIdx.x * kRopeWarps + (threadIdx.x >> 5); unit < units; unit += stride) {
-    const Unit u(a, unit, L::kRows);
-    float c[4] = {1.f, 1.f, 1.f, 1.f}, s[4] = {0.f, 0.f, 0.f, 0.f};
-    if (a.pairs) me.angles(a.pos + u.b * a.pos_sb + static_cast<int64_t>(u.s) * a.axes, c, s);
+  for (int i = 0; i < 2; ++i) accu[i] = accv[i] = make_float2(0.f, 0.f);
+  for (int token = part.token; token < a.tokens; token += part.stride) {
+    const int b = token / a.S, s = token - b * a.S;
+    const int h0 = part.first * L::kRows + me.r;
+    const T* from = row_of<T>(in, b, s, h0);
+    const G* gfrom = row_of<G>(grad, b, s, h0);
+    T* dest = row_of<T>(to, b, s, h0);
+    Raw<T> rx[kAhead];
+    Raw<G> rg[kAhead];
+    auto load = [&](int at) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s[i] = -s[i];  // back
-    auto rows = [&](const RopeRows& in, const RopeRows& grad, const RopeRows& to, const float (&w)[8], float (&acc)[8],
-                    int heads, int first, int last) {
-      for (int at = first; at < last; at += kAhead) {
-        Raw<T> rx[kAhead];
-        Raw<G> rg[kAhead];
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-          const int h = (at + i) * L::kRows + me.r;
-          rx[i] = {};
-          rg[i] = {};
-          if (at + i < last && h < heads) {
-            rg[i].load(row_of<G>(grad, u, h), me.e0, me.e1, kNext);
-            if (a.norm) rx[i].load(row_of<T>(in, u, h), me.e0, me.e1, kNext);
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-          if (at + i >= last) break;
-          const int h = (at + i) * L::kRows + me.r;
-          float x[8], g[8];
-          rg[i].get(g);
-          rotate<kNext>(g, c, s);
-          if (a.norm) {
-            rx[i].get(x);
-            float sq = 0.f, dot = 0.f;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              sq = fmaf(x[j], x[j], sq);
-              dot = fmaf(g[j] * w[j], x[j], dot);
-            }
-            sq = L::row_sum(sq);
-            dot = L::row_sum(dot);
-            const float n = h < heads ? rsqrtf(fmaf(sq, 1.f / D, a.eps)) : 0.f;  // (0 with eps = 0 adds nothing)
-            const float back = dot * n * n * (1.f / D);  // times x: x r mean(g w x r)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              acc[j] = fmaf(g[j], x[j] * n, acc[j]);
-              g[j] = n * fmaf(g[j], w[j], -x[j] * back);
-            }
-          }
-          if (h < heads) Raw<T>::store(row_of<T>(to, u, h), me.e0, me.e1, kNext, g);
+      for (int i = 0; i < kAhead; ++i) {
+        rx[i] = {};
+        rg[i] = {};
+        if (at + i < part.last && (at + i) * L::kRows + me.r < part.heads) {
+          rg[i].load(gfrom + i * grad_step, me.e0, me.e1, kNext);
+          if (a.norm) rx[i].load(from + i * in_step, me.e0, me.e1, kNext);
         }
       }
+      from += kAhead * in_step;
+      gfrom += kAhead * grad_step;
     };
-    rows(a.q, a.qo, a.dq, wq, aq, a.H, u.q0, u.q1);
-    rows(a.k, a.ko, a.dk, wk, ak, a.Hkv, u.k0, u.k1);
+    load(part.first);
+    float2 c[2], sn[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      c[i] = make_float2(1.f, 1.f);
+      sn[i] = make_float2(0.f, 0.f);
+    }
+    if (a.pairs) me.angles(a.pos + b * a.pos_sb + static_cast<int64_t>(s) * a.axes, c, sn);
+    for (int at = part.first; at < part.last;) {
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        if (at + i >= part.last) break;
+        const bool real = (at + i) * L::kRows + me.r < part.heads;
+        float2 u[2], v[2], gu[2], gv[2];
+        rg[i].template get<kNext>(gu, gv);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {  // back
+          const float2 y = fma2(gu[j], c[j], mul2(gv[j], sn[j]));
+          gv[j] = fma2(gv[j], c[j], mul2(gu[j], make_float2(-sn[j].x, -sn[j].y)));
+          gu[j] = y;
+        }
+        if (a.norm) {
+          rx[i].template get<kNext>(u, v);
+          const float2 sq2 = fma2(v[1], v[1], fma2(v[0], v[0], fma2(u[1], u[1], mul2(u[0], u[0]))));
+          float2 dot2 = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) dot2 = fma2(mul2(gv[j], wv[j]), v[j], fma2(mul2(gu[j], wu[j]), u[j], dot2));
+          float sq = sq2.x + sq2.y, dot = dot2.x + dot2.y;
+#pragma unroll
+          for (int o = L::kLanes / 2; o > 0; o >>= 1) {
+            sq += __shfl_xor_sync(0xffffffffu, sq, o);
+            dot += __shfl_xor_sync(0xffffffffu, dot, o);
+          }
+          const float n = real ? rsqrtf(fmaf(sq, 1.f / D, a.eps)) : 0.f;  // (0 with eps = 0 adds nothing)
+          const float back = -dot * n * n * (1.f / D);                    // times x: - x r mean(g w x r)
+          const float2 nn = make_float2(n, n), bb = make_float2(back, back);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            accu[j] = fma2(gu[j], mul2(u[j], nn), accu[j]);
+            accv[j] = fma2(gv[j], mul2(v[j], nn), accv[j]);
+            gu[j] = mul2(nn, fma2(gu[j], wu[j], mul2(u[j], bb)));
+            gv[j] = mul2(nn, fma2(gv[j], wv[j], mul2(v[j], bb)));
+          }
+        }
+        if (real) Raw<T>::template store<kNext>(dest + i * to_step, me.e0, me.e1, gu, gv);
+      }
+      dest += kAhead * to_step;
+      at += kAhead;
+      if (at < part.last) load(at);
+    }
   }
   if (!a.partial) return;
-  // ---- this CTA's part of the weights' gradients, in a fixed order ----
-  __shared__ float sums[kRopeWarps][2][D];
+  // ---- this CTA's part of its weight's gradient, in a fixed order ----
+  __shared__ float sums[kRopeWarps][D];
+  float acc[8];
+  together<kNext>(accu, accv, acc);
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
 #pragma unroll
-    for (int o = L::kLanes; o < 32; o <<= 1) {
-      aq[j] += __shfl_xor_sync(0xffffffffu, aq[j], o);
-      ak[j] += __shfl_xor_sync(0xffffffffu, ak[j], o);
-    }
-    const int e = j < 4 ? me.e0 + j : me.e1 + j - 4;
-    if (me.r == 0) {
-      sums[threadIdx.x >> 5][0][e] = aq[j];
-      sums[threadIdx.x >> 5][1][e] = ak[j];
-    }
+    for (int o = L::kLanes; o < 32; o <<= 1) acc[j] += __shfl_xor_sync(0xffffffffu, acc[j], o);
+    if (me.r == 0) sums[threadIdx.x >> 5][me.element(j)] = acc[j];
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
+  if (threadIdx.x < D) {
     float x = 0.f;
 #pragma unroll
-    for (int w = 0; w < kRopeWarps; ++w) x += sums[w][i / D][i % D];
-    a.partial[static_cast<int64_t>(blockIdx.x) * 2 * D + i] = x;
+    for (int w = 0; w < kRopeWarps; ++w) x += sums[w][threadIdx.x];
+    a.partial[static_cast<int64_t>(blockIdx.x) * D + threadIdx.x] = x;
   }
 }
 
-// Sums the CTAs' parts of the weights' gradients (none: 0): 32 columns a CTA, 32 rows at a time.
-__global__ void __launch_bounds__(1024) rope_weights_kernel(const float* partial, int ctas, int D, float* dwq, float* dwk) {
+// Sums the CTAs' parts of the weights' gradients (none: 0): 32 columns a CTA, 32 parts at a time.
+__global__ void __launch_bounds__(1024) rope_weights_kernel(const float* partial, int groups, int parts, int parts_q, int D,
+                                                            float* dwq, float* dwk) {
   __shared__ float sums[32][33];
-  const int x = threadIdx.x & 31, y = threadIdx.x >> 5, col = blockIdx.x * 32 + x;
+  const int x = threadIdx.x & 31, y = threadIdx.x >> 5, of_k = blockIdx.x * 32 >= D;
+  const int col = blockIdx.x * 32 - of_k * D + x, first = of_k ? parts_q : 0, n = of_k ? parts - parts_q : parts_q;
   grid_wait();
   float sum = 0.f;
 #pragma unroll 4
-  for (int i = y; i < ctas; i += 32) sum += partial[static_cast<int64_t>(i) * 2 * D + col];
+  for (int i = y; i < groups * n; i += 32) {
+    const int group = i / n;
+    sum += partial[static_cast<int64_t>(group * parts + first + i - group * n) * D + col];
+  }
   sums[y][x] = sum;
   __syncthreads();
   sum = sums[x][y];  // a warp per column
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  const int of = blockIdx.x * 32 + y;
-  float* to = of < D ? dwq : dwk;
-  if (x == 0 && to) to[of % D] = sum;
+  float* to = of_k ? dwk : dwq;
+  if (x == 0 && to) to[blockIdx.x * 32 - of_k * D + y] = sum;
 }
 
-// Parts of a token and CTAs of a launch. One unit is a warp's; many parts fill
-// the device when tokens are few, few parts share a token's angles.
+// Parts of a token and CTAs of a launch. Many short parts fill the device when
+// tokens are few; long ones share a token's angles. q's and k's parts should be of
+// the same length, since the CTAs take equal numbers of tokens.
 int plan(RopeArgs& a, int D, int sms, int per_sm) {
-  const int steps = rope_steps(D, a.H, a.Hkv);
-  const int64_t want = static_cast<int64_t>(sms) * per_sm * kRopeWarps * 2;
-  const int64_t parts = (want + a.tokens - 1) / a.tokens;
-  a.parts = static_cast<int>(parts < steps ? parts : steps);
-  const int64_t ctas = (static_cast<int64_t>(a.tokens) * a.parts + kRopeWarps - 1) / kRopeWarps;
-  const int most = sms * per_sm;
-  return static_cast<int>(ctas < most ? ctas : most);
+  const int rows = 256 / D, nq = (a.H + rows - 1) / rows, nk = (a.Hkv + rows - 1) / rows;
+  const int64_t warps = static_cast<int64_t>(sms) * per_sm * kRopeWarps;
+  const int64_t fill = (nq + nk) * static_cast<int64_t>(a.tokens) / warps;  // steps a warp if all are equal
+  const int most = fill < 1 ? 1 : fill < kRopeSteps ? static_cast<int>(fill) : kRopeSteps;
+  double least = 0;
+  for (int per = most; per >= 1 && 2 * per >= most; --per) {
+    int pq = (nq + per - 1) / per, pk = (nk + per - 1) / per;
+    if (pq > kRopeCtas / 4) pq = kRopeCtas / 4;
+    if (pk > kRopeCtas / 4) pk = kRopeCtas / 4;
+    const int longest = std::max((nq + pq - 1) / pq, pk ? (nk + pk - 1) / pk : 0);
+    const double cost = static_cast<double>(pq + pk) * (longest + 1.5);  // an angle costs some 1.5 steps
+    if (per == most || cost < least) {
+      least = cost;
+      a.parts_q = pq;
+      a.parts = pq + pk;
+    }
+  }
+  const int needed = (a.tokens + kRopeWarps - 1) / kRopeWarps, room = std::max(1, std::min(kRopeCtas, sms * per_sm) / a.parts);
+  return std::min(needed, room) * a.parts;
 }
 
 template <typename... P>
@@ -397,16 +486,17 @@ cudaError_t launch(void (*kernel)(P...), const RopeArgs& a, int ctas, cudaStream
 
 template <int D, typename T>
 cudaError_t fwd(RopeArgs& a, bool next, int sms, cudaStream_t s) {
-  const int ctas = plan(a, D, sms, 4);
+  const int ctas = plan(a, D, sms, kFwdCtas);
   return next ? launch(rope_fwd_kernel<D, T, true>, a, ctas, s) : launch(rope_fwd_kernel<D, T, false>, a, ctas, s);
 }
 
 template <int D, typename T, typename G>
 cudaError_t bwd(RopeArgs& a, bool next, int sms, cudaStream_t s) {
   int ctas = 0;
+  a.parts = 1;
   cudaError_t e = cudaSuccess;
   if (a.tokens > 0) {
-    ctas = plan(a, D, sms < 152 ? sms : 152, 2);
+    ctas = plan(a, D, sms, kBwdCtas);
     e = next ? launch(rope_bwd_kernel<D, T, G, true>, a, ctas, s) : launch(rope_bwd_kernel<D, T, G, false>, a, ctas, s);
   }
   if (e != cudaSuccess || !a.partial) return e;
@@ -419,7 +509,8 @@ cudaError_t bwd(RopeArgs& a, bool next, int sms, cudaStream_t s) {
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, rope_weights_kernel, static_cast<const float*>(a.partial), ctas, D, a.dwq, a.dwk);
+  return cudaLaunchKernelEx(&cfg, rope_weights_kernel, static_cast<const float*>(a.partial), ctas / a.parts, a.parts, a.parts_q, D,
+                            a.dwq, a.dwk);
 }
 
 }  // namespace
