@@ -44,11 +44,19 @@ class QkRule(ctypes.Structure):
                 ("positions_shared", ctypes.c_int), ("axes", ctypes.c_int), ("pair_axis", ctypes.c_char_p)]
 
 
+class Q4Cache(ctypes.Structure):
+    """cp_q4_cache."""
+    _fields_ = [("k_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("block_table", ctypes.c_void_p), ("num_pages", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("max_pages", ctypes.c_int)]
+
+
 # every symbol include/cp_attn.h declares, with (restype, argtypes)
 _vp, _i, _i64, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
 _ip = ctypes.POINTER(ctypes.c_int)
 _rule = ctypes.POINTER(ScoreRule)
 _qk = ctypes.POINTER(QkRule)
+_q4 = ctypes.POINTER(Q4Cache)
 _i64p = ctypes.POINTER(ctypes.c_int64)
 SIGNATURES = {
     "cp_status_string": (ctypes.c_char_p, [_i]),
@@ -91,6 +99,10 @@ SIGNATURES = {
     "cp_qk_norm_rope_bwd_workspace_size": (_sz, [_i]),
     "cp_qk_norm_rope_bwd": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64p, _i, _i, _i, _i, _i, _qk, _vp, _sz, _i, _i,
                                  _vp]),
+    "cp_paged_kv_append_q4": (_i, [_vp, _vp, _q4, _vp, _vp, _i, _i, _i, _i, _i, _vp]),
+    "cp_paged_kv_read_q4": (_i, [_q4, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp]),
+    "cp_paged_attn_q4_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i, _i]),
+    "cp_paged_attn_decode_q4": (_i, [_vp, _q4, _vp, _vp, _vp, _i, _i, _i, _i, _f, _f, _vp, _vp, _sz, _i, _i, _vp]),
 }
 CP_NO_ALLOC_WORKSPACE_BYTES = 64 * 1024 * 1024
 

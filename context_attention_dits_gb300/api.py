@@ -592,6 +592,44 @@ def cp_qk_norm_rope_bwd(q, k, dq_out, dk_out, dq, dk, positions=None, freqs=None
                                 dq_weight, dk_weight, workspace), q, stream)
 
 
+# ---------------------------------------------------------------------------
+# the paged cache in 4 bits
+# ---------------------------------------------------------------------------
+def cp_paged_kv_append_q4(k_new, v_new, k_codes, k_scales, v_codes, v_scales, block_table, seq_lens, new_lens=None,
+                          stream=None):
+    """Writes new tokens k_new, v_new [B,T,Hkv,D] into the pages of a cache in 4 bits: codes uint8
+    [num_pages,Hkv,page,D/2], scales bfloat16 [num_pages,Hkv,page,D/64,2] (page at least 16).
+
+    Each 64 values of a row are held as 4-bit codes c with a scale s and an offset z and stand for z + s c (exactly
+    how: cp_attn.h). Otherwise as cp_paged_kv_append.
+    """
+    _bound("paged_kv_append_q4", (k_new, v_new, k_codes, k_scales, v_codes, v_scales, block_table, seq_lens, new_lens),
+           k_new, stream)
+
+
+def cp_paged_kv_read_q4(k_codes, k_scales, v_codes, v_scales, block_table, seq_lens, k_out, v_out, stream=None):
+    """Reads the first T tokens of each sequence of a cache in 4 bits back as values: k_out, v_out [B,T,Hkv,D]
+    (bfloat16 or float32), zero behind a sequence's seq_lens[b] tokens."""
+    _bound("paged_kv_read_q4", (k_codes, k_scales, v_codes, v_scales, block_table, seq_lens, k_out, v_out), k_codes, stream)
+
+
+def cp_paged_attn_q4_workspace_size(B, H, Hkv, D, page_size, max_pages, dtype=torch.bfloat16) -> int:
+    """Workspace bytes of cp_paged_attn_decode_q4 for tables of max_pages pages of page_size rows."""
+    return int(lib().cp_paged_attn_q4_workspace_size(B, H, Hkv, D, page_size, max_pages, _DT[dtype]))
+
+
+def cp_paged_attn_decode_q4(q, k_codes, k_scales, v_codes, v_scales, block_table, seq_lens, out, lse, scale: float,
+                            softcap: float = 0.0, slopes=None, workspace=None, stream=None):
+    """Attention of one new token per sequence, q [B,H,D], over its seq_lens[b] tokens in a paged cache in 4 bits ->
+    out [B,H,D] (float32 or q's dtype), lse [B,H] f32. Otherwise as cp_paged_attn_decode.
+
+    workspace: a CUDA tensor of at least cp_paged_attn_q4_workspace_size(...) bytes, one for each call that may run at
+    the same time; allocated here through torch when None.
+    """
+    _bound("paged_attn_decode_q4", (q, k_codes, k_scales, v_codes, v_scales, block_table, seq_lens, out, lse, scale, softcap,
+                                    slopes, workspace), q, stream)
+
+
 def cp_check_device_status(stream=None) -> int:
     """Synchronizes the stream; returns 0, CP_ERR_TIMEOUT if a kernel's bounded wait expired, or CP_ERR_INVALID_ARG
     if a paged-cache kernel met a page index or a sequence length out of range."""
@@ -619,5 +657,6 @@ __all__ = [
     "cp_scored_attn_validate", "cp_scored_attn_workspace_size", "cp_scored_attn_bwd_workspace_size",
     "cp_scored_attn_fwd", "cp_scored_attn_bwd", "cp_paged_kv_append", "cp_paged_attn_workspace_size",
     "cp_paged_attn_decode", "cp_qk_norm_rope_fwd", "cp_qk_norm_rope_bwd", "cp_qk_norm_rope_bwd_workspace_size",
+    "cp_paged_kv_append_q4", "cp_paged_kv_read_q4", "cp_paged_attn_q4_workspace_size", "cp_paged_attn_decode_q4",
     "cp_status_string", "cp_version",
 ]

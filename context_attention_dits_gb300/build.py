@@ -27,7 +27,7 @@ LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "libcpattn.so")
 BIND = os.path.join(LIBDIR, "_cpbind.so")
 SOURCES = ["attn_tc.cu", "attn_bwd.cu", "attn_bwd_tc.cu", "kernels_simt.cu", "score_fwd_tc.cu", "score_bwd_tc.cu",
-           "score_attn_f32.cu", "paged.cu", "rope.cu", "cp_score_api.cu", "cp_rope_api.cu", "cp_api.cu"]
+           "score_attn_f32.cu", "paged.cu", "paged_q4.cu", "rope.cu", "cp_score_api.cu", "cp_rope_api.cu", "cp_q4_api.cu", "cp_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

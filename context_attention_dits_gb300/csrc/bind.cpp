@@ -77,8 +77,10 @@ struct Workspace {
 
 void* stream_of(int index) { return c10::cuda::getCurrentCUDAStream(index).stream(); }
 
-#define CP_FUNCTIONS(X) \
-  X(cp_qk_norm_rope_fwd) X(cp_qk_norm_rope_bwd) X(cp_qk_norm_rope_bwd_workspace_size)
+#define CP_FUNCTIONS(X)                                                                         \
+  X(cp_qk_norm_rope_fwd) X(cp_qk_norm_rope_bwd) X(cp_qk_norm_rope_bwd_workspace_size)           \
+  X(cp_paged_kv_append_q4) X(cp_paged_kv_read_q4) X(cp_paged_attn_decode_q4)                     \
+  X(cp_paged_attn_q4_workspace_size)
 #define CP_DECLARE(name) decltype(&::name) name##_p = nullptr;
 CP_FUNCTIONS(CP_DECLARE)
 #undef CP_DECLARE
@@ -235,6 +237,115 @@ PyObject* qk_norm_rope_bwd(PyObject* const* a) {
 }
 
 // ---------------------------------------------------------------------------
+// the paged cache in 4 bits
+// ---------------------------------------------------------------------------
+const int32_t* ints(int index, const at::Tensor& t, at::IntArrayRef shape, const char* text) {
+  if (t.scalar_type() != at::kInt) bad_type("block_table, seq_lens and new_lens must be int32");
+  if (!shaped(t, shape)) bad_value(text);
+  dense_on(index, t);
+  return static_cast<const int32_t*>(t.data_ptr());
+}
+
+// a: k_codes, k_scales, v_codes, v_scales, block_table, of B sequences, Hkv heads of D
+cp_q4_cache cache_of(PyObject* const* a, int index, int64_t B, int64_t Hkv, int64_t D) {
+  const at::Tensor *t[4], &table = tensor(a[4]);
+  for (int i = 0; i < 4; ++i) t[i] = &tensor(a[i]);
+  if (t[0]->dim() != 4) bad_value("codes must be [num_pages, Hkv, page, D / 2]");
+  const int64_t pages = t[0]->size(0), page = t[0]->size(2);
+  const int64_t codes[4] = {pages, Hkv, page, D / 2}, scales[5] = {pages, Hkv, page, D / 64, 2};
+  for (int i = 0; i < 4; ++i) {
+    if (t[i]->scalar_type() != (i & 1 ? at::kBFloat16 : at::kByte)) bad_type("codes must be uint8, scales bfloat16");
+    if (!shaped(*t[i], i & 1 ? at::IntArrayRef(scales, 5) : at::IntArrayRef(codes, 4)))
+      bad_value("codes must be [num_pages, Hkv, page, D / 2], scales [num_pages, Hkv, page, D / 64, 2]");
+    dense_on(index, *t[i]);
+  }
+  if (table.dim() != 2) bad_value("block_table must be [B, max_pages]");
+  const int64_t shape[2] = {B, table.size(1)};
+  cp_q4_cache c{};
+  c.k_codes = static_cast<uint8_t*>(t[0]->data_ptr());
+  c.k_scales = t[1]->data_ptr();
+  c.v_codes = static_cast<uint8_t*>(t[2]->data_ptr());
+  c.v_scales = t[3]->data_ptr();
+  c.block_table = ints(index, table, {shape, 2}, "block_table must be [B, max_pages]");
+  // (an empty table has no address, and no entry that is read)
+  if (!c.block_table) c.block_table = reinterpret_cast<const int32_t*>(256);
+  c.num_pages = size_of(pages);
+  c.page_size = size_of(page);
+  c.max_pages = size_of(shape[1]);
+  return c;
+}
+
+// k_new, v_new, the cache's five, seq_lens, new_lens
+PyObject* paged_kv_append_q4(PyObject* const* a) {
+  const at::Tensor &k = tensor(a[0]), &v = tensor(a[1]);
+  const int index = cuda_index(k);
+  if (k.dim() != 4 || !shaped(v, k.sizes())) bad_value("k_new and v_new must be [B, T, Hkv, D]");
+  if (v.scalar_type() != k.scalar_type()) bad_type("k_new and v_new must share a dtype");
+  const cp_dtype dt = type_of(k.scalar_type());
+  dense_on(index, k);
+  dense_on(index, v);
+  const int64_t B = k.size(0);
+  const cp_q4_cache c = cache_of(a + 2, index, B, k.size(2), k.size(3));
+  const int32_t* lens = ints(index, tensor(a[7]), {&B, 1}, "seq_lens must be [B]");
+  const at::Tensor* news = maybe(a[8]);
+  const int32_t* new_lens = news ? ints(index, *news, {&B, 1}, "new_lens must be [B]") : nullptr;
+  const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(index));
+  return PyLong_FromLong(cp_paged_kv_append_q4_p(k.data_ptr(), v.data_ptr(), &c, lens, new_lens, size_of(B),
+                                                 size_of(k.size(1)), size_of(k.size(2)), size_of(k.size(3)), dt,
+                                                 stream_of(index)));
+}
+
+// the cache's five, seq_lens, k_out, v_out
+PyObject* paged_kv_read_q4(PyObject* const* a) {
+  const at::Tensor &k = tensor(a[6]), &v = tensor(a[7]);
+  const int index = cuda_index(tensor(a[0]));
+  if (k.dim() != 4 || !shaped(v, k.sizes())) bad_value("k_out and v_out must be [B, T, Hkv, D]");
+  if (v.scalar_type() != k.scalar_type()) bad_type("k_out and v_out must share a dtype");
+  const cp_dtype dt = type_of(k.scalar_type());
+  dense_on(index, k);
+  dense_on(index, v);
+  const int64_t B = k.size(0);
+  const cp_q4_cache c = cache_of(a, index, B, k.size(2), k.size(3));
+  const int32_t* lens = ints(index, tensor(a[5]), {&B, 1}, "seq_lens must be [B]");
+  const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(index));
+  return PyLong_FromLong(cp_paged_kv_read_q4_p(&c, lens, k.data_ptr(), v.data_ptr(), size_of(B), size_of(k.size(1)),
+                                               size_of(k.size(2)), size_of(k.size(3)), dt, stream_of(index)));
+}
+
+// q, the cache's five, seq_lens, out, lse, scale, softcap, slopes, workspace
+PyObject* paged_attn_decode_q4(PyObject* const* a) {
+  const at::Tensor &q = tensor(a[0]), &out = tensor(a[7]), &lse = tensor(a[8]), &codes = tensor(a[1]);
+  const int index = cuda_index(q);
+  const c10::ScalarType type = q.scalar_type();
+  const cp_dtype dt = type_of(type);
+  if (q.dim() != 3 || codes.dim() != 4) bad_value("q must be [B, H, D], codes [num_pages, Hkv, page, D / 2]");
+  const int64_t B = q.size(0), H = q.size(1), D = q.size(2), Hkv = codes.size(1), lse_shape[2] = {B, H};
+  if (!shaped(out, q.sizes()) || !shaped(lse, {lse_shape, 2})) bad_value("shape mismatch");
+  if (lse.scalar_type() != at::kFloat) bad_type("lse must be float32");
+  if (out.scalar_type() != type && out.scalar_type() != at::kFloat) bad_type("out must be float32 or of q's dtype");
+  dense_on(index, q);
+  dense_on(index, out);
+  dense_on(index, lse);
+  const cp_q4_cache c = cache_of(a + 1, index, B, Hkv, D);
+  const int32_t* lens = ints(index, tensor(a[6]), {&B, 1}, "seq_lens must be [B]");
+  const double scale = PyFloat_AsDouble(a[9]), cap = PyFloat_AsDouble(a[10]);
+  if (PyErr_Occurred()) throw Raised{};
+  const float* slopes = nullptr;
+  if (const at::Tensor* t = maybe(a[11])) {
+    if (t->scalar_type() != at::kFloat || !shaped(*t, {&H, 1})) bad_value("slopes must be float32 [H]");
+    dense_on(index, *t);
+    slopes = static_cast<const float*>(t->data_ptr());
+  }
+  const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(index));
+  const int b = size_of(B), h = size_of(H), hkv = size_of(Hkv), d = size_of(D);
+  const Workspace ws(a[12], cp_paged_attn_q4_workspace_size_p(b, h, hkv, d, c.page_size, c.max_pages, dt), index);
+  return PyLong_FromLong(cp_paged_attn_decode_q4_p(q.data_ptr(), &c, lens, out.data_ptr(),
+                                                   static_cast<float*>(lse.data_ptr()), b, h, hkv, d,
+                                                   static_cast<float>(scale), static_cast<float>(cap), slopes, ws.p, ws.bytes,
+                                                   dt, type_of(out.scalar_type()), stream_of(index)));
+}
+
+// ---------------------------------------------------------------------------
 // the module
 // ---------------------------------------------------------------------------
 template <PyObject* (*kCall)(PyObject* const*), int kArgs>
@@ -276,6 +387,9 @@ PyMethodDef methods[] = {
     {"init", init, METH_O, nullptr},
     method<qk_norm_rope_fwd, 11>("qk_norm_rope_fwd"),
     method<qk_norm_rope_bwd, 16>("qk_norm_rope_bwd"),
+    method<paged_kv_append_q4, 9>("paged_kv_append_q4"),
+    method<paged_kv_read_q4, 8>("paged_kv_read_q4"),
+    method<paged_attn_decode_q4, 13>("paged_attn_decode_q4"),
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_cpbind", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -84,6 +84,7 @@ cudaError_t launch_score_bwd_f32(const ScoreArgs& a, int D, cudaStream_t s);
 constexpr int kPagedCtas = 304;     // decode CTAs at most: two on each of 152 multiprocessors
 constexpr int kPagedBlock = 64;     // keys of one work block
 constexpr int kPagedMaxBatch = 4096;
+constexpr int kPagedMostCtas = 608;  // of any decode kernel: four on each of 152 multiprocessors
 struct PagedArgs {
   int B, T, H, Hkv, G, D;
   int num_pages, page_shift, max_pages;
@@ -92,7 +93,9 @@ struct PagedArgs {
   const int* seq_lens;  // [B]
   const int* new_lens;  // append: [B], or nullptr (all T)
   const void *k_new, *v_new;  // append: [B, T, Hkv, D]
-  void *k_cache, *v_cache;    // [num_pages, page, Hkv, D]
+  void *k_cache, *v_cache;    // [num_pages, page, Hkv, D]; in 4 bits: codes [num_pages, Hkv, page, D / 2]
+  void *k_scales, *v_scales;  // in 4 bits: [num_pages, Hkv, page, D / 64, 2], scale and offset
+  void *k_out, *v_out;        // read: [B, T, Hkv, D]
   const void* q;  // decode: [B, H, D]
   void* out;
   float* lse;  // [B, H]
@@ -103,6 +106,7 @@ struct PagedArgs {
   int2* info;      // workspace: [B * Hkv * groups] which partials make up a unit
   int sms;         // multiprocessors of the device
   uint32_t* err;
+  uint64_t timeout_ns;  // in 4 bits: bound on each wait
 };
 // Query heads that share a key/value head are taken this many at a time.
 constexpr int paged_rows(bool bf16) { return bf16 ? 16 : 8; }
@@ -140,6 +144,29 @@ inline int paged_cluster(int D, bool bf16, int B, int Hkv, int G, int max_pages,
 }
 cudaError_t launch_paged_append(const PagedArgs& a, int elem_bytes, cudaStream_t s);
 cudaError_t launch_paged_decode(const PagedArgs& a, bool bf16, cudaStream_t s);
+
+// The cache in 4 bits.
+constexpr int kQ4Group = 64;   // values that share a scale and an offset
+constexpr int kQ4Block = 128;  // keys of one work block
+constexpr int kQ4MinPage = 16;
+// Query heads of a unit: as many columns of the matrix instruction, or twice.
+constexpr int q4_rows(bool bf16, int G) { return bf16 && G > 8 ? 16 : 8; }
+constexpr int q4_per_sm(bool bf16, int rows) { return bf16 && rows == 8 ? 4 : 2; }
+inline int q4_ctas(bool bf16, int rows, int sms) { return q4_per_sm(bf16, rows) * (sms < 152 ? sms : 152); }
+// CTAs of a cluster that share a unit, or 0 for the list, as paged_cluster.
+inline int q4_cluster(bool bf16, int B, int Hkv, int G, int max_pages, int page_shift) {
+  const int rows = q4_rows(bf16, G);
+  const int64_t blocks = ((static_cast<int64_t>(max_pages) << page_shift) + kQ4Block - 1) / kQ4Block;
+  const int64_t units = static_cast<int64_t>(B) * Hkv * ((G + rows - 1) / rows);
+  const int ctas = q4_per_sm(bf16, rows) * 152;
+  const int most = units <= 8 ? kPagedCluster : kPagedCluster / 2;
+  int cs = 1;
+  while (cs < most && blocks > cs && units * cs * 2 <= ctas) cs *= 2;
+  return units <= ctas && blocks <= cs * 4 ? cs : 0;
+}
+cudaError_t launch_q4_append(const PagedArgs& a, bool bf16, cudaStream_t s);
+cudaError_t launch_q4_read(const PagedArgs& a, bool bf16, cudaStream_t s);
+cudaError_t launch_q4_decode(const PagedArgs& a, bool bf16, cudaStream_t s);
 
 // Lets a kernel use `bytes` of dynamic shared memory, once per device (the call
 // costs as much host time as a launch).

@@ -565,6 +565,69 @@ cp_status cp_qk_norm_rope_bwd(const void* q, const void* k, const void* dq_out, 
                               int D, const cp_qk_rule* rule, void* workspace, size_t ws_bytes, cp_dtype dt,
                               cp_dtype grad_dt, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * The paged cache in 4 bits: some 3.5 times as many tokens in the same bytes, and
+ * as many times fewer to read for a token. The pages have no counterpart to these
+ * calls.
+ *
+ * A row (one token, one head, D values) is cut into groups of 64. A group is held as
+ * 64 codes c of 4 bits, a scale s and an offset z, both bf16, and stands for z + s c:
+ *   z = the largest bf16 number not above the group's values,
+ *   s = the smallest bf16 number not below (largest value - z) / 15 and 2^-100,
+ *   c = min(15, floor((x - z) / s + 1/2)),
+ * each exactly, whatever the rows' type. A group that holds an infinity or a NaN, or
+ * spans more than the largest fp32 number, reads back as NaN (s = z = NaN).
+ *   codes  [num_pages, Hkv, page_size, D / 2] bytes: value 2 i of a row is the lower
+ *          half of its byte i, value 2 i + 1 the upper;
+ *   scales [num_pages, Hkv, page_size, D / 64, 2] bf16: s, z.
+ * (A page holds a head's rows one after another, unlike the cache above, so that
+ * they are read in pieces of 2 KB.) page_size a power of two, 16 to 65536;
+ * num_pages * page_size < 2^31; at most 4096 sequences a call. block_table, lengths
+ * and errors on the device as above: what a bad page index or length names is
+ * reported by cp_check_device_status (CP_ERR_INVALID_ARG) and left out.
+ * -------------------------------------------------------------------------*/
+typedef struct {
+  uint8_t* k_codes; /* device, 16-byte aligned, as the three below */
+  void* k_scales;
+  uint8_t* v_codes;
+  void* v_scales;
+  const int32_t* block_table; /* device [B, max_pages] */
+  int num_pages, page_size, max_pages;
+} cp_q4_cache;
+
+/*
+ * Writes new tokens' rows: as cp_paged_kv_append, k_new, v_new [B, T, Hkv, D] (dt,
+ * dense). Every other row keeps its bytes. Errors: INVALID_ARG, ALIGNMENT, CUDA,
+ * UNSUPPORTED_DEVICE.
+ */
+cp_status cp_paged_kv_append_q4(const void* k_new, const void* v_new, const cp_q4_cache* cache, const int32_t* seq_lens,
+                                const int32_t* new_lens, int B, int T, int Hkv, int D, cp_dtype dt, void* stream);
+
+/*
+ * Reads rows back: k_out, v_out [B, T, Hkv, D] (out_dt, dense) get the values
+ * z + s c (fp32, rounded once) of the first min(T, seq_lens[b]) tokens, and zeros
+ * behind them and for a page out of range: what a prompt's next chunk takes to
+ * cp_scored_attn_fwd. Errors: as above.
+ */
+cp_status cp_paged_kv_read_q4(const cp_q4_cache* cache, const int32_t* seq_lens, void* k_out, void* v_out, int B, int T,
+                              int Hkv, int D, cp_dtype out_dt, void* stream);
+
+/* Host-only: bytes of device workspace (256-byte aligned start; every byte used is
+ * written before it is read) of the call below for tables of max_pages pages of
+ * page_size rows: 0 where it takes one launch and needs none. */
+size_t cp_paged_attn_q4_workspace_size(int B, int H, int Hkv, int D, int page_size, int max_pages, cp_dtype dt);
+
+/*
+ * Attention of one new token per sequence: as cp_paged_attn_decode. Scores are formed
+ * from the codes exactly; the weights, times the values' scales, are rounded to fp16
+ * (fp32 q: to 22 bits) and summed in fp32. q, and k and v as they were appended, are
+ * finite and at most 2^96. Errors: INVALID_ARG, NOT_DIVISIBLE (H % Hkv), ALIGNMENT,
+ * WORKSPACE, CUDA, UNSUPPORTED_DEVICE.
+ */
+cp_status cp_paged_attn_decode_q4(const void* q, const cp_q4_cache* cache, const int32_t* seq_lens, void* out, float* lse,
+                                  int B, int H, int Hkv, int D, float scale, float softcap, const float* slopes,
+                                  void* workspace, size_t ws_bytes, cp_dtype dt, cp_dtype out_dt, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
