@@ -26,6 +26,7 @@
 
 #include "cp_ptx.cuh"
 #include "cp_score.h"
+#include "packed.cuh"
 #include "paged_decode.cuh"
 
 namespace cp {
@@ -118,32 +119,6 @@ __device__ __forceinline__ uint32_t quantise(const float (&x)[8], uint32_t& scal
     }
   }
   return codes;
-}
-
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&x)[8]) {
-  if constexpr (sizeof(T) == 2) {
-    const uint4 v = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-  } else {
-    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-  }
-}
-template <typename T>
-__device__ __forceinline__ void store8(T* p, const float (&x)[8]) {
-  if constexpr (sizeof(T) == 2) {
-    *reinterpret_cast<uint4*>(p) =
-        make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
-  } else {
-    reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
-  }
 }
 
 // Rows (token, head) of sequence blockIdx.y: a warp takes 256 / D of them.
@@ -268,8 +243,24 @@ __device__ __forceinline__ uint32_t centred(uint32_t w) {
   return x;
 }
 
-// bf16 queries: one fp16 part of q and of the weights. fp32 ones: two of each, whose
-// products leave 2^-22 out.
+// cap tanh(y) for y = x / cap within 1: the polynomial of score_math.cuh (relative
+// error 5.0e-8), as a factor of y.
+__device__ __forceinline__ float2 tanh_poly(float2 u) {
+  constexpr float c[7] = {0.9999999502f,  -0.3333283915f,  0.1332520408f, -0.05345702957f,
+                          0.02028998042f, -0.006203379104f, 0.001041022634f};
+  float2 p = twice(c[6]);
+#pragma unroll
+  for (int i = 5; i >= 0; --i) p = fma2(p, u, twice(c[i]));
+  return p;
+}
+
+// bf16 queries: one fp16 part of q and of the weights, and codes as they lie: the
+// bits of c, in fp16, are the (subnormal) number c 2^-24, those of 16 c another 16
+// times as large, so that a word of 8 codes takes five instructions. With them v's
+// products come to sum p s c; what the centre takes off, 8 sum p s of the same
+// rounded weights, is the product with a row of ones. fp32 queries: two parts of each,
+// whose products leave 2^-22 out, and codes as c - 8 from the start, since a sum of
+// numbers above zero would lose more to the instruction's truncation.
 template <int D_, bool kF32, int kTiles>
 struct Q4Unit {
   static constexpr int kD = D_, kRows = 8 * kTiles, kBlock = kQ4Block, kPerSm = q4_per_sm(!kF32, kRows);
@@ -278,11 +269,10 @@ struct Q4Unit {
   static constexpr int kCodes = kChunk * kRowB, kScales = kChunk * kScaleB, kStage = 2 * (kCodes + kScales);
   static constexpr int kStages = 2;
   static constexpr int kState = kRows * (D_ + 2);
-  static constexpr int kWarpB = (kStages * kStage > 2 * kState * 4 ? kStages * kStage : 2 * kState * 4) + 127 & ~127;
+  static constexpr int kWarpB = ((kStages * kStage > 2 * kState * 4 ? kStages * kStage : 2 * kState * 4) + 127) & ~127;
   static constexpr int kSmem = kDecWarps * kWarpB;
   struct Shared {
     uint64_t full[kDecWarps][kStages];
-    uint32_t have[kDecWarps][kStages];  // the keys that a stage holds, a bit each
     uint32_t abort;
   };
 
@@ -306,55 +296,68 @@ struct Q4Unit {
     const int h0 = hk * a.G + hg * kRows, nrow = min(kRows, a.G - hg * kRows);
     // this warp's chunks: keys (4 blk + warp) 32 on, the last below n
     const int last = min(blk1, n > warp * kChunk ? (n - warp * kChunk + kQ4Block - 1) / kQ4Block : 0);
-    const int pieces = a.page_shift >= 5 ? 4 : 8;  // codes and scales of k and v, twice where pages are of 16 rows
-    const int rows = a.page_shift >= 5 ? 32 : 16;
 
-    // ---- loads: a lane a piece ----
+    // ---- loads: a lane a piece (codes and scales of k and v, each twice where pages are of 16 rows) ----
+    const int pieces = a.page_shift >= 5 ? 4 : 8, rows = a.page_shift >= 5 ? 32 : 16;
     const int which = lane & 3, half = lane >> 2;  // k codes, k scales, v codes, v scales
+    const int row_b = which & 1 ? kScaleB : kRowB;
+    const uint32_t piece_b = rows * row_b;
+    const int64_t head_b = static_cast<int64_t>(row_b) << a.page_shift, page_b = head_b * a.Hkv;
     const uint8_t* base = static_cast<const uint8_t*>(which == 0   ? a.k_cache
                                                       : which == 1 ? a.k_scales
                                                       : which == 2 ? a.v_cache
-                                                                   : a.v_scales);
-    const int row_b = which & 1 ? kScaleB : kRowB;
-    const uint32_t off = (which & 2 ? kCodes + kScales : 0) + (which & 1 ? kCodes : 0) + half * rows * row_b;
-    auto find = [&](int blk) {
-      const int pos = (blk * kDecWarps + warp) * kChunk + half * 16;
-      const int page = lane < pieces && blk < last && pos < n ? page_of(a, b, pos) : -1;
-      __syncwarp();
-      return page;
-    };
-    auto load = [&](int blk, int page) {
-      const int pos = (blk * kDecWarps + warp) * kChunk + half * 16;
-      const uint32_t found = __ballot_sync(0xffffffffu, page >= 0);
-      if (lane == 0) {
-        uint32_t on = (found & 1u ? 0xffffu : 0u) | (found & (pieces == 8 ? 16u : 1u) ? 0xffff0000u : 0u);
-        const int rest = n - pos;  // keys from here on
-        if (rest < 32) on &= (1u << rest) - 1;
-        sh.have[warp][ask] = on;
+                                                                   : a.v_scales) +
+                          hk * head_b;
+    const uint32_t dst = smem_addr(wbuf) + (which & 2 ? kCodes + kScales : 0) + (which & 1 ? kCodes : 0) + half * piece_b;
+    const uint32_t bars = smem_addr(&sh.full[warp][0]);
+    const int* table = a.table + static_cast<int64_t>(b) * a.max_pages;
+    const int page_mask = (1 << a.page_shift) - 1;
+    int pos = (blk0 * kDecWarps + warp) * kChunk + half * 16;  // of the chunk that `page` is of
+    int asked = blk0, page = -1;
+    auto find = [&]() {
+      page = -1;
+      if (lane < pieces && asked < last && pos < n) {
+        page = table[pos >> a.page_shift];
+        if (page < 0 || page >= a.num_pages) {
+          atomicOr(a.err, kDevErrPage);
+          page = -1;
+        }
       }
+      __syncwarp();
+    };
+    // asks for the chunk, looks the next one's page up; which of its keys there are, a bit each
+    auto load = [&]() {
+      const uint32_t found = __ballot_sync(0xffffffffu, page >= 0);
+      uint32_t on = found & 1u ? 0xffffffffu : 0u;
+      if (pieces == 8) on = (on & 0xffffu) | (found & 16u ? 0xffff0000u : 0u);
+      const int rest = n - (asked * kDecWarps + warp) * kChunk;
+      if (rest < kChunk) on &= (1u << rest) - 1;
       if (lane < pieces) {
-        const uint32_t bar = smem_addr(&sh.full[warp][ask]), bytes = rows * row_b;
-        mbar_arrive_expect_tx(bar, page >= 0 ? bytes : 0);
-        if (page >= 0)
-          bulk_g2s(smem_addr(wbuf) + ask * kStage + off, base + head_row(a, page, pos, hk) * row_b, bytes, bar);
+        const uint32_t bar = bars + ask * 8;
+        mbar_arrive_expect_tx(bar, page >= 0 ? piece_b : 0);
+        if (page >= 0) bulk_g2s(dst + ask * kStage, base + page * page_b + (pos & page_mask) * row_b, piece_b, bar);
       }
       if (++ask == kStages) ask = 0;
-      __syncwarp();
+      ++asked;
+      pos += kQ4Block;
+      find();
+      return on;
     };
     fence_async();  // (what was read and written here before, by this and by other warps ahead of the barrier)
-    int next = find(blk0), asked = blk0;
+    find();
+    uint32_t coming[kStages - 1] = {};  // the keys of the chunks under way
     if (!aborted(sh)) {
 #pragma unroll
-      for (int st = 0; st < kStages - 1; ++st) {
-        if (asked < last) load(asked++, next);
-        next = find(asked);
-      }
+      for (int st = 0; st < kStages - 1; ++st)
+        if (asked < last) coming[st] = load();
     }
 
     // ---- q: each head's column in fp16, scaled by a power of two so that its largest
     // value lies in [2^14, 2^15); what is below 2^-39 of that is lost ----
+    // Scores leave the products as x / cap, or in units of log2 where there is no cap.
+    const float unit_x = a.cap > 0.f ? a.scale / a.cap : a.scale * kL2e, cap2 = a.cap * kL2e;
     uint32_t qf[kTiles][kGroups][4][kParts][2];  // per step of 16 values
-    float undo[kTiles][2], qsum[kTiles][kGroups][2], slope[kTiles][2];
+    float2 undo[kTiles], qsum[kTiles][kGroups], slope[kTiles];  // of this lane's columns, heads 2 tq and 2 tq + 1
 #pragma unroll
     for (int x = 0; x < kTiles; ++x) {
       const int h = x * 8 + g;
@@ -387,233 +390,289 @@ struct Q4Unit {
         for (int st = 0; st < 4; ++st)
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            // codes i and i + 4 of a word of 8; those of odd i come times 16
+            // codes i and i + 4 of a word of 8; as they lie, those of odd i come times 16
             const int i = (st >> 1) * 8 + (st & 1) * 2 + r;
-            const float up = power_of_2(r ? 10 - e : 14 - e), lo = v[y][i] * up, hi = v[y][i + 4] * up;
+            const float up = power_of_2(r && !kF32 ? 10 - e : 14 - e), lo = v[y][i] * up, hi = v[y][i + 4] * up;
             qf[x][y][st][0][r] = pack_f16x2(lo, hi);
             if constexpr (kF32) {
               const float2 have = unpack_f16x2(qf[x][y][st][0][r]);
               qf[x][y][st][1][r] = pack_f16x2(lo - have.x, hi - have.y);
             }
           }
+      auto column = [&](float z) {  // of heads 2 tq and 2 tq + 1, from the lanes that hold heads g
+        return make_float2(__shfl_sync(0xffffffffu, z, 8 * tq), __shfl_sync(0xffffffffu, z, 8 * tq + 4));
+      };
+      undo[x] = column(power_of_2(kF32 ? e - 14 : e + 10) * unit_x);  // of 2^(14 - e), and 2^-24 of the codes as they lie
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {  // the columns of this lane's scores: heads 2 tq, 2 tq + 1
-        const int from = (2 * tq + c) * 4, hc = x * 8 + 2 * tq + c;
-        undo[x][c] = power_of_2(__shfl_sync(0xffffffffu, e, from) + 10);  // of 2^(14 - e), and 2^-24 of the codes
-#pragma unroll
-        for (int y = 0; y < kGroups; ++y) qsum[x][y][c] = __shfl_sync(0xffffffffu, sum[y], from);
-        slope[x][c] = a.slopes && hc < nrow ? a.slopes[h0 + hc] * kL2e : 0.f;
-      }
+      for (int y = 0; y < kGroups; ++y) qsum[x][y] = column(sum[y] * unit_x);
+      const int hc = x * 8 + 2 * tq;
+      slope[x] = make_float2(a.slopes && hc < nrow ? a.slopes[h0 + hc] * kL2e : 0.f,
+                             a.slopes && hc + 1 < nrow ? a.slopes[h0 + hc + 1] * kL2e : 0.f);
     }
 
-    DecScore score;
-    score.scale = a.scale;
-    score.cap = a.cap;
-    score.inv_cap = a.cap > 0.f ? 1.f / a.cap : 0.f;
-    float m[kTiles][2], l[kTiles][2], zs[kTiles][kGroups][2], o[kTiles][kGroups][4][4];
+    float2 m[kTiles], l[kTiles], zs[kTiles][kGroups], o[kTiles][kGroups][4][2];
 #pragma unroll
-    for (int x = 0; x < kTiles; ++x)
+    for (int x = 0; x < kTiles; ++x) {
+      m[x] = twice(-INFINITY);
+      l[x] = twice(0.f);
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        m[x][c] = -INFINITY;
-        l[x][c] = 0.f;
+      for (int y = 0; y < kGroups; ++y) {
+        zs[x][y] = twice(0.f);
 #pragma unroll
-        for (int y = 0; y < kGroups; ++y) {
-          zs[x][y][c] = 0.f;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) o[x][y][j][2 * c] = o[x][y][j][2 * c + 1] = 0.f;
-        }
+        for (int j = 0; j < 4; ++j) o[x][y][j][0] = o[x][y][j][1] = twice(0.f);
       }
-    int top = 27;  // exponent (biased) of the largest value scale so far: o is in units of 2^(top - 141)
+    }
+    // exponent (biased) of the largest value scale so far, and what brings it below 2^15: o is in units of 2^(top - 141)
+    int top = 27;
+    float fit = power_of_2(141 - 27);
     // Row r of a 16-key tile is key turn(r): neighbours change places in every other
     // pair, so that the lanes of a quarter that read v's rows differ in parity
     auto turn = [](int r) { return r ^ (r >> 1 & 1); };
     const int kr = turn(g), va = turn(2 * tq), vb = turn(2 * tq + 1);
+    const uint8_t* krow = wbuf + kr * kRowB + tq * 8;
+    const uint8_t* zrow = wbuf + kCodes + kr * kScaleB;
+    const uint8_t *vrow_a = wbuf + kCodes + kScales + va * kRowB + g * 4, *vrow_b = wbuf + kCodes + kScales + vb * kRowB + g * 4;
+    auto scales = [](const uint8_t* p, uint32_t (&w)[kGroups]) {
+      if constexpr (kGroups == 2) {
+        const uint2 v = *reinterpret_cast<const uint2*>(p);
+        w[0] = v.x, w[1] = v.y;
+      } else {
+        w[0] = *reinterpret_cast<const uint32_t*>(p);
+      }
+    };
 
     for (int blk = blk0; blk < last; ++blk) {
-      if (!__all_sync(0xffffffffu, mbar_wait_bounded(smem_addr(&sh.full[warp][take]), phase >> take & 1u, &sh.abort, a.err,
-                                                     a.timeout_ns)))
+      if (!__all_sync(0xffffffffu, mbar_wait_bounded(bars + take * 8, phase >> take & 1u, &sh.abort, a.err, a.timeout_ns)))
         break;
-      if (asked < last) load(asked++, next);  // into the stage that the last step read
-      next = find(asked);
-      const uint8_t* kt = wbuf + take * kStage;
-      const uint8_t *kz = kt + kCodes, *vt = kz + kScales, *vz = vt + kCodes;
-      const uint32_t on = sh.have[warp][take];
+      const uint32_t on = coming[0];
+#pragma unroll
+      for (int st = 1; st < kStages - 1; ++st) coming[st - 1] = coming[st];
+      if (asked < last) coming[kStages - 2] = load();  // into the stage that the last step read
+      const int stage = take * kStage;
 
-      // ---- scores, keys as rows: two tiles of 16 ----
-      float s[2][kTiles][4];
+      // ---- scores, keys as rows: two tiles of 16; [tile][row] over the lane's two heads ----
+      float2 s[2][kTiles][2];
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         float dot[kTiles][kGroups][4];
 #pragma unroll
         for (int y = 0; y < kGroups; ++y) {
-          const uint2 wa = *reinterpret_cast<const uint2*>(kt + (16 * t + kr) * kRowB + y * 32 + tq * 8);
-          const uint2 wb = *reinterpret_cast<const uint2*>(kt + (16 * t + kr + 8) * kRowB + y * 32 + tq * 8);
+          const uint2 wa = *reinterpret_cast<const uint2*>(krow + stage + 16 * t * kRowB + y * 32);
+          const uint2 wb = *reinterpret_cast<const uint2*>(krow + stage + (16 * t + 8) * kRowB + y * 32);
+          float low[kTiles][4];
 #pragma unroll
           for (int x = 0; x < kTiles; ++x)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) dot[x][y][e] = 0.f;
+            for (int e = 0; e < 4; ++e) dot[x][y][e] = low[x][e] = 0.f;
 #pragma unroll
           for (int st = 0; st < 4; ++st) {
             const uint32_t ua = (st >> 1 ? wa.y : wa.x) >> (st & 1 ? 8 : 0), ub = (st >> 1 ? wb.y : wb.x) >> (st & 1 ? 8 : 0);
-            // codes as they are: subnormal fp16 numbers, c 2^-24, and 16 c 2^-24
-            const uint32_t a0 = ua & 0x000f000fu, a1 = ub & 0x000f000fu, a2 = ua & 0x00f000f0u, a3 = ub & 0x00f000f0u;
+            const uint32_t a0 = kF32 ? centred<false>(ua) : ua & 0x000f000fu, a1 = kF32 ? centred<false>(ub) : ub & 0x000f000fu;
+            const uint32_t a2 = kF32 ? centred<true>(ua) : ua & 0x00f000f0u, a3 = kF32 ? centred<true>(ub) : ub & 0x00f000f0u;
+#pragma unroll
+            for (int x = 0; x < kTiles; ++x) {
+              if constexpr (kF32) mma_f16(low[x], a0, a1, a2, a3, qf[x][y][st][1][0], qf[x][y][st][1][1]);
+              mma_f16(dot[x][y], a0, a1, a2, a3, qf[x][y][st][0][0], qf[x][y][st][0][1]);
+            }
+          }
+          if constexpr (kF32)
 #pragma unroll
             for (int x = 0; x < kTiles; ++x)
 #pragma unroll
-              for (int p = kParts - 1; p >= 0; --p)
-                mma_f16(dot[x][y], a0, a1, a2, a3, qf[x][y][st][p][0], qf[x][y][st][p][1]);
-          }
+              for (int e = 0; e < 4; ++e) dot[x][y][e] += low[x][e];
         }
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const int key = 16 * t + kr + 8 * r;
-          const bool there = on >> key & 1u;
-          const float dist = static_cast<float>(n - 1 - ((blk * kDecWarps + warp) * kChunk + key));
-          float ks[kGroups], kzz[kGroups];
+          uint32_t w[kGroups];
+          scales(zrow + stage + (16 * t + 8 * r) * kScaleB, w);
 #pragma unroll
-          for (int y = 0; y < kGroups; ++y) {
-            const uint32_t w = *reinterpret_cast<const uint32_t*>(kz + key * kScaleB + y * 4);
-            ks[y] = __uint_as_float(w << 16);
-            kzz[y] = __uint_as_float(w & 0xffff0000u);
-          }
+          for (int x = 0; x < kTiles; ++x) {
+            float2 d = twice(0.f), zq = twice(0.f);
 #pragma unroll
-          for (int x = 0; x < kTiles; ++x)
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              float d = ks[0] * dot[x][0][2 * r + c], zq = kzz[0] * qsum[x][0][c];
-#pragma unroll
-              for (int y = 1; y < kGroups; ++y) {
-                d = fmaf(ks[y], dot[x][y][2 * r + c], d);
-                zq = fmaf(kzz[y], qsum[x][y][c], zq);
-              }
-              s[t][x][2 * r + c] = there ? score(fmaf(d, undo[x][c], zq), slope[x][c], dist) : -INFINITY;
+            for (int y = 0; y < kGroups; ++y) {
+              const float ks = __uint_as_float(w[y] << 16), kz = __uint_as_float(w[y] & 0xffff0000u);
+              const float2 one = make_float2(dot[x][y][2 * r], dot[x][y][2 * r + 1]);
+              d = y ? fma2(twice(ks), one, d) : mul2(twice(ks), one);
+              const float2 zc = twice(kF32 ? fmaf(8.f, ks, kz) : kz);
+              zq = y ? fma2(zc, qsum[x][y], zq) : mul2(zc, qsum[x][y]);
             }
+            s[t][x][r] = fma2(d, undo[x], zq);
+          }
         }
       }
+      const bool part = on != 0xffffffffu;
+      auto there = [&](int t, int r) { return !part || (on >> (kr + 16 * t + 8 * r) & 1u); };
+      if (a.cap > 0.f) {
+        float far = 0.f;
+        if (part)  // a row that holds no key has no say: results do not depend on what lies there
+#pragma unroll
+          for (int i = 0; i < 4 * kTiles; ++i)
+            if (!there(i & 1, i >> 1 & 1)) s[i & 1][i >> 2][i >> 1 & 1] = twice(0.f);
+#pragma unroll
+        for (int i = 0; i < 4 * kTiles; ++i) {
+          const float2 y = s[i & 1][i >> 2][i >> 1 & 1];
+          far = fmax3(far, fabsf(y.x), fabsf(y.y));
+        }
+        if (__all_sync(0xffffffffu, far <= 1.f)) {
+#pragma unroll
+          for (int i = 0; i < 4 * kTiles; ++i) {
+            float2& y = s[i & 1][i >> 2][i >> 1 & 1];
+            y = mul2(mul2(y, twice(cap2)), tanh_poly(mul2(y, y)));
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4 * kTiles; ++i) {
+            float2& y = s[i & 1][i >> 2][i >> 1 & 1];
+            y = make_float2(cap2 * tanhf(y.x), cap2 * tanhf(y.y));
+          }
+        }
+      }
+      if (a.slopes) {
+        const float dist = static_cast<float>(n - 1 - (blk * kDecWarps + warp) * kChunk - kr);
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int x = 0; x < kTiles; ++x) s[t][x][r] = fma2(twice(16 * t + 8 * r - dist), slope[x], s[t][x][r]);
+      }
+      if (part)
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int x = 0; x < kTiles; ++x)
+              if (!there(t, r)) s[t][x][r] = twice(-INFINITY);
 
       // ---- weights ----
-      float f[kTiles][2];
+      float2 f[kTiles];
 #pragma unroll
-      for (int x = 0; x < kTiles; ++x)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          float mx = fmaxf(fmaxf(s[0][x][c], s[0][x][2 + c]), fmaxf(s[1][x][c], s[1][x][2 + c]));
+      for (int x = 0; x < kTiles; ++x) {
+        auto weigh = [&](float& mm, float& ll, float& ff, float& p0, float& p1, float& p2, float& p3) {
+          float mx = fmax3(fmaxf(p0, p1), p2, p3);
 #pragma unroll
           for (int of = 4; of < 32; of <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, of));
-          const float mn = fmaxf(m[x][c], mx), ref = mn == -INFINITY ? 0.f : mn;
-          f[x][c] = kF32 ? exp2f(m[x][c] - ref) : ex2_approx(m[x][c] - ref);
-          m[x][c] = mn;
-          float sum = 0.f;
-#pragma unroll
-          for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              float& p = s[t][x][2 * r + c];
-              p = kF32 ? exp2f(p - ref) : ex2_approx(p - ref);
-              sum += p;
-            }
-          l[x][c] = fmaf(l[x][c], f[x][c], sum);
-        }
+          const float mn = fmaxf(mm, mx), ref = mn == -INFINITY ? 0.f : mn;
+          auto ex2 = [](float z) { return kF32 ? exp2f(z) : ex2_approx(z); };
+          ff = ex2(mm - ref);
+          mm = mn;
+          p0 = ex2(p0 - ref);
+          p1 = ex2(p1 - ref);
+          p2 = ex2(p2 - ref);
+          p3 = ex2(p3 - ref);
+          ll = fmaf(ll, ff, (p0 + p1) + (p2 + p3));
+        };
+        weigh(m[x].x, l[x].x, f[x].x, s[0][x][0].x, s[0][x][1].x, s[1][x][0].x, s[1][x][1].x);
+        weigh(m[x].y, l[x].y, f[x].y, s[0][x][0].y, s[0][x][1].y, s[1][x][0].y, s[1][x][1].y);
+      }
 
       // ---- the values' scales meet the weights: p s in fp16, scaled so that it stays
       // below 2^15; p (z + 8 s) summed as it is ----
-      float vs[2][2][kGroups];  // [tile][row]
-      uint32_t largest = 0;
+      float vs[2][2][kGroups], largest = 0.f;  // [tile][row]
 #pragma unroll
       for (int x = 0; x < kTiles; ++x)
 #pragma unroll
-        for (int y = 0; y < kGroups; ++y)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) zs[x][y][c] *= f[x][c];
+        for (int y = 0; y < kGroups; ++y) zs[x][y] = mul2(zs[x][y], f[x]);
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const int key = 16 * t + kr + 8 * r;
-          const bool there = on >> key & 1u;
+          uint32_t w[kGroups];
+          scales(zrow + stage + kCodes + kScales + (16 * t + 8 * r) * kScaleB, w);
+          if (!there(t, r))  // (and may hold anything)
+#pragma unroll
+            for (int y = 0; y < kGroups; ++y) w[y] = 0;
 #pragma unroll
           for (int y = 0; y < kGroups; ++y) {
-            uint32_t w = *reinterpret_cast<const uint32_t*>(vz + key * kScaleB + y * 4);
-            w = there ? w : 0u;  // (a row that holds no key may hold anything)
-            const float sv = __uint_as_float(w << 16), zz = fmaf(8.f, sv, __uint_as_float(w & 0xffff0000u));
+            const float sv = __uint_as_float(w[y] << 16), zz = fmaf(8.f, sv, __uint_as_float(w[y] & 0xffff0000u));
             vs[t][r][y] = sv;
-            largest = max(largest, w & 0x7fffu);
+            largest = fmaxf(largest, fabsf(sv));
 #pragma unroll
-            for (int x = 0; x < kTiles; ++x)
-#pragma unroll
-              for (int c = 0; c < 2; ++c) zs[x][y][c] = fmaf(s[t][x][2 * r + c], zz, zs[x][y][c]);
+            for (int x = 0; x < kTiles; ++x) zs[x][y] = fma2(s[t][x][r], twice(zz), zs[x][y]);
           }
         }
-      const int now = max(top, static_cast<int>(__reduce_max_sync(0xffffffffu, largest) >> 7));
-      if (now != top) {
-        const float down = now - top > 126 ? 0.f : power_of_2(top - now);
+      if (__any_sync(0xffffffffu, largest * fit >= 32768.f)) {  // seldom: a larger scale than any before
+        const int now = max(top, static_cast<int>(__reduce_max_sync(0xffffffffu, __float_as_uint(largest)) >> 23));
+        const float2 down = twice(now - top > 126 ? 0.f : power_of_2(top - now));
 #pragma unroll
-        for (int x = 0; x < kTiles; ++x)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) f[x][c] *= down;
+        for (int x = 0; x < kTiles; ++x) f[x] = mul2(f[x], down);
         top = now;
+        fit = power_of_2(141 - top);
       }
-      const float fit = power_of_2(141 - top);
-      uint32_t pf[kTiles][kGroups][2][kParts][2];
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int r = 0; r < 2; ++r)
-#pragma unroll
-          for (int y = 0; y < kGroups; ++y) {
-            const float sv = vs[t][r][y] * fit;
-#pragma unroll
-            for (int x = 0; x < kTiles; ++x) {
-              const float u = s[t][x][2 * r] * sv, v = s[t][x][2 * r + 1] * sv;
-              const uint32_t w = pack_f16x2(u, v);
-              pf[x][y][t][0][r] = transpose8(w);
-              if constexpr (kF32) {
-                const float2 have = unpack_f16x2(w);
-                pf[x][y][t][1][r] = transpose8(pack_f16x2(u - have.x, v - have.y));
-              }
-            }
-          }
 
       // ---- O^T += V^T P^T, summed over the chunk apart (the instruction's own sums
       // truncate, which would add up along a long sequence) ----
 #pragma unroll
       for (int y = 0; y < kGroups; ++y) {
-        float add[kTiles][4][4];
+        uint32_t pf[kTiles][2][kParts][2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const float sv = vs[t][r][y] * fit;
+#pragma unroll
+            for (int x = 0; x < kTiles; ++x) {
+              const float2 ps = mul2(s[t][x][r], twice(sv));
+              const uint32_t w = pack_f16x2(ps.x, ps.y);
+              pf[x][t][0][r] = transpose8(w);
+              if constexpr (kF32) {
+                const float2 have = unpack_f16x2(w);
+                pf[x][t][1][r] = transpose8(pack_f16x2(ps.x - have.x, ps.y - have.y));
+              }
+            }
+          }
+        float add[kTiles][4][4], ones[kTiles][4];
 #pragma unroll
         for (int x = 0; x < kTiles; ++x)
 #pragma unroll
           for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) add[x][j][e] = 0.f;
+            for (int e = 0; e < 4; ++e) add[x][j][e] = ones[x][e] = 0.f;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          auto word = [&](int r) {
-            return *reinterpret_cast<const uint32_t*>(vt + (16 * t + r) * kRowB + y * 32 + g * 4);
-          };
-          const uint32_t w0 = word(va), w1 = word(vb), w2 = word(va + 8), w3 = word(vb + 8);
+          const int at = stage + 16 * t * kRowB + y * 32;
+          const uint32_t w0 = *reinterpret_cast<const uint32_t*>(vrow_a + at);
+          const uint32_t w1 = *reinterpret_cast<const uint32_t*>(vrow_b + at);
+          const uint32_t w2 = *reinterpret_cast<const uint32_t*>(vrow_a + at + 8 * kRowB);
+          const uint32_t w3 = *reinterpret_cast<const uint32_t*>(vrow_b + at + 8 * kRowB);
           // two keys' codes side by side: 0 .. 3 of the word, and 4 .. 7
           uint32_t a01 = __byte_perm(w0, w1, 0x5410), b01 = __byte_perm(w0, w1, 0x7632);
           uint32_t a23 = __byte_perm(w2, w3, 0x5410), b23 = __byte_perm(w2, w3, 0x7632);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             if (j == 2) a01 >>= 8, b01 >>= 8, a23 >>= 8, b23 >>= 8;
-            const uint32_t a0 = j & 1 ? centred<true>(a01) : centred<false>(a01);
-            const uint32_t a1 = j & 1 ? centred<true>(b01) : centred<false>(b01);
-            const uint32_t a2 = j & 1 ? centred<true>(a23) : centred<false>(a23);
-            const uint32_t a3 = j & 1 ? centred<true>(b23) : centred<false>(b23);
+            auto codes = [&](uint32_t w) {
+              if constexpr (!kF32) return w & (j & 1 ? 0x00f000f0u : 0x000f000fu);
+              return j & 1 ? centred<true>(w) : centred<false>(w);
+            };
+            const uint32_t a0 = codes(a01), a1 = codes(b01), a2 = codes(a23), a3 = codes(b23);
 #pragma unroll
             for (int x = 0; x < kTiles; ++x)
 #pragma unroll
-              for (int p = kParts - 1; p >= 0; --p) mma_f16(add[x][j], a0, a1, a2, a3, pf[x][y][t][p][0], pf[x][y][t][p][1]);
+              for (int p = kParts - 1; p >= 0; --p) mma_f16(add[x][j], a0, a1, a2, a3, pf[x][t][p][0], pf[x][t][p][1]);
           }
+          if constexpr (!kF32)
+#pragma unroll
+            for (int x = 0; x < kTiles; ++x)
+              mma_f16(ones[x], 0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u, pf[x][t][0][0], pf[x][t][0][1]);
         }
 #pragma unroll
-        for (int x = 0; x < kTiles; ++x)
+        for (int x = 0; x < kTiles; ++x) {
+          // (codes 2^-24 of themselves: so is o, until the end)
+          const float2 off = mul2(make_float2(ones[x][0], ones[x][1]), twice(-0x1p-21f));
 #pragma unroll
           for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[x][y][j][e] = fmaf(o[x][y][j][e], f[x][e & 1], add[x][j][e]);
+            for (int e = 0; e < 2; ++e) {
+              const float2 more = make_float2(add[x][j][2 * e], add[x][j][2 * e + 1]);
+              float2& to = o[x][y][j][e];
+              if constexpr (kF32)
+                to = fma2(to, f[x], more);
+              else
+                to = fma2(more, twice(j & 1 ? 0.0625f : 1.f), fma2(to, f[x], off));
+            }
+        }
       }
       phase ^= 1u << take;
       if (++take == kStages) take = 0;
@@ -621,7 +680,7 @@ struct Q4Unit {
     }
     if (aborted(sh)) {  // copies under way land before the buffers change hands; nothing is asked for any more
       while (take != ask) {
-        mbar_drain(smem_addr(&sh.full[warp][take]), phase >> take & 1u, a.timeout_ns);
+        mbar_drain(bars + take * 8, phase >> take & 1u, a.timeout_ns);
         phase ^= 1u << take;
         if (++take == kStages) take = 0;
       }
@@ -630,29 +689,41 @@ struct Q4Unit {
 
     // ---- this warp's state into its buffers ----
     float* w = reinterpret_cast<float*>(wbuf);
-    const float unit = power_of_2(top - 141);
+    const float unit = power_of_2(top - 141), codes = kF32 ? 1.f : 0x1p24f;
 #pragma unroll
-    for (int x = 0; x < kTiles; ++x)
+    for (int x = 0; x < kTiles; ++x) {
+      auto keep = [&](int r, float mm, float ll, const float (&zz)[kGroups], auto column) {
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int r = x * 8 + 2 * tq + c;
-#pragma unroll
-        for (int of = 4; of < 32; of <<= 1) l[x][c] += __shfl_xor_sync(0xffffffffu, l[x][c], of);
+        for (int of = 4; of < 32; of <<= 1) ll += __shfl_xor_sync(0xffffffffu, ll, of);
 #pragma unroll
         for (int y = 0; y < kGroups; ++y) {
+          float z = zz[y];
 #pragma unroll
-          for (int of = 4; of < 32; of <<= 1) zs[x][y][c] += __shfl_xor_sync(0xffffffffu, zs[x][y][c], of);
+          for (int of = 4; of < 32; of <<= 1) z += __shfl_xor_sync(0xffffffffu, z, of);
+          float out[8];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            w[r * kD + y * kQ4Group + g * 8 + j] = fmaf(o[x][y][j][c], unit, zs[x][y][c]);
-            w[r * kD + y * kQ4Group + g * 8 + j + 4] = fmaf(o[x][y][j][2 + c], unit, zs[x][y][c]);
+            out[j] = fmaf(column(o[x][y][j][0]) * codes, unit, z);
+            out[j + 4] = fmaf(column(o[x][y][j][1]) * codes, unit, z);
           }
+#pragma unroll
+          for (int j = 0; j < 8; j += 2)
+            *reinterpret_cast<float2*>(w + r * kD + y * kQ4Group + g * 8 + j) = make_float2(out[j], out[j + 1]);
         }
         if (g == 0) {
-          w[kRows * kD + 2 * r] = m[x][c];
-          w[kRows * kD + 2 * r + 1] = l[x][c];
+          w[kRows * kD + 2 * r] = mm;
+          w[kRows * kD + 2 * r + 1] = ll;
         }
+      };
+      float zx[kGroups], zy[kGroups];
+#pragma unroll
+      for (int y = 0; y < kGroups; ++y) {
+        zx[y] = zs[x][y].x;
+        zy[y] = zs[x][y].y;
       }
+      keep(x * 8 + 2 * tq, m[x].x, l[x].x, zx, [](float2 v) { return v.x; });
+      keep(x * 8 + 2 * tq + 1, m[x].y, l[x].y, zy, [](float2 v) { return v.y; });
+    }
     fence_async();
   }
 

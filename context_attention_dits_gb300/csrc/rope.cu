@@ -28,6 +28,7 @@
 
 #include "cp_ptx.cuh"
 #include "cp_rope.h"
+#include "packed.cuh"
 
 namespace cp {
 namespace {
@@ -88,10 +89,6 @@ __device__ __forceinline__ uint2 ld8(const void* p) {
   asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p) : "memory");
   return v;
 }
-
-// Packed pairs of fp32 (half the issue slots, the same roundings).
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
 
 // 8 values of a row as the first and the second members of four pairs: neighbours,
 // or the two fours against each other; and back.

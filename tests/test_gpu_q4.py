@@ -7,10 +7,11 @@ A = scale max over keys of sum |q| (s c + |z|):
 * a score is off by d = (D + 32) t A + 2^-22 A (fp32 q in two parts of 11 bits) + 4 u max|x|;
 * a weight, relative, by 2 d, by 2^-21 of the exponential and by n u of the sum;
 * the weights times scales are rounded by w (bf16 q: fp16, 2^-11; fp32: 2^-22) and by
-  n 2^-36 max s at the least where they are small, summed 32 at a time by the instruction
-  (64 t) and n / 32 times in fp32:
-  |out - ref| <= (w + 64 t + 2 (2 d + 2^-21 + n u)) sum_j p (|s (c - 8)| + |z + 8 s|)
-                 + n 2^-36 max s + r |ref|
+  n 2^-36 max s at the least where they are small; sums of p s c and of p s, 8 of which go
+  off the first, are formed 32 keys at a time by the instruction (64 t of each) and
+  n / 32 times in fp32:
+  |out - ref| <= (w + 2 (2 d + 2^-21 + n u)) sum_j p (|s (c - 8)| + |z + 8 s|)
+                 + (64 t + n u) sum_j p s (c + 8) + n 2^-36 max s + r |ref|
   |lse - ref| <= 2 d + 2^-20 + n u + 4 u |ref|
 """
 import numpy as np
@@ -88,6 +89,7 @@ def check_decode(s, scale, out, lse, what, softcap=0.0, slopes=None):
         ks, vs = (np.repeat(rows[x].double().numpy(), 64, axis=-2) for x in ("ks", "vs"))
         kbig = ks[..., 0] * q4.unpack(rows["kc"]) + np.abs(ks[..., 1])
         vbig = np.abs(vs[..., 0] * (q4.unpack(rows["vc"]) - 8)) + np.abs(vs[..., 1] + 8 * vs[..., 0])
+        vsum = vs[..., 0] * (q4.unpack(rows["vc"]) + 8)
         for h in range(H):
             hk = h // G
             x, _ = so.scores(q[b][None, None], k[None], 0, h, scale, softcap=softcap, slopes=slopes, q_pos0=n - 1)
@@ -97,7 +99,7 @@ def check_decode(s, scale, out, lse, what, softcap=0.0, slopes=None):
             want = p @ v[:, hk]
             A = abs(scale) * (kbig[:, hk] @ np.abs(q[b, h])).max()
             d = (D + 32) * 2 * U * A + 2.0 ** -22 * A + 4 * U * (A + np.abs(x[0]).max())
-            bound = ((w + 128 * U + 2 * (2 * d + 2.0 ** -21 + n * U)) * (p @ vbig[:, hk]) +
+            bound = ((w + 2 * (2 * d + 2.0 ** -21 + n * U)) * (p @ vbig[:, hk]) + (128 + n) * U * (p @ vsum[:, hk]) +
                      n * 2.0 ** -36 * vs[:, hk, :, 0].max() + r * np.abs(want))
             over = np.abs(got[b, h] - want) - bound
             assert over.max() <= 0, f"{what} b{b} h{h}: past its bound by {over.max():.3e}"
