@@ -58,7 +58,7 @@ cp_status take_cache(PagedArgs* a, const cp_q4_cache* c, int B, int Hkv, int D, 
 cp_status ran(cudaError_t e) { return e == cudaSuccess ? CP_OK : CP_ERR_CUDA; }
 
 size_t partial_bytes(int G, int D, cp_dtype dt) {
-  const int rows = cp::q4_rows(dt == CP_BF16, G), ctas = cp::q4_per_sm(dt == CP_BF16, rows) * 152;
+  const int rows = cp::q4_rows(dt == CP_BF16, G), ctas = cp::q4_per_sm(dt == CP_BF16, rows, cp::q4_chunk(dt == CP_BF16, rows)) * 152;
   return round_up(static_cast<size_t>(ctas) * 2 * (G < rows ? G : rows) * (D + 2) * 4, 256);
 }
 
@@ -125,7 +125,8 @@ cp_status cp_paged_attn_decode_q4(const void* q, const cp_q4_cache* cache, const
   const int G = H / Hkv, rows = cp::q4_rows(dt == CP_BF16, G), groups = (G + rows - 1) / rows;
   // the list of blocks is indexed in 32 bits
   const int64_t keys = static_cast<int64_t>(cache->max_pages) * cache->page_size;
-  const int64_t blocks = (keys + cp::kQ4Block - 1) / cp::kQ4Block;
+  const int block = 4 * cp::q4_chunk(dt == CP_BF16, rows);
+  const int64_t blocks = (keys + block - 1) / block;
   if (keys > INT_MAX || blocks * Hkv * groups * (B > 0 ? B : 1) > INT_MAX / 2) return CP_ERR_INVALID_ARG;
   if (B == 0) return CP_OK;
   if (!q || !seq_lens || !out || !lse) return CP_ERR_INVALID_ARG;

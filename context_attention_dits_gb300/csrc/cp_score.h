@@ -147,18 +147,27 @@ cudaError_t launch_paged_decode(const PagedArgs& a, bool bf16, cudaStream_t s);
 
 // The cache in 4 bits.
 constexpr int kQ4Group = 64;   // values that share a scale and an offset
-constexpr int kQ4Block = 128;  // keys of one work block
 constexpr int kQ4MinPage = 16;
 // Query heads of a unit: as many columns of the matrix instruction, or twice.
 constexpr int q4_rows(bool bf16, int G) { return bf16 && G > 8 ? 16 : 8; }
-constexpr int q4_per_sm(bool bf16, int rows) { return bf16 && rows == 8 ? 4 : 2; }
-inline int q4_ctas(bool bf16, int rows, int sms) { return q4_per_sm(bf16, rows) * (sms < 152 ? sms : 152); }
+// Keys of a warp's step. Longer steps have more products under way and fewer
+// overheads a key, shorter ones share few keys among more CTAs (clusters).
+constexpr int kQ4FewKeys = 32;
+constexpr int q4_chunk(bool bf16, int rows) { return bf16 && rows == 8 ? 64 : 32; }
+// CTAs on a multiprocessor, as far as their registers go.
+constexpr int q4_per_sm(bool bf16, int rows, int chunk) { return bf16 && rows == 8 ? (chunk == 64 ? 3 : 4) : 2; }
+// CTAs over the list: as many as run at once on 152 multiprocessors at most, with
+// `smem` bytes of shared memory each (the list's own share grows with the batch).
+inline int q4_ctas(bool bf16, int rows, int smem, int sms) {
+  const int by_smem = 228 * 1024 / (smem + 1536), by_regs = q4_per_sm(bf16, rows, q4_chunk(bf16, rows));
+  return (by_smem < by_regs ? by_smem : by_regs) * (sms < 152 ? sms : 152);
+}
 // CTAs of a cluster that share a unit, or 0 for the list, as paged_cluster.
 inline int q4_cluster(bool bf16, int B, int Hkv, int G, int max_pages, int page_shift) {
   const int rows = q4_rows(bf16, G);
-  const int64_t blocks = ((static_cast<int64_t>(max_pages) << page_shift) + kQ4Block - 1) / kQ4Block;
+  const int64_t blocks = ((static_cast<int64_t>(max_pages) << page_shift) + 4 * kQ4FewKeys - 1) / (4 * kQ4FewKeys);
   const int64_t units = static_cast<int64_t>(B) * Hkv * ((G + rows - 1) / rows);
-  const int ctas = q4_per_sm(bf16, rows) * 152;
+  const int ctas = q4_per_sm(bf16, rows, kQ4FewKeys) * 152;
   const int most = units <= 8 ? kPagedCluster : kPagedCluster / 2;
   int cs = 1;
   while (cs < most && blocks > cs && units * cs * 2 <= ctas) cs *= 2;

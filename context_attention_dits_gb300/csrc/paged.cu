@@ -457,8 +457,9 @@ struct Unit : DecCfg<D, T> {
 template <int D, typename T>
 cudaError_t decode_d(const PagedArgs& a, cudaStream_t s) {
   constexpr bool kBf16 = sizeof(T) == 2;
-  return launch_decode<Unit<D, T>>(a, paged_cluster(D, kBf16, a.B, a.Hkv, a.G, a.max_pages, a.page_shift),
-                                   paged_grid(D, kBf16, INT_MAX, a.sms), s);
+  const int cs = paged_cluster(D, kBf16, a.B, a.Hkv, a.G, a.max_pages, a.page_shift);
+  if (cs > 0) return launch_clustered<Unit<D, T>>(a, cs, s);
+  return launch_listed<Unit<D, T>>(a, paged_grid(D, kBf16, INT_MAX, a.sms), s);
 }
 
 }  // namespace

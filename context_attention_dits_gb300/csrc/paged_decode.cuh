@@ -95,7 +95,7 @@ template <class C>
 __global__ void __launch_bounds__(kDecThreads, C::kPerSm) paged_decode_kernel(const __grid_constant__ PagedArgs a) {
   constexpr int D = C::kD;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int cum[kPagedMaxBatch + 1];  // blocks before sequence b
+  int* cum = reinterpret_cast<int*>(smem + C::kSmem);  // [B + 1]: blocks before sequence b
   __shared__ int wsum[kDecWarps];
   __shared__ typename C::Shared shared;
   C unit(a, smem, shared);
@@ -349,25 +349,28 @@ __global__ void __launch_bounds__(kDecThreads, C::kPerSm) paged_decode_cluster_k
   cluster_sync();  // a CTA's shared memory stays until its peers have read it
 }
 
-// One launch by clusters of cs CTAs, or (cs 0) at most `ctas` CTAs over the list and
-// the join of what they leave.
+// One launch by clusters of cs CTAs.
 template <class C>
-cudaError_t launch_decode(const PagedArgs& a, int cs, int ctas, cudaStream_t s) {
+cudaError_t launch_clustered(const PagedArgs& a, int cs, cudaStream_t s) {
+  cudaError_t e;
+  if ((e = allow_smem<paged_decode_cluster_kernel<C>, true>(C::kSmem)) != cudaSuccess) return e;
+  const int units = a.Hkv * ((a.G + C::kRows - 1) / C::kRows);
+  return launch_clusters(paged_decode_cluster_kernel<C>, units, a.B, 1, cs, kDecThreads, C::kSmem, false, s, a);
+}
+
+// At most `ctas` CTAs over the list, and the join of what they leave.
+template <class C>
+cudaError_t launch_listed(const PagedArgs& a, int ctas, cudaStream_t s) {
   constexpr int D = C::kD;
   static_assert(C::kSmem + (kPagedMaxBatch + 8) * 4 <= 227 * 1024, "shared memory budget");
   cudaError_t e;
-  if (cs > 0) {
-    if ((e = allow_smem<paged_decode_cluster_kernel<C>, true>(C::kSmem)) != cudaSuccess) return e;
-    const int units = a.Hkv * ((a.G + C::kRows - 1) / C::kRows);
-    return launch_clusters(paged_decode_cluster_kernel<C>, units, a.B, 1, cs, kDecThreads, C::kSmem, false, s, a);
-  }
-  if ((e = allow_smem<paged_decode_kernel<C>>(C::kSmem)) != cudaSuccess) return e;
+  if ((e = allow_smem<paged_decode_kernel<C>>(C::kSmem + (kPagedMaxBatch + 1) * 4)) != cudaSuccess) return e;
   // blocks of the list if every table were full; a unit of one block is never split
   const int groups = (a.G + C::kRows - 1) / C::kRows;
   const int64_t per_unit = ((static_cast<int64_t>(a.max_pages) << a.page_shift) + C::kBlock - 1) / C::kBlock;
   const int64_t bound = per_unit * a.Hkv * groups * a.B;
   const int grid = bound < 1 ? 1 : bound < ctas ? static_cast<int>(bound) : ctas;
-  paged_decode_kernel<C><<<grid, kDecThreads, C::kSmem, s>>>(a);
+  paged_decode_kernel<C><<<grid, kDecThreads, C::kSmem + (a.B + 1) * 4, s>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess || per_unit <= 1) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(a.H, a.B);

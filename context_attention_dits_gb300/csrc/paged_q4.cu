@@ -205,12 +205,9 @@ __global__ void __launch_bounds__(kRowThreads) q4_read_kernel(const __grid_const
 // ----------------------------------------------------------------------------
 // Decode
 // ----------------------------------------------------------------------------
-constexpr int kChunk = 32;  // keys of a warp and step
-static_assert(kChunk * kDecWarps == kQ4Block, "a block is a chunk of each warp");
-
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -228,6 +225,13 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 }
 __device__ __forceinline__ float2 unpack_f16x2(uint32_t x) { return __half22float2(*reinterpret_cast<__half2*>(&x)); }
 __device__ __forceinline__ float power_of_2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+
+// x plus the offset of a scale word, its upper bf16 number.
+__device__ __forceinline__ float plus_offset(float x, uint32_t w) {
+  float y;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tadd.rn.f32.bf16 %0, hi, %1;\n\t}" : "=f"(y) : "f"(x), "r"(w));
+  return y;
+}
 
 // Two codes (bits 0..3 of each half, or 4..7: kHigh) as fp16 numbers c - 8.
 template <bool kHigh>
@@ -261,9 +265,10 @@ __device__ __forceinline__ float2 tanh_poly(float2 u) {
 // rounded weights, is the product with a row of ones. fp32 queries: two parts of each,
 // whose products leave 2^-22 out, and codes as c - 8 from the start, since a sum of
 // numbers above zero would lose more to the instruction's truncation.
-template <int D_, bool kF32, int kTiles>
+template <int D_, bool kF32, int kTiles, int kChunk>
 struct Q4Unit {
-  static constexpr int kD = D_, kRows = 8 * kTiles, kBlock = kQ4Block, kPerSm = q4_per_sm(!kF32, kRows);
+  static constexpr int kT = kChunk / 16;  // tiles of a warp's keys in a step
+  static constexpr int kD = D_, kRows = 8 * kTiles, kBlock = kChunk * kDecWarps, kPerSm = q4_per_sm(!kF32, kRows, kChunk);
   static constexpr int kGroups = D_ / kQ4Group, kParts = kF32 ? 2 : 1;
   static constexpr int kRowB = D_ / 2, kScaleB = kGroups * 4;  // a row's codes and scales
   static constexpr int kCodes = kChunk * kRowB, kScales = kChunk * kScaleB, kStage = 2 * (kCodes + kScales);
@@ -271,6 +276,7 @@ struct Q4Unit {
   static constexpr int kState = kRows * (D_ + 2);
   static constexpr int kWarpB = ((kStages * kStage > 2 * kState * 4 ? kStages * kStage : 2 * kState * 4) + 127) & ~127;
   static constexpr int kSmem = kDecWarps * kWarpB;
+  using Keys = std::conditional_t<kChunk == 64, uint64_t, uint32_t>;  // a bit a key of a chunk
   struct Shared {
     uint64_t full[kDecWarps][kStages];
     uint32_t abort;
@@ -282,7 +288,7 @@ struct Q4Unit {
 
   __device__ __forceinline__ Q4Unit(const PagedArgs& a, uint8_t*, Shared& sh) {
     if (threadIdx.x < kDecWarps * kStages)
-      mbar_init(smem_addr(&sh.full[0][0] + threadIdx.x), a.page_shift >= 5 ? 4 : 8);
+      mbar_init(smem_addr(&sh.full[0][0] + threadIdx.x), 4 * runs(a));
     if (threadIdx.x == 0) sh.abort = 0;
     fence_mbar_init();
     fence_async();
@@ -295,11 +301,11 @@ struct Q4Unit {
     uint8_t* wbuf = smem + warp * kWarpB;
     const int h0 = hk * a.G + hg * kRows, nrow = min(kRows, a.G - hg * kRows);
     // this warp's chunks: keys (4 blk + warp) 32 on, the last below n
-    const int last = min(blk1, n > warp * kChunk ? (n - warp * kChunk + kQ4Block - 1) / kQ4Block : 0);
+    const int last = min(blk1, n > warp * kChunk ? (n - warp * kChunk + kBlock - 1) / kBlock : 0);
 
-    // ---- loads: a lane a piece (codes and scales of k and v, each twice where pages are of 16 rows) ----
-    const int pieces = a.page_shift >= 5 ? 4 : 8, rows = a.page_shift >= 5 ? 32 : 16;
-    const int which = lane & 3, half = lane >> 2;  // k codes, k scales, v codes, v scales
+    // ---- loads: a lane a piece (codes and scales of k and v, each as often as the chunk meets pages) ----
+    const int pieces = 4 * runs(a), rows = kChunk / runs(a);
+    const int which = lane & 3, run = lane >> 2;  // k codes, k scales, v codes, v scales
     const int row_b = which & 1 ? kScaleB : kRowB;
     const uint32_t piece_b = rows * row_b;
     const int64_t head_b = static_cast<int64_t>(row_b) << a.page_shift, page_b = head_b * a.Hkv;
@@ -308,11 +314,11 @@ struct Q4Unit {
                                                       : which == 2 ? a.v_cache
                                                                    : a.v_scales) +
                           hk * head_b;
-    const uint32_t dst = smem_addr(wbuf) + (which & 2 ? kCodes + kScales : 0) + (which & 1 ? kCodes : 0) + half * piece_b;
+    const uint32_t dst = smem_addr(wbuf) + (which & 2 ? kCodes + kScales : 0) + (which & 1 ? kCodes : 0) + run * piece_b;
     const uint32_t bars = smem_addr(&sh.full[warp][0]);
     const int* table = a.table + static_cast<int64_t>(b) * a.max_pages;
     const int page_mask = (1 << a.page_shift) - 1;
-    int pos = (blk0 * kDecWarps + warp) * kChunk + half * 16;  // of the chunk that `page` is of
+    int pos = (blk0 * kDecWarps + warp) * kChunk + run * rows;  // of the chunk that `page` is of
     int asked = blk0, page = -1;
     auto find = [&]() {
       page = -1;
@@ -327,11 +333,18 @@ struct Q4Unit {
     };
     // asks for the chunk, looks the next one's page up; which of its keys there are, a bit each
     auto load = [&]() {
-      const uint32_t found = __ballot_sync(0xffffffffu, page >= 0);
-      uint32_t on = found & 1u ? 0xffffffffu : 0u;
-      if (pieces == 8) on = (on & 0xffffu) | (found & 16u ? 0xffff0000u : 0u);
+      uint32_t found = __ballot_sync(0xffffffffu, page >= 0) & 0x11111111u;  // a bit a run
+      Keys on;
+      if (found == (0x11111111u >> (32 - pieces))) {
+        on = ~Keys{0};
+      } else {
+        on = 0;
+        const Keys one = rows == 64 ? ~Keys{0} : (Keys{1} << (rows & 63)) - 1;
+        for (int at = 0; found; at += rows, found >>= 4)
+          if (found & 1u) on |= one << at;
+      }
       const int rest = n - (asked * kDecWarps + warp) * kChunk;
-      if (rest < kChunk) on &= (1u << rest) - 1;
+      if (rest < kChunk) on &= (Keys{1} << rest) - 1;
       if (lane < pieces) {
         const uint32_t bar = bars + ask * 8;
         mbar_arrive_expect_tx(bar, page >= 0 ? piece_b : 0);
@@ -339,13 +352,13 @@ struct Q4Unit {
       }
       if (++ask == kStages) ask = 0;
       ++asked;
-      pos += kQ4Block;
+      pos += kBlock;
       find();
       return on;
     };
     fence_async();  // (what was read and written here before, by this and by other warps ahead of the barrier)
     find();
-    uint32_t coming[kStages - 1] = {};  // the keys of the chunks under way
+    Keys coming[kStages - 1] = {};  // the keys of the chunks under way
     if (!aborted(sh)) {
 #pragma unroll
       for (int st = 0; st < kStages - 1; ++st)
@@ -444,16 +457,27 @@ struct Q4Unit {
     for (int blk = blk0; blk < last; ++blk) {
       if (!__all_sync(0xffffffffu, mbar_wait_bounded(bars + take * 8, phase >> take & 1u, &sh.abort, a.err, a.timeout_ns)))
         break;
-      const uint32_t on = coming[0];
+      const Keys on = coming[0];
 #pragma unroll
       for (int st = 1; st < kStages - 1; ++st) coming[st - 1] = coming[st];
       if (asked < last) coming[kStages - 2] = load();  // into the stage that the last step read
       const int stage = take * kStage;
-
-      // ---- scores, keys as rows: two tiles of 16; [tile][row] over the lane's two heads ----
-      float2 s[2][kTiles][2];
+      const bool part = on != ~Keys{0};
+      if (part) {  // rows that hold no key may hold anything: their scales become 0, and no result depends on them
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
+        for (int i = lane; i < kChunk; i += 32)
+          if (!(on >> i & 1u))
+#pragma unroll
+            for (int y = 0; y < 2 * kGroups; ++y)
+              *reinterpret_cast<uint32_t*>(wbuf + stage + kCodes + (y & 1 ? kCodes + kScales : 0) + i * kScaleB + (y >> 1) * 4) = 0;
+        fence_async();  // (before copies come here again)
+        __syncwarp();
+      }
+
+      // ---- scores, keys as rows: tiles of 16; [tile][row] over the lane's two heads ----
+      float2 s[kT][kTiles][2];
+#pragma unroll
+      for (int t = 0; t < kT; ++t) {
         float dot[kTiles][kGroups][4];
 #pragma unroll
         for (int y = 0; y < kGroups; ++y) {
@@ -487,42 +511,37 @@ struct Q4Unit {
           scales(zrow + stage + (16 * t + 8 * r) * kScaleB, w);
 #pragma unroll
           for (int x = 0; x < kTiles; ++x) {
-            float2 d = twice(0.f), zq = twice(0.f);
+            float2 d, zq;
 #pragma unroll
             for (int y = 0; y < kGroups; ++y) {
-              const float ks = __uint_as_float(w[y] << 16), kz = __uint_as_float(w[y] & 0xffff0000u);
-              const float2 one = make_float2(dot[x][y][2 * r], dot[x][y][2 * r + 1]);
-              d = y ? fma2(twice(ks), one, d) : mul2(twice(ks), one);
-              const float2 zc = twice(kF32 ? fmaf(8.f, ks, kz) : kz);
-              zq = y ? fma2(zc, qsum[x][y], zq) : mul2(zc, qsum[x][y]);
+              const float ks = __uint_as_float(w[y] << 16), kz = plus_offset(kF32 ? 8.f * ks : 0.f, w[y]);
+              const float d0 = dot[x][y][2 * r], d1 = dot[x][y][2 * r + 1];
+              d.x = y ? fmaf(ks, d0, d.x) : ks * d0;
+              d.y = y ? fmaf(ks, d1, d.y) : ks * d1;
+              zq.x = y ? fmaf(kz, qsum[x][y].x, zq.x) : kz * qsum[x][y].x;
+              zq.y = y ? fmaf(kz, qsum[x][y].y, zq.y) : kz * qsum[x][y].y;
             }
             s[t][x][r] = fma2(d, undo[x], zq);
           }
         }
       }
-      const bool part = on != 0xffffffffu;
-      auto there = [&](int t, int r) { return !part || (on >> (kr + 16 * t + 8 * r) & 1u); };
       if (a.cap > 0.f) {
         float far = 0.f;
-        if (part)  // a row that holds no key has no say: results do not depend on what lies there
 #pragma unroll
-          for (int i = 0; i < 4 * kTiles; ++i)
-            if (!there(i & 1, i >> 1 & 1)) s[i & 1][i >> 2][i >> 1 & 1] = twice(0.f);
-#pragma unroll
-        for (int i = 0; i < 4 * kTiles; ++i) {
-          const float2 y = s[i & 1][i >> 2][i >> 1 & 1];
+        for (int i = 0; i < 2 * kT * kTiles; ++i) {
+          float2& y = s[i / 2 % kT][i / (2 * kT)][i & 1];
           far = fmax3(far, fabsf(y.x), fabsf(y.y));
         }
         if (__all_sync(0xffffffffu, far <= 1.f)) {
 #pragma unroll
-          for (int i = 0; i < 4 * kTiles; ++i) {
-            float2& y = s[i & 1][i >> 2][i >> 1 & 1];
+          for (int i = 0; i < 2 * kT * kTiles; ++i) {
+            float2& y = s[i / 2 % kT][i / (2 * kT)][i & 1];
             y = mul2(mul2(y, twice(cap2)), tanh_poly(mul2(y, y)));
           }
         } else {
 #pragma unroll
-          for (int i = 0; i < 4 * kTiles; ++i) {
-            float2& y = s[i & 1][i >> 2][i >> 1 & 1];
+          for (int i = 0; i < 2 * kT * kTiles; ++i) {
+            float2& y = s[i / 2 % kT][i / (2 * kT)][i & 1];
             y = make_float2(cap2 * tanhf(y.x), cap2 * tanhf(y.y));
           }
         }
@@ -530,7 +549,7 @@ struct Q4Unit {
       if (a.slopes) {
         const float dist = static_cast<float>(n - 1 - (blk * kDecWarps + warp) * kChunk - kr);
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+        for (int t = 0; t < kT; ++t)
 #pragma unroll
           for (int r = 0; r < 2; ++r)
 #pragma unroll
@@ -538,60 +557,54 @@ struct Q4Unit {
       }
       if (part)
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+        for (int t = 0; t < kT; ++t)
 #pragma unroll
           for (int r = 0; r < 2; ++r)
 #pragma unroll
             for (int x = 0; x < kTiles; ++x)
-              if (!there(t, r)) s[t][x][r] = twice(-INFINITY);
+              if (!(on >> (kr + 16 * t + 8 * r) & 1u)) s[t][x][r] = twice(-INFINITY);
 
       // ---- weights ----
       float2 f[kTiles];
 #pragma unroll
       for (int x = 0; x < kTiles; ++x) {
-        auto weigh = [&](float& mm, float& ll, float& ff, float& p0, float& p1, float& p2, float& p3) {
-          float mx = fmax3(fmaxf(p0, p1), p2, p3);
+        auto weigh = [&](float& mm, float& ll, float& ff, auto p) {
+          float mx = p(0, 0), sum = 0.f;
+#pragma unroll
+          for (int i = 1; i < 2 * kT; ++i) mx = fmaxf(mx, p(i >> 1, i & 1));
 #pragma unroll
           for (int of = 4; of < 32; of <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, of));
           const float mn = fmaxf(mm, mx), ref = mn == -INFINITY ? 0.f : mn;
           auto ex2 = [](float z) { return kF32 ? exp2f(z) : ex2_approx(z); };
           ff = ex2(mm - ref);
           mm = mn;
-          p0 = ex2(p0 - ref);
-          p1 = ex2(p1 - ref);
-          p2 = ex2(p2 - ref);
-          p3 = ex2(p3 - ref);
-          ll = fmaf(ll, ff, (p0 + p1) + (p2 + p3));
+#pragma unroll
+          for (int i = 0; i < 2 * kT; ++i) {
+            float& y = p(i >> 1, i & 1);
+            y = ex2(y - ref);
+            sum += y;
+          }
+          ll = fmaf(ll, ff, sum);
         };
-        weigh(m[x].x, l[x].x, f[x].x, s[0][x][0].x, s[0][x][1].x, s[1][x][0].x, s[1][x][1].x);
-        weigh(m[x].y, l[x].y, f[x].y, s[0][x][0].y, s[0][x][1].y, s[1][x][0].y, s[1][x][1].y);
+        weigh(m[x].x, l[x].x, f[x].x, [&](int t, int r) -> float& { return s[t][x][r].x; });
+        weigh(m[x].y, l[x].y, f[x].y, [&](int t, int r) -> float& { return s[t][x][r].y; });
       }
 
       // ---- the values' scales meet the weights: p s in fp16, scaled so that it stays
       // below 2^15; p (z + 8 s) summed as it is ----
-      float vs[2][2][kGroups], largest = 0.f;  // [tile][row]
+      float largest = 0.f;  // (a lane a key here)
 #pragma unroll
-      for (int x = 0; x < kTiles; ++x)
+      for (int i = 0; i < kChunk; i += 32) {
+        uint32_t w[kGroups];
+        scales(wbuf + stage + 2 * kCodes + kScales + (lane + i) * kScaleB, w);
 #pragma unroll
-        for (int y = 0; y < kGroups; ++y) zs[x][y] = mul2(zs[x][y], f[x]);
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          uint32_t w[kGroups];
-          scales(zrow + stage + kCodes + kScales + (16 * t + 8 * r) * kScaleB, w);
-          if (!there(t, r))  // (and may hold anything)
-#pragma unroll
-            for (int y = 0; y < kGroups; ++y) w[y] = 0;
-#pragma unroll
-          for (int y = 0; y < kGroups; ++y) {
-            const float sv = __uint_as_float(w[y] << 16), zz = fmaf(8.f, sv, __uint_as_float(w[y] & 0xffff0000u));
-            vs[t][r][y] = sv;
-            largest = fmaxf(largest, fabsf(sv));
-#pragma unroll
-            for (int x = 0; x < kTiles; ++x) zs[x][y] = fma2(s[t][x][r], twice(zz), zs[x][y]);
-          }
+        for (int y = 0; y < kGroups; ++y) {
+          largest = fmaxf(largest, fabsf(__uint_as_float(w[y] << 16)));
         }
+      }
+      float2 fz[kTiles];
+#pragma unroll
+      for (int x = 0; x < kTiles; ++x) fz[x] = f[x];
       if (__any_sync(0xffffffffu, largest * fit >= 32768.f)) {  // seldom: a larger scale than any before
         const int now = max(top, static_cast<int>(__reduce_max_sync(0xffffffffu, __float_as_uint(largest)) >> 23));
         const float2 down = twice(now - top > 126 ? 0.f : power_of_2(top - now));
@@ -605,19 +618,25 @@ struct Q4Unit {
       // truncate, which would add up along a long sequence) ----
 #pragma unroll
       for (int y = 0; y < kGroups; ++y) {
-        uint32_t pf[kTiles][2][kParts][2];
+        uint32_t pf[kTiles][kT][kParts][2];
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+        for (int x = 0; x < kTiles; ++x) zs[x][y] = mul2(zs[x][y], fz[x]);
+#pragma unroll
+        for (int t = 0; t < kT; ++t)
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            const float sv = vs[t][r][y] * fit;
+            const uint32_t w = *reinterpret_cast<const uint32_t*>(zrow + stage + kCodes + kScales + (16 * t + 8 * r) * kScaleB + 4 * y);
+            const float sv = __uint_as_float(w << 16), zz = plus_offset(8.f * sv, w), fs = sv * fit;
 #pragma unroll
             for (int x = 0; x < kTiles; ++x) {
-              const float2 ps = mul2(s[t][x][r], twice(sv));
-              const uint32_t w = pack_f16x2(ps.x, ps.y);
-              pf[x][t][0][r] = transpose8(w);
+              const float2 p = s[t][x][r];
+              zs[x][y].x = fmaf(p.x, zz, zs[x][y].x);
+              zs[x][y].y = fmaf(p.y, zz, zs[x][y].y);
+              const float2 ps = make_float2(p.x * fs, p.y * fs);
+              const uint32_t u = pack_f16x2(ps.x, ps.y);
+              pf[x][t][0][r] = transpose8(u);
               if constexpr (kF32) {
-                const float2 have = unpack_f16x2(w);
+                const float2 have = unpack_f16x2(u);
                 pf[x][t][1][r] = transpose8(pack_f16x2(ps.x - have.x, ps.y - have.y));
               }
             }
@@ -630,7 +649,7 @@ struct Q4Unit {
 #pragma unroll
             for (int e = 0; e < 4; ++e) add[x][j][e] = ones[x][e] = 0.f;
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
+        for (int t = 0; t < kT; ++t) {
           const int at = stage + 16 * t * kRowB + y * 32;
           const uint32_t w0 = *reinterpret_cast<const uint32_t*>(vrow_a + at);
           const uint32_t w1 = *reinterpret_cast<const uint32_t*>(vrow_b + at);
@@ -727,6 +746,10 @@ struct Q4Unit {
     fence_async();
   }
 
+  // Pages that a chunk meets.
+  static __device__ __forceinline__ int runs(const PagedArgs& a) {
+    return (1 << a.page_shift) >= kChunk ? 1 : kChunk >> a.page_shift;
+  }
   // The same answer for the whole warp.
   static __device__ __forceinline__ bool aborted(Shared& sh) {
     return __any_sync(0xffffffffu, *static_cast<volatile uint32_t*>(&sh.abort));
@@ -741,9 +764,11 @@ struct Q4Unit {
 
 template <int D, bool kF32, int kTiles>
 cudaError_t decode_q4(const PagedArgs& a, cudaStream_t s) {
-  using U = Q4Unit<D, kF32, kTiles>;
-  return launch_decode<U>(a, q4_cluster(!kF32, a.B, a.Hkv, a.G, a.max_pages, a.page_shift),
-                          q4_ctas(!kF32, U::kRows, a.sms), s);
+  using Few = Q4Unit<D, kF32, kTiles, kQ4FewKeys>;
+  using Many = Q4Unit<D, kF32, kTiles, q4_chunk(!kF32, 8 * kTiles)>;
+  const int cs = q4_cluster(!kF32, a.B, a.Hkv, a.G, a.max_pages, a.page_shift);
+  if (cs > 0) return launch_clustered<Few>(a, cs, s);
+  return launch_listed<Many>(a, q4_ctas(!kF32, Many::kRows, Many::kSmem + (a.B + 1) * 4, a.sms), s);
 }
 
 template <typename... P>
