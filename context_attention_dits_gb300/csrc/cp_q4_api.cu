@@ -58,8 +58,9 @@ cp_status take_cache(PagedArgs* a, const cp_q4_cache* c, int B, int Hkv, int D, 
 cp_status ran(cudaError_t e) { return e == cudaSuccess ? CP_OK : CP_ERR_CUDA; }
 
 size_t partial_bytes(int G, int D, cp_dtype dt) {
-  const int rows = cp::q4_rows(dt == CP_BF16, G), ctas = cp::q4_per_sm(dt == CP_BF16, rows, cp::q4_chunk(dt == CP_BF16, rows)) * 152;
-  return round_up(static_cast<size_t>(ctas) * 2 * (G < rows ? G : rows) * (D + 2) * 4, 256);
+  const int rows = cp::q4_rows(dt == CP_BF16, G);
+  const int workers = 4 * 152 * cp::q4_per_sm(dt == CP_BF16, rows, cp::q4_chunk(dt == CP_BF16, rows));
+  return round_up(static_cast<size_t>(workers) * 2 * (G < rows ? G : rows) * (D + 2) * 4, 256);
 }
 
 }  // namespace
@@ -125,7 +126,7 @@ cp_status cp_paged_attn_decode_q4(const void* q, const cp_q4_cache* cache, const
   const int G = H / Hkv, rows = cp::q4_rows(dt == CP_BF16, G), groups = (G + rows - 1) / rows;
   // the list of blocks is indexed in 32 bits
   const int64_t keys = static_cast<int64_t>(cache->max_pages) * cache->page_size;
-  const int block = 4 * cp::q4_chunk(dt == CP_BF16, rows);
+  const int block = cp::q4_chunk(dt == CP_BF16, rows);
   const int64_t blocks = (keys + block - 1) / block;
   if (keys > INT_MAX || blocks * Hkv * groups * (B > 0 ? B : 1) > INT_MAX / 2) return CP_ERR_INVALID_ARG;
   if (B == 0) return CP_OK;

@@ -155,7 +155,7 @@ constexpr int q4_rows(bool bf16, int G) { return bf16 && G > 8 ? 16 : 8; }
 constexpr int kQ4FewKeys = 32;
 constexpr int q4_chunk(bool bf16, int rows) { return bf16 && rows == 8 ? 64 : 32; }
 // CTAs on a multiprocessor, as far as their registers go.
-constexpr int q4_per_sm(bool bf16, int rows, int chunk) { return bf16 && rows == 8 ? (chunk == 64 ? 3 : 4) : 2; }
+constexpr int q4_per_sm(bool bf16, int rows, int chunk) { return bf16 && rows == 8 ? (chunk == 64 ? 2 : 4) : 2; }
 // CTAs over the list: as many as run at once on 152 multiprocessors at most, with
 // `smem` bytes of shared memory each (the list's own share grows with the batch).
 inline int q4_ctas(bool bf16, int rows, int smem, int sms) {

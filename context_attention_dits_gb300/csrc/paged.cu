@@ -444,6 +444,7 @@ __device__ __forceinline__ void decode_unit(const PagedArgs& a, int b, int n, in
 template <int D, typename T>
 struct Unit : DecCfg<D, T> {
   static constexpr int kD = D, kBlock = kPagedBlock, kPerSm = 0;
+  static constexpr bool kEarly = false;
   struct Shared {
     uint32_t have[kDecWarps][4];  // the rows that a stage holds, a bit each
   };

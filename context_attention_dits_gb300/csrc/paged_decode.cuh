@@ -6,6 +6,7 @@
 //   kWarpB, kState bytes between the warps' buffers, and the floats of a warp's state:
 //                  O [kRows][kD], then m (units of log2) and l of each head
 //   kPerSm         CTAs on a multiprocessor that its registers leave room for (0: whatever comes)
+//   kEarly         clusters may start while their predecessor in the stream ends
 //   Shared, C(a, smem, shared), run(a, b, n, hk, hg, blk0, blk1, smem, shared)
 //                  what a CTA shares and keeps, and a unit's blocks [blk0, blk1) of n
 //                  keys: leaves each warp's state at the start of its buffers
@@ -89,24 +90,15 @@ __device__ __forceinline__ float join_warps(const uint8_t* smem, int i, float& m
   return acc;
 }
 
-// The list: all units' blocks of C::kBlock keys, cut into equal contiguous ranges,
-// one per CTA.
-template <class C>
-__global__ void __launch_bounds__(kDecThreads, C::kPerSm) paged_decode_kernel(const __grid_constant__ PagedArgs a) {
-  constexpr int D = C::kD;
-  extern __shared__ __align__(128) uint8_t smem[];
-  int* cum = reinterpret_cast<int*>(smem + C::kSmem);  // [B + 1]: blocks before sequence b
-  __shared__ int wsum[kDecWarps];
-  __shared__ typename C::Shared shared;
-  C unit(a, smem, shared);
+// The work list: cum[b], b = 0 .. B, becomes the blocks of kBlock keys before sequence
+// b, counting each block HG times. The CTA's threads all come here.
+template <int kBlock>
+__device__ __forceinline__ int work_list(const PagedArgs& a, int HG, int* cum, int* wsum) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int groups = (a.G + C::kRows - 1) / C::kRows;
-  const int HG = a.Hkv * groups;
-  // ---- the work list: an exclusive sum of the sequences' blocks ----
   int carry = 0;
   for (int b0 = 0; b0 < a.B; b0 += kDecThreads) {
     const int b = b0 + threadIdx.x;
-    const int x = b < a.B ? (seq_len(a, b) + C::kBlock - 1) / C::kBlock * HG : 0;
+    const int x = b < a.B ? (seq_len(a, b) + kBlock - 1) / kBlock * HG : 0;
     int s = x;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -125,26 +117,46 @@ __global__ void __launch_bounds__(kDecThreads, C::kPerSm) paged_decode_kernel(co
   }
   if (threadIdx.x == 0) cum[a.B] = carry;
   __syncthreads();
-  const int total = carry;
-  // sequences without a token: out 0, lse -inf
+  return carry;
+}
+// Sequences without a token: out 0, lse -inf.
+template <int D>
+__device__ __forceinline__ void no_tokens(const PagedArgs& a, const int* cum) {
   for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
     if (cum[b + 1] != cum[b]) continue;
     for (int i = threadIdx.x; i < a.H * D; i += kDecThreads) put_out(a, static_cast<int64_t>(b) * a.H * D + i, 0.f);
     for (int i = threadIdx.x; i < a.H; i += kDecThreads) a.lse[static_cast<int64_t>(b) * a.H + i] = -INFINITY;
   }
+}
+// The sequence of the list's block `at`.
+__device__ __forceinline__ int sequence_of(const PagedArgs& a, const int* cum, int at) {
+  int lo = 0, hi = a.B - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) / 2;
+    if (cum[mid] <= at) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+// The list: all units' blocks of C::kBlock keys, cut into equal contiguous ranges,
+// one per CTA.
+template <class C>
+__global__ void __launch_bounds__(kDecThreads, C::kPerSm) paged_decode_kernel(const __grid_constant__ PagedArgs a) {
+  constexpr int D = C::kD;
+  extern __shared__ __align__(128) uint8_t smem[];
+  int* cum = reinterpret_cast<int*>(smem + C::kSmem);  // [B + 1]: blocks before sequence b
+  __shared__ int wsum[kDecWarps];
+  __shared__ typename C::Shared shared;
+  C unit(a, smem, shared);
+  const int groups = (a.G + C::kRows - 1) / C::kRows;
+  const int HG = a.Hkv * groups;
+  const int total = work_list<C::kBlock>(a, HG, cum, wsum);
+  no_tokens<D>(a, cum);
   const int share = (total + gridDim.x - 1) / gridDim.x;
   const int begin = min(total, static_cast<int>(blockIdx.x) * share), end = min(total, begin + share);
   if (begin >= end) return;
 
-  int b = 0;
-  {  // the sequence of the first block
-    int lo = 0, hi = a.B - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) / 2;
-      if (cum[mid] <= begin) lo = mid; else hi = mid - 1;
-    }
-    b = lo;
-  }
+  int b = sequence_of(a, cum, begin);
   for (int at = begin; at < end;) {
     while (cum[b + 1] <= at) ++b;
     const int n = min(max(a.seq_lens[b], 0), table_len(a));
@@ -188,7 +200,7 @@ __global__ void __launch_bounds__(kDecThreads, C::kPerSm) paged_decode_kernel(co
 // Joins the partials of a unit that lay in more than one CTA: the first in the
 // slot that info names, the others in slot 0 of the CTAs up to info.y. A thread
 // per column; the partials' weights first, a thread each, then the columns with
-// eight loads under way (a dependent walk over 32 partials took 10 us).
+// 32 loads under way (a dependent walk over 32 partials took 10 us).
 template <int D>
 __global__ void __launch_bounds__(D) paged_join_kernel(const __grid_constant__ PagedArgs a, int rows) {
   __shared__ float weight[kPagedMostCtas];
@@ -256,15 +268,15 @@ __global__ void __launch_bounds__(D) paged_join_kernel(const __grid_constant__ P
   sum = 0.f;
 #pragma unroll
   for (int i = 0; i < D / 32; ++i) sum += red[1][i];
-  int i = 0;
-  for (; i + 8 <= n; i += 8) {
-    float x[8];
+  for (int i = 0; i < n; i += 32) {
+    float x[32];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) x[u] = part(i + u)[r * D + d];
+    for (int u = 0; u < 32; ++u)
+      if (i + u < n) x[u] = part(i + u)[r * D + d];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) acc = fmaf(x[u], weight[i + u], acc);
+    for (int u = 0; u < 32; ++u)
+      if (i + u < n) acc = fmaf(x[u], weight[i + u], acc);
   }
-  for (; i < n; ++i) acc = fmaf(part(i)[r * D + d], weight[i], acc);
   store();
 }
 
@@ -277,6 +289,7 @@ __global__ void __launch_bounds__(kDecThreads, C::kPerSm) paged_decode_cluster_k
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ typename C::Shared shared;
   C unit(a, smem, shared);
+  if (C::kEarly) grid_wait();
   const int cs = cluster_size(), rank = cluster_rank();
   const int groups = (a.G + C::kRows - 1) / C::kRows;
   const int u = blockIdx.x / cs, b = blockIdx.y, hk = u / groups, hg = u - hk * groups;
@@ -355,7 +368,7 @@ cudaError_t launch_clustered(const PagedArgs& a, int cs, cudaStream_t s) {
   cudaError_t e;
   if ((e = allow_smem<paged_decode_cluster_kernel<C>, true>(C::kSmem)) != cudaSuccess) return e;
   const int units = a.Hkv * ((a.G + C::kRows - 1) / C::kRows);
-  return launch_clusters(paged_decode_cluster_kernel<C>, units, a.B, 1, cs, kDecThreads, C::kSmem, false, s, a);
+  return launch_clusters(paged_decode_cluster_kernel<C>, units, a.B, 1, cs, kDecThreads, C::kSmem, C::kEarly, s, a);
 }
 
 // At most `ctas` CTAs over the list, and the join of what they leave.

@@ -258,6 +258,12 @@ __device__ __forceinline__ float2 tanh_poly(float2 u) {
   return p;
 }
 
+// A warp's part of a unit: chunks first, first + step, ... below last, of sequence b's n
+// keys, for group hg of key/value head hk's query heads.
+struct Part {
+  int b, n, hk, hg, first, last, step;
+};
+
 // bf16 queries: one fp16 part of q and of the weights, and codes as they lie: the
 // bits of c, in fp16, are the (subnormal) number c 2^-24, those of 16 c another 16
 // times as large, so that a word of 8 codes takes five instructions. With them v's
@@ -268,7 +274,7 @@ __device__ __forceinline__ float2 tanh_poly(float2 u) {
 template <int D_, bool kF32, int kTiles, int kChunk>
 struct Q4Unit {
   static constexpr int kT = kChunk / 16;  // tiles of a warp's keys in a step
-  static constexpr int kD = D_, kRows = 8 * kTiles, kBlock = kChunk * kDecWarps, kPerSm = q4_per_sm(!kF32, kRows, kChunk);
+  static constexpr int kD = D_, kRows = 8 * kTiles, kBlock = kChunk, kPerSm = q4_per_sm(!kF32, kRows, kChunk);
   static constexpr int kGroups = D_ / kQ4Group, kParts = kF32 ? 2 : 1;
   static constexpr int kRowB = D_ / 2, kScaleB = kGroups * 4;  // a row's codes and scales
   static constexpr int kCodes = kChunk * kRowB, kScales = kChunk * kScaleB, kStage = 2 * (kCodes + kScales);
@@ -277,14 +283,22 @@ struct Q4Unit {
   static constexpr int kWarpB = ((kStages * kStage > 2 * kState * 4 ? kStages * kStage : 2 * kState * 4) + 127) & ~127;
   static constexpr int kSmem = kDecWarps * kWarpB;
   using Keys = std::conditional_t<kChunk == 64, uint64_t, uint32_t>;  // a bit a key of a chunk
+  static constexpr bool kEarly = true;
+  // the next part's first loads go ahead of this one's end where a stage has room for the state
+  static constexpr bool kAhead = kStages == 2 && kStage >= kState * 4;
   struct Shared {
     uint64_t full[kDecWarps][kStages];
     uint32_t abort;
   };
 
-  // stage and phase of the next chunk to ask for and to take
+  // stage of the next chunk to ask for and to take, and the stages' phases
   int ask = 0, take = 0;
   uint32_t phase = 0;
+  // the loads of a part, a lane a piece (codes and scales of k and v, each as often as a chunk meets pages)
+  int pos, page = 0, asked, last, step;  // of the lane's piece of chunk `asked`
+  const uint8_t* base;
+  const int* table;
+  Keys coming[kStages - 1];  // the keys of the chunks under way
 
   __device__ __forceinline__ Q4Unit(const PagedArgs& a, uint8_t*, Shared& sh) {
     if (threadIdx.x < kDecWarps * kStages)
@@ -295,75 +309,86 @@ struct Q4Unit {
     __syncthreads();
   }
 
+  static __device__ __forceinline__ int row_bytes() { return threadIdx.x & 1 ? kScaleB : kRowB; }
+  // (the page is looked at when its chunk is asked for: an instruction that needs it earlier would wait for the table)
+  __device__ __forceinline__ bool wanted(const PagedArgs& a, int n) const {
+    return static_cast<int>(threadIdx.x & 31) < 4 * runs(a) && asked < last && pos < n;
+  }
+  __device__ __forceinline__ void find(const PagedArgs& a, int n) {
+    if (wanted(a, n)) page = table[pos >> a.page_shift];
+  }
+  // Asks for chunk `asked` of n keys and looks the warp's next one's page up: which keys there are, a bit each.
+  __device__ __forceinline__ Keys load(const PagedArgs& a, int n, uint8_t* smem, Shared& sh) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, pieces = 4 * runs(a), rows = kChunk / runs(a);
+    bool ok = wanted(a, n);
+    if (ok && (page < 0 || page >= a.num_pages)) {
+      atomicOr(a.err, kDevErrPage);
+      ok = false;
+    }
+    uint32_t found = __ballot_sync(0xffffffffu, ok) & 0x11111111u;  // a bit a run
+    Keys on = 0;
+    if (found == (0x11111111u >> (32 - pieces))) {
+      on = ~Keys{0};
+    } else {
+      const Keys one = rows == 64 ? ~Keys{0} : (Keys{1} << (rows & 63)) - 1;
+      for (int at = 0; found; at += rows, found >>= 4)
+        if (found & 1u) on |= one << at;
+    }
+    const int rest = n - asked * kChunk;
+    if (rest < kChunk) on &= (Keys{1} << rest) - 1;
+    if (lane < pieces) {
+      const int row_b = row_bytes(), which = lane & 3;  // k codes, k scales, v codes, v scales
+      const uint32_t bar = smem_addr(&sh.full[warp][ask]), bytes = rows * row_b;
+      const uint32_t dst = smem_addr(smem + warp * kWarpB) + ask * kStage + (which & 2 ? kCodes + kScales : 0) +
+                           (which & 1 ? kCodes : 0) + (lane >> 2) * bytes;
+      const int64_t page_b = (static_cast<int64_t>(row_b) << a.page_shift) * a.Hkv;
+      mbar_arrive_expect_tx(bar, ok ? bytes : 0);
+      if (ok) bulk_g2s(dst, base + page * page_b + (pos & ((1 << a.page_shift) - 1)) * row_b, bytes, bar);
+    }
+    if (++ask == kStages) ask = 0;
+    asked += step;
+    pos += step * kChunk;
+    find(a, n);
+    return on;
+  }
+
+  // The loads of a part's first chunks.
+  __device__ __forceinline__ void start(const PagedArgs& a, const Part& p, uint8_t* smem, Shared& sh) {
+    const int which = threadIdx.x & 3, run = (threadIdx.x & 31) >> 2;
+    base = static_cast<const uint8_t*>(which == 0   ? a.k_cache
+                                       : which == 1 ? a.k_scales
+                                       : which == 2 ? a.v_cache
+                                                    : a.v_scales) +
+           p.hk * (static_cast<int64_t>(row_bytes()) << a.page_shift);
+    table = a.table + static_cast<int64_t>(p.b) * a.max_pages;
+    asked = p.first;
+    step = p.step;
+    last = p.last;
+    pos = asked * kChunk + run * (kChunk / runs(a));
+    fence_async();  // (what was read and written here before)
+    find(a, p.n);
+#pragma unroll
+    for (int st = 0; st < kStages - 1; ++st)
+      if (asked < last && !aborted(sh)) coming[st] = load(a, p.n, smem, sh);
+  }
+
+  // For a cluster: a warp's chunks of blocks [blk0, blk1); its state at the start of its buffers.
   __device__ __forceinline__ void run(const PagedArgs& a, int b, int n, int hk, int hg, int blk0, int blk1, uint8_t* smem,
                                       Shared& sh) {
+    const Part p{b, n, hk, hg, blk0 + static_cast<int>(threadIdx.x >> 5), blk1, kDecWarps};
+    start(a, p, smem, sh);
+    take_part(a, p, nullptr, smem, sh);
+  }
+
+  // A part whose first loads are under way, and those of the following one ahead of its
+  // end. Returns the warp's state: O [kRows][kD], then m and l.
+  __device__ __forceinline__ float* take_part(const PagedArgs& a, const Part& part, const Part* following, uint8_t* smem,
+                                              Shared& sh) {
+    const int b = part.b, n = part.n, hk = part.hk, hg = part.hg;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tq = lane & 3;
     uint8_t* wbuf = smem + warp * kWarpB;
-    const int h0 = hk * a.G + hg * kRows, nrow = min(kRows, a.G - hg * kRows);
-    // this warp's chunks: keys (4 blk + warp) 32 on, the last below n
-    const int last = min(blk1, n > warp * kChunk ? (n - warp * kChunk + kBlock - 1) / kBlock : 0);
-
-    // ---- loads: a lane a piece (codes and scales of k and v, each as often as the chunk meets pages) ----
-    const int pieces = 4 * runs(a), rows = kChunk / runs(a);
-    const int which = lane & 3, run = lane >> 2;  // k codes, k scales, v codes, v scales
-    const int row_b = which & 1 ? kScaleB : kRowB;
-    const uint32_t piece_b = rows * row_b;
-    const int64_t head_b = static_cast<int64_t>(row_b) << a.page_shift, page_b = head_b * a.Hkv;
-    const uint8_t* base = static_cast<const uint8_t*>(which == 0   ? a.k_cache
-                                                      : which == 1 ? a.k_scales
-                                                      : which == 2 ? a.v_cache
-                                                                   : a.v_scales) +
-                          hk * head_b;
-    const uint32_t dst = smem_addr(wbuf) + (which & 2 ? kCodes + kScales : 0) + (which & 1 ? kCodes : 0) + run * piece_b;
     const uint32_t bars = smem_addr(&sh.full[warp][0]);
-    const int* table = a.table + static_cast<int64_t>(b) * a.max_pages;
-    const int page_mask = (1 << a.page_shift) - 1;
-    int pos = (blk0 * kDecWarps + warp) * kChunk + run * rows;  // of the chunk that `page` is of
-    int asked = blk0, page = -1;
-    auto find = [&]() {
-      page = -1;
-      if (lane < pieces && asked < last && pos < n) {
-        page = table[pos >> a.page_shift];
-        if (page < 0 || page >= a.num_pages) {
-          atomicOr(a.err, kDevErrPage);
-          page = -1;
-        }
-      }
-      __syncwarp();
-    };
-    // asks for the chunk, looks the next one's page up; which of its keys there are, a bit each
-    auto load = [&]() {
-      uint32_t found = __ballot_sync(0xffffffffu, page >= 0) & 0x11111111u;  // a bit a run
-      Keys on;
-      if (found == (0x11111111u >> (32 - pieces))) {
-        on = ~Keys{0};
-      } else {
-        on = 0;
-        const Keys one = rows == 64 ? ~Keys{0} : (Keys{1} << (rows & 63)) - 1;
-        for (int at = 0; found; at += rows, found >>= 4)
-          if (found & 1u) on |= one << at;
-      }
-      const int rest = n - (asked * kDecWarps + warp) * kChunk;
-      if (rest < kChunk) on &= (Keys{1} << rest) - 1;
-      if (lane < pieces) {
-        const uint32_t bar = bars + ask * 8;
-        mbar_arrive_expect_tx(bar, page >= 0 ? piece_b : 0);
-        if (page >= 0) bulk_g2s(dst + ask * kStage, base + page * page_b + (pos & page_mask) * row_b, piece_b, bar);
-      }
-      if (++ask == kStages) ask = 0;
-      ++asked;
-      pos += kBlock;
-      find();
-      return on;
-    };
-    fence_async();  // (what was read and written here before, by this and by other warps ahead of the barrier)
-    find();
-    Keys coming[kStages - 1] = {};  // the keys of the chunks under way
-    if (!aborted(sh)) {
-#pragma unroll
-      for (int st = 0; st < kStages - 1; ++st)
-        if (asked < last) coming[st] = load();
-    }
+    const int h0 = hk * a.G + hg * kRows, nrow = min(kRows, a.G - hg * kRows);
 
     // ---- q: each head's column in fp16, scaled by a power of two so that its largest
     // value lies in [2^14, 2^15); what is below 2^-39 of that is lost ----
@@ -454,13 +479,13 @@ struct Q4Unit {
       }
     };
 
-    for (int blk = blk0; blk < last; ++blk) {
+    for (int chunk = part.first; chunk < part.last; chunk += part.step) {
       if (!__all_sync(0xffffffffu, mbar_wait_bounded(bars + take * 8, phase >> take & 1u, &sh.abort, a.err, a.timeout_ns)))
         break;
       const Keys on = coming[0];
 #pragma unroll
       for (int st = 1; st < kStages - 1; ++st) coming[st - 1] = coming[st];
-      if (asked < last) coming[kStages - 2] = load();  // into the stage that the last step read
+      if (asked < last) coming[kStages - 2] = load(a, n, smem, sh);  // into the stage that the last step read
       const int stage = take * kStage;
       const bool part = on != ~Keys{0};
       if (part) {  // rows that hold no key may hold anything: their scales become 0, and no result depends on them
@@ -547,7 +572,7 @@ struct Q4Unit {
         }
       }
       if (a.slopes) {
-        const float dist = static_cast<float>(n - 1 - (blk * kDecWarps + warp) * kChunk - kr);
+        const float dist = static_cast<float>(n - 1 - chunk * kChunk - kr);
 #pragma unroll
         for (int t = 0; t < kT; ++t)
 #pragma unroll
@@ -697,6 +722,8 @@ struct Q4Unit {
       if (++take == kStages) take = 0;
       __syncwarp();
     }
+    if constexpr (kAhead)
+      if (following) start(a, *following, smem, sh);
     if (aborted(sh)) {  // copies under way land before the buffers change hands; nothing is asked for any more
       while (take != ask) {
         mbar_drain(bars + take * 8, phase >> take & 1u, a.timeout_ns);
@@ -707,7 +734,8 @@ struct Q4Unit {
     }
 
     // ---- this warp's state into its buffers ----
-    float* w = reinterpret_cast<float*>(wbuf);
+    // (not where the next copies go)
+    float* const w = reinterpret_cast<float*>(wbuf + (kAhead && following && take == 0 ? kStage : 0));
     const float unit = power_of_2(top - 141), codes = kF32 ? 1.f : 0x1p24f;
 #pragma unroll
     for (int x = 0; x < kTiles; ++x) {
@@ -744,6 +772,7 @@ struct Q4Unit {
       keep(x * 8 + 2 * tq + 1, m[x].y, l[x].y, zy, [](float2 v) { return v.y; });
     }
     fence_async();
+    return w;
   }
 
   // Pages that a chunk meets.
@@ -762,13 +791,174 @@ struct Q4Unit {
   }
 };
 
+// The list: all units' chunks, cut into equal contiguous ranges, one per warp. A warp
+// waits for no other: units within its range it writes out, the one that began before
+// and the one that goes on it leaves as partials, for the join.
+template <class U>
+__global__ void __launch_bounds__(kDecThreads, U::kPerSm) q4_decode_kernel(const __grid_constant__ PagedArgs a) {
+  constexpr int D = U::kD;
+  extern __shared__ __align__(128) uint8_t smem[];
+  int* cum = reinterpret_cast<int*>(smem + U::kSmem);  // [B + 1]: chunks before sequence b
+  __shared__ int wsum[kDecWarps];
+  __shared__ typename U::Shared shared;
+  U unit(a, smem, shared);
+  grid_wait();
+  const int groups = (a.G + U::kRows - 1) / U::kRows, HG = a.Hkv * groups;
+  const int total = work_list<U::kBlock>(a, HG, cum, wsum);
+  grid_release();  // the join's CTAs take their places as these leave
+  no_tokens<D>(a, cum);
+  // (each warp that takes part has a chunk at least, so that a unit's partials lie with neighbours)
+  const int worker = blockIdx.x * kDecWarps + (threadIdx.x >> 5), workers = min(static_cast<int>(gridDim.x) * kDecWarps, total);
+  const int lane = threadIdx.x & 31;
+  if (worker >= workers) return;
+  const int begin = static_cast<int>(static_cast<int64_t>(total) * worker / workers);
+  const int end = static_cast<int>(static_cast<int64_t>(total) * (worker + 1) / workers);
+  int b = sequence_of(a, cum, begin), u = 0, nblk = 0;  // the unit within its sequence, and its chunks
+  auto place = [&](int at) {
+    while (cum[b + 1] <= at) ++b;
+    const int n = min(max(a.seq_lens[b], 0), table_len(a));
+    nblk = (n + U::kBlock - 1) / U::kBlock;
+    u = (at - cum[b]) / nblk;
+    const int first = (at - cum[b]) - u * nblk, hk = u / groups;
+    return Part{b, n, hk, u - hk * groups, first, min(nblk, first + end - at), 1};
+  };
+  const int width = min(U::kRows, a.G);  // heads of a partial: O, then m and l
+  Part p = place(begin);
+  unit.start(a, p, smem, shared);
+  for (int at = begin; at < end;) {
+    const int64_t info = static_cast<int64_t>(p.b) * HG + u;
+    const int h0 = p.hk * a.G + p.hg * U::kRows, nrow = min(U::kRows, a.G - p.hg * U::kRows);
+    const int unit0 = at - p.first, unit1 = unit0 + nblk;  // the unit's chunks in the list
+    const bool whole = at == unit0 && at + p.last - p.first == unit1;
+    const int next = at + p.last - p.first, slot = at == begin ? 0 : 1;
+    Part q = p;
+    if (next < end) q = place(next);
+    const float* w = unit.take_part(a, p, next < end ? &q : nullptr, smem, shared);
+    __syncwarp();
+    if (whole) {
+      const int64_t row0 = static_cast<int64_t>(p.b) * a.H + h0;
+      for (int i = lane; i < nrow * D; i += 32) {
+        const float sum = w[U::kRows * D + 2 * (i / D) + 1];
+        put_out(a, row0 * D + i, sum != 0.f ? w[i] / sum : 0.f);
+      }
+      if (lane < nrow) a.lse[row0 + lane] = natural_lse(w[U::kRows * D + 2 * lane], w[U::kRows * D + 2 * lane + 1]);
+    } else {
+      float* part = a.partial + (static_cast<int64_t>(worker) * 2 + slot) * width * (D + 2);
+      for (int i = 2 * lane; i < nrow * D; i += 64)  // (D + 2 floats a head: 8-byte alignment)
+        *reinterpret_cast<float2*>(part + i) = *reinterpret_cast<const float2*>(w + i);
+      for (int i = lane; i < 2 * nrow; i += 32) part[width * D + i] = w[U::kRows * D + i];
+    }
+    // the warp that begins a unit says which partials make it up; a chunk x lies with warp ((x + 1) workers - 1) / total
+    if (lane == 0 && at == unit0)
+      a.info[info] = whole ? make_int2(0, -1)
+                           : make_int2(worker * 2 + slot, static_cast<int>((static_cast<int64_t>(unit1) * workers - 1) / total));
+    __syncwarp();
+    if constexpr (!U::kAhead)
+      if (next < end) unit.start(a, q, smem, shared);
+    p = q;
+    at = next;
+  }
+}
+
+// Joins the partials of a unit that lay with more than one warp: the first in the slot
+// that info names, the others in slot 0 of the warps up to info.y. kSplit warps a query
+// head take its partials in turn, with a running maximum each, eight under way at once,
+// and meet at the end: three loads one after the other in all. Many warps a head where a
+// unit has many partials, one where it has few (48 ragged sequences of 24 heads, four
+// partials a unit: the call 49.5 us with eight, 46.4 with four).
+template <int D, int kSplit>
+__global__ void __launch_bounds__(kSplit == 1 ? 128 : kSplit * 32) q4_join_kernel(const __grid_constant__ PagedArgs a, int rows) {
+  constexpr int kLane = D / 32, kFlight = 8;
+  __shared__ float acc[kSplit][D], stat[kSplit][2];
+  const int warp = kSplit == 1 ? 0 : threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int h = kSplit == 1 ? blockIdx.x * 4 + (threadIdx.x >> 5) : blockIdx.x, b = blockIdx.y;
+  if (h >= a.H) return;  // (a warp a head: whole warps)
+  const int groups = (a.G + rows - 1) / rows, width = min(rows, a.G), slot_floats = width * (D + 2);
+  const int hk = h / a.G, r = (h - hk * a.G) % rows, hg = (h - hk * a.G) / rows;
+  grid_wait();
+  const int tokens = a.seq_lens[b];
+  const int2 w = a.info[(static_cast<int64_t>(b) * a.Hkv + hk) * groups + hg];  // (of no use where there are no tokens)
+  if (min(tokens, table_len(a)) <= 0 || w.y < 0) return;
+  const int c0 = w.x >> 1, n = w.y - c0 + 1;
+  float m = -INFINITY, l = 0.f, o[kLane] = {};
+  for (int i = warp; i < n; i += kSplit * kFlight) {
+    float2 ml[kFlight];
+    float x[kFlight][kLane];
+#pragma unroll
+    for (int u = 0; u < kFlight; ++u) {
+      const int at = i + u * kSplit;
+      ml[u] = make_float2(-INFINITY, 0.f);
+      if (at < n) {
+        const float* p = a.partial + (static_cast<int64_t>(c0 + at) * 2 + (at == 0 ? w.x & 1 : 0)) * slot_floats;
+        ml[u] = *reinterpret_cast<const float2*>(p + width * D + 2 * r);
+#pragma unroll
+        for (int c = 0; c < kLane; c += 2)
+          *reinterpret_cast<float2*>(&x[u][c]) = *reinterpret_cast<const float2*>(p + r * D + lane * kLane + c);
+      }
+    }
+    float now = m;
+#pragma unroll
+    for (int u = 0; u < kFlight; ++u) now = fmaxf(now, ml[u].x);
+    const float base = now == -INFINITY ? 0.f : now, f = exp2f(m - base);
+    m = now;
+    l *= f;
+#pragma unroll
+    for (int c = 0; c < kLane; ++c) o[c] *= f;
+#pragma unroll
+    for (int u = 0; u < kFlight; ++u) {
+      if (i + u * kSplit >= n) break;
+      const float g = exp2f(ml[u].x - base);
+      l = fmaf(ml[u].y, g, l);
+#pragma unroll
+      for (int c = 0; c < kLane; ++c) o[c] = fmaf(x[u][c], g, o[c]);
+    }
+  }
+  const int64_t row = static_cast<int64_t>(b) * a.H + h;
+  if constexpr (kSplit == 1) {
+#pragma unroll
+    for (int c = 0; c < kLane; ++c) put_out(a, row * D + lane * kLane + c, l != 0.f ? o[c] / l : 0.f);
+    if (lane == 0) a.lse[row] = natural_lse(m, l);
+    return;
+  }
+#pragma unroll
+  for (int c = 0; c < kLane; ++c) acc[warp][lane * kLane + c] = o[c];
+  if (lane == 0) {
+    stat[warp][0] = m;
+    stat[warp][1] = l;
+  }
+  __syncthreads();
+  if (threadIdx.x >= D) return;
+  float mx = -INFINITY, sum = 0.f, x = 0.f;
+#pragma unroll
+  for (int i = 0; i < kSplit; ++i) mx = fmaxf(mx, stat[i][0]);
+  const float base = mx == -INFINITY ? 0.f : mx;
+#pragma unroll
+  for (int i = 0; i < kSplit; ++i) {
+    const float g = exp2f(stat[i][0] - base);
+    sum = fmaf(stat[i][1], g, sum);
+    x = fmaf(acc[i][threadIdx.x], g, x);
+  }
+  put_out(a, row * D + threadIdx.x, sum != 0.f ? x / sum : 0.f);
+  if (threadIdx.x == 0) a.lse[row] = natural_lse(mx, sum);
+}
+
 template <int D, bool kF32, int kTiles>
 cudaError_t decode_q4(const PagedArgs& a, cudaStream_t s) {
   using Few = Q4Unit<D, kF32, kTiles, kQ4FewKeys>;
-  using Many = Q4Unit<D, kF32, kTiles, q4_chunk(!kF32, 8 * kTiles)>;
   const int cs = q4_cluster(!kF32, a.B, a.Hkv, a.G, a.max_pages, a.page_shift);
   if (cs > 0) return launch_clustered<Few>(a, cs, s);
-  return launch_listed<Many>(a, q4_ctas(!kF32, Many::kRows, Many::kSmem + (a.B + 1) * 4, a.sms), s);
+  using U = Q4Unit<D, kF32, kTiles, q4_chunk(!kF32, 8 * kTiles)>;
+  const int smem = U::kSmem + (a.B + 1) * 4;
+  static_assert(U::kSmem + (kPagedMaxBatch + 8) * 4 <= 227 * 1024, "shared memory budget");
+  cudaError_t e;
+  if ((e = allow_smem<q4_decode_kernel<U>>(U::kSmem + (kPagedMaxBatch + 1) * 4)) != cudaSuccess) return e;
+  const int ctas = q4_ctas(!kF32, U::kRows, smem, a.sms), rows = U::kRows;
+  e = launch_clusters(q4_decode_kernel<U>, ctas, 1, 1, 1, kDecThreads, smem, true, s, a);
+  if (e != cudaSuccess) return e;
+  const int64_t units = static_cast<int64_t>(a.B) * a.Hkv * ((a.G + rows - 1) / rows), partials = ctas * kDecWarps / units;
+  if (partials <= 8) return launch_clusters(q4_join_kernel<D, 1>, (a.H + 3) / 4, a.B, 1, 1, 128, 0, true, s, a, rows);
+  if (partials <= 32) return launch_clusters(q4_join_kernel<D, 4>, a.H, a.B, 1, 1, 128, 0, true, s, a, rows);
+  return launch_clusters(q4_join_kernel<D, 16>, a.H, a.B, 1, 1, 512, 0, true, s, a, rows);
 }
 
 template <typename... P>
