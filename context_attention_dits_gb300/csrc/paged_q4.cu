@@ -50,14 +50,14 @@ __device__ __forceinline__ int64_t head_row(const PagedArgs& a, int page, int po
 // ----------------------------------------------------------------------------
 constexpr int kRowThreads = 256;
 
-__device__ __forceinline__ float max_nan(float a, float b) {
+__device__ __forceinline__ float max_nan(float a, float b, float c) {
   float y;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
   return y;
 }
-__device__ __forceinline__ float min_nan(float a, float b) {
+__device__ __forceinline__ float min_nan(float a, float b, float c) {
   float y;
-  asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
   return y;
 }
 
@@ -69,56 +69,74 @@ __device__ __forceinline__ void exact_diff(float a, float b, float& h, float& l)
 }
 
 // This lane's 8 codes (value i in bits 4 i) and its group's scale and offset (bf16,
-// scale in the lower half), from the 8 lanes that share the group.
+// scale in the lower half), from the 8 lanes that share the group. kB16: the values
+// are bf16 numbers. Everything is decided exactly, by candidates from approximate
+// quotients that are never too large and a comparison that raises them.
+template <bool kB16>
 __device__ __forceinline__ uint32_t quantise(const float (&x)[8], uint32_t& scale) {
-  float least = x[0], most = x[0];
-#pragma unroll
-  for (int i = 1; i < 8; ++i) {
-    least = min_nan(least, x[i]);
-    most = max_nan(most, x[i]);
-  }
+  float least = min_nan(min_nan(x[0], x[1], x[2]), x[3], x[4]), most = max_nan(max_nan(x[0], x[1], x[2]), x[3], x[4]);
+  least = min_nan(min_nan(least, x[5], x[6]), x[7], x[7]);
+  most = max_nan(max_nan(most, x[5], x[6]), x[7], x[7]);
 #pragma unroll
   for (int o = 1; o < 8; o <<= 1) {
-    least = min_nan(least, __shfl_xor_sync(0xffffffffu, least, o));
-    most = max_nan(most, __shfl_xor_sync(0xffffffffu, most, o));
+    const float a = __shfl_xor_sync(0xffffffffu, least, o), b = __shfl_xor_sync(0xffffffffu, most, o);
+    least = min_nan(least, a, a);
+    most = max_nan(most, b, b);
   }
-  const uint32_t lb = __float_as_uint(least), low = lb & 0xffffu;
-  const float z = __uint_as_float(lb - low + (low && lb >> 31 ? 0x10000u : 0u));
+  float z = least;
+  if constexpr (!kB16) {
+    const uint32_t lb = __float_as_uint(least), low = lb & 0xffffu;
+    z = __uint_as_float(lb - low + (low && lb >> 31 ? 0x10000u : 0u));
+  }
   float h, l;
   exact_diff(most, z, h, l);
   if (!(fabsf(h) <= FLT_MAX)) {  // a value that is not finite, or a span that fp32 does not hold
     scale = 0x7fff7fffu;         // reads back as NaN
     return 0;
   }
-  float s = __uint_as_float(__float_as_uint(__fdiv_rn(h, 15.f)) & 0xffff0000u);
-  if (__fsub_rn(15.f * s, h) < l) s = __uint_as_float(__float_as_uint(s) + 0x10000u);  // both sides exact
-  s = fmaxf(s, 0x1p-100f);
+  // s: upper bits of a quotient that is at most 2^-19 of itself too small, so two steps up at most
+  uint32_t sb = __float_as_uint(h * (1.f / 15 * (1 - 0x1p-20f))) & 0xffff0000u;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    if (__fsub_rn(15.f * __uint_as_float(sb), h) < l) sb += 0x10000u;  // both sides exact
+  const float s = fmaxf(__uint_as_float(sb), 0x1p-100f);
   scale = __float_as_uint(s) >> 16 | __float_as_uint(z);
-  // The nearest integer, by a sum whose unit is 1: right unless the quotient, off by
-  // 2^-19 at most, is next to a border.
+  // c: the integer nearest to a quotient that is at most 15 2^-18 too small (by a sum
+  // whose unit is 1), raised where the value lies half a step above it or more
   constexpr float kOne = 12582912.f;  // 1.5 2^23
-  const float rs = __frcp_rn(s);
+  const float2 rs = twice(rcp_approx(s) * (1 - 0x1p-20f)), down = twice(-s), zz = twice(-z);
+  const float half = 0.5f * s;
+  float2 d[4];
+  bool exact = kB16;
+  if constexpr (kB16) {
+    // Differences of 8-bit numbers are exact while none is 2^15 times another (or an
+    // offset 0); seldom otherwise, and zeros then count as otherwise too.
+    float small = fabsf(x[0]);
+#pragma unroll
+    for (int i = 1; i < 8; ++i) small = fminf(small, fabsf(x[i]));
+    const float large = fmaxf(fabsf(least), fabsf(most)) * 0x1p-14f;
+    exact = z == 0.f || fminf(small, fabsf(z)) >= large;
+  }
   uint32_t codes = 0;
-  float far = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float d = __fsub_rn(x[i], z), g = fmaf(d, rs, kOne);
-    far = fmaxf(far, fabsf(fmaf(d, rs, -__fsub_rn(g, kOne))));
-    codes += __float_as_uint(g) << (4 * i);
-  }
-  codes -= 0x3f400000u;  // what the eight copies of kOne's bits, 0x4b400000, come to in 32 bits
-  if (far > 0.5f - 0x1p-17f) {
-    codes = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      exact_diff(x[i], z, h, l);
-      int n = static_cast<int>(fminf(fmaf(h, rs, 0.5f), 15.f));
-      if (n > 0 && __fadd_rn(__fsub_rn(h, (n - 0.5f) * s), l) < 0.f) --n;
-      else if (n < 15 && __fadd_rn(__fsub_rn(h, (n + 0.5f) * s), l) >= 0.f) ++n;
-      codes |= static_cast<uint32_t>(n) << (4 * i);
+  for (int i = 0; i < 4; ++i) {
+    d[i] = add2(make_float2(x[2 * i], x[2 * i + 1]), zz);
+    float2 g = fma2(d[i], rs, twice(kOne));
+    const float2 r = fma2(add2(g, twice(-kOne)), down, d[i]);  // exact: d - c s, within a step
+    if (exact) {
+      if (r.x >= half) g.x += 1.f;
+      if (r.y >= half) g.y += 1.f;
+    } else {  // what the difference has lost decides where the rest is half a step
+      float lx, ly;
+      exact_diff(x[2 * i], z, h, lx);
+      exact_diff(x[2 * i + 1], z, h, ly);
+      if (__fadd_rn(__fsub_rn(r.x, half), lx) >= 0.f) g.x += 1.f;
+      if (__fadd_rn(__fsub_rn(r.y, half), ly) >= 0.f) g.y += 1.f;
     }
+    codes += __float_as_uint(g.x) << (8 * i);
+    codes += __float_as_uint(g.y) << (8 * i + 4);
   }
-  return codes;
+  return codes - 0x3f400000u;  // what the eight copies of kOne's bits, 0x4b400000, come to in 32 bits
 }
 
 // Rows (token, head) of sequence blockIdx.y: a warp takes 256 / D of them.
@@ -147,7 +165,8 @@ __global__ void __launch_bounds__(kRowThreads) q4_append_kernel(const __grid_con
       page = page_of(a, b, static_cast<int>(pos));
   }
   uint32_t ks, vs;
-  const uint32_t kc = quantise(k, ks), vc = quantise(v, vs);
+  constexpr bool kB16 = sizeof(T) == 2;
+  const uint32_t kc = quantise<kB16>(k, ks), vc = quantise<kB16>(v, vs);
   if (page < 0) return;
   const int64_t dst = head_row(a, page, static_cast<int>(pos), hk);
   static_cast<uint32_t*>(a.k_cache)[dst * kLanes + l] = kc;
@@ -158,11 +177,19 @@ __global__ void __launch_bounds__(kRowThreads) q4_append_kernel(const __grid_con
   }
 }
 
-// Eight codes as values.
+// Eight codes as values: code i of a half word, in its place within the mantissa of
+// 2^23, is 16^i times itself.
 __device__ __forceinline__ void values8(uint32_t codes, uint32_t scale, float (&x)[8]) {
-  const float s = __uint_as_float(scale << 16), z = __uint_as_float(scale & 0xffff0000u);
+  const float s = __uint_as_float(scale << 16);
+  const float2 z = twice(__uint_as_float(scale & 0xffff0000u)), one = twice(-0x1p23f);
+  const float2 s01 = make_float2(s, s * 0x1p-4f), s23 = make_float2(s * 0x1p-8f, s * 0x1p-12f);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = fmaf(s, static_cast<float>(codes >> (4 * i) & 15u), z);
+  for (int i = 0; i < 2; ++i, codes >>= 16) {
+    auto at = [&](uint32_t mask) { return __uint_as_float((codes & mask) | 0x4b000000u); };
+    const float2 a = fma2(s01, add2(make_float2(at(0xfu), at(0xf0u)), one), z);
+    const float2 b = fma2(s23, add2(make_float2(at(0xf00u), at(0xf000u)), one), z);
+    x[4 * i] = a.x, x[4 * i + 1] = a.y, x[4 * i + 2] = b.x, x[4 * i + 3] = b.y;
+  }
 }
 
 // Rows (token, head) of sequence blockIdx.y: a warp takes kAhead times 256 / D, all
