@@ -52,6 +52,7 @@ cp_status take_cache(PagedArgs* a, const cp_q4_cache* c, int B, int Hkv, int D, 
   a->v_cache = c->v_codes;
   a->v_scales = c->v_scales;
   a->timeout_ns = kWaitTimeoutNs;
+  cp::divide_by(Hkv, &a->hkv_mul, &a->hkv_shift);
   return CP_OK;
 }
 
@@ -72,7 +73,8 @@ cp_status cp_paged_kv_append_q4(const void* k_new, const void* v_new, const cp_q
   PagedArgs a;
   cp_status st = take_cache(&a, cache, B, Hkv, D, dt, B > 0 && T > 0);
   if (st != CP_OK) return st;
-  if (T < 0 || static_cast<int64_t>(B) * T > INT_MAX) return CP_ERR_INVALID_ARG;
+  if (T < 0 || static_cast<int64_t>(B) * T > INT_MAX || static_cast<int64_t>(T) * Hkv > INT_MAX - 65536)
+    return CP_ERR_INVALID_ARG;
   if (B == 0 || T == 0) return CP_OK;
   if (!k_new || !v_new || !seq_lens) return CP_ERR_INVALID_ARG;
   if (!aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(seq_lens, 4) || !aligned(new_lens, 4)) return CP_ERR_ALIGNMENT;
@@ -90,7 +92,8 @@ cp_status cp_paged_kv_read_q4(const cp_q4_cache* cache, const int32_t* seq_lens,
   PagedArgs a;
   cp_status st = take_cache(&a, cache, B, Hkv, D, out_dt, B > 0 && T > 0);
   if (st != CP_OK) return st;
-  if (T < 0 || static_cast<int64_t>(B) * T > INT_MAX) return CP_ERR_INVALID_ARG;
+  if (T < 0 || static_cast<int64_t>(B) * T > INT_MAX || static_cast<int64_t>(T) * Hkv > INT_MAX - 65536)
+    return CP_ERR_INVALID_ARG;
   if (B == 0 || T == 0) return CP_OK;
   if (!k_out || !v_out || !seq_lens) return CP_ERR_INVALID_ARG;
   if (!aligned(k_out, 16) || !aligned(v_out, 16) || !aligned(seq_lens, 4)) return CP_ERR_ALIGNMENT;

@@ -106,7 +106,10 @@ struct PagedArgs {
   int2* info;      // workspace: [B * Hkv * groups] which partials make up a unit
   int sms;         // multiprocessors of the device
   uint32_t* err;
-  uint64_t timeout_ns;  // in 4 bits: bound on each wait
+  // in 4 bits
+  uint64_t timeout_ns;  // bound on each wait
+  uint32_t hkv_mul;     // x / Hkv is the upper word of x hkv_mul, hkv_shift bits less, for x < 2^31
+  int hkv_shift;
 };
 // Query heads that share a key/value head are taken this many at a time.
 constexpr int paged_rows(bool bf16) { return bf16 ? 16 : 8; }
@@ -172,6 +175,14 @@ inline int q4_cluster(bool bf16, int B, int Hkv, int G, int max_pages, int page_
   int cs = 1;
   while (cs < most && blocks > cs && units * cs * 2 <= ctas) cs *= 2;
   return units <= ctas && blocks <= cs * 4 ? cs : 0;
+}
+// Division by d (1 .. 65535) of numbers below 2^31: with 2^s >= d > 2^(s - 1), mul is
+// 2^(31 + s) / d rounded up, off by less than 1, which n < 2^31 makes less than 1 / d.
+inline void divide_by(int d, uint32_t* mul, int* shift) {
+  int s = 0;
+  while ((1 << s) < d) ++s;
+  *mul = static_cast<uint32_t>((uint64_t{1} << (31 + s)) / d + (d & (d - 1) ? 1 : 0));
+  *shift = s - 1;  // (d = 1: -1, and mul 2^31)
 }
 cudaError_t launch_q4_append(const PagedArgs& a, bool bf16, cudaStream_t s);
 cudaError_t launch_q4_read(const PagedArgs& a, bool bf16, cudaStream_t s);

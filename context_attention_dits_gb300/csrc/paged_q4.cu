@@ -61,6 +61,12 @@ __device__ __forceinline__ float min_nan(float a, float b, float c) {
   return y;
 }
 
+__device__ __forceinline__ float fmin3(float a, float b, float c) {
+  float y;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+
 // a - b = h + l exactly.
 __device__ __forceinline__ void exact_diff(float a, float b, float& h, float& l) {
   h = __fsub_rn(a, b);
@@ -111,11 +117,10 @@ __device__ __forceinline__ uint32_t quantise(const float (&x)[8], uint32_t& scal
   if constexpr (kB16) {
     // Differences of 8-bit numbers are exact while none is 2^15 times another (or an
     // offset 0); seldom otherwise, and zeros then count as otherwise too.
-    float small = fabsf(x[0]);
-#pragma unroll
-    for (int i = 1; i < 8; ++i) small = fminf(small, fabsf(x[i]));
+    float small = fmin3(fmin3(fabsf(x[0]), fabsf(x[1]), fabsf(x[2])), fabsf(x[3]), fabsf(x[4]));
+    small = fmin3(fmin3(small, fabsf(x[5]), fabsf(x[6])), fabsf(x[7]), fabsf(z));
     const float large = fmaxf(fabsf(least), fabsf(most)) * 0x1p-14f;
-    exact = z == 0.f || fminf(small, fabsf(z)) >= large;
+    exact = z == 0.f || small >= large;
   }
   uint32_t codes = 0;
 #pragma unroll
@@ -139,20 +144,28 @@ __device__ __forceinline__ uint32_t quantise(const float (&x)[8], uint32_t& scal
   return codes - 0x3f400000u;  // what the eight copies of kOne's bits, 0x4b400000, come to in 32 bits
 }
 
+// Token and head of a row (row < 2^31).
+__device__ __forceinline__ void token_head(const PagedArgs& a, int row, int& t, int& hk) {
+  const uint64_t wide = static_cast<uint64_t>(static_cast<uint32_t>(row)) * a.hkv_mul;
+  t = static_cast<int>(wide >> (32 + a.hkv_shift));
+  hk = row - t * a.Hkv;
+}
+
 // Rows (token, head) of sequence blockIdx.y: a warp takes 256 / D of them.
 template <int D, typename T>
 __global__ void __launch_bounds__(kRowThreads) q4_append_kernel(const __grid_constant__ PagedArgs a) {
   constexpr int kLanes = D / 8;
   const int b = blockIdx.y, l = threadIdx.x % kLanes;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * (kRowThreads / kLanes) + threadIdx.x / kLanes;
-  const int64_t most = static_cast<int64_t>(a.T) * a.Hkv;
+  const int row = blockIdx.x * (kRowThreads / kLanes) + threadIdx.x / kLanes, most = a.T * a.Hkv;
   const bool in = row < most;  // (lanes stay for the shuffles)
-  const int t = static_cast<int>((in ? row : 0) / a.Hkv), hk = static_cast<int>((in ? row : 0) - static_cast<int64_t>(t) * a.Hkv);
+  int t, hk;
+  token_head(a, in ? row : 0, t, hk);
   const int n = a.seq_lens[b];
   const bool live = in && !(a.new_lens && t >= a.new_lens[b]);
+  if (!__any_sync(0xffffffffu, live)) return;  // padding
   float k[8] = {}, v[8] = {};
   if (live) {  // on their way before the row's place is looked up
-    const int64_t at = (static_cast<int64_t>(b) * most + row) * D + l * 8;
+    const int64_t at = (static_cast<int64_t>(b) * most + row) * * D + l * 8;
     load8(static_cast<const T*>(a.k_new) + at, k);
     load8(static_cast<const T*>(a.v_new) + at, v);
   }
@@ -198,16 +211,16 @@ template <int D, typename T>
 __global__ void __launch_bounds__(kRowThreads) q4_read_kernel(const __grid_constant__ PagedArgs a) {
   constexpr int kLanes = D / 8, kAhead = 4, kRows = kRowThreads / kLanes;
   const int b = blockIdx.y, l = threadIdx.x % kLanes;
-  const int64_t most = static_cast<int64_t>(a.T) * a.Hkv;
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * (kRows * kAhead) + threadIdx.x / kLanes;
+  const int most = a.T * a.Hkv, first = blockIdx.x * (kRows * kAhead) + threadIdx.x / kLanes;
   const int n = seq_len(a, b);
   uint32_t kc[kAhead], vc[kAhead], ks[kAhead], vs[kAhead];
 #pragma unroll
   for (int i = 0; i < kAhead; ++i) {
-    const int64_t row = first + i * kRows;
+    const int row = first + i * kRows;
     kc[i] = vc[i] = ks[i] = vs[i] = 0;
     if (row >= most) continue;
-    const int t = static_cast<int>(row / a.Hkv), hk = static_cast<int>(row - static_cast<int64_t>(t) * a.Hkv);
+    int t, hk;
+    token_head(a, row, t, hk);
     const int page = t < n ? page_of(a, b, t) : -1;
     if (page < 0) continue;
     const int64_t src = head_row(a, page, t, hk);
@@ -218,7 +231,7 @@ __global__ void __launch_bounds__(kRowThreads) q4_read_kernel(const __grid_const
   }
 #pragma unroll
   for (int i = 0; i < kAhead; ++i) {
-    const int64_t row = first + i * kRows;
+    const int row = first + i * kRows;
     if (row >= most) break;
     const int64_t at = (static_cast<int64_t>(b) * most + row) * D + l * 8;
     float x[8];
@@ -990,10 +1003,8 @@ cudaError_t decode_q4(const PagedArgs& a, cudaStream_t s) {
 
 template <typename... P>
 cudaError_t launch_rows(void (*kernel)(P...), const PagedArgs& a, int rows_per_cta, cudaStream_t s) {
-  const int64_t rows = static_cast<int64_t>(a.T) * a.Hkv;
-  const int64_t ctas = (rows + rows_per_cta - 1) / rows_per_cta;
-  if (ctas > INT_MAX) return cudaErrorInvalidValue;
-  kernel<<<dim3(static_cast<unsigned>(ctas), a.B), kRowThreads, 0, s>>>(a);
+  const int64_t rows = static_cast<int64_t>(a.T) * a.Hkv;  // below 2^31
+  kernel<<<dim3(static_cast<unsigned>((rows + rows_per_cta - 1) / rows_per_cta), a.B), kRowThreads, 0, s>>>(a);
   return cudaGetLastError();
 }
 

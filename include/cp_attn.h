@@ -597,7 +597,7 @@ typedef struct {
 
 /*
  * Writes new tokens' rows: as cp_paged_kv_append, k_new, v_new [B, T, Hkv, D] (dt,
- * dense). Every other row keeps its bytes. Errors: INVALID_ARG, ALIGNMENT, CUDA,
+ * dense; T * Hkv below 2^31 - 65536). Every other row keeps its bytes. Errors: INVALID_ARG, ALIGNMENT, CUDA,
  * UNSUPPORTED_DEVICE.
  */
 cp_status cp_paged_kv_append_q4(const void* k_new, const void* v_new, const cp_q4_cache* cache, const int32_t* seq_lens,

@@ -55,6 +55,7 @@ def test_append_and_read_tensors():
     for call in (append, read):
         assert call(k=0) == BAD and call(v=0) == BAD and call(k=P + 8) == ALIGN and call(v=P + 4) == ALIGN
         assert call(T=-1) == BAD and call(T=0) == 0 and call(B=4096, T=1 << 20) == BAD
+        assert call(B=1, T=1 << 20, Hkv=2048) == BAD
     assert append(new=P + 1) == ALIGN
     assert _lib.lib().cp_paged_kv_append_q4(P, P, None, P, None, 1, 1, 1, 64, 0, None) == BAD
 
@@ -109,6 +110,13 @@ int main(int argc, char** argv) {
           // powers of two up to 16, all at once on the device, a few blocks each
           if (cs < 0 || cs > 16 || (cs & (cs - 1)) || (cs && (units * cs > 608 || blocks > 8ll * cs))) return 1;
         }
+  for (int d = 1; d <= 65535; d += d < 300 ? 1 : 331) {
+    uint32_t mul;
+    int shift;
+    cp::divide_by(d, &mul, &shift);
+    for (long long n : {0ll, 1ll, d - 1ll, 1ll * d, 12345ll * d - 1, (0x7fffffffll / d) * d - 1, (0x7fffffffll / d) * d, 0x7fffffffll})
+      if (n >= 0 && n <= 0x7fffffffll && static_cast<long long>((static_cast<unsigned long long>(n) * mul) >> (32 + shift)) != n / d) return 2;
+  }
   return 0;
 }
 """
