@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(kRowThreads) q4_append_kernel(const __grid_con
   if (!__any_sync(0xffffffffu, live)) return;  // padding
   float k[8] = {}, v[8] = {};
   if (live) {  // on their way before the row's place is looked up
-    const int64_t at = (static_cast<int64_t>(b) * most + row) * * D + l * 8;
+    const int64_t at = (static_cast<int64_t>(b) * most + row) * D + l * 8;
     load8(static_cast<const T*>(a.k_new) + at, k);
     load8(static_cast<const T*>(a.v_new) + at, v);
   }
