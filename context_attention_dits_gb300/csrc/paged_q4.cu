@@ -45,8 +45,7 @@ __device__ __forceinline__ int64_t head_row(const PagedArgs& a, int page, int po
 }
 
 // ----------------------------------------------------------------------------
-// Append and read. A lane has 8 values of a row, 8 lanes a group: its least and
-// largest value take three shuffles each.
+// Append and read
 // ----------------------------------------------------------------------------
 constexpr int kRowThreads = 256;
 
@@ -74,17 +73,20 @@ __device__ __forceinline__ void exact_diff(float a, float b, float& h, float& l)
   l = __fsub_rn(__fsub_rn(a, __fsub_rn(h, bb)), __fadd_rn(b, bb));
 }
 
-// This lane's 8 codes (value i in bits 4 i) and its group's scale and offset (bf16,
-// scale in the lower half), from the 8 lanes that share the group. kB16: the values
-// are bf16 numbers. Everything is decided exactly, by candidates from approximate
-// quotients that are never too large and a comparison that raises them.
+// This lane's 16 codes (value i of 8 in bits 4 i of a word) and its group's scale and
+// offset (bf16, scale in the lower half), from the 4 lanes that share the group. kB16:
+// the values are bf16 numbers. Everything is decided exactly, by candidates from
+// approximate quotients that are never too large and a comparison that raises them.
 template <bool kB16>
-__device__ __forceinline__ uint32_t quantise(const float (&x)[8], uint32_t& scale) {
-  float least = min_nan(min_nan(x[0], x[1], x[2]), x[3], x[4]), most = max_nan(max_nan(x[0], x[1], x[2]), x[3], x[4]);
-  least = min_nan(min_nan(least, x[5], x[6]), x[7], x[7]);
-  most = max_nan(max_nan(most, x[5], x[6]), x[7], x[7]);
+__device__ __forceinline__ uint2 quantise(const float (&x)[16], uint32_t& scale) {
+  float least = x[0], most = x[0];
 #pragma unroll
-  for (int o = 1; o < 8; o <<= 1) {
+  for (int i = 1; i < 16; i += 2) {
+    least = min_nan(least, x[i], x[(i + 1) & 15]);  // (the last with x[0] again)
+    most = max_nan(most, x[i], x[(i + 1) & 15]);
+  }
+#pragma unroll
+  for (int o = 1; o < 4; o <<= 1) {
     const float a = __shfl_xor_sync(0xffffffffu, least, o), b = __shfl_xor_sync(0xffffffffu, most, o);
     least = min_nan(least, a, a);
     most = max_nan(most, b, b);
@@ -98,7 +100,7 @@ __device__ __forceinline__ uint32_t quantise(const float (&x)[8], uint32_t& scal
   exact_diff(most, z, h, l);
   if (!(fabsf(h) <= FLT_MAX)) {  // a value that is not finite, or a span that fp32 does not hold
     scale = 0x7fff7fffu;         // reads back as NaN
-    return 0;
+    return make_uint2(0, 0);
   }
   // s: upper bits of a quotient that is at most 2^-19 of itself too small, so two steps up at most
   uint32_t sb = __float_as_uint(h * (1.f / 15 * (1 - 0x1p-20f))) & 0xffff0000u;
@@ -112,22 +114,21 @@ __device__ __forceinline__ uint32_t quantise(const float (&x)[8], uint32_t& scal
   constexpr float kOne = 12582912.f;  // 1.5 2^23
   const float2 rs = twice(rcp_approx(s) * (1 - 0x1p-20f)), down = twice(-s), zz = twice(-z);
   const float half = 0.5f * s;
-  float2 d[4];
   bool exact = kB16;
   if constexpr (kB16) {
     // Differences of 8-bit numbers are exact while none is 2^15 times another (or an
     // offset 0); seldom otherwise, and zeros then count as otherwise too.
-    float small = fmin3(fmin3(fabsf(x[0]), fabsf(x[1]), fabsf(x[2])), fabsf(x[3]), fabsf(x[4]));
-    small = fmin3(fmin3(small, fabsf(x[5]), fabsf(x[6])), fabsf(x[7]), fabsf(z));
-    const float large = fmaxf(fabsf(least), fabsf(most)) * 0x1p-14f;
-    exact = z == 0.f || small >= large;
-  }
-  uint32_t codes = 0;
+    float small = fabsf(z);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    d[i] = add2(make_float2(x[2 * i], x[2 * i + 1]), zz);
-    float2 g = fma2(d[i], rs, twice(kOne));
-    const float2 r = fma2(add2(g, twice(-kOne)), down, d[i]);  // exact: d - c s, within a step
+    for (int i = 0; i < 16; i += 2) small = fmin3(small, fabsf(x[i]), fabsf(x[i + 1]));
+    exact = z == 0.f || small >= fmaxf(fabsf(least), fabsf(most)) * 0x1p-14f;
+  }
+  uint32_t codes[2] = {0, 0};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float2 d = add2(make_float2(x[2 * i], x[2 * i + 1]), zz);
+    float2 g = fma2(d, rs, twice(kOne));
+    const float2 r = fma2(add2(g, twice(-kOne)), down, d);  // exact: d - c s, within a step
     if (exact) {
       if (r.x >= half) g.x += 1.f;
       if (r.y >= half) g.y += 1.f;
@@ -138,10 +139,11 @@ __device__ __forceinline__ uint32_t quantise(const float (&x)[8], uint32_t& scal
       if (__fadd_rn(__fsub_rn(r.x, half), lx) >= 0.f) g.x += 1.f;
       if (__fadd_rn(__fsub_rn(r.y, half), ly) >= 0.f) g.y += 1.f;
     }
-    codes += __float_as_uint(g.x) << (8 * i);
-    codes += __float_as_uint(g.y) << (8 * i + 4);
+    codes[i >> 2] += __float_as_uint(g.x) << (8 * (i & 3));
+    codes[i >> 2] += __float_as_uint(g.y) << (8 * (i & 3) + 4);
   }
-  return codes - 0x3f400000u;  // what the eight copies of kOne's bits, 0x4b400000, come to in 32 bits
+  // (the eight copies of kOne's bits, 0x4b400000, come to 0x3f400000 in 32 bits)
+  return make_uint2(codes[0] - 0x3f400000u, codes[1] - 0x3f400000u);
 }
 
 // Token and head of a row (row < 2^31).
@@ -151,10 +153,12 @@ __device__ __forceinline__ void token_head(const PagedArgs& a, int row, int& t, 
   hk = row - t * a.Hkv;
 }
 
-// Rows (token, head) of sequence blockIdx.y: a warp takes 256 / D of them.
+// Rows (token, head) of sequence blockIdx.y: a warp takes 512 / D of them, 16 values a
+// lane. Bound by instructions, so the work that a group takes once is spread over few
+// lanes (8 values a lane: 31.6 us where this takes 26.3).
 template <int D, typename T>
 __global__ void __launch_bounds__(kRowThreads) q4_append_kernel(const __grid_constant__ PagedArgs a) {
-  constexpr int kLanes = D / 8;
+  constexpr int kLanes = D / 16;
   const int b = blockIdx.y, l = threadIdx.x % kLanes;
   const int row = blockIdx.x * (kRowThreads / kLanes) + threadIdx.x / kLanes, most = a.T * a.Hkv;
   const bool in = row < most;  // (lanes stay for the shuffles)
@@ -163,11 +167,21 @@ __global__ void __launch_bounds__(kRowThreads) q4_append_kernel(const __grid_con
   const int n = a.seq_lens[b];
   const bool live = in && !(a.new_lens && t >= a.new_lens[b]);
   if (!__any_sync(0xffffffffu, live)) return;  // padding
-  float k[8] = {}, v[8] = {};
+  float k[16] = {}, v[16] = {};
+  auto load16 = [&](const void* from, float (&x)[16]) {
+    const T* p = static_cast<const T*>(from) + (static_cast<int64_t>(b) * most + row) * D + l * 16;
+    float lo[8], hi[8];
+    load8(p, lo);
+    load8(p + 8, hi);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      x[i] = lo[i];
+      x[8 + i] = hi[i];
+    }
+  };
   if (live) {  // on their way before the row's place is looked up
-    const int64_t at = (static_cast<int64_t>(b) * most + row) * D + l * 8;
-    load8(static_cast<const T*>(a.k_new) + at, k);
-    load8(static_cast<const T*>(a.v_new) + at, v);
+    load16(a.k_new, k);
+    load16(a.v_new, v);
   }
   const uint32_t pos = static_cast<uint32_t>(n) + static_cast<uint32_t>(t);  // (both below 2^31)
   int page = -1;
@@ -177,16 +191,16 @@ __global__ void __launch_bounds__(kRowThreads) q4_append_kernel(const __grid_con
     else
       page = page_of(a, b, static_cast<int>(pos));
   }
-  uint32_t ks, vs;
   constexpr bool kB16 = sizeof(T) == 2;
-  const uint32_t kc = quantise<kB16>(k, ks), vc = quantise<kB16>(v, vs);
+  uint32_t ks, vs;
+  const uint2 kc = quantise<kB16>(k, ks), vc = quantise<kB16>(v, vs);
   if (page < 0) return;
   const int64_t dst = head_row(a, page, static_cast<int>(pos), hk);
-  static_cast<uint32_t*>(a.k_cache)[dst * kLanes + l] = kc;
-  static_cast<uint32_t*>(a.v_cache)[dst * kLanes + l] = vc;
-  if (l % 8 == 0) {
-    static_cast<uint32_t*>(a.k_scales)[dst * (D / kQ4Group) + l / 8] = ks;
-    static_cast<uint32_t*>(a.v_scales)[dst * (D / kQ4Group) + l / 8] = vs;
+  static_cast<uint2*>(a.k_cache)[dst * kLanes + l] = kc;
+  static_cast<uint2*>(a.v_cache)[dst * kLanes + l] = vc;
+  if (l % 4 == 0) {
+    static_cast<uint32_t*>(a.k_scales)[dst * (D / kQ4Group) + l / 4] = ks;
+    static_cast<uint32_t*>(a.v_scales)[dst * (D / kQ4Group) + l / 4] = vs;
   }
 }
 
@@ -1011,7 +1025,7 @@ cudaError_t launch_rows(void (*kernel)(P...), const PagedArgs& a, int rows_per_c
 }  // namespace
 
 cudaError_t launch_q4_append(const PagedArgs& a, bool bf16, cudaStream_t s) {
-  const int rows = kRowThreads / (a.D / 8);
+  const int rows = kRowThreads / (a.D / 16);
   if (a.D == 64)
     return bf16 ? launch_rows(q4_append_kernel<64, __nv_bfloat16>, a, rows, s) : launch_rows(q4_append_kernel<64, float>, a, rows, s);
   return bf16 ? launch_rows(q4_append_kernel<128, __nv_bfloat16>, a, rows, s) : launch_rows(q4_append_kernel<128, float>, a, rows, s);
