@@ -159,6 +159,7 @@ __device__ __forceinline__ void token_head(const PagedArgs& a, int row, int& t, 
 template <int D, typename T>
 __global__ void __launch_bounds__(kRowThreads) q4_append_kernel(const __grid_constant__ PagedArgs a) {
   constexpr int kLanes = D / 16;
+  grid_wait();  // (the launch may start while its predecessor in the stream ends)
   const int b = blockIdx.y, l = threadIdx.x % kLanes;
   const int row = blockIdx.x * (kRowThreads / kLanes) + threadIdx.x / kLanes, most = a.T * a.Hkv;
   const bool in = row < most;  // (lanes stay for the shuffles)
@@ -224,6 +225,7 @@ __device__ __forceinline__ void values8(uint32_t codes, uint32_t scale, float (&
 template <int D, typename T>
 __global__ void __launch_bounds__(kRowThreads) q4_read_kernel(const __grid_constant__ PagedArgs a) {
   constexpr int kLanes = D / 8, kAhead = 4, kRows = kRowThreads / kLanes;
+  grid_wait();
   const int b = blockIdx.y, l = threadIdx.x % kLanes;
   const int most = a.T * a.Hkv, first = blockIdx.x * (kRows * kAhead) + threadIdx.x / kLanes;
   const int n = seq_len(a, b);
@@ -1018,8 +1020,7 @@ cudaError_t decode_q4(const PagedArgs& a, cudaStream_t s) {
 template <typename... P>
 cudaError_t launch_rows(void (*kernel)(P...), const PagedArgs& a, int rows_per_cta, cudaStream_t s) {
   const int64_t rows = static_cast<int64_t>(a.T) * a.Hkv;  // below 2^31
-  kernel<<<dim3(static_cast<unsigned>((rows + rows_per_cta - 1) / rows_per_cta), a.B), kRowThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  return launch_clusters(kernel, (rows + rows_per_cta - 1) / rows_per_cta, a.B, 1, 1, kRowThreads, 0, true, s, a);
 }
 
 }  // namespace

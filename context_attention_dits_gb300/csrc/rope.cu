@@ -28,6 +28,7 @@
 
 #include "cp_ptx.cuh"
 #include "cp_rope.h"
+#include "cp_score.h"
 #include "packed.cuh"
 
 namespace cp {
@@ -257,6 +258,7 @@ template <int D, typename T, bool kNext>
 __global__ void __launch_bounds__(kThreads, kFwdCtas) rope_fwd_kernel(const __grid_constant__ RopeArgs a) {
   using L = Lane<D, T, kNext>;
   constexpr int kAhead = sizeof(T) == 2 ? 4 : 2;  // rows whose loads are under way at once
+  grid_wait();  // (the launch may start while its predecessor in the stream ends)
   const L me(a);
   const Part part(a, L::kRows);
   const RopeRows &in = part.k ? a.k : a.q, &to = part.k ? a.ko : a.qo;
@@ -328,6 +330,7 @@ template <int D, typename T, typename G, bool kNext>
 __global__ void __launch_bounds__(kThreads, kBwdCtas) rope_bwd_kernel(const __grid_constant__ RopeArgs a) {
   using L = Lane<D, T, kNext>;
   constexpr int kAhead = sizeof(T) + sizeof(G) == 4 ? 4 : 2;
+  grid_wait();  // (as the forward)
   const L me(a);
   const Part part(a, L::kRows);
   const RopeRows &in = part.k ? a.k : a.q, &grad = part.k ? a.ko : a.qo, &to = part.k ? a.dk : a.dq;
@@ -475,16 +478,16 @@ int plan(RopeArgs& a, int D, int sms, int per_sm) {
   return std::min(needed, room) * a.parts;
 }
 
-template <typename... P>
-cudaError_t launch(void (*kernel)(P...), const RopeArgs& a, int ctas, cudaStream_t s) {
-  kernel<<<ctas, kThreads, 0, s>>>(a);
-  return cudaGetLastError();
+template <typename... P, typename... A>
+cudaError_t launch(void (*kernel)(P...), int ctas, int threads, cudaStream_t s, const A&... args) {
+  return launch_clusters(kernel, ctas, 1, 1, 1, threads, 0, true, s, args...);
 }
 
 template <int D, typename T>
 cudaError_t fwd(RopeArgs& a, bool next, int sms, cudaStream_t s) {
   const int ctas = plan(a, D, sms, kFwdCtas);
-  return next ? launch(rope_fwd_kernel<D, T, true>, a, ctas, s) : launch(rope_fwd_kernel<D, T, false>, a, ctas, s);
+  return next ? launch(rope_fwd_kernel<D, T, true>, ctas, kThreads, s, a)
+              : launch(rope_fwd_kernel<D, T, false>, ctas, kThreads, s, a);
 }
 
 template <int D, typename T, typename G>
@@ -494,20 +497,12 @@ cudaError_t bwd(RopeArgs& a, bool next, int sms, cudaStream_t s) {
   cudaError_t e = cudaSuccess;
   if (a.tokens > 0) {
     ctas = plan(a, D, sms, kBwdCtas);
-    e = next ? launch(rope_bwd_kernel<D, T, G, true>, a, ctas, s) : launch(rope_bwd_kernel<D, T, G, false>, a, ctas, s);
+    e = next ? launch(rope_bwd_kernel<D, T, G, true>, ctas, kThreads, s, a)
+             : launch(rope_bwd_kernel<D, T, G, false>, ctas, kThreads, s, a);
   }
   if (e != cudaSuccess || !a.partial) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(2 * D / 32);
-  cfg.blockDim = dim3(1024);
-  cfg.stream = s;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;  // prepared while the main kernel runs
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, rope_weights_kernel, static_cast<const float*>(a.partial), ctas / a.parts, a.parts, a.parts_q, D,
-                            a.dwq, a.dwk);
+  return launch(rope_weights_kernel, 2 * D / 32, 1024, s, static_cast<const float*>(a.partial), ctas / a.parts, a.parts,
+                a.parts_q, D, a.dwq, a.dwk);
 }
 
 }  // namespace
