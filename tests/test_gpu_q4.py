@@ -282,6 +282,27 @@ def test_decode_score_rule(dt, cap, bias):
     check_decode(s, 0.3, out, lse, f"cap {cap} bias {bias}", cap, slopes)
 
 
+def test_decode_scores_of_fp32_queries():
+    """The scores themselves (lse of one token) are as good as fp32 products of q and the cached values, over many.
+
+    The root mean square of the distances from float64 is compared with that of the plain form, which rounds 128 products,
+    their sums and 128 values z + s c. Where codes and the upper bits of q are multiplied exactly, the rounding of q's lower
+    bits and of some ten operations is left, so it should be below; twice the plain form's is the bound.
+    """
+    B, H, Hkv, D = 200, 32, 4, 128
+    s = make([1] * B, H, Hkv, D, 16, F4, seed=6)
+    _, lse = decode(s, D ** -0.5, F4)
+    page = s["table"][:, 0].long()
+    codes, scales = s["kc"][page, :, 0], s["ks"][page, :, 0]
+    k = torch.from_numpy(q4.values(codes, scales)).repeat_interleave(H // Hkv, 1)
+    want = (k * s["q"].double()).sum(2) * D ** -0.5
+    sz = scales.float().repeat_interleave(64, 2).repeat_interleave(H // Hkv, 1)
+    c = torch.from_numpy(q4.unpack(codes)).float().repeat_interleave(H // Hkv, 1)
+    plain = ((s["q"] * (sz[..., 1] + sz[..., 0] * c)).sum(2) * D ** -0.5).double()
+    rms = lambda x: float((x - want).square().mean().sqrt())
+    assert rms(lse.double()) <= 2 * rms(plain)
+
+
 @pytest.mark.parametrize("dt", [BF, F4])
 @pytest.mark.parametrize("H,Hkv", [(4, 2), (10, 1)])
 def test_decode_scales_and_queries_of_any_size(dt, H, Hkv):
