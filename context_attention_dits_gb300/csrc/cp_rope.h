@@ -38,6 +38,8 @@ struct RopeArgs {
   int axes;
   float* partial;  // backward: [CTAs][D], or nullptr
   float *dwq, *dwk;
+  uint32_t* err;        // device error word, and the bound on each wait
+  uint64_t timeout_ns;
   uint8_t axis[kRopeMaxPairs];  // of each pair
 };
 

@@ -17,6 +17,8 @@ namespace {
 using cp::RopeArgs;
 using cp::RopeRows;
 
+constexpr uint64_t kWaitTimeoutNs = 1000000000ull;  // 1 s per device-side wait
+
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 // One tensor's address and strides (batch, token, head; dense without them). Sizes
@@ -71,6 +73,7 @@ cp_status take_rule(RopeArgs* a, const cp_qk_rule* r, int B, int S, int H, int H
   if (!aligned(r->freqs, 8) || !aligned(r->positions, 4) || !aligned(r->q_weight, 2) || !aligned(r->k_weight, 2) ||
       (r->weight_dt == CP_F32 && (!aligned(r->q_weight, 4) || !aligned(r->k_weight, 4))))
     return CP_ERR_ALIGNMENT;
+  a->timeout_ns = kWaitTimeoutNs;
   a->S = S;
   a->H = H;
   a->Hkv = Hkv;
@@ -110,9 +113,8 @@ cp_status cp_qk_norm_rope_fwd(const void* q, const void* k, void* q_out, void* k
     if ((st = take_rows(&a.k, k, at(1), B, S, Hkv, D, e, false)) != CP_OK) return st;
     if ((st = take_rows(&a.ko, k_out, at(3), B, S, Hkv, D, e, true)) != CP_OK) return st;
   }
-  uint32_t* err;
   int sms;
-  if ((st = static_cast<cp_status>(cp::host_device(&err, &sms))) != CP_OK) return st;
+  if ((st = static_cast<cp_status>(cp::host_device(&a.err, &sms))) != CP_OK) return st;
   return cp::launch_rope_fwd(a, D, dt == CP_BF16, rule->interleaved != 0, sms, static_cast<cudaStream_t>(stream)) ==
                  cudaSuccess
              ? CP_OK
@@ -155,9 +157,8 @@ cp_status cp_qk_norm_rope_bwd(const void* q, const void* k, const void* dq_out, 
     a.dwq = dq_weight;
     a.dwk = dk_weight;
   }
-  uint32_t* err;
   int sms;
-  if ((st = static_cast<cp_status>(cp::host_device(&err, &sms))) != CP_OK) return st;
+  if ((st = static_cast<cp_status>(cp::host_device(&a.err, &sms))) != CP_OK) return st;
   return cp::launch_rope_bwd(a, D, dt == CP_BF16, grad_dt == CP_F32, rule->interleaved != 0, sms,
                              static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? CP_OK

@@ -35,7 +35,7 @@ namespace cp {
 namespace {
 
 constexpr int kThreads = kRopeWarps * 32;
-constexpr int kFwdCtas = 4, kBwdCtas = 2;  // on a multiprocessor
+constexpr int kFwdCtas = 3, kBwdCtas = 2;  // on a multiprocessor
 constexpr int kRopeSteps = 16;             // row steps of a part at most, while tokens are many
 
 // f 2^64 / 2 pi, whole turns dropped; f as m 2^(e - 1075), m its 53 bits. 2^66 / 2 pi
@@ -75,22 +75,6 @@ __device__ __forceinline__ void cos_sin(uint64_t step, int pos, float& c, float&
   if (quarter == 2 || quarter == 3) s = -s;
 }
 
-// Rows are touched once: past L1. (Not the read-only path: a row may be
-// overwritten in place by the threads that have read it.)
-__device__ __forceinline__ uint4 ld16(const void* p) {
-  uint4 v;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p)
-               : "memory");
-  return v;
-}
-__device__ __forceinline__ uint2 ld8(const void* p) {
-  uint2 v;
-  asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p) : "memory");
-  return v;
-}
-
 // 8 values of a row as the first and the second members of four pairs: neighbours,
 // or the two fours against each other; and back.
 template <bool kNext>
@@ -120,10 +104,10 @@ struct Raw<__nv_bfloat16> {
   uint32_t w[4];
   __device__ __forceinline__ void load(const __nv_bfloat16* row, int e0, int e1, bool one) {
     if (one) {
-      const uint4 v = ld16(row + e0);
+      const uint4 v = *reinterpret_cast<const uint4*>(row + e0);
       w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
     } else {
-      const uint2 x = ld8(row + e0), y = ld8(row + e1);
+      const uint2 x = *reinterpret_cast<const uint2*>(row + e0), y = *reinterpret_cast<const uint2*>(row + e1);
       w[0] = x.x, w[1] = x.y, w[2] = y.x, w[3] = y.y;
     }
   }
@@ -156,7 +140,7 @@ template <>
 struct Raw<float> {
   uint32_t w[8];
   __device__ __forceinline__ void load(const float* row, int e0, int e1, bool) {
-    const uint4 x = ld16(row + e0), y = ld16(row + e1);
+    const uint4 x = *reinterpret_cast<const uint4*>(row + e0), y = *reinterpret_cast<const uint4*>(row + e1);
     w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
     w[4] = y.x, w[5] = y.y, w[6] = y.z, w[7] = y.w;
   }
@@ -232,54 +216,138 @@ struct Lane {
   }
 };
 
-// A CTA's part of every token: rows of q or of k, steps [first, last) of them. Its
-// warps take the tokens in turn.
+// A CTA's part of every token: heads [first, last) of q or of k. Its warps take the
+// tokens in turn.
 struct Part {
   bool k;
-  int first, last, heads, token, stride;
+  int first, last, token, stride;
   __device__ __forceinline__ Part(const RopeArgs& a, int rows) {
     const int group = blockIdx.x / a.parts, part = blockIdx.x - group * a.parts;
     k = part >= a.parts_q;
-    heads = k ? a.Hkv : a.H;
-    const int n = (heads + rows - 1) / rows, of = k ? a.parts - a.parts_q : a.parts_q, at = k ? part - a.parts_q : part;
-    first = static_cast<int>(static_cast<int64_t>(at) * n / of);
-    last = static_cast<int>(static_cast<int64_t>(at + 1) * n / of);
+    const int heads = k ? a.Hkv : a.H, n = (heads + rows - 1) / rows;
+    const int of = k ? a.parts - a.parts_q : a.parts_q, at = k ? part - a.parts_q : part;
+    first = static_cast<int>(static_cast<int64_t>(at) * n / of) * rows;
+    last = min(static_cast<int>(static_cast<int64_t>(at + 1) * n / of) * rows, heads);
     token = group * kRopeWarps + (threadIdx.x >> 5);
     stride = gridDim.x / a.parts * kRopeWarps;
   }
 };
 
-template <typename T>
-__device__ __forceinline__ T* row_of(const RopeRows& x, int b, int s, int head) {
-  return static_cast<T*>(x.p) + b * x.sb + s * x.ss + head * x.sh;
+__device__ __forceinline__ int64_t row_at(const RopeRows& x, int b, int s, int head) {
+  return b * x.sb + s * x.ss + head * x.sh;
 }
+
+// A warp's rows on their way through shared memory: batches of up to kBatch heads of a
+// token (kB > 0: of two tensors), kStages - 1 of them under way while one is worked on,
+// 2 KB (kB: 4 KB) each. As many loads in registers would halve the warps: 4608 tokens of
+// 24 + 24 heads of 128, bf16, with four rows in registers: forward 24.0 us where this
+// takes 22.4, backward 37.8 where this takes 34.7 (32768 tokens forward: 133.8, 130.2).
+// A warp with one batch in all gains nothing (700 tokens of 6 + 3 fp32 heads, backward:
+// 7.7 us from registers, 8.5 here).
+template <int D, int kElemA, int kElemB>
+struct Ring {
+  static constexpr int kRows = 256 / D, kSteps = kElemA == 2 ? 4 : 2, kBatch = kRows * kSteps;
+  static constexpr int kA = kBatch * D * kElemA, kB = kBatch * D * kElemB, kStage = kA + kB;
+  static constexpr int kStages = kElemB ? 2 : 4;
+  static constexpr int kSmem = kRopeWarps * kStages * kStage;
+  static_assert(kBatch <= 16, "a lane a row and tensor");
+  struct Shared {
+    uint64_t full[kRopeWarps][kStages];
+    uint32_t abort;
+  };
+  const RopeArgs& a;
+  const Part& part;
+  const RopeRows &x, &y;  // (y: the second tensor)
+  Shared& sh;
+  uint8_t* buf;
+  uint32_t bars;
+  int token, head, ask = 0, take = 0;  // of the next batch to ask for
+  uint32_t phase = 0;
+
+  __device__ __forceinline__ Ring(const RopeArgs& a_, const Part& p, const RopeRows& x_, const RopeRows& y_, uint8_t* smem, Shared& s)
+      : a(a_), part(p), x(x_), y(y_), sh(s) {
+    const int warp = threadIdx.x >> 5;
+    buf = smem + warp * kStages * kStage;
+    bars = smem_addr(&sh.full[warp][0]);
+    token = p.token;
+    head = p.first;
+  }
+  static __device__ __forceinline__ void set_up(Shared& sh) {
+    if (threadIdx.x < kRopeWarps * kStages) mbar_init(smem_addr(&sh.full[0][0] + threadIdx.x), 1);
+    if (threadIdx.x == 0) sh.abort = 0;
+    fence_mbar_init();
+    fence_async();
+    __syncthreads();
+  }
+  __device__ __forceinline__ void next() {
+    if (token >= a.tokens) return;
+    const int lane = threadIdx.x & 31, n = min(kBatch, part.last - head), b = token / a.S, s = token - b * a.S;
+    const uint32_t bar = bars + ask * 8, to = smem_addr(buf) + ask * kStage;
+    const bool with_x = kB == 0 || a.norm;  // (without a norm the backward does not read x)
+    if (lane == 0) mbar_arrive_expect_tx(bar, n * D * ((with_x ? kElemA : 0) + kElemB));
+    __syncwarp();
+    const bool second = kB > 0 && (lane & 16);
+    const RopeRows& t = second ? y : x;
+    const int elem = second ? kElemB : kElemA, i = kB > 0 ? lane & 15 : lane;
+    if (second || with_x) {
+      // heads side by side are one copy
+      const int rows = t.sh == D ? (i == 0 ? n : 0) : (i < n ? 1 : 0);
+      if (rows)
+        bulk_g2s(to + (second ? kA : 0) + i * D * elem, static_cast<const uint8_t*>(t.p) + row_at(t, b, s, head + i) * elem,
+                 rows * D * elem, bar);
+    }
+    if (++ask == kStages) ask = 0;
+    if ((head += kBatch) >= part.last) {
+      head = part.first;
+      token += part.stride;
+    }
+    __syncwarp();
+  }
+  __device__ __forceinline__ void start() {
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) next();
+  }
+  // The next batch, and the one that goes into the stage worked on before. nullptr: a wait ran out.
+  __device__ __forceinline__ const uint8_t* batch() {
+    if (!__all_sync(0xffffffffu, mbar_wait_bounded(bars + take * 8, phase >> take & 1u, &sh.abort, a.err, a.timeout_ns)))
+      return nullptr;
+    next();
+    return buf + take * kStage;
+  }
+  __device__ __forceinline__ void done() {
+    phase ^= 1u << take;
+    if (++take == kStages) take = 0;
+    __syncwarp();
+  }
+  // After a wait that ran out: what is under way lands.
+  __device__ __forceinline__ void drain() {
+    for (; take != ask; done()) {
+      const uint64_t t0 = global_timer_ns();
+      while (!mbar_try_wait(bars + take * 8, phase >> take & 1u) && global_timer_ns() - t0 < a.timeout_ns) {
+      }
+    }
+  }
+};
 
 template <int D, typename T, bool kNext>
 __global__ void __launch_bounds__(kThreads, kFwdCtas) rope_fwd_kernel(const __grid_constant__ RopeArgs a) {
   using L = Lane<D, T, kNext>;
-  constexpr int kAhead = sizeof(T) == 2 ? 4 : 2;  // rows whose loads are under way at once
+  using R = Ring<D, sizeof(T), 0>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ typename R::Shared shared;
+  R::set_up(shared);
   grid_wait();  // (the launch may start while its predecessor in the stream ends)
-  const L me(a);
   const Part part(a, L::kRows);
   const RopeRows &in = part.k ? a.k : a.q, &to = part.k ? a.ko : a.qo;
-  const int64_t in_step = L::kRows * in.sh, to_step = L::kRows * to.sh;
+  R ring(a, part, in, in, smem, shared);
+  ring.start();
+  const L me(a);
+  const int64_t to_step = L::kRows * to.sh;
   float2 wu[2], wv[2];
   me.weights(a, part.k ? a.wk : a.wq, wu, wv);
   for (int token = part.token; token < a.tokens; token += part.stride) {
     const int b = token / a.S, s = token - b * a.S;
-    const int h0 = part.first * L::kRows + me.r;
-    const T* from = row_of<T>(in, b, s, h0);
-    T* dest = row_of<T>(to, b, s, h0);
-    Raw<T> raw[kAhead];
-    auto load = [&](int at) {
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        raw[i] = {};
-        if (at + i < part.last && (at + i) * L::kRows + me.r < part.heads) raw[i].load(from + i * in_step, me.e0, me.e1, kNext);
-      }
-      from += kAhead * in_step;
-    };
-    load(part.first);  // on their way while the angles are formed
+    T* dest = static_cast<T*>(to.p) + row_at(to, b, s, part.first + me.r);
     // (u, v) -> n (u au - v bv, u bu + v av): weights and angles as one
     float2 au[2], av[2], bu[2], bv[2];
 #pragma unroll
@@ -299,29 +367,33 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas) rope_fwd_kernel(const __gr
         bv[i] = mul2(wv[i], make_float2(-sn[i].x, -sn[i].y));
       }
     }
-    for (int at = part.first; at < part.last;) {
+    for (int head = part.first; head < part.last; head += R::kBatch) {
+      const uint8_t* rows = ring.batch();
+      if (!rows) return ring.drain();
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        if (at + i >= part.last) break;
+      for (int i = 0; i < R::kSteps; ++i) {
+        if (head + i * L::kRows >= part.last) break;
+        const bool real = head + i * L::kRows + me.r < part.last;
+        Raw<T> raw = {};
+        if (real) raw.load(reinterpret_cast<const T*>(rows) + (i * L::kRows + me.r) * D, me.e0, me.e1, kNext);
         float2 u[2], v[2];
-        raw[i].template get<kNext>(u, v);
+        raw.template get<kNext>(u, v);
         float n = 1.f;
         if (a.norm) {
           const float2 sq = fma2(v[1], v[1], fma2(v[0], v[0], fma2(u[1], u[1], mul2(u[0], u[0]))));
           n = rsqrtf(fmaf(L::row_sum(sq.x + sq.y), 1.f / D, a.eps));
         }
-        const float2 nn = make_float2(n, n);
+        const float2 nn = twice(n);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const float2 y = mul2(fma2(u[j], au[j], mul2(v[j], bv[j])), nn);
           v[j] = mul2(fma2(v[j], av[j], mul2(u[j], bu[j])), nn);
           u[j] = y;
         }
-        if ((at + i) * L::kRows + me.r < part.heads) Raw<T>::template store<kNext>(dest + i * to_step, me.e0, me.e1, u, v);
+        if (real) Raw<T>::template store<kNext>(dest, me.e0, me.e1, u, v);
+        dest += to_step;
       }
-      dest += kAhead * to_step;
-      at += kAhead;
-      if (at < part.last) load(at);
+      ring.done();
     }
   }
 }
@@ -329,38 +401,25 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas) rope_fwd_kernel(const __gr
 template <int D, typename T, typename G, bool kNext>
 __global__ void __launch_bounds__(kThreads, kBwdCtas) rope_bwd_kernel(const __grid_constant__ RopeArgs a) {
   using L = Lane<D, T, kNext>;
-  constexpr int kAhead = sizeof(T) + sizeof(G) == 4 ? 4 : 2;
+  using R = Ring<D, sizeof(T), sizeof(G)>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ typename R::Shared shared;
+  R::set_up(shared);
   grid_wait();  // (as the forward)
-  const L me(a);
   const Part part(a, L::kRows);
-  const RopeRows &in = part.k ? a.k : a.q, &grad = part.k ? a.ko : a.qo, &to = part.k ? a.dk : a.dq;
-  const int64_t in_step = L::kRows * in.sh, grad_step = L::kRows * grad.sh, to_step = L::kRows * to.sh;
+  const RopeRows& to = part.k ? a.dk : a.dq;
+  R ring(a, part, part.k ? a.k : a.q, part.k ? a.ko : a.qo, smem, shared);
+  ring.start();
+  const L me(a);
+  const int64_t to_step = L::kRows * to.sh;
   float2 wu[2], wv[2], accu[2], accv[2];
   me.weights(a, part.k ? a.wk : a.wq, wu, wv);
 #pragma unroll
   for (int i = 0; i < 2; ++i) accu[i] = accv[i] = make_float2(0.f, 0.f);
-  for (int token = part.token; token < a.tokens; token += part.stride) {
+  bool ran_out = false;
+  for (int token = part.token; token < a.tokens && !ran_out; token += part.stride) {
     const int b = token / a.S, s = token - b * a.S;
-    const int h0 = part.first * L::kRows + me.r;
-    const T* from = row_of<T>(in, b, s, h0);
-    const G* gfrom = row_of<G>(grad, b, s, h0);
-    T* dest = row_of<T>(to, b, s, h0);
-    Raw<T> rx[kAhead];
-    Raw<G> rg[kAhead];
-    auto load = [&](int at) {
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        rx[i] = {};
-        rg[i] = {};
-        if (at + i < part.last && (at + i) * L::kRows + me.r < part.heads) {
-          rg[i].load(gfrom + i * grad_step, me.e0, me.e1, kNext);
-          if (a.norm) rx[i].load(from + i * in_step, me.e0, me.e1, kNext);
-        }
-      }
-      from += kAhead * in_step;
-      gfrom += kAhead * grad_step;
-    };
-    load(part.first);
+    T* dest = static_cast<T*>(to.p) + row_at(to, b, s, part.first + me.r);
     float2 c[2], sn[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -368,13 +427,24 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas) rope_bwd_kernel(const __gr
       sn[i] = make_float2(0.f, 0.f);
     }
     if (a.pairs) me.angles(a.pos + b * a.pos_sb + static_cast<int64_t>(s) * a.axes, c, sn);
-    for (int at = part.first; at < part.last;) {
+    for (int head = part.first; head < part.last; head += R::kBatch) {
+      const uint8_t* rows = ring.batch();
+      if (!rows) {
+        ran_out = true;
+        break;
+      }
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        if (at + i >= part.last) break;
-        const bool real = (at + i) * L::kRows + me.r < part.heads;
+      for (int i = 0; i < R::kSteps; ++i) {
+        if (head + i * L::kRows >= part.last) break;
+        const bool real = head + i * L::kRows + me.r < part.last;
+        Raw<T> rx = {};
+        Raw<G> rg = {};
+        if (real) {
+          rg.load(reinterpret_cast<const G*>(rows + R::kA) + (i * L::kRows + me.r) * D, me.e0, me.e1, kNext);
+          if (a.norm) rx.load(reinterpret_cast<const T*>(rows) + (i * L::kRows + me.r) * D, me.e0, me.e1, kNext);
+        }
         float2 u[2], v[2], gu[2], gv[2];
-        rg[i].template get<kNext>(gu, gv);
+        rg.template get<kNext>(gu, gv);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {  // back
           const float2 y = fma2(gu[j], c[j], mul2(gv[j], sn[j]));
@@ -382,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas) rope_bwd_kernel(const __gr
           gu[j] = y;
         }
         if (a.norm) {
-          rx[i].template get<kNext>(u, v);
+          rx.template get<kNext>(u, v);
           const float2 sq2 = fma2(v[1], v[1], fma2(v[0], v[0], fma2(u[1], u[1], mul2(u[0], u[0]))));
           float2 dot2 = make_float2(0.f, 0.f);
 #pragma unroll
@@ -395,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas) rope_bwd_kernel(const __gr
           }
           const float n = real ? rsqrtf(fmaf(sq, 1.f / D, a.eps)) : 0.f;  // (0 with eps = 0 adds nothing)
           const float back = -dot * n * n * (1.f / D);                    // times x: - x r mean(g w x r)
-          const float2 nn = make_float2(n, n), bb = make_float2(back, back);
+          const float2 nn = twice(n), bb = twice(back);
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             accu[j] = fma2(gu[j], mul2(u[j], nn), accu[j]);
@@ -404,13 +474,13 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas) rope_bwd_kernel(const __gr
             gv[j] = mul2(nn, fma2(gv[j], wv[j], mul2(v[j], bb)));
           }
         }
-        if (real) Raw<T>::template store<kNext>(dest + i * to_step, me.e0, me.e1, gu, gv);
+        if (real) Raw<T>::template store<kNext>(dest, me.e0, me.e1, gu, gv);
+        dest += to_step;
       }
-      dest += kAhead * to_step;
-      at += kAhead;
-      if (at < part.last) load(at);
+      ring.done();
     }
   }
+  if (ran_out) ring.drain();
   if (!a.partial) return;
   // ---- this CTA's part of its weight's gradient, in a fixed order ----
   __shared__ float sums[kRopeWarps][D];
@@ -478,16 +548,17 @@ int plan(RopeArgs& a, int D, int sms, int per_sm) {
   return std::min(needed, room) * a.parts;
 }
 
-template <typename... P, typename... A>
-cudaError_t launch(void (*kernel)(P...), int ctas, int threads, cudaStream_t s, const A&... args) {
-  return launch_clusters(kernel, ctas, 1, 1, 1, threads, 0, true, s, args...);
+template <auto kKernel, int kSmem>
+cudaError_t launch(const RopeArgs& a, int ctas, cudaStream_t s) {
+  const cudaError_t e = allow_smem<kKernel>(kSmem);
+  return e != cudaSuccess ? e : launch_clusters(kKernel, ctas, 1, 1, 1, kThreads, kSmem, true, s, a);
 }
 
 template <int D, typename T>
 cudaError_t fwd(RopeArgs& a, bool next, int sms, cudaStream_t s) {
   const int ctas = plan(a, D, sms, kFwdCtas);
-  return next ? launch(rope_fwd_kernel<D, T, true>, ctas, kThreads, s, a)
-              : launch(rope_fwd_kernel<D, T, false>, ctas, kThreads, s, a);
+  constexpr int kSmem = Ring<D, sizeof(T), 0>::kSmem;
+  return next ? launch<rope_fwd_kernel<D, T, true>, kSmem>(a, ctas, s) : launch<rope_fwd_kernel<D, T, false>, kSmem>(a, ctas, s);
 }
 
 template <int D, typename T, typename G>
@@ -497,12 +568,12 @@ cudaError_t bwd(RopeArgs& a, bool next, int sms, cudaStream_t s) {
   cudaError_t e = cudaSuccess;
   if (a.tokens > 0) {
     ctas = plan(a, D, sms, kBwdCtas);
-    e = next ? launch(rope_bwd_kernel<D, T, G, true>, ctas, kThreads, s, a)
-             : launch(rope_bwd_kernel<D, T, G, false>, ctas, kThreads, s, a);
+    constexpr int kSmem = Ring<D, sizeof(T), sizeof(G)>::kSmem;
+    e = next ? launch<rope_bwd_kernel<D, T, G, true>, kSmem>(a, ctas, s) : launch<rope_bwd_kernel<D, T, G, false>, kSmem>(a, ctas, s);
   }
   if (e != cudaSuccess || !a.partial) return e;
-  return launch(rope_weights_kernel, 2 * D / 32, 1024, s, static_cast<const float*>(a.partial), ctas / a.parts, a.parts,
-                a.parts_q, D, a.dwq, a.dwk);
+  return launch_clusters(rope_weights_kernel, 2 * D / 32, 1, 1, 1, 1024, 0, true, s, static_cast<const float*>(a.partial),
+                         ctas / a.parts, a.parts, a.parts_q, D, a.dwq, a.dwk);
 }
 
 }  // namespace
