@@ -66,6 +66,13 @@ __device__ __forceinline__ float fmin3(float a, float b, float c) {
   return y;
 }
 
+// 1 where a >= b, else 0.
+__device__ __forceinline__ float at_least(float a, float b) {
+  float y;
+  asm("set.ge.f32.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+
 // a - b = h + l exactly.
 __device__ __forceinline__ void exact_diff(float a, float b, float& h, float& l) {
   h = __fsub_rn(a, b);
@@ -98,17 +105,15 @@ __device__ __forceinline__ uint2 quantise(const float (&x)[16], uint32_t& scale)
   }
   float h, l;
   exact_diff(most, z, h, l);
-  if (!(fabsf(h) <= FLT_MAX)) {  // a value that is not finite, or a span that fp32 does not hold
-    scale = 0x7fff7fffu;         // reads back as NaN
-    return make_uint2(0, 0);
-  }
+  // a value that is not finite, or a span that fp32 does not hold: reads back as NaN, whatever is formed meanwhile
+  const bool bad = !(fabsf(h) <= FLT_MAX);
   // s: upper bits of a quotient that is at most 2^-19 of itself too small, so two steps up at most
   uint32_t sb = __float_as_uint(h * (1.f / 15 * (1 - 0x1p-20f))) & 0xffff0000u;
 #pragma unroll
   for (int i = 0; i < 2; ++i)
     if (__fsub_rn(15.f * __uint_as_float(sb), h) < l) sb += 0x10000u;  // both sides exact
   const float s = fmaxf(__uint_as_float(sb), 0x1p-100f);
-  scale = __float_as_uint(s) >> 16 | __float_as_uint(z);
+  scale = bad ? 0x7fff7fffu : __float_as_uint(s) >> 16 | __float_as_uint(z);
   // c: the integer nearest to a quotient that is at most 15 2^-18 too small (by a sum
   // whose unit is 1), raised where the value lies half a step above it or more
   constexpr float kOne = 12582912.f;  // 1.5 2^23
@@ -123,27 +128,35 @@ __device__ __forceinline__ uint2 quantise(const float (&x)[16], uint32_t& scale)
     for (int i = 0; i < 16; i += 2) small = fmin3(small, fabsf(x[i]), fabsf(x[i + 1]));
     exact = z == 0.f || small >= fmaxf(fabsf(least), fabsf(most)) * 0x1p-14f;
   }
-  uint32_t codes[2] = {0, 0};
+  float2 c[8];  // codes i and i + 8
+  if (kB16 && __all_sync(0xffffffffu, exact)) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float2 d = add2(make_float2(x[2 * i], x[2 * i + 1]), zz);
-    float2 g = fma2(d, rs, twice(kOne));
-    const float2 r = fma2(add2(g, twice(-kOne)), down, d);  // exact: d - c s, within a step
-    if (exact) {
-      if (r.x >= half) g.x += 1.f;
-      if (r.y >= half) g.y += 1.f;
-    } else {  // what the difference has lost decides where the rest is half a step
-      float lx, ly;
-      exact_diff(x[2 * i], z, h, lx);
-      exact_diff(x[2 * i + 1], z, h, ly);
-      if (__fadd_rn(__fsub_rn(r.x, half), lx) >= 0.f) g.x += 1.f;
-      if (__fadd_rn(__fsub_rn(r.y, half), ly) >= 0.f) g.y += 1.f;
+    for (int i = 0; i < 8; ++i) {
+      const float2 d = add2(make_float2(x[i], x[i + 8]), zz);
+      const float2 g = add2(fma2(d, rs, twice(kOne)), twice(-kOne));
+      const float2 r = fma2(g, down, d);  // exact: d - c s, within a step
+      c[i] = add2(g, make_float2(at_least(r.x, half), at_least(r.y, half)));
     }
-    codes[i >> 2] += __float_as_uint(g.x) << (8 * (i & 3));
-    codes[i >> 2] += __float_as_uint(g.y) << (8 * (i & 3) + 4);
+  } else {  // what the difference has lost decides where the rest is half a step
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float2 v = make_float2(x[i], x[i + 8]), minus = twice(-1.f);
+      const float2 d = add2(v, zz);
+      const float2 back = fma2(v, minus, d);
+      const float2 lost = fma2(add2(twice(z), back), minus, fma2(fma2(back, minus, d), minus, v));
+      const float2 g = add2(fma2(d, rs, twice(kOne)), twice(-kOne));
+      const float2 r = add2(add2(fma2(g, down, d), twice(-half)), lost);
+      c[i] = add2(g, make_float2(at_least(r.x, 0.f), at_least(r.y, 0.f)));
+    }
   }
-  // (the eight copies of kOne's bits, 0x4b400000, come to 0x3f400000 in 32 bits)
-  return make_uint2(codes[0] - 0x3f400000u, codes[1] - 0x3f400000u);
+  // four codes at a time are a number below 2^16, exact in fp32
+  uint2 codes;
+  const float2 c03 = fma2(fma2(c[3], twice(16.f), c[2]), twice(256.f), fma2(c[1], twice(16.f), c[0]));
+  const float2 c47 = fma2(fma2(c[7], twice(16.f), c[6]), twice(256.f), fma2(c[5], twice(16.f), c[4]));
+  const float2 lo = add2(c03, twice(0x1p23f)), hi = add2(c47, twice(0x1p23f));
+  codes.x = __byte_perm(__float_as_uint(lo.x), __float_as_uint(hi.x), 0x5410);
+  codes.y = __byte_perm(__float_as_uint(lo.y), __float_as_uint(hi.y), 0x5410);
+  return bad ? make_uint2(0, 0) : codes;
 }
 
 // Token and head of a row (row < 2^31).
@@ -155,7 +168,7 @@ __device__ __forceinline__ void token_head(const PagedArgs& a, int row, int& t, 
 
 // Rows (token, head) of sequence blockIdx.y: a warp takes 512 / D of them, 16 values a
 // lane. Bound by instructions, so the work that a group takes once is spread over few
-// lanes (8 values a lane: 31.6 us where this takes 26.3).
+// lanes (8 values a lane: 31.6 us where 16 took 26.3, with either form of the codes).
 template <int D, typename T>
 __global__ void __launch_bounds__(kRowThreads) q4_append_kernel(const __grid_constant__ PagedArgs a) {
   constexpr int kLanes = D / 16;
