@@ -156,6 +156,7 @@ struct Qk {
     rule.q_weight = w[0] ? w[0]->data_ptr() : nullptr;
     rule.k_weight = w[1] ? w[1]->data_ptr() : nullptr;
     rule.interleaved = PyObject_IsTrue(args[3]);
+    if (rule.interleaved < 0) throw Raised{};
     if (args[1] == Py_None) {
       if (args[0] != Py_None || args[2] != Py_None) bad_value("positions and axes need freqs");
       return;

@@ -515,7 +515,9 @@ cp_status cp_paged_attn_decode(const void* q, const void* k_cache, const void* v
  *   (u, v) -> (u cos t - v sin t, u sin t + v cos t)
  * and the values behind the 2 pairs first ones stay as they are. The angle is formed
  * in 64-bit fixed point of a turn: it is as good at position 2^30 as at 1. Sums and
- * rotation are fp32, results rounded once.
+ * rotation are fp32, results rounded once; with a norm, values are at most 2^60, so that
+ * a row's squares have a sum. Rows pass through bounded waits: one that runs out is
+ * reported by cp_check_device_status.
  * -------------------------------------------------------------------------*/
 typedef struct {
   int norm;                 /* nonzero: root-mean-square norm of each head */
@@ -575,8 +577,9 @@ cp_status cp_qk_norm_rope_bwd(const void* q, const void* k, const void* dq_out, 
  *   z = the largest bf16 number not above the group's values,
  *   s = the smallest bf16 number not below (largest value - z) / 15 and 2^-100,
  *   c = min(15, floor((x - z) / s + 1/2)),
- * each exactly, whatever the rows' type. A group that holds an infinity or a NaN, or
- * spans more than the largest fp32 number, reads back as NaN (s = z = NaN).
+ * each exactly, whatever the rows' type. A group that holds an infinity or a NaN, a
+ * value below the least bf16 number, or spans more than the largest fp32 number, reads
+ * back as NaN (s = z = NaN).
  *   codes  [num_pages, Hkv, page_size, D / 2] bytes: value 2 i of a row is the lower
  *          half of its byte i, value 2 i + 1 the upper;
  *   scales [num_pages, Hkv, page_size, D / 64, 2] bf16: s, z.
@@ -620,7 +623,8 @@ size_t cp_paged_attn_q4_workspace_size(int B, int H, int Hkv, int D, int page_si
 /*
  * Attention of one new token per sequence: as cp_paged_attn_decode. Scores are formed
  * from the codes exactly; the weights, times the values' scales, are rounded to fp16
- * (fp32 q: to 22 bits) and summed in fp32. q, and k and v as they were appended, are
+ * (fp32 q: to 22 bits; what lies below 2^-39 of the largest scale met so far is lost)
+ * and summed in fp32. q, and k and v as they were appended, are
  * finite and at most 2^96. Errors: INVALID_ARG, NOT_DIVISIBLE (H % Hkv), ALIGNMENT,
  * WORKSPACE, CUDA, UNSUPPORTED_DEVICE.
  */

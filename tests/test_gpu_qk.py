@@ -263,6 +263,26 @@ def test_strides_in_place_and_broadcast(inter, dt):
         cpa().cp_qk_norm_rope_fwd(s["q"].cuda(), s["k"].cuda(), q, torch.empty_like(k2), **kw(s))
 
 
+@pytest.mark.parametrize("dt,gdt", [(BF, BF), (BF, F4), (F4, F4)])
+@pytest.mark.parametrize("D,H,Hkv", [(128, 20, 9), (64, 33, 3)])
+def test_many_batches_a_warp(D, H, Hkv, dt, gdt):
+    """Warps that take several tokens of several batches of heads: dense, in place, and heads that do not lie side by side."""
+    s = make(1, 6001, H, Hkv, D, dt, D // 4, 2, seed=9, wdt=F4)
+    check_all(s, "dense", gdt)
+    want, grads = run_fwd(s), run_bwd(s, gdt)
+    q, k = s["q"].cuda(), s["k"].cuda()
+    cpa().cp_qk_norm_rope_fwd(q, k, q, k, **kw(s))
+    assert torch.equal(q, want[0]) and torch.equal(k, want[1])
+    apart = dict(s, **{n: s[n].cuda().transpose(1, 2).contiguous().transpose(1, 2) for n in ("q", "k", "gq", "gk")})
+    assert all(torch.equal(a, b) for a, b in zip(run_fwd(apart), want))
+    assert all(torch.equal(a, b) for a, b in zip(run_bwd(apart, gdt), grads))
+    q, k, gq, gk = (s[n].cuda() for n in ("q", "k", "gq", "gk"))
+    if gdt == dt:   # over the results' gradients
+        cpa().cp_qk_norm_rope_bwd(q, k, gq, gk, gq, gk, **kw(s))
+        assert torch.equal(gq, grads[0]) and torch.equal(gk, grads[1])
+    assert cpa().cp_check_device_status() == 0
+
+
 @pytest.mark.parametrize("dt", [BF, F4])
 def test_queries_alone_and_nothing_at_all(dt):
     s = make(2, 9, 3, 1, 64, dt, 32, 1, seed=6, wdt=F4)
