@@ -47,7 +47,7 @@ __device__ __forceinline__ int64_t head_row(const PagedArgs& a, int page, int po
 // ----------------------------------------------------------------------------
 // Append and read
 // ----------------------------------------------------------------------------
-constexpr int kRowThreads = 256;
+constexpr int kRowThreads = 128;
 
 __device__ __forceinline__ float max_nan(float a, float b, float c) {
   float y;
@@ -168,7 +168,9 @@ __device__ __forceinline__ void token_head(const PagedArgs& a, int row, int& t, 
 
 // Rows (token, head) of sequence blockIdx.y: a warp takes 512 / D of them, 16 values a
 // lane. Bound by instructions, so the work that a group takes once is spread over few
-// lanes (8 values a lane: 31.6 us where 16 took 26.3, with either form of the codes).
+// lanes (8 values a lane: 31.6 us where 16 took 26.3), and keys and values share the
+// look-up of their place (a CTA of either alone: 26.3 us where this takes 22.9: some
+// 17000 new tokens of 6 sequences, 8 heads of 128, bf16: 3.9 TB/s of rows and codes).
 template <int D, typename T>
 __global__ void __launch_bounds__(kRowThreads) q4_append_kernel(const __grid_constant__ PagedArgs a) {
   constexpr int kLanes = D / 16;
@@ -235,9 +237,11 @@ __device__ __forceinline__ void values8(uint32_t codes, uint32_t scale, float (&
 
 // Rows (token, head) of sequence blockIdx.y: a warp takes kAhead times 256 / D, all
 // of whose loads are under way at once (length, page, codes: one after the other).
+// Bound by HBM, most of it the values written: 24.0 us for 6 sequences of up to 5119
+// tokens, 8 heads of 128, 6.0 TB/s (four times 256 / D: 24.6).
 template <int D, typename T>
 __global__ void __launch_bounds__(kRowThreads) q4_read_kernel(const __grid_constant__ PagedArgs a) {
-  constexpr int kLanes = D / 8, kAhead = 4, kRows = kRowThreads / kLanes;
+  constexpr int kLanes = D / 8, kAhead = 2, kRows = kRowThreads / kLanes;
   grid_wait();
   const int b = blockIdx.y, l = threadIdx.x % kLanes;
   const int most = a.T * a.Hkv, first = blockIdx.x * (kRows * kAhead) + threadIdx.x / kLanes;
@@ -1053,7 +1057,7 @@ cudaError_t launch_q4_append(const PagedArgs& a, bool bf16, cudaStream_t s) {
 }
 
 cudaError_t launch_q4_read(const PagedArgs& a, bool bf16, cudaStream_t s) {
-  const int rows = kRowThreads / (a.D / 8) * 4;
+  const int rows = kRowThreads / (a.D / 8) * 2;
   if (a.D == 64)
     return bf16 ? launch_rows(q4_read_kernel<64, __nv_bfloat16>, a, rows, s) : launch_rows(q4_read_kernel<64, float>, a, rows, s);
   return bf16 ? launch_rows(q4_read_kernel<128, __nv_bfloat16>, a, rows, s) : launch_rows(q4_read_kernel<128, float>, a, rows, s);
