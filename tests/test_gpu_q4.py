@@ -571,6 +571,52 @@ def test_rotated_and_cached_tokens():
     assert cpa().cp_check_device_status() == 0
 
 
+@pytest.mark.parametrize("tokens", [128, 1 << 17])   # tables for clusters, and for the list and its join
+def test_back_to_back_calls_see_each_other(tokens):
+    """Each call reads what the one before has written, none waits for the host; the same with a wait after every call."""
+    B, steps, H, Hkv, D, page = 5, 40, 8, 2, 64, 16
+    g = torch.Generator().manual_seed(11)
+    qk = torch.randn((B, 1, H + Hkv, D), generator=g).to(BF).cuda()
+    v = torch.randn((B, 1, Hkv, D), generator=g).to(BF).cuda()
+    freqs = torch.tensor([100.0 ** (-i / 32) for i in range(32)], dtype=torch.float64).cuda()
+    pos = torch.arange(steps + 1, dtype=torch.int32).cuda()[:, None].contiguous()
+    s = widened(make([steps] * B, H, Hkv, D, page, BF, seed=2), tokens)
+    lens = [torch.full((B,), t, dtype=torch.int32, device="cuda") for t in range(steps + 1)]
+    size = cpa().cp_paged_attn_q4_workspace_size(B, H, Hkv, D, page, s["table"].shape[1])
+    assert (size > 0) == (tokens > 128)
+
+    def chain(after):
+        d = [s[x].cuda() for x in CACHE]
+        ws = torch.full((max(size, 256),), 255, dtype=torch.uint8, device="cuda")
+        ws2 = torch.full((cpa().cp_qk_norm_rope_bwd_workspace_size(D),), 255, dtype=torch.uint8, device="cuda")
+        q, k, out = qk[:, :, :H].contiguous(), torch.empty_like(v), torch.empty((B, H, D), dtype=BF, device="cuda")
+        dq, dk, lse = torch.empty_like(q), torch.empty_like(k), torch.empty((B, H), device="cuda")
+        w = [torch.ones(D, device="cuda") for _ in range(2)]
+        rows = [torch.empty((B, steps, Hkv, D), dtype=BF, device="cuda") for _ in range(2)]
+        torch.cuda.synchronize()
+        for t in range(steps):
+            rule = dict(positions=pos[t:t + 1], freqs=freqs, eps=1e-6)
+            # the step's queries are the last one's answers, its weights the last one's gradients
+            cpa().cp_qk_norm_rope_fwd(q, qk[:, :, H:], q, k, q_weight=w[0], k_weight=w[1], **rule)
+            after()
+            cpa().cp_paged_kv_append_q4(k, v, *d, lens[t])
+            after()
+            cpa().cp_paged_attn_decode_q4(q.view(B, H, D), *d, lens[t + 1], out, lse, D ** -0.5, workspace=ws)
+            after()
+            cpa().cp_qk_norm_rope_bwd(out.view(B, 1, H, D), k, q, v, dq, dk, dq_weight=w[0], dk_weight=w[1], workspace=ws2, **rule)
+            after()
+            cpa().cp_qk_norm_rope_fwd(dq, dk, q, k, **rule)
+            after()
+        cpa().cp_paged_kv_read_q4(*d, lens[steps], *rows)
+        torch.cuda.synchronize()
+        return q, k, out, lse, *w, *rows
+
+    got, want = chain(lambda: None), chain(torch.cuda.synchronize)
+    assert all(torch.isfinite(x).all() for x in want)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert cpa().cp_check_device_status() == 0
+
+
 def test_wrapper_refusals():
     s = {a: b.cuda() for a, b in make([5, 5], 4, 2, 64, 16, BF, seed=0).items()}
     out, lse = torch.empty_like(s["q"]), torch.empty((2, 4), device="cuda")

@@ -283,6 +283,26 @@ def test_many_batches_a_warp(D, H, Hkv, dt, gdt):
     assert cpa().cp_check_device_status() == 0
 
 
+def test_offsets_past_32_bits():
+    s = make(2, 3, 4, 1, 64, BF, 32, 1, seed=8, wdt=BF)
+    want, grads = run_fwd(s), run_bwd(s)
+    wide = 1 << 32   # elements from one batch entry to the next
+    buf = torch.empty(wide + (1 << 16), dtype=BF, device="cuda")
+
+    def far(x, at):
+        y = buf.as_strided(x.shape, (wide, *x.stride()[1:]), at)
+        y.copy_(x)
+        return y
+
+    q, k, gq, gk = (far(s[n].cuda(), i << 13) for i, n in enumerate(("q", "k", "gq", "gk")))
+    o = [far(torch.zeros_like(x), (4 + i) << 13) for i, x in enumerate((q.contiguous(), k.contiguous()))]
+    cpa().cp_qk_norm_rope_fwd(q, k, *o, **kw(s))
+    assert all(torch.equal(a, b) for a, b in zip(o, want))
+    w = [torch.empty(64, device="cuda") for _ in range(2)]
+    cpa().cp_qk_norm_rope_bwd(q, k, gq, gk, *o, dq_weight=w[0], dk_weight=w[1], **kw(s))
+    assert all(torch.equal(a, b) for a, b in zip((*o, *w), grads))
+
+
 @pytest.mark.parametrize("dt", [BF, F4])
 def test_queries_alone_and_nothing_at_all(dt):
     s = make(2, 9, 3, 1, 64, dt, 32, 1, seed=6, wdt=F4)
