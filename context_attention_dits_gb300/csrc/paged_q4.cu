@@ -291,6 +291,13 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
+// Four such tiles from shared memory, of rows that the lanes name, eight each, transposed.
+__device__ __forceinline__ void load_transposed(uint32_t at, uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(a), "=r"(b), "=r"(c), "=r"(d)
+               : "r"(at)
+               : "memory");
+}
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -543,13 +550,9 @@ struct Q4Unit {
     // exponent (biased) of the largest value scale so far, and what brings it below 2^15: o is in units of 2^(top - 141)
     int top = 27;
     float fit = power_of_2(141 - 27);
-    // Row r of a 16-key tile is key turn(r): neighbours change places in every other
-    // pair, so that the lanes of a quarter that read v's rows differ in parity
-    auto turn = [](int r) { return r ^ (r >> 1 & 1); };
-    const int kr = turn(g), va = turn(2 * tq), vb = turn(2 * tq + 1);
-    const uint8_t* krow = wbuf + kr * kRowB + tq * 8;
-    const uint8_t* zrow = wbuf + kCodes + kr * kScaleB;
-    const uint8_t *vrow_a = wbuf + kCodes + kScales + va * kRowB + g * 4, *vrow_b = wbuf + kCodes + kScales + vb * kRowB + g * 4;
+    const uint8_t* krow = wbuf + g * kRowB + tq * 8;
+    const uint8_t* zrow = wbuf + kCodes + g * kScaleB;
+    const uint32_t vrows = smem_addr(wbuf) + kCodes + kScales + ((lane & 7) + (lane >> 4) * 8) * kRowB + (lane & 8) * 2;
     auto scales = [](const uint8_t* p, uint32_t (&w)[kGroups]) {
       if constexpr (kGroups == 2) {
         const uint2 v = *reinterpret_cast<const uint2*>(p);
@@ -652,7 +655,7 @@ struct Q4Unit {
         }
       }
       if (a.slopes) {
-        const float dist = static_cast<float>(n - 1 - chunk * kChunk - kr);
+        const float dist = static_cast<float>(n - 1 - chunk * kChunk - g);
 #pragma unroll
         for (int t = 0; t < kT; ++t)
 #pragma unroll
@@ -667,7 +670,7 @@ struct Q4Unit {
           for (int r = 0; r < 2; ++r)
 #pragma unroll
             for (int x = 0; x < kTiles; ++x)
-              if (!(on >> (kr + 16 * t + 8 * r) & 1u)) s[t][x][r] = twice(-INFINITY);
+              if (!(on >> (g + 16 * t + 8 * r) & 1u)) s[t][x][r] = twice(-INFINITY);
 
       // ---- weights ----
       float2 f[kTiles];
@@ -756,13 +759,10 @@ struct Q4Unit {
 #pragma unroll
         for (int t = 0; t < kT; ++t) {
           const int at = stage + 16 * t * kRowB + y * 32;
-          const uint32_t w0 = *reinterpret_cast<const uint32_t*>(vrow_a + at);
-          const uint32_t w1 = *reinterpret_cast<const uint32_t*>(vrow_b + at);
-          const uint32_t w2 = *reinterpret_cast<const uint32_t*>(vrow_a + at + 8 * kRowB);
-          const uint32_t w3 = *reinterpret_cast<const uint32_t*>(vrow_b + at + 8 * kRowB);
-          // two keys' codes side by side: 0 .. 3 of the word, and 4 .. 7
-          uint32_t a01 = __byte_perm(w0, w1, 0x5410), b01 = __byte_perm(w0, w1, 0x7632);
-          uint32_t a23 = __byte_perm(w2, w3, 0x5410), b23 = __byte_perm(w2, w3, 0x7632);
+          // two keys' codes side by side: values 4 g to 4 g + 3, and those 32 behind them (rows
+          // 64 bytes apart meet four to a bank here, which costs less than eight instructions a tile)
+          uint32_t a01, b01, a23, b23;
+          load_transposed(vrows + at, a01, b01, a23, b23);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             if (j == 2) a01 >>= 8, b01 >>= 8, a23 >>= 8, b23 >>= 8;
@@ -833,9 +833,9 @@ struct Q4Unit {
             out[j] = fmaf(column(o[x][y][j][0]) * codes, unit, z);
             out[j + 4] = fmaf(column(o[x][y][j][1]) * codes, unit, z);
           }
-#pragma unroll
-          for (int j = 0; j < 8; j += 2)
-            *reinterpret_cast<float2*>(w + r * kD + y * kQ4Group + g * 8 + j) = make_float2(out[j], out[j + 1]);
+          float4* const to = reinterpret_cast<float4*>(w + r * kD + y * kQ4Group + g * 4);
+          to[0] = make_float4(out[0], out[1], out[2], out[3]);
+          to[8] = make_float4(out[4], out[5], out[6], out[7]);
         }
         if (g == 0) {
           w[kRows * kD + 2 * r] = mm;
@@ -874,9 +874,9 @@ struct Q4Unit {
 // The list: all units' chunks, cut into equal contiguous ranges, one per warp. A warp
 // waits for no other: units within its range it writes out, the one that began before
 // and the one that goes on it leaves as partials, for the join.
-// 2 x 262144 keys, 32 heads on 4 of 128, bf16, capped: 70 us with the join, 4.3 TB/s of
+// 2 x 262144 keys, 32 heads on 4 of 128, bf16, capped: 69 us with the join, 4.4 TB/s of
 // the cache; the copies alone, with nothing formed of them, take 54. Instructions bound
-// it: a warp takes 19 for a key and head (128 codes of k and of v, 8 query heads), most
+// it: a warp takes 18 for a key and head (128 codes of k and of v, 8 query heads), most
 // of them to make operands of codes. More warps a multiprocessor make it slower: shorter
 // steps have more overhead a key, and longer ones spill (three CTAs: 72 us; three of 32
 // keys a step: 79, four: 86).
