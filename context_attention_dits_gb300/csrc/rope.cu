@@ -10,7 +10,7 @@
 //
 // Every value is read once and written once and costs some ten operations, so HBM
 // bounds the long calls (2 or 3 streams; 32768 tokens of 24 + 24 heads of 128, bf16,
-// take 130 us forward, 6.2 TB/s, and 4608 take 22.4, some 4 of them start and end) and
+// take 130 us forward, 6.2 TB/s, and 4608 take 21.7, some 4 of them start and end) and
 // the launch the short ones. A row lies in D / 8 lanes, 8 values each: its sums take 3
 // or 4 shuffles, and a lane holds both members of its four pairs, by one 16-byte piece
 // where pairs are neighbours and two pieces of 8 where they are the row's halves. A
@@ -240,16 +240,19 @@ __device__ __forceinline__ int64_t row_at(const RopeRows& x, int b, int s, int h
 
 // A warp's rows on their way through shared memory: batches of up to kBatch heads of a
 // token (kB > 0: of two tensors), kStages - 1 of them under way while one is worked on,
-// 2 KB (kB: 4 KB) each. As many loads in registers would halve the warps: 4608 tokens of
-// 24 + 24 heads of 128, bf16, with four rows in registers: forward 24.0 us where this
-// takes 22.4, backward 37.8 where this takes 34.7 (32768 tokens forward: 133.8, 130.2).
+// 2 KB (kB: 4 to 6 KB) each. As many loads in registers would halve the warps: 4608
+// tokens of 24 + 24 heads of 128, bf16, with four rows in registers: forward 24.0 us where
+// this takes 21.7, backward 37.8 where this takes 33.2 (32768 tokens forward: 134, 131).
 // A warp with one batch in all gains nothing (700 tokens of 6 + 3 fp32 heads, backward:
 // 7.7 us from registers, 8.5 here).
 template <int D, int kElemA, int kElemB>
 struct Ring {
-  static constexpr int kRows = 256 / D, kSteps = kElemA == 2 ? 4 : 2, kBatch = kRows * kSteps;
+  // (backward of 4607 tokens with six steps 33.2 us, with four 34.0; forward of 4608 tokens
+  // with three stages 21.7, with four or two 22.4; of 32768 131, 131 and 127)
+  static constexpr int kSteps = kElemA != 2 ? 2 : kElemB == 2 && D == 128 ? 6 : 4;
+  static constexpr int kRows = 256 / D, kBatch = kRows * kSteps;
   static constexpr int kA = kBatch * D * kElemA, kB = kBatch * D * kElemB, kStage = kA + kB;
-  static constexpr int kStages = kElemB ? 2 : 4;
+  static constexpr int kStages = kElemB ? 2 : 3;
   static constexpr int kSmem = kRopeWarps * kStages * kStage;
   static_assert(kBatch <= 16, "a lane a row and tensor");
   struct Shared {
