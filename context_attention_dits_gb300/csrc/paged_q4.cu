@@ -130,12 +130,16 @@ __device__ __forceinline__ uint2 quantise(const float (&x)[16], uint32_t& scale)
   }
   float2 c[8];  // codes i and i + 8
   if (kB16 && __all_sync(0xffffffffu, exact)) {
+    // r - s / 2 is 0 or 2^-19.1 s at least (the values' unit, and that of s, of which all
+    // are multiples), so r times a little more than 1 / s rounds to 1 just where r is half
+    // a step or more; and r > - s / 2, since the first quotient was too small
+    const float2 more = twice(rcp_approx(s) * (1 + 0x1p-21f));
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float2 d = add2(make_float2(x[i], x[i + 8]), zz);
-      const float2 g = add2(fma2(d, rs, twice(kOne)), twice(-kOne));
-      const float2 r = fma2(g, down, d);  // exact: d - c s, within a step
-      c[i] = add2(g, make_float2(at_least(r.x, half), at_least(r.y, half)));
+      const float2 g = fma2(d, rs, twice(kOne));
+      const float2 r = fma2(add2(g, twice(-kOne)), down, d);  // exact: d - c s, within a step
+      c[i] = add2(fma2(r, more, g), twice(-kOne));
     }
   } else {  // what the difference has lost decides where the rest is half a step
 #pragma unroll
