@@ -173,8 +173,8 @@ __device__ __forceinline__ void token_head(const PagedArgs& a, int row, int& t, 
 // Rows (token, head) of sequence blockIdx.y: a warp takes 512 / D of them, 16 values a
 // lane. Bound by instructions, so the work that a group takes once is spread over few
 // lanes (8 values a lane: 31.6 us where 16 took 26.3), and keys and values share the
-// look-up of their place (a CTA of either alone: 26.3 us where this takes 22.9: some
-// 17000 new tokens of 6 sequences, 8 heads of 128, bf16: 3.9 TB/s of rows and codes).
+// look-up of their place (a CTA of either alone: 26.3 us where both took 22.9; now 22.2: some
+// 17000 new tokens of 6 sequences, 8 heads of 128, bf16, 4.0 TB/s of rows and codes).
 template <int D, typename T>
 __global__ void __launch_bounds__(kRowThreads) q4_append_kernel(const __grid_constant__ PagedArgs a) {
   constexpr int kLanes = D / 16;
