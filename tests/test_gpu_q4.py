@@ -305,29 +305,23 @@ def test_decode_scores_of_fp32_queries():
 
 @pytest.mark.parametrize("D,n", [(64, 50000), (128, 20000)])
 def test_decode_answers_of_fp32_queries(D, n):
-    """Answers over long tables are as good as fp32 arithmetic's: errors of many keys must not lean to one side.
+    """Errors of many keys do not lean to one side, where answers are small beside the values they are summed of.
 
-    The root mean square of the distances from float64 is compared with that of the plain form in fp32 (a product with the
-    cached values, exponentials, a product); twice that is the bound, both being some 2^-22 of |out| where nothing leans.
+    Weights near one another and values about zero. A weight is off by 2^-22 of the exponential, 2^-22 of its two parts and
+    some 2^-22 of a score below 2, each at random: together 2^-21 at most as a root mean square, and of answers, sums of as
+    many values at random, no more. What leans would count once for each key: sqrt(n) times as much beside them.
     """
-    H, Hkv = 4, 2
+    H, Hkv, scale = 4, 2, D ** -0.5 / 16
     s = make([n], H, Hkv, D, 256, F4, seed=3)
-    s["vs"][..., 1] = -7.5 * s["vs"][..., 0].float()   # values about zero: answers are what is left of many keys
-    out, _ = decode(s, D ** -0.5, F4)
-    rows = {}
-    for x in ("k", "v"):
-        p = s["table"][0].long()
-        at = lambda t: t[p].transpose(1, 2).flatten(0, 1)[:n]
-        rows[x] = torch.from_numpy(q4.values(at(s[x + "c"]), at(s[x + "s"]))).repeat_interleave(H // Hkv, 1)   # [n, H, D]
-
-    def answer(dt):
-        k, v, q = rows["k"].to(dt), rows["v"].to(dt), s["q"][0].to(dt)
-        w = torch.softmax(torch.einsum("hd,nhd->hn", q, k) * D ** -0.5, 1)
-        return torch.einsum("hn,nhd->hd", w, v).double()
-
-    want = answer(torch.float64)
-    rms = lambda x: float((x - want).square().mean().sqrt())
-    assert rms(out[0].double()) <= 2 * max(rms(answer(torch.float32)), 2.0 ** -22 * float(want.square().mean().sqrt()))
+    s["vs"][..., 1] = -7.5 * s["vs"][..., 0].float()
+    out, _ = decode(s, scale, F4)
+    page = s["table"][0].long()
+    at = lambda t: t[page].transpose(1, 2).flatten(0, 1)[:n]
+    k, v = (torch.from_numpy(q4.values(at(s[x + "c"]), at(s[x + "s"]))).repeat_interleave(H // Hkv, 1) for x in "kv")
+    w = torch.softmax(torch.einsum("hd,nhd->hn", s["q"][0].double(), k) * scale, 1)
+    want = torch.einsum("hn,nhd->hd", w, v)
+    rms = lambda x: float(x.square().mean().sqrt())
+    assert rms(out[0].double() - want) <= 2.0 ** -21 * rms(want)
 
 
 @pytest.mark.parametrize("dt", [BF, F4])
