@@ -319,14 +319,16 @@ __device__ __forceinline__ float plus_offset(float x, uint32_t w) {
   return y;
 }
 
-// Two codes (bits 0..3 of each half, or 4..7: kHigh) as fp16 numbers c - 8.
-template <bool kHigh>
-__device__ __forceinline__ uint32_t centred(uint32_t w) {
+// Codes i and i + 4 of a word of 8 (i known when compiled) as fp16 numbers c - 8: a code
+// put into the mantissa of 1024 is 1024 + c (or 1024 + 16 c), and the rest is taken off.
+// (The usual way from short integers to floating point: the bits of a fixed exponent.)
+__device__ __forceinline__ uint32_t codes(uint32_t w, int i) {
   uint32_t x;
-  if (!kHigh) {  // 1024 + c
+  if (i & 2) w >>= 8;
+  if (!(i & 1)) {
     asm("lop3.b32 %0, %1, 0x000f000f, 0x64006400, 0xea;" : "=r"(x) : "r"(w));
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(x) : "r"(x), "r"(0x64086408u));  // 1032
-  } else {  // 1024 + 16 c
+  } else {
     asm("lop3.b32 %0, %1, 0x00f000f0, 0x64006400, 0xea;" : "=r"(x) : "r"(w));
     asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(x) : "r"(x), "r"(0x2c002c00u), "r"(0xd480d480u));  // / 16, - 72
   }
@@ -350,16 +352,17 @@ struct Part {
   int b, n, hk, hg, first, last, step;
 };
 
-// bf16 queries: one fp16 part of q and of the weights, and codes as they lie: the
-// bits of c, in fp16, are the (subnormal) number c 2^-24, those of 16 c another 16
-// times as large, so that a word of 8 codes takes five instructions. With them v's
-// products come to sum p s c; what the centre takes off, 8 sum p s of the same
-// rounded weights, is the product with a row of ones. fp32 queries: two parts of each,
-// whose products leave 2^-22 out, and codes as c - 8 from the start, since a sum of
-// numbers above zero would lose more to the instruction's truncation. The upper part of
-// q is cut to multiples of 16 of at most 2^15, so that its products with codes and
-// their sums over a group are whole numbers of 20 bits, which nothing truncates (with
-// parts of 11 bits each wherever they lie, scores were ten times as far off as fp32's).
+// Codes come as c - 8: the instruction aligns products by the exponents that its operands
+// name and truncates, so that sums of numbers above zero lean, and those of subnormal
+// operands, which name one too large, the more. (The bits of c as they lie are the fp16
+// number c 2^-24 and take one instruction less a pair: 2 x 262144 keys 69 us where this
+// takes 75.6. But answers of so many keys leaned by 4e-4 of themselves, where the weights'
+// rounding costs 7e-5, and scores were 4e-7 off, here 8e-8.)
+// bf16 queries: one fp16 part of q and of the weights. fp32 queries: two parts of each,
+// whose products leave 2^-22 out; the upper part of q is cut to multiples of 16 of at
+// most 2^15, so that its products with codes and their sums over a group are whole
+// numbers of 20 bits, which nothing truncates (with parts of 11 bits each wherever they
+// lie, scores were ten times as far off as fp32's).
 template <int D_, bool kF32, int kTiles, int kChunk>
 struct Q4Unit {
   static constexpr int kT = kChunk / 16;  // tiles of a warp's keys in a step
@@ -517,9 +520,9 @@ struct Q4Unit {
         for (int st = 0; st < 4; ++st)
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            // codes i and i + 4 of a word of 8; as they lie, those of odd i come times 16
+            // codes i and i + 4 of a word of 8
             const int i = (st >> 1) * 8 + (st & 1) * 2 + r;
-            const float up = power_of_2(r && !kF32 ? 10 - e : 14 - e), lo = v[y][i] * up, hi = v[y][i + 4] * up;
+            const float up = power_of_2(14 - e), lo = v[y][i] * up, hi = v[y][i + 4] * up;
             if constexpr (!kF32) {
               qf[x][y][st][0][r] = pack_f16x2(lo, hi);
             } else {
@@ -531,7 +534,7 @@ struct Q4Unit {
       auto column = [&](float z) {  // of heads 2 tq and 2 tq + 1, from the lanes that hold heads g
         return make_float2(__shfl_sync(0xffffffffu, z, 8 * tq), __shfl_sync(0xffffffffu, z, 8 * tq + 4));
       };
-      undo[x] = column(power_of_2(kF32 ? e - 14 : e + 10) * unit_x);  // of 2^(14 - e), and 2^-24 of the codes as they lie
+      undo[x] = column(power_of_2(e - 14) * unit_x);
 #pragma unroll
       for (int y = 0; y < kGroups; ++y) qsum[x][y] = column(sum[y] * unit_x);
       const int hc = x * 8 + 2 * tq;
@@ -602,9 +605,9 @@ struct Q4Unit {
             for (int e = 0; e < 4; ++e) dot[x][y][e] = low[x][e] = 0.f;
 #pragma unroll
           for (int st = 0; st < 4; ++st) {
-            const uint32_t ua = (st >> 1 ? wa.y : wa.x) >> (st & 1 ? 8 : 0), ub = (st >> 1 ? wb.y : wb.x) >> (st & 1 ? 8 : 0);
-            const uint32_t a0 = kF32 ? centred<false>(ua) : ua & 0x000f000fu, a1 = kF32 ? centred<false>(ub) : ub & 0x000f000fu;
-            const uint32_t a2 = kF32 ? centred<true>(ua) : ua & 0x00f000f0u, a3 = kF32 ? centred<true>(ub) : ub & 0x00f000f0u;
+            const uint32_t ua = st >> 1 ? wa.y : wa.x, ub = st >> 1 ? wb.y : wb.x;
+            const uint32_t a0 = codes(ua, 2 * (st & 1)), a1 = codes(ub, 2 * (st & 1));
+            const uint32_t a2 = codes(ua, 2 * (st & 1) + 1), a3 = codes(ub, 2 * (st & 1) + 1);
 #pragma unroll
             for (int x = 0; x < kTiles; ++x) {
               if constexpr (kF32) mma_f16(low[x], a0, a1, a2, a3, qf[x][y][st][1][0], qf[x][y][st][1][1]);
@@ -626,7 +629,7 @@ struct Q4Unit {
             float2 d, zq;
 #pragma unroll
             for (int y = 0; y < kGroups; ++y) {
-              const float ks = __uint_as_float(w[y] << 16), kz = plus_offset(kF32 ? 8.f * ks : 0.f, w[y]);
+              const float ks = __uint_as_float(w[y] << 16), kz = plus_offset(8.f * ks, w[y]);
               const float d0 = dot[x][y][2 * r], d1 = dot[x][y][2 * r + 1];
               d.x = y ? fmaf(ks, d0, d.x) : ks * d0;
               d.y = y ? fmaf(ks, d1, d.y) : ks * d1;
@@ -755,13 +758,13 @@ struct Q4Unit {
           }
         // (fp32: the lower parts' products apart, or the instruction drops them beside the upper ones':
         // 50000 keys were then 1.2e-6 of the result off, now 3e-7)
-        float add[kTiles][4][4], low[kTiles][4][4], ones[kTiles][4];
+        float add[kTiles][4][4], low[kTiles][4][4];
 #pragma unroll
         for (int x = 0; x < kTiles; ++x)
 #pragma unroll
           for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) add[x][j][e] = low[x][j][e] = ones[x][e] = 0.f;
+            for (int e = 0; e < 4; ++e) add[x][j][e] = low[x][j][e] = 0.f;
 #pragma unroll
         for (int t = 0; t < kT; ++t) {
           const int at = stage + 16 * t * kRowB + y * 32;
@@ -771,39 +774,24 @@ struct Q4Unit {
           load_transposed(vrows + at, a01, b01, a23, b23);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            if (j == 2) a01 >>= 8, b01 >>= 8, a23 >>= 8, b23 >>= 8;
-            auto codes = [&](uint32_t w) {
-              if constexpr (!kF32) return w & (j & 1 ? 0x00f000f0u : 0x000f000fu);
-              return j & 1 ? centred<true>(w) : centred<false>(w);
-            };
-            const uint32_t a0 = codes(a01), a1 = codes(b01), a2 = codes(a23), a3 = codes(b23);
+            const uint32_t a0 = codes(a01, j), a1 = codes(b01, j), a2 = codes(a23, j), a3 = codes(b23, j);
 #pragma unroll
             for (int x = 0; x < kTiles; ++x) {
               mma_f16(add[x][j], a0, a1, a2, a3, pf[x][t][0][0], pf[x][t][0][1]);
               if constexpr (kF32) mma_f16(low[x][j], a0, a1, a2, a3, pf[x][t][1][0], pf[x][t][1][1]);
             }
           }
-          if constexpr (!kF32)
-#pragma unroll
-            for (int x = 0; x < kTiles; ++x)
-              mma_f16(ones[x], 0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u, pf[x][t][0][0], pf[x][t][0][1]);
         }
 #pragma unroll
-        for (int x = 0; x < kTiles; ++x) {
-          // (codes 2^-24 of themselves: so is o, until the end)
-          const float2 off = mul2(make_float2(ones[x][0], ones[x][1]), twice(-0x1p-21f));
+        for (int x = 0; x < kTiles; ++x)
 #pragma unroll
           for (int j = 0; j < 4; ++j)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const float2 more = make_float2(add[x][j][2 * e], add[x][j][2 * e + 1]);
               float2& to = o[x][y][j][e];
-              if constexpr (kF32)
-                to = add2(fma2(to, f[x], more), make_float2(low[x][j][2 * e], low[x][j][2 * e + 1]));
-              else
-                to = fma2(more, twice(j & 1 ? 0.0625f : 1.f), fma2(to, f[x], off));
+              to = fma2(to, f[x], make_float2(add[x][j][2 * e], add[x][j][2 * e + 1]));
+              if constexpr (kF32) to = add2(to, make_float2(low[x][j][2 * e], low[x][j][2 * e + 1]));
             }
-        }
       }
       phase ^= 1u << take;
       if (++take == kStages) take = 0;
@@ -823,7 +811,7 @@ struct Q4Unit {
     // ---- this warp's state into its buffers ----
     // (not where the next copies go)
     float* const w = reinterpret_cast<float*>(wbuf + (kAhead && following && take == 0 ? kStage : 0));
-    const float unit = power_of_2(top - 141), codes = kF32 ? 1.f : 0x1p24f;
+    const float unit = power_of_2(top - 141);
 #pragma unroll
     for (int x = 0; x < kTiles; ++x) {
       auto keep = [&](int r, float mm, float ll, const float (&zz)[kGroups], auto column) {
@@ -837,8 +825,8 @@ struct Q4Unit {
           float out[8];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            out[j] = fmaf(column(o[x][y][j][0]) * codes, unit, z);
-            out[j + 4] = fmaf(column(o[x][y][j][1]) * codes, unit, z);
+            out[j] = fmaf(column(o[x][y][j][0]), unit, z);
+            out[j + 4] = fmaf(column(o[x][y][j][1]), unit, z);
           }
           float4* const to = reinterpret_cast<float4*>(w + r * kD + y * kQ4Group + g * 4);
           to[0] = make_float4(out[0], out[1], out[2], out[3]);
@@ -881,7 +869,7 @@ struct Q4Unit {
 // The list: all units' chunks, cut into equal contiguous ranges, one per warp. A warp
 // waits for no other: units within its range it writes out, the one that began before
 // and the one that goes on it leaves as partials, for the join.
-// 2 x 262144 keys, 32 heads on 4 of 128, bf16, capped: 69 us with the join, 4.4 TB/s of
+// 2 x 262144 keys, 32 heads on 4 of 128, bf16, capped: 75.5 us with the join, 4.0 TB/s of
 // the cache; the copies alone, with nothing formed of them, take 54. Instructions bound
 // it: a warp takes 18 for a key and head (128 codes of k and of v, 8 query heads), most
 // of them to make operands of codes. More warps a multiprocessor make it slower: shorter

@@ -621,10 +621,11 @@ cp_status cp_paged_kv_read_q4(const cp_q4_cache* cache, const int32_t* seq_lens,
 size_t cp_paged_attn_q4_workspace_size(int B, int H, int Hkv, int D, int page_size, int max_pages, cp_dtype dt);
 
 /*
- * Attention of one new token per sequence: as cp_paged_attn_decode. Scores are formed
- * from the codes exactly; the weights, times the values' scales, are rounded to fp16
- * (fp32 q: to 22 bits; what lies below 2^-39 of the largest scale met so far is lost)
- * and summed in fp32. q, and k and v as they were appended, are
+ * Attention of one new token per sequence: as cp_paged_attn_decode. Codes and
+ * bf16 q enter the products unrounded (fp32 q: 22 bits; what lies below 2^-39 of a head's
+ * largest value is lost), and sums are fp32; the weights, times the values' scales, are
+ * rounded to fp16 (fp32 q: to 22 bits; what lies below 2^-39 of the largest scale met so
+ * far is lost) and summed in fp32. q, and k and v as they were appended, are
  * finite and at most 2^96. Errors: INVALID_ARG, NOT_DIVISIBLE (H % Hkv), ALIGNMENT,
  * WORKSPACE, CUDA, UNSUPPORTED_DEVICE.
  */

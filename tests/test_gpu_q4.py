@@ -324,6 +324,40 @@ def test_decode_answers_of_fp32_queries(D, n):
     assert rms(out[0].double() - want) <= 2.0 ** -21 * rms(want)
 
 
+@pytest.mark.parametrize("H,Hkv,D", [(24, 8, 128), (32, 4, 128), (32, 2, 64)])
+def test_decode_answers_of_bf16_queries(H, Hkv, D):
+    """The same for bf16 queries, whose weights times scales are rounded to fp16, and for each place of a code in its word.
+
+    A rounding is off by 2^-11 of its weight at most, spread evenly over that by 2^-11 / sqrt(3), and at random, so that
+    answers of as many values at random about zero are off by 2^-11.8 of their size as a root mean square; 2^-11 is the
+    bound. Values stand for z + s c = s (c - 7.5) and are summed as s (c - 8) and s / 2, so the mean of those errors over
+    the values of one place (every fourth of a head) has a part that a head's values share, 0.5 / 4.6 of an error, and a
+    part of each value: together sqrt(0.11^2 / H + 4 / (H D)) of 2^-11.8, of which four times is the bound. What leans adds
+    up over the keys and passes it. (Weights differ by powers of e, so that a product has neighbours of other sizes.)
+    """
+    n, scale = 1 << 18, D ** -0.5
+    s = make([n], H, Hkv, D, 256, BF, seed=3)
+    s["vs"][..., 1] = -7.5 * s["vs"][..., 0].float()
+    out, _ = decode(s, scale, F4)
+    page = s["table"][0].long()
+
+    def rows(x, hk):  # of a head, float64
+        c, sz = (s[x + a][page, hk].cuda().flatten(0, 1)[:n] for a in "cs")
+        sz = sz.double().repeat_interleave(64, 1)
+        return sz[..., 1] + sz[..., 0] * torch.stack((c & 15, c >> 4), -1).flatten(1)
+
+    want = torch.empty((H, D), dtype=torch.float64)
+    for hk in range(Hkv):
+        at = slice(hk * H // Hkv, (hk + 1) * H // Hkv)
+        x = s["q"][0, at].double().cuda() @ rows("k", hk).T * scale
+        want[at] = (torch.softmax(x, 1) @ rows("v", hk)).cpu()
+    off = out[0].double() - want
+    rms = lambda x: float(x.square().mean().sqrt())
+    assert rms(off) <= 2.0 ** -11 * rms(want)
+    lean = off.unflatten(1, (-1, 4)).mean((0, 1)).abs().max()
+    assert float(lean) <= 4 * (0.11 ** 2 / H + 4 / (H * D)) ** 0.5 * 2.0 ** -11.8 * rms(want)
+
+
 @pytest.mark.parametrize("dt", [BF, F4])
 @pytest.mark.parametrize("H,Hkv", [(4, 2), (10, 1)])
 def test_decode_scales_and_queries_of_any_size(dt, H, Hkv):
