@@ -75,6 +75,17 @@ struct Workspace {
   }
 };
 
+// The library's call, without Python's lock: a launch waits where the stream's queue is
+// full, perhaps for a host function that needs the lock. (The arguments' tensors are held
+// by the caller, and what `call` uses has been read from them.)
+template <class F>
+PyObject* unlocked(F call) {
+  PyThreadState* const state = PyEval_SaveThread();
+  const cp_status st = call();
+  PyEval_RestoreThread(state);
+  return PyLong_FromLong(st);
+}
+
 void* stream_of(int index) { return c10::cuda::getCurrentCUDAStream(index).stream(); }
 
 #define CP_FUNCTIONS(X)                                                                         \
@@ -89,7 +100,7 @@ CP_FUNCTIONS(CP_DECLARE)
 // queries and keys between their projections and the attention
 // ---------------------------------------------------------------------------
 struct Heads {
-  const at::Tensor* t;
+  void* p;  // (of an empty tensor nullptr, with which the library does nothing)
   int64_t strides[3];
 };
 // [B, S, heads, D] of a type, a head's values dense
@@ -99,17 +110,14 @@ void heads(Heads* h, int index, c10::ScalarType type, at::IntArrayRef shape, con
   on(index, t);
   const auto st = t.strides();
   if (st[3] != 1) bad_value("the values of a head must be dense");
-  h->t = &t;
+  h->p = t.data_ptr();
   for (int i = 0; i < 3; ++i) h->strides[i] = st[i];
 }
 
-const int64_t* flat(int64_t* to, std::initializer_list<const Heads*> all) {
-  int64_t* p = to;
+void flat(int64_t* to, std::initializer_list<const Heads*> all) {
   for (const Heads* h : all)
-    for (int i = 0; i < 3; ++i) *p++ = h->t ? h->strides[i] : 0;
-  return to;
+    for (int i = 0; i < 3; ++i) *to++ = h->p ? h->strides[i] : 0;
 }
-void* address(const Heads& h) { return h.t ? h.t->data_ptr() : nullptr; }
 
 struct Qk {
   int index, B, S, H, Hkv, D;
@@ -200,9 +208,12 @@ PyObject* qk_norm_rope_fwd(PyObject* const* a) {
   }
   int64_t st[12];
   const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(c.index));
-  return PyLong_FromLong(cp_qk_norm_rope_fwd_p(address(q), address(k), address(qo), address(ko),
-                                               flat(st, {&q, &k, &qo, &ko}), c.B, c.S, c.H, c.Hkv, c.D, &c.rule, c.dt,
-                                               stream_of(c.index)));
+  flat(st, {&q, &k, &qo, &ko});
+  void* const s = stream_of(c.index);
+  return unlocked([&] {
+    return cp_qk_norm_rope_fwd_p(q.p, k.p, qo.p, ko.p, st, c.B, c.S, c.H, c.Hkv, c.D, &c.rule,
+                                 c.dt, s);
+  });
 }
 
 // q, k, dq_out, dk_out, dq, dk, the rule's seven, dq_weight, dk_weight, workspace
@@ -232,9 +243,13 @@ PyObject* qk_norm_rope_bwd(PyObject* const* a) {
   const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(c.index));
   const Workspace ws(a[15], w[0] || w[1] ? cp_qk_norm_rope_bwd_workspace_size_p(c.D) : 0, c.index);
   int64_t st[18];
-  return PyLong_FromLong(cp_qk_norm_rope_bwd_p(address(q), address(k), address(gq), address(gk), address(dq), address(dk),
-                                               w[0], w[1], flat(st, {&q, &k, &gq, &gk, &dq, &dk}), c.B, c.S, c.H, c.Hkv,
-                                               c.D, &c.rule, ws.p, ws.bytes, c.dt, type_of(gtype), stream_of(c.index)));
+  flat(st, {&q, &k, &gq, &gk, &dq, &dk});
+  const cp_dtype gdt = type_of(gtype);
+  void* const s = stream_of(c.index);
+  return unlocked([&] {
+    return cp_qk_norm_rope_bwd_p(q.p, k.p, gq.p, gk.p, dq.p, dk.p, w[0], w[1], st,
+                                 c.B, c.S, c.H, c.Hkv, c.D, &c.rule, ws.p, ws.bytes, c.dt, gdt, s);
+  });
 }
 
 // ---------------------------------------------------------------------------
@@ -291,9 +306,9 @@ PyObject* paged_kv_append_q4(PyObject* const* a) {
   const at::Tensor* news = maybe(a[8]);
   const int32_t* new_lens = news ? ints(index, *news, {&B, 1}, "new_lens must be [B]") : nullptr;
   const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(index));
-  return PyLong_FromLong(cp_paged_kv_append_q4_p(k.data_ptr(), v.data_ptr(), &c, lens, new_lens, size_of(B),
-                                                 size_of(k.size(1)), size_of(k.size(2)), size_of(k.size(3)), dt,
-                                                 stream_of(index)));
+  const int b = size_of(B), t = size_of(k.size(1)), hkv = size_of(k.size(2)), d = size_of(k.size(3));
+  void *const kp = k.data_ptr(), *const vp = v.data_ptr(), *const s = stream_of(index);
+  return unlocked([&] { return cp_paged_kv_append_q4_p(kp, vp, &c, lens, new_lens, b, t, hkv, d, dt, s); });
 }
 
 // the cache's five, seq_lens, k_out, v_out
@@ -309,8 +324,9 @@ PyObject* paged_kv_read_q4(PyObject* const* a) {
   const cp_q4_cache c = cache_of(a, index, B, k.size(2), k.size(3));
   const int32_t* lens = ints(index, tensor(a[5]), {&B, 1}, "seq_lens must be [B]");
   const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(index));
-  return PyLong_FromLong(cp_paged_kv_read_q4_p(&c, lens, k.data_ptr(), v.data_ptr(), size_of(B), size_of(k.size(1)),
-                                               size_of(k.size(2)), size_of(k.size(3)), dt, stream_of(index)));
+  const int b = size_of(B), t = size_of(k.size(1)), hkv = size_of(k.size(2)), d = size_of(k.size(3));
+  void *const kp = k.data_ptr(), *const vp = v.data_ptr(), *const s = stream_of(index);
+  return unlocked([&] { return cp_paged_kv_read_q4_p(&c, lens, kp, vp, b, t, hkv, d, dt, s); });
 }
 
 // q, the cache's five, seq_lens, out, lse, scale, softcap, slopes, workspace
@@ -340,10 +356,13 @@ PyObject* paged_attn_decode_q4(PyObject* const* a) {
   const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(index));
   const int b = size_of(B), h = size_of(H), hkv = size_of(Hkv), d = size_of(D);
   const Workspace ws(a[12], cp_paged_attn_q4_workspace_size_p(b, h, hkv, d, c.page_size, c.max_pages, dt), index);
-  return PyLong_FromLong(cp_paged_attn_decode_q4_p(q.data_ptr(), &c, lens, out.data_ptr(),
-                                                   static_cast<float*>(lse.data_ptr()), b, h, hkv, d,
-                                                   static_cast<float>(scale), static_cast<float>(cap), slopes, ws.p, ws.bytes,
-                                                   dt, type_of(out.scalar_type()), stream_of(index)));
+  const cp_dtype out_dt = type_of(out.scalar_type());
+  void *const qp = q.data_ptr(), *const op = out.data_ptr(), *const s = stream_of(index);
+  float* const lp = static_cast<float*>(lse.data_ptr());
+  return unlocked([&] {
+    return cp_paged_attn_decode_q4_p(qp, &c, lens, op, lp, b, h, hkv, d, static_cast<float>(scale), static_cast<float>(cap),
+                                     slopes, ws.p, ws.bytes, dt, out_dt, s);
+  });
 }
 
 // ---------------------------------------------------------------------------
