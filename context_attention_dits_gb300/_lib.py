@@ -11,7 +11,6 @@ import os
 import threading
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "lib", "libcpattn.so")
-BIND_PATH = os.path.join(os.path.dirname(LIB_PATH), "_cpbind.so")
 
 # status codes (cp_status)
 CP_OK = 0
@@ -141,11 +140,14 @@ def bind():
     if _bind is None:
         with _lock:
             if _bind is None:
-                if not os.path.exists(BIND_PATH):
-                    raise RuntimeError(f"_cpbind.so is not built ({BIND_PATH}); run "
+                from .build import bind_path
+                path = bind_path()  # (torch is loaded now, and with it the libraries that the module needs)
+                if path is None:
+                    raise RuntimeError("these calls need a torch for CUDA")
+                if not os.path.exists(path):
+                    raise RuntimeError(f"the compiled marshalling is not built for this torch ({path}); run "
                                        "`python -m context_attention_dits_gb300.build`")
-                import torch  # noqa: F401  (its libraries)
-                spec = importlib.util.spec_from_file_location("_cpbind", BIND_PATH)
+                spec = importlib.util.spec_from_file_location("_cpbind", path)
                 module = importlib.util.module_from_spec(spec)
                 spec.loader.exec_module(module)
                 module.init(lib()._handle)

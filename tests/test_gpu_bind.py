@@ -27,12 +27,12 @@ def slow(tmp_path_factory):
     """The marshalling over a library whose calls take 0.3 s of host time and launch nothing."""
     if not torch.cuda.is_available():
         pytest.fail("CUDA device required for -m gpu tests")
-    from context_attention_dits_gb300 import _lib, build
+    from context_attention_dits_gb300 import build
     build.build()
     at = tmp_path_factory.mktemp("slow")
     (at / "slow.cpp").write_text(SLOW)
     subprocess.run(["g++", "-shared", "-fPIC", "-o", str(at / "libslow.so"), str(at / "slow.cpp")], check=True)
-    shutil.copy(_lib.BIND_PATH, at / "_cpbind.so")   # (a copy has names of its own)
+    shutil.copy(build.bind_path(), at / "_cpbind.so")   # (a copy has names of its own)
     spec = importlib.util.spec_from_file_location("_cpbind", str(at / "_cpbind.so"))
     module = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(module)
