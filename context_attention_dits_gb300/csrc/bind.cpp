@@ -283,8 +283,6 @@ cp_q4_cache cache_of(PyObject* const* a, int index, int64_t B, int64_t Hkv, int6
   c.v_codes = static_cast<uint8_t*>(t[2]->data_ptr());
   c.v_scales = t[3]->data_ptr();
   c.block_table = ints(index, table, {shape, 2}, "block_table must be [B, max_pages]");
-  // (an empty table has no address, and no entry that is read)
-  if (!c.block_table) c.block_table = reinterpret_cast<const int32_t*>(256);
   c.num_pages = size_of(pages);
   c.page_size = size_of(page);
   c.max_pages = size_of(shape[1]);

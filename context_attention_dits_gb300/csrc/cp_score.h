@@ -81,10 +81,9 @@ cudaError_t launch_score_fwd_f32(const ScoreArgs& a, int D, cudaStream_t s);
 cudaError_t launch_score_bwd_f32(const ScoreArgs& a, int D, cudaStream_t s);
 
 // The paged cache.
-constexpr int kPagedCtas = 304;     // decode CTAs at most: two on each of 152 multiprocessors
+constexpr int kPagedCtas = 304;     // CTAs over the list of blocks at most: two on each of 152 multiprocessors
 constexpr int kPagedBlock = 64;     // keys of one work block
 constexpr int kPagedMaxBatch = 4096;
-constexpr int kPagedMostCtas = 608;  // of any decode kernel: four on each of 152 multiprocessors
 struct PagedArgs {
   int B, T, H, Hkv, G, D;
   int num_pages, page_shift, max_pages;
@@ -102,7 +101,7 @@ struct PagedArgs {
   int out_bf16;
   float scale, cap;
   const float* slopes;
-  float* partial;  // workspace: [kPagedCtas][2] partial results
+  float* partial;  // workspace: [CTAs over the list; in 4 bits their warps][2] partial results
   int2* info;      // workspace: [B * Hkv * groups] which partials make up a unit
   int sms;         // multiprocessors of the device
   uint32_t* err;

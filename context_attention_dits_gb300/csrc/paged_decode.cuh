@@ -1,5 +1,7 @@
-// paged_decode.cuh — one-token attention over a paged cache: the work list, the
-// clusters and the joins, whatever a cached row is. A kernel's class C says the rest:
+// paged_decode.cuh — one-token attention over a paged cache. The clusters, the work
+// list's sums and the writing of results serve both caches; the kernel over the list and
+// its join serve paged.cu alone (paged_q4.cu cuts the list among warps and has its own).
+// A kernel's class C says what a cached row is:
 //   kD, kRows      head width, query heads of a unit (a sequence's key/value head and
 //                  a group of the query heads that share it)
 //   kBlock         keys of a work block, of which each of the CTA's warps has a part
@@ -203,7 +205,7 @@ __global__ void __launch_bounds__(kDecThreads, C::kPerSm) paged_decode_kernel(co
 // 32 loads under way (a dependent walk over 32 partials took 10 us).
 template <int D>
 __global__ void __launch_bounds__(D) paged_join_kernel(const __grid_constant__ PagedArgs a, int rows) {
-  __shared__ float weight[kPagedMostCtas];
+  __shared__ float weight[kPagedCtas];
   __shared__ float red[2][D / 32];
   const int h = blockIdx.x, b = blockIdx.y, d = threadIdx.x, warp = d >> 5;
   grid_wait();
@@ -371,11 +373,12 @@ cudaError_t launch_clustered(const PagedArgs& a, int cs, cudaStream_t s) {
   return launch_clusters(paged_decode_cluster_kernel<C>, units, a.B, 1, cs, kDecThreads, C::kSmem, C::kEarly, s, a);
 }
 
-// At most `ctas` CTAs over the list, and the join of what they leave.
+// At most `ctas` (kPagedCtas or fewer) CTAs over the list, and the join of what they leave.
 template <class C>
 cudaError_t launch_listed(const PagedArgs& a, int ctas, cudaStream_t s) {
   constexpr int D = C::kD;
   static_assert(C::kSmem + (kPagedMaxBatch + 8) * 4 <= 227 * 1024, "shared memory budget");
+  if (ctas > kPagedCtas) return cudaErrorInvalidValue;  // (what the workspace and the join hold)
   cudaError_t e;
   if ((e = allow_smem<paged_decode_kernel<C>>(C::kSmem + (kPagedMaxBatch + 1) * 4)) != cudaSuccess) return e;
   // blocks of the list if every table were full; a unit of one block is never split
