@@ -91,6 +91,15 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity,
   }
 }
 
+// A wait for a copy under way after another wait has run out: as long as a copy could
+// take at all, whatever the limit of that one was, since its target changes hands then.
+constexpr uint64_t kDrainNs = 1000000000ull;
+__device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity) {
+  const uint64_t t0 = global_timer_ns();
+  while (!mbar_try_wait(bar, parity) && global_timer_ns() - t0 < kDrainNs) {
+  }
+}
+
 // ----------------------------------------------------------------------------
 // Overlap of a launch with its predecessor's end (programmatic launches): the
 // predecessor lets its successor start; the successor waits for all of the

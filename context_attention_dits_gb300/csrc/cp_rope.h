@@ -40,6 +40,7 @@ struct RopeArgs {
   float *dwq, *dwk;
   uint32_t* err;        // device error word, and the bound on each wait
   uint64_t timeout_ns;
+  uint32_t stall;       // 0; in tests, warps of each CTA (a bit each) whose copies never count as done
   uint8_t axis[kRopeMaxPairs];  // of each pair
 };
 

@@ -107,6 +107,7 @@ struct PagedArgs {
   uint32_t* err;
   // in 4 bits
   uint64_t timeout_ns;  // bound on each wait
+  uint32_t stall;       // 0; in tests, warps of each decode CTA (a bit each) whose copies never count as done
   uint32_t hkv_mul;     // x / Hkv is the upper word of x hkv_mul, hkv_shift bits less, for x < 2^31
   int hkv_shift;
 };

@@ -394,7 +394,7 @@ struct Q4Unit {
 
   __device__ __forceinline__ Q4Unit(const PagedArgs& a, uint8_t*, Shared& sh) {
     if (threadIdx.x < kDecWarps * kStages)
-      mbar_init(smem_addr(&sh.full[0][0] + threadIdx.x), 4 * runs(a));
+      mbar_init(smem_addr(&sh.full[0][0] + threadIdx.x), 4 * runs(a) + (a.stall >> threadIdx.x / kStages & 1u));
     if (threadIdx.x == 0) sh.abort = 0;
     fence_mbar_init();
     fence_async();
@@ -801,7 +801,7 @@ struct Q4Unit {
       if (following) start(a, *following, smem, sh);
     if (aborted(sh)) {  // copies under way land before the buffers change hands; nothing is asked for any more
       while (take != ask) {
-        mbar_drain(bars + take * 8, phase >> take & 1u, a.timeout_ns);
+        mbar_drain(bars + take * 8, phase >> take & 1u);
         phase ^= 1u << take;
         if (++take == kStages) take = 0;
       }
@@ -857,12 +857,6 @@ struct Q4Unit {
   // The same answer for the whole warp.
   static __device__ __forceinline__ bool aborted(Shared& sh) {
     return __any_sync(0xffffffffu, *static_cast<volatile uint32_t*>(&sh.abort));
-  }
-  // A wait for a copy that is under way after something else has given up.
-  static __device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity, uint64_t timeout_ns) {
-    const uint64_t t0 = global_timer_ns();
-    while (!mbar_try_wait(bar, parity) && global_timer_ns() - t0 < timeout_ns) {
-    }
   }
 };
 

@@ -276,8 +276,9 @@ struct Ring {
     token = p.token;
     head = p.first;
   }
-  static __device__ __forceinline__ void set_up(Shared& sh) {
-    if (threadIdx.x < kRopeWarps * kStages) mbar_init(smem_addr(&sh.full[0][0] + threadIdx.x), 1);
+  static __device__ __forceinline__ void set_up(const RopeArgs& a, Shared& sh) {
+    if (threadIdx.x < kRopeWarps * kStages)
+      mbar_init(smem_addr(&sh.full[0][0] + threadIdx.x), 1 + (a.stall >> threadIdx.x / kStages & 1u));
     if (threadIdx.x == 0) sh.abort = 0;
     fence_mbar_init();
     fence_async();
@@ -325,11 +326,7 @@ struct Ring {
   }
   // After a wait that ran out: what is under way lands.
   __device__ __forceinline__ void drain() {
-    for (; take != ask; done()) {
-      const uint64_t t0 = global_timer_ns();
-      while (!mbar_try_wait(bars + take * 8, phase >> take & 1u) && global_timer_ns() - t0 < a.timeout_ns) {
-      }
-    }
+    for (; take != ask; done()) mbar_drain(bars + take * 8, phase >> take & 1u);
   }
 };
 
@@ -339,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas) rope_fwd_kernel(const __gr
   using R = Ring<D, sizeof(T), 0>;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ typename R::Shared shared;
-  R::set_up(shared);
+  R::set_up(a, shared);
   grid_wait();  // (the launch may start while its predecessor in the stream ends)
   const Part part(a, L::kRows);
   const RopeRows &in = part.k ? a.k : a.q, &to = part.k ? a.ko : a.qo;
@@ -408,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas) rope_bwd_kernel(const __gr
   using R = Ring<D, sizeof(T), sizeof(G)>;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ typename R::Shared shared;
-  R::set_up(shared);
+  R::set_up(a, shared);
   grid_wait();  // (as the forward)
   const Part part(a, L::kRows);
   const RopeRows& to = part.k ? a.dk : a.dq;
