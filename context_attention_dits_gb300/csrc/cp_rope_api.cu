@@ -63,7 +63,7 @@ cp_status take_rule(RopeArgs* a, const cp_qk_rule* r, int B, int S, int H, int H
   if (r->norm && !(r->eps >= 0.f && r->eps <= 1e30f)) return CP_ERR_INVALID_ARG;
   if ((r->q_weight || r->k_weight) && (!r->norm || (r->weight_dt != dt && r->weight_dt != CP_F32)))
     return CP_ERR_INVALID_ARG;
-  if (r->pairs < 0 || 2 * r->pairs > D || r->pairs % 4) return CP_ERR_INVALID_ARG;
+  if (r->pairs < 0 || r->pairs > D / 2 || r->pairs % 4) return CP_ERR_INVALID_ARG;
   if (r->pairs && (r->axes < 1 || r->axes > cp::kRopeMaxAxes)) return CP_ERR_INVALID_ARG;
   if (r->pairs && r->pair_axis)
     for (int i = 0; i < r->pairs; ++i) {

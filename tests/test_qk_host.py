@@ -89,3 +89,10 @@ def test_wrapper_refuses_host_tensors():
         cpa.cp_qk_norm_rope_fwd(q, k, q, k, eps=1e-6)
     with pytest.raises(ValueError):
         cpa.cp_qk_norm_rope_bwd(q, k, q, k, q, k, eps=1e-6)
+
+
+@pytest.mark.parametrize("call", [fwd, bwd])
+@pytest.mark.parametrize("pairs", [1 << 30, 3 << 29, (1 << 31) - 4])
+def test_more_pairs_than_half_an_int(call, pairs):
+    """Twice as many are no int: refused as any other number of pairs that a head has no values for."""
+    assert call(r=rule(pairs=pairs)) == BAD
