@@ -168,6 +168,7 @@ struct Lane {
   static constexpr int kRows = 32 / kLanes;      // of a warp
   static constexpr int kOwn = 4 / kRows;         // pairs whose angle this lane forms
   int l, r, e0, e1;
+  bool some_stay, stays;  // lanes of the warp, this one, behind the pairs
   uint64_t step[kOwn];
   int axis[kOwn];
 
@@ -177,6 +178,8 @@ struct Lane {
     r = lane / kLanes;
     // neighbours: 8 values in a row; halves: 4 of each half, behind the pairs 8 in a row
     const int with = a.pairs / 4;  // lanes with pairs
+    some_stay = with < kLanes;
+    stays = l >= with;
     e0 = kNext ? 8 * l : l < with ? 4 * l : 2 * a.pairs + 8 * (l - with);
     e1 = kNext || l >= with ? e0 + 4 : a.pairs + 4 * l;
 #pragma unroll
@@ -185,6 +188,11 @@ struct Lane {
       step[i] = p < a.pairs ? turn_step(a.freqs[p]) : 0;
       axis[i] = p < a.pairs ? a.axis[p] : 0;
     }
+  }
+  // The members that turn into one another: none behind the pairs, where products with a
+  // sine of 0 would be NaN beside an infinity (the zeros' signs keep those of the values).
+  __device__ __forceinline__ void across(float2& u, float2& v, float u0) const {
+    if (some_stay && stays) u = twice(u0), v = twice(-u0);
   }
   // cos and sin of the lane's four pairs for the token at pos
   __device__ __forceinline__ void angles(const int* pos, float2 (&c)[2], float2 (&s)[2]) const {
@@ -355,7 +363,8 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas) rope_fwd_kernel(const __gr
     for (int i = 0; i < 2; ++i) {
       au[i] = wu[i];
       av[i] = wv[i];
-      bu[i] = bv[i] = make_float2(0.f, 0.f);
+      bu[i] = twice(0.f);
+      bv[i] = twice(-0.f);
     }
     if (a.pairs) {
       float2 c[2], sn[2];
@@ -387,9 +396,10 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas) rope_fwd_kernel(const __gr
         const float2 nn = twice(n);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const float2 y = mul2(fma2(u[j], au[j], mul2(v[j], bv[j])), nn);
-          v[j] = mul2(fma2(v[j], av[j], mul2(u[j], bu[j])), nn);
-          u[j] = y;
+          float2 cu = u[j], cv = v[j];
+          me.across(cu, cv, -0.f);
+          u[j] = mul2(fma2(u[j], au[j], mul2(cv, bv[j])), nn);
+          v[j] = mul2(fma2(v[j], av[j], mul2(cu, bu[j])), nn);
         }
         if (real) Raw<T>::template store<kNext>(dest, me.e0, me.e1, u, v);
         dest += to_step;
@@ -448,9 +458,10 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas) rope_bwd_kernel(const __gr
         rg.template get<kNext>(gu, gv);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {  // back
-          const float2 y = fma2(gu[j], c[j], mul2(gv[j], sn[j]));
-          gv[j] = fma2(gv[j], c[j], mul2(gu[j], make_float2(-sn[j].x, -sn[j].y)));
-          gu[j] = y;
+          float2 cu = gu[j], cv = gv[j];
+          me.across(cu, cv, 0.f);
+          gu[j] = fma2(gu[j], c[j], mul2(cv, sn[j]));
+          gv[j] = fma2(gv[j], c[j], mul2(cu, make_float2(-sn[j].x, -sn[j].y)));
         }
         if (a.norm) {
           rx.template get<kNext>(u, v);

@@ -437,3 +437,21 @@ def test_norm_and_rotation_before_attention():
         for a, b in ((got, dx), (dw, dwr)):
             err = np.linalg.norm(a.cpu().double().numpy() - b) / np.linalg.norm(b)
             assert err <= 6 * 2.0 ** -8, (n, err)
+
+
+@pytest.mark.parametrize("dt", [BF, F4])
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("D,pairs", [(64, 0), (64, 8), (128, 28), (128, 60)])
+def test_values_behind_the_pairs_keep_their_bits(D, pairs, inter, dt):
+    """Without a norm they stay what they are, whatever their neighbours are: infinities, signed zeros, the least numbers."""
+    s = make(2, 9, 3, 2, D, dt, pairs, 2, seed=5, eps=None, inter=inter)
+    odd = torch.tensor([float("inf"), -float("inf"), 0.0, -0.0, 1e-40, -1e38, 3.0])
+    at = torch.randint(0, 14, (2, 9, 3, D), generator=torch.Generator().manual_seed(8))
+    for n in ("q", "gq"):
+        s[n] = torch.where(at < 7, odd[at % 7], s[n].float()).to(dt)
+        s[n][..., :2 * pairs] = 1
+    q, k = run_fwd(s)
+    dq, dk, _, _ = run_bwd(s)
+    bits = torch.int16 if dt == BF else torch.int32
+    for got, want in ((q, s["q"]), (k, s["k"]), (dq, s["gq"]), (dk, s["gk"])):
+        assert torch.equal(got.cpu()[..., 2 * pairs:].view(bits), want[..., 2 * pairs:].view(bits))
