@@ -516,8 +516,9 @@ cp_status cp_paged_attn_decode(const void* q, const void* k_cache, const void* v
  * and the values behind the 2 pairs first ones stay as they are. The angle is formed
  * in 64-bit fixed point of a turn: it is as good at position 2^30 as at 1. Sums and
  * rotation are fp32, results rounded once; with a norm, values are at most 2^60, so that
- * a row's squares have a sum. Rows pass through bounded waits: one that runs out is
- * reported by cp_check_device_status.
+ * a row's squares have a sum (any smaller size will do; a row of zeros with eps 0
+ * becomes NaN). Rows pass through bounded waits: one that runs out is reported by
+ * cp_check_device_status.
  * -------------------------------------------------------------------------*/
 typedef struct {
   int norm;                 /* nonzero: root-mean-square norm of each head */

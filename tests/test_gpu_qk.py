@@ -455,3 +455,34 @@ def test_values_behind_the_pairs_keep_their_bits(D, pairs, inter, dt):
     bits = torch.int16 if dt == BF else torch.int32
     for got, want in ((q, s["q"]), (k, s["k"]), (dq, s["gq"]), (dk, s["gk"])):
         assert torch.equal(got.cpu()[..., 2 * pairs:].view(bits), want[..., 2 * pairs:].view(bits))
+
+
+@pytest.mark.parametrize("dt", [BF, F4])
+@pytest.mark.parametrize("eps", [0.0, 1e-38, 7e-34, 8e-34, 1e-6, 1e30])
+@pytest.mark.parametrize("D,inter", [(64, False), (128, True)])
+def test_rows_of_any_size_below_the_largest(D, inter, eps, dt):
+    """Rows from 2^-120 to 2^56, beside ordinary ones in the same warp: the norm's direction is that of any other row.
+
+    Sizes whose squares fp32 does not hold, where eps hides that (2^-110 is 7.7e-34) and where it does not.
+    """
+    s = make(2, 33, 5, 3, D, dt, 16, 1, seed=6, eps=eps, wdt=dt, inter=inter)
+    e = torch.randint(-120, 57, (2, 33, 8, 1), generator=torch.Generator().manual_seed(9)).float()
+    e[:, ::3] = 0
+    for n, x in (("q", slice(0, 5)), ("k", slice(5, 8))):   # gradients as small, so that those of the rows stay within fp32
+        s[n] = (s[n].float() * torch.exp2(e[:, :, x])).to(dt)
+        s["g" + n] = (s["g" + n].float() * torch.exp2(e[:, :, x])).to(dt)
+    qo, ko = run_fwd(s)
+    dq, dk, wq, wk = run_bwd(s)
+    t, least = turns(s), 2.0 ** -133 if dt == BF else 2.0 ** -149
+    for x, w, g, y, dx, dw in ((s["q"], s["q_weight"], s["gq"], qo, dq, wq), (s["k"], s["k_weight"], s["gk"], ko, dk, wk)):
+        ref = oq.forward(x, t, inter, eps, w)
+        dxr, dwr = oq.backward(x, g, t, inter, eps, w)
+        xs = x.double().numpy()
+        n = 1 / np.sqrt((xs * xs).mean(-1, keepdims=True) + eps)
+        gs, wv = oq.rotate(g.double().numpy(), -t, inter), w.double().numpy()
+        top = lambda a: np.abs(a).max(-1, keepdims=True)
+        # fp32 throughout: 2^-18 of a row's largest terms covers its some 64 roundings each way
+        r, c = half_step(dt), 2.0 ** -18
+        within(y, ref, r * np.abs(ref) + c * top(xs * n * wv) + least, "forward")
+        within(dx, dxr, r * np.abs(dxr) + c * n * top(gs * wv) * (1 + (n * top(xs)) ** 2) + least, "gradients")
+        within(dw, dwr, c * np.abs(gs * xs * n).sum((0, 1, 2)) + least, "weights' gradients")
