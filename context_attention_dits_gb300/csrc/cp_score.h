@@ -176,7 +176,8 @@ inline int q4_cluster(bool bf16, int B, int Hkv, int G, int max_pages, int page_
   while (cs < most && blocks > cs && units * cs * 2 <= ctas) cs *= 2;
   return units <= ctas && blocks <= cs * 4 ? cs : 0;
 }
-// Division by d (1 .. 65535) of numbers below 2^31: with 2^s >= d > 2^(s - 1), mul is
+// Division by d (1 .. 65535) of numbers below 2^31 by a multiplication (that by an invariant
+// integer of Granlund and Montgomery): with 2^s >= d > 2^(s - 1), mul is
 // 2^(31 + s) / d rounded up, off by less than 1, which n < 2^31 makes less than 1 / d.
 inline void divide_by(int d, uint32_t* mul, int* shift) {
   int s = 0;

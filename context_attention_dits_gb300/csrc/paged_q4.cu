@@ -11,10 +11,10 @@
 // pieces (codes, scales), or four in pages of 16 rows.
 //
 // The attention never forms z + s c. With x = q.k and p the weights,
-//   x_j = sum over groups of s_j (q.c_j) + z_j (sum of q)
+//   x_j = sum over groups of s_j (q.(c_j - 8)) + (z_j + 8 s_j) (sum of q)
 //   out = sum_j p_j s_j (c_j - 8) + sum_j p_j (z_j + 8 s_j)
-// so that codes go to the matrix instructions as they are, 4-bit integers being
-// exact in fp16, and scales meet only scores and weights, one number a key.
+// so that codes go to the matrix instructions alone, as c - 8, which is exact in fp16,
+// and scales meet only scores and weights, one number a key.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -73,7 +73,7 @@ __device__ __forceinline__ float at_least(float a, float b) {
   return y;
 }
 
-// a - b = h + l exactly.
+// a - b = h + l exactly (the two-sum of Knuth, of a and -b).
 __device__ __forceinline__ void exact_diff(float a, float b, float& h, float& l) {
   h = __fsub_rn(a, b);
   const float bb = __fsub_rn(h, a);
@@ -864,11 +864,12 @@ struct Q4Unit {
 // waits for no other: units within its range it writes out, the one that began before
 // and the one that goes on it leaves as partials, for the join.
 // 2 x 262144 keys, 32 heads on 4 of 128, bf16, capped: 75.5 us with the join, 4.0 TB/s of
-// the cache; the copies alone, with nothing formed of them, take 54. Instructions bound
-// it: a warp takes 18 for a key and head (128 codes of k and of v, 8 query heads), most
-// of them to make operands of codes. More warps a multiprocessor make it slower: shorter
-// steps have more overhead a key, and longer ones spill (three CTAs: 72 us; three of 32
-// keys a step: 79, four: 86).
+// the cache; the copies alone, with nothing formed of them, take 54. Waiting bounds it: a
+// scheduler has two warps, each of which waits for its own last result half of the time,
+// so that half of the issue slots go by (a warp takes some 20 instructions for a key and
+// head, 128 codes of k and of v for 8 query heads). More warps have shorter steps, with
+// more overhead a key, or spill: three CTAs 74.0 us, but a ragged batch 49.8 where this
+// takes 49.1; of 32 keys a step three take 80.4 (48.7), four 87.7 (52.7).
 template <class U>
 __global__ void __launch_bounds__(kDecThreads, U::kPerSm) q4_decode_kernel(const __grid_constant__ PagedArgs a) {
   constexpr int D = U::kD;
@@ -939,8 +940,8 @@ __global__ void __launch_bounds__(kDecThreads, U::kPerSm) q4_decode_kernel(const
 // that info names, the others in slot 0 of the warps up to info.y. kSplit warps a query
 // head take its partials in turn, with a running maximum each, eight under way at once,
 // and meet at the end: three loads one after the other in all. Many warps a head where a
-// unit has many partials, one where it has few (48 ragged sequences of 24 heads, four
-// partials a unit: the call 49.5 us with eight, 46.4 with four).
+// unit has many partials, one where it has few (48 ragged sequences of 24 heads, three
+// partials a unit on average: the call 49.1 us with one, 49.4 with four).
 template <int D, int kSplit>
 __global__ void __launch_bounds__(kSplit == 1 ? 128 : kSplit * 32) q4_join_kernel(const __grid_constant__ PagedArgs a, int rows) {
   constexpr int kLane = D / 32, kFlight = 8;

@@ -10,7 +10,7 @@
 //
 // Every value is read once and written once and costs some ten operations, so HBM
 // bounds the long calls (2 or 3 streams; 32768 tokens of 24 + 24 heads of 128, bf16,
-// take 130 us forward, 6.2 TB/s, and 4608 take 21.7, some 4 of them start and end) and
+// take 127 us forward, 6.3 TB/s, and 4608 take 22.2, some 4 of them start and end) and
 // the launch the short ones. A row lies in D / 8 lanes, 8 values each: its sums take 3
 // or 4 shuffles, and a lane holds both members of its four pairs, by one 16-byte piece
 // where pairs are neighbours and two pieces of 8 where they are the row's halves. A
@@ -19,8 +19,9 @@
 //
 // An angle of radians in fp32 is worth nothing far out (half a radian at position
 // 2^23). It is kept in turns instead, as 64-bit fixed point: u = f 2^64 / 2 pi,
-// whole turns dropped, and position u is exact but for what u itself is off,
-// half of 2^-64 or so of a turn, times the position.
+// whole turns dropped, and position u is exact but for what u itself is off: less
+// than (1 + f / 200) 2^-64 of a turn (bits dropped, and those of the constant), times
+// the position.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -267,13 +268,13 @@ __device__ __forceinline__ int64_t row_at(const RopeRows& x, int b, int s, int h
 // token (kB > 0: of two tensors), kStages - 1 of them under way while one is worked on,
 // 2 KB (kB: 4 to 6 KB) each. As many loads in registers would halve the warps: 4608
 // tokens of 24 + 24 heads of 128, bf16, with four rows in registers: forward 24.0 us where
-// this takes 21.7, backward 37.8 where this takes 33.2 (32768 tokens forward: 134, 131).
-// A warp with one batch in all gains nothing (700 tokens of 6 + 3 fp32 heads, backward:
-// 7.7 us from registers, 8.5 here).
+// this took 21.7, backward 37.8 where it took 33.2 (32768 tokens forward: 134, 131). A
+// warp with one batch in all gains nothing (700 tokens of 6 + 3 fp32 heads, backward:
+// 7.7 us from registers, 8.5 here): not worth a second kernel beside some 20 us of calls.
 template <int D, int kElemA, int kElemB>
 struct Ring {
-  // (backward of 4607 tokens with six steps 33.2 us, with four 34.0; forward of 4608 tokens
-  // with three stages 21.7, with four or two 22.4; of 32768 131, 131 and 127)
+  // (backward of 4607 tokens with six steps 33.7 us, with four 34.8; forward of 4608 tokens
+  // with three stages 22.2, with four 22.7, with two 22.8; of 32768 127.5, 128.0 and 126.4)
   static constexpr int kSteps = kElemA != 2 ? 2 : kElemB == 2 && D == 128 ? 6 : 4;
   static constexpr int kRows = 256 / D, kBatch = kRows * kSteps;
   static constexpr int kA = kBatch * D * kElemA, kB = kBatch * D * kElemB, kStage = kA + kB;
@@ -357,7 +358,7 @@ struct Ring {
 
 // kTiny: a norm with an eps that does not hide what squares of small values lose in fp32, so
 // that each row is brought about to 1 first (4608 tokens of 24 + 24 heads of 128, bf16: 25.5 us
-// where others take 22.2; a look at every row and a second try: 23.2).
+// where others take 22.2; a look at every row and a second try took 23.2).
 template <int D, typename T, bool kNext, bool kTiny>
 __global__ void __launch_bounds__(kThreads, kFwdCtas) rope_fwd_kernel(const __grid_constant__ RopeArgs a) {
   using L = Lane<D, T, kNext>;

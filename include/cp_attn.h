@@ -514,11 +514,11 @@ cp_status cp_paged_attn_decode(const void* q, const void* k_cache, const void* v
  *   turned by t = positions[b, s, pair_axis[p]] * freqs[p] radians:
  *   (u, v) -> (u cos t - v sin t, u sin t + v cos t)
  * and the values behind the 2 pairs first ones stay as they are. The angle is formed
- * in 64-bit fixed point of a turn: it is as good at position 2^30 as at 1. Sums and
- * rotation are fp32, results rounded once; with a norm, values are at most 2^60, so that
- * a row's squares have a sum (any smaller size will do; a row of zeros with eps 0
- * becomes NaN). Rows pass through bounded waits: one that runs out is reported by
- * cp_check_device_status.
+ * in 64-bit fixed point of a turn: with frequencies up to 2^10 it is as good at position
+ * 2^30 as at 1. Sums and rotation are fp32, results rounded once; with a norm, values are
+ * at most 2^60, so that a row's squares have a sum (any smaller size will do; a row of
+ * zeros with eps 0 becomes NaN). Rows pass through bounded waits: one that runs out is
+ * reported by cp_check_device_status.
  * -------------------------------------------------------------------------*/
 typedef struct {
   int norm;                 /* nonzero: root-mean-square norm of each head */

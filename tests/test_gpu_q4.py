@@ -303,6 +303,27 @@ def test_decode_scores_of_fp32_queries():
     assert rms(lse.double()) <= 2 * rms(plain)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_decode_scores_of_bf16_queries(D):
+    """The same for bf16 queries, whose products with c - 8 are whole numbers of 12 bits times a power of two of q's size.
+
+    Their sums are formed 16 at a time and cut to fp32, four times a group; then a product and a sum for each of two
+    groups, of scale and of offset: no more roundings than the plain form's, of sums no larger. Twice its error is the bound.
+    """
+    B, H, Hkv = 200, 32, 4
+    s = make([1] * B, H, Hkv, D, 16, BF, seed=6)
+    _, lse = decode(s, D ** -0.5, F4)
+    page = s["table"][:, 0].long()
+    codes, scales = s["kc"][page, :, 0], s["ks"][page, :, 0]
+    k = torch.from_numpy(q4.values(codes, scales)).repeat_interleave(H // Hkv, 1)
+    want = (k * s["q"].double()).sum(2) * D ** -0.5
+    sz = scales.float().repeat_interleave(64, 2).repeat_interleave(H // Hkv, 1)
+    c = torch.from_numpy(q4.unpack(codes)).float().repeat_interleave(H // Hkv, 1)
+    plain = ((s["q"].float() * (sz[..., 1] + sz[..., 0] * c)).sum(2) * D ** -0.5).double()
+    rms = lambda x: float((x - want).square().mean().sqrt())
+    assert rms(lse.double()) <= 2 * rms(plain)
+
+
 @pytest.mark.parametrize("D,n", [(64, 50000), (128, 20000)])
 def test_decode_answers_of_fp32_queries(D, n):
     """Errors of many keys do not lean to one side, where answers are small beside the values they are summed of.
